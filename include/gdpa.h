@@ -492,6 +492,84 @@ gdpa_status gdpa_bwd_mx(gdpa_plan plan, const uint8_t* q_el, const uint8_t* q_sc
                         const uint8_t* k_el, const uint8_t* k_sc, const void* v, const void* d_o,
                         float* dq, float* dk, float* dv, float alpha, gdpa_act act, void* stream);
 
+/*
+ * Rotary positions of Q and K rows (rows of jagged batches carry an order or
+ * an event time that neither GDPA nor its softmax variant sees).  The n =
+ * rot_dim first columns of every head row are taken in pairs, (i, i + n/2) in
+ * the HALF layout and (2i, 2i + 1) in the INTERLEAVED one, and pair i of the
+ * row at position p is turned by t = p f_i and scaled by A:
+ *     a' = A (a cos t - b sin t),   b' = A (a sin t + b cos t);
+ * columns behind rot_dim are copied.  gdpa_rope_init makes the frequencies,
+ *     NONE      f_i = base^(-2i/n)
+ *     LINEAR    f_i / factor                       (positions divided)
+ *     NTK       base * factor^(n/(n-2)) in place of base (as NONE for n = 2)
+ *     BY_PARTS  g f_i + (1 - g) f_i / factor with g = clamp((r_i - lo) /
+ *               (hi - lo), 0, 1) and r_i = orig_len f_i / (2 pi), the turns
+ *               of pair i over the original length
+ * and gdpa_rope_init_freqs takes any (radians per position, |f| <= 2^20).
+ * A gdpa_rope is plain host data (no device memory, copied into each launch):
+ * it needs no destruction and serves every device and thread.
+ */
+typedef enum { GDPA_ROPE_HALF = 0, GDPA_ROPE_INTERLEAVED = 1 } gdpa_rope_layout;
+typedef enum {
+    GDPA_ROPE_SCALING_NONE = 0,
+    GDPA_ROPE_SCALING_LINEAR = 1,
+    GDPA_ROPE_SCALING_NTK = 2,
+    GDPA_ROPE_SCALING_BY_PARTS = 3
+} gdpa_rope_scaling;
+#define GDPA_ROPE_MAX_PAIRS 64
+typedef struct {
+    int32_t rot_dim;
+    int32_t layout;
+    float scale;                          /* A */
+    int32_t reserved;
+    uint64_t turns[GDPA_ROPE_MAX_PAIRS];  /* f_i / (2 pi), 2^-64 turns, modulo one turn */
+} gdpa_rope;
+
+/* rot_dim even, 2 .. 128 (UNSUPPORTED above); base >= 1; factor >= 1 unless
+ * NONE; BY_PARTS: orig_len > 0 and lo < hi; scale finite.  INVALID_ARG
+ * otherwise.  Host only. */
+gdpa_status gdpa_rope_init(gdpa_rope* rope, int rot_dim, gdpa_rope_layout layout, double base,
+                           gdpa_rope_scaling scaling, double factor, double orig_len, double lo,
+                           double hi, float scale);
+gdpa_status gdpa_rope_init_freqs(gdpa_rope* rope, int rot_dim, gdpa_rope_layout layout,
+                                 const double* freqs, float scale);
+
+/* Rows x of `heads` heads, and where they go: element (t, h, c) at x[t *
+ * x_token + h * x_head + c], strides in elements (a packed projection's Q or
+ * K part, say).  y may be x with the same strides (in place); it must not
+ * overlap x otherwise. */
+typedef struct {
+    const void* x;
+    void* y;
+    int32_t heads;
+    int64_t x_token, x_head, y_token, y_head;
+} gdpa_rope_tensor;
+
+/*
+ * Turn T rows of d columns of one or two tensors (n = 1 or 2: Q and K of the
+ * same tokens) in one launch; inverse != 0 turns by -t, which is the gradient
+ * (dL/dx of dL/dy, A included).  Rows are bf16 or float32; the angle is exact
+ * to 2^-31 turns at any int32 position, sines and products are float32 and
+ * each value is rounded once.
+ *
+ *   positions   device int32 or int64 (position_bits) [T], any sign; or NULL,
+ *               and then
+ *   off, starts device int32 [B + 1] sample offsets (off[0] = 0) and device
+ *               int32 [B] position of each sample's first row (NULL = 0): row
+ *               t of sample b is at starts[b] + t - off[b].  Rows behind
+ *               off[B] are left as they are, in y too.
+ *
+ * INVALID_ARG for bad pointers, sizes or enums, rot_dim > d, both or neither
+ * of positions and off, and, in the INTERLEAVED layout, odd d or strides or
+ * rows not aligned to a pair; UNSUPPORTED for d > 128 or more than 4096 heads.
+ * Enqueued on `stream` on the current device; no allocation, capturable.
+ */
+gdpa_status gdpa_rope_apply(const gdpa_rope* rope, int inverse, gdpa_dtype dtype, int64_t T, int d,
+                            const gdpa_rope_tensor* tensors, int n, const void* positions,
+                            int position_bits, const int32_t* off, const int32_t* starts, int B,
+                            void* stream);
+
 /* Activation test hook.
  *
  * Evaluates act(x) and act'(x) element-wise with the same device functions

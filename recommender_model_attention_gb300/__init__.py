@@ -18,6 +18,7 @@ from .gdpa import (  # noqa: F401
     MASK,
     MX,
     Plan,
+    Rope,
     STATUS,
     allreduce_seed_grad,
     act_eval,
@@ -26,6 +27,8 @@ from .gdpa import (  # noqa: F401
     gdpa_fwd,
     gdpa_fwd_mx,
     gdpa_fwd_noalloc,
+    gdpa_rope_bwd,
+    gdpa_rope_fwd,
     gdpa_softmax_bwd,
     gdpa_softmax_fwd,
     lib,

@@ -21,6 +21,8 @@ ACT = {"gelu_erf": 0, "gelu_tanh": 1, "silu": 2, "gelu_taylor6": 3, "identity": 
 MASK = {"none": 0, "causal_window": 1}
 SCHED = {"zigzag": 0, "round_robin": 1, "zigzag_timed": 2}
 KERNEL = {"auto": 0, "tcgen05": 1, "simt": 2}
+ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 KV_SPLIT_AUTO = -1   # max_kv_blocks_per_tile: the planner chooses
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported configuration", 3: "CUDA error",
           4: "allocation failed", 5: "kernel barrier wait timed out",
@@ -30,6 +32,17 @@ BLOCK_M = 128
 BLOCK_N = 128
 
 _lib = None
+
+
+class _RopeSpec(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("turns", ctypes.c_uint64 * 64)]
+
+
+class _RopeTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int32),
+                ("x_token", ctypes.c_int64), ("x_head", ctypes.c_int64),
+                ("y_token", ctypes.c_int64), ("y_head", ctypes.c_int64)]
 
 
 class GdpaError(RuntimeError):
@@ -80,6 +93,12 @@ def lib():
             "gdpa_mx_dequantise": [vp, vp, ctypes.c_int64, vp, vp],
             "gdpa_fwd_mx": [vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, st, vp],
             "gdpa_bwd_mx": [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, st, vp],
+            "gdpa_rope_init": [ctypes.POINTER(_RopeSpec), st, st, ctypes.c_double, st, ctypes.c_double,
+                               ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_float],
+            "gdpa_rope_init_freqs": [ctypes.POINTER(_RopeSpec), st, st,
+                                     ctypes.POINTER(ctypes.c_double), ctypes.c_float],
+            "gdpa_rope_apply": [ctypes.POINTER(_RopeSpec), st, st, ctypes.c_int64, st,
+                                ctypes.POINTER(_RopeTensor), st, vp, st, vp, vp, st, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -527,3 +546,128 @@ def gdpa_softmax_bwd(plan: Plan, q, k, v, o, do, lse, dq=None, dk=None, dv=None,
                                _ptr(do), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
                                ctypes.c_float(alpha), _stream_ptr(stream)), "gdpa_softmax_bwd")
     return dq, dk, dv
+
+
+class Rope:
+    """Rotary positions: which columns turn, how fast, and by what amplitude.
+
+    rot_dim: the first columns of every head row that turn (even, <= d).
+    layout: pairs (i, i + rot_dim / 2) "half" or (2 i, 2 i + 1) "interleaved".
+    scaling: "none", "linear" (positions over ``factor``), "ntk" (the base
+    stretched by ``factor``) or "by_parts" (pairs that turn less than ``lo``
+    times over ``orig_len`` positions slowed by ``factor``, those over ``hi``
+    left as they are, a ramp between).  scale: amplitude of the turned columns.
+    freqs: radians per position of each pair instead of base and scaling.
+
+    Host data only: one object serves every device, stream and thread.
+    """
+
+    def __init__(self, rot_dim: int, layout: str = "half", base: float = 10000.0,
+                 scaling: str = "none", factor: float = 1.0, orig_len: float = 0.0, lo: float = 1.0,
+                 hi: float = 32.0, scale: float = 1.0, freqs=None):
+        self.rot_dim, self.layout = int(rot_dim), layout
+        self.spec = _RopeSpec()
+        if freqs is not None:
+            f = np.ascontiguousarray(np.asarray(freqs, dtype=np.float64))
+            if f.shape != (self.rot_dim // 2,):
+                raise ValueError("freqs must have rot_dim / 2 entries")
+            _ok(lib().gdpa_rope_init_freqs(ctypes.byref(self.spec), self.rot_dim,
+                                           ROPE_LAYOUT[layout],
+                                           f.ctypes.data_as(ctypes.POINTER(ctypes.c_double)), scale),
+                "gdpa_rope_init_freqs")
+        else:
+            _ok(lib().gdpa_rope_init(ctypes.byref(self.spec), self.rot_dim, ROPE_LAYOUT[layout], base,
+                                     ROPE_SCALING[scaling], factor, orig_len, lo, hi, scale),
+                "gdpa_rope_init")
+
+
+def _rope_rows(x, y, T, d, like, name):
+    """One tensor of a rope call: checks, and where its rows are and go."""
+    if not x.is_cuda or x.dim() != 3 or x.shape[0] != T or x.shape[2] != d:
+        raise ValueError("%s must be a [%d, heads, %d] CUDA tensor, got %s on %s"
+                         % (name, T, d, tuple(x.shape), x.device))
+    if x.dtype != like.dtype or x.device != like.device:
+        raise TypeError("%s must have q's dtype and device" % name)
+    if y is None:
+        y = x.new_empty(x.shape)
+    elif y.shape != x.shape or y.dtype != x.dtype or y.device != x.device:
+        raise ValueError("%s output must have its input's shape, dtype and device" % name)
+    xs, ys = x.stride(), y.stride()
+    if d > 1 and (xs[2] != 1 or ys[2] != 1):
+        raise ValueError("%s: the columns of a row must be contiguous" % name)
+    if (T > 1 and ys[0] == 0) or (x.shape[1] > 1 and ys[1] == 0):
+        raise ValueError("%s output must not be an expanded tensor" % name)
+    return y, _RopeTensor(x.data_ptr(), y.data_ptr(), x.shape[1], xs[0], xs[1], ys[0], ys[1])
+
+
+def _rope(rope, inverse, q, k, positions, offsets, starts, q_out, k_out, stream):
+    import torch
+    if q.dim() != 3:
+        raise ValueError("q must be a [T, heads, d] tensor")
+    T, _, d = q.shape
+    dev = q.device
+    if (positions is None) == (offsets is None):
+        raise ValueError("give either positions or offsets")
+    if starts is not None and offsets is None:
+        raise ValueError("starts belong to offsets")
+    rows = (_RopeTensor * 2)()
+    q_out, rows[0] = _rope_rows(q, q_out, T, d, q, "q")
+    n = 1
+    if k is not None:
+        k_out, rows[1] = _rope_rows(k, k_out, T, d, q, "k")
+        n = 2
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    bits, B, pos, off, start = 0, 0, 0, 0, 0
+    if positions is not None:
+        if (positions.dtype not in (torch.int32, torch.int64) or tuple(positions.shape) != (T,)
+                or not positions.is_contiguous() or positions.device != dev):
+            raise ValueError("positions must be a contiguous int32 or int64 [T] tensor on q's device")
+        bits = 32 if positions.dtype == torch.int32 else 64
+        pos = positions.data_ptr()
+    else:
+        for t, what in ((offsets, "offsets"), (starts, "starts")):
+            if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous()
+                                  or t.device != dev):
+                raise ValueError("%s must be a contiguous int32 tensor on q's device" % what)
+        B = offsets.shape[0] - 1
+        if B < 0 or (starts is not None and starts.shape[0] != B):
+            raise ValueError("offsets must have B + 1 entries and starts B")
+        off = offsets.data_ptr()
+        start = starts.data_ptr() if starts is not None and B else 0
+    if T:
+        with _current(dev):
+            s = torch.cuda.current_stream(dev) if stream is None else stream
+            _ok(lib().gdpa_rope_apply(ctypes.byref(rope.spec), inverse, _dtype_id(q), T, d, rows, n,
+                                      pos, bits, off, start, B, s.cuda_stream), "gdpa_rope_apply")
+    return q_out if k is None else (q_out, k_out)
+
+
+def _current(device):
+    """A context with ``device`` current; costs nothing when it is already."""
+    import contextlib
+
+    import torch
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def gdpa_rope_fwd(rope: Rope, q, k=None, positions=None, offsets=None, starts=None, q_out=None,
+                  k_out=None, stream=None):
+    """Q (and K of the same tokens) with rotary positions, in one launch.
+
+    q, k: bf16 or float32 [T, heads, d] CUDA tensors, of any token and head
+    strides (the Q and K parts of a packed projection).  positions: int32 or
+    int64 [T]; or offsets (int32 [B + 1] CUDA tensor) with the optional int32
+    [B] ``starts``: row t of sample b is at starts[b] + t - offsets[b], and
+    rows behind the last offset are not written.  q_out, k_out: outputs (q and
+    k themselves to work in place).  Returns q_out, or (q_out, k_out)."""
+    return _rope(rope, 0, q, k, positions, offsets, starts, q_out, k_out, stream)
+
+
+def gdpa_rope_bwd(rope: Rope, dq, dk=None, positions=None, offsets=None, starts=None, dq_out=None,
+                  dk_out=None, stream=None):
+    """Gradients with respect to gdpa_rope_fwd's inputs, given those of its
+    outputs (the inverse turn, the amplitude included); arguments alike."""
+    return _rope(rope, 1, dq, dk, positions, offsets, starts, dq_out, dk_out, stream)
