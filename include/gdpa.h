@@ -570,6 +570,85 @@ gdpa_status gdpa_rope_apply(const gdpa_rope* rope, int inverse, gdpa_dtype dtype
                             int position_bits, const int32_t* off, const int32_t* starts, int B,
                             void* stream);
 
+/*
+ * Shared-prefix attention: GDPA or its softmax variant for a batch whose
+ * samples come in groups that share a long run of keys (the history of one
+ * user, scored against many candidates; the impressions of one request in
+ * training), so that the shared keys are stored and read once.  Samples
+ * [group_off[g], group_off[g+1]) form group g with prefix keys [prefix_off[g],
+ * prefix_off[g+1]) of kp, vp; sample b's own keys are rows kv_off[b] ..
+ * kv_off[b+1] of k, v.  For every query row i of sample b of group g and every
+ * head,
+ *     O_i = sum_j w_ij V_j   over the prefix keys of g and the own keys of b,
+ * w = act(alpha q.k), or softmax over all of them together.  Every query sees
+ * the whole prefix; the mask (and its window) applies to the own keys, with
+ * positions counted from the sample's first row, as in gdpa_plan_create.  A
+ * row that sees no key gives O = 0, lse = -inf and no gradient.
+ *
+ * Heads: Hkv key heads, each shared by H / Hkv consecutive query heads (Hkv =
+ * H: one each).  Layout: q, o, d_o, dq [Tq][H][d]; kp, vp, dkp, dvp
+ * [Tp][Hkv][d]; k, v, dk, dv [Tkv][Hkv][d]; all of one element type, the
+ * gradients too (sums are float32, rounded once); lse float32 [Tq][H].
+ * Single-token decoding is the same call with one query row per sample.
+ *
+ * A gdpa_prefix_plan belongs to its device, like a gdpa_plan, and owns the
+ * workspace its calls share: calls on one plan from several streams are
+ * ordered by the library, calls from several host threads serialised.  Calls
+ * may be captured into a CUDA graph (the first backward of a plan allocates
+ * and is refused with ALLOC while capturing); the plan must outlive the
+ * graph, and replays that share a plan must not overlap on the GPU with each
+ * other or with other calls on the plan.
+ */
+typedef struct gdpa_prefix_plan_s* gdpa_prefix_plan;
+
+/*
+ * Plan a batch: host int32 offsets, read only during the call; kv_off NULL:
+ * no own keys.  d a multiple of 4 up to 128; num_sms 0 = all of the device.
+ * The tables are uploaded on `stream`; launches on any stream wait for them.
+ * INVALID_ARG for NULL pointers, bad sizes or offsets (not starting at 0,
+ * decreasing, group_off[G] != B), H not a multiple of Hkv, window < 1 with
+ * the window mask; UNSUPPORTED for other d, H * d > 2^20 or more than 128
+ * query heads per key head; ALLOC / CUDA.  *out is NULL on failure.
+ */
+gdpa_status gdpa_prefix_create(const int32_t* q_off, const int32_t* kv_off, int B,
+                               const int32_t* group_off, const int32_t* prefix_off, int G, int H,
+                               int Hkv, int d, gdpa_mask mask, int window, int num_sms, void* stream,
+                               gdpa_prefix_plan* out);
+/* The same on the host only (num_sms > 0): to inspect, not to launch. */
+gdpa_status gdpa_prefix_create_host(const int32_t* q_off, const int32_t* kv_off, int B,
+                                    const int32_t* group_off, const int32_t* prefix_off, int G, int H,
+                                    int Hkv, int d, gdpa_mask mask, int window, int num_sms,
+                                    gdpa_prefix_plan* out);
+/* The forward's pieces of work in queue order: int32 [cap][12] rows (first
+ * token; tokens of the first and of the second row tile; key head; first key
+ * row; keys; flags: 1 own keys, 2 one row tile in two halves of alternate
+ * 128-key blocks; position of the token and of the key in their sample; the
+ * two parts written, -1 for none; 0), seg int32 [num_sms + 1] (may be NULL).
+ * INVALID_ARG if cap is too small (*n still receives the count). */
+gdpa_status gdpa_prefix_export(gdpa_prefix_plan plan, int32_t* pieces, int64_t cap, int64_t* n,
+                               int32_t* seg);
+/* As gdpa_plan_set_kernel: AUTO runs bf16 with d = 64 or 128 on the tensor
+ * cores and everything else on the CUDA cores. */
+gdpa_status gdpa_prefix_set_kernel(gdpa_prefix_plan plan, gdpa_kernel kernel);
+
+/* Forward.  lse (may be NULL) is written for GDPA_ACT_SOFTMAX only. */
+gdpa_status gdpa_prefix_fwd(gdpa_prefix_plan plan, gdpa_dtype dtype, const void* q, const void* kp,
+                            const void* vp, const void* k, const void* v, void* o, float* lse,
+                            float alpha, gdpa_act act, void* stream);
+/* Gradients of every input, all overwritten: dkp, dvp summed over the group's
+ * samples, all key gradients over the query heads that share the head.  o and
+ * lse: the forward's outputs (softmax; ignored otherwise). */
+gdpa_status gdpa_prefix_bwd(gdpa_prefix_plan plan, gdpa_dtype dtype, const void* q, const void* kp,
+                            const void* vp, const void* k, const void* v, const void* o,
+                            const void* d_o, const float* lse, void* dq, void* dkp, void* dvp,
+                            void* dk, void* dv, float alpha, gdpa_act act, void* stream);
+
+/* As gdpa_check, gdpa_error_detail, gdpa_plan_launches, gdpa_plan_destroy. */
+gdpa_status gdpa_prefix_check(gdpa_prefix_plan plan, void* stream);
+gdpa_status gdpa_prefix_error_detail(gdpa_prefix_plan plan, int32_t* detail);
+int64_t gdpa_prefix_launches(gdpa_prefix_plan plan);
+void gdpa_prefix_destroy(gdpa_prefix_plan plan);
+
 /* Activation test hook.
  *
  * Evaluates act(x) and act'(x) element-wise with the same device functions

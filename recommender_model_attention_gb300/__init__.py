@@ -18,6 +18,7 @@ from .gdpa import (  # noqa: F401
     MASK,
     MX,
     Plan,
+    PrefixPlan,
     Rope,
     STATUS,
     allreduce_seed_grad,
@@ -27,6 +28,10 @@ from .gdpa import (  # noqa: F401
     gdpa_fwd,
     gdpa_fwd_mx,
     gdpa_fwd_noalloc,
+    gdpa_prefix_bwd,
+    gdpa_prefix_fwd,
+    gdpa_prefix_softmax_bwd,
+    gdpa_prefix_softmax_fwd,
     gdpa_rope_bwd,
     gdpa_rope_fwd,
     gdpa_softmax_bwd,

@@ -1,0 +1,125 @@
+// Internal declarations of shared-prefix attention (gdpa_prefix_*): the plan
+// the host makes, the records its kernels walk, and the launchers.
+//
+// Rows.  The query rows of a key head hk are its r = H / Hkv query heads of
+// every token, packed token by token: row t * r + j is head hk * r + j of
+// token t.  A row tile is tpt = 128 / r whole tokens (at most 128 rows).
+//
+// Parts.  Attention over a union of key ranges is taken range by range: each
+// piece of work gives, for the rows of one tile, unnormalised sums over its
+// keys (and, for softmax, the reference maximum and the weights' sum), in a
+// part of the plan's workspace; the merge joins the parts of every row.
+// Part p holds float4 columns [d / 4][128 rows] (so that a thread per row
+// writes and reads whole lines) and float2 (maximum, sum) [128 rows].
+#pragma once
+
+#include <mutex>
+#include <vector>
+
+#include "gdpa_internal.h"
+
+namespace gdpa {
+
+constexpr int kPieceOwn = 1;    // keys of the samples' own, not of the prefix
+constexpr int kPieceDual = 2;   // one row tile: the slots take alternate key blocks
+
+// One piece of forward work: keys [k0, k0 + nk) against one row tile of
+// tokens [tok, tok + nA), or two tiles, [tok, tok + nA) and the nB tokens
+// behind.  i0 / j0: positions of token `tok` and of key k0 in their sample
+// (own keys).  part[s]: where slot s's sums go (-1: slot unused).
+struct PrefixPiece {
+    int32_t tok, nA, nB, hk;
+    int32_t k0, nk, flags, i0;
+    int32_t j0, part0, part1, pad;
+};
+static_assert(sizeof(PrefixPiece) == 48, "PrefixPiece layout");
+
+// Backward unit: keys [k0, k0 + nk) (nk <= 128) of head hk against tokens
+// [tok, tok + ntok); flags as a piece's.
+struct PrefixUnit {
+    int32_t k0, nk, tok, ntok;
+    int32_t hk, flags, i0, j0;
+};
+static_assert(sizeof(PrefixUnit) == 32, "PrefixUnit layout");
+
+// One (row tile of a group, key head) for the merge: tokens [tok, tok + n),
+// prefix parts [part, part + layers).
+struct PrefixTile {
+    int32_t tok, n, hk, part;
+    int32_t layers, pad[3];
+};
+static_assert(sizeof(PrefixTile) == 32, "PrefixTile layout");
+
+// Per token: where the parts of its own keys are.  Head hk's are [part + hk *
+// layers, ...), its rows from row0 on; layers = 0 without own keys.
+struct PrefixOwn {
+    int32_t part, row0, layers, pad;
+};
+static_assert(sizeof(PrefixOwn) == 16, "PrefixOwn layout");
+
+struct PrefixPlan {
+    int device = 0;
+    bool host_only = false;
+    int B = 0, G = 0, H = 0, Hkv = 0, r = 1, d = 0, mask = 0, window = 0, S = 0;
+    int tpt = 128;               // tokens of a row tile
+    int kernel = GDPA_KERNEL_AUTO;
+    int64_t Tq = 0, Tkv = 0, Tp = 0;
+    int64_t n_parts = 0;
+    std::vector<PrefixPiece> pieces;
+    std::vector<int32_t> seg;        // [S + 1] first piece of each CTA
+    std::vector<PrefixTile> tiles;
+    std::vector<PrefixOwn> own;      // [Tq]
+    std::vector<PrefixUnit> units;
+    std::vector<int32_t> useg;       // [S + 1] first unit of each CTA
+    // device copies, one allocation (offsets below), and workspaces
+    uint8_t* d_tables = nullptr;
+    size_t off_seg = 0, off_tiles = 0, off_own = 0, off_units = 0, off_useg = 0, off_err = 0;
+    float* d_parts = nullptr;        // [n_parts][d / 4][128] float4
+    float* d_ml = nullptr;           // [n_parts][128] float2
+    float* d_grad = nullptr;         // backward: delta [Tq][H], then float32 sums
+    size_t grad_bytes = 0;
+    int32_t last_err[4] = {0, 0, 0, 0};
+    int64_t launches = 0;
+    cudaEvent_t ready = nullptr;     // the upload, on the creation stream
+    cudaEvent_t last = nullptr;      // the plan's latest work
+    cudaStream_t last_stream = nullptr;
+    bool has_work = false;
+    std::mutex lock;                 // host state above
+
+    const PrefixPiece* dev_pieces() const { return (const PrefixPiece*)d_tables; }
+    const int32_t* dev_seg() const { return (const int32_t*)(d_tables + off_seg); }
+    const PrefixTile* dev_tiles() const { return (const PrefixTile*)(d_tables + off_tiles); }
+    const PrefixOwn* dev_own() const { return (const PrefixOwn*)(d_tables + off_own); }
+    const PrefixUnit* dev_units() const { return (const PrefixUnit*)(d_tables + off_units); }
+    const int32_t* dev_useg() const { return (const int32_t*)(d_tables + off_useg); }
+    int32_t* dev_err() const { return (int32_t*)(d_tables + off_err); }
+};
+
+// The tensors of one call (device pointers, checked).
+struct PrefixIO {
+    const void *q, *kp, *vp, *k, *v;
+    void* o = nullptr;               // forward out; backward: the forward's O (softmax)
+    float* lse = nullptr;
+    const void* d_o = nullptr;
+    void *dq = nullptr, *dkp = nullptr, *dvp = nullptr, *dk = nullptr, *dv = nullptr;
+    float alpha = 1.0f;
+    int act = 0;
+};
+
+// Host planner (prefix_plan.cpp): INVALID_ARG for bad offsets.
+gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t* kv_off,
+                              const int32_t* group_off, const int32_t* prefix_off);
+
+// CUDA-core kernels (prefix_simt.cu), float32 arithmetic, any head dim.
+gdpa_status launch_prefix_simt_fwd(PrefixPlan& p, gdpa_dtype dt, const PrefixIO& io, cudaStream_t st);
+gdpa_status launch_prefix_simt_bwd(PrefixPlan& p, gdpa_dtype dt, const PrefixIO& io,
+                                   const float* delta, cudaStream_t st);
+// Join the parts of every row: into O and lse (io.o, io.lse; normalised when
+// `softmax`), of element type dt.
+gdpa_status launch_prefix_merge(PrefixPlan& p, gdpa_dtype dt, void* out, float* lse, bool softmax,
+                                cudaStream_t st);
+// delta[t][h] = dO . O (softmax backward)
+gdpa_status launch_prefix_delta(PrefixPlan& p, gdpa_dtype dt, const PrefixIO& io, float* delta,
+                                cudaStream_t st);
+
+}  // namespace gdpa

@@ -1,0 +1,219 @@
+// Host planner of shared-prefix attention.
+//
+// Forward units are (group, key head, one or two row tiles) against the
+// group's prefix, and (sample, key head, one or two row tiles) against the
+// sample's own keys, in steps of one 128-key block for two row tiles, or of
+// two blocks for a single tile (whose two slots take alternate blocks).  All
+// units' steps form one line that is cut into equal shares, one per CTA, so
+// that ragged groups balance and a short batch spreads a long prefix over
+// every SM; a cut inside a unit costs another part of its rows to merge,
+// which the shares allow for (kPieceCost steps a piece).
+#include <algorithm>
+
+#include "prefix_internal.h"
+
+namespace gdpa {
+namespace {
+
+constexpr int kPieceCost = 3;   // steps a piece costs beside its own
+
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct Unit {
+    PrefixPiece p;       // the whole unit as one piece
+    int64_t steps;
+    int32_t tileA, tileB;   // merge tiles (prefix units)
+};
+
+bool good_offsets(const int32_t* off, int n) {
+    if (!off || off[0] != 0) return false;
+    for (int i = 0; i < n; ++i)
+        if (off[i + 1] < off[i]) return false;
+    return true;
+}
+
+int64_t steps_of(const PrefixPiece& p) {
+    const int64_t nb = cdiv(p.nk, kBN);
+    return p.flags & kPieceDual ? cdiv(nb, 2) : nb;
+}
+
+}  // namespace
+
+gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t* kv_off,
+                              const int32_t* group_off, const int32_t* prefix_off) {
+    if (!good_offsets(q_off, p.B) || !good_offsets(kv_off, p.B) || !good_offsets(group_off, p.G) ||
+        !good_offsets(prefix_off, p.G) || group_off[p.G] != p.B)
+        return GDPA_ERR_INVALID_ARG;
+    p.Tq = q_off[p.B];
+    p.Tkv = kv_off[p.B];
+    p.Tp = prefix_off[p.G];
+    const int tpt = p.tpt;
+    int64_t parts = 0;
+    std::vector<Unit> units;
+    p.own.assign((size_t)p.Tq, PrefixOwn{0, 0, 0, 0});
+    for (int g = 0; g < p.G; ++g) {
+        const int32_t t0 = q_off[group_off[g]], nt = q_off[group_off[g + 1]] - t0;
+        const int32_t np = prefix_off[g + 1] - prefix_off[g];
+        const int nm = (int)cdiv(nt, tpt);
+        for (int hk = 0; hk < p.Hkv; ++hk) {
+            const int32_t first = (int32_t)p.tiles.size();
+            for (int m = 0; m < nm; ++m)
+                p.tiles.push_back(PrefixTile{t0 + m * tpt, std::min(tpt, nt - m * tpt), hk, 0, 0, {}});
+            if (np == 0) continue;
+            for (int m = 0; m < nm; m += 2) {
+                Unit u{};
+                u.tileA = first + m;
+                u.tileB = m + 1 < nm ? first + m + 1 : -1;
+                u.p.tok = p.tiles[u.tileA].tok;
+                u.p.nA = p.tiles[u.tileA].n;
+                u.p.nB = u.tileB >= 0 ? p.tiles[u.tileB].n : 0;
+                u.p.hk = hk;
+                u.p.k0 = prefix_off[g];
+                u.p.nk = np;
+                u.p.flags = u.tileB >= 0 ? 0 : kPieceDual;
+                u.steps = steps_of(u.p);
+                units.push_back(u);
+            }
+        }
+    }
+    const size_t n_prefix = units.size();
+    // own keys: row tiles counted from the sample's first token
+    const bool windowed = p.mask == GDPA_MASK_CAUSAL_WINDOW;
+    for (int b = 0; b < p.B; ++b) {
+        const int32_t lq = q_off[b + 1] - q_off[b], lk = kv_off[b + 1] - kv_off[b];
+        if (lq == 0 || lk == 0) continue;
+        for (int32_t i = 0; i < lq;) {
+            const int32_t nA = std::min(tpt, lq - i), nB = std::min(tpt, lq - i - nA);
+            // hull of the keys these rows see
+            const int32_t lo = windowed ? std::max(0, i - p.window + 1) : 0;
+            const int32_t hi = windowed ? std::min(lk, i + nA + nB) : lk;
+            if (hi > lo) {
+                Unit u{};
+                u.tileA = u.tileB = -1;
+                u.p.tok = q_off[b] + i;
+                u.p.nA = nA;
+                u.p.nB = nB;
+                u.p.k0 = kv_off[b] + lo;
+                u.p.nk = hi - lo;
+                u.p.flags = kPieceOwn | (nB > 0 ? 0 : kPieceDual);
+                u.p.i0 = i;
+                u.p.j0 = lo;
+                u.steps = steps_of(u.p);
+                const int layers = nB == 0 && u.p.nk > kBN ? 2 : 1;
+                const size_t u0 = units.size();
+                for (int hk = 0; hk < p.Hkv; ++hk) {
+                    u.p.hk = hk;
+                    u.p.part0 = (int32_t)(parts + (int64_t)hk * layers);
+                    u.p.part1 = layers == 2 ? u.p.part0 + 1 : -1;
+                    units.push_back(u);
+                }
+                for (int32_t t = 0; t < nA; ++t)
+                    p.own[u.p.tok + t] = PrefixOwn{(int32_t)parts, t * p.r, layers, 0};
+                parts += (int64_t)p.Hkv * layers;
+                if (nB > 0) {
+                    for (int hk = 0; hk < p.Hkv; ++hk) units[u0 + hk].p.part1 = (int32_t)(parts + hk);
+                    for (int32_t t = 0; t < nB; ++t)
+                        p.own[u.p.tok + nA + t] = PrefixOwn{(int32_t)parts, t * p.r, 1, 0};
+                    parts += p.Hkv;
+                }
+            }
+            i += nA + nB;
+        }
+    }
+    // cut the line of steps into S shares
+    int64_t total = 0;
+    for (const Unit& u : units) total += u.steps + kPieceCost;
+    p.pieces.clear();
+    p.seg.assign((size_t)p.S + 1, 0);
+    const int64_t base = cdiv(total + (int64_t)kPieceCost * p.S, p.S);
+    for (int64_t budget = std::max<int64_t>(base, kPieceCost + 1);; budget += 1 + budget / 64) {
+        p.pieces.clear();
+        int cta = 0;
+        int64_t left = budget;
+        bool ok = true;
+        for (size_t n = 0; n < units.size() && ok; ++n) {
+            const Unit& u = units[n];
+            // own units stay whole (their parts are laid out above)
+            int64_t done = 0;
+            while (done < u.steps) {
+                int64_t take = left - kPieceCost;
+                if (n >= n_prefix && take < u.steps && left < budget) take = 0;
+                if (take < 1) {
+                    if (left == budget) {
+                        take = u.steps;   // one share cannot hold it: it does
+                    } else {
+                        if (++cta >= p.S) { ok = false; break; }
+                        p.seg[cta] = (int32_t)p.pieces.size();
+                        left = budget;
+                        continue;
+                    }
+                }
+                take = n >= n_prefix ? u.steps : std::min(take, u.steps - done);
+                const int64_t unit_keys = u.p.flags & kPieceDual ? 2 * kBN : kBN;
+                PrefixPiece q = u.p;
+                q.k0 = (int32_t)(u.p.k0 + done * unit_keys);
+                q.nk = (int32_t)std::min<int64_t>(u.p.nk - done * unit_keys, take * unit_keys);
+                if (n < n_prefix) q.pad = (int32_t)n;
+                p.pieces.push_back(q);
+                done += take;
+                left -= take + kPieceCost;
+            }
+        }
+        if (ok) {
+            for (int c = cta + 1; c <= p.S; ++c) p.seg[c] = (int32_t)p.pieces.size();
+            break;
+        }
+    }
+    // the prefix parts of each tile: its unit's pieces in order
+    for (size_t i = 0; i < p.pieces.size();) {
+        if (p.pieces[i].flags & kPieceOwn) {
+            p.pieces[i++].pad = 0;
+            continue;
+        }
+        const Unit& u = units[p.pieces[i].pad];
+        size_t e = i;
+        while (e < p.pieces.size() && !(p.pieces[e].flags & kPieceOwn) && p.pieces[e].pad == p.pieces[i].pad) ++e;
+        const bool dual = u.p.flags & kPieceDual;
+        p.tiles[u.tileA].part = (int32_t)parts;
+        for (size_t j = i; j < e; ++j) {
+            PrefixPiece& q = p.pieces[j];
+            q.part0 = (int32_t)parts++;
+            q.part1 = -1;
+            if (dual && q.nk > kBN) q.part1 = (int32_t)parts++;
+        }
+        p.tiles[u.tileA].layers = (int32_t)(parts - p.tiles[u.tileA].part);
+        if (!dual) {
+            p.tiles[u.tileB].part = (int32_t)parts;
+            for (size_t j = i; j < e; ++j) p.pieces[j].part1 = (int32_t)parts++;
+            p.tiles[u.tileB].layers = (int32_t)(e - i);
+        }
+        i = e;
+    }
+    for (PrefixPiece& q : p.pieces) q.pad = 0;
+    if (parts > 0x7fffffff) return GDPA_ERR_UNSUPPORTED;
+    p.n_parts = parts;
+
+    // backward: one unit per 128-key block, against all rows that see it
+    p.units.clear();
+    for (int g = 0; g < p.G; ++g) {
+        const int32_t t0 = q_off[group_off[g]], nt = q_off[group_off[g + 1]] - t0;
+        for (int32_t k = prefix_off[g]; k < prefix_off[g + 1]; k += kBN)
+            for (int hk = 0; hk < p.Hkv; ++hk)
+                p.units.push_back(PrefixUnit{k, std::min(kBN, prefix_off[g + 1] - k), t0, nt, hk, 0, 0, 0});
+    }
+    for (int b = 0; b < p.B; ++b) {
+        const int32_t lq = q_off[b + 1] - q_off[b], lk = kv_off[b + 1] - kv_off[b];
+        for (int32_t j = 0; j < lk; j += kBN) {
+            const int32_t nk = std::min(kBN, lk - j);
+            // queries j <= i < j + nk - 1 + window
+            const int32_t lo = windowed ? std::min(lq, j) : 0;
+            const int32_t hi = windowed ? (int32_t)std::min<int64_t>(lq, (int64_t)j + nk - 1 + p.window) : lq;
+            for (int hk = 0; hk < p.Hkv; ++hk)
+                p.units.push_back(PrefixUnit{kv_off[b] + j, nk, q_off[b] + lo, std::max(0, hi - lo), hk,
+                                             kPieceOwn, lo, j});
+        }
+    }
+    return GDPA_OK;
+}
+
+}  // namespace gdpa

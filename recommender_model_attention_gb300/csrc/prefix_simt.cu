@@ -1,0 +1,488 @@
+// Shared-prefix attention on the CUDA cores: float32 arithmetic for float32
+// rows and for head dims that the tensor-core kernels do not take; and the
+// merge of the parts, which both families share.
+//
+// Forward and dQ walk the plan's pieces: a block of 4 warps takes 32 rows of
+// one slot of a piece, 8 rows a warp, and streams its keys through shared
+// memory 32 at a time; a lane owns one key of the scores and four columns of
+// the sums.  Forward keeps a running maximum and sum per row.  dK and dV walk
+// the backward units: 32 keys a block, 8 a warp, all rows that see them
+// streamed 32 at a time, so that each gradient row is written once, by one
+// warp, in an order that never changes.  They are bound by shared-memory
+// reads (9 16-byte reads for 32 multiply-adds in the scores); float32 has no
+// tensor-core path that keeps its products, and these sizes are small.
+#include <cuda_bf16.h>
+
+#include "act.cuh"
+#include "prefix_internal.h"
+#include "tc_common.cuh"
+
+namespace gdpa {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kRows = 32;    // rows (or keys) of a block
+constexpr int kPer = 8;      // of a warp
+
+struct SimtArgs {
+    const PrefixPiece* pieces;
+    const PrefixUnit* units;
+    const void *q, *kp, *vp, *k, *v, *d_o;
+    const float *lse, *delta;
+    float* parts;
+    float* ml;
+    void *dkp, *dvp, *dk, *dv;
+    int H, Hkv, r, d;
+    int windowed, window;
+    float alpha;
+};
+
+__device__ __forceinline__ float ld(const float* p) { return *p; }
+__device__ __forceinline__ float ld(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+}
+__device__ __forceinline__ void st4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void st4(__nv_bfloat16* p, float4 v) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(tc::pack_bf16x2(v.x, v.y), tc::pack_bf16x2(v.z, v.w));
+}
+__device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
+    return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, c))));
+}
+__device__ __forceinline__ void axpy4(float4& y, float a, float4 x) {
+    y.x = fmaf(a, x.x, y.x);
+    y.y = fmaf(a, x.y, y.y);
+    y.z = fmaf(a, x.z, y.z);
+    y.w = fmaf(a, x.w, y.w);
+}
+
+// rows [0, n) of `ld_elems`-strided global rows into a [32][stride] float tile
+template <typename E>
+__device__ __forceinline__ void load_tile(float* dst, int stride, const E* src, int64_t row_stride,
+                                          int n, int d) {
+    const int c4 = d / 4;
+    for (int i = threadIdx.x; i < kRows * c4; i += kThreads) {
+        const int row = i / c4, c = i - row * c4;
+        const float4 v = row < n ? ld4(src + row * row_stride + 4 * c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4*>(dst + row * stride + 4 * c) = v;
+    }
+}
+
+// packed rows [row0, row0 + 32) of tokens from `tok` (row = token * r + head
+// within the group of query heads), rows >= nrows as zeros
+template <typename E>
+__device__ __forceinline__ void load_rows(float* dst, int stride, const E* src, const SimtArgs& a,
+                                          int tok, int hk, int row0, int nrows) {
+    const int c4 = a.d / 4;
+    for (int i = threadIdx.x; i < kRows * c4; i += kThreads) {
+        const int rl = i / c4, c = i - rl * c4, row = row0 + rl;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row < nrows) {
+            const int t = row / a.r;
+            v = ld4(src + ((int64_t)(tok + t) * a.H + hk * a.r + (row - t * a.r)) * a.d + 4 * c);
+        }
+        *reinterpret_cast<float4*>(dst + rl * stride + 4 * c) = v;
+    }
+}
+
+// p and ds of one pair, in the float32 path's precise forms.  t = the scaled
+// score; lse, delta: the row's (softmax).
+template <int ACT>
+__device__ __forceinline__ void p_ds(float t, float dp, float lse, float delta, float& p, float& ds) {
+    if constexpr (ACT == kSoftmax) {
+        p = expf(t - lse);
+        ds = p * (dp - delta);
+    } else {
+        float da;
+        act_dact_f<ACT, false>(t, p, da);
+        ds = dp * da;
+    }
+}
+
+// Forward (BWD false) or dQ (BWD true) of one slot's 32 rows of a piece.
+template <typename E, int ACT, bool BWD>
+__global__ void __launch_bounds__(kThreads) simt_rows_kernel(const SimtArgs a) {
+    extern __shared__ float sm[];
+    const PrefixPiece pc = a.pieces[blockIdx.x];
+    const int slot = blockIdx.y >> 2, sub = blockIdx.y & 3;
+    const int part = slot ? pc.part1 : pc.part0;
+    if (part < 0) return;
+    const bool dual = pc.flags & kPieceDual, own = pc.flags & kPieceOwn;
+    const int tok = pc.tok + (!dual && slot ? pc.nA : 0);
+    const int nrows = (!dual && slot ? pc.nB : pc.nA) * a.r;
+    const int row0 = sub * kRows;
+    if (row0 >= nrows) return;
+    const int i0 = pc.i0 + (tok - pc.tok);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int qs = a.d, ks = a.d + 4;
+    float* Q = sm;                       // [32][d]
+    float* DO = Q + kRows * qs;          // [32][d] (BWD)
+    float* K = DO + (BWD ? kRows * qs : 0);   // [32][d + 4]
+    float* V = K + kRows * ks;
+    float* W = V + kRows * ks + warp * kRows * kPer;   // weights [32 keys][8 rows]
+    const E* kb = (const E*)(own ? a.k : a.kp);
+    const E* vb = (const E*)(own ? a.v : a.vp);
+    load_rows(Q, qs, (const E*)a.q, a, tok, pc.hk, row0, nrows);
+    if constexpr (BWD) load_rows(DO, qs, (const E*)a.d_o, a, tok, pc.hk, row0, nrows);
+    const int c4 = a.d / 4;
+    float4 acc[kPer];
+    float m[kPer], l[kPer], lse[kPer], delta[kPer];
+    int ipos[kPer];
+#pragma unroll
+    for (int w = 0; w < kPer; ++w) {
+        acc[w] = make_float4(0.f, 0.f, 0.f, 0.f);
+        m[w] = -INFINITY;
+        l[w] = 0.f;
+        const int row = row0 + warp * kPer + w, t = row / a.r;
+        ipos[w] = i0 + t;
+        lse[w] = INFINITY;
+        delta[w] = 0.f;
+        if (BWD && ACT == kSoftmax && row < nrows) {
+            const int64_t at = (int64_t)(tok + t) * a.H + pc.hk * a.r + (row - t * a.r);
+            const float x = a.lse[at];
+            lse[w] = x == -INFINITY ? INFINITY : x;   // a row that sees no key: weights 0
+            delta[w] = a.delta[at];
+        }
+    }
+    for (int key = dual ? slot * kBN : 0; key < pc.nk;
+         key += (dual && (key & 127) == 96) ? kRows + kBN : kRows) {
+        const int n = min(kRows, pc.nk - key);
+        __syncthreads();
+        const int64_t src = ((int64_t)(pc.k0 + key) * a.Hkv + pc.hk) * a.d;
+        load_tile(K, ks, kb + src, (int64_t)a.Hkv * a.d, n, a.d);
+        load_tile(V, ks, vb + src, (int64_t)a.Hkv * a.d, n, a.d);
+        __syncthreads();
+        float s[kPer], dp[kPer];
+#pragma unroll
+        for (int w = 0; w < kPer; ++w) s[w] = dp[w] = 0.f;
+        for (int c = 0; c < c4; ++c) {
+            const float4 kv = *reinterpret_cast<const float4*>(K + lane * ks + 4 * c);
+#pragma unroll
+            for (int w = 0; w < kPer; ++w)
+                s[w] = dot4(kv, *reinterpret_cast<const float4*>(Q + (warp * kPer + w) * qs + 4 * c), s[w]);
+            if constexpr (BWD) {
+                const float4 vv = *reinterpret_cast<const float4*>(V + lane * ks + 4 * c);
+#pragma unroll
+                for (int w = 0; w < kPer; ++w)
+                    dp[w] = dot4(vv, *reinterpret_cast<const float4*>(DO + (warp * kPer + w) * qs + 4 * c),
+                                 dp[w]);
+            }
+        }
+        const int jpos = pc.j0 + key + lane;
+        __syncwarp();
+#pragma unroll
+        for (int w = 0; w < kPer; ++w) {
+            bool ok = lane < n;
+            if (own && a.windowed) ok = ok && jpos <= ipos[w] && jpos > ipos[w] - a.window;
+            const float t = s[w] * a.alpha;
+            float out;
+            if constexpr (BWD) {
+                float p;
+                p_ds<ACT>(t, dp[w], lse[w], delta[w], p, out);
+                out = ok ? out * a.alpha : 0.f;
+            } else if constexpr (ACT == kSoftmax) {
+                float top = ok ? t : -INFINITY;
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+                const float mn = fmaxf(m[w], top);
+                const float ref = mn == -INFINITY ? 0.f : mn;
+                out = ok ? expf(t - ref) : 0.f;
+                float sum = out;
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+                const float f = expf(m[w] - ref);   // 0 while m is still -inf
+                l[w] = fmaf(l[w], f, sum);
+                acc[w].x *= f; acc[w].y *= f; acc[w].z *= f; acc[w].w *= f;
+                m[w] = mn;
+            } else {
+                out = ok ? act_f<ACT, false>(t) : 0.f;
+            }
+            W[lane * kPer + w] = out;
+        }
+        __syncwarp();
+        if (lane < c4) {
+            const float* X = BWD ? K : V;
+            for (int j = 0; j < n; ++j) {
+                const float4 x = *reinterpret_cast<const float4*>(X + j * ks + 4 * lane);
+                float p[kPer];
+                *reinterpret_cast<float4*>(p) = *reinterpret_cast<const float4*>(W + j * kPer);
+                *reinterpret_cast<float4*>(p + 4) = *reinterpret_cast<const float4*>(W + j * kPer + 4);
+#pragma unroll
+                for (int w = 0; w < kPer; ++w) axpy4(acc[w], p[w], x);
+            }
+        }
+    }
+    float4* out = reinterpret_cast<float4*>(a.parts) + (int64_t)part * c4 * 128;
+#pragma unroll
+    for (int w = 0; w < kPer; ++w) {
+        const int row = row0 + warp * kPer + w;
+        if (row >= nrows) break;
+        if (lane < c4) out[lane * 128 + row] = acc[w];
+        if (!BWD && ACT == kSoftmax && lane == 0)   // maximum in base 2, as the merge takes it
+            reinterpret_cast<float2*>(a.ml)[(int64_t)part * 128 + row] = make_float2(m[w] * kLog2e, l[w]);
+    }
+}
+
+// dK and dV of 32 keys of a unit: every row that sees them, in order.
+template <typename E, int ACT>
+__global__ void __launch_bounds__(kThreads) simt_keys_kernel(const SimtArgs a) {
+    extern __shared__ float sm[];
+    const PrefixUnit u = a.units[blockIdx.x];
+    const int key0 = blockIdx.y * kRows;
+    const int n = min(kRows, u.nk - key0);
+    if (n <= 0) return;
+    const bool own = u.flags & kPieceOwn;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int ks = a.d, qs = a.d + 4;
+    float* K = sm;                     // [32][d]
+    float* V = K + kRows * ks;
+    float* Q = V + kRows * ks;         // [32][d + 4]
+    float* DO = Q + kRows * qs;
+    float* W = DO + kRows * qs + warp * 2 * kRows * kPer;   // p, ds [32 rows][8 keys]
+    float* X = W + kRows * kPer;
+    const int64_t src = ((int64_t)(u.k0 + key0) * a.Hkv + u.hk) * a.d, stride = (int64_t)a.Hkv * a.d;
+    load_tile(K, ks, (const E*)(own ? a.k : a.kp) + src, stride, n, a.d);
+    load_tile(V, ks, (const E*)(own ? a.v : a.vp) + src, stride, n, a.d);
+    const int c4 = a.d / 4, nrows = u.ntok * a.r;
+    float4 gk[kPer], gv[kPer];
+#pragma unroll
+    for (int w = 0; w < kPer; ++w) gk[w] = gv[w] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int row0 = 0; row0 < nrows; row0 += kRows) {
+        __syncthreads();
+        load_rows(Q, qs, (const E*)a.q, a, u.tok, u.hk, row0, nrows);
+        load_rows(DO, qs, (const E*)a.d_o, a, u.tok, u.hk, row0, nrows);
+        __syncthreads();
+        const int row = row0 + lane, t = row / a.r, ipos = u.i0 + t;
+        float lse = INFINITY, delta = 0.f;
+        if (ACT == kSoftmax && row < nrows) {
+            const int64_t at = (int64_t)(u.tok + t) * a.H + u.hk * a.r + (row - t * a.r);
+            const float x = a.lse[at];
+            lse = x == -INFINITY ? INFINITY : x;
+            delta = a.delta[at];
+        }
+        float s[kPer], dp[kPer];
+#pragma unroll
+        for (int w = 0; w < kPer; ++w) s[w] = dp[w] = 0.f;
+        for (int c = 0; c < c4; ++c) {
+            const float4 qv = *reinterpret_cast<const float4*>(Q + lane * qs + 4 * c);
+            const float4 dv = *reinterpret_cast<const float4*>(DO + lane * qs + 4 * c);
+#pragma unroll
+            for (int w = 0; w < kPer; ++w) {
+                s[w] = dot4(qv, *reinterpret_cast<const float4*>(K + (warp * kPer + w) * ks + 4 * c), s[w]);
+                dp[w] = dot4(dv, *reinterpret_cast<const float4*>(V + (warp * kPer + w) * ks + 4 * c), dp[w]);
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int w = 0; w < kPer; ++w) {
+            const int jpos = u.j0 + key0 + warp * kPer + w;
+            bool ok = row < nrows && warp * kPer + w < n;
+            if (own && a.windowed) ok = ok && jpos <= ipos && jpos > ipos - a.window;
+            float p, ds;
+            p_ds<ACT>(s[w] * a.alpha, dp[w], lse, delta, p, ds);
+            W[lane * kPer + w] = ok ? p : 0.f;
+            X[lane * kPer + w] = ok ? ds * a.alpha : 0.f;
+        }
+        __syncwarp();
+        if (lane < c4) {
+            const int m = min(kRows, nrows - row0);
+            for (int i = 0; i < m; ++i) {
+                const float4 qv = *reinterpret_cast<const float4*>(Q + i * qs + 4 * lane);
+                const float4 dv = *reinterpret_cast<const float4*>(DO + i * qs + 4 * lane);
+                float p[kPer], x[kPer];
+                *reinterpret_cast<float4*>(p) = *reinterpret_cast<const float4*>(W + i * kPer);
+                *reinterpret_cast<float4*>(p + 4) = *reinterpret_cast<const float4*>(W + i * kPer + 4);
+                *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(X + i * kPer);
+                *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(X + i * kPer + 4);
+#pragma unroll
+                for (int w = 0; w < kPer; ++w) {
+                    axpy4(gv[w], p[w], dv);
+                    axpy4(gk[w], x[w], qv);
+                }
+            }
+        }
+    }
+    if (lane < c4) {
+        E* dk = (E*)(own ? a.dk : a.dkp) + src;
+        E* dv = (E*)(own ? a.dv : a.dvp) + src;
+#pragma unroll
+        for (int w = 0; w < kPer; ++w) {
+            const int j = warp * kPer + w;
+            if (j >= n) break;
+            st4(dk + j * stride + 4 * lane, gk[w]);
+            st4(dv + j * stride + 4 * lane, gv[w]);
+        }
+    }
+}
+
+// Join the parts of 32 rows of a tile: warp w takes float4 columns 4 (w + 8
+// i) .. + 3 of every row (a thread writes 16 consecutive columns of its row).
+template <typename E>
+__global__ void __launch_bounds__(256) merge_kernel(const PrefixTile* tiles, const PrefixOwn* owns,
+                                                    const float* parts, const float* ml, E* out,
+                                                    float* lse, int H, int r, int d, int softmax) {
+    const PrefixTile t = tiles[blockIdx.x];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = blockIdx.y * 32 + lane;
+    if (row >= t.n * r) return;
+    const int tl = row / r, j = row - tl * r;
+    const int tok = t.tok + tl;
+    const PrefixOwn ow = owns[tok];
+    const int own0 = ow.part + t.hk * ow.layers, orow = ow.row0 + j;
+    const float2* st = reinterpret_cast<const float2*>(ml);
+    float top = -INFINITY, sum = 0.f;
+    if (softmax) {
+        for (int i = 0; i < t.layers; ++i) top = fmaxf(top, st[(int64_t)(t.part + i) * 128 + row].x);
+        for (int i = 0; i < ow.layers; ++i) top = fmaxf(top, st[(int64_t)(own0 + i) * 128 + orow].x);
+    }
+    const float ref = top == -INFINITY ? 0.f : top;
+    const int64_t at = (int64_t)tok * H + t.hk * r + j;
+    const int c4 = d / 4;
+    for (int c = warp * 4; c < c4; c += 32) {
+        float4 acc[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        sum = 0.f;
+        for (int i = 0; i < t.layers + ow.layers; ++i) {
+            const bool pre = i < t.layers;
+            const int64_t part = pre ? t.part + i : own0 + i - t.layers;
+            const int prow = pre ? row : orow;
+            float w = 1.f;
+            if (softmax) {
+                const float2 s = st[part * 128 + prow];
+                w = exp2f(s.x - ref);   // 0 for a part without a visible key
+                sum = fmaf(w, s.y, sum);
+                if (s.x == -INFINITY) continue;
+            }
+            const float4* src = reinterpret_cast<const float4*>(parts) + part * c4 * 128 + prow;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (c + x < c4) axpy4(acc[x], w, src[(c + x) * 128]);
+        }
+        const float inv = !softmax ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if (c + x < c4)
+                st4(out + at * d + 4 * (c + x), make_float4(acc[x].x * inv, acc[x].y * inv,
+                                                            acc[x].z * inv, acc[x].w * inv));
+    }
+    if (softmax && lse && warp == 0)
+        lse[at] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+}
+
+// delta = dO . O of every row, a warp a row
+template <typename E>
+__global__ void __launch_bounds__(256) delta_kernel(const E* d_o, const E* o, float* delta,
+                                                    int64_t rows, int d) {
+    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row >= rows) return;
+    const int lane = threadIdx.x & 31;
+    float s = 0.f;
+    if (4 * lane < d) s = dot4(ld4(d_o + row * d + 4 * lane), ld4(o + row * d + 4 * lane), 0.f);
+    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(~0u, s, x);
+    if (lane == 0) delta[row] = s;
+}
+
+SimtArgs args_of(const PrefixPlan& p, const PrefixIO& io, const float* delta) {
+    SimtArgs a;
+    a.pieces = p.dev_pieces();
+    a.units = p.dev_units();
+    a.q = io.q; a.kp = io.kp; a.vp = io.vp; a.k = io.k; a.v = io.v;
+    a.d_o = io.d_o;
+    a.lse = io.lse;
+    a.delta = delta;
+    a.parts = p.d_parts;
+    a.ml = p.d_ml;
+    a.dkp = io.dkp; a.dvp = io.dvp; a.dk = io.dk; a.dv = io.dv;
+    a.H = p.H; a.Hkv = p.Hkv; a.r = p.r; a.d = p.d;
+    a.windowed = p.mask == GDPA_MASK_CAUSAL_WINDOW;
+    a.window = p.window;
+    a.alpha = io.alpha;
+    return a;
+}
+
+template <typename K>
+gdpa_status go(K kern, dim3 grid, int smem, PrefixPlan& p, const SimtArgs& a, cudaStream_t st) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return GDPA_ERR_CUDA;
+    kern<<<grid, kThreads, smem, st>>>(a);
+    p.launches += 1;
+    return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+}
+
+#define PREFIX_DISPATCH(act, ...)                                         \
+    if ((act) == kSoftmax) { constexpr int A = kSoftmax; __VA_ARGS__; }   \
+    else GDPA_DISPATCH_ACT(act, A, __VA_ARGS__)
+
+template <typename E>
+gdpa_status fwd_t(PrefixPlan& p, const PrefixIO& io, cudaStream_t st) {
+    gdpa_status s = GDPA_OK;
+    if (!p.pieces.empty()) {
+        const SimtArgs a = args_of(p, io, nullptr);
+        const int smem = (kRows * p.d + 2 * kRows * (p.d + 4) + 4 * kRows * kPer) * 4;
+        const dim3 grid((unsigned)p.pieces.size(), 8);
+        PREFIX_DISPATCH(io.act, s = go(simt_rows_kernel<E, A, false>, grid, smem, p, a, st))
+    }
+    return s;
+}
+
+template <typename E>
+gdpa_status bwd_t(PrefixPlan& p, const PrefixIO& io, const float* delta, cudaStream_t st) {
+    gdpa_status s = GDPA_OK;
+    const SimtArgs a = args_of(p, io, delta);
+    if (!p.pieces.empty()) {
+        const int smem = (2 * kRows * p.d + 2 * kRows * (p.d + 4) + 4 * kRows * kPer) * 4;
+        const dim3 grid((unsigned)p.pieces.size(), 8);
+        PREFIX_DISPATCH(io.act, s = go(simt_rows_kernel<E, A, true>, grid, smem, p, a, st))
+    }
+    if (s == GDPA_OK && !p.units.empty()) {
+        const int smem = (2 * kRows * p.d + 2 * kRows * (p.d + 4) + 8 * kRows * kPer) * 4;
+        const dim3 grid((unsigned)p.units.size(), 4);
+        PREFIX_DISPATCH(io.act, s = go(simt_keys_kernel<E, A>, grid, smem, p, a, st))
+    }
+    return s;
+}
+
+}  // namespace
+
+gdpa_status launch_prefix_simt_fwd(PrefixPlan& p, gdpa_dtype dt, const PrefixIO& io, cudaStream_t st) {
+    return dt == GDPA_BF16 ? fwd_t<__nv_bfloat16>(p, io, st) : fwd_t<float>(p, io, st);
+}
+
+gdpa_status launch_prefix_simt_bwd(PrefixPlan& p, gdpa_dtype dt, const PrefixIO& io,
+                                   const float* delta, cudaStream_t st) {
+    return dt == GDPA_BF16 ? bwd_t<__nv_bfloat16>(p, io, delta, st) : bwd_t<float>(p, io, delta, st);
+}
+
+gdpa_status launch_prefix_merge(PrefixPlan& p, gdpa_dtype dt, void* out, float* lse, bool softmax,
+                                cudaStream_t st) {
+    if (p.tiles.empty()) return GDPA_OK;
+    const dim3 grid((unsigned)p.tiles.size(), 4);
+    if (dt == GDPA_BF16)
+        merge_kernel<<<grid, 256, 0, st>>>(p.dev_tiles(), p.dev_own(), p.d_parts, p.d_ml,
+                                           (__nv_bfloat16*)out, lse, p.H, p.r, p.d, softmax);
+    else
+        merge_kernel<<<grid, 256, 0, st>>>(p.dev_tiles(), p.dev_own(), p.d_parts, p.d_ml, (float*)out,
+                                           lse, p.H, p.r, p.d, softmax);
+    p.launches += 1;
+    return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+}
+
+gdpa_status launch_prefix_delta(PrefixPlan& p, gdpa_dtype dt, const PrefixIO& io, float* delta,
+                                cudaStream_t st) {
+    const int64_t rows = p.Tq * p.H;
+    if (rows == 0) return GDPA_OK;
+    const int64_t blocks = (rows + 7) / 8;
+    if (blocks > 0x7fffffff) return GDPA_ERR_UNSUPPORTED;
+    if (dt == GDPA_BF16)
+        delta_kernel<<<(unsigned)blocks, 256, 0, st>>>((const __nv_bfloat16*)io.d_o,
+                                                       (const __nv_bfloat16*)io.o, delta, rows, p.d);
+    else
+        delta_kernel<<<(unsigned)blocks, 256, 0, st>>>((const float*)io.d_o, (const float*)io.o,
+                                                       delta, rows, p.d);
+    p.launches += 1;
+    return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+}
+
+}  // namespace gdpa

@@ -99,6 +99,16 @@ def lib():
                                      ctypes.POINTER(ctypes.c_double), ctypes.c_float],
             "gdpa_rope_apply": [ctypes.POINTER(_RopeSpec), st, st, ctypes.c_int64, st,
                                 ctypes.POINTER(_RopeTensor), st, vp, st, vp, vp, st, vp],
+            "gdpa_prefix_create": [i32p, i32p, st, i32p, i32p, st, st, st, st, st, st, st, vp,
+                                   ctypes.POINTER(vp)],
+            "gdpa_prefix_create_host": [i32p, i32p, st, i32p, i32p, st, st, st, st, st, st, st,
+                                        ctypes.POINTER(vp)],
+            "gdpa_prefix_export": [vp, i32p, ctypes.c_int64, i64p, i32p],
+            "gdpa_prefix_set_kernel": [vp, st],
+            "gdpa_prefix_fwd": [vp, st] + [vp] * 7 + [ctypes.c_float, st, vp],
+            "gdpa_prefix_bwd": [vp, st] + [vp] * 13 + [ctypes.c_float, st, vp],
+            "gdpa_prefix_check": [vp, vp],
+            "gdpa_prefix_error_detail": [vp, i32p],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -108,6 +118,10 @@ def lib():
         L.gdpa_plan_launches.restype = ctypes.c_int64
         L.gdpa_plan_destroy.argtypes = [vp]
         L.gdpa_plan_destroy.restype = None
+        L.gdpa_prefix_launches.argtypes = [vp]
+        L.gdpa_prefix_launches.restype = ctypes.c_int64
+        L.gdpa_prefix_destroy.argtypes = [vp]
+        L.gdpa_prefix_destroy.restype = None
         L.gdpa_status_str.argtypes = [ctypes.c_int]
         L.gdpa_status_str.restype = ctypes.c_char_p
         _lib = L
@@ -671,3 +685,200 @@ def gdpa_rope_bwd(rope: Rope, dq, dk=None, positions=None, offsets=None, starts=
     """Gradients with respect to gdpa_rope_fwd's inputs, given those of its
     outputs (the inverse turn, the amplitude included); arguments alike."""
     return _rope(rope, 1, dq, dk, positions, offsets, starts, dq_out, dk_out, stream)
+
+
+class PrefixPlan:
+    """Plan of shared-prefix attention: samples in groups that share keys.
+
+    q_off, kv_off: int32 [B + 1] offsets of each sample's query rows and own
+    keys (kv_off None: no own keys).  group_off: int32 [G + 1], group g holds
+    samples group_off[g] .. group_off[g + 1].  prefix_off: int32 [G + 1], its
+    prefix is rows prefix_off[g] .. prefix_off[g + 1] of kp and vp.  H query
+    heads, ``kv_heads`` key heads (H unless given; a divisor of H).  mask,
+    window: over a sample's own keys, as Plan's; the prefix is always seen.
+
+    Belongs to the device that is current when it is made.
+    """
+
+    def __init__(self, q_off, kv_off, group_off, prefix_off, H: int, d: int, kv_heads=None,
+                 mask: str = "none", window: int = 0, num_sms: int = 0, stream=None,
+                 host_only: bool = False):
+        L = lib()
+        self._h = None
+        qo, qp = _i32(q_off)
+        ko, kp = _i32(np.zeros_like(qo) if kv_off is None else kv_off)
+        go, gp = _i32(group_off)
+        po, pp = _i32(prefix_off)
+        if qo.ndim != 1 or qo.shape != ko.shape or len(qo) < 1:
+            raise ValueError("q_off and kv_off must both have B + 1 entries")
+        if go.ndim != 1 or go.shape != po.shape or len(go) < 1:
+            raise ValueError("group_off and prefix_off must both have G + 1 entries")
+        self.B, self.G = len(qo) - 1, len(go) - 1
+        self.H, self.d = int(H), int(d)
+        self.Hkv = self.H if kv_heads is None else int(kv_heads)
+        self.Tq, self.Tkv, self.Tp = int(qo[-1]), int(ko[-1]), int(po[-1])
+        self.num_sms = int(num_sms)
+        h = ctypes.c_void_p()
+        args = (qp, kp, self.B, gp, pp, self.G, self.H, self.Hkv, self.d, MASK[mask], int(window),
+                int(num_sms))
+        self.device = None
+        if host_only:
+            _ok(L.gdpa_prefix_create_host(*args, ctypes.byref(h)), "gdpa_prefix_create_host")
+        else:
+            import torch
+            self.device = torch.cuda.current_device()
+            _ok(L.gdpa_prefix_create(*args, _stream_ptr(stream), ctypes.byref(h)),
+                "gdpa_prefix_create")
+        self._h = h
+
+    @property
+    def handle(self):
+        if self._h is None:
+            raise RuntimeError("plan destroyed")
+        return self._h
+
+    def export(self):
+        """(pieces int32 [n, 12], seg int32 [num_sms + 1]) of a plan made with
+        an explicit num_sms; columns as gdpa_prefix_export."""
+        n = ctypes.c_int64()
+        i32p = ctypes.POINTER(ctypes.c_int32)
+        seg = np.zeros(self.num_sms + 1, dtype=np.int32) if self.num_sms else None
+        lib().gdpa_prefix_export(self.handle, None, 0, ctypes.byref(n), None)
+        pieces = np.zeros((max(1, n.value), 12), dtype=np.int32)
+        _ok(lib().gdpa_prefix_export(self.handle, pieces.ctypes.data_as(i32p), n.value,
+                                     ctypes.byref(n),
+                                     None if seg is None else seg.ctypes.data_as(i32p)),
+            "gdpa_prefix_export")
+        return pieces[:n.value], seg
+
+    def set_kernel(self, kernel: str):
+        _ok(lib().gdpa_prefix_set_kernel(self.handle, KERNEL[kernel]), "gdpa_prefix_set_kernel")
+
+    def check(self, stream=None):
+        """Wait for the plan's work; raise if a kernel reported a failure."""
+        status = lib().gdpa_prefix_check(self.handle, _stream_ptr(stream))
+        if status != 0:
+            d = (ctypes.c_int32 * 4)()
+            lib().gdpa_prefix_error_detail(self.handle, d)
+            raise GdpaError(status, "gdpa_prefix_check (device code %d, wait site %d, CTA %d, %d)"
+                            % tuple(int(v) for v in d))
+
+    @property
+    def launches(self) -> int:
+        return int(lib().gdpa_prefix_launches(self.handle))
+
+    def destroy(self):
+        if getattr(self, "_h", None) is not None:
+            lib().gdpa_prefix_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+
+def _prefix_tensor(t, rows, heads, plan, name, dtype):
+    """Address of a checked [rows, heads, d] tensor (None for no rows)."""
+    if t is None and rows == 0:
+        return None
+    if not t.is_cuda or t.device.index != plan.device:
+        raise ValueError("%s must be on the plan's device cuda:%s" % (name, plan.device))
+    if t.shape != (rows, heads, plan.d):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), (rows, heads, plan.d)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s" % (name, dtype))
+    return t.data_ptr() if rows else None
+
+
+def _prefix_lse(lse, plan):
+    import torch
+    if (lse.dtype != torch.float32 or lse.shape != (plan.Tq, plan.H) or not lse.is_contiguous()
+            or not lse.is_cuda or lse.device.index != plan.device):
+        raise ValueError("lse must be a contiguous float32 [Tq, H] tensor on the plan's device")
+    return lse.data_ptr() if plan.Tq else None
+
+
+def _prefix_inputs(plan, q, kp, vp, k, v):
+    dt, dev = q.dtype, plan.device
+    if dev is None:
+        raise ValueError("a host-only plan cannot launch")
+    return [_prefix_tensor(q, plan.Tq, plan.H, plan, "q", dt),
+            _prefix_tensor(kp, plan.Tp, plan.Hkv, plan, "kp", dt),
+            _prefix_tensor(vp, plan.Tp, plan.Hkv, plan, "vp", dt),
+            _prefix_tensor(k, plan.Tkv, plan.Hkv, plan, "k", dt),
+            _prefix_tensor(v, plan.Tkv, plan.Hkv, plan, "v", dt)]
+
+
+def _prefix_stream(plan, stream):
+    import torch
+    return (torch.cuda.current_stream(plan.device) if stream is None else stream).cuda_stream
+
+
+def _prefix_fwd(plan, q, kp, vp, k, v, o, lse, alpha, act, stream):
+    ptrs = _prefix_inputs(plan, q, kp, vp, k, v)
+    o = q.new_empty(q.shape) if o is None else o
+    po = _prefix_tensor(o, plan.Tq, plan.H, plan, "o", q.dtype)
+    pl = None if lse is None else _prefix_lse(lse, plan)
+    with _current(q.device):
+        _ok(lib().gdpa_prefix_fwd(plan.handle, _dtype_id(q), *ptrs, po, pl,
+                                  plan.d ** -0.5 if alpha is None else alpha, ACT[act],
+                                  _prefix_stream(plan, stream)), "gdpa_prefix_fwd")
+    return o
+
+
+def gdpa_prefix_fwd(plan: PrefixPlan, q, kp, vp, k=None, v=None, o=None, alpha=None,
+                    act: str = "gelu_erf", stream=None):
+    """O ([Tq, H, d], dtype of q): every query attends to its group's prefix
+    (kp, vp [Tp, kv_heads, d]) and its sample's own keys (k, v [Tkv, kv_heads,
+    d]; None if there are none) with weights act(alpha q.k)."""
+    return _prefix_fwd(plan, q, kp, vp, k, v, o, None, alpha, act, stream)
+
+
+def gdpa_prefix_softmax_fwd(plan: PrefixPlan, q, kp, vp, k=None, v=None, o=None, lse=None,
+                            alpha=None, stream=None):
+    """The softmax variant over prefix and own keys together: (O, lse)."""
+    import torch
+    if lse is None:
+        lse = torch.empty((plan.Tq, plan.H), dtype=torch.float32, device=q.device)
+    return _prefix_fwd(plan, q, kp, vp, k, v, o, lse, alpha, "softmax", stream), lse
+
+
+def _prefix_bwd(plan, q, kp, vp, k, v, o, do, lse, grads, alpha, act, stream):
+    dt = q.dtype
+    ptrs = _prefix_inputs(plan, q, kp, vp, k, v)
+    po = None if o is None else _prefix_tensor(o, plan.Tq, plan.H, plan, "o", dt)
+    pdo = _prefix_tensor(do, plan.Tq, plan.H, plan, "do", dt)
+    pl = None if lse is None else _prefix_lse(lse, plan)
+    out, pg = [], []
+    for g, rows, heads, name in zip(grads, (plan.Tq, plan.Tp, plan.Tp, plan.Tkv, plan.Tkv),
+                                    (plan.H,) + (plan.Hkv,) * 4, ("dq", "dkp", "dvp", "dk", "dv")):
+        g = q.new_empty((rows, heads, plan.d)) if g is None else g
+        pg.append(_prefix_tensor(g, rows, heads, plan, name, dt))
+        out.append(g)
+    with _current(q.device):
+        _ok(lib().gdpa_prefix_bwd(plan.handle, _dtype_id(q), *ptrs, po, pdo, pl, *pg,
+                                  plan.d ** -0.5 if alpha is None else alpha, ACT[act],
+                                  _prefix_stream(plan, stream)), "gdpa_prefix_bwd")
+    return tuple(out)
+
+
+def gdpa_prefix_bwd(plan: PrefixPlan, q, kp, vp, k, v, do, dq=None, dkp=None, dvp=None, dk=None,
+                    dv=None, alpha=None, act: str = "gelu_erf", stream=None):
+    """(dQ, dKp, dVp, dK, dV) given dO, in the inputs' dtype: the prefix's
+    summed over the group's samples, key gradients over the query heads that
+    share a key head."""
+    if act == "softmax":
+        raise ValueError("the softmax variant's gradients come from gdpa_prefix_softmax_bwd")
+    return _prefix_bwd(plan, q, kp, vp, k, v, None, do, None, (dq, dkp, dvp, dk, dv), alpha, act,
+                       stream)
+
+
+def gdpa_prefix_softmax_bwd(plan: PrefixPlan, q, kp, vp, k, v, o, do, lse, dq=None, dkp=None,
+                            dvp=None, dk=None, dv=None, alpha=None, stream=None):
+    """(dQ, dKp, dVp, dK, dV) of the softmax variant from its forward's O and lse."""
+    return _prefix_bwd(plan, q, kp, vp, k, v, o, do, lse, (dq, dkp, dvp, dk, dv), alpha, "softmax",
+                       stream)
