@@ -194,8 +194,7 @@ gdpa_status check_inputs(const PrefixPlan& p, gdpa_dtype dtype, const PrefixIO& 
 
 // true when this plan and type run on the tensor-core kernels
 bool use_tc(const PrefixPlan& p, gdpa_dtype dt) {
-    (void)p; (void)dt;
-    return false;
+    return dt == GDPA_BF16 && p.kernel != GDPA_KERNEL_SIMT && (p.d == 64 || p.d == 128);
 }
 
 gdpa_status fwd(gdpa_prefix_plan plan, gdpa_dtype dtype, const PrefixIO& io, void* stream) {
@@ -211,7 +210,8 @@ gdpa_status fwd(gdpa_prefix_plan plan, gdpa_dtype dtype, const PrefixIO& io, voi
     std::lock_guard<std::mutex> hold(p.lock);
     const bool cap = capturing(st);
     if (gdpa_status s = begin_work(p, st, cap)) return s;
-    gdpa_status s = gdpa::launch_prefix_simt_fwd(p, dtype, io, st);
+    gdpa_status s = use_tc(p, dtype) ? gdpa::launch_prefix_tc_fwd(p, io, st)
+                                     : gdpa::launch_prefix_simt_fwd(p, dtype, io, st);
     if (s == GDPA_OK) s = gdpa::launch_prefix_merge(p, dtype, io.o, sm ? io.lse : nullptr, sm, st);
     const gdpa_status e = end_work(p, st, cap);
     return s != GDPA_OK ? s : e;

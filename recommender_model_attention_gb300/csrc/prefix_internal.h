@@ -114,6 +114,8 @@ gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t
 gdpa_status launch_prefix_simt_fwd(PrefixPlan& p, gdpa_dtype dt, const PrefixIO& io, cudaStream_t st);
 gdpa_status launch_prefix_simt_bwd(PrefixPlan& p, gdpa_dtype dt, const PrefixIO& io,
                                    const float* delta, cudaStream_t st);
+// Tensor-core forward (prefix_tc_fwd.cu; bf16, d = 64 or 128): the parts.
+gdpa_status launch_prefix_tc_fwd(PrefixPlan& p, const PrefixIO& io, cudaStream_t st);
 // Join the parts of every row: into O and lse (io.o, io.lse; normalised when
 // `softmax`), of element type dt.
 gdpa_status launch_prefix_merge(PrefixPlan& p, gdpa_dtype dt, void* out, float* lse, bool softmax,

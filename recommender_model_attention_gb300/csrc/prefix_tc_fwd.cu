@@ -1,0 +1,492 @@
+// Shared-prefix attention forward on the tensor cores (bf16 rows, d = 64 or
+// 128): the parts of every row tile, for the merge to join.
+//
+// One CTA per planned share walks its pieces.  A piece is one or two row
+// tiles (packed token by token, query heads of one key head side by side; a
+// 3-D TMA box does the packing) against a run of keys.  Two slots, each with
+// its own score and sum columns in TMEM (128 + d) and one warpgroup, a thread
+// a row:
+//   two tiles: slot s holds tile s, both read the same key blocks;
+//   one tile:  slot s takes the key blocks s, s + 2, ... of the same rows and
+//              gives a part of its own.
+// Warp 0 loads (TMA): the piece's query tiles, then K and V blocks through
+// one ring, in the order in which the tensor core takes them.  Warp 1 issues
+// S = Q K^T and O += P V: slot 0's P V and next S run while slot 1's weights
+// are computed, and the other way round.  The warpgroups keep the row maximum
+// as a reference that only moves when it would be passed by more than 8 (in
+// base 2: weights stay below 2^8), so O is rescaled in TMEM a few times a
+// piece rather than at every block; that S is complete says that the P V
+// before it is (they are issued in that order and commits follow all work
+// issued before), so the rescale needs no wait of its own.
+//
+// Rows of keys behind the piece's last one share its 16-row step: their
+// scores are masked by selection and the rows of V are cleared in shared
+// memory, so that what they hold (another sample's rows, infinities) does not
+// reach P V as 0 * inf.
+//
+// Every wait is bounded (csrc/tc_common.cuh); P is rounded to bf16 for the
+// product, the weights' sum is taken in float32 before that rounding.
+#include <cuda_bf16.h>
+
+#include "act.cuh"
+#include "prefix_internal.h"
+#include "tc_common.cuh"
+
+namespace gdpa {
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 64 + 256;
+constexpr int kHalfBytes = 128 * 128;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRise = 8.0f;   // the reference follows a maximum this far above it
+
+template <int D>
+struct PfCfg {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kTile = 128 * D * 2;
+    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffKV = 2 * kTile;
+    static constexpr int kOffBar = kOffKV + kStages * kTile;
+    enum {
+        kQFull = 0, kQEmpty, kFull, kEmpty = kFull + kStages, kSFull = kEmpty + kStages,
+        kPFull = kSFull + 2, kOFull = kPFull + 2, kOFree = kOFull + 2, kMmaDone = kOFree + 2, kNumBars
+    };
+    static constexpr int kSmem = kOffBar + kNumBars * 8 + 16 + 1024;
+};
+
+struct PfParams {
+    const PrefixPiece* pieces;
+    const int32_t* seg;
+    float* parts;
+    float* ml;
+    int r, tpt, windowed, window;
+    int q_bytes;      // bytes of one query tile's load
+    float alpha;
+    int32_t* err;
+    uint64_t wait_ns;
+};
+
+__device__ __forceinline__ PrefixPiece load_piece(const PrefixPiece* p) {
+    const int4* q = reinterpret_cast<const int4*>(p);
+    const int4 a = __ldg(q), b = __ldg(q + 1), c = __ldg(q + 2);
+    PrefixPiece t;
+    t.tok = a.x; t.nA = a.y; t.nB = a.z; t.hk = a.w;
+    t.k0 = b.x; t.nk = b.y; t.flags = b.z; t.i0 = b.w;
+    t.j0 = c.x; t.part0 = c.y; t.part1 = c.z; t.pad = 0;
+    return t;
+}
+
+// Blocks of a piece, of each slot, and where they lie in the ring (counted
+// from the piece's first load).
+struct Walk {
+    int nb, n0, n1;
+    bool dual;
+    __device__ __forceinline__ Walk(const PrefixPiece& p) {
+        nb = (p.nk + kBN - 1) / kBN;
+        dual = p.flags & kPieceDual;
+        n0 = dual ? (nb + 1) >> 1 : nb;
+        n1 = dual ? nb >> 1 : nb;
+    }
+    __device__ __forceinline__ int blocks(int s) const { return s ? n1 : n0; }
+    __device__ __forceinline__ int block(int s, int j) const { return dual ? 2 * j + s : j; }
+    // two tiles: K0 V0 K1 V1 ...; one tile: K0 K1 V0 K2 V1 K3 ...
+    __device__ __forceinline__ int k_at(int b) const { return dual ? (b < 2 ? b : 2 * b - 1) : 2 * b; }
+    __device__ __forceinline__ int v_at(int b) const { return dual ? min(b + 2, nb) + b : 2 * b + 1; }
+};
+
+__device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, void* dst,
+                                            int32_t x, int32_t y, int32_t z, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
+template <int D>
+__device__ void pf_producer(const CUtensorMap* tmQ, const CUtensorMap* tmKp, const CUtensorMap* tmVp,
+                            const CUtensorMap* tmK, const CUtensorMap* tmV, const PfParams& prm,
+                            uint8_t* smem, uint64_t* bars, int seg0, int seg1, const Abort& ab) {
+    using C = PfCfg<D>;
+    const uint64_t keep = policy_evict_last(), once = policy_evict_first();
+    int32_t q_armed = -1, armed[C::kStages];
+    for (int s = 0; s < C::kStages; ++s) armed[s] = -1;
+    uint32_t c = 0;
+    for (int t = seg0; t < seg1; ++t) {
+        const PrefixPiece p = load_piece(prm.pieces + t);
+        const Walk w(p);
+        const uint32_t n = (uint32_t)(t - seg0);
+        if (!mbar_wait(&bars[C::kQEmpty], (n & 1) ^ 1, ab, 61)) goto unwind;
+        mbar_arrive_expect_tx(&bars[C::kQFull], (uint32_t)(prm.q_bytes * (p.nB > 0 ? 2 : 1)));
+        q_armed = (int32_t)(n & 1);
+        for (int half = 0; half < (p.nB > 0 ? 2 : 1); ++half)
+#pragma unroll
+            for (int hf = 0; hf < C::kHalves; ++hf)
+                tma_load_3d(tmQ, &bars[C::kQFull], smem + C::kOffQ + half * C::kTile + hf * kHalfBytes,
+                            hf * 64, p.hk * prm.r, p.tok + half * p.nA, once);
+        const bool own = p.flags & kPieceOwn;
+        const CUtensorMap* mk = own ? tmK : tmKp;
+        const CUtensorMap* mv = own ? tmV : tmVp;
+        auto load = [&](const CUtensorMap* map, int b) -> bool {
+            const uint32_t st = c % C::kStages, ph = (c / C::kStages) & 1;
+            if (!mbar_wait(&bars[C::kEmpty + st], ph ^ 1, ab, 62)) return false;
+            mbar_arrive_expect_tx(&bars[C::kFull + st], C::kTile);
+            armed[st] = (int32_t)ph;
+#pragma unroll
+            for (int hf = 0; hf < C::kHalves; ++hf)
+                tma_load_2d(map, &bars[C::kFull + st], smem + C::kOffKV + st * C::kTile + hf * kHalfBytes,
+                            p.hk * D + hf * 64, p.k0 + b * kBN, keep);
+            ++c;
+            return true;
+        };
+        if (w.dual) {
+            for (int b = 0; b < w.nb + 2; ++b) {
+                if (b >= 2 && !load(mv, b - 2)) goto unwind;
+                if (b < w.nb && !load(mk, b)) goto unwind;
+            }
+        } else {
+            for (int b = 0; b < w.nb; ++b)
+                if (!load(mk, b) || !load(mv, b)) goto unwind;
+        }
+    }
+unwind:
+    // never leave the CTA with a TMA write still in flight
+    if (q_armed >= 0) mbar_wait_teardown(&bars[C::kQFull], (uint32_t)q_armed);
+    for (int s = 0; s < C::kStages; ++s)
+        if (armed[s] >= 0) mbar_wait_teardown(&bars[C::kFull + s], (uint32_t)armed[s]);
+}
+
+template <int D>
+__device__ void pf_mma(const PfParams& prm, uint8_t* smem, uint64_t* bars, uint32_t tmem, int seg0,
+                       int seg1, const Abort& ab) {
+    using C = PfCfg<D>;
+    constexpr uint32_t idesc_pv = idesc_bf16(128, D, false, true);
+    uint32_t base = 0, items[2] = {0, 0}, used[2] = {0, 0};   // blocks and pieces of each slot so far
+    for (int t = seg0; t < seg1; ++t) {
+        const PrefixPiece p = load_piece(prm.pieces + t);
+        const Walk w(p);
+        auto stage = [&](int at) { return (base + (uint32_t)at) % C::kStages; };
+        auto phase = [&](int at) { return ((base + (uint32_t)at) / C::kStages) & 1; };
+        auto n16 = [&](int b) { return (uint32_t)((min(kBN, p.nk - b * kBN) + 15) & ~15); };
+        auto issue_s = [&](int s, int j) -> bool {
+            const int b = w.block(s, j), at = w.k_at(b);
+            if (!wg_wait(&bars[C::kFull + stage(at)], phase(at), ab, 64)) return false;
+            tc_fence_after();
+            const uint64_t qd = smem_desc_sw128(
+                smem_u32(smem + C::kOffQ + (s && !w.dual ? C::kTile : 0)), 16, 1024);
+            const uint64_t kd = smem_desc_sw128(smem_u32(smem + C::kOffKV + stage(at) * C::kTile), 16, 1024);
+            const uint32_t id = idesc_bf16(128, n16(b), false, false);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+                mma_ss(tmem + s * 128, qd + kmajor_step(k), kd + kmajor_step(k), id, k > 0);
+            mma_commit(&bars[C::kSFull + s]);
+            if (w.dual || s == 1) mma_commit(&bars[C::kEmpty + stage(at)]);
+            // the piece's last S: its queries may be replaced
+            if (b == w.nb - 1 && (w.dual || s == 1)) mma_commit(&bars[C::kQEmpty]);
+            return true;
+        };
+        if (!wg_wait(&bars[C::kQFull], (uint32_t)(t - seg0) & 1, ab, 63)) goto drain;
+        for (int s = 0; s < 2; ++s)
+            if (w.blocks(s) > 0 && !issue_s(s, 0)) goto drain;
+        for (int j = 0; j < w.n0; ++j) {
+            for (int s = 0; s < 2; ++s) {
+                const int n = w.blocks(s);
+                if (j >= n) continue;
+                const int b = w.block(s, j), at = w.v_at(b);
+                // the slot's sums of its previous piece have been read
+                if (j == 0 && !wg_wait(&bars[C::kOFree + s], (used[s] & 1) ^ 1, ab, 65)) goto drain;
+                if (!wg_wait(&bars[C::kPFull + s], (items[s] + j) & 1, ab, 66)) goto drain;
+                if (!wg_wait(&bars[C::kFull + stage(at)], phase(at), ab, 67)) goto drain;
+                tc_fence_after();
+                const uint32_t vb = smem_u32(smem + C::kOffKV + stage(at) * C::kTile);
+                const uint64_t vd = smem_desc_sw128(vb, kHalfBytes, 1024);
+                const uint32_t steps = n16(b) / 16;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if ((uint32_t)k < steps)
+                        mma_ts(tmem + 256 + s * 128, tmem + s * 128 + 8 * k, vd + mnmajor_step(k), idesc_pv,
+                               j > 0 || k > 0);
+                if (w.dual || s == 1) mma_commit(&bars[C::kEmpty + stage(at)]);
+                if (j == n - 1)
+                    mma_commit(&bars[C::kOFull + s]);
+                else if (!issue_s(s, j + 1))
+                    goto drain;
+            }
+        }
+        for (int s = 0; s < 2; ++s)
+            if (w.blocks(s) > 0) {
+                items[s] += w.blocks(s);
+                used[s] += 1;
+            }
+        base += 2 * (uint32_t)w.nb;
+    }
+drain:
+    mma_commit(&bars[C::kMmaDone]);
+    mbar_wait_teardown(&bars[C::kMmaDone], 0);
+}
+
+template <int D, int ACT>
+__device__ void pf_rows(const PfParams& prm, uint8_t* smem, uint64_t* bars, uint32_t tmem, int seg0,
+                        int seg1, const Abort& ab) {
+    using C = PfCfg<D>;
+    constexpr bool kSm = ACT == kSoftmax;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int s = (warp - 2) >> 2;
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const int tid = (int)threadIdx.x - 64 - 128 * s;
+    const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t sc = trow + s * 128, oc = trow + 256 + s * 128;
+    const bool flip = kSm && prm.alpha < 0.0f;
+    ActScale ks = act_scale<ACT>(prm.alpha);
+    if (kSm) {   // (a zero scale would make NaN of masked scores)
+        ks.c0 = fabsf(ks.c0);
+        if (ks.c0 < 1e-30f) ks.c0 = 1e-30f;
+    }
+    uint32_t base = 0, items = 0, used = 0;
+    for (int t = seg0; t < seg1; ++t) {
+        const PrefixPiece p = load_piece(prm.pieces + t);
+        const Walk w(p);
+        const int n = w.blocks(s);
+        const int part = s ? p.part1 : p.part0;
+        const int shift = s && !w.dual ? p.nA : 0;              // tokens before this slot's
+        const int nrows = (s && !w.dual ? p.nB : p.nA) * prm.r;
+        const bool real = row < nrows;
+        const bool banded = (p.flags & kPieceOwn) && prm.windowed;
+        const int ipos = p.i0 + shift + row / prm.r;
+        float ref = -INFINITY, sum = 0.0f;
+        for (int j = 0; j < n; ++j) {
+            const int b = w.block(s, j);
+            const int nv = min(kBN, p.nk - b * kBN);
+            if (!wg_wait(&bars[C::kSFull + s], (items + j) & 1, ab, 71)) return;
+            tc_fence_after();
+            uint32_t x[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (c * 32 < nv) tmem_ld32(sc + c * 32, *reinterpret_cast<uint32_t(*)[32]>(x + c * 32));
+            tmem_ld_wait();
+            if (flip) {
+#pragma unroll
+                for (int e = 0; e < 128; ++e) x[e] ^= 0x80000000u;
+            }
+            if (nv < kBN || banded) {
+                // first and one past the last column this row sees
+                int lo = 0, hi = nv;
+                if (banded) {
+                    const int j0 = p.j0 + b * kBN;
+                    hi = min(hi, ipos - j0 + 1);
+                    lo = ipos - j0 >= prm.window ? ipos - j0 - prm.window + 1 : 0;
+                }
+#pragma unroll
+                for (int e = 0; e < 128; ++e)
+                    if (e < lo || e >= hi) x[e] = 0xff800000u;   // -inf
+            }
+            if constexpr (kSm) {
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int e = 0; e < 128; e += 4)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) m4[u] = fmaxf(m4[u], __uint_as_float(x[e + u]));
+                const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * ks.c0;
+                const bool up = real && top > ref + kRise;   // also from -inf
+                if (__any_sync(0xffffffffu, up)) {
+                    const float nref = up ? top : ref;
+                    const float f = up ? ex2_approx(ref - nref) : 1.0f;   // 0 from -inf
+                    ref = nref;
+                    sum *= f;
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(oc + c, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st16(oc + c, o);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+            }
+            const float nref = kSm ? (ref == -INFINITY ? 0.0f : -ref) : 0.0f;
+            uint64_t sum2 = f2_make(0.0f, 0.0f);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (c * 32 >= nv) continue;
+                uint32_t pk[16];
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    float p0, p1;
+                    const float s0 = __uint_as_float(x[c * 32 + e]), s1 = __uint_as_float(x[c * 32 + e + 1]);
+                    if constexpr (kSm) {
+                        const float2 tt = f2_split(f2_fma(f2_make(s0, s1), f2_make(ks.c0, ks.c0), f2_make(nref, nref)));
+                        p0 = ex2_approx(tt.x);
+                        p1 = ex2_approx(tt.y);
+                        sum2 = f2_fma(f2_make(p0, p1), f2_make(1.0f, 1.0f), sum2);
+                    } else {
+                        act_s2<ACT>(s0, s1, ks, p0, p1);
+                        if (nv < kBN || banded) {
+                            if (s0 == -INFINITY) p0 = 0.0f;
+                            if (s1 == -INFINITY) p1 = 0.0f;
+                        }
+                    }
+                    pk[e >> 1] = pack_bf16x2(p0, p1);
+                }
+                tmem_st16(sc + c * 16, pk);
+            }
+            if constexpr (kSm) {
+                const float2 a = f2_split(sum2);
+                sum += a.x + a.y;
+            }
+            tmem_st_wait();
+            if (nv & 15) {
+                // V rows behind the last key, inside its 16-row step
+                const int at = w.v_at(b);
+                const uint32_t st = (base + (uint32_t)at) % C::kStages, ph = ((base + (uint32_t)at) / C::kStages) & 1;
+                if (!wg_wait(&bars[C::kFull + st], ph, ab, 72)) return;
+                uint8_t* v = smem + C::kOffKV + st * C::kTile;
+                const int n0 = nv, cnt = ((nv + 15) & ~15) - nv;
+                for (int i = tid; i < cnt * (D / 8); i += 128) {
+                    const int rr = n0 + i / (D / 8), ch = i % (D / 8);
+                    *reinterpret_cast<uint4*>(v + (ch >> 3) * kHalfBytes + rr * 128 + ((ch & 7) << 4)) =
+                        make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+            }
+            tc_fence_before();
+            mbar_arrive(&bars[C::kPFull + s]);
+        }
+        if (n > 0) {
+            if (!wg_wait(&bars[C::kOFull + s], used & 1, ab, 73)) return;
+            tc_fence_after();
+            float4* out = reinterpret_cast<float4*>(prm.parts) + (int64_t)part * (D / 4) * 128 + row;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(oc + c * 32, o);
+                tmem_ld_wait();
+                if (real) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        out[(c * 8 + e) * 128] =
+                            make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                        __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(&bars[C::kOFree + s]);
+            if (kSm && real) reinterpret_cast<float2*>(prm.ml)[(int64_t)part * 128 + row] = make_float2(ref, sum);
+            items += n;
+            used += 1;
+        }
+        base += 2 * (uint32_t)w.nb;
+    }
+}
+
+template <int D, int ACT>
+__global__ void __launch_bounds__(kThreads, 1)
+prefix_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmKp,
+                  const __grid_constant__ CUtensorMap tmVp, const __grid_constant__ CUtensorMap tmK,
+                  const __grid_constant__ CUtensorMap tmV, const PfParams prm) {
+    using C = PfCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int seg0 = prm.seg[blockIdx.x], seg1 = prm.seg[blockIdx.x + 1];
+    if (seg0 == seg1) return;   // the whole CTA
+    if (threadIdx.x == 0) {
+        for (int b = 0; b < C::kNumBars; ++b) {
+            const bool rows = (b >= C::kPFull && b < C::kPFull + 2) || (b >= C::kOFree && b < C::kOFree + 2);
+            mbar_init(&bars[b], rows ? 128u : 1u);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmQ);
+        tma_prefetch_desc(&tmKp);
+        tma_prefetch_desc(&tmVp);
+    }
+    if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const Abort ab{abort_flag, prm.err, prm.wait_ns};
+    if (warp == 0) {
+        if (lane == 0) pf_producer<D>(&tmQ, &tmKp, &tmVp, &tmK, &tmV, prm, smem, bars, seg0, seg1, ab);
+        __syncwarp();
+    } else if (warp == 1) {
+        pf_mma<D>(prm, smem, bars, tmem, seg0, seg1, ab);
+        __syncwarp();
+    } else {
+        pf_rows<D, ACT>(prm, smem, bars, tmem, seg0, seg1, ab);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int D, int ACT>
+gdpa_status launch(PrefixPlan& p, const CUtensorMap* m, const PfParams& prm, cudaStream_t st) {
+    auto kern = prefix_fwd_kernel<D, ACT>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PfCfg<D>::kSmem) !=
+        cudaSuccess)
+        return GDPA_ERR_CUDA;
+    kern<<<p.S, kThreads, PfCfg<D>::kSmem, st>>>(m[0], m[1], m[2], m[3], m[4], prm);
+    p.launches += 1;
+    return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+}
+
+}  // namespace
+
+gdpa_status launch_prefix_tc_fwd(PrefixPlan& p, const PrefixIO& io, cudaStream_t st) {
+    if (p.pieces.empty()) return GDPA_OK;
+    CUtensorMap m[5];
+    const uint64_t krow = (uint64_t)p.Hkv * p.d;
+    // tensors without rows are never loaded from: any map will do
+    const void* kp = p.Tp ? io.kp : io.k;
+    const void* vp = p.Tp ? io.vp : io.v;
+    const void* k = p.Tkv ? io.k : io.kp;
+    const void* v = p.Tkv ? io.v : io.vp;
+    const uint64_t np = p.Tp ? p.Tp : p.Tkv, nk = p.Tkv ? p.Tkv : p.Tp;
+    if (!tc::make_tmap_rows(&m[0], io.q, p.Tq, p.H, p.d, p.r, p.tpt) ||
+        !tc::make_tmap_bf16(&m[1], kp, np, krow, 128) || !tc::make_tmap_bf16(&m[2], vp, np, krow, 128) ||
+        !tc::make_tmap_bf16(&m[3], k, nk, krow, 128) || !tc::make_tmap_bf16(&m[4], v, nk, krow, 128))
+        return GDPA_ERR_CUDA;
+    PfParams prm;
+    prm.pieces = p.dev_pieces();
+    prm.seg = p.dev_seg();
+    prm.parts = p.d_parts;
+    prm.ml = p.d_ml;
+    prm.r = p.r;
+    prm.tpt = p.tpt;
+    prm.windowed = p.mask == GDPA_MASK_CAUSAL_WINDOW;
+    prm.window = p.window;
+    prm.q_bytes = p.tpt * p.r * p.d * 2;
+    prm.alpha = io.alpha;
+    prm.err = p.dev_err();
+    prm.wait_ns = tc::wait_limit_ns(0);
+    gdpa_status s = GDPA_OK;
+    if (p.d == 128) {
+        if (io.act == kSoftmax)
+            s = launch<128, kSoftmax>(p, m, prm, st);
+        else
+            GDPA_DISPATCH_ACT(io.act, A, s = launch<128, A>(p, m, prm, st))
+    } else {
+        if (io.act == kSoftmax)
+            s = launch<64, kSoftmax>(p, m, prm, st);
+        else
+            GDPA_DISPATCH_ACT(io.act, A, s = launch<64, A>(p, m, prm, st))
+    }
+    return s;
+}
+
+}  // namespace gdpa

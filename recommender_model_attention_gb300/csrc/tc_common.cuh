@@ -472,5 +472,11 @@ bool make_tmap_bf16(CUtensorMap* map, const void* base, uint64_t rows, uint64_t 
 bool make_tmap_f32(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_elems,
                    uint32_t box_rows, uint32_t box_cols);
 
+// 3-D bf16 map over [tokens][heads][d] rows with a [box_tokens][box_heads][64]
+// box and 128-byte swizzle: box row t * box_heads + j is head j of token t
+// (query rows packed token by token).
+bool make_tmap_rows(CUtensorMap* map, const void* base, uint64_t tokens, uint32_t heads, uint32_t d,
+                    uint32_t box_heads, uint32_t box_tokens);
+
 }  // namespace tc
 }  // namespace gdpa

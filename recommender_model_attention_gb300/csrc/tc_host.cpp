@@ -61,5 +61,18 @@ bool make_tmap_f32(CUtensorMap* map, const void* base, uint64_t rows, uint64_t r
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tmap_rows(CUtensorMap* map, const void* base, uint64_t tokens, uint32_t heads, uint32_t d,
+                    uint32_t box_heads, uint32_t box_tokens) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || !base || tokens == 0) return false;
+    const cuuint64_t dims[3] = {d, heads, tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)heads * d * 2};
+    const cuuint32_t box[3] = {64, box_heads, box_tokens};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides,
+              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace tc
 }  // namespace gdpa
