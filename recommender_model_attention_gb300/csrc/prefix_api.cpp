@@ -141,19 +141,17 @@ gdpa_status create(const int32_t* q_off, const int32_t* kv_off, int B, const int
         }
         p->off_err = at;
         at += 256;
-        const size_t part = (size_t)d * gdpa::kBM * sizeof(float);
-        if (cudaMallocAsync((void**)&p->d_tables, at, st) != cudaSuccess) {
-            p->d_tables = nullptr;
-            s = GDPA_ERR_ALLOC;
-        } else if (p->n_parts > 0 &&
-                   (cudaMallocAsync((void**)&p->d_parts, p->n_parts * part, st) != cudaSuccess)) {
-            p->d_parts = nullptr;
-            s = GDPA_ERR_ALLOC;
-        } else if (p->n_parts > 0 && cudaMallocAsync((void**)&p->d_ml, p->n_parts * gdpa::kBM * 8, st) !=
-                                         cudaSuccess) {
-            p->d_ml = nullptr;
-            s = GDPA_ERR_ALLOC;
-        }
+        const size_t rows = (size_t)p->n_part_rows;
+        auto take = [&](void** dst, size_t bytes) {
+            if (s != GDPA_OK || bytes == 0) return;
+            if (cudaMallocAsync(dst, bytes, st) != cudaSuccess) {
+                *dst = nullptr;
+                s = GDPA_ERR_ALLOC;
+            }
+        };
+        take((void**)&p->d_tables, at);
+        take((void**)&p->d_parts, rows * d * sizeof(float));
+        take((void**)&p->d_ml, rows * 2 * sizeof(float));
         if (s == GDPA_ERR_ALLOC) cudaGetLastError();
         // pageable sources: the copies have read them when the calls return
         size_t pos = 0;
@@ -210,9 +208,14 @@ gdpa_status fwd(gdpa_prefix_plan plan, gdpa_dtype dtype, const PrefixIO& io, voi
     std::lock_guard<std::mutex> hold(p.lock);
     const bool cap = capturing(st);
     if (gdpa_status s = begin_work(p, st, cap)) return s;
-    gdpa_status s = use_tc(p, dtype) ? gdpa::launch_prefix_tc_fwd(p, io, st)
-                                     : gdpa::launch_prefix_simt_fwd(p, dtype, io, st);
-    if (s == GDPA_OK) s = gdpa::launch_prefix_merge(p, dtype, io.o, sm ? io.lse : nullptr, sm, st);
+    gdpa_status s;
+    if (use_tc(p, dtype)) {
+        s = gdpa::launch_prefix_tc_fwd(p, io, st);
+        if (s == GDPA_OK) s = gdpa::launch_prefix_own_merge(p, io, st);
+    } else {
+        s = gdpa::launch_prefix_simt_fwd(p, dtype, io, st);
+        if (s == GDPA_OK) s = gdpa::launch_prefix_merge(p, dtype, io.o, sm ? io.lse : nullptr, sm, st);
+    }
     const gdpa_status e = end_work(p, st, cap);
     return s != GDPA_OK ? s : e;
 }

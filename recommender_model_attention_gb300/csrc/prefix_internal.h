@@ -8,9 +8,14 @@
 // Parts.  Attention over a union of key ranges is taken range by range: each
 // piece of work gives, for the rows of one tile, unnormalised sums over its
 // keys (and, for softmax, the reference maximum and the weights' sum), in a
-// part of the plan's workspace; the merge joins the parts of every row.
-// Part p holds float4 columns [d / 4][128 rows] (so that a thread per row
-// writes and reads whole lines) and float2 (maximum, sum) [128 rows].
+// part of the plan's workspace; the merge joins the parts of every row.  A
+// part of n rows starts at a row offset of the workspace and holds float4
+// columns [d / 4][n] (so that a thread per row writes and reads whole lines)
+// and float2 (maximum in base 2, sum) [n].
+//
+// Own keys of few rows and keys ("small": the rule is in prefix_plan.cpp) are
+// taken by the tensor-core family's merge itself, which reads them once and
+// needs no part; the CUDA-core family walks their pieces like any other.
 #pragma once
 
 #include <mutex>
@@ -26,7 +31,7 @@ constexpr int kPieceDual = 2;   // one row tile: the slots take alternate key bl
 // One piece of forward work: keys [k0, k0 + nk) against one row tile of
 // tokens [tok, tok + nA), or two tiles, [tok, tok + nA) and the nB tokens
 // behind.  i0 / j0: positions of token `tok` and of key k0 in their sample
-// (own keys).  part[s]: where slot s's sums go (-1: slot unused).
+// (own keys).  part0/1: row offset of slot 0/1's sums (-1: unused).
 struct PrefixPiece {
     int32_t tok, nA, nB, hk;
     int32_t k0, nk, flags, i0;
@@ -43,19 +48,21 @@ struct PrefixUnit {
 static_assert(sizeof(PrefixUnit) == 32, "PrefixUnit layout");
 
 // One (row tile of a group, key head) for the merge: tokens [tok, tok + n),
-// prefix parts [part, part + layers).
+// prefix parts at row offsets part + i * n * r, i < layers.
 struct PrefixTile {
     int32_t tok, n, hk, part;
     int32_t layers, pad[3];
 };
 static_assert(sizeof(PrefixTile) == 32, "PrefixTile layout");
 
-// Per token: where the parts of its own keys are.  Head hk's are [part + hk *
-// layers, ...), its rows from row0 on; layers = 0 without own keys.
+// Per token, its own keys: head hk's parts are at part + (hk * layers + i) *
+// rows, the token's rows there from row0 on; layers = 0 without own keys.  The
+// keys themselves: rows [k0, k0 + nk), the token at position i of its sample.
 struct PrefixOwn {
-    int32_t part, row0, layers, pad;
+    int32_t part, row0, layers, rows;
+    int32_t k0, nk, i, small;
 };
-static_assert(sizeof(PrefixOwn) == 16, "PrefixOwn layout");
+static_assert(sizeof(PrefixOwn) == 32, "PrefixOwn layout");
 
 struct PrefixPlan {
     int device = 0;
@@ -64,8 +71,8 @@ struct PrefixPlan {
     int tpt = 128;               // tokens of a row tile
     int kernel = GDPA_KERNEL_AUTO;
     int64_t Tq = 0, Tkv = 0, Tp = 0;
-    int64_t n_parts = 0;
-    std::vector<PrefixPiece> pieces;
+    int64_t n_part_rows = 0;
+    std::vector<PrefixPiece> pieces; // the tensor-core family's, then the small own ones
     std::vector<int32_t> seg;        // [S + 1] first piece of each CTA
     std::vector<PrefixTile> tiles;
     std::vector<PrefixOwn> own;      // [Tq]
@@ -74,8 +81,8 @@ struct PrefixPlan {
     // device copies, one allocation (offsets below), and workspaces
     uint8_t* d_tables = nullptr;
     size_t off_seg = 0, off_tiles = 0, off_own = 0, off_units = 0, off_useg = 0, off_err = 0;
-    float* d_parts = nullptr;        // [n_parts][d / 4][128] float4
-    float* d_ml = nullptr;           // [n_parts][128] float2
+    float* d_parts = nullptr;        // [n_part_rows] x d floats
+    float* d_ml = nullptr;           // [n_part_rows] float2
     float* d_grad = nullptr;         // backward: delta [Tq][H], then float32 sums
     size_t grad_bytes = 0;
     int32_t last_err[4] = {0, 0, 0, 0};
@@ -116,6 +123,8 @@ gdpa_status launch_prefix_simt_bwd(PrefixPlan& p, gdpa_dtype dt, const PrefixIO&
                                    const float* delta, cudaStream_t st);
 // Tensor-core forward (prefix_tc_fwd.cu; bf16, d = 64 or 128): the parts.
 gdpa_status launch_prefix_tc_fwd(PrefixPlan& p, const PrefixIO& io, cudaStream_t st);
+// Its end (prefix_own.cu): the small own keys and the join of all parts.
+gdpa_status launch_prefix_own_merge(PrefixPlan& p, const PrefixIO& io, cudaStream_t st);
 // Join the parts of every row: into O and lse (io.o, io.lse; normalised when
 // `softmax`), of element type dt.
 gdpa_status launch_prefix_merge(PrefixPlan& p, gdpa_dtype dt, void* out, float* lse, bool softmax,

@@ -17,6 +17,11 @@ namespace {
 
 constexpr int kPieceCost = 3;   // steps a piece costs beside its own
 
+// Own keys of samples with at most this many packed rows and keys are taken
+// by the merge (prefix_own.cu), which streams them without a tile's latency.
+constexpr int kSmallRows = 64;
+constexpr int kSmallKeys = 512;
+
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct Unit {
@@ -48,9 +53,9 @@ gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t
     p.Tkv = kv_off[p.B];
     p.Tp = prefix_off[p.G];
     const int tpt = p.tpt;
-    int64_t parts = 0;
+    int64_t parts = 0;   // rows of the workspace given out
     std::vector<Unit> units;
-    p.own.assign((size_t)p.Tq, PrefixOwn{0, 0, 0, 0});
+    p.own.assign((size_t)p.Tq, PrefixOwn{0, 0, 0, 0, 0, 0, 0, 0});
     for (int g = 0; g < p.G; ++g) {
         const int32_t t0 = q_off[group_off[g]], nt = q_off[group_off[g + 1]] - t0;
         const int32_t np = prefix_off[g + 1] - prefix_off[g];
@@ -79,14 +84,19 @@ gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t
     const size_t n_prefix = units.size();
     // own keys: row tiles counted from the sample's first token
     const bool windowed = p.mask == GDPA_MASK_CAUSAL_WINDOW;
+    std::vector<Unit> small_units;
     for (int b = 0; b < p.B; ++b) {
         const int32_t lq = q_off[b + 1] - q_off[b], lk = kv_off[b + 1] - kv_off[b];
         if (lq == 0 || lk == 0) continue;
+        const bool small = (p.d == 64 || p.d == 128) && (int64_t)lq * p.r <= kSmallRows && lk <= kSmallKeys;
+        std::vector<Unit>& to = small ? small_units : units;
         for (int32_t i = 0; i < lq;) {
             const int32_t nA = std::min(tpt, lq - i), nB = std::min(tpt, lq - i - nA);
             // hull of the keys these rows see
             const int32_t lo = windowed ? std::max(0, i - p.window + 1) : 0;
             const int32_t hi = windowed ? std::min(lk, i + nA + nB) : lk;
+            for (int32_t t = 0; t < nA + nB; ++t)
+                p.own[q_off[b] + i + t] = PrefixOwn{0, 0, 0, 0, kv_off[b], lk, i + t, small ? 1 : 0};
             if (hi > lo) {
                 Unit u{};
                 u.tileA = u.tileB = -1;
@@ -100,22 +110,35 @@ gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t
                 u.p.j0 = lo;
                 u.steps = steps_of(u.p);
                 const int layers = nB == 0 && u.p.nk > kBN ? 2 : 1;
-                const size_t u0 = units.size();
+                const int32_t ra = nA * p.r, rb = nB * p.r;
+                const size_t u0 = to.size();
                 for (int hk = 0; hk < p.Hkv; ++hk) {
                     u.p.hk = hk;
-                    u.p.part0 = (int32_t)(parts + (int64_t)hk * layers);
-                    u.p.part1 = layers == 2 ? u.p.part0 + 1 : -1;
-                    units.push_back(u);
+                    u.p.part0 = (int32_t)(parts + (int64_t)hk * layers * ra);
+                    u.p.part1 = layers == 2 ? u.p.part0 + ra : -1;
+                    to.push_back(u);
                 }
-                for (int32_t t = 0; t < nA; ++t)
-                    p.own[u.p.tok + t] = PrefixOwn{(int32_t)parts, t * p.r, layers, 0};
-                parts += (int64_t)p.Hkv * layers;
+                for (int32_t t = 0; t < nA; ++t) {
+                    PrefixOwn& o = p.own[u.p.tok + t];
+                    o.part = (int32_t)parts;
+                    o.row0 = t * p.r;
+                    o.layers = layers;
+                    o.rows = ra;
+                }
+                parts += (int64_t)p.Hkv * layers * ra;
                 if (nB > 0) {
-                    for (int hk = 0; hk < p.Hkv; ++hk) units[u0 + hk].p.part1 = (int32_t)(parts + hk);
-                    for (int32_t t = 0; t < nB; ++t)
-                        p.own[u.p.tok + nA + t] = PrefixOwn{(int32_t)parts, t * p.r, 1, 0};
-                    parts += p.Hkv;
+                    for (int hk = 0; hk < p.Hkv; ++hk)
+                        to[u0 + hk].p.part1 = (int32_t)(parts + (int64_t)hk * rb);
+                    for (int32_t t = 0; t < nB; ++t) {
+                        PrefixOwn& o = p.own[u.p.tok + nA + t];
+                        o.part = (int32_t)parts;
+                        o.row0 = t * p.r;
+                        o.layers = 1;
+                        o.rows = rb;
+                    }
+                    parts += (int64_t)p.Hkv * rb;
                 }
+                if (parts > 0x7fffffff) return GDPA_ERR_UNSUPPORTED;
             }
             i += nA + nB;
         }
@@ -174,24 +197,34 @@ gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t
         size_t e = i;
         while (e < p.pieces.size() && !(p.pieces[e].flags & kPieceOwn) && p.pieces[e].pad == p.pieces[i].pad) ++e;
         const bool dual = u.p.flags & kPieceDual;
-        p.tiles[u.tileA].part = (int32_t)parts;
+        const int32_t ra = u.p.nA * p.r, rb = u.p.nB * p.r;
+        PrefixTile& ta = p.tiles[u.tileA];
+        ta.part = (int32_t)parts;
         for (size_t j = i; j < e; ++j) {
             PrefixPiece& q = p.pieces[j];
-            q.part0 = (int32_t)parts++;
+            q.part0 = (int32_t)parts;
+            parts += ra;
             q.part1 = -1;
-            if (dual && q.nk > kBN) q.part1 = (int32_t)parts++;
+            if (dual && q.nk > kBN) {
+                q.part1 = (int32_t)parts;
+                parts += ra;
+            }
         }
-        p.tiles[u.tileA].layers = (int32_t)(parts - p.tiles[u.tileA].part);
+        ta.layers = (int32_t)((parts - ta.part) / ra);
         if (!dual) {
             p.tiles[u.tileB].part = (int32_t)parts;
-            for (size_t j = i; j < e; ++j) p.pieces[j].part1 = (int32_t)parts++;
             p.tiles[u.tileB].layers = (int32_t)(e - i);
+            for (size_t j = i; j < e; ++j) {
+                p.pieces[j].part1 = (int32_t)parts;
+                parts += rb;
+            }
         }
+        if (parts > 0x7fffffff) return GDPA_ERR_UNSUPPORTED;
         i = e;
     }
     for (PrefixPiece& q : p.pieces) q.pad = 0;
-    if (parts > 0x7fffffff) return GDPA_ERR_UNSUPPORTED;
-    p.n_parts = parts;
+    for (const Unit& u : small_units) p.pieces.push_back(u.p);
+    p.n_part_rows = parts;
 
     // backward: one unit per 128-key block, against all rows that see it
     p.units.clear();

@@ -213,14 +213,14 @@ __global__ void __launch_bounds__(kThreads) simt_rows_kernel(const SimtArgs a) {
             }
         }
     }
-    float4* out = reinterpret_cast<float4*>(a.parts) + (int64_t)part * c4 * 128;
+    float4* out = reinterpret_cast<float4*>(a.parts) + (int64_t)part * c4;
 #pragma unroll
     for (int w = 0; w < kPer; ++w) {
         const int row = row0 + warp * kPer + w;
         if (row >= nrows) break;
-        if (lane < c4) out[lane * 128 + row] = acc[w];
+        if (lane < c4) out[lane * nrows + row] = acc[w];
         if (!BWD && ACT == kSoftmax && lane == 0)   // maximum in base 2, as the merge takes it
-            reinterpret_cast<float2*>(a.ml)[(int64_t)part * 128 + row] = make_float2(m[w] * kLog2e, l[w]);
+            reinterpret_cast<float2*>(a.ml)[(int64_t)part + row] = make_float2(m[w] * kLog2e, l[w]);
     }
 }
 
@@ -329,12 +329,13 @@ __global__ void __launch_bounds__(256) merge_kernel(const PrefixTile* tiles, con
     const int tl = row / r, j = row - tl * r;
     const int tok = t.tok + tl;
     const PrefixOwn ow = owns[tok];
-    const int own0 = ow.part + t.hk * ow.layers, orow = ow.row0 + j;
+    const int nr = t.n * r, orow = ow.row0 + j;
+    const int64_t own0 = (int64_t)ow.part + (int64_t)t.hk * ow.layers * ow.rows;
     const float2* st = reinterpret_cast<const float2*>(ml);
     float top = -INFINITY, sum = 0.f;
     if (softmax) {
-        for (int i = 0; i < t.layers; ++i) top = fmaxf(top, st[(int64_t)(t.part + i) * 128 + row].x);
-        for (int i = 0; i < ow.layers; ++i) top = fmaxf(top, st[(int64_t)(own0 + i) * 128 + orow].x);
+        for (int i = 0; i < t.layers; ++i) top = fmaxf(top, st[(int64_t)t.part + (int64_t)i * nr + row].x);
+        for (int i = 0; i < ow.layers; ++i) top = fmaxf(top, st[own0 + (int64_t)i * ow.rows + orow].x);
     }
     const float ref = top == -INFINITY ? 0.f : top;
     const int64_t at = (int64_t)tok * H + t.hk * r + j;
@@ -346,19 +347,19 @@ __global__ void __launch_bounds__(256) merge_kernel(const PrefixTile* tiles, con
         sum = 0.f;
         for (int i = 0; i < t.layers + ow.layers; ++i) {
             const bool pre = i < t.layers;
-            const int64_t part = pre ? t.part + i : own0 + i - t.layers;
-            const int prow = pre ? row : orow;
+            const int n = pre ? nr : ow.rows, prow = pre ? row : orow;
+            const int64_t part = pre ? t.part + (int64_t)i * nr : own0 + (int64_t)(i - t.layers) * n;
             float w = 1.f;
             if (softmax) {
-                const float2 s = st[part * 128 + prow];
+                const float2 s = st[part + prow];
                 w = exp2f(s.x - ref);   // 0 for a part without a visible key
                 sum = fmaf(w, s.y, sum);
                 if (s.x == -INFINITY) continue;
             }
-            const float4* src = reinterpret_cast<const float4*>(parts) + part * c4 * 128 + prow;
+            const float4* src = reinterpret_cast<const float4*>(parts) + part * c4 + prow;
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-                if (c + x < c4) axpy4(acc[x], w, src[(c + x) * 128]);
+                if (c + x < c4) axpy4(acc[x], w, src[(int64_t)(c + x) * n]);
         }
         const float inv = !softmax ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll

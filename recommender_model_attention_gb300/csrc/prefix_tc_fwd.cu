@@ -362,7 +362,7 @@ __device__ void pf_rows(const PfParams& prm, uint8_t* smem, uint64_t* bars, uint
         if (n > 0) {
             if (!wg_wait(&bars[C::kOFull + s], used & 1, ab, 73)) return;
             tc_fence_after();
-            float4* out = reinterpret_cast<float4*>(prm.parts) + (int64_t)part * (D / 4) * 128 + row;
+            float4* out = reinterpret_cast<float4*>(prm.parts) + (int64_t)part * (D / 4) + row;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -371,14 +371,14 @@ __device__ void pf_rows(const PfParams& prm, uint8_t* smem, uint64_t* bars, uint
                 if (real) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        out[(c * 8 + e) * 128] =
+                        out[(c * 8 + e) * nrows] =
                             make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
                                         __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
                 }
             }
             tc_fence_before();
             mbar_arrive(&bars[C::kOFree + s]);
-            if (kSm && real) reinterpret_cast<float2*>(prm.ml)[(int64_t)part * 128 + row] = make_float2(ref, sum);
+            if (kSm && real) reinterpret_cast<float2*>(prm.ml)[(int64_t)part + row] = make_float2(ref, sum);
             items += n;
             used += 1;
         }
@@ -448,7 +448,7 @@ gdpa_status launch(PrefixPlan& p, const CUtensorMap* m, const PfParams& prm, cud
 }  // namespace
 
 gdpa_status launch_prefix_tc_fwd(PrefixPlan& p, const PrefixIO& io, cudaStream_t st) {
-    if (p.pieces.empty()) return GDPA_OK;
+    if (p.seg[p.S] == 0) return GDPA_OK;
     CUtensorMap m[5];
     const uint64_t krow = (uint64_t)p.Hkv * p.d;
     // tensors without rows are never loaded from: any map will do

@@ -68,7 +68,8 @@ def _covered(plan, offs, H, Hkv, window):
     q_off, kv_off, g_off, p_off = offs
     r, tpt = H // Hkv, 128 // (H // Hkv)
     pieces, seg = plan.export()
-    assert seg[0] == 0 and seg[-1] == len(pieces) and np.all(np.diff(seg) >= 0)
+    assert seg[0] == 0 and np.all(np.diff(seg) >= 0) and seg[-1] <= len(pieces)
+    assert np.all(pieces[seg[-1]:, 6] & 1)   # behind the queues: small own pieces only
     pre = np.zeros((plan.Tq, Hkv, plan.Tp), dtype=np.int8)
     own = np.zeros((plan.Tq, Hkv, max(1, plan.Tkv)), dtype=np.int8)
     parts = []
@@ -78,11 +79,12 @@ def _covered(plan, offs, H, Hkv, window):
         if flags & 2:
             assert nb == 0 and (pb >= 0) == (nk > 128)
         to[tok:tok + na + nb, hk, k0:k0 + nk] += 1
-        parts += [p for p in (pa, pb) if p >= 0]
+        parts += [(p, n * r) for p, n in ((pa, na), (pb, na if flags & 2 else nb)) if p >= 0]
         if flags & 1:
             b = int(np.searchsorted(q_off, tok, side="right")) - 1
             assert tok == q_off[b] + i0 and k0 == kv_off[b] + j0
-    assert sorted(parts) == list(range(len(parts)))   # every part written once
+    parts.sort()   # rows of the workspace: one part behind the other
+    assert [p for p, _ in parts] == np.cumsum([0] + [n for _, n in parts]).tolist()[:-1]
     for rows, p, o, see in orc.groups(*offs, "causal_window" if window else "none", window):
         for hk in range(Hkv):
             assert np.all(pre[rows][:, hk][:, p] == 1)
