@@ -125,7 +125,7 @@ gdpa_status create(const int32_t* q_off, const int32_t* kv_off, int B, const int
         s = GDPA_ERR_ALLOC;
     }
     if (s == GDPA_OK && !host_only) {
-        // one table upload: pieces, seg, tiles, own, units, useg, error word
+        // one table upload: all lists, then the error word
         struct { const void* src; size_t bytes; size_t* off; } t[] = {
             {p->pieces.data(), p->pieces.size() * sizeof(gdpa::PrefixPiece), nullptr},
             {p->seg.data(), p->seg.size() * 4, &p->off_seg},
@@ -133,6 +133,7 @@ gdpa_status create(const int32_t* q_off, const int32_t* kv_off, int B, const int
             {p->own.data(), p->own.size() * sizeof(gdpa::PrefixOwn), &p->off_own},
             {p->units.data(), p->units.size() * sizeof(gdpa::PrefixUnit), &p->off_units},
             {p->useg.data(), p->useg.size() * 4, &p->off_useg},
+            {p->smalls.data(), p->smalls.size() * sizeof(gdpa::PrefixUnit), &p->off_smalls},
         };
         size_t at = 0;
         for (auto& e : t) {
@@ -250,7 +251,12 @@ gdpa_status bwd(gdpa_prefix_plan plan, gdpa_dtype dtype, const PrefixIO& io, voi
     }
     gdpa_status s = GDPA_OK;
     if (sm) s = gdpa::launch_prefix_delta(p, dtype, io, p.d_grad, st);
-    if (s == GDPA_OK) s = gdpa::launch_prefix_simt_bwd(p, dtype, io, p.d_grad, st);
+    if (use_tc(p, dtype)) {
+        if (s == GDPA_OK) s = gdpa::launch_prefix_own_bwd(p, io, p.d_grad, st);
+        if (s == GDPA_OK) s = gdpa::launch_prefix_tc_bwd(p, io, p.d_grad, st);
+    } else if (s == GDPA_OK) {
+        s = gdpa::launch_prefix_simt_bwd(p, dtype, io, p.d_grad, st);
+    }
     if (s == GDPA_OK) s = gdpa::launch_prefix_merge(p, dtype, io.dq, nullptr, false, st);
     const gdpa_status e = end_work(p, st, cap);
     return s != GDPA_OK ? s : e;

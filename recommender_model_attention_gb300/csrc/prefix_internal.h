@@ -76,11 +76,12 @@ struct PrefixPlan {
     std::vector<int32_t> seg;        // [S + 1] first piece of each CTA
     std::vector<PrefixTile> tiles;
     std::vector<PrefixOwn> own;      // [Tq]
-    std::vector<PrefixUnit> units;
+    std::vector<PrefixUnit> units;   // the tensor-core family's, then the small own ones
     std::vector<int32_t> useg;       // [S + 1] first unit of each CTA
+    std::vector<PrefixUnit> smalls;  // small own keys, whole: one per sample and key head
     // device copies, one allocation (offsets below), and workspaces
     uint8_t* d_tables = nullptr;
-    size_t off_seg = 0, off_tiles = 0, off_own = 0, off_units = 0, off_useg = 0, off_err = 0;
+    size_t off_seg = 0, off_tiles = 0, off_own = 0, off_units = 0, off_useg = 0, off_smalls = 0, off_err = 0;
     float* d_parts = nullptr;        // [n_part_rows] x d floats
     float* d_ml = nullptr;           // [n_part_rows] float2
     float* d_grad = nullptr;         // backward: delta [Tq][H], then float32 sums
@@ -99,6 +100,7 @@ struct PrefixPlan {
     const PrefixOwn* dev_own() const { return (const PrefixOwn*)(d_tables + off_own); }
     const PrefixUnit* dev_units() const { return (const PrefixUnit*)(d_tables + off_units); }
     const int32_t* dev_useg() const { return (const int32_t*)(d_tables + off_useg); }
+    const PrefixUnit* dev_smalls() const { return (const PrefixUnit*)(d_tables + off_smalls); }
     int32_t* dev_err() const { return (int32_t*)(d_tables + off_err); }
 };
 
@@ -125,6 +127,10 @@ gdpa_status launch_prefix_simt_bwd(PrefixPlan& p, gdpa_dtype dt, const PrefixIO&
 gdpa_status launch_prefix_tc_fwd(PrefixPlan& p, const PrefixIO& io, cudaStream_t st);
 // Its end (prefix_own.cu): the small own keys and the join of all parts.
 gdpa_status launch_prefix_own_merge(PrefixPlan& p, const PrefixIO& io, cudaStream_t st);
+// Tensor-core backward (prefix_tc_bwd.cu): dK, dV, and the parts of dQ, of all
+// but the small own keys, whose are prefix_own_bwd.cu's.
+gdpa_status launch_prefix_tc_bwd(PrefixPlan& p, const PrefixIO& io, const float* delta, cudaStream_t st);
+gdpa_status launch_prefix_own_bwd(PrefixPlan& p, const PrefixIO& io, const float* delta, cudaStream_t st);
 // Join the parts of every row: into O and lse (io.o, io.lse; normalised when
 // `softmax`), of element type dt.
 gdpa_status launch_prefix_merge(PrefixPlan& p, gdpa_dtype dt, void* out, float* lse, bool softmax,

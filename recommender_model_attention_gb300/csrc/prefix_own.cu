@@ -19,6 +19,7 @@
 
 #include "act.cuh"
 #include "prefix_internal.h"
+#include "prefix_mma.cuh"
 #include "tc_common.cuh"
 
 namespace gdpa {
@@ -39,25 +40,6 @@ struct OwnArgs {
     int windowed, window;
     float alpha;
 };
-
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint4 ldg16(const __nv_bfloat16* p) {
-    return __ldg(reinterpret_cast<const uint4*>(p));
-}
-
-// element e (0..7) of two 16-byte vectors as a packed pair (first: low half)
-__device__ __forceinline__ uint32_t pair_of(const uint4& x, const uint4& y, int e) {
-    const uint32_t a = (&x.x)[e >> 1], b = (&y.x)[e >> 1];
-    return __byte_perm(a, b, (e & 1) ? 0x7632 : 0x5410);
-}
 
 // Attention of packed rows [0, nrows) (<= 16; row i at q + qoff(i)) over keys
 // [0, nk): unnormalised sums into out[i][D + 4], (maximum, sum) into st[i].

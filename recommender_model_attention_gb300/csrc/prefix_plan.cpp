@@ -37,6 +37,10 @@ bool good_offsets(const int32_t* off, int n) {
     return true;
 }
 
+bool is_small(const PrefixPlan& p, int32_t lq, int32_t lk) {
+    return (p.d == 64 || p.d == 128) && (int64_t)lq * p.r <= kSmallRows && lk <= kSmallKeys;
+}
+
 int64_t steps_of(const PrefixPiece& p) {
     const int64_t nb = cdiv(p.nk, kBN);
     return p.flags & kPieceDual ? cdiv(nb, 2) : nb;
@@ -88,7 +92,7 @@ gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t
     for (int b = 0; b < p.B; ++b) {
         const int32_t lq = q_off[b + 1] - q_off[b], lk = kv_off[b + 1] - kv_off[b];
         if (lq == 0 || lk == 0) continue;
-        const bool small = (p.d == 64 || p.d == 128) && (int64_t)lq * p.r <= kSmallRows && lk <= kSmallKeys;
+        const bool small = is_small(p, lq, lk);
         std::vector<Unit>& to = small ? small_units : units;
         for (int32_t i = 0; i < lq;) {
             const int32_t nA = std::min(tpt, lq - i), nB = std::min(tpt, lq - i - nA);
@@ -105,11 +109,11 @@ gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t
                 u.p.nB = nB;
                 u.p.k0 = kv_off[b] + lo;
                 u.p.nk = hi - lo;
-                u.p.flags = kPieceOwn | (nB > 0 ? 0 : kPieceDual);
+                u.p.flags = kPieceOwn | (nB > 0 || small ? 0 : kPieceDual);
                 u.p.i0 = i;
                 u.p.j0 = lo;
                 u.steps = steps_of(u.p);
-                const int layers = nB == 0 && u.p.nk > kBN ? 2 : 1;
+                const int layers = u.p.flags & kPieceDual && u.p.nk > kBN ? 2 : 1;
                 const int32_t ra = nA * p.r, rb = nB * p.r;
                 const size_t u0 = to.size();
                 for (int hk = 0; hk < p.Hkv; ++hk) {
@@ -234,18 +238,41 @@ gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t
             for (int hk = 0; hk < p.Hkv; ++hk)
                 p.units.push_back(PrefixUnit{k, std::min(kBN, prefix_off[g + 1] - k), t0, nt, hk, 0, 0, 0});
     }
+    std::vector<PrefixUnit> small_blocks;
     for (int b = 0; b < p.B; ++b) {
         const int32_t lq = q_off[b + 1] - q_off[b], lk = kv_off[b + 1] - kv_off[b];
+        const bool small = lq > 0 && is_small(p, lq, lk);
         for (int32_t j = 0; j < lk; j += kBN) {
             const int32_t nk = std::min(kBN, lk - j);
             // queries j <= i < j + nk - 1 + window
             const int32_t lo = windowed ? std::min(lq, j) : 0;
             const int32_t hi = windowed ? (int32_t)std::min<int64_t>(lq, (int64_t)j + nk - 1 + p.window) : lq;
             for (int hk = 0; hk < p.Hkv; ++hk)
-                p.units.push_back(PrefixUnit{kv_off[b] + j, nk, q_off[b] + lo, std::max(0, hi - lo), hk,
-                                             kPieceOwn, lo, j});
+                (small ? small_blocks : p.units)
+                    .push_back(PrefixUnit{kv_off[b] + j, nk, q_off[b] + lo, std::max(0, hi - lo), hk, kPieceOwn,
+                                          lo, j});
         }
+        if (small)
+            for (int hk = 0; hk < p.Hkv && lk > 0; ++hk)
+                p.smalls.push_back(PrefixUnit{kv_off[b], lk, q_off[b], lq, hk, kPieceOwn, 0, 0});
     }
+    // deal them by their row tiles (and a unit's own loads and stores) in
+    // snake order, longest first
+    const int64_t n = (int64_t)p.units.size();
+    std::vector<std::vector<PrefixUnit>> queue((size_t)p.S);
+    std::stable_sort(p.units.begin(), p.units.end(),
+                     [](const PrefixUnit& x, const PrefixUnit& y) { return x.ntok > y.ntok; });
+    for (int64_t i = 0; i < n; ++i) {
+        const int64_t round = i / p.S, at = i % p.S;
+        queue[(size_t)(round & 1 ? p.S - 1 - at : at)].push_back(p.units[(size_t)i]);
+    }
+    p.units.clear();
+    p.useg.assign((size_t)p.S + 1, 0);
+    for (int c = 0; c < p.S; ++c) {
+        p.units.insert(p.units.end(), queue[(size_t)c].begin(), queue[(size_t)c].end());
+        p.useg[(size_t)c + 1] = (int32_t)p.units.size();
+    }
+    p.units.insert(p.units.end(), small_blocks.begin(), small_blocks.end());
     return GDPA_OK;
 }
 

@@ -1,0 +1,799 @@
+// Shared-prefix attention backward on the tensor cores (bf16 rows, d = 64 or
+// 128), as two kernels that each keep their result in TMEM until it is done:
+//
+//   dK, dV (prefix_dkv_kernel): a unit is a 128-key block of one key head
+//     against every packed query row that sees it.  Scores are formed
+//     transposed, S^T = K Q^T and dP^T = V dO^T, so that the weights leave the
+//     warps as the TMEM operand of the next products, dV += P^T dO and dK +=
+//     dS^T Q: nothing is staged in shared memory or transposed, and the keys'
+//     gradients, summed over all rows and heads, are rounded once.
+//   dQ (prefix_dq_kernel): a run is a row tile against a piece's key blocks,
+//     S = Q K^T, dP = dO V^T, dQ += dS K; the parts are joined by the merge.
+//
+// Forming the scores twice (7 products a tile instead of 5) is what it costs
+// to have no float32 dQ in memory: adding each tile's 64 KB to it atomically
+// would move more bytes through L2 than all operands, in an order that
+// changes the sums from run to run.  Results here are the same bits every time.
+//
+// Both walk items of 64 columns (query rows, or keys): two slots of TMEM
+// columns [S | dP], a warpgroup each, thread = lane.  While one slot's weights
+// are computed the tensor core runs the other slot's products and the next
+// scores: item e's closing products, then S and dP of item e + 2 into the same
+// columns.  Rows behind the last one of an item share its 16-row step: their
+// weights are zero by selection, and the rows themselves are cleared in
+// shared memory so that what lies there does not enter as 0 * inf.
+//
+// Every wait is bounded (csrc/tc_common.cuh).
+#include <cuda_bf16.h>
+
+#include "act.cuh"
+#include "prefix_internal.h"
+#include "tc_common.cuh"
+
+namespace gdpa {
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 64 + 256;
+constexpr int kHalfBytes = 128 * 128;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kItem = 64;   // columns of an item
+
+struct BwArgs {
+    const PrefixUnit* units;
+    const PrefixPiece* pieces;
+    const int32_t* seg;
+    const float* lse;
+    const float* delta;
+    float* parts;
+    __nv_bfloat16 *dkp, *dvp, *dk, *dv;
+    int H, Hkv, r, tpt, windowed, window;
+    int q_bytes;
+    float alpha;
+    int32_t* err;
+    uint64_t wait_ns;
+};
+
+__device__ __forceinline__ void load3(const CUtensorMap* map, uint64_t* bar, void* dst, int32_t x,
+                                      int32_t y, int32_t z, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
+// weights and score gradients of two pairs
+template <int ACT>
+__device__ __forceinline__ void weights2(float s0, float s1, float dp0, float dp1, const ActScale& k,
+                                         float l0, float l1, float d0, float d1, float& p0, float& p1,
+                                         float& ds0, float& ds1) {
+    if constexpr (ACT == kSoftmax) {
+        const float2 t = f2_split(f2_fma(f2_make(s0, s1), f2_make(k.c0, k.c0), f2_make(-l0, -l1)));
+        p0 = ex2_approx(t.x);
+        p1 = ex2_approx(t.y);
+        ds0 = p0 * (dp0 - d0);
+        ds1 = p1 * (dp1 - d1);
+    } else {
+        float a0, a1;
+        act_dact_s2<ACT>(s0, s1, k, p0, p1, a0, a1);
+        const float2 d = f2_split(f2_mul(f2_make(dp0, dp1), f2_make(a0, a1)));
+        ds0 = d.x;
+        ds1 = d.y;
+    }
+}
+
+// clear rows [r0, r1) of a [128][D] tile in shared memory (a warpgroup)
+template <int D>
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int r0, int r1, int tid) {
+    for (int i = tid; i < (r1 - r0) * (D / 8); i += 128) {
+        const int row = r0 + i / (D / 8), ch = i % (D / 8);
+        *reinterpret_cast<uint4*>(tile + (ch >> 3) * kHalfBytes + row * 128 + ((ch & 7) << 4)) =
+            make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+__device__ __forceinline__ void bar_wg(int id) {
+    asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
+}
+
+// ----------------------------------------------------------------- dK and dV
+
+template <int D>
+struct KvCfg {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kTile = 128 * D * 2;
+    static constexpr int kOffK = 0, kOffV = kTile, kOffQ = 2 * kTile, kOffDO = 4 * kTile;   // Q, dO: 2 stages
+    static constexpr int kOffStat = 6 * kTile;   // [slot][2][64] (lse, delta) pairs
+    static constexpr int kOffBar = kOffStat + 2 * 2 * 64 * 8;
+    enum { kKVFull = 0, kKVEmpty, kFull, kEmpty = kFull + 2, kSDFull = kEmpty + 2, kPFull = kSDFull + 2,
+           kAccFull = kPFull + 2, kAccFree, kMmaDone, kNumBars };
+    static constexpr int kSmem = kOffBar + kNumBars * 8 + 16 + 1024;
+};
+
+__device__ __forceinline__ PrefixUnit load_unit(const PrefixUnit* p) {
+    const int4* q = reinterpret_cast<const int4*>(p);
+    const int4 a = __ldg(q), b = __ldg(q + 1);
+    PrefixUnit u;
+    u.k0 = a.x; u.nk = a.y; u.tok = a.z; u.ntok = a.w;
+    u.hk = b.x; u.flags = b.y; u.i0 = b.z; u.j0 = b.w;
+    return u;
+}
+
+// rows of tile m of a unit, and its 64-row items
+__device__ __forceinline__ int tile_rows(const PrefixUnit& u, const BwArgs& a, int m) {
+    return min(a.tpt, u.ntok - m * a.tpt) * a.r;
+}
+
+template <int D>
+__device__ void kv_producer(const CUtensorMap* tmQ, const CUtensorMap* tmDO, const CUtensorMap* tmKp,
+                            const CUtensorMap* tmVp, const CUtensorMap* tmK, const CUtensorMap* tmV,
+                            const BwArgs& a, uint8_t* smem, uint64_t* bars, int seg0, int seg1,
+                            const Abort& ab) {
+    using C = KvCfg<D>;
+    const uint64_t keep = policy_evict_last(), once = policy_evict_first();
+    int32_t kv_armed = -1, armed[2] = {-1, -1};
+    uint32_t nu = 0, i = 0;
+    for (int t = seg0; t < seg1; ++t) {
+        const PrefixUnit u = load_unit(a.units + t);
+        const int tiles = (u.ntok + a.tpt - 1) / a.tpt;
+        if (tiles == 0) continue;
+        if (!mbar_wait(&bars[C::kKVEmpty], (nu & 1) ^ 1, ab, 81)) goto unwind;
+        mbar_arrive_expect_tx(&bars[C::kKVFull], 2 * C::kTile);
+        kv_armed = (int32_t)(nu & 1);
+        {
+            const bool own = u.flags & kPieceOwn;
+            const CUtensorMap *mk = own ? tmK : tmKp, *mv = own ? tmV : tmVp;
+#pragma unroll
+            for (int hf = 0; hf < C::kHalves; ++hf) {
+                tma_load_2d(mk, &bars[C::kKVFull], smem + C::kOffK + hf * kHalfBytes, u.hk * D + hf * 64,
+                            u.k0, once);
+                tma_load_2d(mv, &bars[C::kKVFull], smem + C::kOffV + hf * kHalfBytes, u.hk * D + hf * 64,
+                            u.k0, once);
+            }
+        }
+        for (int m = 0; m < tiles; ++m, ++i) {
+            const uint32_t st = i & 1, ph = (i >> 1) & 1;
+            if (!mbar_wait(&bars[C::kEmpty + st], ph ^ 1, ab, 82)) goto unwind;
+            mbar_arrive_expect_tx(&bars[C::kFull + st], 2 * (uint32_t)a.q_bytes);
+            armed[st] = (int32_t)ph;
+#pragma unroll
+            for (int hf = 0; hf < C::kHalves; ++hf) {
+                load3(tmQ, &bars[C::kFull + st], smem + C::kOffQ + st * C::kTile + hf * kHalfBytes, hf * 64,
+                      u.hk * a.r, u.tok + m * a.tpt, keep);
+                load3(tmDO, &bars[C::kFull + st], smem + C::kOffDO + st * C::kTile + hf * kHalfBytes, hf * 64,
+                      u.hk * a.r, u.tok + m * a.tpt, keep);
+            }
+        }
+        ++nu;
+    }
+unwind:
+    if (kv_armed >= 0) mbar_wait_teardown(&bars[C::kKVFull], (uint32_t)kv_armed);
+    for (int s = 0; s < 2; ++s)
+        if (armed[s] >= 0) mbar_wait_teardown(&bars[C::kFull + s], (uint32_t)armed[s]);
+}
+
+template <int D>
+__device__ void kv_mma(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t tmem, int seg0, int seg1,
+                       const Abort& ab) {
+    using C = KvCfg<D>;
+    constexpr uint32_t idesc_acc = idesc_bf16(128, D, false, true);
+    const uint64_t kd = smem_desc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
+    const uint64_t vd = smem_desc_sw128(smem_u32(smem + C::kOffV), 16, 1024);
+    uint32_t nu = 0, tile0 = 0, e0 = 0;   // units, tiles and items before this unit
+    for (int t = seg0; t < seg1; ++t) {
+        const PrefixUnit u = load_unit(a.units + t);
+        const int tiles = (u.ntok + a.tpt - 1) / a.tpt;
+        if (tiles == 0) continue;
+        const int full = a.tpt * a.r > kItem ? 2 : 1;   // items of every tile but the last
+        const int items = (tiles - 1) * full + (tile_rows(u, a, tiles - 1) + kItem - 1) / kItem;
+        auto rows16 = [&](int x) {
+            const int n = min(kItem, tile_rows(u, a, x / full) - (x % full) * kItem);
+            return (uint32_t)((n + 15) & ~15);
+        };
+        auto issue_s = [&](int x) -> bool {
+            const uint32_t st = (tile0 + x / full) & 1, ph = ((tile0 + x / full) >> 1) & 1;
+            if (!wg_wait(&bars[C::kFull + st], ph, ab, 84)) return false;
+            tc_fence_after();
+            const uint32_t col = tmem + ((e0 + x) & 1) * 128;
+            const uint32_t off = st * C::kTile + (x % full) * (kItem * 128);
+            const uint64_t qd = smem_desc_sw128(smem_u32(smem + C::kOffQ + off), 16, 1024);
+            const uint64_t dd = smem_desc_sw128(smem_u32(smem + C::kOffDO + off), 16, 1024);
+            const uint32_t id = idesc_bf16(128, rows16(x), false, false);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) mma_ss(col, kd + kmajor_step(k), qd + kmajor_step(k), id, k > 0);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) mma_ss(col + 64, vd + kmajor_step(k), dd + kmajor_step(k), id, k > 0);
+            mma_commit(&bars[C::kSDFull + ((e0 + x) & 1)]);
+            if (x == items - 1) mma_commit(&bars[C::kKVEmpty]);
+            return true;
+        };
+        if (!wg_wait(&bars[C::kKVFull], nu & 1, ab, 83)) goto drain;
+        if (!issue_s(0) || (items > 1 && !issue_s(1))) goto drain;
+        for (int x = 0; x < items; ++x) {
+            const uint32_t e = e0 + x, st = (tile0 + x / full) & 1;
+            if (x == 0 && !wg_wait(&bars[C::kAccFree], (nu & 1) ^ 1, ab, 85)) goto drain;
+            if (!wg_wait(&bars[C::kPFull + (e & 1)], (e >> 1) & 1, ab, 86)) goto drain;
+            tc_fence_after();
+            const uint32_t col = tmem + (e & 1) * 128;
+            const uint32_t off = st * C::kTile + (x % full) * (kItem * 128);
+            const uint64_t qd = smem_desc_sw128(smem_u32(smem + C::kOffQ + off), kHalfBytes, 1024);
+            const uint64_t dd = smem_desc_sw128(smem_u32(smem + C::kOffDO + off), kHalfBytes, 1024);
+            const uint32_t steps = rows16(x) / 16;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if ((uint32_t)k < steps)
+                    mma_ts(tmem + 256, col + 8 * k, dd + mnmajor_step(k), idesc_acc, x > 0 || k > 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if ((uint32_t)k < steps)
+                    mma_ts(tmem + 384, col + 64 + 8 * k, qd + mnmajor_step(k), idesc_acc, x > 0 || k > 0);
+            if (x % full == full - 1 || x == items - 1) mma_commit(&bars[C::kEmpty + st]);
+            if (x == items - 1) mma_commit(&bars[C::kAccFull]);
+            if (x + 2 < items && !issue_s(x + 2)) goto drain;
+        }
+        ++nu;
+        tile0 += tiles;
+        e0 += items;
+    }
+drain:
+    mma_commit(&bars[C::kMmaDone]);
+    mbar_wait_teardown(&bars[C::kMmaDone], 0);
+}
+
+// 32 packed columns of a row from the accumulator at `col` (scaled) as bf16
+__device__ __forceinline__ void store32(uint32_t col, float scale, __nv_bfloat16* dst, bool real) {
+    uint32_t v[32];
+    tmem_ld32(col, v);
+    tmem_ld_wait();
+    if (!real) return;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            w[e] = pack_bf16x2(__uint_as_float(v[8 * c + 2 * e]) * scale,
+                               __uint_as_float(v[8 * c + 2 * e + 1]) * scale);
+        reinterpret_cast<uint4*>(dst)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+template <int D, int ACT>
+__device__ void kv_rows(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t tmem, int seg0, int seg1,
+                        const Abort& ab) {
+    using C = KvCfg<D>;
+    constexpr bool kSm = ACT == kSoftmax;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int s = (warp - 2) >> 2, quarter = warp & 3;
+    const int key = quarter * 32 + lane;   // TMEM lane
+    const int tid = (int)threadIdx.x - 64 - 128 * s;
+    const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t col = trow + s * 128;
+    float2* stat = reinterpret_cast<float2*>(smem + C::kOffStat) + s * 128;   // [2][64]
+    const ActScale ks = act_scale<ACT>(a.alpha);
+    uint32_t nu = 0, tile0 = 0, e0 = 0;
+    for (int t = seg0; t < seg1; ++t) {
+        const PrefixUnit u = load_unit(a.units + t);
+        const bool own = u.flags & kPieceOwn;
+        const int tiles = (u.ntok + a.tpt - 1) / a.tpt;
+        __nv_bfloat16* dk = (own ? a.dk : a.dkp) + ((int64_t)(u.k0 + key) * a.Hkv + u.hk) * D;
+        __nv_bfloat16* dv = (own ? a.dv : a.dvp) + ((int64_t)(u.k0 + key) * a.Hkv + u.hk) * D;
+        const bool real = key < u.nk;
+        if (tiles == 0) {   // keys that no row sees
+            uint4* z = reinterpret_cast<uint4*>(s ? dk : dv);
+            if (real)
+                for (int c = 0; c < D / 8; ++c) z[c] = make_uint4(0u, 0u, 0u, 0u);
+            continue;
+        }
+        const int full = a.tpt * a.r > kItem ? 2 : 1;
+        const int items = (tiles - 1) * full + (tile_rows(u, a, tiles - 1) + kItem - 1) / kItem;
+        const bool banded = own && a.windowed;
+        const int jpos = u.j0 + key;
+        // this slot's items of the unit: those with (e0 + x) odd or even
+        int x = (int)((e0 ^ (uint32_t)s) & 1);
+        float2 next = make_float2(INFINITY, 0.0f);
+        auto stats = [&](int xi) -> float2 {   // of row tid of item xi
+            float2 v = make_float2(INFINITY, 0.0f);
+            if (kSm && tid < kItem && xi < items) {
+                const int row = (xi % full) * kItem + tid, m = xi / full;
+                if (row < tile_rows(u, a, m)) {
+                    const int tt = row / a.r;
+                    const int64_t at = (int64_t)(u.tok + m * a.tpt + tt) * a.H + u.hk * a.r + (row - tt * a.r);
+                    const float l = a.lse[at];
+                    v.x = l == -INFINITY ? INFINITY : l * kLog2e;   // a row without keys: weights 0
+                    v.y = a.delta[at];
+                }
+            }
+            return v;
+        };
+        if (kSm) next = stats(x);
+        for (; x < items; x += 2) {
+            const uint32_t e = e0 + x, buf = (e >> 1) & 1;
+            const int m = x / full, r0 = (x % full) * kItem;
+            const int n = min(kItem, tile_rows(u, a, m) - r0);
+            float2* sb = stat + buf * kItem;
+            if (kSm) {
+                if (tid < kItem) sb[tid] = next;
+                next = stats(x + 2);
+                bar_wg(1 + s);
+            }
+            if (!wg_wait(&bars[C::kSDFull + s], (e >> 1) & 1, ab, 91)) return;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (c * 16 >= n) continue;
+                uint32_t sv[16], dv16[16], pk[8], dk8[8];
+                tmem_ld16(col + c * 16, sv);
+                tmem_ld16(col + 64 + c * 16, dv16);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    float l0 = 0.f, l1 = 0.f, d0 = 0.f, d1 = 0.f, p0, p1, g0, g1;
+                    if constexpr (kSm) {
+                        const float4 st = *reinterpret_cast<const float4*>(sb + c * 16 + i);
+                        l0 = st.x; d0 = st.y; l1 = st.z; d1 = st.w;
+                    }
+                    weights2<ACT>(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1]),
+                                  __uint_as_float(dv16[i]), __uint_as_float(dv16[i + 1]), ks, l0, l1, d0, d1,
+                                  p0, p1, g0, g1);
+                    if (banded || n < kItem) {
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) {
+                            const int row = c * 16 + i + w;
+                            bool ok = row < n;
+                            if (banded) {
+                                const int ipos = u.i0 + m * a.tpt + (r0 + row) / a.r;
+                                ok = ok && jpos <= ipos && jpos > ipos - a.window;
+                            }
+                            if (!ok) (w ? p1 : p0) = (w ? g1 : g0) = 0.0f;
+                        }
+                    }
+                    pk[i >> 1] = pack_bf16x2(p0, p1);
+                    dk8[i >> 1] = pack_bf16x2(g0, g1);
+                }
+                tmem_st8(col + c * 8, pk);
+                tmem_st8(col + 64 + c * 8, dk8);
+            }
+            tmem_st_wait();
+            if (n & 15) {
+                const uint32_t st = (tile0 + m) & 1;
+                clear_rows<D>(smem + C::kOffQ + st * C::kTile, r0 + n, r0 + ((n + 15) & ~15), tid);
+                clear_rows<D>(smem + C::kOffDO + st * C::kTile, r0 + n, r0 + ((n + 15) & ~15), tid);
+                fence_proxy_async_smem();
+            }
+            tc_fence_before();
+            mbar_arrive(&bars[C::kPFull + s]);
+        }
+        if (!wg_wait(&bars[C::kAccFull], nu & 1, ab, 92)) return;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < D; c += 32)
+            store32(trow + (s ? 384 : 256) + c, s ? a.alpha : 1.0f, (s ? dk : dv) + c, real);
+        tc_fence_before();
+        mbar_arrive(&bars[C::kAccFree]);
+        ++nu;
+        tile0 += tiles;
+        e0 += items;
+    }
+}
+
+template <int D, int ACT>
+__global__ void __launch_bounds__(kThreads, 1)
+prefix_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
+                  const __grid_constant__ CUtensorMap tmKp, const __grid_constant__ CUtensorMap tmVp,
+                  const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                  const BwArgs a) {
+    using C = KvCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int seg0 = a.seg[blockIdx.x], seg1 = a.seg[blockIdx.x + 1];
+    if (seg0 == seg1) return;
+    if (threadIdx.x == 0) {
+        for (int b = 0; b < C::kNumBars; ++b)
+            mbar_init(&bars[b], b == C::kPFull || b == C::kPFull + 1 ? 128u : b == C::kAccFree ? 256u : 1u);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const Abort ab{abort_flag, a.err, a.wait_ns};
+    if (warp == 0) {
+        if (lane == 0) kv_producer<D>(&tmQ, &tmDO, &tmKp, &tmVp, &tmK, &tmV, a, smem, bars, seg0, seg1, ab);
+        __syncwarp();
+    } else if (warp == 1) {
+        kv_mma<D>(a, smem, bars, tmem, seg0, seg1, ab);
+        __syncwarp();
+    } else {
+        kv_rows<D, ACT>(a, smem, bars, tmem, seg0, seg1, ab);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ------------------------------------------------------------------------ dQ
+
+template <int D>
+struct DqCfg {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kTile = 128 * D * 2;
+    static constexpr int kStages = D == 128 ? 5 : 8;   // K and V tiles in turn
+    static constexpr int kOffQ = 0, kOffDO = kTile, kOffKV = 2 * kTile;
+    static constexpr int kOffBar = kOffKV + kStages * kTile;
+    enum { kQFull = 0, kQEmpty, kFull, kEmpty = kFull + kStages, kSDFull = kEmpty + kStages,
+           kPFull = kSDFull + 2, kAccFull = kPFull + 2, kAccFree, kMmaDone, kNumBars };
+    static constexpr int kSmem = kOffBar + kNumBars * 8 + 16 + 1024;
+};
+
+__device__ __forceinline__ PrefixPiece load_piece(const PrefixPiece* p) {
+    const int4* q = reinterpret_cast<const int4*>(p);
+    const int4 a = __ldg(q), b = __ldg(q + 1), c = __ldg(q + 2);
+    PrefixPiece t;
+    t.tok = a.x; t.nA = a.y; t.nB = a.z; t.hk = a.w;
+    t.k0 = b.x; t.nk = b.y; t.flags = b.z; t.i0 = b.w;
+    t.j0 = c.x; t.part0 = c.y; t.part1 = c.z; t.pad = 0;
+    return t;
+}
+
+// A run: one row tile against the key blocks of one slot of a piece.
+struct Run {
+    int tok, rows, i0, part, blocks, step, first;
+    int nk;
+    __device__ __forceinline__ Run(const PrefixPiece& p, int s, int r) {
+        const int nb = (p.nk + kBN - 1) / kBN;
+        const bool dual = p.flags & kPieceDual;
+        const bool second = s && !dual;
+        tok = p.tok + (second ? p.nA : 0);
+        i0 = p.i0 + (second ? p.nA : 0);
+        rows = (second ? p.nB : p.nA) * r;
+        part = s ? p.part1 : p.part0;
+        step = dual ? 2 : 1;
+        first = dual ? s : 0;
+        blocks = part < 0 ? 0 : dual ? (s ? nb >> 1 : (nb + 1) >> 1) : nb;
+        nk = p.nk;
+    }
+    __device__ __forceinline__ int block(int j) const { return first + j * step; }
+    __device__ __forceinline__ int keys(int j) const { return min(kBN, nk - block(j) * kBN); }
+    // items of 64 keys: two a block but for a short last one
+    __device__ __forceinline__ int items() const {
+        return blocks == 0 ? 0 : 2 * (blocks - 1) + (keys(blocks - 1) > kItem ? 2 : 1);
+    }
+};
+
+template <int D>
+__device__ void dq_producer(const CUtensorMap* tmQ, const CUtensorMap* tmDO, const CUtensorMap* tmKp,
+                            const CUtensorMap* tmVp, const CUtensorMap* tmK, const CUtensorMap* tmV,
+                            const BwArgs& a, uint8_t* smem, uint64_t* bars, int seg0, int seg1,
+                            const Abort& ab) {
+    using C = DqCfg<D>;
+    const uint64_t keep = policy_evict_last(), once = policy_evict_first();
+    int32_t q_armed = -1, armed[C::kStages];
+    for (int s = 0; s < C::kStages; ++s) armed[s] = -1;
+    uint32_t nr = 0, c = 0;
+    for (int t = 2 * seg0; t < 2 * seg1; ++t) {
+        const PrefixPiece p = load_piece(a.pieces + (t >> 1));
+        const Run run(p, t & 1, a.r);
+        if (run.blocks == 0) continue;
+        if (!mbar_wait(&bars[C::kQEmpty], (nr & 1) ^ 1, ab, 101)) goto unwind;
+        mbar_arrive_expect_tx(&bars[C::kQFull], 2 * (uint32_t)a.q_bytes);
+        q_armed = (int32_t)(nr & 1);
+#pragma unroll
+        for (int hf = 0; hf < C::kHalves; ++hf) {
+            load3(tmQ, &bars[C::kQFull], smem + C::kOffQ + hf * kHalfBytes, hf * 64, p.hk * a.r, run.tok, once);
+            load3(tmDO, &bars[C::kQFull], smem + C::kOffDO + hf * kHalfBytes, hf * 64, p.hk * a.r, run.tok, once);
+        }
+        const bool own = p.flags & kPieceOwn;
+        for (int j = 0; j < run.blocks; ++j)
+            for (int kv = 0; kv < 2; ++kv, ++c) {
+                const CUtensorMap* map = kv ? (own ? tmV : tmVp) : (own ? tmK : tmKp);
+                const uint32_t st = c % C::kStages, ph = (c / C::kStages) & 1;
+                if (!mbar_wait(&bars[C::kEmpty + st], ph ^ 1, ab, 102)) goto unwind;
+                mbar_arrive_expect_tx(&bars[C::kFull + st], C::kTile);
+                armed[st] = (int32_t)ph;
+#pragma unroll
+                for (int hf = 0; hf < C::kHalves; ++hf)
+                    tma_load_2d(map, &bars[C::kFull + st], smem + C::kOffKV + st * C::kTile + hf * kHalfBytes,
+                                p.hk * D + hf * 64, p.k0 + run.block(j) * kBN, keep);
+            }
+        ++nr;
+    }
+unwind:
+    if (q_armed >= 0) mbar_wait_teardown(&bars[C::kQFull], (uint32_t)q_armed);
+    for (int s = 0; s < C::kStages; ++s)
+        if (armed[s] >= 0) mbar_wait_teardown(&bars[C::kFull + s], (uint32_t)armed[s]);
+}
+
+template <int D>
+__device__ void dq_mma(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t tmem, int seg0, int seg1,
+                       const Abort& ab) {
+    using C = DqCfg<D>;
+    constexpr uint32_t idesc_acc = idesc_bf16(128, D, false, true);
+    const uint64_t qd = smem_desc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
+    const uint64_t dd = smem_desc_sw128(smem_u32(smem + C::kOffDO), 16, 1024);
+    uint32_t nr = 0, ring = 0, e0 = 0;
+    for (int t = 2 * seg0; t < 2 * seg1; ++t) {
+        const PrefixPiece p = load_piece(a.pieces + (t >> 1));
+        const Run run(p, t & 1, a.r);
+        if (run.blocks == 0) continue;
+        const int items = run.items();
+        auto n16 = [&](int x) {
+            return (uint32_t)((min(kItem, run.keys(x >> 1) - (x & 1) * kItem) + 15) & ~15);
+        };
+        auto last_of = [&](int x) { return (x & 1) || x == items - 1; };   // of its block
+        auto stage = [&](int x, int kv) { return (ring + 2 * (uint32_t)(x >> 1) + kv) % C::kStages; };
+        auto phase = [&](int x, int kv) { return ((ring + 2 * (uint32_t)(x >> 1) + kv) / C::kStages) & 1; };
+        auto issue_s = [&](int x) -> bool {
+            const uint32_t sk = stage(x, 0), sv = stage(x, 1);
+            if (!wg_wait(&bars[C::kFull + sk], phase(x, 0), ab, 104)) return false;
+            if (!wg_wait(&bars[C::kFull + sv], phase(x, 1), ab, 105)) return false;
+            tc_fence_after();
+            const uint32_t col = tmem + ((e0 + x) & 1) * 128, off = (x & 1) * (kItem * 128);
+            const uint64_t kd = smem_desc_sw128(smem_u32(smem + C::kOffKV + sk * C::kTile + off), 16, 1024);
+            const uint64_t vd = smem_desc_sw128(smem_u32(smem + C::kOffKV + sv * C::kTile + off), 16, 1024);
+            const uint32_t id = idesc_bf16(128, n16(x), false, false);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) mma_ss(col, qd + kmajor_step(k), kd + kmajor_step(k), id, k > 0);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) mma_ss(col + 64, dd + kmajor_step(k), vd + kmajor_step(k), id, k > 0);
+            mma_commit(&bars[C::kSDFull + ((e0 + x) & 1)]);
+            if (last_of(x)) mma_commit(&bars[C::kEmpty + sv]);
+            if (x == items - 1) mma_commit(&bars[C::kQEmpty]);
+            return true;
+        };
+        if (!wg_wait(&bars[C::kQFull], nr & 1, ab, 103)) goto drain;
+        if (!issue_s(0) || (items > 1 && !issue_s(1))) goto drain;
+        for (int x = 0; x < items; ++x) {
+            const uint32_t e = e0 + x;
+            if (x == 0 && !wg_wait(&bars[C::kAccFree], (nr & 1) ^ 1, ab, 106)) goto drain;
+            if (!wg_wait(&bars[C::kPFull + (e & 1)], (e >> 1) & 1, ab, 107)) goto drain;
+            tc_fence_after();
+            const uint32_t sk = stage(x, 0);
+            const uint64_t kd = smem_desc_sw128(
+                smem_u32(smem + C::kOffKV + sk * C::kTile + (x & 1) * (kItem * 128)), kHalfBytes, 1024);
+            const uint32_t steps = n16(x) / 16;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if ((uint32_t)k < steps)
+                    mma_ts(tmem + 256, tmem + (e & 1) * 128 + 8 * k, kd + mnmajor_step(k), idesc_acc, x > 0 || k > 0);
+            if (last_of(x)) mma_commit(&bars[C::kEmpty + sk]);
+            if (x == items - 1) mma_commit(&bars[C::kAccFull]);
+            if (x + 2 < items && !issue_s(x + 2)) goto drain;
+        }
+        ++nr;
+        ring += 2 * (uint32_t)run.blocks;
+        e0 += items;
+    }
+drain:
+    mma_commit(&bars[C::kMmaDone]);
+    mbar_wait_teardown(&bars[C::kMmaDone], 0);
+}
+
+template <int D, int ACT>
+__device__ void dq_rows(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t tmem, int seg0, int seg1,
+                        const Abort& ab) {
+    using C = DqCfg<D>;
+    constexpr bool kSm = ACT == kSoftmax;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int s = (warp - 2) >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const int tid = (int)threadIdx.x - 64 - 128 * s;
+    const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t col = trow + s * 128;
+    const ActScale ks = act_scale<ACT>(a.alpha);
+    const int rt = row / a.r, rj = row - rt * a.r;
+    uint32_t nr = 0, ring = 0, e0 = 0;
+    for (int t = 2 * seg0; t < 2 * seg1; ++t) {
+        const PrefixPiece p = load_piece(a.pieces + (t >> 1));
+        const Run run(p, t & 1, a.r);
+        if (run.blocks == 0) continue;
+        const int items = run.items();
+        const bool real = row < run.rows;
+        const bool banded = (p.flags & kPieceOwn) && a.windowed;
+        const int ipos = run.i0 + rt;
+        float lse2 = INFINITY, delta = 0.0f;
+        if (kSm && real) {
+            const int64_t at = (int64_t)(run.tok + rt) * a.H + p.hk * a.r + rj;
+            const float l = a.lse[at];
+            lse2 = l == -INFINITY ? INFINITY : l * kLog2e;
+            delta = a.delta[at];
+        }
+        for (int x = (int)((e0 ^ (uint32_t)s) & 1); x < items; x += 2) {
+            const uint32_t e = e0 + x;
+            const int n = min(kItem, run.keys(x >> 1) - (x & 1) * kItem);
+            const int j0 = p.j0 + run.block(x >> 1) * kBN + (x & 1) * kItem;
+            int lo = 0, hi = n;   // columns this row sees
+            if (banded) {
+                hi = min(hi, ipos - j0 + 1);
+                lo = ipos - j0 >= a.window ? ipos - j0 - a.window + 1 : 0;
+            }
+            if (!wg_wait(&bars[C::kSDFull + s], (e >> 1) & 1, ab, 111)) return;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (c * 16 >= n) continue;
+                uint32_t sv[16], dv16[16], dk8[8];
+                tmem_ld16(col + c * 16, sv);
+                tmem_ld16(col + 64 + c * 16, dv16);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    float p0, p1, g0, g1;
+                    weights2<ACT>(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1]),
+                                  __uint_as_float(dv16[i]), __uint_as_float(dv16[i + 1]), ks, lse2, lse2, delta,
+                                  delta, p0, p1, g0, g1);
+                    if (banded || n < kItem) {
+                        if (c * 16 + i < lo || c * 16 + i >= hi) g0 = 0.0f;
+                        if (c * 16 + i + 1 < lo || c * 16 + i + 1 >= hi) g1 = 0.0f;
+                    }
+                    dk8[i >> 1] = pack_bf16x2(g0, g1);
+                }
+                tmem_st8(col + c * 8, dk8);
+            }
+            tmem_st_wait();
+            if (n & 15) {
+                const uint32_t sk = (ring + 2 * (uint32_t)(x >> 1)) % C::kStages;
+                const int r0 = (x & 1) * kItem;
+                clear_rows<D>(smem + C::kOffKV + sk * C::kTile, r0 + n, r0 + ((n + 15) & ~15), tid);
+                fence_proxy_async_smem();
+            }
+            tc_fence_before();
+            mbar_arrive(&bars[C::kPFull + s]);
+        }
+        if (!wg_wait(&bars[C::kAccFull], nr & 1, ab, 112)) return;
+        tc_fence_after();
+        float4* out = reinterpret_cast<float4*>(a.parts) + (int64_t)run.part * (D / 4) + row;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {   // the slot's half of the columns
+            const int c0 = s * (D / 2) + c * 32;
+            uint32_t o[32];
+            tmem_ld32(trow + 256 + c0, o);
+            tmem_ld_wait();
+            if (real) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    out[(int64_t)(c0 / 4 + e) * run.rows] =
+                        make_float4(__uint_as_float(o[4 * e]) * a.alpha, __uint_as_float(o[4 * e + 1]) * a.alpha,
+                                    __uint_as_float(o[4 * e + 2]) * a.alpha, __uint_as_float(o[4 * e + 3]) * a.alpha);
+            }
+        }
+        tc_fence_before();
+        mbar_arrive(&bars[C::kAccFree]);
+        ++nr;
+        ring += 2 * (uint32_t)run.blocks;
+        e0 += items;
+    }
+}
+
+template <int D, int ACT>
+__global__ void __launch_bounds__(kThreads, 1)
+prefix_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
+                 const __grid_constant__ CUtensorMap tmKp, const __grid_constant__ CUtensorMap tmVp,
+                 const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                 const BwArgs a) {
+    using C = DqCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int seg0 = a.seg[blockIdx.x], seg1 = a.seg[blockIdx.x + 1];
+    if (seg0 == seg1) return;
+    if (threadIdx.x == 0) {
+        for (int b = 0; b < C::kNumBars; ++b)
+            mbar_init(&bars[b], b == C::kPFull || b == C::kPFull + 1 ? 128u : b == C::kAccFree ? 256u : 1u);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const Abort ab{abort_flag, a.err, a.wait_ns};
+    if (warp == 0) {
+        if (lane == 0) dq_producer<D>(&tmQ, &tmDO, &tmKp, &tmVp, &tmK, &tmV, a, smem, bars, seg0, seg1, ab);
+        __syncwarp();
+    } else if (warp == 1) {
+        dq_mma<D>(a, smem, bars, tmem, seg0, seg1, ab);
+        __syncwarp();
+    } else {
+        dq_rows<D, ACT>(a, smem, bars, tmem, seg0, seg1, ab);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <typename K>
+gdpa_status go(K kern, int smem, PrefixPlan& p, const CUtensorMap* m, const BwArgs& a, cudaStream_t st) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return GDPA_ERR_CUDA;
+    kern<<<p.S, kThreads, smem, st>>>(m[0], m[1], m[2], m[3], m[4], m[5], a);
+    p.launches += 1;
+    return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+}
+
+template <int D, int ACT>
+gdpa_status launch(PrefixPlan& p, const CUtensorMap* m, BwArgs& a, cudaStream_t st) {
+    gdpa_status s = GDPA_OK;
+    if (p.useg[p.S] > 0) {
+        a.seg = p.dev_useg();
+        s = go(prefix_dkv_kernel<D, ACT>, KvCfg<D>::kSmem, p, m, a, st);
+    }
+    if (s == GDPA_OK && p.seg[p.S] > 0) {
+        a.seg = p.dev_seg();
+        s = go(prefix_dq_kernel<D, ACT>, DqCfg<D>::kSmem, p, m, a, st);
+    }
+    return s;
+}
+
+}  // namespace
+
+gdpa_status launch_prefix_tc_bwd(PrefixPlan& p, const PrefixIO& io, const float* delta, cudaStream_t st) {
+    if (p.seg[p.S] == 0 && p.useg[p.S] == 0) return GDPA_OK;
+    CUtensorMap m[6];
+    const uint64_t krow = (uint64_t)p.Hkv * p.d;
+    // tensors without rows are never loaded from: any map will do
+    const void* kp = p.Tp ? io.kp : io.k;
+    const void* vp = p.Tp ? io.vp : io.v;
+    const void* k = p.Tkv ? io.k : io.kp;
+    const void* v = p.Tkv ? io.v : io.vp;
+    const uint64_t np = p.Tp ? p.Tp : p.Tkv, nk = p.Tkv ? p.Tkv : p.Tp;
+    const uint64_t nq = p.Tq ? p.Tq : 1;
+    if (!tc::make_tmap_rows(&m[0], p.Tq ? io.q : kp, nq, p.Tq ? p.H : p.Hkv, p.d, p.Tq ? p.r : 1, p.tpt) ||
+        !tc::make_tmap_rows(&m[1], p.Tq ? io.d_o : kp, nq, p.Tq ? p.H : p.Hkv, p.d, p.Tq ? p.r : 1, p.tpt) ||
+        !tc::make_tmap_bf16(&m[2], kp, np, krow, 128) || !tc::make_tmap_bf16(&m[3], vp, np, krow, 128) ||
+        !tc::make_tmap_bf16(&m[4], k, nk, krow, 128) || !tc::make_tmap_bf16(&m[5], v, nk, krow, 128))
+        return GDPA_ERR_CUDA;
+    BwArgs a;
+    a.units = p.dev_units();
+    a.pieces = p.dev_pieces();
+    a.seg = nullptr;
+    a.lse = io.lse;
+    a.delta = delta;
+    a.parts = p.d_parts;
+    a.dkp = (__nv_bfloat16*)io.dkp;
+    a.dvp = (__nv_bfloat16*)io.dvp;
+    a.dk = (__nv_bfloat16*)io.dk;
+    a.dv = (__nv_bfloat16*)io.dv;
+    a.H = p.H;
+    a.Hkv = p.Hkv;
+    a.r = p.r;
+    a.tpt = p.tpt;
+    a.windowed = p.mask == GDPA_MASK_CAUSAL_WINDOW;
+    a.window = p.window;
+    a.q_bytes = p.tpt * p.r * p.d * 2;
+    a.alpha = io.alpha;
+    a.err = p.dev_err();
+    a.wait_ns = tc::wait_limit_ns(0);
+    gdpa_status s = GDPA_OK;
+    if (p.d == 128) {
+        if (io.act == kSoftmax)
+            s = launch<128, kSoftmax>(p, m, a, st);
+        else
+            GDPA_DISPATCH_ACT(io.act, A, s = launch<128, A>(p, m, a, st))
+    } else {
+        if (io.act == kSoftmax)
+            s = launch<64, kSoftmax>(p, m, a, st);
+        else
+            GDPA_DISPATCH_ACT(io.act, A, s = launch<64, A>(p, m, a, st))
+    }
+    return s;
+}
+
+}  // namespace gdpa
