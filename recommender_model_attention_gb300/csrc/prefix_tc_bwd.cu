@@ -16,7 +16,8 @@
 // changes the sums from run to run.  Results here are the same bits every time.
 //
 // Both walk items of 64 columns (query rows, or keys): two slots of TMEM
-// columns [S | dP], a warpgroup each, thread = lane.  While one slot's weights
+// columns [S | dP], two warpgroups each, which take 32 of the columns, thread =
+// lane.  While one slot's weights
 // are computed the tensor core runs the other slot's products and the next
 // scores: item e's closing products, then S and dP of item e + 2 into the same
 // columns.  Rows behind the last one of an item share its 16-row step: their
@@ -35,7 +36,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 64 + 256;
+constexpr int kThreads = 64 + 512;
 constexpr int kHalfBytes = 128 * 128;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kItem = 64;   // columns of an item
@@ -64,6 +65,10 @@ __device__ __forceinline__ void load3(const CUtensorMap* map, uint64_t* bar, voi
         : "memory");
 }
 
+// Where 16-column step k of an item's packed weights lies: each warpgroup's 32
+// columns, packed in 16, over the first of its own scores.
+__device__ __forceinline__ constexpr uint32_t packed(int k) { return (k >> 1) * 32 + (k & 1) * 8; }
+
 // weights and score gradients of two pairs
 template <int ACT>
 __device__ __forceinline__ void weights2(float s0, float s1, float dp0, float dp1, const ActScale& k,
@@ -84,7 +89,7 @@ __device__ __forceinline__ void weights2(float s0, float s1, float dp0, float dp
     }
 }
 
-// clear rows [r0, r1) of a [128][D] tile in shared memory (a warpgroup)
+// clear rows [r0, r1) of a [128][D] tile in shared memory (128 threads)
 template <int D>
 __device__ __forceinline__ void clear_rows(uint8_t* tile, int r0, int r1, int tid) {
     for (int i = tid; i < (r1 - r0) * (D / 8); i += 128) {
@@ -94,10 +99,6 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int r0, int r1, int ti
     }
 }
 
-__device__ __forceinline__ void bar_wg(int id) {
-    asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
-}
-
 // ----------------------------------------------------------------- dK and dV
 
 template <int D>
@@ -105,8 +106,8 @@ struct KvCfg {
     static constexpr int kHalves = D / 64;
     static constexpr int kTile = 128 * D * 2;
     static constexpr int kOffK = 0, kOffV = kTile, kOffQ = 2 * kTile, kOffDO = 4 * kTile;   // Q, dO: 2 stages
-    static constexpr int kOffStat = 6 * kTile;   // [slot][2][64] (lse, delta) pairs
-    static constexpr int kOffBar = kOffStat + 2 * 2 * 64 * 8;
+    static constexpr int kOffStat = 6 * kTile;   // [16 warps][2][32] (lse, delta) pairs
+    static constexpr int kOffBar = kOffStat + 16 * 2 * 32 * 8;
     enum { kKVFull = 0, kKVEmpty, kFull, kEmpty = kFull + 2, kSDFull = kEmpty + 2, kPFull = kSDFull + 2,
            kAccFull = kPFull + 2, kAccFree, kMmaDone, kNumBars };
     static constexpr int kSmem = kOffBar + kNumBars * 8 + 16 + 1024;
@@ -224,11 +225,11 @@ __device__ void kv_mma(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t 
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 if ((uint32_t)k < steps)
-                    mma_ts(tmem + 256, col + 8 * k, dd + mnmajor_step(k), idesc_acc, x > 0 || k > 0);
+                    mma_ts(tmem + 256, col + packed(k), dd + mnmajor_step(k), idesc_acc, x > 0 || k > 0);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 if ((uint32_t)k < steps)
-                    mma_ts(tmem + 384, col + 64 + 8 * k, qd + mnmajor_step(k), idesc_acc, x > 0 || k > 0);
+                    mma_ts(tmem + 384, col + 64 + packed(k), qd + mnmajor_step(k), idesc_acc, x > 0 || k > 0);
             if (x % full == full - 1 || x == items - 1) mma_commit(&bars[C::kEmpty + st]);
             if (x == items - 1) mma_commit(&bars[C::kAccFull]);
             if (x + 2 < items && !issue_s(x + 2)) goto drain;
@@ -265,12 +266,13 @@ __device__ void kv_rows(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t
     using C = KvCfg<D>;
     constexpr bool kSm = ACT == kSoftmax;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int s = (warp - 2) >> 2, quarter = warp & 3;
+    const int s = (warp - 2) >> 3, h = ((warp - 2) >> 2) & 1, quarter = warp & 3;
     const int key = quarter * 32 + lane;   // TMEM lane
-    const int tid = (int)threadIdx.x - 64 - 128 * s;
+    const int tid = (int)(threadIdx.x - 64) & 127;
     const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t col = trow + s * 128;
-    float2* stat = reinterpret_cast<float2*>(smem + C::kOffStat) + s * 128;   // [2][64]
+    const uint32_t col = trow + s * 128 + 32 * h;   // this thread's 32 rows' scores
+    // a warp's row statistics, two items' in turn
+    float2* stat = reinterpret_cast<float2*>(smem + C::kOffStat) + (warp - 2) * 64;
     const ActScale ks = act_scale<ACT>(a.alpha);
     uint32_t nu = 0, tile0 = 0, e0 = 0;
     for (int t = seg0; t < seg1; ++t) {
@@ -283,20 +285,17 @@ __device__ void kv_rows(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t
         if (tiles == 0) {   // keys that no row sees
             uint4* z = reinterpret_cast<uint4*>(s ? dk : dv);
             if (real)
-                for (int c = 0; c < D / 8; ++c) z[c] = make_uint4(0u, 0u, 0u, 0u);
+                for (int c = h * (D / 16); c < (h + 1) * (D / 16); ++c) z[c] = make_uint4(0u, 0u, 0u, 0u);
             continue;
         }
         const int full = a.tpt * a.r > kItem ? 2 : 1;
         const int items = (tiles - 1) * full + (tile_rows(u, a, tiles - 1) + kItem - 1) / kItem;
         const bool banded = own && a.windowed;
         const int jpos = u.j0 + key;
-        // this slot's items of the unit: those with (e0 + x) odd or even
-        int x = (int)((e0 ^ (uint32_t)s) & 1);
-        float2 next = make_float2(INFINITY, 0.0f);
-        auto stats = [&](int xi) -> float2 {   // of row tid of item xi
+        auto stats = [&](int xi) -> float2 {   // of row 32 h + lane of item xi
             float2 v = make_float2(INFINITY, 0.0f);
-            if (kSm && tid < kItem && xi < items) {
-                const int row = (xi % full) * kItem + tid, m = xi / full;
+            if (kSm && xi < items) {
+                const int m = full == 2 ? xi >> 1 : xi, row = (full == 2 ? (xi & 1) * kItem : 0) + 32 * h + lane;
                 if (row < tile_rows(u, a, m)) {
                     const int tt = row / a.r;
                     const int64_t at = (int64_t)(u.tok + m * a.tpt + tt) * a.H + u.hk * a.r + (row - tt * a.r);
@@ -307,43 +306,47 @@ __device__ void kv_rows(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t
             }
             return v;
         };
+        // this slot's items of the unit: those with e0 + x of its parity
+        int x = (int)((e0 ^ (uint32_t)s) & 1);
+        float2 next = make_float2(INFINITY, 0.0f);
         if (kSm) next = stats(x);
         for (; x < items; x += 2) {
-            const uint32_t e = e0 + x, buf = (e >> 1) & 1;
-            const int m = x / full, r0 = (x % full) * kItem;
-            const int n = min(kItem, tile_rows(u, a, m) - r0);
-            float2* sb = stat + buf * kItem;
+            const uint32_t e = e0 + x;
+            const int m = full == 2 ? x >> 1 : x, r0 = full == 2 ? (x & 1) * kItem : 0;
+            const int n = min(kItem, tile_rows(u, a, m) - r0) - 32 * h;   // rows here, may be <= 0
+            const float2* sb = stat + ((e >> 1) & 1) * 32;
             if (kSm) {
-                if (tid < kItem) sb[tid] = next;
+                stat[((e >> 1) & 1) * 32 + lane] = next;
                 next = stats(x + 2);
-                bar_wg(1 + s);
+                __syncwarp();
             }
             if (!wg_wait(&bars[C::kSDFull + s], (e >> 1) & 1, ab, 91)) return;
             tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (c * 16 >= n) continue;
+            const bool cut = banded || n < 32;
+#pragma unroll 1
+            for (int c = 0; c < 32; c += 16) {
+                if (c >= n) break;
                 uint32_t sv[16], dv16[16], pk[8], dk8[8];
-                tmem_ld16(col + c * 16, sv);
-                tmem_ld16(col + 64 + c * 16, dv16);
+                tmem_ld16(col + c, sv);
+                tmem_ld16(col + 64 + c, dv16);
                 tmem_ld_wait();
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
                     float l0 = 0.f, l1 = 0.f, d0 = 0.f, d1 = 0.f, p0, p1, g0, g1;
                     if constexpr (kSm) {
-                        const float4 st = *reinterpret_cast<const float4*>(sb + c * 16 + i);
+                        const float4 st = *reinterpret_cast<const float4*>(sb + c + i);
                         l0 = st.x; d0 = st.y; l1 = st.z; d1 = st.w;
                     }
                     weights2<ACT>(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1]),
                                   __uint_as_float(dv16[i]), __uint_as_float(dv16[i + 1]), ks, l0, l1, d0, d1,
                                   p0, p1, g0, g1);
-                    if (banded || n < kItem) {
+                    if (cut) {
 #pragma unroll
                         for (int w = 0; w < 2; ++w) {
-                            const int row = c * 16 + i + w;
+                            const int row = c + i + w;
                             bool ok = row < n;
                             if (banded) {
-                                const int ipos = u.i0 + m * a.tpt + (r0 + row) / a.r;
+                                const int ipos = u.i0 + m * a.tpt + (r0 + 32 * h + row) / a.r;
                                 ok = ok && jpos <= ipos && jpos > ipos - a.window;
                             }
                             if (!ok) (w ? p1 : p0) = (w ? g1 : g0) = 0.0f;
@@ -352,14 +355,16 @@ __device__ void kv_rows(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t
                     pk[i >> 1] = pack_bf16x2(p0, p1);
                     dk8[i >> 1] = pack_bf16x2(g0, g1);
                 }
-                tmem_st8(col + c * 8, pk);
-                tmem_st8(col + 64 + c * 8, dk8);
+                // over this thread's own scores: 16 packed columns of 32
+                tmem_st8(col + c / 2, pk);
+                tmem_st8(col + 64 + c / 2, dk8);
             }
             tmem_st_wait();
-            if (n & 15) {
+            if (n > 0 && n < 32 && (n & 15)) {
                 const uint32_t st = (tile0 + m) & 1;
-                clear_rows<D>(smem + C::kOffQ + st * C::kTile, r0 + n, r0 + ((n + 15) & ~15), tid);
-                clear_rows<D>(smem + C::kOffDO + st * C::kTile, r0 + n, r0 + ((n + 15) & ~15), tid);
+                const int z0 = r0 + 32 * h + n, z1 = r0 + 32 * h + ((n + 15) & ~15);
+                clear_rows<D>(smem + C::kOffQ + st * C::kTile, z0, z1, tid);
+                clear_rows<D>(smem + C::kOffDO + st * C::kTile, z0, z1, tid);
                 fence_proxy_async_smem();
             }
             tc_fence_before();
@@ -367,8 +372,8 @@ __device__ void kv_rows(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t
         }
         if (!wg_wait(&bars[C::kAccFull], nu & 1, ab, 92)) return;
         tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < D; c += 32)
+#pragma unroll 1
+        for (int c = h * (D / 2); c < (h + 1) * (D / 2); c += 32)
             store32(trow + (s ? 384 : 256) + c, s ? a.alpha : 1.0f, (s ? dk : dv) + c, real);
         tc_fence_before();
         mbar_arrive(&bars[C::kAccFree]);
@@ -395,7 +400,7 @@ prefix_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     if (seg0 == seg1) return;
     if (threadIdx.x == 0) {
         for (int b = 0; b < C::kNumBars; ++b)
-            mbar_init(&bars[b], b == C::kPFull || b == C::kPFull + 1 ? 128u : b == C::kAccFree ? 256u : 1u);
+            mbar_init(&bars[b], b == C::kPFull || b == C::kPFull + 1 ? 256u : b == C::kAccFree ? 512u : 1u);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -565,7 +570,8 @@ __device__ void dq_mma(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t 
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 if ((uint32_t)k < steps)
-                    mma_ts(tmem + 256, tmem + (e & 1) * 128 + 8 * k, kd + mnmajor_step(k), idesc_acc, x > 0 || k > 0);
+                    mma_ts(tmem + 256, tmem + (e & 1) * 128 + packed(k), kd + mnmajor_step(k), idesc_acc,
+                           x > 0 || k > 0);
             if (last_of(x)) mma_commit(&bars[C::kEmpty + sk]);
             if (x == items - 1) mma_commit(&bars[C::kAccFull]);
             if (x + 2 < items && !issue_s(x + 2)) goto drain;
@@ -585,11 +591,11 @@ __device__ void dq_rows(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t
     using C = DqCfg<D>;
     constexpr bool kSm = ACT == kSoftmax;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int s = (warp - 2) >> 2, quarter = warp & 3;
+    const int s = (warp - 2) >> 3, h = ((warp - 2) >> 2) & 1, quarter = warp & 3;
     const int row = quarter * 32 + lane;
-    const int tid = (int)threadIdx.x - 64 - 128 * s;
+    const int tid = (int)(threadIdx.x - 64) & 127;
     const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t col = trow + s * 128;
+    const uint32_t col = trow + s * 128 + 32 * h;   // this thread's 32 keys' scores
     const ActScale ks = act_scale<ACT>(a.alpha);
     const int rt = row / a.r, rj = row - rt * a.r;
     uint32_t nr = 0, ring = 0, e0 = 0;
@@ -610,21 +616,22 @@ __device__ void dq_rows(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t
         }
         for (int x = (int)((e0 ^ (uint32_t)s) & 1); x < items; x += 2) {
             const uint32_t e = e0 + x;
-            const int n = min(kItem, run.keys(x >> 1) - (x & 1) * kItem);
-            const int j0 = p.j0 + run.block(x >> 1) * kBN + (x & 1) * kItem;
+            const int n = min(kItem, run.keys(x >> 1) - (x & 1) * kItem) - 32 * h;   // keys here, may be <= 0
+            const bool cut = banded || n < 32;
             int lo = 0, hi = n;   // columns this row sees
             if (banded) {
-                hi = min(hi, ipos - j0 + 1);
-                lo = ipos - j0 >= a.window ? ipos - j0 - a.window + 1 : 0;
+                const int at = ipos - (p.j0 + run.block(x >> 1) * kBN + (x & 1) * kItem + 32 * h);
+                hi = min(hi, at + 1);
+                lo = at >= a.window ? at - a.window + 1 : 0;
             }
             if (!wg_wait(&bars[C::kSDFull + s], (e >> 1) & 1, ab, 111)) return;
             tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (c * 16 >= n) continue;
+#pragma unroll 1
+            for (int c = 0; c < 32; c += 16) {
+                if (c >= n) break;
                 uint32_t sv[16], dv16[16], dk8[8];
-                tmem_ld16(col + c * 16, sv);
-                tmem_ld16(col + 64 + c * 16, dv16);
+                tmem_ld16(col + c, sv);
+                tmem_ld16(col + 64 + c, dv16);
                 tmem_ld_wait();
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
@@ -632,18 +639,18 @@ __device__ void dq_rows(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t
                     weights2<ACT>(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1]),
                                   __uint_as_float(dv16[i]), __uint_as_float(dv16[i + 1]), ks, lse2, lse2, delta,
                                   delta, p0, p1, g0, g1);
-                    if (banded || n < kItem) {
-                        if (c * 16 + i < lo || c * 16 + i >= hi) g0 = 0.0f;
-                        if (c * 16 + i + 1 < lo || c * 16 + i + 1 >= hi) g1 = 0.0f;
+                    if (cut) {
+                        if (c + i < lo || c + i >= hi) g0 = 0.0f;
+                        if (c + i + 1 < lo || c + i + 1 >= hi) g1 = 0.0f;
                     }
                     dk8[i >> 1] = pack_bf16x2(g0, g1);
                 }
-                tmem_st8(col + c * 8, dk8);
+                tmem_st8(col + c / 2, dk8);   // over this thread's own scores
             }
             tmem_st_wait();
-            if (n & 15) {
+            if (n > 0 && n < 32 && (n & 15)) {
                 const uint32_t sk = (ring + 2 * (uint32_t)(x >> 1)) % C::kStages;
-                const int r0 = (x & 1) * kItem;
+                const int r0 = (x & 1) * kItem + 32 * h;
                 clear_rows<D>(smem + C::kOffKV + sk * C::kTile, r0 + n, r0 + ((n + 15) & ~15), tid);
                 fence_proxy_async_smem();
             }
@@ -653,18 +660,21 @@ __device__ void dq_rows(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t
         if (!wg_wait(&bars[C::kAccFull], nr & 1, ab, 112)) return;
         tc_fence_after();
         float4* out = reinterpret_cast<float4*>(a.parts) + (int64_t)run.part * (D / 4) + row;
+        {   // this warpgroup's quarter of the columns
+            constexpr int kQ = D / 4;
+            const int c0 = (2 * s + h) * kQ;
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {   // the slot's half of the columns
-            const int c0 = s * (D / 2) + c * 32;
-            uint32_t o[32];
-            tmem_ld32(trow + 256 + c0, o);
-            tmem_ld_wait();
-            if (real) {
+            for (int c = 0; c < kQ; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(trow + 256 + c0 + c, o);
+                tmem_ld_wait();
+                if (real) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    out[(int64_t)(c0 / 4 + e) * run.rows] =
-                        make_float4(__uint_as_float(o[4 * e]) * a.alpha, __uint_as_float(o[4 * e + 1]) * a.alpha,
-                                    __uint_as_float(o[4 * e + 2]) * a.alpha, __uint_as_float(o[4 * e + 3]) * a.alpha);
+                    for (int e = 0; e < 4; ++e)
+                        out[(int64_t)((c0 + c) / 4 + e) * run.rows] =
+                            make_float4(__uint_as_float(o[4 * e]) * a.alpha, __uint_as_float(o[4 * e + 1]) * a.alpha,
+                                        __uint_as_float(o[4 * e + 2]) * a.alpha, __uint_as_float(o[4 * e + 3]) * a.alpha);
+                }
             }
         }
         tc_fence_before();
@@ -692,7 +702,7 @@ prefix_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     if (seg0 == seg1) return;
     if (threadIdx.x == 0) {
         for (int b = 0; b < C::kNumBars; ++b)
-            mbar_init(&bars[b], b == C::kPFull || b == C::kPFull + 1 ? 128u : b == C::kAccFree ? 256u : 1u);
+            mbar_init(&bars[b], b == C::kPFull || b == C::kPFull + 1 ? 256u : b == C::kAccFree ? 512u : 1u);
         *abort_flag = 0;
         fence_mbar_init();
     }

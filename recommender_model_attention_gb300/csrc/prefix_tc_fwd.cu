@@ -4,16 +4,18 @@
 // One CTA per planned share walks its pieces.  A piece is one or two row
 // tiles (packed token by token, query heads of one key head side by side; a
 // 3-D TMA box does the packing) against a run of keys.  Two slots, each with
-// its own score and sum columns in TMEM (128 + d) and one warpgroup, a thread
-// a row:
+// its own score and sum columns in TMEM (128 + d) and two warpgroups, which
+// take 64 keys of a block each, a thread a row:
 //   two tiles: slot s holds tile s, both read the same key blocks;
 //   one tile:  slot s takes the key blocks s, s + 2, ... of the same rows and
 //              gives a part of its own.
 // Warp 0 loads (TMA): the piece's query tiles, then K and V blocks through
 // one ring, in the order in which the tensor core takes them.  Warp 1 issues
 // S = Q K^T and O += P V: slot 0's P V and next S run while slot 1's weights
-// are computed, and the other way round.  The warpgroups keep the row maximum
-// as a reference that only moves when it would be passed by more than 8 (in
+// are computed, and the other way round; the P V of a block's first 64 keys
+// starts when their warpgroup is done.  The warpgroups (a row's two threads
+// exchange their maxima through shared memory) keep the row maximum as a
+// reference that only moves when it would be passed by more than 8 (in
 // base 2: weights stay below 2^8), so O is rescaled in TMEM a few times a
 // piece rather than at every block; that S is complete says that the P V
 // before it is (they are issued in that order and commits follow all work
@@ -37,7 +39,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 64 + 256;
+constexpr int kThreads = 64 + 512;
 constexpr int kHalfBytes = 128 * 128;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRise = 8.0f;   // the reference follows a maximum this far above it
@@ -52,9 +54,12 @@ struct PfCfg {
     static constexpr int kOffBar = kOffKV + kStages * kTile;
     enum {
         kQFull = 0, kQEmpty, kFull, kEmpty = kFull + kStages, kSFull = kEmpty + kStages,
-        kPFull = kSFull + 2, kOFull = kPFull + 2, kOFree = kOFull + 2, kMmaDone = kOFree + 2, kNumBars
+        kPFull = kSFull + 2,    // per slot and half of the block's keys
+        kOFull = kPFull + 4, kOFree = kOFull + 2, kMeet = kOFree + 2, kMmaDone = kMeet + 2, kNumBars
     };
-    static constexpr int kSmem = kOffBar + kNumBars * 8 + 16 + 1024;
+    static constexpr int kOffXchg = kOffBar + kNumBars * 8 + 16;   // [slot][half][128] maxima
+    static constexpr int kSmem = kOffXchg + 2 * 2 * 128 * 4;       // no room for an alignment gap
+    static_assert(kSmem <= 232448, "shared memory of a block");
 };
 
 struct PfParams {
@@ -198,17 +203,20 @@ __device__ void pf_mma(const PfParams& prm, uint8_t* smem, uint64_t* bars, uint3
                 const int b = w.block(s, j), at = w.v_at(b);
                 // the slot's sums of its previous piece have been read
                 if (j == 0 && !wg_wait(&bars[C::kOFree + s], (used[s] & 1) ^ 1, ab, 65)) goto drain;
-                if (!wg_wait(&bars[C::kPFull + s], (items[s] + j) & 1, ab, 66)) goto drain;
                 if (!wg_wait(&bars[C::kFull + stage(at)], phase(at), ab, 67)) goto drain;
-                tc_fence_after();
                 const uint32_t vb = smem_u32(smem + C::kOffKV + stage(at) * C::kTile);
                 const uint64_t vd = smem_desc_sw128(vb, kHalfBytes, 1024);
                 const uint32_t steps = n16(b) / 16;
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if ((uint32_t)k < steps)
-                        mma_ts(tmem + 256 + s * 128, tmem + s * 128 + 8 * k, vd + mnmajor_step(k), idesc_pv,
-                               j > 0 || k > 0);
+                for (int h = 0; h < 2; ++h) {
+                    if (!wg_wait(&bars[C::kPFull + 2 * s + h], (items[s] + j) & 1, ab, 66)) goto drain;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 4 * h; k < 4 * h + 4; ++k)
+                        if ((uint32_t)k < steps)
+                            mma_ts(tmem + 256 + s * 128, tmem + s * 128 + 64 * h + 8 * (k - 4 * h),
+                                   vd + mnmajor_step(k), idesc_pv, j > 0 || k > 0);
+                }
                 if (w.dual || s == 1) mma_commit(&bars[C::kEmpty + stage(at)]);
                 if (j == n - 1)
                     mma_commit(&bars[C::kOFull + s]);
@@ -234,19 +242,20 @@ __device__ void pf_rows(const PfParams& prm, uint8_t* smem, uint64_t* bars, uint
     using C = PfCfg<D>;
     constexpr bool kSm = ACT == kSoftmax;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int s = (warp - 2) >> 2;
+    const int s = (warp - 2) >> 3, h = ((warp - 2) >> 2) & 1;   // slot, half of the keys
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;
-    const int tid = (int)threadIdx.x - 64 - 128 * s;
+    const int tid = (int)(threadIdx.x - 64) & 127;
     const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t sc = trow + s * 128, oc = trow + 256 + s * 128;
+    float* xchg = reinterpret_cast<float*>(smem + C::kOffXchg) + s * 256;
     const bool flip = kSm && prm.alpha < 0.0f;
     ActScale ks = act_scale<ACT>(prm.alpha);
     if (kSm) {   // (a zero scale would make NaN of masked scores)
         ks.c0 = fabsf(ks.c0);
         if (ks.c0 < 1e-30f) ks.c0 = 1e-30f;
     }
-    uint32_t base = 0, items = 0, used = 0;
+    uint32_t base = 0, items = 0, used = 0, met = 0;
     for (int t = seg0; t < seg1; ++t) {
         const PrefixPiece p = load_piece(prm.pieces + t);
         const Walk w(p);
@@ -260,46 +269,59 @@ __device__ void pf_rows(const PfParams& prm, uint8_t* smem, uint64_t* bars, uint
         float ref = -INFINITY, sum = 0.0f;
         for (int j = 0; j < n; ++j) {
             const int b = w.block(s, j);
-            const int nv = min(kBN, p.nk - b * kBN);
+            const int nv = min(kBN, p.nk - b * kBN) - 64 * h;   // this half's keys, may be <= 0
+            const bool cut = nv < 64 || banded;
+            int lo = 0, hi = nv;   // columns this row sees
+            if (banded) {
+                const int at = ipos - (p.j0 + b * kBN + 64 * h);
+                hi = min(hi, at + 1);
+                lo = at >= prm.window ? at - prm.window + 1 : 0;
+            }
             if (!wg_wait(&bars[C::kSFull + s], (items + j) & 1, ab, 71)) return;
             tc_fence_after();
-            uint32_t x[128];
+            // 32 scores from column c on, those the row does not see as -inf
+            auto scores = [&](int c, uint32_t (&x)[32]) {
+                tmem_ld32(sc + 64 * h + c, x);
+                tmem_ld_wait();
+                if (flip) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (c * 32 < nv) tmem_ld32(sc + c * 32, *reinterpret_cast<uint32_t(*)[32]>(x + c * 32));
-            tmem_ld_wait();
-            if (flip) {
-#pragma unroll
-                for (int e = 0; e < 128; ++e) x[e] ^= 0x80000000u;
-            }
-            if (nv < kBN || banded) {
-                // first and one past the last column this row sees
-                int lo = 0, hi = nv;
-                if (banded) {
-                    const int j0 = p.j0 + b * kBN;
-                    hi = min(hi, ipos - j0 + 1);
-                    lo = ipos - j0 >= prm.window ? ipos - j0 - prm.window + 1 : 0;
+                    for (int e = 0; e < 32; ++e) x[e] ^= 0x80000000u;
                 }
+                if (cut) {
 #pragma unroll
-                for (int e = 0; e < 128; ++e)
-                    if (e < lo || e >= hi) x[e] = 0xff800000u;   // -inf
-            }
+                    for (int e = 0; e < 32; ++e)
+                        if (c + e < lo || c + e >= hi) x[e] = 0xff800000u;
+                }
+            };
             if constexpr (kSm) {
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                for (int c = 0; c < 64; c += 32) {
+                    if (c >= nv) break;
+                    uint32_t x[32];
+                    scores(c, x);
 #pragma unroll
-                for (int e = 0; e < 128; e += 4)
+                    for (int e = 0; e < 32; e += 4)
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) m4[u] = fmaxf(m4[u], __uint_as_float(x[e + u]));
-                const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * ks.c0;
+                        for (int u = 0; u < 4; ++u) m4[u] = fmaxf(m4[u], __uint_as_float(x[e + u]));
+                }
+                float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                // the row's other 64 keys: both threads go on with the same
+                // maximum (S of the next block comes only after both have
+                // read, so one buffer is enough)
+                xchg[h * 128 + row] = top;
+                mbar_arrive(&bars[C::kMeet + s]);
+                if (!wg_wait(&bars[C::kMeet + s], met++ & 1, ab, 74)) return;
+                top = fmaxf(top, xchg[(h ^ 1) * 128 + row]) * ks.c0;
                 const bool up = real && top > ref + kRise;   // also from -inf
                 if (__any_sync(0xffffffffu, up)) {
                     const float nref = up ? top : ref;
                     const float f = up ? ex2_approx(ref - nref) : 1.0f;   // 0 from -inf
                     ref = nref;
                     sum *= f;
-                    if (j > 0) {
+                    if (j > 0) {   // each thread rescales its half of the row's sums
 #pragma unroll 1
-                        for (int c = 0; c < D; c += 16) {
+                        for (int c = h * (D / 2); c < (h + 1) * (D / 2); c += 16) {
                             uint32_t o[16];
                             tmem_ld16(oc + c, o);
                             tmem_ld_wait();
@@ -310,17 +332,21 @@ __device__ void pf_rows(const PfParams& prm, uint8_t* smem, uint64_t* bars, uint
                         tmem_st_wait();
                     }
                 }
+                tc_fence_before();
             }
+            // this half's sums are ready for the other half's product
+            mbar_arrive(&bars[C::kPFull + 2 * s + (h ^ 1)]);
             const float nref = kSm ? (ref == -INFINITY ? 0.0f : -ref) : 0.0f;
             uint64_t sum2 = f2_make(0.0f, 0.0f);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                if (c * 32 >= nv) continue;
-                uint32_t pk[16];
+#pragma unroll 1
+            for (int c = 0; c < 64; c += 32) {
+                if (c >= nv) break;
+                uint32_t x[32], pk[16];
+                scores(c, x);
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
                     float p0, p1;
-                    const float s0 = __uint_as_float(x[c * 32 + e]), s1 = __uint_as_float(x[c * 32 + e + 1]);
+                    const float s0 = __uint_as_float(x[e]), s1 = __uint_as_float(x[e + 1]);
                     if constexpr (kSm) {
                         const float2 tt = f2_split(f2_fma(f2_make(s0, s1), f2_make(ks.c0, ks.c0), f2_make(nref, nref)));
                         p0 = ex2_approx(tt.x);
@@ -328,27 +354,27 @@ __device__ void pf_rows(const PfParams& prm, uint8_t* smem, uint64_t* bars, uint
                         sum2 = f2_fma(f2_make(p0, p1), f2_make(1.0f, 1.0f), sum2);
                     } else {
                         act_s2<ACT>(s0, s1, ks, p0, p1);
-                        if (nv < kBN || banded) {
+                        if (cut) {
                             if (s0 == -INFINITY) p0 = 0.0f;
                             if (s1 == -INFINITY) p1 = 0.0f;
                         }
                     }
                     pk[e >> 1] = pack_bf16x2(p0, p1);
                 }
-                tmem_st16(sc + c * 16, pk);
+                tmem_st16(sc + 64 * h + c / 2, pk);   // over this thread's own scores, already read
             }
             if constexpr (kSm) {
                 const float2 a = f2_split(sum2);
                 sum += a.x + a.y;
             }
             tmem_st_wait();
-            if (nv & 15) {
+            if (nv > 0 && nv < 64 && (nv & 15)) {
                 // V rows behind the last key, inside its 16-row step
                 const int at = w.v_at(b);
                 const uint32_t st = (base + (uint32_t)at) % C::kStages, ph = ((base + (uint32_t)at) / C::kStages) & 1;
                 if (!wg_wait(&bars[C::kFull + st], ph, ab, 72)) return;
                 uint8_t* v = smem + C::kOffKV + st * C::kTile;
-                const int n0 = nv, cnt = ((nv + 15) & ~15) - nv;
+                const int n0 = 64 * h + nv, cnt = ((nv + 15) & ~15) - nv;
                 for (int i = tid; i < cnt * (D / 8); i += 128) {
                     const int rr = n0 + i / (D / 8), ch = i % (D / 8);
                     *reinterpret_cast<uint4*>(v + (ch >> 3) * kHalfBytes + rr * 128 + ((ch & 7) << 4)) =
@@ -357,28 +383,45 @@ __device__ void pf_rows(const PfParams& prm, uint8_t* smem, uint64_t* bars, uint
                 fence_proxy_async_smem();
             }
             tc_fence_before();
-            mbar_arrive(&bars[C::kPFull + s]);
+            mbar_arrive(&bars[C::kPFull + 2 * s + h]);
         }
         if (n > 0) {
             if (!wg_wait(&bars[C::kOFull + s], used & 1, ab, 73)) return;
             tc_fence_after();
             float4* out = reinterpret_cast<float4*>(prm.parts) + (int64_t)part * (D / 4) + row;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
+            for (int c = 0; c < D / 64; ++c) {
+                const int c0 = h * (D / 2) + c * 32;
                 uint32_t o[32];
-                tmem_ld32(oc + c * 32, o);
+                tmem_ld32(oc + c0, o);
                 tmem_ld_wait();
                 if (real) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        out[(c * 8 + e) * nrows] =
+                        out[(c0 / 4 + e) * nrows] =
                             make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
                                         __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
                 }
             }
+            if constexpr (kSm) {
+                // the row's sum over both halves of the keys, through a column
+                // of O that has been read
+                if (h == 1) {
+                    tmem_st1(oc + D - 1, __float_as_uint(sum));
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                mbar_arrive(&bars[C::kMeet + s]);
+                if (!wg_wait(&bars[C::kMeet + s], met++ & 1, ab, 75)) return;
+                tc_fence_after();
+                if (h == 0) {
+                    const float other = __uint_as_float(tmem_ld1(oc + D - 1));
+                    tmem_ld_wait();
+                    if (real) reinterpret_cast<float2*>(prm.ml)[(int64_t)part + row] = make_float2(ref, sum + other);
+                }
+            }
             tc_fence_before();
             mbar_arrive(&bars[C::kOFree + s]);
-            if (kSm && real) reinterpret_cast<float2*>(prm.ml)[(int64_t)part + row] = make_float2(ref, sum);
             items += n;
             used += 1;
         }
@@ -392,18 +435,21 @@ prefix_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                   const __grid_constant__ CUtensorMap tmVp, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const PfParams prm) {
     using C = PfCfg<D>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int seg0 = prm.seg[blockIdx.x], seg1 = prm.seg[blockIdx.x + 1];
     if (seg0 == seg1) return;   // the whole CTA
+    if (smem_u32(smem) & 1023u) {   // the swizzled tiles need the alignment declared above
+        if (threadIdx.x == 0) atomicCAS(prm.err, 0, kDevBad);
+        return;
+    }
     if (threadIdx.x == 0) {
         for (int b = 0; b < C::kNumBars; ++b) {
-            const bool rows = (b >= C::kPFull && b < C::kPFull + 2) || (b >= C::kOFree && b < C::kOFree + 2);
-            mbar_init(&bars[b], rows ? 128u : 1u);
+            const bool rows = (b >= C::kPFull && b < C::kPFull + 4) || (b >= C::kOFree && b < C::kMeet + 2);
+            mbar_init(&bars[b], rows ? 256u : 1u);
         }
         *abort_flag = 0;
         fence_mbar_init();
