@@ -134,6 +134,7 @@ gdpa_status create(const int32_t* q_off, const int32_t* kv_off, int B, const int
             {p->units.data(), p->units.size() * sizeof(gdpa::PrefixUnit), &p->off_units},
             {p->useg.data(), p->useg.size() * 4, &p->off_useg},
             {p->smalls.data(), p->smalls.size() * sizeof(gdpa::PrefixUnit), &p->off_smalls},
+            {p->eights.data(), p->eights.size() * sizeof(gdpa::PrefixUnit), &p->off_eights},
         };
         size_t at = 0;
         for (auto& e : t) {
@@ -211,12 +212,12 @@ gdpa_status fwd(gdpa_prefix_plan plan, gdpa_dtype dtype, const PrefixIO& io, voi
     if (gdpa_status s = begin_work(p, st, cap)) return s;
     gdpa_status s;
     if (use_tc(p, dtype)) {
-        s = gdpa::launch_prefix_tc_fwd(p, io, st);
-        if (s == GDPA_OK) s = gdpa::launch_prefix_own_merge(p, io, st);
+        s = gdpa::launch_prefix_own_fwd(p, io, st);
+        if (s == GDPA_OK) s = gdpa::launch_prefix_tc_fwd(p, io, st);
     } else {
         s = gdpa::launch_prefix_simt_fwd(p, dtype, io, st);
-        if (s == GDPA_OK) s = gdpa::launch_prefix_merge(p, dtype, io.o, sm ? io.lse : nullptr, sm, st);
     }
+    if (s == GDPA_OK) s = gdpa::launch_prefix_merge(p, dtype, io.o, sm ? io.lse : nullptr, sm, st);
     const gdpa_status e = end_work(p, st, cap);
     return s != GDPA_OK ? s : e;
 }
@@ -252,6 +253,7 @@ gdpa_status bwd(gdpa_prefix_plan plan, gdpa_dtype dtype, const PrefixIO& io, voi
     gdpa_status s = GDPA_OK;
     if (sm) s = gdpa::launch_prefix_delta(p, dtype, io, p.d_grad, st);
     if (use_tc(p, dtype)) {
+        if (s == GDPA_OK) s = gdpa::launch_prefix_own_bwd8(p, io, p.d_grad, st);
         if (s == GDPA_OK) s = gdpa::launch_prefix_own_bwd(p, io, p.d_grad, st);
         if (s == GDPA_OK) s = gdpa::launch_prefix_tc_bwd(p, io, p.d_grad, st);
     } else if (s == GDPA_OK) {

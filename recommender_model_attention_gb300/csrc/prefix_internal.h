@@ -14,8 +14,8 @@
 // and float2 (maximum in base 2, sum) [n].
 //
 // Own keys of few rows and keys ("small": the rule is in prefix_plan.cpp) are
-// taken by the tensor-core family's merge itself, which reads them once and
-// needs no part; the CUDA-core family walks their pieces like any other.
+// taken by warp-level kernels in the tensor-core family; the CUDA-core family
+// walks their pieces like any other.
 #pragma once
 
 #include <mutex>
@@ -78,10 +78,13 @@ struct PrefixPlan {
     std::vector<PrefixOwn> own;      // [Tq]
     std::vector<PrefixUnit> units;   // the tensor-core family's, then the small own ones
     std::vector<int32_t> useg;       // [S + 1] first unit of each CTA
-    std::vector<PrefixUnit> smalls;  // small own keys, whole: one per sample and key head
+    // small own keys: one unit per sample and key head, those of at most 8
+    // packed rows first; and the same cut into 8 rows each (j0: the first)
+    std::vector<PrefixUnit> smalls, eights;
+    int64_t n_small8 = 0;
     // device copies, one allocation (offsets below), and workspaces
     uint8_t* d_tables = nullptr;
-    size_t off_seg = 0, off_tiles = 0, off_own = 0, off_units = 0, off_useg = 0, off_smalls = 0, off_err = 0;
+    size_t off_seg = 0, off_tiles = 0, off_own = 0, off_units = 0, off_useg = 0, off_smalls = 0, off_eights = 0, off_err = 0;
     float* d_parts = nullptr;        // [n_part_rows] x d floats
     float* d_ml = nullptr;           // [n_part_rows] float2
     float* d_grad = nullptr;         // backward: delta [Tq][H], then float32 sums
@@ -101,6 +104,7 @@ struct PrefixPlan {
     const PrefixUnit* dev_units() const { return (const PrefixUnit*)(d_tables + off_units); }
     const int32_t* dev_useg() const { return (const int32_t*)(d_tables + off_useg); }
     const PrefixUnit* dev_smalls() const { return (const PrefixUnit*)(d_tables + off_smalls); }
+    const PrefixUnit* dev_eights() const { return (const PrefixUnit*)(d_tables + off_eights); }
     int32_t* dev_err() const { return (int32_t*)(d_tables + off_err); }
 };
 
@@ -125,11 +129,13 @@ gdpa_status launch_prefix_simt_bwd(PrefixPlan& p, gdpa_dtype dt, const PrefixIO&
                                    const float* delta, cudaStream_t st);
 // Tensor-core forward (prefix_tc_fwd.cu; bf16, d = 64 or 128): the parts.
 gdpa_status launch_prefix_tc_fwd(PrefixPlan& p, const PrefixIO& io, cudaStream_t st);
-// Its end (prefix_own.cu): the small own keys and the join of all parts.
-gdpa_status launch_prefix_own_merge(PrefixPlan& p, const PrefixIO& io, cudaStream_t st);
+// The parts of the small own keys (prefix_own.cu).
+gdpa_status launch_prefix_own_fwd(PrefixPlan& p, const PrefixIO& io, cudaStream_t st);
 // Tensor-core backward (prefix_tc_bwd.cu): dK, dV, and the parts of dQ, of all
-// but the small own keys, whose are prefix_own_bwd.cu's.
+// but the small own keys, whose are prefix_own.cu's (units of at most 8 rows)
+// and prefix_own_bwd.cu's.
 gdpa_status launch_prefix_tc_bwd(PrefixPlan& p, const PrefixIO& io, const float* delta, cudaStream_t st);
+gdpa_status launch_prefix_own_bwd8(PrefixPlan& p, const PrefixIO& io, const float* delta, cudaStream_t st);
 gdpa_status launch_prefix_own_bwd(PrefixPlan& p, const PrefixIO& io, const float* delta, cudaStream_t st);
 // Join the parts of every row: into O and lse (io.o, io.lse; normalised when
 // `softmax`), of element type dt.

@@ -1,22 +1,22 @@
-// The end of the tensor-core forward of shared-prefix attention: every row's
-// small own keys, joined with its prefix parts, into O and lse.
+// Shared-prefix attention, tensor-core family: the small own keys (the rule is
+// the planner's: few packed rows, few keys), forward and backward, for up to 8
+// packed rows of a sample at a time.
 //
-// A block takes 32 packed rows of a tile.  First its 8 warps take the rows'
-// samples in turn (at most 16 rows of one sample at a time, usually one or a
-// few) and stream the sample's keys through registers: 16 keys a step, m16n8k16
-// products, K and V straight from global memory in 16-byte loads.  The order
-// of the contraction is free, so K's columns are dealt to the lanes as they
-// are loaded (lane q of a quad takes columns 32 i + 8 q .. + 7, the queries
-// alike), and V's 8-column loads make the lane of row group g own output
-// columns 8 g + i of product i: nothing passes through shared memory or is
-// transposed but by byte permutes.  Work is bounded by reading the keys once:
-// a 128-row tile on the fifth-generation tensor core would cost each sample
-// its whole chain of latencies (1.7 us a 128-key block) for a row or two.
-// Then a thread per (row, 16 columns) joins the sums in shared memory with the
-// row's parts.  (One user, 512 candidates with 8-64 own keys, 16384 shared:
-// 280 us with the own keys as tensor-core tiles.)
-#include <cuda_bf16.h>
-
+// A warp takes 8 rows of one (sample, key head) and streams the sample's keys
+// through registers, 16 a step, with m16n8k16 products in the orientation
+// that fills them with 8 rows: S^T = K Q^T (16 keys x 8 rows), then O^T = V^T
+// P^T.  The order of a contraction is free, so K's columns are dealt to the
+// lanes as 16-byte loads bring them (lane q of a quad takes columns 32 i + 8 q
+// .. + 7, the queries alike), and V's 8-column loads make the lane of group g
+// own output columns 8 g + e of product e; a weight's 8x8 blocks change from
+// accumulator to operand layout by movmatrix.  Nothing passes through shared
+// memory.  The work is bounded by reading the keys once; a 128-row tile on the
+// fifth-generation tensor core would cost every sample its whole chain of
+// latencies for a row or two.
+//
+// The backward of a unit of at most 8 rows runs in one warp too: each key's
+// dK and dV are done in its step, dQ^T = K^T dS^T adds up over the steps, so
+// every sum has one owner and one order.
 #include "act.cuh"
 #include "prefix_internal.h"
 #include "prefix_mma.cuh"
@@ -25,274 +25,333 @@
 namespace gdpa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRows = 32;
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
 
 struct OwnArgs {
-    const PrefixTile* tiles;
+    const PrefixUnit* units;   // 8 rows of a sample each (j0: the first packed row)
+    int n;
     const PrefixOwn* own;
-    const __nv_bfloat16 *q, *k, *v;
-    __nv_bfloat16* o;
-    float* lse;
-    const float* parts;
-    const float* ml;
+    const __nv_bfloat16 *q, *k, *v, *d_o;
+    __nv_bfloat16 *dk, *dv;
+    const float *lse, *delta;
+    float* parts;
+    float* ml;
     int H, Hkv, r;
     int windowed, window;
     float alpha;
 };
 
-// Attention of packed rows [0, nrows) (<= 16; row i at q + qoff(i)) over keys
-// [0, nk): unnormalised sums into out[i][D + 4], (maximum, sum) into st[i].
-template <int D, int ACT, typename QP>
-__device__ void own_rows(const OwnArgs& a, QP qrow, int nrows, const __nv_bfloat16* k,
-                         const __nv_bfloat16* v, int64_t ks, int nk, const int* ipos, float* out,
-                         float2* st, int lane) {
+// the transpose of an 8x8 block of 16-bit values spread over the warp
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+    uint32_t o;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(o) : "r"(v));
+    return o;
+}
+
+// A operand of product e of X^T (columns x keys): rows g and g + 8 of the
+// operand are columns 8 g + e and, for d = 128, 64 + 8 g + e (d = 64: 8 g + e
+// and 8 g + e + 4); x[u][h] are 8 columns of keys 2 q, 2 q + 1, 2 q + 8, 2 q + 9.
+template <int D>
+__device__ __forceinline__ void operand_t(const uint4 (&x)[4][D / 64], int e, uint32_t& a0, uint32_t& a1,
+                                          uint32_t& a2, uint32_t& a3) {
+    constexpr int h = D == 128 ? 1 : 0, f = D == 128 ? 0 : 4;
+    a0 = pair_of(x[0][0], x[1][0], e);
+    a1 = pair_of(x[0][h], x[1][h], e + f);
+    a2 = pair_of(x[2][0], x[3][0], e);
+    a3 = pair_of(x[2][h], x[3][h], e + f);
+}
+template <int D>
+constexpr int products() { return D / 16; }
+
+// Write X^T's accumulator of rows 2 q + w (w = 0, 1) to a part: columns 8 g ..
+// + 7 and, for d = 128, 64 + 8 g .. + 7.
+template <int D>
+__device__ __forceinline__ void store_part(const float (&acc)[D / 16][4], float scale, float* parts, int64_t part,
+                                           int rows, int row0, int nrows, int g, int q) {
+    float4* out = reinterpret_cast<float4*>(parts) + part * (D / 4);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const int row = row0 + 2 * q + w;
+        if (2 * q + w >= nrows) continue;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {   // float4 column: which products, which half
+            const int e = D == 128 ? 4 * (c & 1) : 0, x = D == 128 ? c >> 1 : c;
+            const int col = D == 128 ? (c >> 1) * 16 + 2 * g + (c & 1) : 2 * g + c;
+            out[(int64_t)col * rows + row] =
+                make_float4(acc[e][2 * x + w] * scale, acc[e + 1][2 * x + w] * scale,
+                            acc[e + 2][2 * x + w] * scale, acc[e + 3][2 * x + w] * scale);
+        }
+    }
+}
+
+struct Rows {   // the unit's rows, as this lane meets them
+    int nrows, row0, tok, hk, r, H;
+    __device__ __forceinline__ int64_t at(int i) const {   // row of [Tq][H]
+        const int x = row0 + i, t = x / r;
+        return (int64_t)(tok + t) * H + hk * r + (x - t * r);
+    }
+};
+
+template <int D, int ACT>
+__global__ void __launch_bounds__(kThreads, 4) own_fwd_kernel(const OwnArgs a) {
     constexpr bool kSm = ACT == kSoftmax;
     constexpr int kC = D / 32;
-    const int g = lane >> 2, q = lane & 3;
-    uint4 qa[kC], qb[kC];
+    const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (unit >= a.n) return;
+    const PrefixUnit u = a.units[unit];
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const Rows rows{min(8, u.ntok * a.r - u.j0), u.j0, u.tok, u.hk, a.r, a.H};
+    const int64_t ks = (int64_t)a.Hkv * D, k_at = (int64_t)u.k0 * ks + u.hk * D;
+    const __nv_bfloat16 *K = a.k + k_at, *V = a.v + k_at;
+    const PrefixOwn ow = a.own[u.tok];
     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    uint4 qb[kC];
+    {
+        const int64_t at = g < rows.nrows ? rows.at(g) * D : 0;
 #pragma unroll
-    for (int i = 0; i < kC; ++i) {
-        qa[i] = g < nrows ? ldg16(qrow(g) + 32 * i + 8 * q) : z;
-        qb[i] = g + 8 < nrows ? ldg16(qrow(g + 8) + 32 * i + 8 * q) : z;
+        for (int i = 0; i < kC; ++i) qb[i] = g < rows.nrows ? ldg16(a.q + at + 32 * i + 8 * q) : z;
     }
     const ActScale sc = act_scale<ACT>(a.alpha);
-    float acc[D / 8][4];
+    float acc[products<D>()][4];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-    const int pos[2] = {ipos[0], ipos[1]};
-    int key_lo = 0, key_hi = nk;
-    if (a.windowed) {   // keys some row of the warp sees
-        int lo = max(0, min(pos[0], pos[1]) - a.window + 1), hi = max(pos[0], pos[1]) + 1;
-        for (int o = 4; o < 32; o <<= 1) {
-            lo = min(lo, __shfl_xor_sync(~0u, lo, o));
-            hi = max(hi, __shfl_xor_sync(~0u, hi, o));
-        }
-        key_lo = lo & ~15;
-        key_hi = min(nk, hi);
+    for (int e = 0; e < products<D>(); ++e) acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};   // rows 2 q, 2 q + 1
+    const int pos[2] = {(rows.row0 + min(2 * q, rows.nrows - 1)) / a.r,
+                        (rows.row0 + min(2 * q + 1, rows.nrows - 1)) / a.r};
+    int ja = 0, jb = u.nk;
+    if (a.windowed) {   // keys some row sees
+        ja = max(0, rows.row0 / a.r - a.window + 1);
+        jb = min(jb, (rows.row0 + rows.nrows - 1) / a.r + 1);
     }
-    for (int j0 = key_lo; j0 < key_hi; j0 += 16) {
-        uint4 kk[2][kC], vv[4][D / 64];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const int j = min(j0 + 8 * n + g, nk - 1);
-#pragma unroll
-            for (int i = 0; i < kC; ++i) kk[n][i] = ldg16(k + j * ks + 32 * i + 8 * q);
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int j = j0 + 2 * q + (u & 1) + (u >> 1) * 8;
-#pragma unroll
-            for (int h = 0; h < D / 64; ++h) vv[u][h] = j < nk ? ldg16(v + j * ks + 64 * h + 8 * g) : z;
-        }
-        float s[2][4];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+    for (int j0 = ja; j0 < jb; j0 += 16) {
+        uint4 ka[kC], kb[kC], vv[4][D / 64];
+        {
+            const int64_t x = min(j0 + g, jb - 1) * ks, y = min(j0 + g + 8, jb - 1) * ks;
 #pragma unroll
             for (int i = 0; i < kC; ++i) {
-                mma16816(s[n], qa[i].x, qb[i].x, qa[i].y, qb[i].y, kk[n][i].x, kk[n][i].y);
-                mma16816(s[n], qa[i].z, qb[i].z, qa[i].w, qb[i].w, kk[n][i].z, kk[n][i].w);
+                ka[i] = ldg16(K + x + 32 * i + 8 * q);
+                kb[i] = ldg16(K + y + 32 * i + 8 * q);
             }
         }
-        // row half x (rows g, g + 8): weights of keys j0 + 8 n + 2 q + u
-        uint32_t p[2][2];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            bool ok[4];
-            float t[4];
+        for (int w = 0; w < 4; ++w) {
+            const int j = j0 + 2 * q + (w & 1) + (w >> 1) * 8;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int j = j0 + 8 * (e >> 1) + 2 * q + (e & 1);
-                ok[e] = j < nk;
-                if (a.windowed) ok[e] = ok[e] && j <= pos[x] && j > pos[x] - a.window;
-                t[e] = s[e >> 1][2 * x + (e & 1)];
+            for (int h = 0; h < D / 64; ++h)   // (values nobody sees must not enter as 0 * inf)
+                vv[w][h] = j < jb ? ldg16(V + j * ks + 64 * h + 8 * g) : z;
+        }
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // key g: rows 2 q, + 1; key g + 8: the same
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+            mma16816(s, ka[i].x, kb[i].x, ka[i].y, kb[i].y, qb[i].x, qb[i].y);
+            mma16816(s, ka[i].z, kb[i].z, ka[i].w, kb[i].w, qb[i].z, qb[i].w);
+        }
+        float p[4];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            bool ok[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int j = j0 + g + 8 * x;
+                ok[x] = j < jb;
+                if (a.windowed) ok[x] = ok[x] && j <= pos[w] && j > pos[w] - a.window;
             }
-            float w[4];
             if constexpr (kSm) {
-                float top = -INFINITY;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    t[e] = ok[e] ? t[e] * sc.c0 : -INFINITY;
-                    top = fmaxf(top, t[e]);
-                }
-                top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-                const float mn = fmaxf(m[x], top);
+                const float t0 = ok[0] ? s[w] * sc.c0 : -INFINITY, t1 = ok[1] ? s[2 + w] * sc.c0 : -INFINITY;
+                float top = fmaxf(t0, t1);
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
+                const float mn = fmaxf(m[w], top);
                 const float ref = mn == -INFINITY ? 0.0f : mn;
-                const float f = ex2_approx(m[x] - ref);
-                m[x] = mn;
-                float sum = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    w[e] = ex2_approx(t[e] - ref);
-                    sum += w[e];
-                }
-                l[x] = fmaf(l[x], f, sum);
+                const float f = ex2_approx(m[w] - ref);
+                m[w] = mn;
+                p[w] = ex2_approx(t0 - ref);
+                p[2 + w] = ex2_approx(t1 - ref);
+                l[w] = fmaf(l[w], f, p[w] + p[2 + w]);
                 if (f != 1.0f) {
 #pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        acc[i][2 * x] *= f;
-                        acc[i][2 * x + 1] *= f;
+                    for (int e = 0; e < products<D>(); ++e) {
+                        acc[e][w] *= f;
+                        acc[e][2 + w] *= f;
                     }
                 }
             } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = ok[e] ? act_s<ACT>(t[e], sc) : 0.0f;
+                p[w] = ok[0] ? act_s<ACT>(s[w], sc) : 0.0f;
+                p[2 + w] = ok[1] ? act_s<ACT>(s[2 + w], sc) : 0.0f;
             }
-            p[x][0] = tc::pack_bf16x2(w[0], w[1]);
-            p[x][1] = tc::pack_bf16x2(w[2], w[3]);
         }
+        const uint32_t b0 = transposed(tc::pack_bf16x2(p[0], p[1])), b1 = transposed(tc::pack_bf16x2(p[2], p[3]));
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                mma16816(acc[8 * h + e], p[0][0], p[1][0], p[0][1], p[1][1],
-                         pair_of(vv[0][h], vv[1][h], e), pair_of(vv[2][h], vv[3][h], e));
-    }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        const int row = g + 8 * x;
-        if (kSm) {
-            l[x] += __shfl_xor_sync(~0u, l[x], 1);
-            l[x] += __shfl_xor_sync(~0u, l[x], 2);
+        for (int e = 0; e < products<D>(); ++e) {
+            uint32_t a0, a1, a2, a3;
+            operand_t<D>(vv, e, a0, a1, a2, a3);
+            mma16816(acc[e], a0, a1, a2, a3, b0, b1);
         }
-        if (row >= nrows) continue;
-        if (kSm && q == 0) st[row] = make_float2(m[x], l[x]);
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-            for (int u = 0; u < 2; ++u)   // product 8 h + e holds columns 64 h + 16 q + 8 u + e
-#pragma unroll
-                for (int e = 0; e < 8; e += 4)
-                    *reinterpret_cast<float4*>(out + row * (D + 4) + 64 * h + 16 * q + 8 * u + e) =
-                        make_float4(acc[8 * h + e][2 * x + u], acc[8 * h + e + 1][2 * x + u],
-                                    acc[8 * h + e + 2][2 * x + u], acc[8 * h + e + 3][2 * x + u]);
     }
-}
-
-template <int D, int ACT>
-__global__ void __launch_bounds__(kThreads) own_merge_kernel(const OwnArgs a) {
-    constexpr bool kSm = ACT == kSoftmax;
-    __shared__ __align__(16) float own_o[kRows * (D + 4)];
-    __shared__ float2 own_st[kRows];
-    const PrefixTile t = a.tiles[blockIdx.x];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nrows = t.n * a.r, row0 = blockIdx.y * kRows;
-    if (row0 >= nrows) return;
-    const int row = row0 + lane;
-    const bool real = row < nrows;
-    const int tl = real ? row / a.r : 0, j = row - tl * a.r, tok = t.tok + tl;
-    PrefixOwn ow = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (real) ow = a.own[tok];
-    const bool small = ow.small && ow.nk > 0;
-    // runs of rows of one sample, cut at 16 rows: lane `lane` starts one?
-    const int prev_k0 = __shfl_up_sync(~0u, ow.k0, 1);
-    const bool prev_small = __shfl_up_sync(~0u, (int)small, 1);
-    const bool fresh = lane == 0 || prev_k0 != ow.k0 || prev_small != small;
-    const uint32_t starts = __ballot_sync(~0u, fresh);
-    const int run0 = 31 - __clz(starts & (0xffffffffu >> (31 - lane)));
-    const uint32_t cuts = __ballot_sync(~0u, fresh || (lane - run0) % 16 == 0);
-    const uint32_t work = __ballot_sync(~0u, small) & cuts;
-    int unit = 0;
-    for (uint32_t w = work; w; w &= w - 1, ++unit) {
-        if (unit % (kThreads / 32) != warp) continue;
-        const int ra = __ffs(w) - 1;
-        const uint32_t later = ra == 31 ? 0u : cuts >> (ra + 1);
-        const int rb = min(later ? ra + __ffs(later) : 32, nrows - row0);
-        const int k0 = __shfl_sync(~0u, ow.k0, ra), nk = __shfl_sync(~0u, ow.nk, ra);
-        const int ip[2] = {__shfl_sync(~0u, ow.i, min(ra + (lane >> 2), rb - 1)),
-                           __shfl_sync(~0u, ow.i, min(ra + (lane >> 2) + 8, rb - 1))};
-        auto qrow = [&](int i) {
-            const int x = row0 + ra + i, tt = x / a.r;
-            return a.q + ((int64_t)(t.tok + tt) * a.H + t.hk * a.r + (x - tt * a.r)) * D;
-        };
-        const int64_t ks = (int64_t)a.Hkv * D, k_at = (int64_t)k0 * ks + t.hk * D;
-        own_rows<D, ACT>(a, qrow, rb - ra, a.k + k_at, a.v + k_at, ks, nk, ip, own_o + ra * (D + 4),
-                         own_st + ra, lane);
-    }
-    __syncthreads();
-    if (!real) return;
-    const int layers = small ? 0 : ow.layers;
-    const int orow = ow.row0 + j;
-    const int64_t own0 = (int64_t)ow.part + (int64_t)t.hk * ow.layers * ow.rows;
-    const float2* st = reinterpret_cast<const float2*>(a.ml);
-    float top = -INFINITY, sum = 0.0f, ref = 0.0f;
+    if (ow.layers == 0) return;   // no row of the sample sees an own key
+    const int64_t part = (int64_t)ow.part + (int64_t)u.hk * ow.rows;
+    store_part<D>(acc, 1.0f, a.parts, part, ow.rows, rows.row0, rows.nrows, g, q);
     if (kSm) {
-        for (int i = 0; i < t.layers; ++i) top = fmaxf(top, st[(int64_t)t.part + (int64_t)i * nrows + row].x);
-        for (int i = 0; i < layers; ++i) top = fmaxf(top, st[own0 + (int64_t)i * ow.rows + orow].x);
-        if (small) top = fmaxf(top, own_st[lane].x);
-        ref = top == -INFINITY ? 0.0f : top;
-    }
-    const int c = warp * (D / 32);   // this thread's float4 columns: D / 8 values of its row
-    if constexpr (D == 128 || D == 64) {
-        constexpr int kN = D / 32;
-        float4 acc[kN];
 #pragma unroll
-        for (int x = 0; x < kN; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto add = [&](float w, const float4& s, float4& y) {
-            y.x = fmaf(w, s.x, y.x);
-            y.y = fmaf(w, s.y, y.y);
-            y.z = fmaf(w, s.z, y.z);
-            y.w = fmaf(w, s.w, y.w);
-        };
-        if (small) {
-            float w = 1.0f;
-            if (kSm) {
-                const float2 s = own_st[lane];
-                w = ex2_approx(s.x - ref);   // 0 for a row that sees none of them
-                sum = w * s.y;
-            }
-#pragma unroll
-            for (int x = 0; x < kN; ++x)
-                add(w, *reinterpret_cast<const float4*>(own_o + lane * (D + 4) + 4 * (c + x)), acc[x]);
+        for (int w = 0; w < 2; ++w) {
+            for (int o = 4; o < 32; o <<= 1) l[w] += __shfl_xor_sync(~0u, l[w], o);
+            if (g == 0 && 2 * q + w < rows.nrows)
+                reinterpret_cast<float2*>(a.ml)[part + rows.row0 + 2 * q + w] = make_float2(m[w], l[w]);
         }
-        for (int i = 0; i < t.layers + layers; ++i) {
-            const bool pre = i < t.layers;
-            const int n = pre ? nrows : ow.rows, prow = pre ? row : orow;
-            const int64_t part = pre ? (int64_t)t.part + (int64_t)i * nrows : own0 + (int64_t)(i - t.layers) * n;
-            float w = 1.0f;
-            if (kSm) {
-                const float2 s = st[part + prow];
-                w = ex2_approx(s.x - ref);
-                sum = fmaf(w, s.y, sum);
-                if (s.x == -INFINITY) continue;
-            }
-            const float4* src = reinterpret_cast<const float4*>(a.parts) + part * (D / 4) + prow;
-#pragma unroll
-            for (int x = 0; x < kN; ++x) add(w, src[(int64_t)(c + x) * n], acc[x]);
-        }
-        const float inv = !kSm ? 1.0f : sum > 0.0f ? 1.0f / sum : 0.0f;
-        const int64_t at = (int64_t)tok * a.H + t.hk * a.r + j;
-        uint32_t out[2 * kN];
-#pragma unroll
-        for (int x = 0; x < kN; ++x) {
-            out[2 * x] = tc::pack_bf16x2(acc[x].x * inv, acc[x].y * inv);
-            out[2 * x + 1] = tc::pack_bf16x2(acc[x].z * inv, acc[x].w * inv);
-        }
-        uint4* dst = reinterpret_cast<uint4*>(a.o + at * D + 4 * c);
-#pragma unroll
-        for (int x = 0; x < kN / 2; ++x)
-            dst[x] = make_uint4(out[4 * x], out[4 * x + 1], out[4 * x + 2], out[4 * x + 3]);
-        if (kSm && a.lse && warp == 0)
-            a.lse[at] = sum > 0.0f ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
     }
 }
 
-}  // namespace
+// Backward of units of at most 8 rows.
+template <int D, int ACT>
+__global__ void __launch_bounds__(kThreads, 2) own_bwd8_kernel(const OwnArgs a) {
+    constexpr bool kSm = ACT == kSoftmax;
+    constexpr int kC = D / 32, kW = D / 64;
+    const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (unit >= a.n) return;
+    const PrefixUnit u = a.units[unit];
+    const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const Rows rows{min(8, u.ntok * a.r), 0, u.tok, u.hk, a.r, a.H};
+    const int64_t ks = (int64_t)a.Hkv * D, k_at = (int64_t)u.k0 * ks + u.hk * D;
+    const __nv_bfloat16 *K = a.k + k_at, *V = a.v + k_at;
+    const PrefixOwn ow = a.own[u.tok];
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    const ActScale sc = act_scale<ACT>(a.alpha);
+    // rows as the second operand of the scores (row g) and of dK, dV (rows
+    // 2 q, 2 q + 1; the contraction's rows 8 .. 15 are zeros)
+    uint4 qb[kC], ob[kC], qv[2][kW], ov[2][kW];
+    float l2[2] = {INFINITY, INFINITY}, dl[2] = {0.0f, 0.0f};
+    int pos[2];
+    {
+        const int64_t at = g < rows.nrows ? rows.at(g) * D : 0;
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+            qb[i] = g < rows.nrows ? ldg16(a.q + at + 32 * i + 8 * q) : z;
+            ob[i] = g < rows.nrows ? ldg16(a.d_o + at + 32 * i + 8 * q) : z;
+        }
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const int i = 2 * q + w;
+            const bool real = i < rows.nrows;
+            const int64_t x = real ? rows.at(i) : 0;
+            pos[w] = i / a.r;
+#pragma unroll
+            for (int h = 0; h < kW; ++h) {
+                qv[w][h] = real ? ldg16(a.q + x * D + 64 * h + 8 * g) : z;
+                ov[w][h] = real ? ldg16(a.d_o + x * D + 64 * h + 8 * g) : z;
+            }
+            if (kSm && real) {
+                const float y = a.lse[x];
+                l2[w] = y == -INFINITY ? INFINITY : y * kLog2e;
+                dl[w] = a.delta[x];
+            }
+        }
+    }
+    float acc[products<D>()][4];   // dQ^T
+#pragma unroll
+    for (int e = 0; e < products<D>(); ++e) acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.0f;
+    for (int j0 = 0; j0 < u.nk; j0 += 16) {
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, dp[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        uint4 kv[4][kW];
+        {
+            const int64_t x = min(j0 + g, u.nk - 1) * ks, y = min(j0 + g + 8, u.nk - 1) * ks;
+            uint4 ka[kC], kb[kC], va[kC], vb[kC];
+#pragma unroll
+            for (int i = 0; i < kC; ++i) {
+                ka[i] = ldg16(K + x + 32 * i + 8 * q);
+                kb[i] = ldg16(K + y + 32 * i + 8 * q);
+                va[i] = ldg16(V + x + 32 * i + 8 * q);
+                vb[i] = ldg16(V + y + 32 * i + 8 * q);
+            }
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const int j = j0 + 2 * q + (w & 1) + (w >> 1) * 8;
+#pragma unroll
+                for (int h = 0; h < kW; ++h) kv[w][h] = j < u.nk ? ldg16(K + j * ks + 64 * h + 8 * g) : z;
+            }
+#pragma unroll
+            for (int i = 0; i < kC; ++i) {
+                mma16816(s, ka[i].x, kb[i].x, ka[i].y, kb[i].y, qb[i].x, qb[i].y);
+                mma16816(dp, va[i].x, vb[i].x, va[i].y, vb[i].y, ob[i].x, ob[i].y);
+                mma16816(s, ka[i].z, kb[i].z, ka[i].w, kb[i].w, qb[i].z, qb[i].w);
+                mma16816(dp, va[i].z, vb[i].z, va[i].w, vb[i].w, ob[i].z, ob[i].w);
+            }
+        }
+        float p[4], ds[4];
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int j = j0 + g + 8 * x, c = 2 * x + w;
+                bool ok = j < u.nk && 2 * q + w < rows.nrows;
+                if (a.windowed) ok = ok && j <= pos[w] && j > pos[w] - a.window;
+                if constexpr (kSm) {
+                    p[c] = ex2_approx(fmaf(s[c], sc.c0, -l2[w]));
+                    ds[c] = p[c] * (dp[c] - dl[w]);
+                } else {
+                    float da;
+                    act_dact_s<ACT>(s[c], sc, p[c], da);
+                    ds[c] = dp[c] * da;
+                }
+                if (!ok) p[c] = ds[c] = 0.0f;
+            }
+        // rows 2 q, 2 q + 1 of keys g and g + 8: the first operand of dV, dK
+        const uint32_t p0 = tc::pack_bf16x2(p[0], p[1]), p1 = tc::pack_bf16x2(p[2], p[3]);
+        const uint32_t d0 = tc::pack_bf16x2(ds[0], ds[1]), d1 = tc::pack_bf16x2(ds[2], ds[3]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)   // dV, then dK
+#pragma unroll
+            for (int h = 0; h < kW; ++h) {
+                float o[8][4];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.0f;
+                    const uint32_t b = i ? pair_of(qv[0][h], qv[1][h], e) : pair_of(ov[0][h], ov[1][h], e);
+                    mma16816(o[e], i ? d0 : p0, i ? d1 : p1, 0u, 0u, b, 0u);
+                }
+                // product e: columns 64 h + 16 q + e and + 8 + e of keys g, g + 8
+                const float f = i ? a.alpha : 1.0f;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int j = j0 + g + 8 * x;
+                    if (j >= u.nk) continue;
+                    __nv_bfloat16* dst = (i ? a.dk : a.dv) + k_at + j * ks + 64 * h + 16 * q;
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            y[e] = tc::pack_bf16x2(o[2 * e][2 * x + w] * f, o[2 * e + 1][2 * x + w] * f);
+                        reinterpret_cast<uint4*>(dst)[w] = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                }
+            }
+        const uint32_t b0 = transposed(d0), b1 = transposed(d1);
+#pragma unroll
+        for (int e = 0; e < products<D>(); ++e) {
+            uint32_t a0, a1, a2, a3;
+            operand_t<D>(kv, e, a0, a1, a2, a3);
+            mma16816(acc[e], a0, a1, a2, a3, b0, b1);
+        }
+    }
+    if (ow.layers == 0) return;
+    store_part<D>(acc, a.alpha, a.parts, (int64_t)ow.part + (int64_t)u.hk * ow.rows, ow.rows, 0, rows.nrows, g, q);
+}
 
-gdpa_status launch_prefix_own_merge(PrefixPlan& p, const PrefixIO& io, cudaStream_t st) {
-    if (p.tiles.empty()) return GDPA_OK;
+OwnArgs args_of(const PrefixPlan& p, const PrefixIO& io, const float* delta) {
     OwnArgs a;
-    a.tiles = p.dev_tiles();
+    a.units = nullptr;
+    a.n = 0;
     a.own = p.dev_own();
     a.q = (const __nv_bfloat16*)io.q;
     a.k = (const __nv_bfloat16*)io.k;
     a.v = (const __nv_bfloat16*)io.v;
-    a.o = (__nv_bfloat16*)io.o;
-    a.lse = io.act == kSoftmax ? io.lse : nullptr;
+    a.d_o = (const __nv_bfloat16*)io.d_o;
+    a.dk = (__nv_bfloat16*)io.dk;
+    a.dv = (__nv_bfloat16*)io.dv;
+    a.lse = io.lse;
+    a.delta = delta;
     a.parts = p.d_parts;
     a.ml = p.d_ml;
     a.H = p.H;
@@ -301,20 +360,49 @@ gdpa_status launch_prefix_own_merge(PrefixPlan& p, const PrefixIO& io, cudaStrea
     a.windowed = p.mask == GDPA_MASK_CAUSAL_WINDOW;
     a.window = p.window;
     a.alpha = io.alpha;
-    const dim3 grid((unsigned)p.tiles.size(), 4);
+    return a;
+}
+
+template <int D, int ACT>
+void go(bool bwd, const OwnArgs& a, cudaStream_t st) {
+    const unsigned grid = (unsigned)((a.n + kWarps - 1) / kWarps);
+    if (bwd)
+        own_bwd8_kernel<D, ACT><<<grid, kThreads, 0, st>>>(a);
+    else
+        own_fwd_kernel<D, ACT><<<grid, kThreads, 0, st>>>(a);
+}
+
+gdpa_status dispatch(bool bwd, PrefixPlan& p, const OwnArgs& a, int act, cudaStream_t st) {
+    if (a.n == 0) return GDPA_OK;
     if (p.d == 128) {
-        if (io.act == kSoftmax)
-            own_merge_kernel<128, kSoftmax><<<grid, kThreads, 0, st>>>(a);
+        if (act == kSoftmax)
+            go<128, kSoftmax>(bwd, a, st);
         else
-            GDPA_DISPATCH_ACT(io.act, A, own_merge_kernel<128, A><<<grid, kThreads, 0, st>>>(a))
+            GDPA_DISPATCH_ACT(act, A, go<128, A>(bwd, a, st))
     } else {
-        if (io.act == kSoftmax)
-            own_merge_kernel<64, kSoftmax><<<grid, kThreads, 0, st>>>(a);
+        if (act == kSoftmax)
+            go<64, kSoftmax>(bwd, a, st);
         else
-            GDPA_DISPATCH_ACT(io.act, A, own_merge_kernel<64, A><<<grid, kThreads, 0, st>>>(a))
+            GDPA_DISPATCH_ACT(act, A, go<64, A>(bwd, a, st))
     }
     p.launches += 1;
     return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+}
+
+}  // namespace
+
+gdpa_status launch_prefix_own_fwd(PrefixPlan& p, const PrefixIO& io, cudaStream_t st) {
+    OwnArgs a = args_of(p, io, nullptr);
+    a.units = p.dev_eights();
+    a.n = (int)p.eights.size();
+    return dispatch(false, p, a, io.act, st);
+}
+
+gdpa_status launch_prefix_own_bwd8(PrefixPlan& p, const PrefixIO& io, const float* delta, cudaStream_t st) {
+    OwnArgs a = args_of(p, io, delta);
+    a.units = p.dev_smalls();
+    a.n = (int)p.n_small8;
+    return dispatch(true, p, a, io.act, st);
 }
 
 }  // namespace gdpa

@@ -1,6 +1,6 @@
-// Shared-prefix attention backward: the small own keys (the rule is the
-// planner's: few packed rows, few keys), with warp-level products straight
-// from global memory as in the forward (prefix_own.cu).
+// Shared-prefix attention backward: the small own keys of units of 9 to 64
+// packed rows, with warp-level products straight from global memory (as
+// prefix_own.cu, which has the units of at most 8 rows).
 //
 // A block takes one (sample, key head); its 4 warps deal its tasks:
 //   key tasks, 16 keys and 64 of the d columns: over the sample's rows 16 at
@@ -254,9 +254,9 @@ __global__ void __launch_bounds__(kThreads) own_bwd_kernel(const OwnBwArgs a) {
 }  // namespace
 
 gdpa_status launch_prefix_own_bwd(PrefixPlan& p, const PrefixIO& io, const float* delta, cudaStream_t st) {
-    if (p.smalls.empty()) return GDPA_OK;
+    if ((int64_t)p.smalls.size() == p.n_small8) return GDPA_OK;
     OwnBwArgs a;
-    a.units = p.dev_smalls();
+    a.units = p.dev_smalls() + p.n_small8;
     a.own = p.dev_own();
     a.q = (const __nv_bfloat16*)io.q;
     a.k = (const __nv_bfloat16*)io.k;
@@ -273,7 +273,7 @@ gdpa_status launch_prefix_own_bwd(PrefixPlan& p, const PrefixIO& io, const float
     a.windowed = p.mask == GDPA_MASK_CAUSAL_WINDOW;
     a.window = p.window;
     a.alpha = io.alpha;
-    const unsigned grid = (unsigned)p.smalls.size();
+    const unsigned grid = (unsigned)((int64_t)p.smalls.size() - p.n_small8);
     if (p.d == 128) {
         if (io.act == kSoftmax)
             own_bwd_kernel<128, kSoftmax><<<grid, kThreads, 0, st>>>(a);

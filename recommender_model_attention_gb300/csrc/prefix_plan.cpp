@@ -17,8 +17,8 @@ namespace {
 
 constexpr int kPieceCost = 3;   // steps a piece costs beside its own
 
-// Own keys of samples with at most this many packed rows and keys are taken
-// by the merge (prefix_own.cu), which streams them without a tile's latency.
+// Own keys of samples with at most this many packed rows and keys are streamed
+// by warp-level kernels (prefix_own.cu), without a tile's latency.
 constexpr int kSmallRows = 64;
 constexpr int kSmallKeys = 512;
 
@@ -238,7 +238,7 @@ gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t
             for (int hk = 0; hk < p.Hkv; ++hk)
                 p.units.push_back(PrefixUnit{k, std::min(kBN, prefix_off[g + 1] - k), t0, nt, hk, 0, 0, 0});
     }
-    std::vector<PrefixUnit> small_blocks;
+    std::vector<PrefixUnit> small_blocks, more;
     for (int b = 0; b < p.B; ++b) {
         const int32_t lq = q_off[b + 1] - q_off[b], lk = kv_off[b + 1] - kv_off[b];
         const bool small = lq > 0 && is_small(p, lq, lk);
@@ -252,10 +252,19 @@ gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t
                     .push_back(PrefixUnit{kv_off[b] + j, nk, q_off[b] + lo, std::max(0, hi - lo), hk, kPieceOwn,
                                           lo, j});
         }
-        if (small)
-            for (int hk = 0; hk < p.Hkv && lk > 0; ++hk)
-                p.smalls.push_back(PrefixUnit{kv_off[b], lk, q_off[b], lq, hk, kPieceOwn, 0, 0});
+        if (small && lk > 0)
+            for (int hk = 0; hk < p.Hkv; ++hk) {
+                const PrefixUnit u{kv_off[b], lk, q_off[b], lq, hk, kPieceOwn, 0, 0};
+                (lq * p.r <= 8 ? p.smalls : more).push_back(u);
+                p.eights.push_back(u);
+                for (int32_t row = 8; row < lq * p.r; row += 8) {
+                    p.eights.push_back(u);
+                    p.eights.back().j0 = row;
+                }
+            }
     }
+    p.n_small8 = (int64_t)p.smalls.size();
+    p.smalls.insert(p.smalls.end(), more.begin(), more.end());
     // deal them by their row tiles (and a unit's own loads and stores) in
     // snake order, longest first
     const int64_t n = (int64_t)p.units.size();

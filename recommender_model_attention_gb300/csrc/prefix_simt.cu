@@ -316,59 +316,76 @@ __global__ void __launch_bounds__(kThreads) simt_keys_kernel(const SimtArgs a) {
     }
 }
 
-// Join the parts of 32 rows of a tile: warp w takes float4 columns 4 (w + 8
-// i) .. + 3 of every row (a thread writes 16 consecutive columns of its row).
+// Join the parts of 8 rows of a tile: a thread per (row, 4 columns), a warp's
+// four threads of a row sharing the look at its maxima, eight layers of loads
+// in flight at a time.
 template <typename E>
 __global__ void __launch_bounds__(256) merge_kernel(const PrefixTile* tiles, const PrefixOwn* owns,
                                                     const float* parts, const float* ml, E* out,
                                                     float* lse, int H, int r, int d, int softmax) {
     const PrefixTile t = tiles[blockIdx.x];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row = blockIdx.y * 32 + lane;
-    if (row >= t.n * r) return;
-    const int tl = row / r, j = row - tl * r;
-    const int tok = t.tok + tl;
-    const PrefixOwn ow = owns[tok];
-    const int nr = t.n * r, orow = ow.row0 + j;
+    const int nrows = t.n * r, row = blockIdx.y * 8 + (lane & 7);
+    if (blockIdx.y * 8 >= nrows) return;
+    const bool real = row < nrows;
+    const int tl = real ? row / r : 0, j = row - tl * r, tok = t.tok + tl;
+    PrefixOwn ow = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (real) ow = owns[tok];
+    const int orow = ow.row0 + j, total = real ? t.layers + ow.layers : 0;
     const int64_t own0 = (int64_t)ow.part + (int64_t)t.hk * ow.layers * ow.rows;
     const float2* st = reinterpret_cast<const float2*>(ml);
-    float top = -INFINITY, sum = 0.f;
+    // layer x: its first row in the workspace, its rows, this row's place
+    auto place = [&](int x, int& n, int& at) {
+        const bool pre = x < t.layers;
+        n = pre ? nrows : ow.rows;
+        at = pre ? row : orow;
+        return pre ? (int64_t)t.part + (int64_t)x * nrows : own0 + (int64_t)(x - t.layers) * ow.rows;
+    };
+    const int c4 = d / 4, c = (lane >> 3) + 4 * warp;
+    float top = -INFINITY, ref = 0.f, sum = 0.f;
     if (softmax) {
-        for (int i = 0; i < t.layers; ++i) top = fmaxf(top, st[(int64_t)t.part + (int64_t)i * nr + row].x);
-        for (int i = 0; i < ow.layers; ++i) top = fmaxf(top, st[own0 + (int64_t)i * ow.rows + orow].x);
+#pragma unroll 4
+        for (int x = lane >> 3; x < total; x += 4) {
+            int n, at;
+            const int64_t p = place(x, n, at);
+            top = fmaxf(top, st[p + at].x);
+        }
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
+        ref = top == -INFINITY ? 0.f : top;
     }
-    const float ref = top == -INFINITY ? 0.f : top;
-    const int64_t at = (int64_t)tok * H + t.hk * r + j;
-    const int c4 = d / 4;
-    for (int c = warp * 4; c < c4; c += 32) {
-        float4 acc[4];
+    if (!real || c >= c4) return;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4* src = reinterpret_cast<const float4*>(parts);
+    for (int x0 = 0; x0 < total; x0 += 8) {
+        float2 s[8];
+        float4 v[8];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-        sum = 0.f;
-        for (int i = 0; i < t.layers + ow.layers; ++i) {
-            const bool pre = i < t.layers;
-            const int n = pre ? nr : ow.rows, prow = pre ? row : orow;
-            const int64_t part = pre ? t.part + (int64_t)i * nr : own0 + (int64_t)(i - t.layers) * n;
+        for (int u = 0; u < 8; ++u) {
+            s[u] = make_float2(-INFINITY, 0.f);
+            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (x0 + u < total) {
+                int n, at;
+                const int64_t p = place(x0 + u, n, at);
+                if (softmax) s[u] = st[p + at];
+                v[u] = src[p * c4 + (int64_t)c * n + at];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
             float w = 1.f;
             if (softmax) {
-                const float2 s = st[part + prow];
-                w = exp2f(s.x - ref);   // 0 for a part without a visible key
-                sum = fmaf(w, s.y, sum);
-                if (s.x == -INFINITY) continue;
+                w = exp2f(s[u].x - ref);   // 0 for a part without a visible key
+                sum = fmaf(w, s[u].y, sum);
+                if (s[u].x == -INFINITY) continue;
             }
-            const float4* src = reinterpret_cast<const float4*>(parts) + part * c4 + prow;
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                if (c + x < c4) axpy4(acc[x], w, src[(int64_t)(c + x) * n]);
+            axpy4(acc, w, v[u]);
         }
-        const float inv = !softmax ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-            if (c + x < c4)
-                st4(out + at * d + 4 * (c + x), make_float4(acc[x].x * inv, acc[x].y * inv,
-                                                            acc[x].z * inv, acc[x].w * inv));
     }
-    if (softmax && lse && warp == 0)
+    const float inv = !softmax ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
+    const int64_t at = (int64_t)tok * H + t.hk * r + j;
+    st4(out + at * d + 4 * c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    if (softmax && lse && c == 0)
         lse[at] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
 }
 
@@ -459,7 +476,7 @@ gdpa_status launch_prefix_simt_bwd(PrefixPlan& p, gdpa_dtype dt, const PrefixIO&
 gdpa_status launch_prefix_merge(PrefixPlan& p, gdpa_dtype dt, void* out, float* lse, bool softmax,
                                 cudaStream_t st) {
     if (p.tiles.empty()) return GDPA_OK;
-    const dim3 grid((unsigned)p.tiles.size(), 4);
+    const dim3 grid((unsigned)p.tiles.size(), kBM / 8);
     if (dt == GDPA_BF16)
         merge_kernel<<<grid, 256, 0, st>>>(p.dev_tiles(), p.dev_own(), p.d_parts, p.d_ml,
                                            (__nv_bfloat16*)out, lse, p.H, p.r, p.d, softmax);

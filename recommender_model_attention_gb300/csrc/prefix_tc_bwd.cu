@@ -28,8 +28,7 @@
 #include <cuda_bf16.h>
 
 #include "act.cuh"
-#include "prefix_internal.h"
-#include "tc_common.cuh"
+#include "prefix_tc.cuh"
 
 namespace gdpa {
 namespace {
@@ -55,19 +54,6 @@ struct BwArgs {
     int32_t* err;
     uint64_t wait_ns;
 };
-
-__device__ __forceinline__ void load3(const CUtensorMap* map, uint64_t* bar, void* dst, int32_t x,
-                                      int32_t y, int32_t z, uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
-        : "memory");
-}
-
-// Where 16-column step k of an item's packed weights lies: each warpgroup's 32
-// columns, packed in 16, over the first of its own scores.
-__device__ __forceinline__ constexpr uint32_t packed(int k) { return (k >> 1) * 32 + (k & 1) * 8; }
 
 // weights and score gradients of two pairs
 template <int ACT>
@@ -113,15 +99,6 @@ struct KvCfg {
     static constexpr int kSmem = kOffBar + kNumBars * 8 + 16 + 1024;
 };
 
-__device__ __forceinline__ PrefixUnit load_unit(const PrefixUnit* p) {
-    const int4* q = reinterpret_cast<const int4*>(p);
-    const int4 a = __ldg(q), b = __ldg(q + 1);
-    PrefixUnit u;
-    u.k0 = a.x; u.nk = a.y; u.tok = a.z; u.ntok = a.w;
-    u.hk = b.x; u.flags = b.y; u.i0 = b.z; u.j0 = b.w;
-    return u;
-}
-
 // rows of tile m of a unit, and its 64-row items
 __device__ __forceinline__ int tile_rows(const PrefixUnit& u, const BwArgs& a, int m) {
     return min(a.tpt, u.ntok - m * a.tpt) * a.r;
@@ -161,9 +138,9 @@ __device__ void kv_producer(const CUtensorMap* tmQ, const CUtensorMap* tmDO, con
             armed[st] = (int32_t)ph;
 #pragma unroll
             for (int hf = 0; hf < C::kHalves; ++hf) {
-                load3(tmQ, &bars[C::kFull + st], smem + C::kOffQ + st * C::kTile + hf * kHalfBytes, hf * 64,
+                tma_load_3d(tmQ, &bars[C::kFull + st], smem + C::kOffQ + st * C::kTile + hf * kHalfBytes, hf * 64,
                       u.hk * a.r, u.tok + m * a.tpt, keep);
-                load3(tmDO, &bars[C::kFull + st], smem + C::kOffDO + st * C::kTile + hf * kHalfBytes, hf * 64,
+                tma_load_3d(tmDO, &bars[C::kFull + st], smem + C::kOffDO + st * C::kTile + hf * kHalfBytes, hf * 64,
                       u.hk * a.r, u.tok + m * a.tpt, keep);
             }
         }
@@ -182,9 +159,13 @@ __device__ void kv_mma(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t 
     constexpr uint32_t idesc_acc = idesc_bf16(128, D, false, true);
     const uint64_t kd = smem_desc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
     const uint64_t vd = smem_desc_sw128(smem_u32(smem + C::kOffV), 16, 1024);
+    tmem = (uint32_t)uniform((int)tmem);
+    seg0 = uniform(seg0);
+    seg1 = uniform(seg1);
     uint32_t nu = 0, tile0 = 0, e0 = 0;   // units, tiles and items before this unit
     for (int t = seg0; t < seg1; ++t) {
-        const PrefixUnit u = load_unit(a.units + t);
+        PrefixUnit u = load_unit(a.units + t);
+        u.ntok = uniform(u.ntok);
         const int tiles = (u.ntok + a.tpt - 1) / a.tpt;
         if (tiles == 0) continue;
         const int full = a.tpt * a.r > kItem ? 2 : 1;   // items of every tile but the last
@@ -202,10 +183,8 @@ __device__ void kv_mma(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t 
             const uint64_t qd = smem_desc_sw128(smem_u32(smem + C::kOffQ + off), 16, 1024);
             const uint64_t dd = smem_desc_sw128(smem_u32(smem + C::kOffDO + off), 16, 1024);
             const uint32_t id = idesc_bf16(128, rows16(x), false, false);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) mma_ss(col, kd + kmajor_step(k), qd + kmajor_step(k), id, k > 0);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) mma_ss(col + 64, vd + kmajor_step(k), dd + kmajor_step(k), id, k > 0);
+            mma_scores<D>(col, kd, qd, id);
+            mma_scores<D>(col + 64, vd, dd, id);
             mma_commit(&bars[C::kSDFull + ((e0 + x) & 1)]);
             if (x == items - 1) mma_commit(&bars[C::kKVEmpty]);
             return true;
@@ -222,14 +201,8 @@ __device__ void kv_mma(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t 
             const uint64_t qd = smem_desc_sw128(smem_u32(smem + C::kOffQ + off), kHalfBytes, 1024);
             const uint64_t dd = smem_desc_sw128(smem_u32(smem + C::kOffDO + off), kHalfBytes, 1024);
             const uint32_t steps = rows16(x) / 16;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if ((uint32_t)k < steps)
-                    mma_ts(tmem + 256, col + packed(k), dd + mnmajor_step(k), idesc_acc, x > 0 || k > 0);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if ((uint32_t)k < steps)
-                    mma_ts(tmem + 384, col + 64 + packed(k), qd + mnmajor_step(k), idesc_acc, x > 0 || k > 0);
+            mma_sums(tmem + 256, col, col + 32, dd, idesc_acc, steps, x > 0);
+            mma_sums(tmem + 384, col + 64, col + 96, qd, idesc_acc, steps, x > 0);
             if (x % full == full - 1 || x == items - 1) mma_commit(&bars[C::kEmpty + st]);
             if (x == items - 1) mma_commit(&bars[C::kAccFull]);
             if (x + 2 < items && !issue_s(x + 2)) goto drain;
@@ -441,16 +414,6 @@ struct DqCfg {
     static constexpr int kSmem = kOffBar + kNumBars * 8 + 16 + 1024;
 };
 
-__device__ __forceinline__ PrefixPiece load_piece(const PrefixPiece* p) {
-    const int4* q = reinterpret_cast<const int4*>(p);
-    const int4 a = __ldg(q), b = __ldg(q + 1), c = __ldg(q + 2);
-    PrefixPiece t;
-    t.tok = a.x; t.nA = a.y; t.nB = a.z; t.hk = a.w;
-    t.k0 = b.x; t.nk = b.y; t.flags = b.z; t.i0 = b.w;
-    t.j0 = c.x; t.part0 = c.y; t.part1 = c.z; t.pad = 0;
-    return t;
-}
-
 // A run: one row tile against the key blocks of one slot of a piece.
 struct Run {
     int tok, rows, i0, part, blocks, step, first;
@@ -495,8 +458,8 @@ __device__ void dq_producer(const CUtensorMap* tmQ, const CUtensorMap* tmDO, con
         q_armed = (int32_t)(nr & 1);
 #pragma unroll
         for (int hf = 0; hf < C::kHalves; ++hf) {
-            load3(tmQ, &bars[C::kQFull], smem + C::kOffQ + hf * kHalfBytes, hf * 64, p.hk * a.r, run.tok, once);
-            load3(tmDO, &bars[C::kQFull], smem + C::kOffDO + hf * kHalfBytes, hf * 64, p.hk * a.r, run.tok, once);
+            tma_load_3d(tmQ, &bars[C::kQFull], smem + C::kOffQ + hf * kHalfBytes, hf * 64, p.hk * a.r, run.tok, once);
+            tma_load_3d(tmDO, &bars[C::kQFull], smem + C::kOffDO + hf * kHalfBytes, hf * 64, p.hk * a.r, run.tok, once);
         }
         const bool own = p.flags & kPieceOwn;
         for (int j = 0; j < run.blocks; ++j)
@@ -526,9 +489,13 @@ __device__ void dq_mma(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t 
     constexpr uint32_t idesc_acc = idesc_bf16(128, D, false, true);
     const uint64_t qd = smem_desc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
     const uint64_t dd = smem_desc_sw128(smem_u32(smem + C::kOffDO), 16, 1024);
+    tmem = (uint32_t)uniform((int)tmem);
+    seg0 = uniform(seg0);
+    seg1 = uniform(seg1);
     uint32_t nr = 0, ring = 0, e0 = 0;
     for (int t = 2 * seg0; t < 2 * seg1; ++t) {
-        const PrefixPiece p = load_piece(a.pieces + (t >> 1));
+        PrefixPiece p = load_piece(a.pieces + (t >> 1));
+        p.nk = uniform(p.nk); p.flags = uniform(p.flags); p.part0 = uniform(p.part0); p.part1 = uniform(p.part1);
         const Run run(p, t & 1, a.r);
         if (run.blocks == 0) continue;
         const int items = run.items();
@@ -547,10 +514,8 @@ __device__ void dq_mma(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t 
             const uint64_t kd = smem_desc_sw128(smem_u32(smem + C::kOffKV + sk * C::kTile + off), 16, 1024);
             const uint64_t vd = smem_desc_sw128(smem_u32(smem + C::kOffKV + sv * C::kTile + off), 16, 1024);
             const uint32_t id = idesc_bf16(128, n16(x), false, false);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) mma_ss(col, qd + kmajor_step(k), kd + kmajor_step(k), id, k > 0);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) mma_ss(col + 64, dd + kmajor_step(k), vd + kmajor_step(k), id, k > 0);
+            mma_scores<D>(col, qd, kd, id);
+            mma_scores<D>(col + 64, dd, vd, id);
             mma_commit(&bars[C::kSDFull + ((e0 + x) & 1)]);
             if (last_of(x)) mma_commit(&bars[C::kEmpty + sv]);
             if (x == items - 1) mma_commit(&bars[C::kQEmpty]);
@@ -567,11 +532,8 @@ __device__ void dq_mma(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t 
             const uint64_t kd = smem_desc_sw128(
                 smem_u32(smem + C::kOffKV + sk * C::kTile + (x & 1) * (kItem * 128)), kHalfBytes, 1024);
             const uint32_t steps = n16(x) / 16;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if ((uint32_t)k < steps)
-                    mma_ts(tmem + 256, tmem + (e & 1) * 128 + packed(k), kd + mnmajor_step(k), idesc_acc,
-                           x > 0 || k > 0);
+            const uint32_t col = tmem + (e & 1) * 128;
+            mma_sums(tmem + 256, col, col + 32, kd, idesc_acc, steps, x > 0);
             if (last_of(x)) mma_commit(&bars[C::kEmpty + sk]);
             if (x == items - 1) mma_commit(&bars[C::kAccFull]);
             if (x + 2 < items && !issue_s(x + 2)) goto drain;

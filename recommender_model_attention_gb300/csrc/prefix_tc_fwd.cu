@@ -11,9 +11,10 @@
 //              gives a part of its own.
 // Warp 0 loads (TMA): the piece's query tiles, then K and V blocks through
 // one ring, in the order in which the tensor core takes them.  Warp 1 issues
-// S = Q K^T and O += P V: slot 0's P V and next S run while slot 1's weights
-// are computed, and the other way round; the P V of a block's first 64 keys
-// starts when their warpgroup is done.  The warpgroups (a row's two threads
+// S = Q K^T and O += P V: one slot's P V and next S run while the other's
+// weights are computed; the P V of a block's first 64 keys starts when their
+// warpgroup is done.  (An issuer per slot was no faster: a slot's chain of
+// scores, weights and sums is what takes the time.)  The warpgroups (a row's two threads
 // exchange their maxima through shared memory) keep the row maximum as a
 // reference that only moves when it would be passed by more than 8 (in
 // base 2: weights stay below 2^8), so O is rescaled in TMEM a few times a
@@ -31,8 +32,7 @@
 #include <cuda_bf16.h>
 
 #include "act.cuh"
-#include "prefix_internal.h"
-#include "tc_common.cuh"
+#include "prefix_tc.cuh"
 
 namespace gdpa {
 namespace {
@@ -74,16 +74,6 @@ struct PfParams {
     uint64_t wait_ns;
 };
 
-__device__ __forceinline__ PrefixPiece load_piece(const PrefixPiece* p) {
-    const int4* q = reinterpret_cast<const int4*>(p);
-    const int4 a = __ldg(q), b = __ldg(q + 1), c = __ldg(q + 2);
-    PrefixPiece t;
-    t.tok = a.x; t.nA = a.y; t.nB = a.z; t.hk = a.w;
-    t.k0 = b.x; t.nk = b.y; t.flags = b.z; t.i0 = b.w;
-    t.j0 = c.x; t.part0 = c.y; t.part1 = c.z; t.pad = 0;
-    return t;
-}
-
 // Blocks of a piece, of each slot, and where they lie in the ring (counted
 // from the piece's first load).
 struct Walk {
@@ -101,15 +91,6 @@ struct Walk {
     __device__ __forceinline__ int k_at(int b) const { return dual ? (b < 2 ? b : 2 * b - 1) : 2 * b; }
     __device__ __forceinline__ int v_at(int b) const { return dual ? min(b + 2, nb) + b : 2 * b + 1; }
 };
-
-__device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* bar, void* dst,
-                                            int32_t x, int32_t y, int32_t z, uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
-        : "memory");
-}
 
 template <int D>
 __device__ void pf_producer(const CUtensorMap* tmQ, const CUtensorMap* tmKp, const CUtensorMap* tmVp,
@@ -165,70 +146,65 @@ unwind:
 }
 
 template <int D>
-__device__ void pf_mma(const PfParams& prm, uint8_t* smem, uint64_t* bars, uint32_t tmem, int seg0,
-                       int seg1, const Abort& ab) {
+__device__ void pf_mma(const PfParams& prm, uint8_t* smem, uint64_t* bars, uint32_t tmem, int seg0, int seg1,
+                       const Abort& ab) {
     using C = PfCfg<D>;
     constexpr uint32_t idesc_pv = idesc_bf16(128, D, false, true);
-    uint32_t base = 0, items[2] = {0, 0}, used[2] = {0, 0};   // blocks and pieces of each slot so far
+    uint32_t base = 0, items0 = 0, items1 = 0, used0 = 0, used1 = 0;   // ring places; blocks, pieces of a slot
+    tmem = (uint32_t)uniform((int)tmem);
+    const uint32_t kv = smem_u32(smem + C::kOffKV);
     for (int t = seg0; t < seg1; ++t) {
-        const PrefixPiece p = load_piece(prm.pieces + t);
+        PrefixPiece p = load_piece(prm.pieces + t);
+        p.nk = uniform(p.nk);
+        p.flags = uniform(p.flags);
         const Walk w(p);
-        auto stage = [&](int at) { return (base + (uint32_t)at) % C::kStages; };
-        auto phase = [&](int at) { return ((base + (uint32_t)at) / C::kStages) & 1; };
-        auto n16 = [&](int b) { return (uint32_t)((min(kBN, p.nk - b * kBN) + 15) & ~15); };
-        auto issue_s = [&](int s, int j) -> bool {
-            const int b = w.block(s, j), at = w.k_at(b);
-            if (!wg_wait(&bars[C::kFull + stage(at)], phase(at), ab, 64)) return false;
-            tc_fence_after();
-            const uint64_t qd = smem_desc_sw128(
-                smem_u32(smem + C::kOffQ + (s && !w.dual ? C::kTile : 0)), 16, 1024);
-            const uint64_t kd = smem_desc_sw128(smem_u32(smem + C::kOffKV + stage(at) * C::kTile), 16, 1024);
-            const uint32_t id = idesc_bf16(128, n16(b), false, false);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-                mma_ss(tmem + s * 128, qd + kmajor_step(k), kd + kmajor_step(k), id, k > 0);
-            mma_commit(&bars[C::kSFull + s]);
-            if (w.dual || s == 1) mma_commit(&bars[C::kEmpty + stage(at)]);
-            // the piece's last S: its queries may be replaced
-            if (b == w.nb - 1 && (w.dual || s == 1)) mma_commit(&bars[C::kQEmpty]);
-            return true;
-        };
         if (!wg_wait(&bars[C::kQFull], (uint32_t)(t - seg0) & 1, ab, 63)) goto drain;
-        for (int s = 0; s < 2; ++s)
-            if (w.blocks(s) > 0 && !issue_s(s, 0)) goto drain;
-        for (int j = 0; j < w.n0; ++j) {
-            for (int s = 0; s < 2; ++s) {
-                const int n = w.blocks(s);
-                if (j >= n) continue;
-                const int b = w.block(s, j), at = w.v_at(b);
+        // step j: each slot's P V of its block j - 1 (behind the first), then
+        // its S of block j (before the last)
+#pragma unroll 1
+        for (int x = 0; x < 2 * (w.n0 + 1); ++x) {
+            const int s = x & 1, j = (x >> 1) - 1, n = w.blocks(s);
+            const uint32_t scol = tmem + s * 128, ocol = tmem + 256 + s * 128;
+            const bool frees = w.dual || s == 1;   // the last slot to read a block
+            if (j >= 0 && j < n) {
+                const int b = w.block(s, j);
+                const uint32_t at = base + (uint32_t)w.v_at(b), st = at % C::kStages;
+                const uint32_t keys = (uint32_t)min(kBN, p.nk - b * kBN);
+                const uint64_t vd = smem_desc_sw128(kv + st * C::kTile, kHalfBytes, 1024);
+                const uint32_t ph = ((s ? items1 : items0) + j) & 1;
                 // the slot's sums of its previous piece have been read
-                if (j == 0 && !wg_wait(&bars[C::kOFree + s], (used[s] & 1) ^ 1, ab, 65)) goto drain;
-                if (!wg_wait(&bars[C::kFull + stage(at)], phase(at), ab, 67)) goto drain;
-                const uint32_t vb = smem_u32(smem + C::kOffKV + stage(at) * C::kTile);
-                const uint64_t vd = smem_desc_sw128(vb, kHalfBytes, 1024);
-                const uint32_t steps = n16(b) / 16;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (!wg_wait(&bars[C::kPFull + 2 * s + h], (items[s] + j) & 1, ab, 66)) goto drain;
-                    tc_fence_after();
-#pragma unroll
-                    for (int k = 4 * h; k < 4 * h + 4; ++k)
-                        if ((uint32_t)k < steps)
-                            mma_ts(tmem + 256 + s * 128, tmem + s * 128 + 64 * h + 8 * (k - 4 * h),
-                                   vd + mnmajor_step(k), idesc_pv, j > 0 || k > 0);
-                }
-                if (w.dual || s == 1) mma_commit(&bars[C::kEmpty + stage(at)]);
-                if (j == n - 1)
-                    mma_commit(&bars[C::kOFull + s]);
-                else if (!issue_s(s, j + 1))
+                if (j == 0 && !wg_wait(&bars[C::kOFree + s], ((s ? used1 : used0) & 1) ^ 1, ab, 65)) goto drain;
+                if (!wg_wait(&bars[C::kFull + st], (at / C::kStages) & 1, ab, 67) ||
+                    !wg_wait(&bars[C::kPFull + 2 * s], ph, ab, 66))
                     goto drain;
+                tc_fence_after();
+                mma_sums(ocol, scol, scol + 16, vd, idesc_pv, min(4u, (keys + 15) >> 4), j > 0);
+                if (!wg_wait(&bars[C::kPFull + 2 * s + 1], ph, ab, 68)) goto drain;
+                if (keys > 64) {
+                    tc_fence_after();
+                    mma_sums(ocol, scol + 64, scol + 80, vd + mnmajor_step(4), idesc_pv, (keys - 49) >> 4, 1);
+                }
+                if (frees) mma_commit(&bars[C::kEmpty + st]);
+                if (j == n - 1) mma_commit(&bars[C::kOFull + s]);
+            }
+            if (j + 1 < n) {
+                const int b = w.block(s, j + 1);
+                const uint32_t at = base + (uint32_t)w.k_at(b), st = at % C::kStages;
+                const uint32_t keys16 = (uint32_t)(min(kBN, p.nk - b * kBN) + 15) & ~15u;
+                if (!wg_wait(&bars[C::kFull + st], (at / C::kStages) & 1, ab, 64)) goto drain;
+                tc_fence_after();
+                mma_scores<D>(scol, smem_desc_sw128(smem_u32(smem + C::kOffQ + (s && !w.dual ? C::kTile : 0)), 16, 1024),
+                              smem_desc_sw128(kv + st * C::kTile, 16, 1024), idesc_bf16(128, keys16, false, false));
+                mma_commit(&bars[C::kSFull + s]);
+                if (frees) mma_commit(&bars[C::kEmpty + st]);
+                // the piece's last S: its queries may be replaced
+                if (b == w.nb - 1 && frees) mma_commit(&bars[C::kQEmpty]);
             }
         }
-        for (int s = 0; s < 2; ++s)
-            if (w.blocks(s) > 0) {
-                items[s] += w.blocks(s);
-                used[s] += 1;
-            }
+        items0 += w.n0;
+        items1 += w.n1;
+        used0 += w.n0 > 0;
+        used1 += w.n1 > 0;
         base += 2 * (uint32_t)w.nb;
     }
 drain:
