@@ -152,68 +152,78 @@ unwind:
         if (armed[s] >= 0) mbar_wait_teardown(&bars[C::kFull + s], (uint32_t)armed[s]);
 }
 
+// The issuer (one lane).
 template <int D>
-__device__ void kv_mma(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t tmem, int seg0, int seg1,
-                       const Abort& ab) {
+__device__ __forceinline__ void kv_mma(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t tmem, int seg0,
+                                       int seg1, const Abort& ab) {
     using C = KvCfg<D>;
-    constexpr uint32_t idesc_acc = idesc_bf16(128, D, false, true);
+    constexpr uint32_t idesc_acc = idesc_bf16(128, D, false, true), idesc_full = idesc_bf16(128, kItem, false, false);
+    constexpr uint64_t kTileDesc = C::kTile >> 4, kItemDesc = (kItem * 128) >> 4;
     const uint64_t kd = smem_desc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
     const uint64_t vd = smem_desc_sw128(smem_u32(smem + C::kOffV), 16, 1024);
-    tmem = (uint32_t)uniform((int)tmem);
-    seg0 = uniform(seg0);
-    seg1 = uniform(seg1);
-    uint32_t nu = 0, tile0 = 0, e0 = 0;   // units, tiles and items before this unit
+    const uint64_t q_k = smem_desc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
+    const uint64_t q_mn = smem_desc_sw128(smem_u32(smem + C::kOffQ), kHalfBytes, 1024);
+    constexpr uint64_t kDO = (C::kOffDO - C::kOffQ) >> 4;
+    const int full = a.tpt * a.r > kItem ? 2 : 1;   // items of every tile but the last
+    // places of the item whose scores come next (A) and whose sums do (B): its
+    // tile's stage, its half of the tile, its slot's parity
+    RingAt<2> tileA, tileB;
+    uint32_t slotA = 0, slotB = 0, p_ph = 0, kv_ph = 0, acc_ph = 1;
     for (int t = seg0; t < seg1; ++t) {
-        PrefixUnit u = load_unit(a.units + t);
-        u.ntok = uniform(u.ntok);
+        const PrefixUnit u = load_unit(a.units + t);
         const int tiles = (u.ntok + a.tpt - 1) / a.tpt;
         if (tiles == 0) continue;
-        const int full = a.tpt * a.r > kItem ? 2 : 1;   // items of every tile but the last
-        const int items = (tiles - 1) * full + (tile_rows(u, a, tiles - 1) + kItem - 1) / kItem;
-        auto rows16 = [&](int x) {
-            const int n = min(kItem, tile_rows(u, a, x / full) - (x % full) * kItem);
-            return (uint32_t)((n + 15) & ~15);
-        };
-        auto issue_s = [&](int x) -> bool {
-            const uint32_t st = (tile0 + x / full) & 1, ph = ((tile0 + x / full) >> 1) & 1;
-            if (!wg_wait(&bars[C::kFull + st], ph, ab, 84)) return false;
+        const int last_rows = tile_rows(u, a, tiles - 1);
+        const int items = (tiles - 1) * full + (last_rows + kItem - 1) / kItem;
+        const uint32_t last16 = (uint32_t)((last_rows - (last_rows > kItem ? kItem : 0) + 15) & ~15);
+        const uint32_t idesc_last = idesc_bf16(128, last16, false, false);
+        // (a full tile's second item may be short too: tpt * r rows)
+        const uint32_t tail16 = full == 2 ? (uint32_t)((a.tpt * a.r - kItem + 15) & ~15) : 64u;
+        const uint32_t idesc_tail = idesc_bf16(128, tail16, false, false);
+        uint32_t halfA = 0, halfB = 0;
+        auto scores = [&](int x) -> bool {
+            if (halfA == 0 && !mbar_wait<true>(&bars[C::kFull + tileA.st], tileA.ph, ab, 84)) return false;
             tc_fence_after();
-            const uint32_t col = tmem + ((e0 + x) & 1) * 128;
-            const uint32_t off = st * C::kTile + (x % full) * (kItem * 128);
-            const uint64_t qd = smem_desc_sw128(smem_u32(smem + C::kOffQ + off), 16, 1024);
-            const uint64_t dd = smem_desc_sw128(smem_u32(smem + C::kOffDO + off), 16, 1024);
-            const uint32_t id = idesc_bf16(128, rows16(x), false, false);
-            mma_scores<D>(col, kd, qd, id);
-            mma_scores<D>(col + 64, vd, dd, id);
-            mma_commit(&bars[C::kSDFull + ((e0 + x) & 1)]);
-            if (x == items - 1) mma_commit(&bars[C::kKVEmpty]);
+            const uint64_t off = tileA.st * kTileDesc + halfA * kItemDesc;
+            const uint32_t id = x == items - 1 ? idesc_last : halfA ? idesc_tail : idesc_full;
+            const uint32_t col = tmem + slotA * 128;
+            one_scores<D>(col, kd, q_k + off, id);
+            one_scores<D>(col + 64, vd, q_k + kDO + off, id);
+            one_commit(&bars[C::kSDFull + slotA]);
+            if (x == items - 1) one_commit(&bars[C::kKVEmpty]);
+            slotA ^= 1;
+            if (++halfA == (uint32_t)full || x == items - 1) {
+                halfA = 0;
+                tileA.next();
+            }
             return true;
         };
-        if (!wg_wait(&bars[C::kKVFull], nu & 1, ab, 83)) goto drain;
-        if (!issue_s(0) || (items > 1 && !issue_s(1))) goto drain;
+        if (!mbar_wait<true>(&bars[C::kKVFull], kv_ph, ab, 83)) return;
+        kv_ph ^= 1;
+        if (!scores(0) || (items > 1 && !scores(1))) return;
         for (int x = 0; x < items; ++x) {
-            const uint32_t e = e0 + x, st = (tile0 + x / full) & 1;
-            if (x == 0 && !wg_wait(&bars[C::kAccFree], (nu & 1) ^ 1, ab, 85)) goto drain;
-            if (!wg_wait(&bars[C::kPFull + (e & 1)], (e >> 1) & 1, ab, 86)) goto drain;
+            if (x == 0) {
+                if (!mbar_wait<true>(&bars[C::kAccFree], acc_ph, ab, 85)) return;
+                acc_ph ^= 1;
+            }
+            if (!mbar_wait<true>(&bars[C::kPFull + slotB], p_ph, ab, 86)) return;
             tc_fence_after();
-            const uint32_t col = tmem + (e & 1) * 128;
-            const uint32_t off = st * C::kTile + (x % full) * (kItem * 128);
-            const uint64_t qd = smem_desc_sw128(smem_u32(smem + C::kOffQ + off), kHalfBytes, 1024);
-            const uint64_t dd = smem_desc_sw128(smem_u32(smem + C::kOffDO + off), kHalfBytes, 1024);
-            const uint32_t steps = rows16(x) / 16;
-            mma_sums(tmem + 256, col, col + 32, dd, idesc_acc, steps, x > 0);
-            mma_sums(tmem + 384, col + 64, col + 96, qd, idesc_acc, steps, x > 0);
-            if (x % full == full - 1 || x == items - 1) mma_commit(&bars[C::kEmpty + st]);
-            if (x == items - 1) mma_commit(&bars[C::kAccFull]);
-            if (x + 2 < items && !issue_s(x + 2)) goto drain;
+            const uint64_t off = q_mn + tileB.st * kTileDesc + halfB * kItemDesc;
+            const uint32_t steps = (x == items - 1 ? last16 : halfB ? tail16 : 64u) >> 4;
+            const uint32_t col = tmem + slotB * 128;
+            one_sums(tmem + 256, col, col + 32, off + kDO, idesc_acc, steps, x > 0);
+            one_sums(tmem + 384, col + 64, col + 96, off, idesc_acc, steps, x > 0);
+            p_ph ^= slotB;
+            slotB ^= 1;
+            if (++halfB == (uint32_t)full || x == items - 1) {
+                one_commit(&bars[C::kEmpty + tileB.st]);
+                halfB = 0;
+                tileB.next();
+            }
+            if (x == items - 1) one_commit(&bars[C::kAccFull]);
+            if (x + 2 < items && !scores(x + 2)) return;
         }
-        ++nu;
-        tile0 += tiles;
-        e0 += items;
     }
-drain:
-    mma_commit(&bars[C::kMmaDone]);
-    mbar_wait_teardown(&bars[C::kMmaDone], 0);
 }
 
 // 32 packed columns of a row from the accumulator at `col` (scaled) as bf16
@@ -387,7 +397,12 @@ prefix_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         if (lane == 0) kv_producer<D>(&tmQ, &tmDO, &tmKp, &tmVp, &tmK, &tmV, a, smem, bars, seg0, seg1, ab);
         __syncwarp();
     } else if (warp == 1) {
-        kv_mma<D>(a, smem, bars, tmem, seg0, seg1, ab);
+        if (elect_one()) {
+            kv_mma<D>(a, smem, bars, tmem, seg0, seg1, ab);
+            // all of its products complete before TMEM is released
+            one_commit(&bars[C::kMmaDone]);
+            mbar_wait_teardown(&bars[C::kMmaDone], 0);
+        }
         __syncwarp();
     } else {
         kv_rows<D, ACT>(a, smem, bars, tmem, seg0, seg1, ab);
@@ -482,69 +497,74 @@ unwind:
         if (armed[s] >= 0) mbar_wait_teardown(&bars[C::kFull + s], (uint32_t)armed[s]);
 }
 
+// The issuer (one lane).
 template <int D>
-__device__ void dq_mma(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t tmem, int seg0, int seg1,
-                       const Abort& ab) {
+__device__ __forceinline__ void dq_mma(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t tmem, int seg0,
+                                       int seg1, const Abort& ab) {
     using C = DqCfg<D>;
-    constexpr uint32_t idesc_acc = idesc_bf16(128, D, false, true);
+    constexpr uint32_t idesc_acc = idesc_bf16(128, D, false, true), idesc_full = idesc_bf16(128, kItem, false, false);
+    constexpr uint64_t kTileDesc = C::kTile >> 4, kItemDesc = (kItem * 128) >> 4;
     const uint64_t qd = smem_desc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
     const uint64_t dd = smem_desc_sw128(smem_u32(smem + C::kOffDO), 16, 1024);
-    tmem = (uint32_t)uniform((int)tmem);
-    seg0 = uniform(seg0);
-    seg1 = uniform(seg1);
-    uint32_t nr = 0, ring = 0, e0 = 0;
+    const uint64_t kv_k = smem_desc_sw128(smem_u32(smem + C::kOffKV), 16, 1024);
+    const uint64_t kv_mn = smem_desc_sw128(smem_u32(smem + C::kOffKV), kHalfBytes, 1024);
+    // ring places of the blocks whose scores come next and whose sums do (K,
+    // with V behind it)
+    RingAt<C::kStages> kA, kB;
+    uint32_t slotA = 0, slotB = 0, p_ph = 0, q_ph = 0, acc_ph = 1;
     for (int t = 2 * seg0; t < 2 * seg1; ++t) {
-        PrefixPiece p = load_piece(a.pieces + (t >> 1));
-        p.nk = uniform(p.nk); p.flags = uniform(p.flags); p.part0 = uniform(p.part0); p.part1 = uniform(p.part1);
+        const PrefixPiece p = load_piece(a.pieces + (t >> 1));
         const Run run(p, t & 1, a.r);
         if (run.blocks == 0) continue;
         const int items = run.items();
-        auto n16 = [&](int x) {
-            return (uint32_t)((min(kItem, run.keys(x >> 1) - (x & 1) * kItem) + 15) & ~15);
-        };
-        auto last_of = [&](int x) { return (x & 1) || x == items - 1; };   // of its block
-        auto stage = [&](int x, int kv) { return (ring + 2 * (uint32_t)(x >> 1) + kv) % C::kStages; };
-        auto phase = [&](int x, int kv) { return ((ring + 2 * (uint32_t)(x >> 1) + kv) / C::kStages) & 1; };
-        auto issue_s = [&](int x) -> bool {
-            const uint32_t sk = stage(x, 0), sv = stage(x, 1);
-            if (!wg_wait(&bars[C::kFull + sk], phase(x, 0), ab, 104)) return false;
-            if (!wg_wait(&bars[C::kFull + sv], phase(x, 1), ab, 105)) return false;
+        const int last_keys = run.keys(run.blocks - 1);
+        const uint32_t last16 = (uint32_t)((last_keys - (last_keys > kItem ? kItem : 0) + 15) & ~15);
+        const uint32_t idesc_last = idesc_bf16(128, last16, false, false);
+        auto scores = [&](int x) -> bool {
+            RingAt<C::kStages> v = kA;
+            v.next();
+            if (!(x & 1) && (!mbar_wait<true>(&bars[C::kFull + kA.st], kA.ph, ab, 104) ||
+                             !mbar_wait<true>(&bars[C::kFull + v.st], v.ph, ab, 105)))
+                return false;
             tc_fence_after();
-            const uint32_t col = tmem + ((e0 + x) & 1) * 128, off = (x & 1) * (kItem * 128);
-            const uint64_t kd = smem_desc_sw128(smem_u32(smem + C::kOffKV + sk * C::kTile + off), 16, 1024);
-            const uint64_t vd = smem_desc_sw128(smem_u32(smem + C::kOffKV + sv * C::kTile + off), 16, 1024);
-            const uint32_t id = idesc_bf16(128, n16(x), false, false);
-            mma_scores<D>(col, qd, kd, id);
-            mma_scores<D>(col + 64, dd, vd, id);
-            mma_commit(&bars[C::kSDFull + ((e0 + x) & 1)]);
-            if (last_of(x)) mma_commit(&bars[C::kEmpty + sv]);
-            if (x == items - 1) mma_commit(&bars[C::kQEmpty]);
+            const uint64_t half = (x & 1) * kItemDesc;
+            const uint32_t col = tmem + slotA * 128, id = x == items - 1 ? idesc_last : idesc_full;
+            one_scores<D>(col, qd, kv_k + kA.st * kTileDesc + half, id);
+            one_scores<D>(col + 64, dd, kv_k + v.st * kTileDesc + half, id);
+            one_commit(&bars[C::kSDFull + slotA]);
+            slotA ^= 1;
+            if ((x & 1) || x == items - 1) {
+                one_commit(&bars[C::kEmpty + v.st]);
+                kA = v;
+                kA.next();
+            }
+            if (x == items - 1) one_commit(&bars[C::kQEmpty]);
             return true;
         };
-        if (!wg_wait(&bars[C::kQFull], nr & 1, ab, 103)) goto drain;
-        if (!issue_s(0) || (items > 1 && !issue_s(1))) goto drain;
+        if (!mbar_wait<true>(&bars[C::kQFull], q_ph, ab, 103)) return;
+        q_ph ^= 1;
+        if (!scores(0) || (items > 1 && !scores(1))) return;
         for (int x = 0; x < items; ++x) {
-            const uint32_t e = e0 + x;
-            if (x == 0 && !wg_wait(&bars[C::kAccFree], (nr & 1) ^ 1, ab, 106)) goto drain;
-            if (!wg_wait(&bars[C::kPFull + (e & 1)], (e >> 1) & 1, ab, 107)) goto drain;
+            if (x == 0) {
+                if (!mbar_wait<true>(&bars[C::kAccFree], acc_ph, ab, 106)) return;
+                acc_ph ^= 1;
+            }
+            if (!mbar_wait<true>(&bars[C::kPFull + slotB], p_ph, ab, 107)) return;
             tc_fence_after();
-            const uint32_t sk = stage(x, 0);
-            const uint64_t kd = smem_desc_sw128(
-                smem_u32(smem + C::kOffKV + sk * C::kTile + (x & 1) * (kItem * 128)), kHalfBytes, 1024);
-            const uint32_t steps = n16(x) / 16;
-            const uint32_t col = tmem + (e & 1) * 128;
-            mma_sums(tmem + 256, col, col + 32, kd, idesc_acc, steps, x > 0);
-            if (last_of(x)) mma_commit(&bars[C::kEmpty + sk]);
-            if (x == items - 1) mma_commit(&bars[C::kAccFull]);
-            if (x + 2 < items && !issue_s(x + 2)) goto drain;
+            const uint32_t col = tmem + slotB * 128;
+            one_sums(tmem + 256, col, col + 32, kv_mn + kB.st * kTileDesc + (x & 1) * kItemDesc, idesc_acc,
+                     (x == items - 1 ? last16 : 64u) >> 4, x > 0);
+            p_ph ^= slotB;
+            slotB ^= 1;
+            if ((x & 1) || x == items - 1) {
+                one_commit(&bars[C::kEmpty + kB.st]);
+                kB.next();
+                kB.next();
+            }
+            if (x == items - 1) one_commit(&bars[C::kAccFull]);
+            if (x + 2 < items && !scores(x + 2)) return;
         }
-        ++nr;
-        ring += 2 * (uint32_t)run.blocks;
-        e0 += items;
     }
-drain:
-    mma_commit(&bars[C::kMmaDone]);
-    mbar_wait_teardown(&bars[C::kMmaDone], 0);
 }
 
 template <int D, int ACT>
@@ -678,7 +698,12 @@ prefix_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if (lane == 0) dq_producer<D>(&tmQ, &tmDO, &tmKp, &tmVp, &tmK, &tmV, a, smem, bars, seg0, seg1, ab);
         __syncwarp();
     } else if (warp == 1) {
-        dq_mma<D>(a, smem, bars, tmem, seg0, seg1, ab);
+        if (elect_one()) {
+            dq_mma<D>(a, smem, bars, tmem, seg0, seg1, ab);
+            // all of its products complete before TMEM is released
+            one_commit(&bars[C::kMmaDone]);
+            mbar_wait_teardown(&bars[C::kMmaDone], 0);
+        }
         __syncwarp();
     } else {
         dq_rows<D, ACT>(a, smem, bars, tmem, seg0, seg1, ab);
