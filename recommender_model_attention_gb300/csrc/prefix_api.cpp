@@ -58,6 +58,7 @@ bool capturing(cudaStream_t st) {
 // happened.
 gdpa_status begin_work(PrefixPlan& p, cudaStream_t st, bool captured) {
     if (captured) {
+        p.chain = 0;
         cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
         if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return GDPA_ERR_CUDA;
         const bool ok = cudaEventSynchronize(p.ready) == cudaSuccess &&
@@ -65,7 +66,16 @@ gdpa_status begin_work(PrefixPlan& p, cudaStream_t st, bool captured) {
         cudaThreadExchangeStreamCaptureMode(&mode);
         return ok ? GDPA_OK : GDPA_ERR_CUDA;
     }
-    if (cudaStreamWaitEvent(st, p.ready, 0) != cudaSuccess) return GDPA_ERR_CUDA;
+    p.chain = 0;
+    if (!p.is_ready) {
+        if (cudaStreamWaitEvent(st, p.ready, 0) != cudaSuccess) return GDPA_ERR_CUDA;
+        // (a query could spoil a capture that another thread has under way)
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return GDPA_ERR_CUDA;
+        p.is_ready = cudaEventQuery(p.ready) == cudaSuccess;
+        cudaThreadExchangeStreamCaptureMode(&mode);
+        if (!p.is_ready) cudaGetLastError();   // not ready is not an error
+    }
     if (p.has_work && p.last_stream != st && cudaStreamWaitEvent(st, p.last, 0) != cudaSuccess)
         return GDPA_ERR_CUDA;
     return GDPA_OK;

@@ -18,7 +18,9 @@
 // walks their pieces like any other.
 #pragma once
 
+#include <atomic>
 #include <mutex>
+#include <utility>
 #include <vector>
 
 #include "gdpa_internal.h"
@@ -91,10 +93,11 @@ struct PrefixPlan {
     size_t grad_bytes = 0;
     int32_t last_err[4] = {0, 0, 0, 0};
     int64_t launches = 0;
+    int chain = 0;                   // kernels of the current call that a next one may start beside
     cudaEvent_t ready = nullptr;     // the upload, on the creation stream
     cudaEvent_t last = nullptr;      // the plan's latest work
     cudaStream_t last_stream = nullptr;
-    bool has_work = false;
+    bool has_work = false, is_ready = false;   // is_ready: the upload is known to be over
     std::mutex lock;                 // host state above
 
     const PrefixPiece* dev_pieces() const { return (const PrefixPiece*)d_tables; }
@@ -118,6 +121,42 @@ struct PrefixIO {
     float alpha = 1.0f;
     int act = 0;
 };
+
+// Raise a kernel's dynamic shared-memory limit, once per device (`done`: one
+// bit each, a static of the caller's).
+template <typename K>
+bool allow_smem(K kern, int bytes, int device, std::atomic<uint64_t>& done) {
+    const uint64_t bit = device < 64 ? 1ull << device : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
+
+// Launch a kernel; `early`: it may start once every block of the kernel before
+// it on the stream has called grid_let_next (or ended), and must itself call
+// grid_wait_previous before it ends, or before it reads what that kernel
+// wrote: its own end then also says that the kernel before it has ended.
+template <typename... P, typename... A>
+bool launch_kernel(void (*kern)(P...), dim3 grid, int threads, int smem, cudaStream_t st, bool early,
+                   A&&... args) {
+    cudaLaunchConfig_t c = {};
+    c.gridDim = grid;
+    c.blockDim = dim3((unsigned)threads);
+    c.dynamicSmemBytes = (size_t)smem;
+    c.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = at;
+    c.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&c, kern, std::forward<A>(args)...) == cudaSuccess;
+}
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void grid_let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+#endif
 
 // Host planner (prefix_plan.cpp): INVALID_ARG for bad offsets.
 gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t* kv_off,

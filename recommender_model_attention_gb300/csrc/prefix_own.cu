@@ -85,6 +85,21 @@ __device__ __forceinline__ void store_part(const float (&acc)[D / 16][4], float 
     }
 }
 
+// Bring keys [j0, j1) of K and V (rows of D columns, ks apart) into L2, a 128-
+// byte line a lane: the steps' loads then wait for L2 rather than, each in
+// turn, for memory.
+template <int D>
+__device__ __forceinline__ void prefetch_keys(const __nv_bfloat16* K, const __nv_bfloat16* V, int64_t ks, int j0,
+                                              int j1, int lane) {
+    constexpr int kLines = D / 64;
+    for (int i = lane; i < (j1 - j0) * 2 * kLines; i += 32) {
+        const int j = j0 + i / (2 * kLines), x = i % (2 * kLines);
+        const __nv_bfloat16* p = (x < kLines ? K : V) + j * ks + (x % kLines) * 64;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+    }
+}
+constexpr int kAhead = 64;   // keys
+
 struct Rows {   // the unit's rows, as this lane meets them
     int nrows, row0, tok, hk, r, H;
     __device__ __forceinline__ int64_t at(int i) const {   // row of [Tq][H]
@@ -97,6 +112,7 @@ template <int D, int ACT>
 __global__ void __launch_bounds__(kThreads, 4) own_fwd_kernel(const OwnArgs a) {
     constexpr bool kSm = ACT == kSoftmax;
     constexpr int kC = D / 32;
+    grid_let_next();
     const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (unit >= a.n) return;
     const PrefixUnit u = a.units[unit];
@@ -104,6 +120,12 @@ __global__ void __launch_bounds__(kThreads, 4) own_fwd_kernel(const OwnArgs a) {
     const Rows rows{min(8, u.ntok * a.r - u.j0), u.j0, u.tok, u.hk, a.r, a.H};
     const int64_t ks = (int64_t)a.Hkv * D, k_at = (int64_t)u.k0 * ks + u.hk * D;
     const __nv_bfloat16 *K = a.k + k_at, *V = a.v + k_at;
+    int ja = 0, jb = u.nk;
+    if (a.windowed) {   // keys some row sees
+        ja = max(0, rows.row0 / a.r - a.window + 1);
+        jb = min(jb, (rows.row0 + rows.nrows - 1) / a.r + 1);
+    }
+    prefetch_keys<D>(K, V, ks, ja, min(jb, ja + kAhead), lane);
     const PrefixOwn ow = a.own[u.tok];
     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
     uint4 qb[kC];
@@ -119,12 +141,8 @@ __global__ void __launch_bounds__(kThreads, 4) own_fwd_kernel(const OwnArgs a) {
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};   // rows 2 q, 2 q + 1
     const int pos[2] = {(rows.row0 + min(2 * q, rows.nrows - 1)) / a.r,
                         (rows.row0 + min(2 * q + 1, rows.nrows - 1)) / a.r};
-    int ja = 0, jb = u.nk;
-    if (a.windowed) {   // keys some row sees
-        ja = max(0, rows.row0 / a.r - a.window + 1);
-        jb = min(jb, (rows.row0 + rows.nrows - 1) / a.r + 1);
-    }
     for (int j0 = ja; j0 < jb; j0 += 16) {
+        if (j0 + kAhead < jb) prefetch_keys<D>(K, V, ks, j0 + kAhead, min(jb, j0 + kAhead + 16), lane);
         uint4 ka[kC], kb[kC], vv[4][D / 64];
         {
             const int64_t x = min(j0 + g, jb - 1) * ks, y = min(j0 + g + 8, jb - 1) * ks;
@@ -208,6 +226,7 @@ template <int D, int ACT>
 __global__ void __launch_bounds__(kThreads, 2) own_bwd8_kernel(const OwnArgs a) {
     constexpr bool kSm = ACT == kSoftmax;
     constexpr int kC = D / 32, kW = D / 64;
+    grid_let_next();
     const int unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (unit >= a.n) return;
     const PrefixUnit u = a.units[unit];
@@ -215,6 +234,7 @@ __global__ void __launch_bounds__(kThreads, 2) own_bwd8_kernel(const OwnArgs a) 
     const Rows rows{min(8, u.ntok * a.r), 0, u.tok, u.hk, a.r, a.H};
     const int64_t ks = (int64_t)a.Hkv * D, k_at = (int64_t)u.k0 * ks + u.hk * D;
     const __nv_bfloat16 *K = a.k + k_at, *V = a.v + k_at;
+    prefetch_keys<D>(K, V, ks, 0, min(u.nk, kAhead), lane);
     const PrefixOwn ow = a.own[u.tok];
     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
     const ActScale sc = act_scale<ACT>(a.alpha);
@@ -252,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 2) own_bwd8_kernel(const OwnArgs a) 
 #pragma unroll
     for (int e = 0; e < products<D>(); ++e) acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.0f;
     for (int j0 = 0; j0 < u.nk; j0 += 16) {
+        if (j0 + kAhead < u.nk) prefetch_keys<D>(K, V, ks, j0 + kAhead, min(u.nk, j0 + kAhead + 16), lane);
         float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, dp[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         uint4 kv[4][kW];
         {
@@ -386,6 +407,7 @@ gdpa_status dispatch(bool bwd, PrefixPlan& p, const OwnArgs& a, int act, cudaStr
             GDPA_DISPATCH_ACT(act, A, go<64, A>(bwd, a, st))
     }
     p.launches += 1;
+    p.chain += 1;
     return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
 }
 

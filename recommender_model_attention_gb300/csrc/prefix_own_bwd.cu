@@ -49,6 +49,7 @@ template <int D, int ACT>
 __global__ void __launch_bounds__(kThreads) own_bwd_kernel(const OwnBwArgs a) {
     constexpr bool kSm = ACT == kSoftmax;
     constexpr int kC = D / 32, kW = D / 64;
+    grid_let_next();
     const PrefixUnit u = a.units[blockIdx.x];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, q = lane & 3;
@@ -286,6 +287,7 @@ gdpa_status launch_prefix_own_bwd(PrefixPlan& p, const PrefixIO& io, const float
             GDPA_DISPATCH_ACT(io.act, A, own_bwd_kernel<64, A><<<grid, kThreads, 0, st>>>(a))
     }
     p.launches += 1;
+    p.chain += 1;
     return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
 }
 

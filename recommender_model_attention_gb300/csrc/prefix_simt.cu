@@ -316,9 +316,10 @@ __global__ void __launch_bounds__(kThreads) simt_keys_kernel(const SimtArgs a) {
     }
 }
 
-// Join the parts of 8 rows of a tile: a thread per (row, 4 columns), a warp's
-// four threads of a row sharing the look at its maxima, eight layers of loads
-// in flight at a time.
+// Join the parts of 8 rows of a tile: a thread per (row, 4 columns).  The
+// first eight layers, usually all, are loaded together before anything is
+// known of them; further ones eight at a time, a warp's four threads of a row
+// sharing a look at their maxima.
 template <typename E>
 __global__ void __launch_bounds__(256) merge_kernel(const PrefixTile* tiles, const PrefixOwn* owns,
                                                     const float* parts, const float* ml, E* out,
@@ -334,6 +335,8 @@ __global__ void __launch_bounds__(256) merge_kernel(const PrefixTile* tiles, con
     const int orow = ow.row0 + j, total = real ? t.layers + ow.layers : 0;
     const int64_t own0 = (int64_t)ow.part + (int64_t)t.hk * ow.layers * ow.rows;
     const float2* st = reinterpret_cast<const float2*>(ml);
+    const float4* src = reinterpret_cast<const float4*>(parts);
+    const int c4 = d / 4, c = (lane >> 3) + 4 * warp;
     // layer x: its first row in the workspace, its rows, this row's place
     auto place = [&](int x, int& n, int& at) {
         const bool pre = x < t.layers;
@@ -341,43 +344,48 @@ __global__ void __launch_bounds__(256) merge_kernel(const PrefixTile* tiles, con
         at = pre ? row : orow;
         return pre ? (int64_t)t.part + (int64_t)x * nrows : own0 + (int64_t)(x - t.layers) * ow.rows;
     };
-    const int c4 = d / 4, c = (lane >> 3) + 4 * warp;
-    float top = -INFINITY, ref = 0.f, sum = 0.f;
-    if (softmax) {
-#pragma unroll 4
-        for (int x = lane >> 3; x < total; x += 4) {
-            int n, at;
-            const int64_t p = place(x, n, at);
-            top = fmaxf(top, st[p + at].x);
-        }
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
-        ref = top == -INFINITY ? 0.f : top;
-    }
-    if (!real || c >= c4) return;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4* src = reinterpret_cast<const float4*>(parts);
-    for (int x0 = 0; x0 < total; x0 += 8) {
-        float2 s[8];
-        float4 v[8];
+    float2 s[8];
+    float4 v[8];
+    auto load8 = [&](int x0) {
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             s[u] = make_float2(-INFINITY, 0.f);
             v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (x0 + u < total) {
+            if (x0 + u < total && c < c4) {
                 int n, at;
                 const int64_t p = place(x0 + u, n, at);
                 if (softmax) s[u] = st[p + at];
                 v[u] = src[p * c4 + (int64_t)c * n + at];
             }
         }
+    };
+    grid_wait_previous();
+    load8(0);
+    float top = -INFINITY, ref = 0.f, sum = 0.f;
+    if (softmax) {
+#pragma unroll 4
+        for (int x = 8 + (lane >> 3); x < total; x += 4) {
+            int n, at;
+            const int64_t p = place(x, n, at);
+            top = fmaxf(top, st[p + at].x);
+        }
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
+#pragma unroll
+        for (int u = 0; u < 8; ++u) top = fmaxf(top, s[u].x);
+        ref = top == -INFINITY ? 0.f : top;
+    }
+    if (!real || c >= c4) return;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x0 = 0; x0 < total; x0 += 8) {
+        if (x0 > 0) load8(x0);
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             float w = 1.f;
             if (softmax) {
-                w = exp2f(s[u].x - ref);   // 0 for a part without a visible key
+                if (s[u].x == -INFINITY) continue;   // no such layer, or nothing visible in it
+                w = exp2f(s[u].x - ref);
                 sum = fmaf(w, s[u].y, sum);
-                if (s[u].x == -INFINITY) continue;
             }
             axpy4(acc, w, v[u]);
         }
@@ -420,11 +428,13 @@ SimtArgs args_of(const PrefixPlan& p, const PrefixIO& io, const float* delta) {
     return a;
 }
 
-template <typename K>
-gdpa_status go(K kern, dim3 grid, int smem, PrefixPlan& p, const SimtArgs& a, cudaStream_t st) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return GDPA_ERR_CUDA;
-    kern<<<grid, kThreads, smem, st>>>(a);
+template <auto kKern>
+gdpa_status go(dim3 grid, int smem, PrefixPlan& p, const SimtArgs& a, cudaStream_t st) {
+    // the most any head dim takes (the dK, dV kernel's, d = 128)
+    constexpr int kMost = (2 * kRows * 128 + 2 * kRows * 132 + 8 * kRows * kPer) * 4;
+    static std::atomic<uint64_t> done{0};
+    if (!allow_smem(kKern, kMost, p.device, done)) return GDPA_ERR_CUDA;
+    kKern<<<grid, kThreads, smem, st>>>(a);
     p.launches += 1;
     return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
 }
@@ -440,7 +450,7 @@ gdpa_status fwd_t(PrefixPlan& p, const PrefixIO& io, cudaStream_t st) {
         const SimtArgs a = args_of(p, io, nullptr);
         const int smem = (kRows * p.d + 2 * kRows * (p.d + 4) + 4 * kRows * kPer) * 4;
         const dim3 grid((unsigned)p.pieces.size(), 8);
-        PREFIX_DISPATCH(io.act, s = go(simt_rows_kernel<E, A, false>, grid, smem, p, a, st))
+        PREFIX_DISPATCH(io.act, s = (go<simt_rows_kernel<E, A, false>>(grid, smem, p, a, st)))
     }
     return s;
 }
@@ -452,12 +462,12 @@ gdpa_status bwd_t(PrefixPlan& p, const PrefixIO& io, const float* delta, cudaStr
     if (!p.pieces.empty()) {
         const int smem = (2 * kRows * p.d + 2 * kRows * (p.d + 4) + 4 * kRows * kPer) * 4;
         const dim3 grid((unsigned)p.pieces.size(), 8);
-        PREFIX_DISPATCH(io.act, s = go(simt_rows_kernel<E, A, true>, grid, smem, p, a, st))
+        PREFIX_DISPATCH(io.act, s = (go<simt_rows_kernel<E, A, true>>(grid, smem, p, a, st)))
     }
     if (s == GDPA_OK && !p.units.empty()) {
         const int smem = (2 * kRows * p.d + 2 * kRows * (p.d + 4) + 8 * kRows * kPer) * 4;
         const dim3 grid((unsigned)p.units.size(), 4);
-        PREFIX_DISPATCH(io.act, s = go(simt_keys_kernel<E, A>, grid, smem, p, a, st))
+        PREFIX_DISPATCH(io.act, s = (go<simt_keys_kernel<E, A>>(grid, smem, p, a, st)))
     }
     return s;
 }
@@ -477,14 +487,16 @@ gdpa_status launch_prefix_merge(PrefixPlan& p, gdpa_dtype dt, void* out, float* 
                                 cudaStream_t st) {
     if (p.tiles.empty()) return GDPA_OK;
     const dim3 grid((unsigned)p.tiles.size(), kBM / 8);
-    if (dt == GDPA_BF16)
-        merge_kernel<<<grid, 256, 0, st>>>(p.dev_tiles(), p.dev_own(), p.d_parts, p.d_ml,
-                                           (__nv_bfloat16*)out, lse, p.H, p.r, p.d, softmax);
-    else
-        merge_kernel<<<grid, 256, 0, st>>>(p.dev_tiles(), p.dev_own(), p.d_parts, p.d_ml, (float*)out,
-                                           lse, p.H, p.r, p.d, softmax);
+    const float *parts = p.d_parts, *ml = p.d_ml;
+    const bool early = p.chain > 0;
+    const int sm = softmax;
+    const bool ok = dt == GDPA_BF16
+                        ? launch_kernel(merge_kernel<__nv_bfloat16>, grid, 256, 0, st, early, p.dev_tiles(),
+                                        p.dev_own(), parts, ml, (__nv_bfloat16*)out, lse, p.H, p.r, p.d, sm)
+                        : launch_kernel(merge_kernel<float>, grid, 256, 0, st, early, p.dev_tiles(), p.dev_own(),
+                                        parts, ml, (float*)out, lse, p.H, p.r, p.d, sm);
     p.launches += 1;
-    return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+    return ok ? GDPA_OK : GDPA_ERR_CUDA;
 }
 
 gdpa_status launch_prefix_delta(PrefixPlan& p, gdpa_dtype dt, const PrefixIO& io, float* delta,

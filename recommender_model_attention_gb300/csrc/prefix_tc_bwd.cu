@@ -379,8 +379,12 @@ prefix_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_let_next();
     const int seg0 = a.seg[blockIdx.x], seg1 = a.seg[blockIdx.x + 1];
-    if (seg0 == seg1) return;
+    if (seg0 == seg1) {
+        grid_wait_previous();
+        return;
+    }
     if (threadIdx.x == 0) {
         for (int b = 0; b < C::kNumBars; ++b)
             mbar_init(&bars[b], b == C::kPFull || b == C::kPFull + 1 ? 256u : b == C::kAccFree ? 512u : 1u);
@@ -413,6 +417,7 @@ prefix_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
+    grid_wait_previous();   // (a kernel that nothing here reads from)
 }
 
 // ------------------------------------------------------------------------ dQ
@@ -680,8 +685,12 @@ prefix_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_let_next();
     const int seg0 = a.seg[blockIdx.x], seg1 = a.seg[blockIdx.x + 1];
-    if (seg0 == seg1) return;
+    if (seg0 == seg1) {
+        grid_wait_previous();
+        return;
+    }
     if (threadIdx.x == 0) {
         for (int b = 0; b < C::kNumBars; ++b)
             mbar_init(&bars[b], b == C::kPFull || b == C::kPFull + 1 ? 256u : b == C::kAccFree ? 512u : 1u);
@@ -714,15 +723,18 @@ prefix_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
+    grid_wait_previous();   // (a kernel that nothing here reads from)
 }
 
 template <typename K>
-gdpa_status go(K kern, int smem, PrefixPlan& p, const CUtensorMap* m, const BwArgs& a, cudaStream_t st) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return GDPA_ERR_CUDA;
-    kern<<<p.S, kThreads, smem, st>>>(m[0], m[1], m[2], m[3], m[4], m[5], a);
+gdpa_status go(K kern, int smem, std::atomic<uint64_t>& done, PrefixPlan& p, const CUtensorMap* m, const BwArgs& a,
+               cudaStream_t st) {
+    if (!allow_smem(kern, smem, p.device, done)) return GDPA_ERR_CUDA;
+    const bool ok = launch_kernel(kern, dim3((unsigned)p.S), kThreads, smem, st, p.chain > 0, m[0], m[1], m[2], m[3],
+                                  m[4], m[5], a);
     p.launches += 1;
-    return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+    p.chain += 1;
+    return ok ? GDPA_OK : GDPA_ERR_CUDA;
 }
 
 template <int D, int ACT>
@@ -730,11 +742,13 @@ gdpa_status launch(PrefixPlan& p, const CUtensorMap* m, BwArgs& a, cudaStream_t 
     gdpa_status s = GDPA_OK;
     if (p.useg[p.S] > 0) {
         a.seg = p.dev_useg();
-        s = go(prefix_dkv_kernel<D, ACT>, KvCfg<D>::kSmem, p, m, a, st);
+        static std::atomic<uint64_t> done{0};
+        s = go(prefix_dkv_kernel<D, ACT>, KvCfg<D>::kSmem, done, p, m, a, st);
     }
     if (s == GDPA_OK && p.seg[p.S] > 0) {
         a.seg = p.dev_seg();
-        s = go(prefix_dq_kernel<D, ACT>, DqCfg<D>::kSmem, p, m, a, st);
+        static std::atomic<uint64_t> done{0};
+        s = go(prefix_dq_kernel<D, ACT>, DqCfg<D>::kSmem, done, p, m, a, st);
     }
     return s;
 }

@@ -447,8 +447,12 @@ prefix_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::kNumBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    grid_let_next();
     const int seg0 = prm.seg[blockIdx.x], seg1 = prm.seg[blockIdx.x + 1];
-    if (seg0 == seg1) return;   // the whole CTA
+    if (seg0 == seg1) {   // the whole CTA
+        grid_wait_previous();
+        return;
+    }
     if (threadIdx.x == 0) {
         for (int b = 0; b < C::kNumBars; ++b) {
             const bool rows = (b >= C::kPFull && b < C::kPFull + 4) || (b >= C::kOFree && b < C::kOFree + 2);
@@ -491,17 +495,19 @@ prefix_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     }
+    grid_wait_previous();   // (the own keys' kernel, which nothing here reads)
 }
 
 template <int D, int ACT>
 gdpa_status launch(PrefixPlan& p, const CUtensorMap* m, const PfParams& prm, cudaStream_t st) {
     auto kern = prefix_fwd_kernel<D, ACT>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PfCfg<D>::kSmem) !=
-        cudaSuccess)
-        return GDPA_ERR_CUDA;
-    kern<<<p.S, kThreads, PfCfg<D>::kSmem, st>>>(m[0], m[1], m[2], m[3], m[4], prm);
+    static std::atomic<uint64_t> done{0};
+    if (!allow_smem(kern, PfCfg<D>::kSmem, p.device, done)) return GDPA_ERR_CUDA;
+    const bool ok = launch_kernel(kern, dim3((unsigned)p.S), kThreads, PfCfg<D>::kSmem, st, p.chain > 0, m[0], m[1],
+                                  m[2], m[3], m[4], prm);
     p.launches += 1;
-    return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+    p.chain += 1;
+    return ok ? GDPA_OK : GDPA_ERR_CUDA;
 }
 
 }  // namespace

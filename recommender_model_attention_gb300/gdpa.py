@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import NamedTuple
 
 import numpy as np
@@ -39,12 +40,6 @@ class _RopeSpec(ctypes.Structure):
                 ("reserved", ctypes.c_int32), ("turns", ctypes.c_uint64 * 64)]
 
 
-class _RopeTensor(ctypes.Structure):
-    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int32),
-                ("x_token", ctypes.c_int64), ("x_head", ctypes.c_int64),
-                ("y_token", ctypes.c_int64), ("y_head", ctypes.c_int64)]
-
-
 class GdpaError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__("%s: %s (status %d)" % (what, STATUS.get(status, "?"), status))
@@ -59,7 +54,7 @@ def lib():
             raise RuntimeError("GDPA CUDA library missing (%s); build it with "
                                "recommender_model_attention_gb300.build()" % LIB_PATH)
         try:
-            import torch  # noqa: F401  (loads the CUDA runtime the library links)
+            _torch_names()   # (importing torch loads the CUDA runtime the library links)
         except ImportError:
             pass
         L = ctypes.CDLL(LIB_PATH)
@@ -98,7 +93,7 @@ def lib():
             "gdpa_rope_init_freqs": [ctypes.POINTER(_RopeSpec), st, st,
                                      ctypes.POINTER(ctypes.c_double), ctypes.c_float],
             "gdpa_rope_apply": [ctypes.POINTER(_RopeSpec), st, st, ctypes.c_int64, st,
-                                ctypes.POINTER(_RopeTensor), st, vp, st, vp, vp, st, vp],
+                                vp, st, vp, st, vp, vp, st, vp],
             "gdpa_prefix_create": [i32p, i32p, st, i32p, i32p, st, st, st, st, st, st, st, vp,
                                    ctypes.POINTER(vp)],
             "gdpa_prefix_create_host": [i32p, i32p, st, i32p, i32p, st, st, st, st, st, st, st,
@@ -126,6 +121,24 @@ def lib():
         L.gdpa_status_str.restype = ctypes.c_char_p
         _lib = L
     return _lib
+
+
+# What the calls need of torch, looked up once by lib(): these entry points are
+# also used for a handful of rows, where marshalling is most of the time.
+_DTYPE_ID = _POSITION_BITS = _empty = _raw_stream = _current_device = _on_device = None
+
+
+def _torch_names():
+    global _DTYPE_ID, _POSITION_BITS, _empty, _raw_stream, _current_device, _on_device
+    import torch
+    _DTYPE_ID = {torch.bfloat16: 0, torch.float32: 1}
+    _POSITION_BITS = {torch.int32: 32, torch.int64: 64}
+    _empty = torch.empty
+    _current_device, _on_device = torch.cuda.current_device, torch.cuda.device
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if _raw_stream is None:
+        def _raw_stream(index):
+            return torch.cuda.current_stream(index).cuda_stream
 
 
 def _ok(status: int, what: str):
@@ -581,6 +594,7 @@ class Rope:
                  hi: float = 32.0, scale: float = 1.0, freqs=None):
         self.rot_dim, self.layout = int(rot_dim), layout
         self.spec = _RopeSpec()
+        self._ref = ctypes.byref(self.spec)
         if freqs is not None:
             f = np.ascontiguousarray(np.asarray(freqs, dtype=np.float64))
             if f.shape != (self.rot_dim // 2,):
@@ -595,76 +609,79 @@ class Rope:
                 "gdpa_rope_init")
 
 
-def _rope_rows(x, y, T, d, like, name):
-    """One tensor of a rope call: checks, and where its rows are and go."""
-    if not x.is_cuda or x.dim() != 3 or x.shape[0] != T or x.shape[2] != d:
-        raise ValueError("%s must be a [%d, heads, %d] CUDA tensor, got %s on %s"
-                         % (name, T, d, tuple(x.shape), x.device))
-    if x.dtype != like.dtype or x.device != like.device:
-        raise TypeError("%s must have q's dtype and device" % name)
+# gdpa_rope_tensor: x, y, heads, then the four strides
+_rope_tensor = struct.Struct("=QQi4xqqqq").pack
+
+
+def _rope_rows(x, y, T, d, dtype, dev, name):
+    """One tensor of a rope call: checks; its output, and its packed record."""
+    shape, xs = x.shape, x.stride()
+    if len(shape) != 3 or shape[0] != T or shape[2] != d or x.device != dev:
+        raise ValueError("%s must be a [%d, heads, %d] tensor on %s, got %s on %s"
+                         % (name, T, d, dev, tuple(shape), x.device))
+    if x.dtype != dtype:
+        raise TypeError("%s must be %s" % (name, dtype))
+    heads = shape[1]
     if y is None:
-        y = x.new_empty(x.shape)
-    elif y.shape != x.shape or y.dtype != x.dtype or y.device != x.device:
-        raise ValueError("%s output must have its input's shape, dtype and device" % name)
-    xs, ys = x.stride(), y.stride()
+        y = _empty(shape, dtype=dtype, device=dev)
+        ys = (heads * d, d, 1)
+    else:
+        if y.shape != shape or y.dtype != dtype or y.device != dev:
+            raise ValueError("%s output must have its input's shape, dtype and device" % name)
+        ys = y.stride()
+        if (T > 1 and ys[0] == 0) or (heads > 1 and ys[1] == 0):
+            raise ValueError("%s output must not be an expanded tensor" % name)
     if d > 1 and (xs[2] != 1 or ys[2] != 1):
         raise ValueError("%s: the columns of a row must be contiguous" % name)
-    if (T > 1 and ys[0] == 0) or (x.shape[1] > 1 and ys[1] == 0):
-        raise ValueError("%s output must not be an expanded tensor" % name)
-    return y, _RopeTensor(x.data_ptr(), y.data_ptr(), x.shape[1], xs[0], xs[1], ys[0], ys[1])
+    return y, _rope_tensor(x.data_ptr(), y.data_ptr(), heads, xs[0], xs[1], ys[0], ys[1])
 
 
 def _rope(rope, inverse, q, k, positions, offsets, starts, q_out, k_out, stream):
-    import torch
-    if q.dim() != 3:
-        raise ValueError("q must be a [T, heads, d] tensor")
-    T, _, d = q.shape
-    dev = q.device
+    shape = q.shape
+    if len(shape) != 3 or not q.is_cuda:
+        raise ValueError("q must be a [T, heads, d] CUDA tensor")
+    T, d, dev, dtype = shape[0], shape[2], q.device, q.dtype
+    kind = _DTYPE_ID.get(dtype)
+    if kind is None:
+        raise TypeError("GDPA takes bfloat16 or float32 tensors, got %s" % dtype)
     if (positions is None) == (offsets is None):
         raise ValueError("give either positions or offsets")
     if starts is not None and offsets is None:
         raise ValueError("starts belong to offsets")
-    rows = (_RopeTensor * 2)()
-    q_out, rows[0] = _rope_rows(q, q_out, T, d, q, "q")
+    q_out, rows = _rope_rows(q, q_out, T, d, dtype, dev, "q")
     n = 1
     if k is not None:
-        k_out, rows[1] = _rope_rows(k, k_out, T, d, q, "k")
+        k_out, more = _rope_rows(k, k_out, T, d, dtype, dev, "k")
+        rows += more
         n = 2
     elif k_out is not None:
         raise ValueError("k_out without k")
-    bits, B, pos, off, start = 0, 0, 0, 0, 0
+    bits, B, pos, off, start = 0, 0, None, None, None
     if positions is not None:
-        if (positions.dtype not in (torch.int32, torch.int64) or tuple(positions.shape) != (T,)
-                or not positions.is_contiguous() or positions.device != dev):
+        bits = _POSITION_BITS.get(positions.dtype)
+        if bits is None or positions.shape != (T,) or not positions.is_contiguous() or positions.device != dev:
             raise ValueError("positions must be a contiguous int32 or int64 [T] tensor on q's device")
-        bits = 32 if positions.dtype == torch.int32 else 64
         pos = positions.data_ptr()
     else:
         for t, what in ((offsets, "offsets"), (starts, "starts")):
-            if t is not None and (t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous()
-                                  or t.device != dev):
+            if t is not None and (_POSITION_BITS.get(t.dtype) != 32 or t.dim() != 1
+                                  or not t.is_contiguous() or t.device != dev):
                 raise ValueError("%s must be a contiguous int32 tensor on q's device" % what)
         B = offsets.shape[0] - 1
         if B < 0 or (starts is not None and starts.shape[0] != B):
             raise ValueError("offsets must have B + 1 entries and starts B")
         off = offsets.data_ptr()
-        start = starts.data_ptr() if starts is not None and B else 0
+        start = starts.data_ptr() if starts is not None and B else None
     if T:
-        with _current(dev):
-            s = torch.cuda.current_stream(dev) if stream is None else stream
-            _ok(lib().gdpa_rope_apply(ctypes.byref(rope.spec), inverse, _dtype_id(q), T, d, rows, n,
-                                      pos, bits, off, start, B, s.cuda_stream), "gdpa_rope_apply")
+        index = dev.index
+        args = (rope._ref, inverse, kind, T, d, rows, n, pos, bits, off, start, B,
+                _raw_stream(index) if stream is None else stream.cuda_stream)
+        if index == _current_device():
+            _ok(lib().gdpa_rope_apply(*args), "gdpa_rope_apply")
+        else:
+            with _on_device(index):
+                _ok(lib().gdpa_rope_apply(*args), "gdpa_rope_apply")
     return q_out if k is None else (q_out, k_out)
-
-
-def _current(device):
-    """A context with ``device`` current; costs nothing when it is already."""
-    import contextlib
-
-    import torch
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
 
 
 def gdpa_rope_fwd(rope: Rope, q, k=None, positions=None, offsets=None, starts=None, q_out=None,
@@ -718,6 +735,8 @@ class PrefixPlan:
         self.Hkv = self.H if kv_heads is None else int(kv_heads)
         self.Tq, self.Tkv, self.Tp = int(qo[-1]), int(ko[-1]), int(po[-1])
         self.num_sms = int(num_sms)
+        self._rows, self._lse = (self.Tq, self.H, self.d), (self.Tq, self.H)
+        self._prefix, self._keys = (self.Tp, self.Hkv, self.d), (self.Tkv, self.Hkv, self.d)
         h = ctypes.c_void_p()
         args = (qp, kp, self.B, gp, pp, self.G, self.H, self.Hkv, self.d, MASK[mask], int(window),
                 int(num_sms))
@@ -726,7 +745,7 @@ class PrefixPlan:
             _ok(L.gdpa_prefix_create_host(*args, ctypes.byref(h)), "gdpa_prefix_create_host")
         else:
             import torch
-            self.device = torch.cuda.current_device()
+            self.device = torch.device("cuda", torch.cuda.current_device())
             _ok(L.gdpa_prefix_create(*args, _stream_ptr(stream), ctypes.byref(h)),
                 "gdpa_prefix_create")
         self._h = h
@@ -779,54 +798,61 @@ class PrefixPlan:
             pass
 
 
-def _prefix_tensor(t, rows, heads, plan, name, dtype):
-    """Address of a checked [rows, heads, d] tensor (None for no rows)."""
-    if t is None and rows == 0:
+def _prefix_tensor(t, shape, plan, name, dtype):
+    """Address of a checked tensor of that shape (None for no rows)."""
+    if t is None and shape[0] == 0:
         return None
-    if not t.is_cuda or t.device.index != plan.device:
-        raise ValueError("%s must be on the plan's device cuda:%s" % (name, plan.device))
-    if t.shape != (rows, heads, plan.d):
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), (rows, heads, plan.d)))
+    if t is None or t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s"
+                         % (name, None if t is None else tuple(t.shape), shape))
+    if t.device != plan.device:
+        raise ValueError("%s must be on the plan's device %s" % (name, plan.device))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     if t.dtype != dtype:
         raise TypeError("%s must be %s" % (name, dtype))
-    return t.data_ptr() if rows else None
+    return t.data_ptr() if shape[0] else None
 
 
 def _prefix_lse(lse, plan):
     import torch
-    if (lse.dtype != torch.float32 or lse.shape != (plan.Tq, plan.H) or not lse.is_contiguous()
-            or not lse.is_cuda or lse.device.index != plan.device):
+    if (lse.dtype != torch.float32 or lse.shape != plan._lse or not lse.is_contiguous()
+            or lse.device != plan.device):
         raise ValueError("lse must be a contiguous float32 [Tq, H] tensor on the plan's device")
     return lse.data_ptr() if plan.Tq else None
 
 
 def _prefix_inputs(plan, q, kp, vp, k, v):
-    dt, dev = q.dtype, plan.device
-    if dev is None:
+    if plan.device is None:
         raise ValueError("a host-only plan cannot launch")
-    return [_prefix_tensor(q, plan.Tq, plan.H, plan, "q", dt),
-            _prefix_tensor(kp, plan.Tp, plan.Hkv, plan, "kp", dt),
-            _prefix_tensor(vp, plan.Tp, plan.Hkv, plan, "vp", dt),
-            _prefix_tensor(k, plan.Tkv, plan.Hkv, plan, "k", dt),
-            _prefix_tensor(v, plan.Tkv, plan.Hkv, plan, "v", dt)]
+    dt = q.dtype
+    kind = _DTYPE_ID.get(dt)
+    if kind is None:
+        raise TypeError("GDPA takes bfloat16 or float32 tensors, got %s" % dt)
+    return (kind, _prefix_tensor(q, plan._rows, plan, "q", dt),
+            _prefix_tensor(kp, plan._prefix, plan, "kp", dt),
+            _prefix_tensor(vp, plan._prefix, plan, "vp", dt),
+            _prefix_tensor(k, plan._keys, plan, "k", dt), _prefix_tensor(v, plan._keys, plan, "v", dt))
 
 
-def _prefix_stream(plan, stream):
-    import torch
-    return (torch.cuda.current_stream(plan.device) if stream is None else stream).cuda_stream
+def _prefix_call(f, what, plan, args, alpha, act, stream):
+    index = plan.device.index
+    args += (plan.d ** -0.5 if alpha is None else alpha, ACT[act],
+             _raw_stream(index) if stream is None else stream.cuda_stream)
+    if index == _current_device():
+        _ok(f(plan.handle, *args), what)
+    else:
+        with _on_device(index):
+            _ok(f(plan.handle, *args), what)
 
 
 def _prefix_fwd(plan, q, kp, vp, k, v, o, lse, alpha, act, stream):
-    ptrs = _prefix_inputs(plan, q, kp, vp, k, v)
-    o = q.new_empty(q.shape) if o is None else o
-    po = _prefix_tensor(o, plan.Tq, plan.H, plan, "o", q.dtype)
-    pl = None if lse is None else _prefix_lse(lse, plan)
-    with _current(q.device):
-        _ok(lib().gdpa_prefix_fwd(plan.handle, _dtype_id(q), *ptrs, po, pl,
-                                  plan.d ** -0.5 if alpha is None else alpha, ACT[act],
-                                  _prefix_stream(plan, stream)), "gdpa_prefix_fwd")
+    args = _prefix_inputs(plan, q, kp, vp, k, v)
+    if o is None:
+        o = _empty(plan._rows, dtype=q.dtype, device=plan.device)
+    args += (_prefix_tensor(o, plan._rows, plan, "o", q.dtype),
+             None if lse is None else _prefix_lse(lse, plan))
+    _prefix_call(lib().gdpa_prefix_fwd, "gdpa_prefix_fwd", plan, args, alpha, act, stream)
     return o
 
 
@@ -843,26 +869,22 @@ def gdpa_prefix_softmax_fwd(plan: PrefixPlan, q, kp, vp, k=None, v=None, o=None,
     """The softmax variant over prefix and own keys together: (O, lse)."""
     import torch
     if lse is None:
-        lse = torch.empty((plan.Tq, plan.H), dtype=torch.float32, device=q.device)
+        lse = _empty(plan._lse, dtype=torch.float32, device=plan.device)
     return _prefix_fwd(plan, q, kp, vp, k, v, o, lse, alpha, "softmax", stream), lse
 
 
 def _prefix_bwd(plan, q, kp, vp, k, v, o, do, lse, grads, alpha, act, stream):
     dt = q.dtype
-    ptrs = _prefix_inputs(plan, q, kp, vp, k, v)
-    po = None if o is None else _prefix_tensor(o, plan.Tq, plan.H, plan, "o", dt)
-    pdo = _prefix_tensor(do, plan.Tq, plan.H, plan, "do", dt)
-    pl = None if lse is None else _prefix_lse(lse, plan)
-    out, pg = [], []
-    for g, rows, heads, name in zip(grads, (plan.Tq, plan.Tp, plan.Tp, plan.Tkv, plan.Tkv),
-                                    (plan.H,) + (plan.Hkv,) * 4, ("dq", "dkp", "dvp", "dk", "dv")):
-        g = q.new_empty((rows, heads, plan.d)) if g is None else g
-        pg.append(_prefix_tensor(g, rows, heads, plan, name, dt))
+    args = _prefix_inputs(plan, q, kp, vp, k, v)
+    args += (None if o is None else _prefix_tensor(o, plan._rows, plan, "o", dt),
+             _prefix_tensor(do, plan._rows, plan, "do", dt), None if lse is None else _prefix_lse(lse, plan))
+    out = []
+    for g, shape, name in zip(grads, (plan._rows, plan._prefix, plan._prefix, plan._keys, plan._keys),
+                              ("dq", "dkp", "dvp", "dk", "dv")):
+        g = _empty(shape, dtype=dt, device=plan.device) if g is None else g
+        args += (_prefix_tensor(g, shape, plan, name, dt),)
         out.append(g)
-    with _current(q.device):
-        _ok(lib().gdpa_prefix_bwd(plan.handle, _dtype_id(q), *ptrs, po, pdo, pl, *pg,
-                                  plan.d ** -0.5 if alpha is None else alpha, ACT[act],
-                                  _prefix_stream(plan, stream)), "gdpa_prefix_bwd")
+    _prefix_call(lib().gdpa_prefix_bwd, "gdpa_prefix_bwd", plan, args, alpha, act, stream)
     return tuple(out)
 
 

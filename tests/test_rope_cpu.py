@@ -100,9 +100,7 @@ def test_refused_sizes():
 
 
 def _apply(rope, dtype=0, T=4, d=8, heads=2, n=1, pos=64, bits=32, off=0, B=0, x=4096, tok=16, head=8):
-    rows = (raw._RopeTensor * 2)()
-    for i in range(2):
-        rows[i] = raw._RopeTensor(x, x, heads, tok, head, tok, head)
+    rows = 2 * raw._rope_tensor(x, x, heads, tok, head, tok, head)
     return gd.lib().gdpa_rope_apply(ctypes.byref(rope.spec), 0, dtype, T, d, rows, n, pos, bits, off,
                                     0, B, 0)
 
