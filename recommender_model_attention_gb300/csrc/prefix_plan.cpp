@@ -4,10 +4,10 @@
 // group's prefix, and (sample, key head, one or two row tiles) against the
 // sample's own keys, in steps of one 128-key block for two row tiles, or of
 // two blocks for a single tile (whose two slots take alternate blocks).  All
-// units' steps form one line that is cut into equal shares, one per CTA, so
-// that ragged groups balance and a short batch spreads a long prefix over
-// every SM; a cut inside a unit costs another part of its rows to merge,
-// which the shares allow for (kPieceCost steps a piece).
+// units' steps are dealt in equal shares, one per CTA, so that ragged groups
+// balance and a short batch spreads a long prefix over every SM; a cut inside
+// a unit costs another part of its rows to merge, which the shares allow for
+// (kPieceCost steps a piece).
 #include <algorithm>
 
 #include "prefix_internal.h"
@@ -147,65 +147,91 @@ gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t
             i += nA + nB;
         }
     }
-    // cut the line of steps into S shares
+    // Cut the steps into S shares.  A prefix unit gives as many whole shares as
+    // it has; those of one (group, key head) start on the same keys at the same
+    // time, so that its row tiles read them from L2 once.  What is left of the
+    // units, and the own units, form one line that is cut into the remaining
+    // shares.
     int64_t total = 0;
     for (const Unit& u : units) total += u.steps + kPieceCost;
-    p.pieces.clear();
-    p.seg.assign((size_t)p.S + 1, 0);
-    const int64_t base = cdiv(total + (int64_t)kPieceCost * p.S, p.S);
+    auto piece_of = [&](size_t n, int64_t done, int64_t take) {
+        const Unit& u = units[n];
+        const int64_t unit_keys = u.p.flags & kPieceDual ? 2 * kBN : kBN;
+        PrefixPiece q = u.p;
+        q.k0 = (int32_t)(u.p.k0 + done * unit_keys);
+        q.nk = (int32_t)std::min<int64_t>(u.p.nk - done * unit_keys, take * unit_keys);
+        if (n < n_prefix) q.pad = (int32_t)n;
+        return q;
+    };
+    const int64_t base = cdiv(total, p.S);
     for (int64_t budget = std::max<int64_t>(base, kPieceCost + 1);; budget += 1 + budget / 64) {
         p.pieces.clear();
+        p.seg.assign((size_t)p.S + 1, 0);
         int cta = 0;
-        int64_t left = budget;
         bool ok = true;
+        const int64_t share = budget - kPieceCost;
+        // whole shares, the units of a (group, key head) side by side
+        for (size_t n = 0; n < n_prefix && ok;) {
+            size_t e = n + 1;
+            while (e < n_prefix && units[e].p.k0 == units[n].p.k0 && units[e].p.hk == units[n].p.hk) ++e;
+            int64_t most = 0;
+            for (size_t i = n; i < e; ++i) most = std::max(most, units[i].steps / share);
+            for (int64_t c = 0; c < most && ok; ++c)
+                for (size_t i = n; i < e; ++i) {
+                    if (units[i].steps / share <= c) continue;
+                    if (cta >= p.S) {
+                        ok = false;
+                        break;
+                    }
+                    p.pieces.push_back(piece_of(i, c * share, share));
+                    p.seg[(size_t)++cta] = (int32_t)p.pieces.size();
+                }
+            n = e;
+        }
+        // the line
+        int64_t left = budget;
+        bool open = false;   // the current share has pieces
         for (size_t n = 0; n < units.size() && ok; ++n) {
             const Unit& u = units[n];
-            // own units stay whole (their parts are laid out above)
-            int64_t done = 0;
+            const bool own = n >= n_prefix;   // own units stay whole (their parts are laid out above)
+            int64_t done = own ? 0 : u.steps / share * share;
             while (done < u.steps) {
                 int64_t take = left - kPieceCost;
-                if (n >= n_prefix && take < u.steps && left < budget) take = 0;
-                if (take < 1) {
-                    if (left == budget) {
-                        take = u.steps;   // one share cannot hold it: it does
-                    } else {
-                        if (++cta >= p.S) { ok = false; break; }
-                        p.seg[cta] = (int32_t)p.pieces.size();
-                        left = budget;
-                        continue;
-                    }
+                if (open && (take < 1 || (own && take < u.steps))) {
+                    p.seg[(size_t)++cta] = (int32_t)p.pieces.size();
+                    left = budget;
+                    open = false;
+                    continue;
                 }
-                take = n >= n_prefix ? u.steps : std::min(take, u.steps - done);
-                const int64_t unit_keys = u.p.flags & kPieceDual ? 2 * kBN : kBN;
-                PrefixPiece q = u.p;
-                q.k0 = (int32_t)(u.p.k0 + done * unit_keys);
-                q.nk = (int32_t)std::min<int64_t>(u.p.nk - done * unit_keys, take * unit_keys);
-                if (n < n_prefix) q.pad = (int32_t)n;
-                p.pieces.push_back(q);
+                if (cta >= p.S) {
+                    ok = false;
+                    break;
+                }
+                take = own ? u.steps : std::min(take, u.steps - done);
+                p.pieces.push_back(piece_of(n, done, take));
+                open = true;
                 done += take;
                 left -= take + kPieceCost;
             }
         }
         if (ok) {
-            for (int c = cta + 1; c <= p.S; ++c) p.seg[c] = (int32_t)p.pieces.size();
+            if (open) ++cta;
+            for (int c = cta; c <= p.S; ++c) p.seg[(size_t)c] = (int32_t)p.pieces.size();
             break;
         }
     }
-    // the prefix parts of each tile: its unit's pieces in order
-    for (size_t i = 0; i < p.pieces.size();) {
-        if (p.pieces[i].flags & kPieceOwn) {
-            p.pieces[i++].pad = 0;
-            continue;
-        }
-        const Unit& u = units[p.pieces[i].pad];
-        size_t e = i;
-        while (e < p.pieces.size() && !(p.pieces[e].flags & kPieceOwn) && p.pieces[e].pad == p.pieces[i].pad) ++e;
+    // a unit's pieces, in order of keys, for its parts
+    std::vector<std::vector<int32_t>> of_unit(n_prefix);
+    for (size_t i = 0; i < p.pieces.size(); ++i)
+        if (!(p.pieces[i].flags & kPieceOwn)) of_unit[(size_t)p.pieces[i].pad].push_back((int32_t)i);
+    for (size_t n = 0; n < n_prefix; ++n) {
+        const Unit& u = units[n];
         const bool dual = u.p.flags & kPieceDual;
         const int32_t ra = u.p.nA * p.r, rb = u.p.nB * p.r;
         PrefixTile& ta = p.tiles[u.tileA];
         ta.part = (int32_t)parts;
-        for (size_t j = i; j < e; ++j) {
-            PrefixPiece& q = p.pieces[j];
+        for (int32_t i : of_unit[n]) {
+            PrefixPiece& q = p.pieces[(size_t)i];
             q.part0 = (int32_t)parts;
             parts += ra;
             q.part1 = -1;
@@ -217,14 +243,13 @@ gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t
         ta.layers = (int32_t)((parts - ta.part) / ra);
         if (!dual) {
             p.tiles[u.tileB].part = (int32_t)parts;
-            p.tiles[u.tileB].layers = (int32_t)(e - i);
-            for (size_t j = i; j < e; ++j) {
-                p.pieces[j].part1 = (int32_t)parts;
+            p.tiles[u.tileB].layers = (int32_t)of_unit[n].size();
+            for (int32_t i : of_unit[n]) {
+                p.pieces[(size_t)i].part1 = (int32_t)parts;
                 parts += rb;
             }
         }
         if (parts > 0x7fffffff) return GDPA_ERR_UNSUPPORTED;
-        i = e;
     }
     for (PrefixPiece& q : p.pieces) q.pad = 0;
     for (const Unit& u : small_units) p.pieces.push_back(u.p);

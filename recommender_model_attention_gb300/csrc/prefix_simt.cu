@@ -317,11 +317,12 @@ __global__ void __launch_bounds__(kThreads) simt_keys_kernel(const SimtArgs a) {
 }
 
 // Join the parts of 8 rows of a tile: a thread per (row, 4 columns).  The
-// first eight layers, usually all, are loaded together before anything is
-// known of them; further ones eight at a time, a warp's four threads of a row
-// sharing a look at their maxima.
+// first four layers, usually all, are loaded together before anything is known
+// of them; further ones four at a time, a warp's four threads of a row sharing
+// a look at their maxima.  Few registers, so that many blocks hide the chain of
+// loads (tile, token, layers) of each other.
 template <typename E>
-__global__ void __launch_bounds__(256) merge_kernel(const PrefixTile* tiles, const PrefixOwn* owns,
+__global__ void __launch_bounds__(256, 4) merge_kernel(const PrefixTile* tiles, const PrefixOwn* owns,
                                                     const float* parts, const float* ml, E* out,
                                                     float* lse, int H, int r, int d, int softmax) {
     const PrefixTile t = tiles[blockIdx.x];
@@ -344,11 +345,11 @@ __global__ void __launch_bounds__(256) merge_kernel(const PrefixTile* tiles, con
         at = pre ? row : orow;
         return pre ? (int64_t)t.part + (int64_t)x * nrows : own0 + (int64_t)(x - t.layers) * ow.rows;
     };
-    float2 s[8];
-    float4 v[8];
-    auto load8 = [&](int x0) {
+    float2 s[4];
+    float4 v[4];
+    auto load4 = [&](int x0) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < 4; ++u) {
             s[u] = make_float2(-INFINITY, 0.f);
             v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (x0 + u < total && c < c4) {
@@ -360,11 +361,11 @@ __global__ void __launch_bounds__(256) merge_kernel(const PrefixTile* tiles, con
         }
     };
     grid_wait_previous();
-    load8(0);
+    load4(0);
     float top = -INFINITY, ref = 0.f, sum = 0.f;
     if (softmax) {
 #pragma unroll 4
-        for (int x = 8 + (lane >> 3); x < total; x += 4) {
+        for (int x = 4 + (lane >> 3); x < total; x += 4) {
             int n, at;
             const int64_t p = place(x, n, at);
             top = fmaxf(top, st[p + at].x);
@@ -372,15 +373,15 @@ __global__ void __launch_bounds__(256) merge_kernel(const PrefixTile* tiles, con
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
 #pragma unroll
-        for (int u = 0; u < 8; ++u) top = fmaxf(top, s[u].x);
+        for (int u = 0; u < 4; ++u) top = fmaxf(top, s[u].x);
         ref = top == -INFINITY ? 0.f : top;
     }
     if (!real || c >= c4) return;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int x0 = 0; x0 < total; x0 += 8) {
-        if (x0 > 0) load8(x0);
+    for (int x0 = 0; x0 < total; x0 += 4) {
+        if (x0 > 0) load4(x0);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < 4; ++u) {
             float w = 1.f;
             if (softmax) {
                 if (s[u].x == -INFINITY) continue;   // no such layer, or nothing visible in it
@@ -487,13 +488,14 @@ gdpa_status launch_prefix_merge(PrefixPlan& p, gdpa_dtype dt, void* out, float* 
                                 cudaStream_t st) {
     if (p.tiles.empty()) return GDPA_OK;
     const dim3 grid((unsigned)p.tiles.size(), kBM / 8);
+    const int threads = p.d > 64 ? 256 : 128;   // a warp has 16 columns of 8 rows
     const float *parts = p.d_parts, *ml = p.d_ml;
     const bool early = p.chain > 0;
     const int sm = softmax;
     const bool ok = dt == GDPA_BF16
-                        ? launch_kernel(merge_kernel<__nv_bfloat16>, grid, 256, 0, st, early, p.dev_tiles(),
+                        ? launch_kernel(merge_kernel<__nv_bfloat16>, grid, threads, 0, st, early, p.dev_tiles(),
                                         p.dev_own(), parts, ml, (__nv_bfloat16*)out, lse, p.H, p.r, p.d, sm)
-                        : launch_kernel(merge_kernel<float>, grid, 256, 0, st, early, p.dev_tiles(), p.dev_own(),
+                        : launch_kernel(merge_kernel<float>, grid, threads, 0, st, early, p.dev_tiles(), p.dev_own(),
                                         parts, ml, (float*)out, lse, p.H, p.r, p.d, sm);
     p.launches += 1;
     return ok ? GDPA_OK : GDPA_ERR_CUDA;

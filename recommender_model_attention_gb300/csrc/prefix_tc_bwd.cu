@@ -16,8 +16,8 @@
 // changes the sums from run to run.  Results here are the same bits every time.
 //
 // Both walk items of 64 columns (query rows, or keys): two slots of TMEM
-// columns [S | dP], two warpgroups each, which take 32 of the columns, thread =
-// lane.  While one slot's weights
+// columns [S | dP], a warpgroup each, thread = lane, whose 128 scores are read
+// at once into registers that the first warpgroup has handed over.  While one slot's weights
 // are computed the tensor core runs the other slot's products and the next
 // scores: item e's closing products, then S and dP of item e + 2 into the same
 // columns.  Rows behind the last one of an item share its 16-row step: their
@@ -35,7 +35,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 64 + 512;
+constexpr int kThreads = 384;   // producer and issuer (and two idle warps), a warpgroup per slot
 constexpr int kHalfBytes = 128 * 128;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kItem = 64;   // columns of an item
@@ -92,8 +92,8 @@ struct KvCfg {
     static constexpr int kHalves = D / 64;
     static constexpr int kTile = 128 * D * 2;
     static constexpr int kOffK = 0, kOffV = kTile, kOffQ = 2 * kTile, kOffDO = 4 * kTile;   // Q, dO: 2 stages
-    static constexpr int kOffStat = 6 * kTile;   // [16 warps][2][32] (lse, delta) pairs
-    static constexpr int kOffBar = kOffStat + 16 * 2 * 32 * 8;
+    static constexpr int kOffStat = 6 * kTile;   // [8 warps][2][64] (lse, delta) pairs
+    static constexpr int kOffBar = kOffStat + 8 * 2 * 64 * 8;
     enum { kKVFull = 0, kKVEmpty, kFull, kEmpty = kFull + 2, kSDFull = kEmpty + 2, kPFull = kSDFull + 2,
            kAccFull = kPFull + 2, kAccFree, kMmaDone, kNumBars };
     static constexpr int kSmem = kOffBar + kNumBars * 8 + 16 + 1024;
@@ -105,7 +105,7 @@ __device__ __forceinline__ int tile_rows(const PrefixUnit& u, const BwArgs& a, i
 }
 
 template <int D>
-__device__ void kv_producer(const CUtensorMap* tmQ, const CUtensorMap* tmDO, const CUtensorMap* tmKp,
+__device__ __forceinline__ void kv_producer(const CUtensorMap* tmQ, const CUtensorMap* tmDO, const CUtensorMap* tmKp,
                             const CUtensorMap* tmVp, const CUtensorMap* tmK, const CUtensorMap* tmV,
                             const BwArgs& a, uint8_t* smem, uint64_t* bars, int seg0, int seg1,
                             const Abort& ab) {
@@ -117,7 +117,7 @@ __device__ void kv_producer(const CUtensorMap* tmQ, const CUtensorMap* tmDO, con
         const PrefixUnit u = load_unit(a.units + t);
         const int tiles = (u.ntok + a.tpt - 1) / a.tpt;
         if (tiles == 0) continue;
-        if (!mbar_wait(&bars[C::kKVEmpty], (nu & 1) ^ 1, ab, 81)) goto unwind;
+        if (!mbar_wait<true>(&bars[C::kKVEmpty], (nu & 1) ^ 1, ab, 81)) goto unwind;
         mbar_arrive_expect_tx(&bars[C::kKVFull], 2 * C::kTile);
         kv_armed = (int32_t)(nu & 1);
         {
@@ -133,7 +133,7 @@ __device__ void kv_producer(const CUtensorMap* tmQ, const CUtensorMap* tmDO, con
         }
         for (int m = 0; m < tiles; ++m, ++i) {
             const uint32_t st = i & 1, ph = (i >> 1) & 1;
-            if (!mbar_wait(&bars[C::kEmpty + st], ph ^ 1, ab, 82)) goto unwind;
+            if (!mbar_wait<true>(&bars[C::kEmpty + st], ph ^ 1, ab, 82)) goto unwind;
             mbar_arrive_expect_tx(&bars[C::kFull + st], 2 * (uint32_t)a.q_bytes);
             armed[st] = (int32_t)ph;
 #pragma unroll
@@ -211,8 +211,8 @@ __device__ __forceinline__ void kv_mma(const BwArgs& a, uint8_t* smem, uint64_t*
             const uint64_t off = q_mn + tileB.st * kTileDesc + halfB * kItemDesc;
             const uint32_t steps = (x == items - 1 ? last16 : halfB ? tail16 : 64u) >> 4;
             const uint32_t col = tmem + slotB * 128;
-            one_sums(tmem + 256, col, col + 32, off + kDO, idesc_acc, steps, x > 0);
-            one_sums(tmem + 384, col + 64, col + 96, off, idesc_acc, steps, x > 0);
+            one_sums(tmem + 256, col, col + 16, off + kDO, idesc_acc, steps, x > 0);
+            one_sums(tmem + 384, col + 64, col + 80, off, idesc_acc, steps, x > 0);
             p_ph ^= slotB;
             slotB ^= 1;
             if (++halfB == (uint32_t)full || x == items - 1) {
@@ -226,59 +226,42 @@ __device__ __forceinline__ void kv_mma(const BwArgs& a, uint8_t* smem, uint64_t*
     }
 }
 
-// 32 packed columns of a row from the accumulator at `col` (scaled) as bf16
-__device__ __forceinline__ void store32(uint32_t col, float scale, __nv_bfloat16* dst, bool real) {
-    uint32_t v[32];
-    tmem_ld32(col, v);
-    tmem_ld_wait();
-    if (!real) return;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            w[e] = pack_bf16x2(__uint_as_float(v[8 * c + 2 * e]) * scale,
-                               __uint_as_float(v[8 * c + 2 * e + 1]) * scale);
-        reinterpret_cast<uint4*>(dst)[c] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-}
-
 template <int D, int ACT>
-__device__ void kv_rows(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t tmem, int seg0, int seg1,
-                        const Abort& ab) {
+__device__ __forceinline__ void kv_rows(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t tmem, int seg0,
+                                        int seg1, const Abort& ab) {
     using C = KvCfg<D>;
     constexpr bool kSm = ACT == kSoftmax;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int s = (warp - 2) >> 3, h = ((warp - 2) >> 2) & 1, quarter = warp & 3;
+    const int s = (warp - 4) >> 2, quarter = warp & 3;
     const int key = quarter * 32 + lane;   // TMEM lane
-    const int tid = (int)(threadIdx.x - 64) & 127;
     const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t col = trow + s * 128 + 32 * h;   // this thread's 32 rows' scores
+    const uint32_t col = trow + s * 128;
     // a warp's row statistics, two items' in turn
-    float2* stat = reinterpret_cast<float2*>(smem + C::kOffStat) + (warp - 2) * 64;
+    float2* stat = reinterpret_cast<float2*>(smem + C::kOffStat) + (warp - 4) * 128;
     const ActScale ks = act_scale<ACT>(a.alpha);
-    uint32_t nu = 0, tile0 = 0, e0 = 0;
+    const int full = a.tpt * a.r > kItem ? 2 : 1;
+    uint32_t acc_ph = 0, tile0 = 0, e0 = 0;
+    PrefixUnit u = load_unit(a.units + seg0);
     for (int t = seg0; t < seg1; ++t) {
-        const PrefixUnit u = load_unit(a.units + t);
+        const PrefixUnit coming = load_unit(a.units + min(t + 1, seg1 - 1));
         const bool own = u.flags & kPieceOwn;
         const int tiles = (u.ntok + a.tpt - 1) / a.tpt;
-        __nv_bfloat16* dk = (own ? a.dk : a.dkp) + ((int64_t)(u.k0 + key) * a.Hkv + u.hk) * D;
-        __nv_bfloat16* dv = (own ? a.dv : a.dvp) + ((int64_t)(u.k0 + key) * a.Hkv + u.hk) * D;
+        __nv_bfloat16* dst = s ? (own ? a.dk : a.dkp) : (own ? a.dv : a.dvp);
+        dst += ((int64_t)(u.k0 + key) * a.Hkv + u.hk) * D;
         const bool real = key < u.nk;
         if (tiles == 0) {   // keys that no row sees
-            uint4* z = reinterpret_cast<uint4*>(s ? dk : dv);
             if (real)
-                for (int c = h * (D / 16); c < (h + 1) * (D / 16); ++c) z[c] = make_uint4(0u, 0u, 0u, 0u);
+                for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(dst)[c] = make_uint4(0u, 0u, 0u, 0u);
+            u = coming;
             continue;
         }
-        const int full = a.tpt * a.r > kItem ? 2 : 1;
         const int items = (tiles - 1) * full + (tile_rows(u, a, tiles - 1) + kItem - 1) / kItem;
         const bool banded = own && a.windowed;
         const int jpos = u.j0 + key;
-        auto stats = [&](int xi) -> float2 {   // of row 32 h + lane of item xi
+        auto stats = [&](int xi, int half) -> float2 {   // of row 32 half + lane of item xi
             float2 v = make_float2(INFINITY, 0.0f);
             if (kSm && xi < items) {
-                const int m = full == 2 ? xi >> 1 : xi, row = (full == 2 ? (xi & 1) * kItem : 0) + 32 * h + lane;
+                const int m = full == 2 ? xi >> 1 : xi, row = (full == 2 ? (xi & 1) * kItem : 0) + 32 * half + lane;
                 if (row < tile_rows(u, a, m)) {
                     const int tt = row / a.r;
                     const int64_t at = (int64_t)(u.tok + m * a.tpt + tt) * a.H + u.hk * a.r + (row - tt * a.r);
@@ -291,28 +274,42 @@ __device__ void kv_rows(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t
         };
         // this slot's items of the unit: those with e0 + x of its parity
         int x = (int)((e0 ^ (uint32_t)s) & 1);
-        float2 next = make_float2(INFINITY, 0.0f);
-        if (kSm) next = stats(x);
+        float2 next0 = make_float2(INFINITY, 0.0f), next1 = next0;
+        if (kSm) {
+            next0 = stats(x, 0);
+            next1 = stats(x, 1);
+        }
         for (; x < items; x += 2) {
             const uint32_t e = e0 + x;
             const int m = full == 2 ? x >> 1 : x, r0 = full == 2 ? (x & 1) * kItem : 0;
-            const int n = min(kItem, tile_rows(u, a, m) - r0) - 32 * h;   // rows here, may be <= 0
-            const float2* sb = stat + ((e >> 1) & 1) * 32;
+            const int n = min(kItem, tile_rows(u, a, m) - r0);
+            float2* sb = stat + ((e >> 1) & 1) * 64;
             if (kSm) {
-                stat[((e >> 1) & 1) * 32 + lane] = next;
-                next = stats(x + 2);
+                sb[lane] = next0;
+                sb[32 + lane] = next1;
+                next0 = stats(x + 2, 0);
+                next1 = stats(x + 2, 1);
                 __syncwarp();
             }
-            if (!wg_wait(&bars[C::kSDFull + s], (e >> 1) & 1, ab, 91)) return;
+            if (!wg_wait<true>(&bars[C::kSDFull + s], (e >> 1) & 1, ab, 91)) return;
             tc_fence_after();
-            const bool cut = banded || n < 32;
-#pragma unroll 1
-            for (int c = 0; c < 32; c += 16) {
-                if (c >= n) break;
-                uint32_t sv[16], dv16[16], pk[8], dk8[8];
-                tmem_ld16(col + c, sv);
-                tmem_ld16(col + 64 + c, dv16);
-                tmem_ld_wait();
+            const bool cut = banded || n < kItem;
+            int lo = 0, hi = n;   // rows that see this key: positions jpos .. jpos + window - 1
+            if (banded) {
+                const int64_t first = (int64_t)(jpos - u.i0 - m * a.tpt) * a.r - r0;
+                lo = (int)max((int64_t)0, first);
+                hi = (int)max((int64_t)0, min((int64_t)n, first + (int64_t)a.window * a.r));
+            }
+            uint32_t sv[64], pv[64];
+#pragma unroll
+            for (int c = 0; c < 64; c += 32) {
+                tmem_ld32(col + c, *reinterpret_cast<uint32_t(*)[32]>(sv + c));
+                tmem_ld32(col + 64 + c, *reinterpret_cast<uint32_t(*)[32]>(pv + c));
+            }
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 64; c += 16) {
+                uint32_t pk[8], dk8[8];
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
                     float l0 = 0.f, l1 = 0.f, d0 = 0.f, d1 = 0.f, p0, p1, g0, g1;
@@ -320,49 +317,60 @@ __device__ void kv_rows(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t
                         const float4 st = *reinterpret_cast<const float4*>(sb + c + i);
                         l0 = st.x; d0 = st.y; l1 = st.z; d1 = st.w;
                     }
-                    weights2<ACT>(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1]),
-                                  __uint_as_float(dv16[i]), __uint_as_float(dv16[i + 1]), ks, l0, l1, d0, d1,
+                    weights2<ACT>(__uint_as_float(sv[c + i]), __uint_as_float(sv[c + i + 1]),
+                                  __uint_as_float(pv[c + i]), __uint_as_float(pv[c + i + 1]), ks, l0, l1, d0, d1,
                                   p0, p1, g0, g1);
                     if (cut) {
-#pragma unroll
-                        for (int w = 0; w < 2; ++w) {
-                            const int row = c + i + w;
-                            bool ok = row < n;
-                            if (banded) {
-                                const int ipos = u.i0 + m * a.tpt + (r0 + 32 * h + row) / a.r;
-                                ok = ok && jpos <= ipos && jpos > ipos - a.window;
-                            }
-                            if (!ok) (w ? p1 : p0) = (w ? g1 : g0) = 0.0f;
-                        }
+                        const bool ok0 = c + i >= lo && c + i < hi, ok1 = c + i + 1 >= lo && c + i + 1 < hi;
+                        p0 = ok0 ? p0 : 0.0f;
+                        g0 = ok0 ? g0 : 0.0f;
+                        p1 = ok1 ? p1 : 0.0f;
+                        g1 = ok1 ? g1 : 0.0f;
                     }
                     pk[i >> 1] = pack_bf16x2(p0, p1);
                     dk8[i >> 1] = pack_bf16x2(g0, g1);
                 }
-                // over this thread's own scores: 16 packed columns of 32
-                tmem_st8(col + c / 2, pk);
+                tmem_st8(col + c / 2, pk);   // over scores that have been read
                 tmem_st8(col + 64 + c / 2, dk8);
             }
             tmem_st_wait();
-            if (n > 0 && n < 32 && (n & 15)) {
+            if (n & 15) {
                 const uint32_t st = (tile0 + m) & 1;
-                const int z0 = r0 + 32 * h + n, z1 = r0 + 32 * h + ((n + 15) & ~15);
-                clear_rows<D>(smem + C::kOffQ + st * C::kTile, z0, z1, tid);
-                clear_rows<D>(smem + C::kOffDO + st * C::kTile, z0, z1, tid);
+                clear_rows<D>(smem + C::kOffQ + st * C::kTile, r0 + n, r0 + ((n + 15) & ~15), key);
+                clear_rows<D>(smem + C::kOffDO + st * C::kTile, r0 + n, r0 + ((n + 15) & ~15), key);
                 fence_proxy_async_smem();
             }
             tc_fence_before();
             mbar_arrive(&bars[C::kPFull + s]);
         }
-        if (!wg_wait(&bars[C::kAccFull], nu & 1, ab, 92)) return;
+        if (!wg_wait<true>(&bars[C::kAccFull], acc_ph, ab, 92)) return;
+        acc_ph ^= 1;
         tc_fence_after();
-#pragma unroll 1
-        for (int c = h * (D / 2); c < (h + 1) * (D / 2); c += 32)
-            store32(trow + (s ? 384 : 256) + c, s ? a.alpha : 1.0f, (s ? dk : dv) + c, real);
-        tc_fence_before();
-        mbar_arrive(&bars[C::kAccFree]);
-        ++nu;
+#pragma unroll
+        for (int c = 0; c < D; c += 64) {   // slot 0: dV, slot 1: dK
+            uint32_t v[64];
+            tmem_ld32(trow + 256 + 128 * s + c, *reinterpret_cast<uint32_t(*)[32]>(v));
+            tmem_ld32(trow + 256 + 128 * s + c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+            tmem_ld_wait();
+            if (c + 64 == D) {
+                tc_fence_before();
+                mbar_arrive(&bars[C::kAccFree]);
+            }
+            const float f = s ? a.alpha : 1.0f;
+            if (real) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+                        o[w] = pack_bf16x2(__uint_as_float(v[8 * i + 2 * w]) * f, __uint_as_float(v[8 * i + 2 * w + 1]) * f);
+                    reinterpret_cast<uint4*>(dst + c)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+        }
         tile0 += tiles;
         e0 += items;
+        u = coming;
     }
 }
 
@@ -387,7 +395,7 @@ prefix_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     }
     if (threadIdx.x == 0) {
         for (int b = 0; b < C::kNumBars; ++b)
-            mbar_init(&bars[b], b == C::kPFull || b == C::kPFull + 1 ? 256u : b == C::kAccFree ? 512u : 1u);
+            mbar_init(&bars[b], b == C::kPFull || b == C::kPFull + 1 ? 128u : b == C::kAccFree ? 256u : 1u);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -397,18 +405,23 @@ prefix_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const Abort ab{abort_flag, a.err, a.wait_ns};
-    if (warp == 0) {
-        if (lane == 0) kv_producer<D>(&tmQ, &tmDO, &tmKp, &tmVp, &tmK, &tmV, a, smem, bars, seg0, seg1, ab);
-        __syncwarp();
-    } else if (warp == 1) {
-        if (elect_one()) {
-            kv_mma<D>(a, smem, bars, tmem, seg0, seg1, ab);
-            // all of its products complete before TMEM is released
-            one_commit(&bars[C::kMmaDone]);
-            mbar_wait_teardown(&bars[C::kMmaDone], 0);
+    // 384 threads start with 168 registers: 88 + 2 * 208 a triple
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 0) {
+            if (lane == 0) kv_producer<D>(&tmQ, &tmDO, &tmKp, &tmVp, &tmK, &tmV, a, smem, bars, seg0, seg1, ab);
+            __syncwarp();
+        } else if (warp == 1) {
+            if (elect_one()) {
+                kv_mma<D>(a, smem, bars, tmem, seg0, seg1, ab);
+                // all of its products complete before TMEM is released
+                one_commit(&bars[C::kMmaDone]);
+                mbar_wait_teardown(&bars[C::kMmaDone], 0);
+            }
+            __syncwarp();
         }
-        __syncwarp();
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         kv_rows<D, ACT>(a, smem, bars, tmem, seg0, seg1, ab);
     }
     tc_fence_before();
@@ -460,7 +473,7 @@ struct Run {
 };
 
 template <int D>
-__device__ void dq_producer(const CUtensorMap* tmQ, const CUtensorMap* tmDO, const CUtensorMap* tmKp,
+__device__ __forceinline__ void dq_producer(const CUtensorMap* tmQ, const CUtensorMap* tmDO, const CUtensorMap* tmKp,
                             const CUtensorMap* tmVp, const CUtensorMap* tmK, const CUtensorMap* tmV,
                             const BwArgs& a, uint8_t* smem, uint64_t* bars, int seg0, int seg1,
                             const Abort& ab) {
@@ -473,7 +486,7 @@ __device__ void dq_producer(const CUtensorMap* tmQ, const CUtensorMap* tmDO, con
         const PrefixPiece p = load_piece(a.pieces + (t >> 1));
         const Run run(p, t & 1, a.r);
         if (run.blocks == 0) continue;
-        if (!mbar_wait(&bars[C::kQEmpty], (nr & 1) ^ 1, ab, 101)) goto unwind;
+        if (!mbar_wait<true>(&bars[C::kQEmpty], (nr & 1) ^ 1, ab, 101)) goto unwind;
         mbar_arrive_expect_tx(&bars[C::kQFull], 2 * (uint32_t)a.q_bytes);
         q_armed = (int32_t)(nr & 1);
 #pragma unroll
@@ -486,7 +499,7 @@ __device__ void dq_producer(const CUtensorMap* tmQ, const CUtensorMap* tmDO, con
             for (int kv = 0; kv < 2; ++kv, ++c) {
                 const CUtensorMap* map = kv ? (own ? tmV : tmVp) : (own ? tmK : tmKp);
                 const uint32_t st = c % C::kStages, ph = (c / C::kStages) & 1;
-                if (!mbar_wait(&bars[C::kEmpty + st], ph ^ 1, ab, 102)) goto unwind;
+                if (!mbar_wait<true>(&bars[C::kEmpty + st], ph ^ 1, ab, 102)) goto unwind;
                 mbar_arrive_expect_tx(&bars[C::kFull + st], C::kTile);
                 armed[st] = (int32_t)ph;
 #pragma unroll
@@ -557,7 +570,7 @@ __device__ __forceinline__ void dq_mma(const BwArgs& a, uint8_t* smem, uint64_t*
             if (!mbar_wait<true>(&bars[C::kPFull + slotB], p_ph, ab, 107)) return;
             tc_fence_after();
             const uint32_t col = tmem + slotB * 128;
-            one_sums(tmem + 256, col, col + 32, kv_mn + kB.st * kTileDesc + (x & 1) * kItemDesc, idesc_acc,
+            one_sums(tmem + 256, col, col + 16, kv_mn + kB.st * kTileDesc + (x & 1) * kItemDesc, idesc_acc,
                      (x == items - 1 ? last16 : 64u) >> 4, x > 0);
             p_ph ^= slotB;
             slotB ^= 1;
@@ -573,19 +586,18 @@ __device__ __forceinline__ void dq_mma(const BwArgs& a, uint8_t* smem, uint64_t*
 }
 
 template <int D, int ACT>
-__device__ void dq_rows(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t tmem, int seg0, int seg1,
-                        const Abort& ab) {
+__device__ __forceinline__ void dq_rows(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t tmem, int seg0,
+                                        int seg1, const Abort& ab) {
     using C = DqCfg<D>;
     constexpr bool kSm = ACT == kSoftmax;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int s = (warp - 2) >> 3, h = ((warp - 2) >> 2) & 1, quarter = warp & 3;
+    const int s = (warp - 4) >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
-    const int tid = (int)(threadIdx.x - 64) & 127;
     const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t col = trow + s * 128 + 32 * h;   // this thread's 32 keys' scores
+    const uint32_t col = trow + s * 128;
     const ActScale ks = act_scale<ACT>(a.alpha);
     const int rt = row / a.r, rj = row - rt * a.r;
-    uint32_t nr = 0, ring = 0, e0 = 0;
+    uint32_t acc_ph = 0, ring = 0, e0 = 0;
     for (int t = 2 * seg0; t < 2 * seg1; ++t) {
         const PrefixPiece p = load_piece(a.pieces + (t >> 1));
         const Run run(p, t & 1, a.r);
@@ -603,28 +615,31 @@ __device__ void dq_rows(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t
         }
         for (int x = (int)((e0 ^ (uint32_t)s) & 1); x < items; x += 2) {
             const uint32_t e = e0 + x;
-            const int n = min(kItem, run.keys(x >> 1) - (x & 1) * kItem) - 32 * h;   // keys here, may be <= 0
-            const bool cut = banded || n < 32;
+            const int n = min(kItem, run.keys(x >> 1) - (x & 1) * kItem);
+            const bool cut = banded || n < kItem;
             int lo = 0, hi = n;   // columns this row sees
             if (banded) {
-                const int at = ipos - (p.j0 + run.block(x >> 1) * kBN + (x & 1) * kItem + 32 * h);
+                const int at = ipos - (p.j0 + run.block(x >> 1) * kBN + (x & 1) * kItem);
                 hi = min(hi, at + 1);
                 lo = at >= a.window ? at - a.window + 1 : 0;
             }
-            if (!wg_wait(&bars[C::kSDFull + s], (e >> 1) & 1, ab, 111)) return;
+            if (!wg_wait<true>(&bars[C::kSDFull + s], (e >> 1) & 1, ab, 111)) return;
             tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < 32; c += 16) {
-                if (c >= n) break;
-                uint32_t sv[16], dv16[16], dk8[8];
-                tmem_ld16(col + c, sv);
-                tmem_ld16(col + 64 + c, dv16);
-                tmem_ld_wait();
+            uint32_t sv[64], pv[64];
+#pragma unroll
+            for (int c = 0; c < 64; c += 32) {
+                tmem_ld32(col + c, *reinterpret_cast<uint32_t(*)[32]>(sv + c));
+                tmem_ld32(col + 64 + c, *reinterpret_cast<uint32_t(*)[32]>(pv + c));
+            }
+            tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 64; c += 16) {
+                uint32_t dk8[8];
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
                     float p0, p1, g0, g1;
-                    weights2<ACT>(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1]),
-                                  __uint_as_float(dv16[i]), __uint_as_float(dv16[i + 1]), ks, lse2, lse2, delta,
+                    weights2<ACT>(__uint_as_float(sv[c + i]), __uint_as_float(sv[c + i + 1]),
+                                  __uint_as_float(pv[c + i]), __uint_as_float(pv[c + i + 1]), ks, lse2, lse2, delta,
                                   delta, p0, p1, g0, g1);
                     if (cut) {
                         if (c + i < lo || c + i >= hi) g0 = 0.0f;
@@ -632,41 +647,38 @@ __device__ void dq_rows(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t
                     }
                     dk8[i >> 1] = pack_bf16x2(g0, g1);
                 }
-                tmem_st8(col + c / 2, dk8);   // over this thread's own scores
+                tmem_st8(col + c / 2, dk8);   // over scores that have been read
             }
             tmem_st_wait();
-            if (n > 0 && n < 32 && (n & 15)) {
+            if (n & 15) {
                 const uint32_t sk = (ring + 2 * (uint32_t)(x >> 1)) % C::kStages;
-                const int r0 = (x & 1) * kItem + 32 * h;
-                clear_rows<D>(smem + C::kOffKV + sk * C::kTile, r0 + n, r0 + ((n + 15) & ~15), tid);
+                const int r0 = (x & 1) * kItem;
+                clear_rows<D>(smem + C::kOffKV + sk * C::kTile, r0 + n, r0 + ((n + 15) & ~15), row);
                 fence_proxy_async_smem();
             }
             tc_fence_before();
             mbar_arrive(&bars[C::kPFull + s]);
         }
-        if (!wg_wait(&bars[C::kAccFull], nr & 1, ab, 112)) return;
+        if (!wg_wait<true>(&bars[C::kAccFull], acc_ph, ab, 112)) return;
+        acc_ph ^= 1;
         tc_fence_after();
         float4* out = reinterpret_cast<float4*>(a.parts) + (int64_t)run.part * (D / 4) + row;
-        {   // this warpgroup's quarter of the columns
-            constexpr int kQ = D / 4;
-            const int c0 = (2 * s + h) * kQ;
+        {   // this slot's half of the columns
+            const int c0 = s * (D / 2);
+            uint32_t o[D / 2];
 #pragma unroll
-            for (int c = 0; c < kQ; c += 16) {
-                uint32_t o[16];
-                tmem_ld16(trow + 256 + c0 + c, o);
-                tmem_ld_wait();
-                if (real) {
+            for (int c = 0; c < D / 2; c += 32) tmem_ld32(trow + 256 + c0 + c, *reinterpret_cast<uint32_t(*)[32]>(o + c));
+            tmem_ld_wait();
+            tc_fence_before();
+            mbar_arrive(&bars[C::kAccFree]);
+            if (real) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        out[(int64_t)((c0 + c) / 4 + e) * run.rows] =
-                            make_float4(__uint_as_float(o[4 * e]) * a.alpha, __uint_as_float(o[4 * e + 1]) * a.alpha,
-                                        __uint_as_float(o[4 * e + 2]) * a.alpha, __uint_as_float(o[4 * e + 3]) * a.alpha);
-                }
+                for (int e = 0; e < D / 8; ++e)
+                    out[(int64_t)(c0 / 4 + e) * run.rows] =
+                        make_float4(__uint_as_float(o[4 * e]) * a.alpha, __uint_as_float(o[4 * e + 1]) * a.alpha,
+                                    __uint_as_float(o[4 * e + 2]) * a.alpha, __uint_as_float(o[4 * e + 3]) * a.alpha);
             }
         }
-        tc_fence_before();
-        mbar_arrive(&bars[C::kAccFree]);
-        ++nr;
         ring += 2 * (uint32_t)run.blocks;
         e0 += items;
     }
@@ -693,7 +705,7 @@ prefix_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     }
     if (threadIdx.x == 0) {
         for (int b = 0; b < C::kNumBars; ++b)
-            mbar_init(&bars[b], b == C::kPFull || b == C::kPFull + 1 ? 256u : b == C::kAccFree ? 512u : 1u);
+            mbar_init(&bars[b], b == C::kPFull || b == C::kPFull + 1 ? 128u : b == C::kAccFree ? 256u : 1u);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -703,18 +715,23 @@ prefix_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const Abort ab{abort_flag, a.err, a.wait_ns};
-    if (warp == 0) {
-        if (lane == 0) dq_producer<D>(&tmQ, &tmDO, &tmKp, &tmVp, &tmK, &tmV, a, smem, bars, seg0, seg1, ab);
-        __syncwarp();
-    } else if (warp == 1) {
-        if (elect_one()) {
-            dq_mma<D>(a, smem, bars, tmem, seg0, seg1, ab);
-            // all of its products complete before TMEM is released
-            one_commit(&bars[C::kMmaDone]);
-            mbar_wait_teardown(&bars[C::kMmaDone], 0);
+    // 384 threads start with 168 registers: 88 + 2 * 208 a triple
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 0) {
+            if (lane == 0) dq_producer<D>(&tmQ, &tmDO, &tmKp, &tmVp, &tmK, &tmV, a, smem, bars, seg0, seg1, ab);
+            __syncwarp();
+        } else if (warp == 1) {
+            if (elect_one()) {
+                dq_mma<D>(a, smem, bars, tmem, seg0, seg1, ab);
+                // all of its products complete before TMEM is released
+                one_commit(&bars[C::kMmaDone]);
+                mbar_wait_teardown(&bars[C::kMmaDone], 0);
+            }
+            __syncwarp();
         }
-        __syncwarp();
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         dq_rows<D, ACT>(a, smem, bars, tmem, seg0, seg1, ab);
     }
     tc_fence_before();

@@ -88,7 +88,6 @@ struct Walk {
     __device__ __forceinline__ int blocks(int s) const { return s ? n1 : n0; }
     __device__ __forceinline__ int block(int s, int j) const { return dual ? 2 * j + s : j; }
     // two tiles: K0 V0 K1 V1 ...; one tile: K0 K1 V0 K2 V1 K3 ...
-    __device__ __forceinline__ int k_at(int b) const { return dual ? (b < 2 ? b : 2 * b - 1) : 2 * b; }
     __device__ __forceinline__ int v_at(int b) const { return dual ? min(b + 2, nb) + b : 2 * b + 1; }
 };
 
