@@ -36,6 +36,7 @@ namespace {
 using namespace tc;
 
 constexpr int kThreads = 384;   // producer and issuer (and two idle warps), a warpgroup per slot
+constexpr int kKvThreads = 512; // and one that drains dK and dV
 constexpr int kHalfBytes = 128 * 128;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kItem = 64;   // columns of an item
@@ -91,10 +92,10 @@ template <int D>
 struct KvCfg {
     static constexpr int kHalves = D / 64;
     static constexpr int kTile = 128 * D * 2;
-    static constexpr int kOffK = 0, kOffV = kTile, kOffQ = 2 * kTile, kOffDO = 4 * kTile;   // Q, dO: 2 stages
-    static constexpr int kOffStat = 6 * kTile;   // [8 warps][2][64] (lse, delta) pairs
+    static constexpr int kPair = 2 * kTile;      // K and V of a unit, or Q and dO of a tile; 3 of them
+    static constexpr int kOffStat = 3 * kPair;   // [8 warps][2][64] (lse, delta) pairs
     static constexpr int kOffBar = kOffStat + 8 * 2 * 64 * 8;
-    enum { kKVFull = 0, kKVEmpty, kFull, kEmpty = kFull + 2, kSDFull = kEmpty + 2, kPFull = kSDFull + 2,
+    enum { kFull = 0, kEmpty = kFull + 3, kSDFull = kEmpty + 3, kPFull = kSDFull + 2,
            kAccFull = kPFull + 2, kAccFree, kMmaDone, kNumBars };
     static constexpr int kSmem = kOffBar + kNumBars * 8 + 16 + 1024;
 };
@@ -104,126 +105,184 @@ __device__ __forceinline__ int tile_rows(const PrefixUnit& u, const BwArgs& a, i
     return min(a.tpt, u.ntok - m * a.tpt) * a.r;
 }
 
+// Items of a unit (0: no row sees its keys).
+__device__ __forceinline__ int unit_items(const PrefixUnit& u, const BwArgs& a, int full) {
+    const int tiles = (u.ntok + a.tpt - 1) / a.tpt;
+    return tiles == 0 ? 0 : (tiles - 1) * full + (tile_rows(u, a, tiles - 1) + kItem - 1) / kItem;
+}
+
+// Which of the three pairs of buffers hold a unit's keys and its tiles (in
+// turn).  The next unit's keys go where no recent tile is, so that they load
+// while this unit is worked on; its first tile where this unit's keys were.
+struct Places {
+    uint32_t kv = 0, x = 1, y = 2;
+    __device__ __forceinline__ uint32_t tile(int m) const { return m & 1 ? y : x; }
+    __device__ __forceinline__ void next(int tiles) {
+        const uint32_t last = tiles & 1 ? x : y, other = tiles & 1 ? y : x;
+        x = kv;
+        kv = other;
+        y = last;
+    }
+};
+
 template <int D>
 __device__ __forceinline__ void kv_producer(const CUtensorMap* tmQ, const CUtensorMap* tmDO, const CUtensorMap* tmKp,
-                            const CUtensorMap* tmVp, const CUtensorMap* tmK, const CUtensorMap* tmV,
-                            const BwArgs& a, uint8_t* smem, uint64_t* bars, int seg0, int seg1,
-                            const Abort& ab) {
+                                            const CUtensorMap* tmVp, const CUtensorMap* tmK, const CUtensorMap* tmV,
+                                            const BwArgs& a, uint8_t* smem, uint64_t* bars, int seg0, int seg1,
+                                            const Abort& ab) {
     using C = KvCfg<D>;
     const uint64_t keep = policy_evict_last(), once = policy_evict_first();
-    int32_t kv_armed = -1, armed[2] = {-1, -1};
-    uint32_t nu = 0, i = 0;
+    int32_t armed[3] = {-1, -1, -1};
+    uint32_t ph = 7;   // per pair: the parity of "empty" to wait for
+    Places at;
+    // a pair is free: arm it for the next load
+    auto take = [&](uint32_t pair, uint32_t bytes) -> bool {
+        if (!mbar_wait<true>(&bars[C::kEmpty + pair], (ph >> pair) & 1, ab, 81)) return false;
+        ph ^= 1u << pair;
+        mbar_arrive_expect_tx(&bars[C::kFull + pair], bytes);
+        armed[pair] = (int32_t)((ph >> pair) & 1);
+        return true;
+    };
     for (int t = seg0; t < seg1; ++t) {
         const PrefixUnit u = load_unit(a.units + t);
         const int tiles = (u.ntok + a.tpt - 1) / a.tpt;
         if (tiles == 0) continue;
-        if (!mbar_wait<true>(&bars[C::kKVEmpty], (nu & 1) ^ 1, ab, 81)) goto unwind;
-        mbar_arrive_expect_tx(&bars[C::kKVFull], 2 * C::kTile);
-        kv_armed = (int32_t)(nu & 1);
-        {
-            const bool own = u.flags & kPieceOwn;
-            const CUtensorMap *mk = own ? tmK : tmKp, *mv = own ? tmV : tmVp;
+        const bool own = u.flags & kPieceOwn;
+        const CUtensorMap *mk = own ? tmK : tmKp, *mv = own ? tmV : tmVp;
+        if (!take(at.kv, 2 * C::kTile)) goto unwind;
+#pragma unroll
+        for (int hf = 0; hf < C::kHalves; ++hf) {
+            uint8_t* dst = smem + at.kv * C::kPair + hf * kHalfBytes;
+            tma_load_2d(mk, &bars[C::kFull + at.kv], dst, u.hk * D + hf * 64, u.k0, once);
+            tma_load_2d(mv, &bars[C::kFull + at.kv], dst + C::kTile, u.hk * D + hf * 64, u.k0, once);
+        }
+        for (int m = 0; m < tiles; ++m) {
+            const uint32_t pair = at.tile(m);
+            if (!take(pair, 2 * (uint32_t)a.q_bytes)) goto unwind;
 #pragma unroll
             for (int hf = 0; hf < C::kHalves; ++hf) {
-                tma_load_2d(mk, &bars[C::kKVFull], smem + C::kOffK + hf * kHalfBytes, u.hk * D + hf * 64,
-                            u.k0, once);
-                tma_load_2d(mv, &bars[C::kKVFull], smem + C::kOffV + hf * kHalfBytes, u.hk * D + hf * 64,
-                            u.k0, once);
+                uint8_t* dst = smem + pair * C::kPair + hf * kHalfBytes;
+                tma_load_3d(tmQ, &bars[C::kFull + pair], dst, hf * 64, u.hk * a.r, u.tok + m * a.tpt, keep);
+                tma_load_3d(tmDO, &bars[C::kFull + pair], dst + C::kTile, hf * 64, u.hk * a.r, u.tok + m * a.tpt, keep);
             }
         }
-        for (int m = 0; m < tiles; ++m, ++i) {
-            const uint32_t st = i & 1, ph = (i >> 1) & 1;
-            if (!mbar_wait<true>(&bars[C::kEmpty + st], ph ^ 1, ab, 82)) goto unwind;
-            mbar_arrive_expect_tx(&bars[C::kFull + st], 2 * (uint32_t)a.q_bytes);
-            armed[st] = (int32_t)ph;
-#pragma unroll
-            for (int hf = 0; hf < C::kHalves; ++hf) {
-                tma_load_3d(tmQ, &bars[C::kFull + st], smem + C::kOffQ + st * C::kTile + hf * kHalfBytes, hf * 64,
-                      u.hk * a.r, u.tok + m * a.tpt, keep);
-                tma_load_3d(tmDO, &bars[C::kFull + st], smem + C::kOffDO + st * C::kTile + hf * kHalfBytes, hf * 64,
-                      u.hk * a.r, u.tok + m * a.tpt, keep);
-            }
-        }
-        ++nu;
+        at.next(tiles);
     }
 unwind:
-    if (kv_armed >= 0) mbar_wait_teardown(&bars[C::kKVFull], (uint32_t)kv_armed);
-    for (int s = 0; s < 2; ++s)
+    // never leave the CTA with a TMA write still in flight
+    for (int s = 0; s < 3; ++s)
         if (armed[s] >= 0) mbar_wait_teardown(&bars[C::kFull + s], (uint32_t)armed[s]);
 }
+
+// A walk over the items of a CTA's units, for the issuer: it runs one for the
+// scores and, two items behind, one for the sums, across units.
+struct ItemWalk {
+    PrefixUnit u;
+    Places at;
+    int t, tiles, items, x, last_rows;
+    __device__ __forceinline__ void load(const BwArgs& a, int full, int seg1) {
+        for (; t < seg1; ++t) {   // units without rows have no items
+            u = load_unit(a.units + t);
+            tiles = (u.ntok + a.tpt - 1) / a.tpt;
+            if (tiles > 0) break;
+        }
+        x = 0;
+        if (t < seg1) {
+            last_rows = tile_rows(u, a, tiles - 1);
+            items = (tiles - 1) * full + (last_rows + kItem - 1) / kItem;
+        }
+    }
+    __device__ __forceinline__ bool last() const { return x == items - 1; }
+    __device__ __forceinline__ void next(const BwArgs& a, int full, int seg1) {
+        if (++x < items) return;
+        at.next(tiles);
+        ++t;
+        load(a, full, seg1);
+    }
+};
 
 // The issuer (one lane).
 template <int D>
 __device__ __forceinline__ void kv_mma(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t tmem, int seg0,
                                        int seg1, const Abort& ab) {
     using C = KvCfg<D>;
-    constexpr uint32_t idesc_acc = idesc_bf16(128, D, false, true), idesc_full = idesc_bf16(128, kItem, false, false);
-    constexpr uint64_t kTileDesc = C::kTile >> 4, kItemDesc = (kItem * 128) >> 4;
-    const uint64_t kd = smem_desc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
-    const uint64_t vd = smem_desc_sw128(smem_u32(smem + C::kOffV), 16, 1024);
-    const uint64_t q_k = smem_desc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
-    const uint64_t q_mn = smem_desc_sw128(smem_u32(smem + C::kOffQ), kHalfBytes, 1024);
-    constexpr uint64_t kDO = (C::kOffDO - C::kOffQ) >> 4;
-    const int full = a.tpt * a.r > kItem ? 2 : 1;   // items of every tile but the last
-    // places of the item whose scores come next (A) and whose sums do (B): its
-    // tile's stage, its half of the tile, its slot's parity
-    RingAt<2> tileA, tileB;
-    uint32_t slotA = 0, slotB = 0, p_ph = 0, kv_ph = 0, acc_ph = 1;
-    for (int t = seg0; t < seg1; ++t) {
-        const PrefixUnit u = load_unit(a.units + t);
-        const int tiles = (u.ntok + a.tpt - 1) / a.tpt;
-        if (tiles == 0) continue;
-        const int last_rows = tile_rows(u, a, tiles - 1);
-        const int items = (tiles - 1) * full + (last_rows + kItem - 1) / kItem;
-        const uint32_t last16 = (uint32_t)((last_rows - (last_rows > kItem ? kItem : 0) + 15) & ~15);
-        const uint32_t idesc_last = idesc_bf16(128, last16, false, false);
-        // (a full tile's second item may be short too: tpt * r rows)
-        const uint32_t tail16 = full == 2 ? (uint32_t)((a.tpt * a.r - kItem + 15) & ~15) : 64u;
-        const uint32_t idesc_tail = idesc_bf16(128, tail16, false, false);
-        uint32_t halfA = 0, halfB = 0;
-        auto scores = [&](int x) -> bool {
-            if (halfA == 0 && !mbar_wait<true>(&bars[C::kFull + tileA.st], tileA.ph, ab, 84)) return false;
-            tc_fence_after();
-            const uint64_t off = tileA.st * kTileDesc + halfA * kItemDesc;
-            const uint32_t id = x == items - 1 ? idesc_last : halfA ? idesc_tail : idesc_full;
-            const uint32_t col = tmem + slotA * 128;
-            one_scores<D>(col, kd, q_k + off, id);
-            one_scores<D>(col + 64, vd, q_k + kDO + off, id);
-            one_commit(&bars[C::kSDFull + slotA]);
-            if (x == items - 1) one_commit(&bars[C::kKVEmpty]);
-            slotA ^= 1;
-            if (++halfA == (uint32_t)full || x == items - 1) {
-                halfA = 0;
-                tileA.next();
-            }
-            return true;
-        };
-        if (!mbar_wait<true>(&bars[C::kKVFull], kv_ph, ab, 83)) return;
-        kv_ph ^= 1;
-        if (!scores(0) || (items > 1 && !scores(1))) return;
-        for (int x = 0; x < items; ++x) {
-            if (x == 0) {
-                if (!mbar_wait<true>(&bars[C::kAccFree], acc_ph, ab, 85)) return;
-                acc_ph ^= 1;
-            }
-            if (!mbar_wait<true>(&bars[C::kPFull + slotB], p_ph, ab, 86)) return;
-            tc_fence_after();
-            const uint64_t off = q_mn + tileB.st * kTileDesc + halfB * kItemDesc;
-            const uint32_t steps = (x == items - 1 ? last16 : halfB ? tail16 : 64u) >> 4;
-            const uint32_t col = tmem + slotB * 128;
-            one_sums(tmem + 256, col, col + 16, off + kDO, idesc_acc, steps, x > 0);
-            one_sums(tmem + 384, col + 64, col + 80, off, idesc_acc, steps, x > 0);
-            p_ph ^= slotB;
-            slotB ^= 1;
-            if (++halfB == (uint32_t)full || x == items - 1) {
-                one_commit(&bars[C::kEmpty + tileB.st]);
-                halfB = 0;
-                tileB.next();
-            }
-            if (x == items - 1) one_commit(&bars[C::kAccFull]);
-            if (x + 2 < items && !scores(x + 2)) return;
+    constexpr uint32_t idesc_acc = idesc_bf16(128, D, false, true);
+    constexpr uint64_t kPairDesc = C::kPair >> 4, kTileDesc = C::kTile >> 4, kItemDesc = (kItem * 128) >> 4;
+    const uint64_t k_major = smem_desc_sw128(smem_u32(smem), 16, 1024);
+    const uint64_t mn_major = smem_desc_sw128(smem_u32(smem), kHalfBytes, 1024);
+    const int full = a.tpt * a.r > kItem ? 2 : 1;   // items of every tile but a unit's last
+    // rows of an item, in 16s
+    auto rows16 = [&](const ItemWalk& w, int half) {
+        const int n = w.x >= (w.tiles - 1) * full ? w.last_rows : a.tpt * a.r;
+        return (uint32_t)((min(kItem, n - half * kItem) + 15) & ~15);
+    };
+    ItemWalk A, B;
+    A.t = B.t = seg0;
+    A.load(a, full, seg1);
+    B.load(a, full, seg1);
+    uint32_t slotA = 0, slotB = 0, p_ph = 0, acc_ph = 1, ph = 0;
+    auto landed = [&](uint32_t pair) -> bool {
+        if (!mbar_wait<true>(&bars[C::kFull + pair], (ph >> pair) & 1, ab, 83)) return false;
+        ph ^= 1u << pair;
+        return true;
+    };
+    auto scores = [&]() -> bool {
+        const int m = full == 2 ? A.x >> 1 : A.x, half = full == 2 ? A.x & 1 : 0;
+        const uint32_t pair = A.at.tile(m);
+        if (A.x == 0 && !landed(A.at.kv)) return false;
+        if (half == 0 && !landed(pair)) return false;
+        tc_fence_after();
+        const uint64_t kd = k_major + A.at.kv * kPairDesc, qd = k_major + pair * kPairDesc + half * kItemDesc;
+        const uint32_t id = idesc_bf16(128, rows16(A, half), false, false), col = tmem + slotA * 128;
+        one_scores<D>(col, kd, qd, id);
+        one_scores<D>(col + 64, kd + kTileDesc, qd + kTileDesc, id);
+        one_commit(&bars[C::kSDFull + slotA]);
+        if (A.last()) one_commit(&bars[C::kEmpty + A.at.kv]);
+        slotA ^= 1;
+        A.next(a, full, seg1);
+        return true;
+    };
+    for (int i = 0; i < 2; ++i)
+        if (A.t < seg1 && !scores()) return;
+    while (B.t < seg1) {
+        const int m = full == 2 ? B.x >> 1 : B.x, half = full == 2 ? B.x & 1 : 0;
+        const uint32_t pair = B.at.tile(m), col = tmem + slotB * 128;
+        const bool last = B.last();
+        if (B.x == 0) {   // the accumulators of the unit before have been read
+            if (!mbar_wait<true>(&bars[C::kAccFree], acc_ph, ab, 85)) return;
+            acc_ph ^= 1;
+        }
+        if (!mbar_wait<true>(&bars[C::kPFull + slotB], p_ph, ab, 86)) return;
+        tc_fence_after();
+        const uint64_t qd = mn_major + pair * kPairDesc + half * kItemDesc;
+        const uint32_t steps = rows16(B, half) >> 4;
+        one_sums(tmem + 256, col, col + 16, qd + kTileDesc, idesc_acc, steps, B.x > 0);
+        one_sums(tmem + 384, col + 64, col + 80, qd, idesc_acc, steps, B.x > 0);
+        p_ph ^= slotB;
+        slotB ^= 1;
+        if (half == full - 1 || last) one_commit(&bars[C::kEmpty + pair]);
+        if (last) one_commit(&bars[C::kAccFull]);
+        B.next(a, full, seg1);
+        if (A.t < seg1 && !scores()) return;
+    }
+}
+
+// The (lse, delta) of row 32 half + lane of item x of a unit.
+template <bool kSm>
+__device__ __forceinline__ float2 row_stats(const PrefixUnit& u, const BwArgs& a, int full, int items, int x,
+                                            int half, int lane) {
+    float2 v = make_float2(INFINITY, 0.0f);
+    if (kSm && x < items) {
+        const int m = full == 2 ? x >> 1 : x, row = (full == 2 ? (x & 1) * kItem : 0) + 32 * half + lane;
+        if (row < tile_rows(u, a, m)) {
+            const int tt = row / a.r;
+            const int64_t at = (int64_t)(u.tok + m * a.tpt + tt) * a.H + u.hk * a.r + (row - tt * a.r);
+            const float l = a.lse[at];
+            v.x = l == -INFINITY ? INFINITY : l * kLog2e;   // a row without keys: weights 0
+            v.y = a.delta[at];
         }
     }
+    return v;
 }
 
 template <int D, int ACT>
@@ -234,50 +293,29 @@ __device__ __forceinline__ void kv_rows(const BwArgs& a, uint8_t* smem, uint64_t
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int s = (warp - 4) >> 2, quarter = warp & 3;
     const int key = quarter * 32 + lane;   // TMEM lane
-    const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t col = trow + s * 128;
+    const uint32_t col = tmem + ((uint32_t)(quarter * 32) << 16) + s * 128;
     // a warp's row statistics, two items' in turn
     float2* stat = reinterpret_cast<float2*>(smem + C::kOffStat) + (warp - 4) * 128;
     const ActScale ks = act_scale<ACT>(a.alpha);
     const int full = a.tpt * a.r > kItem ? 2 : 1;
-    uint32_t acc_ph = 0, tile0 = 0, e0 = 0;
+    uint32_t e0 = 0;
+    Places at;
     PrefixUnit u = load_unit(a.units + seg0);
+    int items = unit_items(u, a, full);
+    // the statistics of this slot's next item, on their way while the one
+    // before it is worked on
+    float2 next0 = row_stats<kSm>(u, a, full, items, s, 0, lane);
+    float2 next1 = row_stats<kSm>(u, a, full, items, s, 1, lane);
     for (int t = seg0; t < seg1; ++t) {
         const PrefixUnit coming = load_unit(a.units + min(t + 1, seg1 - 1));
-        const bool own = u.flags & kPieceOwn;
-        const int tiles = (u.ntok + a.tpt - 1) / a.tpt;
-        __nv_bfloat16* dst = s ? (own ? a.dk : a.dkp) : (own ? a.dv : a.dvp);
-        dst += ((int64_t)(u.k0 + key) * a.Hkv + u.hk) * D;
-        const bool real = key < u.nk;
-        if (tiles == 0) {   // keys that no row sees
-            if (real)
-                for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(dst)[c] = make_uint4(0u, 0u, 0u, 0u);
-            u = coming;
-            continue;
-        }
-        const int items = (tiles - 1) * full + (tile_rows(u, a, tiles - 1) + kItem - 1) / kItem;
-        const bool banded = own && a.windowed;
+        const bool banded = (u.flags & kPieceOwn) && a.windowed;
         const int jpos = u.j0 + key;
-        auto stats = [&](int xi, int half) -> float2 {   // of row 32 half + lane of item xi
-            float2 v = make_float2(INFINITY, 0.0f);
-            if (kSm && xi < items) {
-                const int m = full == 2 ? xi >> 1 : xi, row = (full == 2 ? (xi & 1) * kItem : 0) + 32 * half + lane;
-                if (row < tile_rows(u, a, m)) {
-                    const int tt = row / a.r;
-                    const int64_t at = (int64_t)(u.tok + m * a.tpt + tt) * a.H + u.hk * a.r + (row - tt * a.r);
-                    const float l = a.lse[at];
-                    v.x = l == -INFINITY ? INFINITY : l * kLog2e;   // a row without keys: weights 0
-                    v.y = a.delta[at];
-                }
-            }
-            return v;
-        };
         // this slot's items of the unit: those with e0 + x of its parity
         int x = (int)((e0 ^ (uint32_t)s) & 1);
-        float2 next0 = make_float2(INFINITY, 0.0f), next1 = next0;
-        if (kSm) {
-            next0 = stats(x, 0);
-            next1 = stats(x, 1);
+        const int coming_items = unit_items(coming, a, full), coming_x = (int)((e0 + items) ^ (uint32_t)s) & 1;
+        if (x >= items) {   // none: the next unit's instead
+            next0 = row_stats<kSm>(coming, a, full, coming_items, coming_x, 0, lane);
+            next1 = row_stats<kSm>(coming, a, full, coming_items, coming_x, 1, lane);
         }
         for (; x < items; x += 2) {
             const uint32_t e = e0 + x;
@@ -287,8 +325,11 @@ __device__ __forceinline__ void kv_rows(const BwArgs& a, uint8_t* smem, uint64_t
             if (kSm) {
                 sb[lane] = next0;
                 sb[32 + lane] = next1;
-                next0 = stats(x + 2, 0);
-                next1 = stats(x + 2, 1);
+                const bool more = x + 2 < items;
+                next0 = row_stats<kSm>(more ? u : coming, a, full, more ? items : coming_items, more ? x + 2 : coming_x,
+                                       0, lane);
+                next1 = row_stats<kSm>(more ? u : coming, a, full, more ? items : coming_items, more ? x + 2 : coming_x,
+                                       1, lane);
                 __syncwarp();
             }
             if (!wg_wait<true>(&bars[C::kSDFull + s], (e >> 1) & 1, ab, 91)) return;
@@ -300,82 +341,109 @@ __device__ __forceinline__ void kv_rows(const BwArgs& a, uint8_t* smem, uint64_t
                 lo = (int)max((int64_t)0, first);
                 hi = (int)max((int64_t)0, min((int64_t)n, first + (int64_t)a.window * a.r));
             }
-            uint32_t sv[64], pv[64];
+#pragma unroll 1
+            for (int c0 = 0; c0 < 64; c0 += 32) {   // (registers, and half the code)
+                uint32_t sv[32], pv[32];
+                tmem_ld32(col + c0, sv);
+                tmem_ld32(col + 64 + c0, pv);
+                tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < 64; c += 32) {
-                tmem_ld32(col + c, *reinterpret_cast<uint32_t(*)[32]>(sv + c));
-                tmem_ld32(col + 64 + c, *reinterpret_cast<uint32_t(*)[32]>(pv + c));
-            }
-            tmem_ld_wait();
+                for (int c = 0; c < 32; c += 16) {
+                    uint32_t pk[8], dk8[8];
 #pragma unroll
-            for (int c = 0; c < 64; c += 16) {
-                uint32_t pk[8], dk8[8];
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    float l0 = 0.f, l1 = 0.f, d0 = 0.f, d1 = 0.f, p0, p1, g0, g1;
-                    if constexpr (kSm) {
-                        const float4 st = *reinterpret_cast<const float4*>(sb + c + i);
-                        l0 = st.x; d0 = st.y; l1 = st.z; d1 = st.w;
+                    for (int i = 0; i < 16; i += 2) {
+                        float l0 = 0.f, l1 = 0.f, d0 = 0.f, d1 = 0.f, p0, p1, g0, g1;
+                        if constexpr (kSm) {
+                            const float4 st = *reinterpret_cast<const float4*>(sb + c0 + c + i);
+                            l0 = st.x; d0 = st.y; l1 = st.z; d1 = st.w;
+                        }
+                        weights2<ACT>(__uint_as_float(sv[c + i]), __uint_as_float(sv[c + i + 1]),
+                                      __uint_as_float(pv[c + i]), __uint_as_float(pv[c + i + 1]), ks, l0, l1, d0,
+                                      d1, p0, p1, g0, g1);
+                        if (cut) {
+                            const int j = c + i, lo0 = lo - c0, hi0 = hi - c0;
+                            const bool ok0 = j >= lo0 && j < hi0, ok1 = j + 1 >= lo0 && j + 1 < hi0;
+                            p0 = ok0 ? p0 : 0.0f;
+                            g0 = ok0 ? g0 : 0.0f;
+                            p1 = ok1 ? p1 : 0.0f;
+                            g1 = ok1 ? g1 : 0.0f;
+                        }
+                        pk[i >> 1] = pack_bf16x2(p0, p1);
+                        dk8[i >> 1] = pack_bf16x2(g0, g1);
                     }
-                    weights2<ACT>(__uint_as_float(sv[c + i]), __uint_as_float(sv[c + i + 1]),
-                                  __uint_as_float(pv[c + i]), __uint_as_float(pv[c + i + 1]), ks, l0, l1, d0, d1,
-                                  p0, p1, g0, g1);
-                    if (cut) {
-                        const bool ok0 = c + i >= lo && c + i < hi, ok1 = c + i + 1 >= lo && c + i + 1 < hi;
-                        p0 = ok0 ? p0 : 0.0f;
-                        g0 = ok0 ? g0 : 0.0f;
-                        p1 = ok1 ? p1 : 0.0f;
-                        g1 = ok1 ? g1 : 0.0f;
-                    }
-                    pk[i >> 1] = pack_bf16x2(p0, p1);
-                    dk8[i >> 1] = pack_bf16x2(g0, g1);
+                    tmem_st8(col + (c0 + c) / 2, pk);   // over scores that have been read
+                    tmem_st8(col + 64 + (c0 + c) / 2, dk8);
                 }
-                tmem_st8(col + c / 2, pk);   // over scores that have been read
-                tmem_st8(col + 64 + c / 2, dk8);
             }
             tmem_st_wait();
             if (n & 15) {
-                const uint32_t st = (tile0 + m) & 1;
-                clear_rows<D>(smem + C::kOffQ + st * C::kTile, r0 + n, r0 + ((n + 15) & ~15), key);
-                clear_rows<D>(smem + C::kOffDO + st * C::kTile, r0 + n, r0 + ((n + 15) & ~15), key);
+                uint8_t* rows = smem + at.tile(m) * C::kPair;
+                clear_rows<D>(rows, r0 + n, r0 + ((n + 15) & ~15), key);
+                clear_rows<D>(rows + C::kTile, r0 + n, r0 + ((n + 15) & ~15), key);
                 fence_proxy_async_smem();
             }
             tc_fence_before();
             mbar_arrive(&bars[C::kPFull + s]);
         }
-        if (!wg_wait<true>(&bars[C::kAccFull], acc_ph, ab, 92)) return;
-        acc_ph ^= 1;
+        if (items > 0) at.next((u.ntok + a.tpt - 1) / a.tpt);
+        e0 += items;
+        u = coming;
+        items = coming_items;
+    }
+}
+
+// The units' dV and dK from TMEM to memory (a warpgroup of its own: short
+// units would otherwise wait for it before their weights).
+template <int D>
+__device__ __forceinline__ void kv_drain(const BwArgs& a, uint64_t* bars, uint32_t tmem, int seg0, int seg1,
+                                         const Abort& ab) {
+    using C = KvCfg<D>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quarter = warp & 3;
+    const int key = quarter * 32 + lane;
+    const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
+    uint32_t ph = 0;
+    for (int t = seg0; t < seg1; ++t) {
+        const PrefixUnit u = load_unit(a.units + t);
+        const bool own = u.flags & kPieceOwn, real = key < u.nk;
+        const int64_t at = ((int64_t)(u.k0 + key) * a.Hkv + u.hk) * D;
+        __nv_bfloat16 *dv = (own ? a.dv : a.dvp) + at, *dk = (own ? a.dk : a.dkp) + at;
+        if (u.ntok == 0) {   // keys that no row sees
+            if (real)
+                for (int c = 0; c < D / 8; ++c)
+                    reinterpret_cast<uint4*>(dv)[c] = reinterpret_cast<uint4*>(dk)[c] = make_uint4(0u, 0u, 0u, 0u);
+            continue;
+        }
+        if (!wg_wait<true>(&bars[C::kAccFull], ph, ab, 92)) return;
+        ph ^= 1;
         tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < D; c += 64) {   // slot 0: dV, slot 1: dK
-            uint32_t v[64];
-            tmem_ld32(trow + 256 + 128 * s + c, *reinterpret_cast<uint32_t(*)[32]>(v));
-            tmem_ld32(trow + 256 + 128 * s + c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+#pragma unroll 1
+        for (int x = 0; x < 2 * D; x += 32) {
+            const bool second = x >= D;
+            const int c = second ? x - D : x;
+            uint32_t v[32];
+            tmem_ld32(trow + (second ? 384 : 256) + c, v);
             tmem_ld_wait();
-            if (c + 64 == D) {
+            if (x + 32 == 2 * D) {
                 tc_fence_before();
                 mbar_arrive(&bars[C::kAccFree]);
             }
-            const float f = s ? a.alpha : 1.0f;
+            const float f = second ? a.alpha : 1.0f;
             if (real) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < 4; ++i) {
                     uint32_t o[4];
 #pragma unroll
                     for (int w = 0; w < 4; ++w)
                         o[w] = pack_bf16x2(__uint_as_float(v[8 * i + 2 * w]) * f, __uint_as_float(v[8 * i + 2 * w + 1]) * f);
-                    reinterpret_cast<uint4*>(dst + c)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+                    reinterpret_cast<uint4*>((second ? dk : dv) + c)[i] = make_uint4(o[0], o[1], o[2], o[3]);
                 }
             }
         }
-        tile0 += tiles;
-        e0 += items;
-        u = coming;
     }
 }
 
 template <int D, int ACT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kKvThreads, 1)
 prefix_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
                   const __grid_constant__ CUtensorMap tmKp, const __grid_constant__ CUtensorMap tmVp,
                   const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -395,7 +463,7 @@ prefix_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     }
     if (threadIdx.x == 0) {
         for (int b = 0; b < C::kNumBars; ++b)
-            mbar_init(&bars[b], b == C::kPFull || b == C::kPFull + 1 ? 128u : b == C::kAccFree ? 256u : 1u);
+            mbar_init(&bars[b], b == C::kPFull || b == C::kPFull + 1 ? 128u : b == C::kAccFree ? 128u : 1u);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -405,9 +473,9 @@ prefix_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const Abort ab{abort_flag, a.err, a.wait_ns};
-    // 384 threads start with 168 registers: 88 + 2 * 208 a triple
+    // 512 threads start with 128 registers: 2 * 80 + 2 * 176 four of them
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (warp == 0) {
             if (lane == 0) kv_producer<D>(&tmQ, &tmDO, &tmKp, &tmVp, &tmK, &tmV, a, smem, bars, seg0, seg1, ab);
             __syncwarp();
@@ -420,8 +488,11 @@ prefix_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             }
             __syncwarp();
         }
+    } else if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        kv_drain<D>(a, bars, tmem, seg0, seg1, ab);
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         kv_rows<D, ACT>(a, smem, bars, tmem, seg0, seg1, ab);
     }
     tc_fence_before();
@@ -744,10 +815,10 @@ prefix_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 }
 
 template <typename K>
-gdpa_status go(K kern, int smem, std::atomic<uint64_t>& done, PrefixPlan& p, const CUtensorMap* m, const BwArgs& a,
+gdpa_status go(K kern, int threads, int smem, std::atomic<uint64_t>& done, PrefixPlan& p, const CUtensorMap* m, const BwArgs& a,
                cudaStream_t st) {
     if (!allow_smem(kern, smem, p.device, done)) return GDPA_ERR_CUDA;
-    const bool ok = launch_kernel(kern, dim3((unsigned)p.S), kThreads, smem, st, p.chain > 0, m[0], m[1], m[2], m[3],
+    const bool ok = launch_kernel(kern, dim3((unsigned)p.S), threads, smem, st, p.chain > 0, m[0], m[1], m[2], m[3],
                                   m[4], m[5], a);
     p.launches += 1;
     p.chain += 1;
@@ -760,12 +831,12 @@ gdpa_status launch(PrefixPlan& p, const CUtensorMap* m, BwArgs& a, cudaStream_t 
     if (p.useg[p.S] > 0) {
         a.seg = p.dev_useg();
         static std::atomic<uint64_t> done{0};
-        s = go(prefix_dkv_kernel<D, ACT>, KvCfg<D>::kSmem, done, p, m, a, st);
+        s = go(prefix_dkv_kernel<D, ACT>, kKvThreads, KvCfg<D>::kSmem, done, p, m, a, st);
     }
     if (s == GDPA_OK && p.seg[p.S] > 0) {
         a.seg = p.dev_seg();
         static std::atomic<uint64_t> done{0};
-        s = go(prefix_dq_kernel<D, ACT>, DqCfg<D>::kSmem, done, p, m, a, st);
+        s = go(prefix_dq_kernel<D, ACT>, kThreads, DqCfg<D>::kSmem, done, p, m, a, st);
     }
     return s;
 }
