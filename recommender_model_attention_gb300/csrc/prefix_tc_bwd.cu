@@ -15,14 +15,29 @@
 // would move more bytes through L2 than all operands, in an order that
 // changes the sums from run to run.  Results here are the same bits every time.
 //
-// Both walk items of 64 columns (query rows, or keys): two slots of TMEM
-// columns [S | dP], a warpgroup each, thread = lane, whose 128 scores are read
-// at once into registers that the first warpgroup has handed over.  While one slot's weights
-// are computed the tensor core runs the other slot's products and the next
-// scores: item e's closing products, then S and dP of item e + 2 into the same
-// columns.  Rows behind the last one of an item share its 16-row step: their
-// weights are zero by selection, and the rows themselves are cleared in
-// shared memory so that what lies there does not enter as 0 * inf.
+// dK and dV walk items of 64 query rows through two slots of TMEM columns
+// [S^T | dP^T], a warpgroup each, thread = key: while one slot's weights are
+// computed the tensor core runs the other slot's products, then item e's sums
+// and the scores of item e + 2 into the same columns.  The sums leave through
+// a warpgroup of their own, and the next unit's keys load into whichever of
+// three pairs of buffers is free, so that short units follow one another
+// without a gap (32 ragged users of 64 .. 2048 keys: 46 us; with the keys in
+// one place and the two slots' warpgroups storing the sums 65 us).
+// dQ walks blocks of 128 keys: S and dP go into registers at once and the next
+// block's scores into the freed columns, dS into one of two places of its own
+// (99 us against 108 in the form above, 1024 rows x 8192 keys x 16 heads).
+//
+// What bounds them, on those 1024 rows x 8192 keys x 16 heads with GELU: dK
+// and dV 132 us, products 128 x 64 x 16 whose operands take 120 of the 128
+// bytes shared memory gives a cycle, against loads and clears of their own;
+// halving the traffic would take 128-row items, for which TMEM has no room
+// beside 256 columns of sums.  dQ 99 us: 64 KB of K and V a block from L2, 5.4
+// TB/s in all.  Softmax batches of ragged users are bound by the few row tiles
+// a unit has.
+//
+// Rows behind the last one of an item share its 16-row step: their weights are
+// zero by selection, and the rows themselves are cleared in shared memory so
+// that what lies there does not enter as 0 * inf.
 //
 // Every wait is bounded (csrc/tc_common.cuh).
 #include <cuda_bf16.h>
@@ -510,11 +525,15 @@ template <int D>
 struct DqCfg {
     static constexpr int kHalves = D / 64;
     static constexpr int kTile = 128 * D * 2;
-    static constexpr int kStages = D == 128 ? 5 : 8;   // K and V tiles in turn
+    // V and K tiles in turn: V first, as it is done with after the scores and
+    // K only after the sums, so that with 5 places both tiles of a block wait
+    // for ones that were done with a block ago (K first: 109 us, not 99, where
+    // 1024 rows meet 8192 keys in 16 heads)
+    static constexpr int kStages = D == 128 ? 5 : 8;
     static constexpr int kOffQ = 0, kOffDO = kTile, kOffKV = 2 * kTile;
     static constexpr int kOffBar = kOffKV + kStages * kTile;
-    enum { kQFull = 0, kQEmpty, kFull, kEmpty = kFull + kStages, kSDFull = kEmpty + kStages,
-           kPFull = kSDFull + 2, kAccFull = kPFull + 2, kAccFree, kMmaDone, kNumBars };
+    enum { kQFull = 0, kQEmpty, kFull, kEmpty = kFull + kStages, kSDFull = kEmpty + kStages, kSDFree,
+           kPFull, kAccFull = kPFull + 2, kAccFree, kMmaDone, kNumBars };
     static constexpr int kSmem = kOffBar + kNumBars * 8 + 16 + 1024;
 };
 
@@ -537,10 +556,6 @@ struct Run {
     }
     __device__ __forceinline__ int block(int j) const { return first + j * step; }
     __device__ __forceinline__ int keys(int j) const { return min(kBN, nk - block(j) * kBN); }
-    // items of 64 keys: two a block but for a short last one
-    __device__ __forceinline__ int items() const {
-        return blocks == 0 ? 0 : 2 * (blocks - 1) + (keys(blocks - 1) > kItem ? 2 : 1);
-    }
 };
 
 template <int D>
@@ -568,7 +583,7 @@ __device__ __forceinline__ void dq_producer(const CUtensorMap* tmQ, const CUtens
         const bool own = p.flags & kPieceOwn;
         for (int j = 0; j < run.blocks; ++j)
             for (int kv = 0; kv < 2; ++kv, ++c) {
-                const CUtensorMap* map = kv ? (own ? tmV : tmVp) : (own ? tmK : tmKp);
+                const CUtensorMap* map = kv ? (own ? tmK : tmKp) : (own ? tmV : tmVp);
                 const uint32_t st = c % C::kStages, ph = (c / C::kStages) & 1;
                 if (!mbar_wait<true>(&bars[C::kEmpty + st], ph ^ 1, ab, 102)) goto unwind;
                 mbar_arrive_expect_tx(&bars[C::kFull + st], C::kTile);
@@ -591,67 +606,65 @@ template <int D>
 __device__ __forceinline__ void dq_mma(const BwArgs& a, uint8_t* smem, uint64_t* bars, uint32_t tmem, int seg0,
                                        int seg1, const Abort& ab) {
     using C = DqCfg<D>;
-    constexpr uint32_t idesc_acc = idesc_bf16(128, D, false, true), idesc_full = idesc_bf16(128, kItem, false, false);
-    constexpr uint64_t kTileDesc = C::kTile >> 4, kItemDesc = (kItem * 128) >> 4;
+    constexpr uint32_t idesc_acc = idesc_bf16(128, D, false, true), idesc_full = idesc_bf16(128, kBN, false, false);
+    constexpr uint64_t kTileDesc = C::kTile >> 4, kHalfDesc = (64 * 128) >> 4;
     const uint64_t qd = smem_desc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
     const uint64_t dd = smem_desc_sw128(smem_u32(smem + C::kOffDO), 16, 1024);
     const uint64_t kv_k = smem_desc_sw128(smem_u32(smem + C::kOffKV), 16, 1024);
     const uint64_t kv_mn = smem_desc_sw128(smem_u32(smem + C::kOffKV), kHalfBytes, 1024);
-    // ring places of the blocks whose scores come next and whose sums do (K,
-    // with V behind it)
-    RingAt<C::kStages> kA, kB;
-    uint32_t slotA = 0, slotB = 0, p_ph = 0, q_ph = 0, acc_ph = 1;
+    // ring places of the V whose scores come next (its K is behind it) and of
+    // the K whose sums do
+    RingAt<C::kStages> v, kB;
+    kB.next();
+    uint32_t slot = 0, p_ph = 0, q_ph = 0, acc_ph = 1, s_ph = 1;
     for (int t = 2 * seg0; t < 2 * seg1; ++t) {
         const PrefixPiece p = load_piece(a.pieces + (t >> 1));
         const Run run(p, t & 1, a.r);
         if (run.blocks == 0) continue;
-        const int items = run.items();
-        const int last_keys = run.keys(run.blocks - 1);
-        const uint32_t last16 = (uint32_t)((last_keys - (last_keys > kItem ? kItem : 0) + 15) & ~15);
+        const uint32_t last16 = (uint32_t)((run.keys(run.blocks - 1) + 15) & ~15);
         const uint32_t idesc_last = idesc_bf16(128, last16, false, false);
-        auto scores = [&](int x) -> bool {
-            RingAt<C::kStages> v = kA;
-            v.next();
-            if (!(x & 1) && (!mbar_wait<true>(&bars[C::kFull + kA.st], kA.ph, ab, 104) ||
-                             !mbar_wait<true>(&bars[C::kFull + v.st], v.ph, ab, 105)))
+        auto scores = [&](bool last) -> bool {
+            RingAt<C::kStages> k = v;
+            k.next();
+            if (!mbar_wait<true>(&bars[C::kFull + v.st], v.ph, ab, 104) ||
+                !mbar_wait<true>(&bars[C::kFull + k.st], k.ph, ab, 105) ||
+                !mbar_wait<true>(&bars[C::kSDFree], s_ph, ab, 108))
                 return false;
+            s_ph ^= 1;
             tc_fence_after();
-            const uint64_t half = (x & 1) * kItemDesc;
-            const uint32_t col = tmem + slotA * 128, id = x == items - 1 ? idesc_last : idesc_full;
-            one_scores<D>(col, qd, kv_k + kA.st * kTileDesc + half, id);
-            one_scores<D>(col + 64, dd, kv_k + v.st * kTileDesc + half, id);
-            one_commit(&bars[C::kSDFull + slotA]);
-            slotA ^= 1;
-            if ((x & 1) || x == items - 1) {
-                one_commit(&bars[C::kEmpty + v.st]);
-                kA = v;
-                kA.next();
-            }
-            if (x == items - 1) one_commit(&bars[C::kQEmpty]);
+            const uint32_t id = last ? idesc_last : idesc_full;
+            one_scores<D>(tmem, qd, kv_k + k.st * kTileDesc, id);
+            one_scores<D>(tmem + 128, dd, kv_k + v.st * kTileDesc, id);
+            one_commit(&bars[C::kSDFull]);
+            one_commit(&bars[C::kEmpty + v.st]);
+            if (last) one_commit(&bars[C::kQEmpty]);
+            v = k;
+            v.next();
             return true;
         };
         if (!mbar_wait<true>(&bars[C::kQFull], q_ph, ab, 103)) return;
         q_ph ^= 1;
-        if (!scores(0) || (items > 1 && !scores(1))) return;
-        for (int x = 0; x < items; ++x) {
-            if (x == 0) {
+        if (!scores(run.blocks == 1)) return;
+        for (int j = 0; j < run.blocks; ++j) {
+            const bool last = j == run.blocks - 1;
+            if (!last && !scores(j == run.blocks - 2)) return;
+            if (j == 0) {
                 if (!mbar_wait<true>(&bars[C::kAccFree], acc_ph, ab, 106)) return;
                 acc_ph ^= 1;
             }
-            if (!mbar_wait<true>(&bars[C::kPFull + slotB], p_ph, ab, 107)) return;
+            if (!mbar_wait<true>(&bars[C::kPFull + slot], p_ph, ab, 107)) return;
             tc_fence_after();
-            const uint32_t col = tmem + slotB * 128;
-            one_sums(tmem + 256, col, col + 16, kv_mn + kB.st * kTileDesc + (x & 1) * kItemDesc, idesc_acc,
-                     (x == items - 1 ? last16 : 64u) >> 4, x > 0);
-            p_ph ^= slotB;
-            slotB ^= 1;
-            if ((x & 1) || x == items - 1) {
-                one_commit(&bars[C::kEmpty + kB.st]);
-                kB.next();
-                kB.next();
-            }
-            if (x == items - 1) one_commit(&bars[C::kAccFull]);
-            if (x + 2 < items && !scores(x + 2)) return;
+            const uint32_t col = tmem + 384 + slot * 64;
+            const uint64_t kd = kv_mn + kB.st * kTileDesc;
+            const uint32_t steps = (last ? last16 : (uint32_t)kBN) >> 4;
+            one_sums(tmem + 256, col, col + 16, kd, idesc_acc, min(steps, 4u), j > 0);
+            if (steps > 4) one_sums(tmem + 256, col + 32, col + 48, kd + kHalfDesc, idesc_acc, steps - 4, 1);
+            one_commit(&bars[C::kEmpty + kB.st]);
+            if (last) one_commit(&bars[C::kAccFull]);
+            p_ph ^= slot;
+            slot ^= 1;
+            kB.next();
+            kB.next();
         }
     }
 }
@@ -662,18 +675,19 @@ __device__ __forceinline__ void dq_rows(const BwArgs& a, uint8_t* smem, uint64_t
     using C = DqCfg<D>;
     constexpr bool kSm = ACT == kSoftmax;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int s = (warp - 4) >> 2, quarter = warp & 3;
+    const int s = (warp - 4) >> 2, quarter = warp & 3;   // s: which 64 keys of a block
     const int row = quarter * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t col = trow + s * 128;
+    const uint32_t col = trow + s * 64;
     const ActScale ks = act_scale<ACT>(a.alpha);
     const int rt = row / a.r, rj = row - rt * a.r;
-    uint32_t acc_ph = 0, ring = 0, e0 = 0;
+    uint32_t acc_ph = 0, e = 0;
+    RingAt<C::kStages> ring;   // of K
+    ring.next();
     for (int t = 2 * seg0; t < 2 * seg1; ++t) {
         const PrefixPiece p = load_piece(a.pieces + (t >> 1));
         const Run run(p, t & 1, a.r);
         if (run.blocks == 0) continue;
-        const int items = run.items();
         const bool real = row < run.rows;
         const bool banded = (p.flags & kPieceOwn) && a.windowed;
         const int ipos = run.i0 + rt;
@@ -684,57 +698,63 @@ __device__ __forceinline__ void dq_rows(const BwArgs& a, uint8_t* smem, uint64_t
             lse2 = l == -INFINITY ? INFINITY : l * kLog2e;
             delta = a.delta[at];
         }
-        for (int x = (int)((e0 ^ (uint32_t)s) & 1); x < items; x += 2) {
-            const uint32_t e = e0 + x;
-            const int n = min(kItem, run.keys(x >> 1) - (x & 1) * kItem);
-            const bool cut = banded || n < kItem;
+        for (int j = 0; j < run.blocks; ++j, ++e) {
+            const int n = run.keys(j) - s * 64;   // of this warpgroup's 64
+            const bool cut = banded || n < 64;
             int lo = 0, hi = n;   // columns this row sees
             if (banded) {
-                const int at = ipos - (p.j0 + run.block(x >> 1) * kBN + (x & 1) * kItem);
+                const int at = ipos - (p.j0 + run.block(j) * kBN + s * 64);
                 hi = min(hi, at + 1);
                 lo = at >= a.window ? at - a.window + 1 : 0;
             }
-            if (!wg_wait<true>(&bars[C::kSDFull + s], (e >> 1) & 1, ab, 111)) return;
+            if (!wg_wait<true>(&bars[C::kSDFull], e & 1, ab, 111)) return;
             tc_fence_after();
             uint32_t sv[64], pv[64];
 #pragma unroll
             for (int c = 0; c < 64; c += 32) {
                 tmem_ld32(col + c, *reinterpret_cast<uint32_t(*)[32]>(sv + c));
-                tmem_ld32(col + 64 + c, *reinterpret_cast<uint32_t(*)[32]>(pv + c));
+                tmem_ld32(col + 128 + c, *reinterpret_cast<uint32_t(*)[32]>(pv + c));
             }
             tmem_ld_wait();
-#pragma unroll
-            for (int c = 0; c < 64; c += 16) {
-                uint32_t dk8[8];
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    float p0, p1, g0, g1;
-                    weights2<ACT>(__uint_as_float(sv[c + i]), __uint_as_float(sv[c + i + 1]),
-                                  __uint_as_float(pv[c + i]), __uint_as_float(pv[c + i + 1]), ks, lse2, lse2, delta,
-                                  delta, p0, p1, g0, g1);
-                    if (cut) {
-                        if (c + i < lo || c + i >= hi) g0 = 0.0f;
-                        if (c + i + 1 < lo || c + i + 1 >= hi) g1 = 0.0f;
-                    }
-                    dk8[i >> 1] = pack_bf16x2(g0, g1);
-                }
-                tmem_st8(col + c / 2, dk8);   // over scores that have been read
-            }
-            tmem_st_wait();
-            if (n & 15) {
-                const uint32_t sk = (ring + 2 * (uint32_t)(x >> 1)) % C::kStages;
-                const int r0 = (x & 1) * kItem;
-                clear_rows<D>(smem + C::kOffKV + sk * C::kTile, r0 + n, r0 + ((n + 15) & ~15), row);
-                fence_proxy_async_smem();
-            }
             tc_fence_before();
-            mbar_arrive(&bars[C::kPFull + s]);
+            mbar_arrive(&bars[C::kSDFree]);   // the next block's scores may come
+            if (n > 0) {
+                const uint32_t to = trow + 384 + (e & 1) * 64 + s * 32;
+#pragma unroll
+                for (int c = 0; c < 64; c += 16) {
+                    uint32_t dk8[8];
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        float p0, p1, g0, g1;
+                        weights2<ACT>(__uint_as_float(sv[c + i]), __uint_as_float(sv[c + i + 1]),
+                                      __uint_as_float(pv[c + i]), __uint_as_float(pv[c + i + 1]), ks, lse2, lse2,
+                                      delta, delta, p0, p1, g0, g1);
+                        if (cut) {
+                            if (c + i < lo || c + i >= hi) g0 = 0.0f;
+                            if (c + i + 1 < lo || c + i + 1 >= hi) g1 = 0.0f;
+                        }
+                        dk8[i >> 1] = pack_bf16x2(g0, g1);
+                    }
+                    // (the sums two blocks before, which read this place, were
+                    // issued before this block's scores and are complete)
+                    tmem_st8(to + c / 2, dk8);
+                }
+                tmem_st_wait();
+                if (n < 64 && (n & 15)) {
+                    clear_rows<D>(smem + C::kOffKV + ring.st * C::kTile, s * 64 + n, s * 64 + ((n + 15) & ~15), row);
+                    fence_proxy_async_smem();
+                }
+            }
+            ring.next();
+            ring.next();
+            tc_fence_before();
+            mbar_arrive(&bars[C::kPFull + (e & 1)]);
         }
         if (!wg_wait<true>(&bars[C::kAccFull], acc_ph, ab, 112)) return;
         acc_ph ^= 1;
         tc_fence_after();
         float4* out = reinterpret_cast<float4*>(a.parts) + (int64_t)run.part * (D / 4) + row;
-        {   // this slot's half of the columns
+        {   // this warpgroup's half of the columns
             const int c0 = s * (D / 2);
             uint32_t o[D / 2];
 #pragma unroll
@@ -750,8 +770,6 @@ __device__ __forceinline__ void dq_rows(const BwArgs& a, uint8_t* smem, uint64_t
                                     __uint_as_float(o[4 * e + 2]) * a.alpha, __uint_as_float(o[4 * e + 3]) * a.alpha);
             }
         }
-        ring += 2 * (uint32_t)run.blocks;
-        e0 += items;
     }
 }
 
@@ -776,7 +794,7 @@ prefix_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     }
     if (threadIdx.x == 0) {
         for (int b = 0; b < C::kNumBars; ++b)
-            mbar_init(&bars[b], b == C::kPFull || b == C::kPFull + 1 ? 128u : b == C::kAccFree ? 256u : 1u);
+            mbar_init(&bars[b], b == C::kPFull || b == C::kPFull + 1 || b == C::kSDFree || b == C::kAccFree ? 256u : 1u);
         *abort_flag = 0;
         fence_mbar_init();
     }
