@@ -254,6 +254,12 @@ gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t
     for (PrefixPiece& q : p.pieces) q.pad = 0;
     for (const Unit& u : small_units) p.pieces.push_back(u.p);
     p.n_part_rows = parts;
+    p.row_blocks = 0;
+    for (const PrefixPiece& q : p.pieces) {
+        const int32_t second = q.flags & kPieceDual ? q.nA : q.nB;
+        if (q.part0 >= 0) p.row_blocks += cdiv((int64_t)q.nA * p.r, 32);
+        if (q.part1 >= 0) p.row_blocks += cdiv((int64_t)second * p.r, 32);
+    }
 
     // backward: one unit per 128-key block, against all rows that see it
     p.units.clear();

@@ -3,9 +3,11 @@
 // merge of the parts, which both families share.
 //
 // Forward and dQ walk the plan's pieces: a block of 4 warps takes 32 rows of
-// one slot of a piece, 8 rows a warp, and streams its keys through shared
-// memory 32 at a time; a lane owns one key of the scores and four columns of
-// the sums.  Forward keeps a running maximum and sum per row.  dK and dV walk
+// one slot of a piece, 8 rows a warp (or 8 rows, 2 a warp), and streams its
+// keys through shared memory 32 at a time; a lane owns one key of the scores,
+// and for the sums four columns of every key, or of every second, fourth, ...
+// where a row has fewer than 128 columns.  Forward keeps a running maximum and
+// sum per row.  dK and dV walk
 // the backward units: 32 keys a block, 8 a warp, all rows that see them
 // streamed 32 at a time, so that each gradient row is written once, by one
 // warp, in an order that never changes.  They are bound by shared-memory
@@ -71,13 +73,13 @@ __device__ __forceinline__ void load_tile(float* dst, int stride, const E* src, 
     }
 }
 
-// packed rows [row0, row0 + 32) of tokens from `tok` (row = token * r + head
+// packed rows [row0, row0 + ROWS) of tokens from `tok` (row = token * r + head
 // within the group of query heads), rows >= nrows as zeros
-template <typename E>
+template <int ROWS, typename E>
 __device__ __forceinline__ void load_rows(float* dst, int stride, const E* src, const SimtArgs& a,
                                           int tok, int hk, int row0, int nrows) {
     const int c4 = a.d / 4;
-    for (int i = threadIdx.x; i < kRows * c4; i += kThreads) {
+    for (int i = threadIdx.x; i < ROWS * c4; i += kThreads) {
         const int rl = i / c4, c = i - rl * c4, row = row0 + rl;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (row < nrows) {
@@ -102,41 +104,68 @@ __device__ __forceinline__ void p_ds(float t, float dp, float lse, float delta, 
     }
 }
 
-// Forward (BWD false) or dQ (BWD true) of one slot's 32 rows of a piece.
-template <typename E, int ACT, bool BWD>
+template <int R>
+__device__ __forceinline__ void load_weights(float* p, const float* w) {
+    if constexpr (R == 2) {
+        *reinterpret_cast<float2*>(p) = *reinterpret_cast<const float2*>(w);
+    } else {
+#pragma unroll
+        for (int i = 0; i < R; i += 4) *reinterpret_cast<float4*>(p + i) = *reinterpret_cast<const float4*>(w + i);
+    }
+}
+
+// the sum over a warp's ng groups of c4 lanes, in its first group
+__device__ __forceinline__ void join_lanes(float4& v, int lane, int g, int ng, int c4) {
+    for (int s = 1; s < ng; s *= 2) {
+        const int from = (lane + s * c4) & 31;
+        const float x = __shfl_sync(~0u, v.x, from), y = __shfl_sync(~0u, v.y, from);
+        const float z = __shfl_sync(~0u, v.z, from), w = __shfl_sync(~0u, v.w, from);
+        if ((g & (2 * s - 1)) == 0 && g + s < ng) {
+            v.x += x;
+            v.y += y;
+            v.z += z;
+            v.w += w;
+        }
+    }
+}
+
+// Forward (BWD false) or dQ (BWD true) of 4 R rows of a slot of a piece, R a warp.
+template <typename E, int ACT, bool BWD, int R>
 __global__ void __launch_bounds__(kThreads) simt_rows_kernel(const SimtArgs a) {
     extern __shared__ float sm[];
     const PrefixPiece pc = a.pieces[blockIdx.x];
-    const int slot = blockIdx.y >> 2, sub = blockIdx.y & 3;
+    constexpr int kBlock = 4 * R, kSubs = kBM / kBlock;
+    const int slot = blockIdx.y / kSubs, sub = blockIdx.y % kSubs;
     const int part = slot ? pc.part1 : pc.part0;
     if (part < 0) return;
     const bool dual = pc.flags & kPieceDual, own = pc.flags & kPieceOwn;
     const int tok = pc.tok + (!dual && slot ? pc.nA : 0);
     const int nrows = (!dual && slot ? pc.nB : pc.nA) * a.r;
-    const int row0 = sub * kRows;
+    const int row0 = sub * kBlock;
     if (row0 >= nrows) return;
     const int i0 = pc.i0 + (tok - pc.tok);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int qs = a.d, ks = a.d + 4;
-    float* Q = sm;                       // [32][d]
-    float* DO = Q + kRows * qs;          // [32][d] (BWD)
-    float* K = DO + (BWD ? kRows * qs : 0);   // [32][d + 4]
+    float* Q = sm;                       // [4 R][d]
+    float* DO = Q + kBlock * qs;          // [4 R][d] (BWD)
+    float* K = DO + (BWD ? kBlock * qs : 0);   // [32][d + 4]
     float* V = K + kRows * ks;
-    float* W = V + kRows * ks + warp * kRows * kPer;   // weights [32 keys][8 rows]
+    float* W = V + kRows * ks + warp * kRows * R;   // weights [32 keys][R rows]
     const E* kb = (const E*)(own ? a.k : a.kp);
     const E* vb = (const E*)(own ? a.v : a.vp);
-    load_rows(Q, qs, (const E*)a.q, a, tok, pc.hk, row0, nrows);
-    if constexpr (BWD) load_rows(DO, qs, (const E*)a.d_o, a, tok, pc.hk, row0, nrows);
-    const int c4 = a.d / 4;
-    float4 acc[kPer];
-    float m[kPer], l[kPer], lse[kPer], delta[kPer];
-    int ipos[kPer];
+    load_rows<kBlock>(Q, qs, (const E*)a.q, a, tok, pc.hk, row0, nrows);
+    if constexpr (BWD) load_rows<kBlock>(DO, qs, (const E*)a.d_o, a, tok, pc.hk, row0, nrows);
+    // the sums: a lane has four columns of every ng-th key
+    const int c4 = a.d / 4, ng = 32 / c4, g = lane / c4, gc = lane - g * c4;
+    float4 acc[R];
+    float m[R], l[R], lse[R], delta[R];
+    int ipos[R];
 #pragma unroll
-    for (int w = 0; w < kPer; ++w) {
+    for (int w = 0; w < R; ++w) {
         acc[w] = make_float4(0.f, 0.f, 0.f, 0.f);
         m[w] = -INFINITY;
         l[w] = 0.f;
-        const int row = row0 + warp * kPer + w, t = row / a.r;
+        const int row = row0 + warp * R + w, t = row / a.r;
         ipos[w] = i0 + t;
         lse[w] = INFINITY;
         delta[w] = 0.f;
@@ -155,26 +184,26 @@ __global__ void __launch_bounds__(kThreads) simt_rows_kernel(const SimtArgs a) {
         load_tile(K, ks, kb + src, (int64_t)a.Hkv * a.d, n, a.d);
         load_tile(V, ks, vb + src, (int64_t)a.Hkv * a.d, n, a.d);
         __syncthreads();
-        float s[kPer], dp[kPer];
+        float s[R], dp[R];
 #pragma unroll
-        for (int w = 0; w < kPer; ++w) s[w] = dp[w] = 0.f;
+        for (int w = 0; w < R; ++w) s[w] = dp[w] = 0.f;
         for (int c = 0; c < c4; ++c) {
             const float4 kv = *reinterpret_cast<const float4*>(K + lane * ks + 4 * c);
 #pragma unroll
-            for (int w = 0; w < kPer; ++w)
-                s[w] = dot4(kv, *reinterpret_cast<const float4*>(Q + (warp * kPer + w) * qs + 4 * c), s[w]);
+            for (int w = 0; w < R; ++w)
+                s[w] = dot4(kv, *reinterpret_cast<const float4*>(Q + (warp * R + w) * qs + 4 * c), s[w]);
             if constexpr (BWD) {
                 const float4 vv = *reinterpret_cast<const float4*>(V + lane * ks + 4 * c);
 #pragma unroll
-                for (int w = 0; w < kPer; ++w)
-                    dp[w] = dot4(vv, *reinterpret_cast<const float4*>(DO + (warp * kPer + w) * qs + 4 * c),
+                for (int w = 0; w < R; ++w)
+                    dp[w] = dot4(vv, *reinterpret_cast<const float4*>(DO + (warp * R + w) * qs + 4 * c),
                                  dp[w]);
             }
         }
         const int jpos = pc.j0 + key + lane;
         __syncwarp();
 #pragma unroll
-        for (int w = 0; w < kPer; ++w) {
+        for (int w = 0; w < R; ++w) {
             bool ok = lane < n;
             if (own && a.windowed) ok = ok && jpos <= ipos[w] && jpos > ipos[w] - a.window;
             const float t = s[w] * a.alpha;
@@ -198,25 +227,26 @@ __global__ void __launch_bounds__(kThreads) simt_rows_kernel(const SimtArgs a) {
             } else {
                 out = ok ? act_f<ACT, false>(t) : 0.f;
             }
-            W[lane * kPer + w] = out;
+            W[lane * R + w] = out;
         }
         __syncwarp();
-        if (lane < c4) {
+        if (g < ng) {
             const float* X = BWD ? K : V;
-            for (int j = 0; j < n; ++j) {
-                const float4 x = *reinterpret_cast<const float4*>(X + j * ks + 4 * lane);
-                float p[kPer];
-                *reinterpret_cast<float4*>(p) = *reinterpret_cast<const float4*>(W + j * kPer);
-                *reinterpret_cast<float4*>(p + 4) = *reinterpret_cast<const float4*>(W + j * kPer + 4);
+            for (int j = g; j < n; j += ng) {
+                const float4 x = *reinterpret_cast<const float4*>(X + j * ks + 4 * gc);
+                float p[R];
+                load_weights<R>(p, W + j * R);
 #pragma unroll
-                for (int w = 0; w < kPer; ++w) axpy4(acc[w], p[w], x);
+                for (int w = 0; w < R; ++w) axpy4(acc[w], p[w], x);
             }
         }
     }
+#pragma unroll
+    for (int w = 0; w < R; ++w) join_lanes(acc[w], lane, g, ng, c4);
     float4* out = reinterpret_cast<float4*>(a.parts) + (int64_t)part * c4;
 #pragma unroll
-    for (int w = 0; w < kPer; ++w) {
-        const int row = row0 + warp * kPer + w;
+    for (int w = 0; w < R; ++w) {
+        const int row = row0 + warp * R + w;
         if (row >= nrows) break;
         if (lane < c4) out[lane * nrows + row] = acc[w];
         if (!BWD && ACT == kSoftmax && lane == 0)   // maximum in base 2, as the merge takes it
@@ -244,14 +274,14 @@ __global__ void __launch_bounds__(kThreads) simt_keys_kernel(const SimtArgs a) {
     const int64_t src = ((int64_t)(u.k0 + key0) * a.Hkv + u.hk) * a.d, stride = (int64_t)a.Hkv * a.d;
     load_tile(K, ks, (const E*)(own ? a.k : a.kp) + src, stride, n, a.d);
     load_tile(V, ks, (const E*)(own ? a.v : a.vp) + src, stride, n, a.d);
-    const int c4 = a.d / 4, nrows = u.ntok * a.r;
+    const int c4 = a.d / 4, ng = 32 / c4, g = lane / c4, gc = lane - g * c4, nrows = u.ntok * a.r;
     float4 gk[kPer], gv[kPer];
 #pragma unroll
     for (int w = 0; w < kPer; ++w) gk[w] = gv[w] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int row0 = 0; row0 < nrows; row0 += kRows) {
         __syncthreads();
-        load_rows(Q, qs, (const E*)a.q, a, u.tok, u.hk, row0, nrows);
-        load_rows(DO, qs, (const E*)a.d_o, a, u.tok, u.hk, row0, nrows);
+        load_rows<kRows>(Q, qs, (const E*)a.q, a, u.tok, u.hk, row0, nrows);
+        load_rows<kRows>(DO, qs, (const E*)a.d_o, a, u.tok, u.hk, row0, nrows);
         __syncthreads();
         const int row = row0 + lane, t = row / a.r, ipos = u.i0 + t;
         float lse = INFINITY, delta = 0.f;
@@ -285,16 +315,14 @@ __global__ void __launch_bounds__(kThreads) simt_keys_kernel(const SimtArgs a) {
             X[lane * kPer + w] = ok ? ds * a.alpha : 0.f;
         }
         __syncwarp();
-        if (lane < c4) {
+        if (g < ng) {
             const int m = min(kRows, nrows - row0);
-            for (int i = 0; i < m; ++i) {
-                const float4 qv = *reinterpret_cast<const float4*>(Q + i * qs + 4 * lane);
-                const float4 dv = *reinterpret_cast<const float4*>(DO + i * qs + 4 * lane);
+            for (int i = g; i < m; i += ng) {
+                const float4 qv = *reinterpret_cast<const float4*>(Q + i * qs + 4 * gc);
+                const float4 dv = *reinterpret_cast<const float4*>(DO + i * qs + 4 * gc);
                 float p[kPer], x[kPer];
-                *reinterpret_cast<float4*>(p) = *reinterpret_cast<const float4*>(W + i * kPer);
-                *reinterpret_cast<float4*>(p + 4) = *reinterpret_cast<const float4*>(W + i * kPer + 4);
-                *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(X + i * kPer);
-                *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(X + i * kPer + 4);
+                load_weights<kPer>(p, W + i * kPer);
+                load_weights<kPer>(x, X + i * kPer);
 #pragma unroll
                 for (int w = 0; w < kPer; ++w) {
                     axpy4(gv[w], p[w], dv);
@@ -302,6 +330,11 @@ __global__ void __launch_bounds__(kThreads) simt_keys_kernel(const SimtArgs a) {
                 }
             }
         }
+    }
+#pragma unroll
+    for (int w = 0; w < kPer; ++w) {
+        join_lanes(gv[w], lane, g, ng, c4);
+        join_lanes(gk[w], lane, g, ng, c4);
     }
     if (lane < c4) {
         E* dk = (E*)(own ? a.dk : a.dkp) + src;
@@ -444,27 +477,37 @@ gdpa_status go(dim3 grid, int smem, PrefixPlan& p, const SimtArgs& a, cudaStream
     if ((act) == kSoftmax) { constexpr int A = kSoftmax; __VA_ARGS__; }   \
     else GDPA_DISPATCH_ACT(act, A, __VA_ARGS__)
 
+template <typename E, bool BWD, int R>
+gdpa_status rows_t(PrefixPlan& p, int act, const SimtArgs& a, cudaStream_t st) {
+    gdpa_status s = GDPA_OK;
+    const int smem = ((BWD ? 2 : 1) * 4 * R * p.d + 2 * kRows * (p.d + 4) + 4 * kRows * R) * 4;
+    const dim3 grid((unsigned)p.pieces.size(), 2 * kBM / (4 * R));
+    PREFIX_DISPATCH(act, s = (go<simt_rows_kernel<E, A, BWD, R>>(grid, smem, p, a, st)))
+    return s;
+}
+
+template <typename E, bool BWD>
+gdpa_status rows_of(PrefixPlan& p, int act, const SimtArgs& a, cudaStream_t st) {
+    if (p.pieces.empty()) return GDPA_OK;
+    // 2 rows a warp: a quarter of the instructions on a warp's way, for four
+    // times the reads of keys.  Better where few blocks are there to hide them
+    // (4 users of 40 rows, 500 keys, d = 32: 20 us, 27 with 8 rows; one row
+    // against 4096 keys, d = 128: 32 and 42), and up to 48 columns always (8
+    // users of 256 rows, 2000 keys, 4 heads, d = 48: 372 and 456); from 64 on
+    // 8 rows (the same with d = 64: 279, 356 with 2; 512 rows, d = 128: 421, 698).
+    return p.d < 64 || p.row_blocks <= 2 * p.S ? rows_t<E, BWD, 2>(p, act, a, st)
+                                               : rows_t<E, BWD, kPer>(p, act, a, st);
+}
+
 template <typename E>
 gdpa_status fwd_t(PrefixPlan& p, const PrefixIO& io, cudaStream_t st) {
-    gdpa_status s = GDPA_OK;
-    if (!p.pieces.empty()) {
-        const SimtArgs a = args_of(p, io, nullptr);
-        const int smem = (kRows * p.d + 2 * kRows * (p.d + 4) + 4 * kRows * kPer) * 4;
-        const dim3 grid((unsigned)p.pieces.size(), 8);
-        PREFIX_DISPATCH(io.act, s = (go<simt_rows_kernel<E, A, false>>(grid, smem, p, a, st)))
-    }
-    return s;
+    return rows_of<E, false>(p, io.act, args_of(p, io, nullptr), st);
 }
 
 template <typename E>
 gdpa_status bwd_t(PrefixPlan& p, const PrefixIO& io, const float* delta, cudaStream_t st) {
-    gdpa_status s = GDPA_OK;
     const SimtArgs a = args_of(p, io, delta);
-    if (!p.pieces.empty()) {
-        const int smem = (2 * kRows * p.d + 2 * kRows * (p.d + 4) + 4 * kRows * kPer) * 4;
-        const dim3 grid((unsigned)p.pieces.size(), 8);
-        PREFIX_DISPATCH(io.act, s = (go<simt_rows_kernel<E, A, true>>(grid, smem, p, a, st)))
-    }
+    gdpa_status s = rows_of<E, true>(p, io.act, a, st);
     if (s == GDPA_OK && !p.units.empty()) {
         const int smem = (2 * kRows * p.d + 2 * kRows * (p.d + 4) + 8 * kRows * kPer) * 4;
         const dim3 grid((unsigned)p.units.size(), 4);
