@@ -145,6 +145,7 @@ gdpa_status create(const int32_t* q_off, const int32_t* kv_off, int B, const int
             {p->useg.data(), p->useg.size() * 4, &p->off_useg},
             {p->smalls.data(), p->smalls.size() * sizeof(gdpa::PrefixUnit), &p->off_smalls},
             {p->eights.data(), p->eights.size() * sizeof(gdpa::PrefixUnit), &p->off_eights},
+            {p->joins.data(), p->joins.size() * sizeof(gdpa::PrefixUnit), &p->off_joins},
         };
         size_t at = 0;
         for (auto& e : t) {
@@ -249,7 +250,8 @@ gdpa_status bwd(gdpa_prefix_plan plan, gdpa_dtype dtype, const PrefixIO& io, voi
     cudaStream_t st = (cudaStream_t)stream;
     std::lock_guard<std::mutex> hold(p.lock);
     const bool cap = capturing(st);
-    const size_t need = (size_t)p.Tq * p.H * sizeof(float);
+    const size_t unit_parts = (size_t)p.n_unit_parts * 2 * gdpa::kBN * p.d;   // floats
+    const size_t need = (unit_parts + (size_t)p.Tq * p.H) * sizeof(float);
     if (p.grad_bytes < need && cap) return GDPA_ERR_ALLOC;   // a graph must not own the workspace
     if (gdpa_status s = begin_work(p, st, cap)) return s;
     if (p.grad_bytes < need) {
@@ -261,14 +263,16 @@ gdpa_status bwd(gdpa_prefix_plan plan, gdpa_dtype dtype, const PrefixIO& io, voi
         p.grad_bytes = need;
     }
     gdpa_status s = GDPA_OK;
-    if (sm) s = gdpa::launch_prefix_delta(p, dtype, io, p.d_grad, st);
+    float* delta = p.d_grad + unit_parts;
+    if (sm) s = gdpa::launch_prefix_delta(p, dtype, io, delta, st);
     if (use_tc(p, dtype)) {
-        if (s == GDPA_OK) s = gdpa::launch_prefix_own_bwd8(p, io, p.d_grad, st);
-        if (s == GDPA_OK) s = gdpa::launch_prefix_own_bwd(p, io, p.d_grad, st);
-        if (s == GDPA_OK) s = gdpa::launch_prefix_tc_bwd(p, io, p.d_grad, st);
+        if (s == GDPA_OK) s = gdpa::launch_prefix_own_bwd8(p, io, delta, st);
+        if (s == GDPA_OK) s = gdpa::launch_prefix_own_bwd(p, io, delta, st);
+        if (s == GDPA_OK) s = gdpa::launch_prefix_tc_bwd(p, io, delta, st);
     } else if (s == GDPA_OK) {
-        s = gdpa::launch_prefix_simt_bwd(p, dtype, io, p.d_grad, st);
+        s = gdpa::launch_prefix_simt_bwd(p, dtype, io, delta, st);
     }
+    if (s == GDPA_OK) s = gdpa::launch_prefix_join(p, dtype, io, st);
     if (s == GDPA_OK) s = gdpa::launch_prefix_merge(p, dtype, io.dq, nullptr, false, st);
     const gdpa_status e = end_work(p, st, cap);
     return s != GDPA_OK ? s : e;

@@ -28,6 +28,7 @@
 namespace gdpa {
 
 constexpr int kPieceOwn = 1;    // keys of the samples' own, not of the prefix
+constexpr int kUnitPart = 256;
 constexpr int kPieceDual = 2;   // one row tile: the slots take alternate key blocks
 
 // One piece of forward work: keys [k0, k0 + nk) against one row tile of
@@ -42,7 +43,10 @@ struct PrefixPiece {
 static_assert(sizeof(PrefixPiece) == 48, "PrefixPiece layout");
 
 // Backward unit: keys [k0, k0 + nk) (nk <= 128) of head hk against tokens
-// [tok, tok + ntok); flags as a piece's.
+// [tok, tok + ntok), token `tok` at position i0 of its sample, key k0 at j0
+// (own keys).  flags as a piece's; kUnitPart * (i + 1): one of several ranges of
+// the tokens, whose dV and dK go to part i of the workspace, [128 keys][d]
+// floats each.  In the list of joins: parts [tok, tok + ntok).
 struct PrefixUnit {
     int32_t k0, nk, tok, ntok;
     int32_t hk, flags, i0, j0;
@@ -81,16 +85,18 @@ struct PrefixPlan {
     std::vector<PrefixOwn> own;      // [Tq]
     std::vector<PrefixUnit> units;   // the tensor-core family's, then the small own ones
     std::vector<int32_t> useg;       // [S + 1] first unit of each CTA
+    std::vector<PrefixUnit> joins;   // units in ranges, for the sum over them
+    int64_t n_unit_parts = 0;
     // small own keys: one unit per sample and key head, those of at most 8
     // packed rows first; and the same cut into 8 rows each (j0: the first)
     std::vector<PrefixUnit> smalls, eights;
     int64_t n_small8 = 0;
     // device copies, one allocation (offsets below), and workspaces
     uint8_t* d_tables = nullptr;
-    size_t off_seg = 0, off_tiles = 0, off_own = 0, off_units = 0, off_useg = 0, off_smalls = 0, off_eights = 0, off_err = 0;
+    size_t off_seg = 0, off_tiles = 0, off_own = 0, off_units = 0, off_useg = 0, off_smalls = 0, off_eights = 0, off_joins = 0, off_err = 0;
     float* d_parts = nullptr;        // [n_part_rows] x d floats
     float* d_ml = nullptr;           // [n_part_rows] float2
-    float* d_grad = nullptr;         // backward: delta [Tq][H], then float32 sums
+    float* d_grad = nullptr;         // backward: the parts of split units, then delta [Tq][H]
     size_t grad_bytes = 0;
     int32_t last_err[4] = {0, 0, 0, 0};
     int64_t launches = 0;
@@ -106,6 +112,7 @@ struct PrefixPlan {
     const PrefixTile* dev_tiles() const { return (const PrefixTile*)(d_tables + off_tiles); }
     const PrefixOwn* dev_own() const { return (const PrefixOwn*)(d_tables + off_own); }
     const PrefixUnit* dev_units() const { return (const PrefixUnit*)(d_tables + off_units); }
+    const PrefixUnit* dev_joins() const { return (const PrefixUnit*)(d_tables + off_joins); }
     const int32_t* dev_useg() const { return (const int32_t*)(d_tables + off_useg); }
     const PrefixUnit* dev_smalls() const { return (const PrefixUnit*)(d_tables + off_smalls); }
     const PrefixUnit* dev_eights() const { return (const PrefixUnit*)(d_tables + off_eights); }
@@ -181,6 +188,8 @@ gdpa_status launch_prefix_own_bwd(PrefixPlan& p, const PrefixIO& io, const float
 // `softmax`), of element type dt.
 gdpa_status launch_prefix_merge(PrefixPlan& p, gdpa_dtype dt, void* out, float* lse, bool softmax,
                                 cudaStream_t st);
+// Sum the parts of split backward units: into dkp, dvp, dk, dv.
+gdpa_status launch_prefix_join(PrefixPlan& p, gdpa_dtype dt, const PrefixIO& io, cudaStream_t st);
 // delta[t][h] = dO . O (softmax backward)
 gdpa_status launch_prefix_delta(PrefixPlan& p, gdpa_dtype dt, const PrefixIO& io, float* delta,
                                 cudaStream_t st);

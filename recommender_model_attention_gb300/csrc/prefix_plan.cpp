@@ -22,6 +22,8 @@ constexpr int kPieceCost = 3;   // steps a piece costs beside its own
 constexpr int kSmallRows = 64;
 constexpr int kSmallKeys = 512;
 
+constexpr int kSplitTiles = 4;   // row tiles that a range of a split backward unit has at least
+
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct Unit {
@@ -44,6 +46,44 @@ bool is_small(const PrefixPlan& p, int32_t lq, int32_t lk) {
 int64_t steps_of(const PrefixPiece& p) {
     const int64_t nb = cdiv(p.nk, kBN);
     return p.flags & kPieceDual ? cdiv(nb, 2) : nb;
+}
+
+// Cut units with more rows than a share of all (few keys, many rows) into
+// ranges of their tokens, so that every SM has work: each writes float32 sums
+// of its own, which a kernel joins in order.  (Backward of 4 users, 2000 rows a
+// head, on 100 keys: 8 heads sharing one, d = 128, 131 us, whole 331; 8 key
+// heads 137 and 152; 17 users, 18144 rows on 40 keys of one float32 head, d =
+// 32, 1055 and 3283.)
+void split_units(PrefixPlan& p) {
+    p.joins.clear();
+    p.n_unit_parts = 0;
+    // the tensor-core kernel has one CTA an SM, the others several
+    const int64_t lanes = p.d == 64 || p.d == 128 ? p.S : 4 * (int64_t)p.S;
+    int64_t total = 0;
+    for (const PrefixUnit& u : p.units) total += cdiv(u.ntok, p.tpt);
+    const int64_t share = std::max<int64_t>(cdiv(total, lanes), kSplitTiles);
+    std::vector<PrefixUnit> out;
+    for (const PrefixUnit& u : p.units) {
+        const int64_t tiles = cdiv(u.ntok, p.tpt);
+        if (2 * tiles <= 3 * share) {
+            out.push_back(u);
+            continue;
+        }
+        const int64_t each = cdiv(tiles, cdiv(tiles, share)) * p.tpt;   // tokens
+        PrefixUnit j = u;
+        j.tok = (int32_t)p.n_unit_parts;
+        for (int64_t at = 0; at < u.ntok; at += each) {
+            PrefixUnit c = u;
+            c.tok += (int32_t)at;
+            c.i0 += (int32_t)at;
+            c.ntok = (int32_t)std::min<int64_t>(each, u.ntok - at);
+            c.flags |= (int32_t)(++p.n_unit_parts) * kUnitPart;
+            out.push_back(c);
+        }
+        j.ntok = (int32_t)p.n_unit_parts - j.tok;
+        p.joins.push_back(j);
+    }
+    p.units.swap(out);
 }
 
 }  // namespace
@@ -296,6 +336,7 @@ gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t
     }
     p.n_small8 = (int64_t)p.smalls.size();
     p.smalls.insert(p.smalls.end(), more.begin(), more.end());
+    split_units(p);
     // deal them by their row tiles (and a unit's own loads and stores) in
     // snake order, longest first
     const int64_t n = (int64_t)p.units.size();

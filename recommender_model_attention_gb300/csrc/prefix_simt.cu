@@ -33,6 +33,7 @@ struct SimtArgs {
     const float *lse, *delta;
     float* parts;
     float* ml;
+    float* unit_parts;
     void *dkp, *dvp, *dk, *dv;
     int H, Hkv, r, d;
     int windowed, window;
@@ -337,15 +338,42 @@ __global__ void __launch_bounds__(kThreads) simt_keys_kernel(const SimtArgs a) {
         join_lanes(gk[w], lane, g, ng, c4);
     }
     if (lane < c4) {
+        const int split = u.flags / kUnitPart;
         E* dk = (E*)(own ? a.dk : a.dkp) + src;
         E* dv = (E*)(own ? a.dv : a.dvp) + src;
 #pragma unroll
         for (int w = 0; w < kPer; ++w) {
             const int j = warp * kPer + w;
             if (j >= n) break;
+            if (split) {   // one of several ranges of the rows
+                float* to = a.unit_parts + ((int64_t)(split - 1) * 2 * kBN + key0 + j) * a.d + 4 * lane;
+                st4(to, gv[w]);
+                st4(to + (int64_t)kBN * a.d, gk[w]);
+                continue;
+            }
             st4(dk + j * stride + 4 * lane, gk[w]);
             st4(dv + j * stride + 4 * lane, gv[w]);
         }
+    }
+}
+
+// dK and dV of 8 keys of a unit whose rows were split, its parts in order.
+template <typename E>
+__global__ void __launch_bounds__(256) join_kernel(const PrefixUnit* joins, const float* parts, E* dkp, E* dvp,
+                                                   E* dk, E* dv, int Hkv, int d) {
+    const PrefixUnit u = joins[blockIdx.x];
+    const int c4 = d / 4, key0 = blockIdx.y * 8, n = min(8, u.nk - key0);
+    grid_wait_previous();
+    const bool own = u.flags & kPieceOwn;
+    for (int i = threadIdx.x; i < 2 * n * c4; i += blockDim.x) {
+        const bool second = i >= n * c4;
+        const int x = second ? i - n * c4 : i, key = key0 + x / c4, c = 4 * (x % c4);
+        const float* src = parts + ((int64_t)u.tok * 2 * kBN + (second ? kBN : 0) + key) * d + c;
+        float4 sum = ld4(src);
+#pragma unroll 4
+        for (int t = 1; t < u.ntok; ++t) axpy4(sum, 1.f, ld4(src + (int64_t)t * 2 * kBN * d));
+        E* to = second ? (own ? dk : dkp) : (own ? dv : dvp);
+        st4(to + ((int64_t)(u.k0 + key) * Hkv + u.hk) * d + c, sum);
     }
 }
 
@@ -455,6 +483,7 @@ SimtArgs args_of(const PrefixPlan& p, const PrefixIO& io, const float* delta) {
     a.parts = p.d_parts;
     a.ml = p.d_ml;
     a.dkp = io.dkp; a.dvp = io.dvp; a.dk = io.dk; a.dv = io.dv;
+    a.unit_parts = p.d_grad;
     a.H = p.H; a.Hkv = p.Hkv; a.r = p.r; a.d = p.d;
     a.windowed = p.mask == GDPA_MASK_CAUSAL_WINDOW;
     a.window = p.window;
@@ -525,6 +554,22 @@ gdpa_status launch_prefix_simt_fwd(PrefixPlan& p, gdpa_dtype dt, const PrefixIO&
 gdpa_status launch_prefix_simt_bwd(PrefixPlan& p, gdpa_dtype dt, const PrefixIO& io,
                                    const float* delta, cudaStream_t st) {
     return dt == GDPA_BF16 ? bwd_t<__nv_bfloat16>(p, io, delta, st) : bwd_t<float>(p, io, delta, st);
+}
+
+gdpa_status launch_prefix_join(PrefixPlan& p, gdpa_dtype dt, const PrefixIO& io, cudaStream_t st) {
+    if (p.joins.empty()) return GDPA_OK;
+    const dim3 grid((unsigned)p.joins.size(), kBN / 8);
+    const bool early = p.chain > 0;
+    const float* parts = p.d_grad;
+    auto go = [&](auto* t) {
+        using E = std::remove_pointer_t<decltype(t)>;
+        return launch_kernel(join_kernel<E>, grid, 256, 0, st, early, p.dev_joins(), parts, (E*)io.dkp, (E*)io.dvp,
+                             (E*)io.dk, (E*)io.dv, p.Hkv, p.d);
+    };
+    const bool ok = dt == GDPA_BF16 ? go((__nv_bfloat16*)nullptr) : go((float*)nullptr);
+    p.launches += 1;
+    p.chain += 1;
+    return ok ? GDPA_OK : GDPA_ERR_CUDA;
 }
 
 gdpa_status launch_prefix_merge(PrefixPlan& p, gdpa_dtype dt, void* out, float* lse, bool softmax,

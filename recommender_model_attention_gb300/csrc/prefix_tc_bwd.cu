@@ -63,6 +63,7 @@ struct BwArgs {
     const float* lse;
     const float* delta;
     float* parts;
+    float* unit_parts;
     __nv_bfloat16 *dkp, *dvp, *dk, *dv;
     int H, Hkv, r, tpt, windowed, window;
     int q_bytes;
@@ -420,6 +421,7 @@ __device__ __forceinline__ void kv_drain(const BwArgs& a, uint64_t* bars, uint32
     for (int t = seg0; t < seg1; ++t) {
         const PrefixUnit u = load_unit(a.units + t);
         const bool own = u.flags & kPieceOwn, real = key < u.nk;
+        const int split = u.flags / kUnitPart;
         const int64_t at = ((int64_t)(u.k0 + key) * a.Hkv + u.hk) * D;
         __nv_bfloat16 *dv = (own ? a.dv : a.dvp) + at, *dk = (own ? a.dk : a.dkp) + at;
         if (u.ntok == 0) {   // keys that no row sees
@@ -443,7 +445,13 @@ __device__ __forceinline__ void kv_drain(const BwArgs& a, uint64_t* bars, uint32
                 mbar_arrive(&bars[C::kAccFree]);
             }
             const float f = second ? a.alpha : 1.0f;
-            if (real) {
+            if (real && split) {   // one of several ranges of the rows
+                float4* to = reinterpret_cast<float4*>(a.unit_parts + ((int64_t)(split - 1) * 256 + (second ? 128 : 0) + key) * D + c);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    to[i] = make_float4(__uint_as_float(v[4 * i]) * f, __uint_as_float(v[4 * i + 1]) * f,
+                                        __uint_as_float(v[4 * i + 2]) * f, __uint_as_float(v[4 * i + 3]) * f);
+            } else if (real) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t o[4];
@@ -884,6 +892,7 @@ gdpa_status launch_prefix_tc_bwd(PrefixPlan& p, const PrefixIO& io, const float*
     a.lse = io.lse;
     a.delta = delta;
     a.parts = p.d_parts;
+    a.unit_parts = p.d_grad;
     a.dkp = (__nv_bfloat16*)io.dkp;
     a.dvp = (__nv_bfloat16*)io.dvp;
     a.dk = (__nv_bfloat16*)io.dk;

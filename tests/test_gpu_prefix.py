@@ -329,6 +329,28 @@ def test_together_with_rotary_positions():
     check_f32(dv, wg[4], "dv")
 
 
+@pytest.mark.parametrize("dt,d", [("bf16", 128), ("bf16", 64), ("f32", 32), ("f32", 128)])
+@pytest.mark.parametrize("act", ["softmax", "gelu_tanh"])
+@pytest.mark.parametrize("shape", ["prefix", "two_prefixes", "own", "own_window"])
+def test_many_rows_on_few_keys(shape, act, dt, d):
+    """Key blocks whose rows are cut into ranges (more than six tiles of 128
+    packed rows on a block, few blocks): the parts' sums, rows that end inside
+    a tile, causal positions past a cut; and the same bits again."""
+    offs, window = {
+        "prefix": (batch([37] * 30, [5] * 30, [30], [70]), 0),
+        "two_prefixes": (batch([40] * 21 + [3] * 2, [0] * 23, [21, 2], [1, 130]), 0),
+        "own": (batch([1100, 7], [150, 2], [1, 1], [3, 0]), 0),
+        "own_window": (batch([1500], [200], [1], [3]), 700),
+    }[shape]
+    H, Hkv = 4, 1
+    plan, x, o, lse, grads = run(offs, H, Hkv, d, dt, act, window=window)
+    kw = dict(alpha=d ** -0.5)
+    again = (gd.gdpa_prefix_softmax_bwd(plan, *x[:5], o, x[5], lse, **kw) if act == "softmax"
+             else gd.gdpa_prefix_bwd(plan, *x[:5], x[5], act=act, **kw))
+    for a, b in zip(grads, again):
+        assert torch.equal(a, b)
+
+
 def test_refusals():
     offs = batch([5], [4], [1], [30])
     x = make(offs, 2, 2, 32, "f32")
