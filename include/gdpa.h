@@ -583,7 +583,10 @@ gdpa_status gdpa_rope_apply(const gdpa_rope* rope, int inverse, gdpa_dtype dtype
  * w = act(alpha q.k), or softmax over all of them together.  Every query sees
  * the whole prefix; the mask (and its window) applies to the own keys, with
  * positions counted from the sample's first row, as in gdpa_plan_create.  A
- * row that sees no key gives O = 0, lse = -inf and no gradient.
+ * row that sees no key gives O = 0, lse = -inf and no gradient.  Rows of other
+ * samples and groups never enter a result, whatever they hold; a key that the
+ * mask hides from a row, but not from all of its sample's, enters with weight
+ * 0, so its value must be finite.
  *
  * Heads: Hkv key heads, each shared by H / Hkv consecutive query heads (Hkv =
  * H: one each).  Layout: q, o, d_o, dq [Tq][H][d]; kp, vp, dkp, dvp
@@ -623,8 +626,11 @@ gdpa_status gdpa_prefix_create_host(const int32_t* q_off, const int32_t* kv_off,
  * token; tokens of the first and of the second row tile; key head; first key
  * row; keys; flags: 1 own keys, 2 one row tile in two halves of alternate
  * 128-key blocks; position of the token and of the key in their sample; the
- * two parts written, -1 for none; 0), seg int32 [num_sms + 1] (may be NULL).
- * INVALID_ARG if cap is too small (*n still receives the count). */
+ * row of the workspace from which each tile's sums are written, -1 for none;
+ * 0), seg int32 [num_sms + 1] (may be NULL).  The pieces behind
+ * seg[num_sms] are small samples' own keys, which the tensor-core path runs in
+ * a kernel of their own.  INVALID_ARG if cap is too small (*n still receives
+ * the count). */
 gdpa_status gdpa_prefix_export(gdpa_prefix_plan plan, int32_t* pieces, int64_t cap, int64_t* n,
                                int32_t* seg);
 /* As gdpa_plan_set_kernel: AUTO runs bf16 with d = 64 or 128 on the tensor

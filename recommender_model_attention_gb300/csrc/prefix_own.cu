@@ -9,14 +9,18 @@
 // lanes as 16-byte loads bring them (lane q of a quad takes columns 32 i + 8 q
 // .. + 7, the queries alike), and V's 8-column loads make the lane of group g
 // own output columns 8 g + e of product e; a weight's 8x8 blocks change from
-// accumulator to operand layout by movmatrix.  Nothing passes through shared
-// memory.  The work is bounded by reading the keys once; a 128-row tile on the
-// fifth-generation tensor core would cost every sample its whole chain of
-// latencies for a row or two.
+// accumulator to operand layout by movmatrix.  The work is bounded by reading
+// the keys once; a 128-row tile on the fifth-generation tensor core would cost
+// every sample its whole chain of latencies for a row or two.  Forward, 16
+// warps an SM, keys in registers: 75 MB of keys of 512 candidates in 20 us
+// (through shared memory as below 19, and slower for d = 64).
 //
 // The backward of a unit of at most 8 rows runs in one warp too: each key's
 // dK and dV are done in its step, dQ^T = K^T dS^T adds up over the steps, so
-// every sum has one owner and one order.
+// every sum has one owner and one order.  It has registers for 8 warps an SM
+// only, so the next step's keys are copied to shared memory meanwhile, and dK
+// and dV leave as whole sectors: 47 us for a training batch of 32 users (0.2
+// GB in all); keys loaded into registers 54, with 12 warps 54, half sectors 54.
 #include "act.cuh"
 #include "prefix_internal.h"
 #include "prefix_mma.cuh"
@@ -221,6 +225,32 @@ __global__ void __launch_bounds__(kThreads, 4) own_fwd_kernel(const OwnArgs a) {
     }
 }
 
+// 16 keys of K, then of V, in shared memory: rows of D + 8 columns, so that
+// four rows two apart start in different banks.  A lane's copies of the keys
+// from j0 on (rows past the last one hold it again).
+template <int D>
+struct Stage {
+    static constexpr int kRow = D + 8, kKeys = 16 * kRow;   // elements
+    static constexpr int kBytes = 2 * kKeys * 2;
+};
+
+template <int D>
+__device__ __forceinline__ void load_stage(__nv_bfloat16* to, const __nv_bfloat16* K, const __nv_bfloat16* V,
+                                           int64_t ks, int j0, int nk, int lane) {
+    constexpr int kChunks = D / 8;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int x = lane + 32 * i, row = x / kChunks, c = 8 * (x % kChunks);
+        const __nv_bfloat16* src = (row < 16 ? K : V) + min(j0 + (row & 15), nk - 1) * ks + c;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(to + row * Stage<D>::kRow + c)),
+                     "l"(src)
+                     : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+__device__ __forceinline__ uint4 lds16(const __nv_bfloat16* p) { return *reinterpret_cast<const uint4*>(p); }
+
 // Backward of units of at most 8 rows.
 template <int D, int ACT>
 __global__ void __launch_bounds__(kThreads, 2) own_bwd8_kernel(const OwnArgs a) {
@@ -234,7 +264,10 @@ __global__ void __launch_bounds__(kThreads, 2) own_bwd8_kernel(const OwnArgs a) 
     const Rows rows{min(8, u.ntok * a.r), 0, u.tok, u.hk, a.r, a.H};
     const int64_t ks = (int64_t)a.Hkv * D, k_at = (int64_t)u.k0 * ks + u.hk * D;
     const __nv_bfloat16 *K = a.k + k_at, *V = a.v + k_at;
-    prefetch_keys<D>(K, V, ks, 0, min(u.nk, kAhead), lane);
+    extern __shared__ uint4 own_smem[];   // two stages a warp
+    __nv_bfloat16* stage = reinterpret_cast<__nv_bfloat16*>(own_smem) + (threadIdx.x >> 5) * 4 * Stage<D>::kKeys;
+    load_stage<D>(stage, K, V, ks, 0, u.nk, lane);
+    prefetch_keys<D>(K, V, ks, 16, min(u.nk, kAhead), lane);
     const PrefixOwn ow = a.own[u.tok];
     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
     const ActScale sc = act_scale<ACT>(a.alpha);
@@ -268,35 +301,33 @@ __global__ void __launch_bounds__(kThreads, 2) own_bwd8_kernel(const OwnArgs a) 
             }
         }
     }
+    const bool wide = !(((uintptr_t)a.dk | (uintptr_t)a.dv) & 31);
     float acc[products<D>()][4];   // dQ^T
 #pragma unroll
     for (int e = 0; e < products<D>(); ++e) acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.0f;
+#pragma unroll 1
     for (int j0 = 0; j0 < u.nk; j0 += 16) {
-        if (j0 + kAhead < u.nk) prefetch_keys<D>(K, V, ks, j0 + kAhead, min(u.nk, j0 + kAhead + 16), lane);
+        const __nv_bfloat16* kk = stage + (j0 & 16 ? 2 * Stage<D>::kKeys : 0);
+        const __nv_bfloat16* vv = kk + Stage<D>::kKeys;
+        if (j0 + 16 < u.nk) {   // the next keys' copies fly while these are worked on
+            load_stage<D>(stage + (j0 & 16 ? 0 : 2 * Stage<D>::kKeys), K, V, ks, j0 + 16, u.nk, lane);
+            if (j0 + kAhead < u.nk) prefetch_keys<D>(K, V, ks, j0 + kAhead, min(u.nk, j0 + kAhead + 16), lane);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        }
+        __syncwarp();
         float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, dp[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        uint4 kv[4][kW];
         {
-            const int64_t x = min(j0 + g, u.nk - 1) * ks, y = min(j0 + g + 8, u.nk - 1) * ks;
-            uint4 ka[kC], kb[kC], va[kC], vb[kC];
+            const int x = g * Stage<D>::kRow + 8 * q, y = x + 8 * Stage<D>::kRow;
 #pragma unroll
             for (int i = 0; i < kC; ++i) {
-                ka[i] = ldg16(K + x + 32 * i + 8 * q);
-                kb[i] = ldg16(K + y + 32 * i + 8 * q);
-                va[i] = ldg16(V + x + 32 * i + 8 * q);
-                vb[i] = ldg16(V + y + 32 * i + 8 * q);
-            }
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const int j = j0 + 2 * q + (w & 1) + (w >> 1) * 8;
-#pragma unroll
-                for (int h = 0; h < kW; ++h) kv[w][h] = j < u.nk ? ldg16(K + j * ks + 64 * h + 8 * g) : z;
-            }
-#pragma unroll
-            for (int i = 0; i < kC; ++i) {
-                mma16816(s, ka[i].x, kb[i].x, ka[i].y, kb[i].y, qb[i].x, qb[i].y);
-                mma16816(dp, va[i].x, vb[i].x, va[i].y, vb[i].y, ob[i].x, ob[i].y);
-                mma16816(s, ka[i].z, kb[i].z, ka[i].w, kb[i].w, qb[i].z, qb[i].w);
-                mma16816(dp, va[i].z, vb[i].z, va[i].w, vb[i].w, ob[i].z, ob[i].w);
+                const uint4 ka = lds16(kk + x + 32 * i), kb = lds16(kk + y + 32 * i);
+                const uint4 va = lds16(vv + x + 32 * i), vb = lds16(vv + y + 32 * i);
+                mma16816(s, ka.x, kb.x, ka.y, kb.y, qb[i].x, qb[i].y);
+                mma16816(dp, va.x, vb.x, va.y, vb.y, ob[i].x, ob[i].y);
+                mma16816(s, ka.z, kb.z, ka.w, kb.w, qb[i].z, qb[i].w);
+                mma16816(dp, va.z, vb.z, va.w, vb.w, ob[i].z, ob[i].w);
             }
         }
         float p[4], ds[4];
@@ -338,16 +369,23 @@ __global__ void __launch_bounds__(kThreads, 2) own_bwd8_kernel(const OwnArgs a) 
                     const int j = j0 + g + 8 * x;
                     if (j >= u.nk) continue;
                     __nv_bfloat16* dst = (i ? a.dk : a.dv) + k_at + j * ks + 64 * h + 16 * q;
+                    uint32_t y[8];
 #pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        uint32_t y[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            y[e] = tc::pack_bf16x2(o[2 * e][2 * x + w] * f, o[2 * e + 1][2 * x + w] * f);
-                        reinterpret_cast<uint4*>(dst)[w] = make_uint4(y[0], y[1], y[2], y[3]);
-                    }
+                    for (int e = 0; e < 8; ++e)
+                        y[e] = tc::pack_bf16x2(o[2 * (e & 3)][2 * x + (e >> 2)] * f,
+                                               o[2 * (e & 3) + 1][2 * x + (e >> 2)] * f);
+                    store_sector(dst, y, wide);
                 }
             }
+        uint4 kv[4][kW];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const int j = 2 * q + (w & 1) + (w >> 1) * 8;
+#pragma unroll
+            for (int h = 0; h < kW; ++h)
+                kv[w][h] = j0 + j < u.nk ? lds16(kk + j * Stage<D>::kRow + 64 * h + 8 * g) : z;
+        }
+        __syncwarp();   // (read: the next step's copies may overwrite them)
         const uint32_t b0 = transposed(d0), b1 = transposed(d1);
 #pragma unroll
         for (int e = 0; e < products<D>(); ++e) {
@@ -385,30 +423,36 @@ OwnArgs args_of(const PrefixPlan& p, const PrefixIO& io, const float* delta) {
 }
 
 template <int D, int ACT>
-void go(bool bwd, const OwnArgs& a, cudaStream_t st) {
+bool go(bool bwd, int device, const OwnArgs& a, cudaStream_t st) {
     const unsigned grid = (unsigned)((a.n + kWarps - 1) / kWarps);
-    if (bwd)
-        own_bwd8_kernel<D, ACT><<<grid, kThreads, 0, st>>>(a);
-    else
+    if (bwd) {
+        constexpr int kSmem = kWarps * 2 * Stage<D>::kBytes;
+        static std::atomic<uint64_t> done{0};
+        if (!allow_smem(own_bwd8_kernel<D, ACT>, kSmem, device, done)) return false;
+        own_bwd8_kernel<D, ACT><<<grid, kThreads, kSmem, st>>>(a);
+    } else {
         own_fwd_kernel<D, ACT><<<grid, kThreads, 0, st>>>(a);
+    }
+    return true;
 }
 
 gdpa_status dispatch(bool bwd, PrefixPlan& p, const OwnArgs& a, int act, cudaStream_t st) {
     if (a.n == 0) return GDPA_OK;
+    bool ok = false;
     if (p.d == 128) {
         if (act == kSoftmax)
-            go<128, kSoftmax>(bwd, a, st);
+            ok = go<128, kSoftmax>(bwd, p.device, a, st);
         else
-            GDPA_DISPATCH_ACT(act, A, go<128, A>(bwd, a, st))
+            GDPA_DISPATCH_ACT(act, A, ok = go<128, A>(bwd, p.device, a, st))
     } else {
         if (act == kSoftmax)
-            go<64, kSoftmax>(bwd, a, st);
+            ok = go<64, kSoftmax>(bwd, p.device, a, st);
         else
-            GDPA_DISPATCH_ACT(act, A, go<64, A>(bwd, a, st))
+            GDPA_DISPATCH_ACT(act, A, ok = go<64, A>(bwd, p.device, a, st))
     }
     p.launches += 1;
     p.chain += 1;
-    return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+    return ok && cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
 }
 
 }  // namespace

@@ -151,14 +151,12 @@ __global__ void __launch_bounds__(kThreads) own_bwd_kernel(const OwnBwArgs a) {
                 for (int i = 0; i < 2; ++i) {
                     __nv_bfloat16* dst = (i ? a.dk : a.dv) + k_at + j * ks + 64 * h + 16 * q;
                     const float f = i ? a.alpha : 1.0f;
+                    uint32_t o[8];
 #pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        uint32_t o[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            o[e] = tc::pack_bf16x2(acc[i][2 * e][2 * x + w] * f, acc[i][2 * e + 1][2 * x + w] * f);
-                        reinterpret_cast<uint4*>(dst)[w] = make_uint4(o[0], o[1], o[2], o[3]);
-                    }
+                    for (int e = 0; e < 8; ++e)
+                        o[e] = tc::pack_bf16x2(acc[i][2 * (e & 3)][2 * x + (e >> 2)] * f,
+                                               acc[i][2 * (e & 3) + 1][2 * x + (e >> 2)] * f);
+                    store_sector(dst, o, !(((uintptr_t)a.dk | (uintptr_t)a.dv) & 31));
                 }
             }
         } else {

@@ -21,19 +21,20 @@
 // and the scores of item e + 2 into the same columns.  The sums leave through
 // a warpgroup of their own, and the next unit's keys load into whichever of
 // three pairs of buffers is free, so that short units follow one another
-// without a gap (32 ragged users of 64 .. 2048 keys: 46 us; with the keys in
-// one place and the two slots' warpgroups storing the sums 65 us).
+// without a gap (32 ragged users of 64 .. 2048 keys: 41 us; with the keys in
+// one place and the two slots' warpgroups storing the sums 65 us, with stores
+// of half sectors 46).
 // dQ walks blocks of 128 keys: S and dP go into registers at once and the next
 // block's scores into the freed columns, dS into one of two places of its own
 // (99 us against 108 in the form above, 1024 rows x 8192 keys x 16 heads).
 //
 // What bounds them, on those 1024 rows x 8192 keys x 16 heads with GELU: dK
-// and dV 132 us, products 128 x 64 x 16 whose operands take 120 of the 128
-// bytes shared memory gives a cycle, against loads and clears of their own;
-// halving the traffic would take 128-row items, for which TMEM has no room
-// beside 256 columns of sums.  dQ 99 us: 64 KB of K and V a block from L2, 5.4
-// TB/s in all.  Softmax batches of ragged users are bound by the few row tiles
-// a unit has.
+// and dV 128 us, the tensor pipe busy 46% of them: products 128 x 64 x 16 whose
+// operands take 120 of the 128 bytes shared memory gives a cycle, and a slot's
+// chain of scores, weights and sums; 128-row items would read less, but TMEM
+// has no room for them beside 256 columns of sums.  dQ 99 us, tensor pipe 49%:
+// 64 KB of K and V a block, 5.4 TB/s in all, arrive late for the issuer.
+// Softmax batches of ragged users are bound by the few row tiles a unit has.
 //
 // Rows behind the last one of an item share its 16-row step: their weights are
 // zero by selection, and the rows themselves are cleared in shared memory so
@@ -424,6 +425,7 @@ __device__ __forceinline__ void kv_drain(const BwArgs& a, uint64_t* bars, uint32
         const int split = u.flags / kUnitPart;
         const int64_t at = ((int64_t)(u.k0 + key) * a.Hkv + u.hk) * D;
         __nv_bfloat16 *dv = (own ? a.dv : a.dvp) + at, *dk = (own ? a.dk : a.dkp) + at;
+        const bool wide = !(((uintptr_t)dv | (uintptr_t)dk) & 31);
         if (u.ntok == 0) {   // keys that no row sees
             if (real)
                 for (int c = 0; c < D / 8; ++c)
@@ -453,12 +455,13 @@ __device__ __forceinline__ void kv_drain(const BwArgs& a, uint64_t* bars, uint32
                                         __uint_as_float(v[4 * i + 2]) * f, __uint_as_float(v[4 * i + 3]) * f);
             } else if (real) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t o[4];
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t o[8];
 #pragma unroll
-                    for (int w = 0; w < 4; ++w)
-                        o[w] = pack_bf16x2(__uint_as_float(v[8 * i + 2 * w]) * f, __uint_as_float(v[8 * i + 2 * w + 1]) * f);
-                    reinterpret_cast<uint4*>((second ? dk : dv) + c)[i] = make_uint4(o[0], o[1], o[2], o[3]);
+                    for (int w = 0; w < 8; ++w)
+                        o[w] = pack_bf16x2(__uint_as_float(v[16 * i + 2 * w]) * f,
+                                           __uint_as_float(v[16 * i + 2 * w + 1]) * f);
+                    store_sector((second ? dk : dv) + c + 16 * i, o, wide);
                 }
             }
         }

@@ -351,6 +351,29 @@ def test_many_rows_on_few_keys(shape, act, dt, d):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dt,d", [("bf16", 128), ("bf16", 64), ("f32", 32)])
+def test_rows_aligned_to_16_bytes_only(dt, d):
+    """Every tensor 16 bytes past a 32-byte boundary: the same bits."""
+    H, Hkv = 4, 2
+    plan, x, o, lse, grads = run(RAGGED, H, Hkv, d, dt, "softmax")
+
+    def moved(t):
+        step = 16 // t.element_size()
+        y = torch.empty(t.numel() + 2 * step, dtype=t.dtype, device="cuda")
+        at = step if y.data_ptr() % 32 == 0 else 2 * step
+        y = y[at:at + t.numel()].view(t.shape)
+        assert y.data_ptr() % 32 == 16
+        return y.copy_(t)
+    kw = dict(alpha=d ** -0.5)
+    m = [moved(t) for t in x]
+    o2, _ = gd.gdpa_prefix_softmax_fwd(plan, *m[:5], o=moved(o), **kw)
+    outs = dict(zip(("dq", "dkp", "dvp", "dk", "dv"), (moved(g).fill_(7.0) for g in grads)))
+    got = gd.gdpa_prefix_softmax_bwd(plan, *m[:5], moved(o), m[5], lse, **outs, **kw)
+    assert torch.equal(o2, o)
+    for a, b in zip(got, grads):
+        assert torch.equal(a, b)
+
+
 def test_refusals():
     offs = batch([5], [4], [1], [30])
     x = make(offs, 2, 2, 32, "f32")
