@@ -165,6 +165,10 @@ bool launch_kernel(void (*kern)(P...), dim3 grid, int threads, int smem, cudaStr
 __device__ __forceinline__ void grid_let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// A part's maximum, for the merge, which passes over parts whose maximum is
+// -inf (nothing visible): one whose only scores are NaN must count.
+__device__ __forceinline__ float counted(float m, float l) { return l != l && m == -INFINITY ? 0.0f : m; }
+
 // 32 bytes of a row: as one store, a whole sector, where the row is aligned to
 // it.  (Halves of sectors stored one after the other cost the gradients of the
 // own keys 54 us, not 47, in a training batch of 32 users.)

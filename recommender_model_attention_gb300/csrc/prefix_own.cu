@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 4) own_fwd_kernel(const OwnArgs a) {
         for (int w = 0; w < 2; ++w) {
             for (int o = 4; o < 32; o <<= 1) l[w] += __shfl_xor_sync(~0u, l[w], o);
             if (g == 0 && 2 * q + w < rows.nrows)
-                reinterpret_cast<float2*>(a.ml)[part + rows.row0 + 2 * q + w] = make_float2(m[w], l[w]);
+                reinterpret_cast<float2*>(a.ml)[part + rows.row0 + 2 * q + w] = make_float2(counted(m[w], l[w]), l[w]);
         }
     }
 }

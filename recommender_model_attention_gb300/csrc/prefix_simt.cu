@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads) simt_rows_kernel(const SimtArgs a) {
         if (row >= nrows) break;
         if (lane < c4) out[lane * nrows + row] = acc[w];
         if (!BWD && ACT == kSoftmax && lane == 0)   // maximum in base 2, as the merge takes it
-            reinterpret_cast<float2*>(a.ml)[(int64_t)part + row] = make_float2(m[w] * kLog2e, l[w]);
+            reinterpret_cast<float2*>(a.ml)[(int64_t)part + row] = make_float2(counted(m[w] * kLog2e, l[w]), l[w]);
     }
 }
 
@@ -452,11 +452,11 @@ __global__ void __launch_bounds__(256, 4) merge_kernel(const PrefixTile* tiles, 
             axpy4(acc, w, v[u]);
         }
     }
-    const float inv = !softmax ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = !softmax ? 1.f : sum == 0.f ? 0.f : 1.f / sum;   // (a NaN stays one)
     const int64_t at = (int64_t)tok * H + t.hk * r + j;
     st4(out + at * d + 4 * c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
     if (softmax && lse && c == 0)
-        lse[at] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994530942f : -INFINITY;
+        lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
 }
 
 // delta = dO . O of every row, a warp a row

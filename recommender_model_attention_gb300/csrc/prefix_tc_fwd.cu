@@ -266,6 +266,13 @@ __device__ __forceinline__ float2 exp2_poly(float2 t) {
     return make_float2(t.x < -126.0f ? 0.0f : a, t.y < -126.0f ? 0.0f : b);
 }
 
+// the largest of three, NaN if any is
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
+
 template <int D, int ACT>
 __device__ __forceinline__ void pf_rows(const PfParams& prm, uint8_t* smem, uint64_t* bars, uint32_t tmem,
                                         int seg0, int seg1, const Abort& ab) {
@@ -326,8 +333,12 @@ __device__ __forceinline__ void pf_rows(const PfParams& prm, uint8_t* smem, uint
                 for (int e = 0; e < 128; e += 8)
 #pragma unroll
                     for (int u = 0; u < 4; ++u)
-                        m4[u] = fmaxf(fmaxf(m4[u], __uint_as_float(x[e + u])), __uint_as_float(x[e + 4 + u]));
-                const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * ks.c0;
+                        m4[u] = max3_nan(m4[u], __uint_as_float(x[e + u]), __uint_as_float(x[e + 4 + u]));
+                const float top = max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]) * ks.c0;
+                if (top != top) {   // (exp2_poly would take a NaN for a number)
+                    sum = top;
+                    if (ref == -INFINITY) ref = 0.0f;   // the part counts
+                }
                 const bool up = real && top > ref + kRise;   // also from -inf
                 if (__any_sync(0xffffffffu, up)) {
                     const float nref = up ? top : ref;

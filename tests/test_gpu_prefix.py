@@ -374,6 +374,29 @@ def test_rows_aligned_to_16_bytes_only(dt, d):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dt,d,kernel", [("bf16", 128, "auto"), ("bf16", 64, "auto"), ("f32", 32, "auto"),
+                                         ("bf16", 128, "simt")])
+@pytest.mark.parametrize("key", [0, 3, 4, 5, 130])
+def test_nan_scores_reach_the_rows_that_see_them(dt, d, kernel, key):
+    """A NaN key makes O and lse NaN for exactly the rows that see it: of a
+    group (prefix), or of a sample (its only own key, and one of many)."""
+    lq, lkv = [3, 1, 9, 70], [1, 0, 200, 140]
+    offs = batch(lq, lkv, [2, 2], [150, 0])
+    x = make(offs, 2, 2, d, dt)
+    plan = gd.PrefixPlan(*offs, 2, d)
+    plan.set_kernel(kernel)
+    first, q_off = int(offs[1][2]), offs[0]
+    for where, row, rows in (("prefix", key, (0, 4)), ("only own", 0, (0, 3)), ("small own", first + key, (4, 13)),
+                             ("own", int(offs[1][3]) + key, (13, 83))):
+        y = [t.clone() for t in x]
+        y[1 if where == "prefix" else 3][row, 1] = float("nan")
+        o, lse = gd.gdpa_prefix_softmax_fwd(plan, *y[:5])
+        seen = torch.zeros(83, 2, dtype=torch.bool, device="cuda")
+        seen[rows[0]:rows[1], 1] = True
+        assert torch.equal(torch.isnan(lse), seen), where
+        assert torch.equal(torch.isnan(o).all(-1), seen) and torch.equal(torch.isnan(o).any(-1), seen), where
+
+
 def test_refusals():
     offs = batch([5], [4], [1], [30])
     x = make(offs, 2, 2, 32, "f32")
