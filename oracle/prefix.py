@@ -108,7 +108,7 @@ def bwd(offs, q, kp, vp, k, v, do, alpha, act, mask="none", window=0, o=None, ls
                 w, wr, wf, w1, wx = terms[t]
                 out[n][at, h if n == "dq" else e] += scale * a(w, b)
                 for i, m in enumerate((wr + 2.0 ** -4 * wf, w1, wx)):
-                    size[n][i][at, h if n == "dq" else e] += scale * a(m, np.abs(b))
+                    size[n][i][at, h if n == "dq" else e] += abs(scale) * a(m, np.abs(b))
             add("dq", rows, "q", lambda w, b: w @ b, key, alpha)
             left = lambda s: (lambda w, b: w[:, s].T @ b)  # noqa: E731
             P, O = slice(0, np_), slice(np_, None)

@@ -65,7 +65,7 @@ void split_units(PrefixPlan& p) {
     std::vector<PrefixUnit> out;
     for (const PrefixUnit& u : p.units) {
         const int64_t tiles = cdiv(u.ntok, p.tpt);
-        if (2 * tiles <= 3 * share) {
+        if (2 * tiles <= 3 * share || p.n_unit_parts > 1 << 20) {   // (flags hold part numbers up to 2^23)
             out.push_back(u);
             continue;
         }

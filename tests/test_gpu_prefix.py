@@ -397,6 +397,57 @@ def test_nan_scores_reach_the_rows_that_see_them(dt, d, kernel, key):
         assert torch.equal(torch.isnan(o).all(-1), seen) and torch.equal(torch.isnan(o).any(-1), seen), where
 
 
+@pytest.mark.parametrize("dt,d", [("bf16", 128), ("bf16", 64), ("f32", 32)])
+@pytest.mark.parametrize("act", ["softmax", "silu"])
+@pytest.mark.parametrize("alpha", [0.0, -0.125])
+def test_scales_of_zero_and_below(alpha, act, dt, d):
+    run(RAGGED, 4, 2, d, dt, act, window=3, alpha=alpha)
+
+
+@pytest.mark.parametrize("dt,d", [("bf16", 128), ("f32", 32)])
+@pytest.mark.parametrize("offs", [batch([], [], [], []), batch([0, 0], [40, 0], [1, 1], [5, 300]),
+                                  batch([2], [0], [1], [0])])
+def test_nothing_to_do(offs, dt, d):
+    """No samples; keys without rows (gradients of zeros); rows without keys."""
+    plan, x, o, lse, grads = run(offs, 2, 2, d, dt, "softmax")
+    assert torch.all(o == 0) and torch.all(lse == -float("inf"))
+    for g in grads:
+        assert torch.all(g == 0)
+
+
+def test_two_host_threads_share_a_plan():
+    import threading
+    offs = batch([5, 60, 1], [4, 70, 0], [2, 1], [300, 600])
+    d = 128
+    plan = gd.PrefixPlan(*offs, 4, d, kv_heads=2)
+    x = [make(offs, 4, 2, d, "bf16", seed=i) for i in range(2)]
+    want = []
+    for y in x:
+        o, lse = gd.gdpa_prefix_softmax_fwd(plan, *y[:5])
+        want.append((o, gd.gdpa_prefix_softmax_bwd(plan, *y[:5], o, y[5], lse)))
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        y, st = x[i], torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            for _ in range(10):
+                o, lse = gd.gdpa_prefix_softmax_fwd(plan, *y[:5])
+                got[i].append((o, gd.gdpa_prefix_softmax_bwd(plan, *y[:5], o, y[5], lse)))
+        st.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        assert len(got[i]) == 10
+        for o, g in got[i]:
+            assert torch.equal(o, want[i][0])
+            for a, b in zip(g, want[i][1]):
+                assert torch.equal(a, b)
+
+
 def test_refusals():
     offs = batch([5], [4], [1], [30])
     x = make(offs, 2, 2, 32, "f32")
