@@ -62,13 +62,11 @@ struct PrefixTile {
 static_assert(sizeof(PrefixTile) == 32, "PrefixTile layout");
 
 // Per token, its own keys: head hk's parts are at part + (hk * layers + i) *
-// rows, the token's rows there from row0 on; layers = 0 without own keys.  The
-// keys themselves: rows [k0, k0 + nk), the token at position i of its sample.
+// rows, the token's rows there from row0 on; layers = 0 without own keys.
 struct PrefixOwn {
     int32_t part, row0, layers, rows;
-    int32_t k0, nk, i, small;
 };
-static_assert(sizeof(PrefixOwn) == 32, "PrefixOwn layout");
+static_assert(sizeof(PrefixOwn) == 16, "PrefixOwn layout");
 
 struct PrefixPlan {
     int device = 0;
@@ -79,6 +77,7 @@ struct PrefixPlan {
     int64_t Tq = 0, Tkv = 0, Tp = 0;
     int64_t n_part_rows = 0;
     int64_t row_blocks = 0;      // 32-row blocks of the pieces' slots
+    int max_layers = 0;          // most prefix parts of a row tile
     std::vector<PrefixPiece> pieces; // the tensor-core family's, then the small own ones
     std::vector<int32_t> seg;        // [S + 1] first piece of each CTA
     std::vector<PrefixTile> tiles;

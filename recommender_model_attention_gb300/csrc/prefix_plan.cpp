@@ -99,7 +99,7 @@ gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t
     const int tpt = p.tpt;
     int64_t parts = 0;   // rows of the workspace given out
     std::vector<Unit> units;
-    p.own.assign((size_t)p.Tq, PrefixOwn{0, 0, 0, 0, 0, 0, 0, 0});
+    p.own.assign((size_t)p.Tq, PrefixOwn{0, 0, 0, 0});
     for (int g = 0; g < p.G; ++g) {
         const int32_t t0 = q_off[group_off[g]], nt = q_off[group_off[g + 1]] - t0;
         const int32_t np = prefix_off[g + 1] - prefix_off[g];
@@ -139,8 +139,6 @@ gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t
             // hull of the keys these rows see
             const int32_t lo = windowed ? std::max(0, i - p.window + 1) : 0;
             const int32_t hi = windowed ? std::min(lk, i + nA + nB) : lk;
-            for (int32_t t = 0; t < nA + nB; ++t)
-                p.own[q_off[b] + i + t] = PrefixOwn{0, 0, 0, 0, kv_off[b], lk, i + t, small ? 1 : 0};
             if (hi > lo) {
                 Unit u{};
                 u.tileA = u.tileB = -1;
@@ -294,6 +292,8 @@ gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t
     for (PrefixPiece& q : p.pieces) q.pad = 0;
     for (const Unit& u : small_units) p.pieces.push_back(u.p);
     p.n_part_rows = parts;
+    p.max_layers = 0;
+    for (const PrefixTile& t : p.tiles) p.max_layers = std::max(p.max_layers, t.layers);
     p.row_blocks = 0;
     for (const PrefixPiece& q : p.pieces) {
         const int32_t second = q.flags & kPieceDual ? q.nA : q.nB;

@@ -378,12 +378,12 @@ __global__ void __launch_bounds__(256) join_kernel(const PrefixUnit* joins, cons
 }
 
 // Join the parts of 8 rows of a tile: a thread per (row, 4 columns).  The
-// first four layers, usually all, are loaded together before anything is known
-// of them; further ones four at a time, a warp's four threads of a row sharing
-// a look at their maxima.  Few registers, so that many blocks hide the chain of
-// loads (tile, token, layers) of each other.
-template <typename E>
-__global__ void __launch_bounds__(256, 4) merge_kernel(const PrefixTile* tiles, const PrefixOwn* owns,
+// first kAtOnce layers, usually all, are loaded together before anything is
+// known of them; further ones as many at a time, a warp's four threads of a row
+// sharing a look at their maxima.  Few registers, so that many blocks hide the
+// chain of loads (tile, token, layers) of each other.
+template <typename E, int kAtOnce>
+__global__ void __launch_bounds__(256, kAtOnce > 4 ? 2 : 4) merge_kernel(const PrefixTile* tiles, const PrefixOwn* owns,
                                                     const float* parts, const float* ml, E* out,
                                                     float* lse, int H, int r, int d, int softmax) {
     const PrefixTile t = tiles[blockIdx.x];
@@ -392,8 +392,9 @@ __global__ void __launch_bounds__(256, 4) merge_kernel(const PrefixTile* tiles, 
     if (blockIdx.y * 8 >= nrows) return;
     const bool real = row < nrows;
     const int tl = real ? row / r : 0, j = row - tl * r, tok = t.tok + tl;
-    PrefixOwn ow = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (real) ow = owns[tok];
+    int4 own4 = make_int4(0, 0, 0, 0);
+    if (real) own4 = __ldg(reinterpret_cast<const int4*>(owns + tok));
+    const PrefixOwn ow = {own4.x, own4.y, own4.z, own4.w};
     const int orow = ow.row0 + j, total = real ? t.layers + ow.layers : 0;
     const int64_t own0 = (int64_t)ow.part + (int64_t)t.hk * ow.layers * ow.rows;
     const float2* st = reinterpret_cast<const float2*>(ml);
@@ -406,11 +407,11 @@ __global__ void __launch_bounds__(256, 4) merge_kernel(const PrefixTile* tiles, 
         at = pre ? row : orow;
         return pre ? (int64_t)t.part + (int64_t)x * nrows : own0 + (int64_t)(x - t.layers) * ow.rows;
     };
-    float2 s[4];
-    float4 v[4];
-    auto load4 = [&](int x0) {
+    float2 s[kAtOnce];
+    float4 v[kAtOnce];
+    auto load = [&](int x0) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < kAtOnce; ++u) {
             s[u] = make_float2(-INFINITY, 0.f);
             v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (x0 + u < total && c < c4) {
@@ -422,11 +423,11 @@ __global__ void __launch_bounds__(256, 4) merge_kernel(const PrefixTile* tiles, 
         }
     };
     grid_wait_previous();
-    load4(0);
+    load(0);
     float top = -INFINITY, ref = 0.f, sum = 0.f;
     if (softmax) {
 #pragma unroll 4
-        for (int x = 4 + (lane >> 3); x < total; x += 4) {
+        for (int x = kAtOnce + (lane >> 3); x < total; x += 4) {
             int n, at;
             const int64_t p = place(x, n, at);
             top = fmaxf(top, st[p + at].x);
@@ -434,15 +435,15 @@ __global__ void __launch_bounds__(256, 4) merge_kernel(const PrefixTile* tiles, 
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
 #pragma unroll
-        for (int u = 0; u < 4; ++u) top = fmaxf(top, s[u].x);
+        for (int u = 0; u < kAtOnce; ++u) top = fmaxf(top, s[u].x);
         ref = top == -INFINITY ? 0.f : top;
     }
     if (!real || c >= c4) return;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int x0 = 0; x0 < total; x0 += 4) {
-        if (x0 > 0) load4(x0);
+    for (int x0 = 0; x0 < total; x0 += kAtOnce) {
+        if (x0 > 0) load(x0);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < kAtOnce; ++u) {
             float w = 1.f;
             if (softmax) {
                 if (s[u].x == -INFINITY) continue;   // no such layer, or nothing visible in it
@@ -580,11 +581,17 @@ gdpa_status launch_prefix_merge(PrefixPlan& p, gdpa_dtype dt, void* out, float* 
     const float *parts = p.d_parts, *ml = p.d_ml;
     const bool early = p.chain > 0;
     const int sm = softmax;
-    const bool ok = dt == GDPA_BF16
-                        ? launch_kernel(merge_kernel<__nv_bfloat16>, grid, threads, 0, st, early, p.dev_tiles(),
-                                        p.dev_own(), parts, ml, (__nv_bfloat16*)out, lse, p.H, p.r, p.d, sm)
-                        : launch_kernel(merge_kernel<float>, grid, threads, 0, st, early, p.dev_tiles(), p.dev_own(),
-                                        parts, ml, (float*)out, lse, p.H, p.r, p.d, sm);
+    auto go = [&](auto* o, auto kern) {
+        return launch_kernel(kern, grid, threads, 0, st, early, p.dev_tiles(), p.dev_own(), parts, ml, o, lse, p.H,
+                             p.r, p.d, sm);
+    };
+    using B = __nv_bfloat16;
+    // many layers are few rows' (a decoding step): rounds of 12 loads (38 layers
+    // of 4 tiles: 9 us, 13 with 4; 5 layers of 32 tiles 10 and 9)
+    const bool deep = p.max_layers > 8;
+    const bool ok = dt == GDPA_BF16 ? (deep ? go((B*)out, merge_kernel<B, 12>) : go((B*)out, merge_kernel<B, 4>))
+                    : deep          ? go((float*)out, merge_kernel<float, 12>)
+                                    : go((float*)out, merge_kernel<float, 4>);
     p.launches += 1;
     return ok ? GDPA_OK : GDPA_ERR_CUDA;
 }
