@@ -125,12 +125,13 @@ def lib():
 
 # What the calls need of torch, looked up once by lib(): these entry points are
 # also used for a handful of rows, where marshalling is most of the time.
-_DTYPE_ID = _POSITION_BITS = _empty = _raw_stream = _current_device = _on_device = None
+_DTYPE_ID = _POSITION_BITS = _empty = _raw_stream = _current_device = _on_device = _f32 = None
 
 
 def _torch_names():
-    global _DTYPE_ID, _POSITION_BITS, _empty, _raw_stream, _current_device, _on_device
+    global _DTYPE_ID, _POSITION_BITS, _empty, _raw_stream, _current_device, _on_device, _f32
     import torch
+    _f32 = torch.float32
     _DTYPE_ID = {torch.bfloat16: 0, torch.float32: 1}
     _POSITION_BITS = {torch.int32: 32, torch.int64: 64}
     _empty = torch.empty
@@ -815,8 +816,7 @@ def _prefix_tensor(t, shape, plan, name, dtype):
 
 
 def _prefix_lse(lse, plan):
-    import torch
-    if (lse.dtype != torch.float32 or lse.shape != plan._lse or not lse.is_contiguous()
+    if (lse.dtype != _f32 or lse.shape != plan._lse or not lse.is_contiguous()
             or lse.device != plan.device):
         raise ValueError("lse must be a contiguous float32 [Tq, H] tensor on the plan's device")
     return lse.data_ptr() if plan.Tq else None
@@ -846,12 +846,14 @@ def _prefix_call(f, what, plan, args, alpha, act, stream):
             _ok(f(plan.handle, *args), what)
 
 
-def _prefix_fwd(plan, q, kp, vp, k, v, o, lse, alpha, act, stream):
+def _prefix_fwd(plan, q, kp, vp, k, v, o, lse_ptr, alpha, act, stream):
     args = _prefix_inputs(plan, q, kp, vp, k, v)
     if o is None:
         o = _empty(plan._rows, dtype=q.dtype, device=plan.device)
-    args += (_prefix_tensor(o, plan._rows, plan, "o", q.dtype),
-             None if lse is None else _prefix_lse(lse, plan))
+        out = o.data_ptr()
+    else:
+        out = _prefix_tensor(o, plan._rows, plan, "o", q.dtype)
+    args += (out, lse_ptr)
     _prefix_call(lib().gdpa_prefix_fwd, "gdpa_prefix_fwd", plan, args, alpha, act, stream)
     return o
 
@@ -867,10 +869,14 @@ def gdpa_prefix_fwd(plan: PrefixPlan, q, kp, vp, k=None, v=None, o=None, alpha=N
 def gdpa_prefix_softmax_fwd(plan: PrefixPlan, q, kp, vp, k=None, v=None, o=None, lse=None,
                             alpha=None, stream=None):
     """The softmax variant over prefix and own keys together: (O, lse)."""
-    import torch
+    if plan.device is None:
+        raise ValueError("a host-only plan cannot launch")
     if lse is None:
-        lse = _empty(plan._lse, dtype=torch.float32, device=plan.device)
-    return _prefix_fwd(plan, q, kp, vp, k, v, o, lse, alpha, "softmax", stream), lse
+        lse = _empty(plan._lse, dtype=_f32, device=plan.device)
+        ptr = lse.data_ptr()
+    else:
+        ptr = _prefix_lse(lse, plan)
+    return _prefix_fwd(plan, q, kp, vp, k, v, o, ptr, alpha, "softmax", stream), lse
 
 
 def _prefix_bwd(plan, q, kp, vp, k, v, o, do, lse, grads, alpha, act, stream):
@@ -881,8 +887,11 @@ def _prefix_bwd(plan, q, kp, vp, k, v, o, do, lse, grads, alpha, act, stream):
     out = []
     for g, shape, name in zip(grads, (plan._rows, plan._prefix, plan._prefix, plan._keys, plan._keys),
                               ("dq", "dkp", "dvp", "dk", "dv")):
-        g = _empty(shape, dtype=dt, device=plan.device) if g is None else g
-        args += (_prefix_tensor(g, shape, plan, name, dt),)
+        if g is None:
+            g = _empty(shape, dtype=dt, device=plan.device)
+            args += (g.data_ptr(),)
+        else:
+            args += (_prefix_tensor(g, shape, plan, name, dt),)
         out.append(g)
     _prefix_call(lib().gdpa_prefix_bwd, "gdpa_prefix_bwd", plan, args, alpha, act, stream)
     return tuple(out)
