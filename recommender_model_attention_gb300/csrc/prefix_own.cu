@@ -249,6 +249,11 @@ __device__ __forceinline__ void load_stage(__nv_bfloat16* to, const __nv_bfloat1
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
+// a pair less its rounding to bf16, rounded itself
+__device__ __forceinline__ uint32_t rest_of(float x, float y, uint32_t rounded) {
+    return tc::pack_bf16x2(x - __uint_as_float(rounded << 16), y - __uint_as_float(rounded & 0xffff0000u));
+}
+
 __device__ __forceinline__ uint4 lds16(const __nv_bfloat16* p) { return *reinterpret_cast<const uint4*>(p); }
 
 // Backward of units of at most 8 rows.
@@ -272,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 2) own_bwd8_kernel(const OwnArgs a) 
     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
     const ActScale sc = act_scale<ACT>(a.alpha);
     // rows as the second operand of the scores (row g) and of dK, dV (rows
-    // 2 q, 2 q + 1; the contraction's rows 8 .. 15 are zeros)
+    // 2 q, 2 q + 1, twice)
     uint4 qb[kC], ob[kC], qv[2][kW], ov[2][kW];
     float l2[2] = {INFINITY, INFINITY}, dl[2] = {0.0f, 0.0f};
     int pos[2];
@@ -348,9 +353,12 @@ __global__ void __launch_bounds__(kThreads, 2) own_bwd8_kernel(const OwnArgs a) 
                 }
                 if (!ok) p[c] = ds[c] = 0.0f;
             }
-        // rows 2 q, 2 q + 1 of keys g and g + 8: the first operand of dV, dK
+        // rows 2 q, 2 q + 1 of keys g and g + 8: the first operand of dV, dK;
+        // what bf16 leaves of them takes the contraction's other 8 rows
         const uint32_t p0 = tc::pack_bf16x2(p[0], p[1]), p1 = tc::pack_bf16x2(p[2], p[3]);
         const uint32_t d0 = tc::pack_bf16x2(ds[0], ds[1]), d1 = tc::pack_bf16x2(ds[2], ds[3]);
+        const uint32_t p2 = rest_of(p[0], p[1], p0), p3 = rest_of(p[2], p[3], p1);
+        const uint32_t d2 = rest_of(ds[0], ds[1], d0), d3 = rest_of(ds[2], ds[3], d1);
 #pragma unroll
         for (int i = 0; i < 2; ++i)   // dV, then dK
 #pragma unroll
@@ -360,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 2) own_bwd8_kernel(const OwnArgs a) 
                 for (int e = 0; e < 8; ++e) {
                     o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.0f;
                     const uint32_t b = i ? pair_of(qv[0][h], qv[1][h], e) : pair_of(ov[0][h], ov[1][h], e);
-                    mma16816(o[e], i ? d0 : p0, i ? d1 : p1, 0u, 0u, b, 0u);
+                    mma16816(o[e], i ? d0 : p0, i ? d1 : p1, i ? d2 : p2, i ? d3 : p3, b, b);
                 }
                 // product e: columns 64 h + 16 q + e and + 8 + e of keys g, g + 8
                 const float f = i ? a.alpha : 1.0f;

@@ -294,11 +294,15 @@ gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t
     p.n_part_rows = parts;
     p.max_layers = 0;
     for (const PrefixTile& t : p.tiles) p.max_layers = std::max(p.max_layers, t.layers);
-    p.row_blocks = 0;
+    p.row_blocks = p.row_blocks8 = 0;
+    auto count = [&](int64_t rows) {
+        p.row_blocks += cdiv(rows, 32);
+        p.row_blocks8 += cdiv(rows, 8);
+    };
     for (const PrefixPiece& q : p.pieces) {
         const int32_t second = q.flags & kPieceDual ? q.nA : q.nB;
-        if (q.part0 >= 0) p.row_blocks += cdiv((int64_t)q.nA * p.r, 32);
-        if (q.part1 >= 0) p.row_blocks += cdiv((int64_t)second * p.r, 32);
+        if (q.part0 >= 0) count((int64_t)q.nA * p.r);
+        if (q.part1 >= 0) count((int64_t)second * p.r);
     }
 
     // backward: one unit per 128-key block, against all rows that see it

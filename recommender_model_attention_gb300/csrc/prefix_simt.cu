@@ -188,17 +188,27 @@ __global__ void __launch_bounds__(kThreads) simt_rows_kernel(const SimtArgs a) {
         float s[R], dp[R];
 #pragma unroll
         for (int w = 0; w < R; ++w) s[w] = dp[w] = 0.f;
-        for (int c = 0; c < c4; ++c) {
-            const float4 kv = *reinterpret_cast<const float4*>(K + lane * ks + 4 * c);
+        // (16 columns at a time: shorter chains of roundings)
+        for (int c0 = 0; c0 < c4; c0 += 4) {
+            float s16[R], dp16[R];
 #pragma unroll
-            for (int w = 0; w < R; ++w)
-                s[w] = dot4(kv, *reinterpret_cast<const float4*>(Q + (warp * R + w) * qs + 4 * c), s[w]);
-            if constexpr (BWD) {
-                const float4 vv = *reinterpret_cast<const float4*>(V + lane * ks + 4 * c);
+            for (int w = 0; w < R; ++w) s16[w] = dp16[w] = 0.f;
+            for (int c = c0; c < min(c0 + 4, c4); ++c) {
+                const float4 kv = *reinterpret_cast<const float4*>(K + lane * ks + 4 * c);
 #pragma unroll
                 for (int w = 0; w < R; ++w)
-                    dp[w] = dot4(vv, *reinterpret_cast<const float4*>(DO + (warp * R + w) * qs + 4 * c),
-                                 dp[w]);
+                    s16[w] = dot4(kv, *reinterpret_cast<const float4*>(Q + (warp * R + w) * qs + 4 * c), s16[w]);
+                if constexpr (BWD) {
+                    const float4 vv = *reinterpret_cast<const float4*>(V + lane * ks + 4 * c);
+#pragma unroll
+                    for (int w = 0; w < R; ++w)
+                        dp16[w] = dot4(vv, *reinterpret_cast<const float4*>(DO + (warp * R + w) * qs + 4 * c), dp16[w]);
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < R; ++w) {
+                s[w] += s16[w];
+                if (BWD) dp[w] += dp16[w];
             }
         }
         const int jpos = pc.j0 + key + lane;
@@ -295,13 +305,23 @@ __global__ void __launch_bounds__(kThreads) simt_keys_kernel(const SimtArgs a) {
         float s[kPer], dp[kPer];
 #pragma unroll
         for (int w = 0; w < kPer; ++w) s[w] = dp[w] = 0.f;
-        for (int c = 0; c < c4; ++c) {
-            const float4 qv = *reinterpret_cast<const float4*>(Q + lane * qs + 4 * c);
-            const float4 dv = *reinterpret_cast<const float4*>(DO + lane * qs + 4 * c);
+        for (int c0 = 0; c0 < c4; c0 += 4) {
+            float s16[kPer], dp16[kPer];
+#pragma unroll
+            for (int w = 0; w < kPer; ++w) s16[w] = dp16[w] = 0.f;
+            for (int c = c0; c < min(c0 + 4, c4); ++c) {
+                const float4 qv = *reinterpret_cast<const float4*>(Q + lane * qs + 4 * c);
+                const float4 dv = *reinterpret_cast<const float4*>(DO + lane * qs + 4 * c);
+#pragma unroll
+                for (int w = 0; w < kPer; ++w) {
+                    s16[w] = dot4(qv, *reinterpret_cast<const float4*>(K + (warp * kPer + w) * ks + 4 * c), s16[w]);
+                    dp16[w] = dot4(dv, *reinterpret_cast<const float4*>(V + (warp * kPer + w) * ks + 4 * c), dp16[w]);
+                }
+            }
 #pragma unroll
             for (int w = 0; w < kPer; ++w) {
-                s[w] = dot4(qv, *reinterpret_cast<const float4*>(K + (warp * kPer + w) * ks + 4 * c), s[w]);
-                dp[w] = dot4(dv, *reinterpret_cast<const float4*>(V + (warp * kPer + w) * ks + 4 * c), dp[w]);
+                s[w] += s16[w];
+                dp[w] += dp16[w];
             }
         }
         __syncwarp();
@@ -522,11 +542,13 @@ gdpa_status rows_of(PrefixPlan& p, int act, const SimtArgs& a, cudaStream_t st) 
     // 2 rows a warp: a quarter of the instructions on a warp's way, for four
     // times the reads of keys.  Better where few blocks are there to hide them
     // (4 users of 40 rows, 500 keys, d = 32: 20 us, 27 with 8 rows; one row
-    // against 4096 keys, d = 128: 32 and 42), and up to 48 columns always (8
-    // users of 256 rows, 2000 keys, 4 heads, d = 48: 372 and 456); from 64 on
-    // 8 rows (the same with d = 64: 279, 356 with 2; 512 rows, d = 128: 421, 698).
-    return p.d < 64 || p.row_blocks <= 2 * p.S ? rows_t<E, BWD, 2>(p, act, a, st)
-                                               : rows_t<E, BWD, kPer>(p, act, a, st);
+    // against 4096 keys, d = 128: 32 and 42), where samples have few rows, and up
+    // to 48 columns always (8 users of 256 rows, 2000 keys, 4 heads, d = 48: 372
+    // and 456); from 64 on 8 rows (the same with d = 64: 279, 356 with 2; 512
+    // rows, d = 128: 421, 698).
+    return p.d < 64 || p.row_blocks <= 2 * p.S || p.row_blocks8 <= 2 * p.row_blocks
+               ? rows_t<E, BWD, 2>(p, act, a, st)
+               : rows_t<E, BWD, kPer>(p, act, a, st);
 }
 
 template <typename E>
@@ -586,9 +608,10 @@ gdpa_status launch_prefix_merge(PrefixPlan& p, gdpa_dtype dt, void* out, float* 
                              p.r, p.d, sm);
     };
     using B = __nv_bfloat16;
-    // many layers are few rows' (a decoding step): rounds of 12 loads (38 layers
-    // of 4 tiles: 9 us, 13 with 4; 5 layers of 32 tiles 10 and 9)
-    const bool deep = p.max_layers > 8;
+    // few row tiles of many layers (a decoding step): rounds of 12 loads, where
+    // they leave room for all blocks at once (38 layers of 4 tiles: 9 us, 13 with
+    // 4; up to 10 layers of 122 tiles 16 and 12)
+    const bool deep = p.max_layers > 8 && (int64_t)grid.x * grid.y <= 2 * p.S;
     const bool ok = dt == GDPA_BF16 ? (deep ? go((B*)out, merge_kernel<B, 12>) : go((B*)out, merge_kernel<B, 4>))
                     : deep          ? go((float*)out, merge_kernel<float, 12>)
                                     : go((float*)out, merge_kernel<float, 4>);
