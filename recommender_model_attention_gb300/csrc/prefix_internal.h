@@ -76,7 +76,8 @@ struct PrefixPlan {
     int kernel = GDPA_KERNEL_AUTO;
     int64_t Tq = 0, Tkv = 0, Tp = 0;
     int64_t n_part_rows = 0;
-    int64_t row_blocks = 0, row_blocks8 = 0;   // 32-row and 8-row blocks of the pieces' slots
+    int64_t row_blocks = 0;      // 32-row blocks of the pieces' slots
+    int64_t row_work = 0, row_work8 = 0;   // keys of all 32-row and of all 8-row blocks
     int max_layers = 0;          // most prefix parts of a row tile
     std::vector<PrefixPiece> pieces; // the tensor-core family's, then the small own ones
     std::vector<int32_t> seg;        // [S + 1] first piece of each CTA

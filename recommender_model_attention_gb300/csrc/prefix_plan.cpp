@@ -294,15 +294,18 @@ gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t
     p.n_part_rows = parts;
     p.max_layers = 0;
     for (const PrefixTile& t : p.tiles) p.max_layers = std::max(p.max_layers, t.layers);
-    p.row_blocks = p.row_blocks8 = 0;
-    auto count = [&](int64_t rows) {
+    p.row_blocks = 0;
+    p.row_work = p.row_work8 = 0;
+    auto count = [&](const PrefixPiece& q, int64_t rows) {
+        const int64_t keys = q.flags & kPieceDual ? cdiv(q.nk, 2) : q.nk;
         p.row_blocks += cdiv(rows, 32);
-        p.row_blocks8 += cdiv(rows, 8);
+        p.row_work += cdiv(rows, 32) * keys;
+        p.row_work8 += cdiv(rows, 8) * keys;
     };
     for (const PrefixPiece& q : p.pieces) {
         const int32_t second = q.flags & kPieceDual ? q.nA : q.nB;
-        if (q.part0 >= 0) count((int64_t)q.nA * p.r);
-        if (q.part1 >= 0) count((int64_t)second * p.r);
+        if (q.part0 >= 0) count(q, (int64_t)q.nA * p.r);
+        if (q.part1 >= 0) count(q, (int64_t)second * p.r);
     }
 
     // backward: one unit per 128-key block, against all rows that see it

@@ -74,6 +74,20 @@ __device__ __forceinline__ void load_tile(float* dst, int stride, const E* src, 
     }
 }
 
+// The same of float32 rows, copied while the threads go on (rows past n as
+// zeros); tile_arrived waits for the thread's own copies.
+__device__ __forceinline__ void copy_tile(float* dst, int stride, const float* src, int64_t row_stride, int n, int d) {
+    const int c4 = d / 4;
+    for (int i = threadIdx.x; i < kRows * c4; i += kThreads) {
+        const int row = i / c4, c = i - row * c4;
+        const float* from = src + (row < n ? row : 0) * row_stride + 4 * c;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst + row * stride + 4 * c)),
+                     "l"(from), "r"(row < n ? 16 : 0)
+                     : "memory");
+    }
+}
+__device__ __forceinline__ void tile_arrived() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // packed rows [row0, row0 + ROWS) of tokens from `tok` (row = token * r + head
 // within the group of query heads), rows >= nrows as zeros
 template <int ROWS, typename E>
@@ -149,9 +163,12 @@ __global__ void __launch_bounds__(kThreads) simt_rows_kernel(const SimtArgs a) {
     const int qs = a.d, ks = a.d + 4;
     float* Q = sm;                       // [4 R][d]
     float* DO = Q + kBlock * qs;          // [4 R][d] (BWD)
-    float* K = DO + (BWD ? kBlock * qs : 0);   // [32][d + 4]
-    float* V = K + kRows * ks;
-    float* W = V + kRows * ks + warp * kRows * R;   // weights [32 keys][R rows]
+    // float32 keys, few rows: two tiles in turn, the next one copied meanwhile
+    // (8 rows a warp hide the loads behind more blocks: 512 rows, d = 128, 421
+    // us, 547 with the shared memory of two tiles and shorter sums)
+    constexpr int kTiles = sizeof(E) == 4 && R == 2 ? 2 : 1;
+    float* const KV = DO + (BWD ? kBlock * qs : 0);   // K, V: [32][d + 4] each
+    float* W = KV + kTiles * 2 * kRows * ks + warp * kRows * R;   // weights [32 keys][R rows]
     const E* kb = (const E*)(own ? a.k : a.kp);
     const E* vb = (const E*)(own ? a.v : a.vp);
     load_rows<kBlock>(Q, qs, (const E*)a.q, a, tok, pc.hk, row0, nrows);
@@ -177,38 +194,64 @@ __global__ void __launch_bounds__(kThreads) simt_rows_kernel(const SimtArgs a) {
             delta[w] = a.delta[at];
         }
     }
-    for (int key = dual ? slot * kBN : 0; key < pc.nk;
-         key += (dual && (key & 127) == 96) ? kRows + kBN : kRows) {
+    auto after = [&](int key) { return key + ((dual && (key & 127) == 96) ? kRows + kBN : kRows); };
+    auto fetch = [&](int key, float* K) {
         const int n = min(kRows, pc.nk - key);
-        __syncthreads();
-        const int64_t src = ((int64_t)(pc.k0 + key) * a.Hkv + pc.hk) * a.d;
-        load_tile(K, ks, kb + src, (int64_t)a.Hkv * a.d, n, a.d);
-        load_tile(V, ks, vb + src, (int64_t)a.Hkv * a.d, n, a.d);
-        __syncthreads();
+        const int64_t src = ((int64_t)(pc.k0 + key) * a.Hkv + pc.hk) * a.d, stride = (int64_t)a.Hkv * a.d;
+        if constexpr (kTiles == 2) {
+            copy_tile(K, ks, kb + src, stride, n, a.d);
+            copy_tile(K + kRows * ks, ks, vb + src, stride, n, a.d);
+        } else {
+            load_tile(K, ks, kb + src, stride, n, a.d);
+            load_tile(K + kRows * ks, ks, vb + src, stride, n, a.d);
+        }
+    };
+    int turn = 0;
+    const int key_first = dual ? slot * kBN : 0;
+    if (kTiles == 2 && key_first < pc.nk) fetch(key_first, KV);
+    for (int key = key_first; key < pc.nk; key = after(key)) {
+        const int n = min(kRows, pc.nk - key);
+        float *K = KV + turn * 2 * kRows * ks, *V = K + kRows * ks;
+        if constexpr (kTiles == 2) {
+            tile_arrived();
+            __syncthreads();   // and the tile before has been read
+            turn ^= 1;
+            if (after(key) < pc.nk) fetch(after(key), KV + turn * 2 * kRows * ks);
+        } else {
+            __syncthreads();
+            fetch(key, K);
+            __syncthreads();
+        }
         float s[R], dp[R];
 #pragma unroll
         for (int w = 0; w < R; ++w) s[w] = dp[w] = 0.f;
-        // (16 columns at a time: shorter chains of roundings)
-        for (int c0 = 0; c0 < c4; c0 += 4) {
-            float s16[R], dp16[R];
+        if constexpr (BWD) {   // 16 columns at a time: dP less delta cancels, so shorter chains of roundings
+            for (int c0 = 0; c0 < c4; c0 += 4) {
+                float s16[R], dp16[R];
 #pragma unroll
-            for (int w = 0; w < R; ++w) s16[w] = dp16[w] = 0.f;
-            for (int c = c0; c < min(c0 + 4, c4); ++c) {
+                for (int w = 0; w < R; ++w) s16[w] = dp16[w] = 0.f;
+                for (int c = c0; c < min(c0 + 4, c4); ++c) {
+                    const float4 kv = *reinterpret_cast<const float4*>(K + lane * ks + 4 * c);
+                    const float4 vv = *reinterpret_cast<const float4*>(V + lane * ks + 4 * c);
+#pragma unroll
+                    for (int w = 0; w < R; ++w) {
+                        const int at = (warp * R + w) * qs + 4 * c;
+                        s16[w] = dot4(kv, *reinterpret_cast<const float4*>(Q + at), s16[w]);
+                        dp16[w] = dot4(vv, *reinterpret_cast<const float4*>(DO + at), dp16[w]);
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < R; ++w) {
+                    s[w] += s16[w];
+                    dp[w] += dp16[w];
+                }
+            }
+        } else {
+            for (int c = 0; c < c4; ++c) {
                 const float4 kv = *reinterpret_cast<const float4*>(K + lane * ks + 4 * c);
 #pragma unroll
                 for (int w = 0; w < R; ++w)
-                    s16[w] = dot4(kv, *reinterpret_cast<const float4*>(Q + (warp * R + w) * qs + 4 * c), s16[w]);
-                if constexpr (BWD) {
-                    const float4 vv = *reinterpret_cast<const float4*>(V + lane * ks + 4 * c);
-#pragma unroll
-                    for (int w = 0; w < R; ++w)
-                        dp16[w] = dot4(vv, *reinterpret_cast<const float4*>(DO + (warp * R + w) * qs + 4 * c), dp16[w]);
-                }
-            }
-#pragma unroll
-            for (int w = 0; w < R; ++w) {
-                s[w] += s16[w];
-                if (BWD) dp[w] += dp16[w];
+                    s[w] = dot4(kv, *reinterpret_cast<const float4*>(Q + (warp * R + w) * qs + 4 * c), s[w]);
             }
         }
         const int jpos = pc.j0 + key + lane;
@@ -514,8 +557,10 @@ SimtArgs args_of(const PrefixPlan& p, const PrefixIO& io, const float* delta) {
 
 template <auto kKern>
 gdpa_status go(dim3 grid, int smem, PrefixPlan& p, const SimtArgs& a, cudaStream_t st) {
-    // the most any head dim takes (the dK, dV kernel's, d = 128)
-    constexpr int kMost = (2 * kRows * 128 + 2 * kRows * 132 + 8 * kRows * kPer) * 4;
+    // the most any kernel takes, at d = 128: dK and dV, or dQ with 2 rows a warp
+    constexpr int kKeysMost = (2 * kRows * 128 + 2 * kRows * 132 + 8 * kRows * kPer) * 4;
+    constexpr int kRowsMost = (2 * 8 * 128 + 4 * kRows * 132 + 4 * kRows * 2) * 4;
+    constexpr int kMost = kKeysMost > kRowsMost ? kKeysMost : kRowsMost;
     static std::atomic<uint64_t> done{0};
     if (!allow_smem(kKern, kMost, p.device, done)) return GDPA_ERR_CUDA;
     kKern<<<grid, kThreads, smem, st>>>(a);
@@ -530,7 +575,8 @@ gdpa_status go(dim3 grid, int smem, PrefixPlan& p, const SimtArgs& a, cudaStream
 template <typename E, bool BWD, int R>
 gdpa_status rows_t(PrefixPlan& p, int act, const SimtArgs& a, cudaStream_t st) {
     gdpa_status s = GDPA_OK;
-    const int smem = ((BWD ? 2 : 1) * 4 * R * p.d + 2 * kRows * (p.d + 4) + 4 * kRows * R) * 4;
+    const int tiles = sizeof(E) == 4 && R == 2 ? 2 : 1;
+    const int smem = ((BWD ? 2 : 1) * 4 * R * p.d + tiles * 2 * kRows * (p.d + 4) + 4 * kRows * R) * 4;
     const dim3 grid((unsigned)p.pieces.size(), 2 * kBM / (4 * R));
     PREFIX_DISPATCH(act, s = (go<simt_rows_kernel<E, A, BWD, R>>(grid, smem, p, a, st)))
     return s;
@@ -546,7 +592,7 @@ gdpa_status rows_of(PrefixPlan& p, int act, const SimtArgs& a, cudaStream_t st) 
     // to 48 columns always (8 users of 256 rows, 2000 keys, 4 heads, d = 48: 372
     // and 456); from 64 on 8 rows (the same with d = 64: 279, 356 with 2; 512
     // rows, d = 128: 421, 698).
-    return p.d < 64 || p.row_blocks <= 2 * p.S || p.row_blocks8 <= 2 * p.row_blocks
+    return p.d < 64 || p.row_blocks <= 2 * p.S || p.row_work8 <= 2 * p.row_work
                ? rows_t<E, BWD, 2>(p, act, a, st)
                : rows_t<E, BWD, kPer>(p, act, a, st);
 }
