@@ -145,6 +145,7 @@ gdpa_status create(const int32_t* q_off, const int32_t* kv_off, int B, const int
             {p->useg.data(), p->useg.size() * 4, &p->off_useg},
             {p->smalls.data(), p->smalls.size() * sizeof(gdpa::PrefixUnit), &p->off_smalls},
             {p->eights.data(), p->eights.size() * sizeof(gdpa::PrefixUnit), &p->off_eights},
+            {p->blocks.data(), p->blocks.size() * sizeof(gdpa::RowBlock), &p->off_blocks},
             {p->joins.data(), p->joins.size() * sizeof(gdpa::PrefixUnit), &p->off_joins},
         };
         size_t at = 0;

@@ -42,6 +42,12 @@ struct PrefixPiece {
 };
 static_assert(sizeof(PrefixPiece) == 48, "PrefixPiece layout");
 
+// 4 warp_rows rows of a piece's slot: rows from 4 warp_rows * (sub >> 1) on of
+// slot sub & 1.
+struct RowBlock {
+    int32_t piece, sub;
+};
+
 // Backward unit: keys [k0, k0 + nk) (nk <= 128) of head hk against tokens
 // [tok, tok + ntok), token `tok` at position i0 of its sample, key k0 at j0
 // (own keys).  flags as a piece's; kUnitPart * (i + 1): one of several ranges of
@@ -76,8 +82,8 @@ struct PrefixPlan {
     int kernel = GDPA_KERNEL_AUTO;
     int64_t Tq = 0, Tkv = 0, Tp = 0;
     int64_t n_part_rows = 0;
-    int64_t row_blocks = 0;      // 32-row blocks of the pieces' slots
-    int64_t row_work = 0, row_work8 = 0;   // keys of all 32-row and of all 8-row blocks
+    std::vector<RowBlock> blocks;   // of the CUDA-core kernels, 4 warp_rows rows each
+    int warp_rows = 8;
     int max_layers = 0;          // most prefix parts of a row tile
     std::vector<PrefixPiece> pieces; // the tensor-core family's, then the small own ones
     std::vector<int32_t> seg;        // [S + 1] first piece of each CTA
@@ -93,7 +99,7 @@ struct PrefixPlan {
     int64_t n_small8 = 0;
     // device copies, one allocation (offsets below), and workspaces
     uint8_t* d_tables = nullptr;
-    size_t off_seg = 0, off_tiles = 0, off_own = 0, off_units = 0, off_useg = 0, off_smalls = 0, off_eights = 0, off_joins = 0, off_err = 0;
+    size_t off_seg = 0, off_tiles = 0, off_own = 0, off_units = 0, off_useg = 0, off_smalls = 0, off_eights = 0, off_joins = 0, off_blocks = 0, off_err = 0;
     float* d_parts = nullptr;        // [n_part_rows] x d floats
     float* d_ml = nullptr;           // [n_part_rows] float2
     float* d_grad = nullptr;         // backward: the parts of split units, then delta [Tq][H]
@@ -112,6 +118,7 @@ struct PrefixPlan {
     const PrefixTile* dev_tiles() const { return (const PrefixTile*)(d_tables + off_tiles); }
     const PrefixOwn* dev_own() const { return (const PrefixOwn*)(d_tables + off_own); }
     const PrefixUnit* dev_units() const { return (const PrefixUnit*)(d_tables + off_units); }
+    const RowBlock* dev_blocks() const { return (const RowBlock*)(d_tables + off_blocks); }
     const PrefixUnit* dev_joins() const { return (const PrefixUnit*)(d_tables + off_joins); }
     const int32_t* dev_useg() const { return (const int32_t*)(d_tables + off_useg); }
     const PrefixUnit* dev_smalls() const { return (const PrefixUnit*)(d_tables + off_smalls); }

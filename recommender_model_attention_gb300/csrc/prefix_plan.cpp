@@ -48,6 +48,37 @@ int64_t steps_of(const PrefixPiece& p) {
     return p.flags & kPieceDual ? cdiv(nb, 2) : nb;
 }
 
+// The CUDA-core kernels' row blocks: 8 rows (2 a warp) or 32 (8 a warp).
+//
+// 2 rows a warp: a quarter of the instructions on a warp's way, for four times
+// the reads of keys.  Better where few blocks are there to hide them (4 users of
+// 40 rows, 500 keys, d = 32: 20 us, 27 with 8 rows; one row against 4096 keys, d
+// = 128: 32 and 42), where the keys meet few rows, and up to 48 columns always (8
+// users of 256 rows, 2000 keys, 4 heads, d = 48: 372 and 456); from 64 on 8 rows
+// (the same with d = 64: 279, 356 with 2; 512 rows, d = 128: 421, 698).
+void make_row_blocks(PrefixPlan& p) {
+    int64_t blocks = 0, work = 0, work8 = 0;
+    auto rows_of = [&](const PrefixPiece& q, int slot) -> int64_t {
+        if ((slot ? q.part1 : q.part0) < 0) return 0;
+        return (int64_t)(slot && !(q.flags & kPieceDual) ? q.nB : q.nA) * p.r;
+    };
+    for (const PrefixPiece& q : p.pieces)
+        for (int slot = 0; slot < 2; ++slot) {
+            const int64_t rows = rows_of(q, slot), keys = q.flags & kPieceDual ? cdiv(q.nk, 2) : q.nk;
+            blocks += cdiv(rows, 32);
+            work += cdiv(rows, 32) * keys;
+            work8 += cdiv(rows, 8) * keys;
+        }
+    p.warp_rows = p.d < 64 || blocks <= 2 * p.S || work8 <= 2 * work ? 2 : 8;
+    p.blocks.clear();
+    for (size_t i = 0; i < p.pieces.size(); ++i)
+        for (int slot = 0; slot < 2; ++slot) {
+            const int64_t n = cdiv(rows_of(p.pieces[i], slot), 4 * p.warp_rows);
+            for (int64_t sub = 0; sub < n; ++sub)
+                p.blocks.push_back(RowBlock{(int32_t)i, (int32_t)(2 * sub + slot)});
+        }
+}
+
 // Cut units with more rows than a share of all (few keys, many rows) into
 // ranges of their tokens, so that every SM has work: each writes float32 sums
 // of its own, which a kernel joins in order.  (Backward of 4 users, 2000 rows a
@@ -294,19 +325,7 @@ gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t
     p.n_part_rows = parts;
     p.max_layers = 0;
     for (const PrefixTile& t : p.tiles) p.max_layers = std::max(p.max_layers, t.layers);
-    p.row_blocks = 0;
-    p.row_work = p.row_work8 = 0;
-    auto count = [&](const PrefixPiece& q, int64_t rows) {
-        const int64_t keys = q.flags & kPieceDual ? cdiv(q.nk, 2) : q.nk;
-        p.row_blocks += cdiv(rows, 32);
-        p.row_work += cdiv(rows, 32) * keys;
-        p.row_work8 += cdiv(rows, 8) * keys;
-    };
-    for (const PrefixPiece& q : p.pieces) {
-        const int32_t second = q.flags & kPieceDual ? q.nA : q.nB;
-        if (q.part0 >= 0) count(q, (int64_t)q.nA * p.r);
-        if (q.part1 >= 0) count(q, (int64_t)second * p.r);
-    }
+    make_row_blocks(p);
 
     // backward: one unit per 128-key block, against all rows that see it
     p.units.clear();

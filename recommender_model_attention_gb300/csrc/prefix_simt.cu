@@ -28,6 +28,7 @@ constexpr int kPer = 8;      // of a warp
 
 struct SimtArgs {
     const PrefixPiece* pieces;
+    const RowBlock* blocks;
     const PrefixUnit* units;
     const void *q, *kp, *vp, *k, *v, *d_o;
     const float *lse, *delta;
@@ -146,18 +147,16 @@ __device__ __forceinline__ void join_lanes(float4& v, int lane, int g, int ng, i
 
 // Forward (BWD false) or dQ (BWD true) of 4 R rows of a slot of a piece, R a warp.
 template <typename E, int ACT, bool BWD, int R>
-__global__ void __launch_bounds__(kThreads) simt_rows_kernel(const SimtArgs a) {
+__global__ void __launch_bounds__(kThreads, R == 2 ? 7 : BWD ? 3 : 4) simt_rows_kernel(const SimtArgs a) {
     extern __shared__ float sm[];
-    const PrefixPiece pc = a.pieces[blockIdx.x];
-    constexpr int kBlock = 4 * R, kSubs = kBM / kBlock;
-    const int slot = blockIdx.y / kSubs, sub = blockIdx.y % kSubs;
+    constexpr int kBlock = 4 * R;
+    const RowBlock rb = a.blocks[blockIdx.x];
+    const PrefixPiece pc = a.pieces[rb.piece];
+    const int slot = rb.sub & 1, row0 = (rb.sub >> 1) * kBlock;
     const int part = slot ? pc.part1 : pc.part0;
-    if (part < 0) return;
     const bool dual = pc.flags & kPieceDual, own = pc.flags & kPieceOwn;
     const int tok = pc.tok + (!dual && slot ? pc.nA : 0);
     const int nrows = (!dual && slot ? pc.nB : pc.nA) * a.r;
-    const int row0 = sub * kBlock;
-    if (row0 >= nrows) return;
     const int i0 = pc.i0 + (tok - pc.tok);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int qs = a.d, ks = a.d + 4;
@@ -539,6 +538,7 @@ __global__ void __launch_bounds__(256) delta_kernel(const E* d_o, const E* o, fl
 SimtArgs args_of(const PrefixPlan& p, const PrefixIO& io, const float* delta) {
     SimtArgs a;
     a.pieces = p.dev_pieces();
+    a.blocks = p.dev_blocks();
     a.units = p.dev_units();
     a.q = io.q; a.kp = io.kp; a.vp = io.vp; a.k = io.k; a.v = io.v;
     a.d_o = io.d_o;
@@ -577,24 +577,15 @@ gdpa_status rows_t(PrefixPlan& p, int act, const SimtArgs& a, cudaStream_t st) {
     gdpa_status s = GDPA_OK;
     const int tiles = sizeof(E) == 4 && R == 2 ? 2 : 1;
     const int smem = ((BWD ? 2 : 1) * 4 * R * p.d + tiles * 2 * kRows * (p.d + 4) + 4 * kRows * R) * 4;
-    const dim3 grid((unsigned)p.pieces.size(), 2 * kBM / (4 * R));
+    const dim3 grid((unsigned)p.blocks.size());
     PREFIX_DISPATCH(act, s = (go<simt_rows_kernel<E, A, BWD, R>>(grid, smem, p, a, st)))
     return s;
 }
 
 template <typename E, bool BWD>
 gdpa_status rows_of(PrefixPlan& p, int act, const SimtArgs& a, cudaStream_t st) {
-    if (p.pieces.empty()) return GDPA_OK;
-    // 2 rows a warp: a quarter of the instructions on a warp's way, for four
-    // times the reads of keys.  Better where few blocks are there to hide them
-    // (4 users of 40 rows, 500 keys, d = 32: 20 us, 27 with 8 rows; one row
-    // against 4096 keys, d = 128: 32 and 42), where samples have few rows, and up
-    // to 48 columns always (8 users of 256 rows, 2000 keys, 4 heads, d = 48: 372
-    // and 456); from 64 on 8 rows (the same with d = 64: 279, 356 with 2; 512
-    // rows, d = 128: 421, 698).
-    return p.d < 64 || p.row_blocks <= 2 * p.S || p.row_work8 <= 2 * p.row_work
-               ? rows_t<E, BWD, 2>(p, act, a, st)
-               : rows_t<E, BWD, kPer>(p, act, a, st);
+    if (p.blocks.empty()) return GDPA_OK;
+    return p.warp_rows == 2 ? rows_t<E, BWD, 2>(p, act, a, st) : rows_t<E, BWD, kPer>(p, act, a, st);
 }
 
 template <typename E>
