@@ -52,10 +52,11 @@ int64_t steps_of(const PrefixPiece& p) {
 //
 // 2 rows a warp: a quarter of the instructions on a warp's way, for four times
 // the reads of keys.  Better where few blocks are there to hide them (4 users of
-// 40 rows, 500 keys, d = 32: 20 us, 27 with 8 rows; one row against 4096 keys, d
-// = 128: 32 and 42), where the keys meet few rows, and up to 48 columns always (8
-// users of 256 rows, 2000 keys, 4 heads, d = 48: 372 and 456); from 64 on 8 rows
-// (the same with d = 64: 279, 356 with 2; 512 rows, d = 128: 421, 698).
+// 40 rows, 500 keys, d = 32: 21 us, 25 with 8 rows; one row against 4096 keys, d
+// = 128: 26 and 42), where the keys meet few rows, and up to 48 columns always (8
+// users of 256 rows, 2000 keys, 4 heads, d = 48: 272 and 384; samples of 36 rows
+// and 120 own keys, d = 32: 312 and 401); from 64 on 8 rows (256 rows, 2000 keys,
+// d = 64: 248, 303 with 2; 512 rows, d = 128: 431, 663).
 void make_row_blocks(PrefixPlan& p) {
     int64_t blocks = 0, work = 0, work8 = 0;
     auto rows_of = [&](const PrefixPiece& q, int slot) -> int64_t {

@@ -163,8 +163,8 @@ __global__ void __launch_bounds__(kThreads, R == 2 ? 7 : BWD ? 3 : 4) simt_rows_
     float* Q = sm;                       // [4 R][d]
     float* DO = Q + kBlock * qs;          // [4 R][d] (BWD)
     // float32 keys, few rows: two tiles in turn, the next one copied meanwhile
-    // (8 rows a warp hide the loads behind more blocks: 512 rows, d = 128, 421
-    // us, 547 with the shared memory of two tiles and shorter sums)
+    // (8 rows a warp hide the loads behind more blocks, for which two tiles
+    // leave no shared memory)
     constexpr int kTiles = sizeof(E) == 4 && R == 2 ? 2 : 1;
     float* const KV = DO + (BWD ? kBlock * qs : 0);   // K, V: [32][d + 4] each
     float* W = KV + kTiles * 2 * kRows * ks + warp * kRows * R;   // weights [32 keys][R rows]
