@@ -5,7 +5,16 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include "prefix_internal.h"
+
 namespace gdpa {
+
+// Of the keys of a unit that is a whole sample, those that some row sees (a
+// causal row sees its own position's key: all up to the last row's).  The rest
+// must not enter dQ, whose contraction runs over all of them, as 0 * inf.
+__device__ __forceinline__ int keys_seen(const PrefixUnit& u, int windowed) {
+    return windowed ? min(u.nk, u.ntok) : u.nk;
+}
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {

@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(kThreads, 2) own_bwd8_kernel(const OwnArgs a) 
     const Rows rows{min(8, u.ntok * a.r), 0, u.tok, u.hk, a.r, a.H};
     const int64_t ks = (int64_t)a.Hkv * D, k_at = (int64_t)u.k0 * ks + u.hk * D;
     const __nv_bfloat16 *K = a.k + k_at, *V = a.v + k_at;
+    const int seen = keys_seen(u, a.windowed);
     extern __shared__ uint4 own_smem[];   // two stages a warp
     __nv_bfloat16* stage = reinterpret_cast<__nv_bfloat16*>(own_smem) + (threadIdx.x >> 5) * 4 * Stage<D>::kKeys;
     load_stage<D>(stage, K, V, ks, 0, u.nk, lane);
@@ -391,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 2) own_bwd8_kernel(const OwnArgs a) 
             const int j = 2 * q + (w & 1) + (w >> 1) * 8;
 #pragma unroll
             for (int h = 0; h < kW; ++h)
-                kv[w][h] = j0 + j < u.nk ? lds16(kk + j * Stage<D>::kRow + 64 * h + 8 * g) : z;
+                kv[w][h] = j0 + j < seen ? lds16(kk + j * Stage<D>::kRow + 64 * h + 8 * g) : z;
         }
         __syncwarp();   // (read: the next step's copies may overwrite them)
         const uint32_t b0 = transposed(d0), b1 = transposed(d1);

@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kThreads) own_bwd_kernel(const OwnBwArgs a) {
     const PrefixUnit u = a.units[blockIdx.x];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, q = lane & 3;
-    const int nrows = u.ntok * a.r;
+    const int nrows = u.ntok * a.r, seen = keys_seen(u, a.windowed);
     const int64_t ks = (int64_t)a.Hkv * D, k_at = (int64_t)u.k0 * ks + u.hk * D;
     const __nv_bfloat16 *K = a.k + k_at, *V = a.v + k_at;
     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) own_bwd_kernel(const OwnBwArgs a) {
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
                         const int j = j0 + 2 * q + (w & 1) + (w >> 1) * 8;
-                        kv[w] = j < u.nk ? ldg16(K + j * ks + 64 * h + 8 * g) : z;
+                        kv[w] = j < seen ? ldg16(K + j * ks + 64 * h + 8 * g) : z;
                     }
 #pragma unroll
                     for (int e = 0; e < 8; ++e)

@@ -1,0 +1,61 @@
+"""Shared-prefix attention on the GPU at the edges of what its calls allow:
+what the window hides, streams, captures and limits.  Helpers and bounds as
+test_gpu_prefix.py."""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import recommender_model_attention_gb300 as gd  # noqa: E402
+from prefix_util import batch  # noqa: E402
+from test_gpu_prefix import make  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+KINDS = [("bf16", 128, "auto"), ("bf16", 64, "auto"), ("bf16", 128, "simt"), ("bf16", 64, "simt"),
+         ("f32", 32, "auto")]
+
+
+def setup_module(_):
+    gd.build()
+
+
+def both(plan, x, act):
+    """Forward and gradients: a list of tensors."""
+    if act == "softmax":
+        o, lse = gd.gdpa_prefix_softmax_fwd(plan, *x[:5])
+        out = [o, lse, *gd.gdpa_prefix_softmax_bwd(plan, *x[:5], o, x[5], lse)]
+    else:
+        out = [gd.gdpa_prefix_fwd(plan, *x[:5], act=act), *gd.gdpa_prefix_bwd(plan, *x[:5], x[5], act=act)]
+    plan.check()
+    return out
+
+
+def garbage(t, rows):
+    """t with infinities and NaN in turn in the given rows."""
+    t = t.clone()
+    for i, bad in enumerate((float("nan"), float("inf"), -float("inf"))):
+        t[rows[i::3]] = bad
+    return t
+
+
+@pytest.mark.parametrize("dt,d,kernel", KINDS)
+@pytest.mark.parametrize("act", ["softmax", "silu"])
+@pytest.mark.parametrize("window", [1, 5, 100, 2 ** 31 - 1])
+def test_keys_hidden_from_all_rows_may_hold_anything(window, act, dt, d, kernel):
+    """Own keys behind their sample's last row, in samples of up to 8, up to 64
+    and more packed rows: the same bits whatever they hold, gradients of 0."""
+    lq, lkv = [2, 1, 4, 20, 32, 130, 6], [40, 9, 17, 60, 300, 200, 6]
+    offs = batch(lq, lkv, [3, 4], [37, 0])
+    x = make(offs, 2, 1, d, dt)
+    plan = gd.PrefixPlan(*offs, 2, d, kv_heads=1, mask="causal_window", window=window)
+    plan.set_kernel(kernel)
+    rows = torch.from_numpy(np.concatenate(
+        [np.arange(offs[1][b] + min(lq[b], lkv[b]), offs[1][b + 1]) for b in range(len(lq))])).cuda()
+    want = both(plan, x, act)
+    got = both(plan, [x[0], x[1], x[2], garbage(x[3], rows), garbage(x[4], rows), x[5]], act)
+    for a, b in zip(got, want):
+        assert torch.isfinite(b).all() and torch.equal(a, b)
+    for g in got[-2:]:
+        assert torch.all(g[rows] == 0)
