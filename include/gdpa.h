@@ -584,9 +584,11 @@ gdpa_status gdpa_rope_apply(const gdpa_rope* rope, int inverse, gdpa_dtype dtype
  * the whole prefix; the mask (and its window) applies to the own keys, with
  * positions counted from the sample's first row, as in gdpa_plan_create.  A
  * row that sees no key gives O = 0, lse = -inf and no gradient.  Rows of other
- * samples and groups never enter a result, whatever they hold; a key that the
- * mask hides from a row, but not from all of its sample's, enters with weight
- * 0, so its rows of k and v must be finite.
+ * samples and groups never enter a result, whatever they hold, nor do keys that
+ * the mask hides from every row of their sample, nor rows that see no key; a
+ * key that the mask hides from a row, but not from all of its sample's, enters
+ * with weight 0, so its rows of k and v (and that row's of q and d_o) must be
+ * finite.
  *
  * Heads: Hkv key heads, each shared by H / Hkv consecutive query heads (Hkv =
  * H: one each).  Layout: q, o, d_o, dq [Tq][H][d]; kp, vp, dkp, dvp

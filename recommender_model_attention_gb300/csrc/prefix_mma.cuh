@@ -16,6 +16,12 @@ __device__ __forceinline__ int keys_seen(const PrefixUnit& u, int windowed) {
     return windowed ? min(u.nk, u.ntok) : u.nk;
 }
 
+// Whether the row at position pos of such a sample sees any key: one behind the
+// last key's window does not, and must not enter dK and dV the same way.
+__device__ __forceinline__ bool sees_keys(const PrefixUnit& u, int pos, int windowed, int window) {
+    return !windowed || pos - window < u.nk - 1;
+}
+
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(

@@ -295,10 +295,11 @@ __global__ void __launch_bounds__(kThreads, 2) own_bwd8_kernel(const OwnArgs a) 
             const bool real = i < rows.nrows;
             const int64_t x = real ? rows.at(i) : 0;
             pos[w] = i / a.r;
+            const bool sees = real && sees_keys(u, pos[w], a.windowed, a.window);
 #pragma unroll
             for (int h = 0; h < kW; ++h) {
-                qv[w][h] = real ? ldg16(a.q + x * D + 64 * h + 8 * g) : z;
-                ov[w][h] = real ? ldg16(a.d_o + x * D + 64 * h + 8 * g) : z;
+                qv[w][h] = sees ? ldg16(a.q + x * D + 64 * h + 8 * g) : z;
+                ov[w][h] = sees ? ldg16(a.d_o + x * D + 64 * h + 8 * g) : z;
             }
             if (kSm && real) {
                 const float y = a.lse[x];

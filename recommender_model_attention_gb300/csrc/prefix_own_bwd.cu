@@ -116,8 +116,9 @@ __global__ void __launch_bounds__(kThreads) own_bwd_kernel(const OwnBwArgs a) {
                             dl[w] = a.delta[at];
                         }
                         ip[w] = u.i0 + x / a.r;
-                        qv[2 * n + w] = real ? ldg16(a.q + at * D + 64 * h + 8 * g) : z;
-                        ov[2 * n + w] = real ? ldg16(a.d_o + at * D + 64 * h + 8 * g) : z;
+                        const bool sees = real && sees_keys(u, ip[w], a.windowed, a.window);
+                        qv[2 * n + w] = sees ? ldg16(a.q + at * D + 64 * h + 8 * g) : z;
+                        ov[2 * n + w] = sees ? ldg16(a.d_o + at * D + 64 * h + 8 * g) : z;
                     }
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {

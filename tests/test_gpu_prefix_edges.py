@@ -59,3 +59,28 @@ def test_keys_hidden_from_all_rows_may_hold_anything(window, act, dt, d, kernel)
         assert torch.isfinite(b).all() and torch.equal(a, b)
     for g in got[-2:]:
         assert torch.all(g[rows] == 0)
+
+
+@pytest.mark.parametrize("dt,d,kernel", KINDS)
+@pytest.mark.parametrize("act", ["softmax", "silu"])
+@pytest.mark.parametrize("window", [1, 3])
+def test_rows_that_see_no_key_may_hold_anything(window, act, dt, d, kernel):
+    """Query rows behind the last own key's window, in groups without a prefix:
+    they leave every gradient as it is and have none."""
+    lq, lkv = [4, 30, 200, 3], [1, 3, 5, 3]
+    offs = batch(lq, lkv, [2, 2], [0, 0])
+    x = make(offs, 2, 1, d, dt)
+    plan = gd.PrefixPlan(*offs, 2, d, kv_heads=1, mask="causal_window", window=window)
+    plan.set_kernel(kernel)
+    rows = torch.from_numpy(np.concatenate(
+        [np.arange(offs[0][b] + min(lq[b], lkv[b] + window - 1), offs[0][b + 1]) for b in range(len(lq))])).cuda()
+    assert len(rows) > 100
+    want = both(plan, x, act)
+    got = both(plan, [garbage(x[0], rows), *x[1:5], garbage(x[5], rows)], act)
+    for i, (a, b) in enumerate(zip(got, want)):
+        if act == "softmax" and i == 1:
+            assert torch.all(a[rows] == -float("inf"))
+        else:
+            assert torch.isfinite(b).all()
+        assert torch.equal(a, b)
+    assert torch.all(got[0][rows] == 0) and torch.all(got[-5][rows] == 0)
