@@ -53,12 +53,14 @@ bool capturing(cudaStream_t st) {
 }
 
 // Order work on `st` after the plan's upload and, the workspace being one,
-// after the plan's work on another stream.  A captured launch cannot depend
-// on events from outside its graph: the host makes sure that they have
-// happened.
+// after the plan's work so far.  That is waited for whatever the handle: equal
+// ones need not be the same stream (the per-thread default stream is another
+// one in every thread, a new stream may get a destroyed one's handle).  A
+// captured launch cannot depend on events from outside its graph: the host
+// makes sure that they have happened.
 gdpa_status begin_work(PrefixPlan& p, cudaStream_t st, bool captured) {
+    p.chain = 0;
     if (captured) {
-        p.chain = 0;
         cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
         if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return GDPA_ERR_CUDA;
         const bool ok = cudaEventSynchronize(p.ready) == cudaSuccess &&
@@ -66,7 +68,6 @@ gdpa_status begin_work(PrefixPlan& p, cudaStream_t st, bool captured) {
         cudaThreadExchangeStreamCaptureMode(&mode);
         return ok ? GDPA_OK : GDPA_ERR_CUDA;
     }
-    p.chain = 0;
     if (!p.is_ready) {
         if (cudaStreamWaitEvent(st, p.ready, 0) != cudaSuccess) return GDPA_ERR_CUDA;
         // (a query could spoil a capture that another thread has under way)
@@ -76,8 +77,7 @@ gdpa_status begin_work(PrefixPlan& p, cudaStream_t st, bool captured) {
         cudaThreadExchangeStreamCaptureMode(&mode);
         if (!p.is_ready) cudaGetLastError();   // not ready is not an error
     }
-    if (p.has_work && p.last_stream != st && cudaStreamWaitEvent(st, p.last, 0) != cudaSuccess)
-        return GDPA_ERR_CUDA;
+    if (p.has_work && cudaStreamWaitEvent(st, p.last, 0) != cudaSuccess) return GDPA_ERR_CUDA;
     return GDPA_OK;
 }
 
@@ -85,7 +85,6 @@ gdpa_status end_work(PrefixPlan& p, cudaStream_t st, bool captured) {
     if (captured) return GDPA_OK;   // the graph's replays are the caller's to order
     if (cudaEventRecord(p.last, st) != cudaSuccess) return GDPA_ERR_CUDA;
     p.has_work = true;
-    p.last_stream = st;
     return GDPA_OK;
 }
 

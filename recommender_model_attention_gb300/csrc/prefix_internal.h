@@ -109,7 +109,6 @@ struct PrefixPlan {
     int chain = 0;                   // kernels of the current call that a next one may start beside
     cudaEvent_t ready = nullptr;     // the upload, on the creation stream
     cudaEvent_t last = nullptr;      // the plan's latest work
-    cudaStream_t last_stream = nullptr;
     bool has_work = false, is_ready = false;   // is_ready: the upload is known to be over
     std::mutex lock;                 // host state above
 

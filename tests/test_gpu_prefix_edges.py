@@ -84,3 +84,48 @@ def test_rows_that_see_no_key_may_hold_anything(window, act, dt, d, kernel):
             assert torch.isfinite(b).all()
         assert torch.equal(a, b)
     assert torch.all(got[0][rows] == 0) and torch.all(got[-5][rows] == 0)
+
+
+class PerThread:
+    """The per-thread default stream: one handle, another stream in each thread."""
+    cuda_stream = 2
+
+
+def test_threads_on_the_per_thread_stream_share_a_plan():
+    """Two host threads, each on its own per-thread default stream (equal
+    handles), forward and backward on one plan and different inputs: the
+    workspace is one, so the calls have to follow one another on the GPU."""
+    import threading
+    offs = batch([5, 300, 1], [4, 310, 0], [2, 1], [2000, 9000])
+    d = 128
+    plan = gd.PrefixPlan(*offs, 4, d, kv_heads=2)
+    x = [make(offs, 4, 2, d, "bf16", seed=i) for i in range(2)]
+    want = [both(plan, y, "softmax") for y in x]
+    # a turn of outputs per call, made here: allocations belong to a stream
+    outs = [[[torch.zeros_like(t) for t in want[i]] for _ in range(20)] for i in range(2)]
+    torch.cuda.synchronize()
+    meet, failed = threading.Barrier(2), []
+
+    def work(i):
+        try:
+            meet.wait(60)
+            y = x[i]
+            for o, lse, *g in outs[i]:
+                gd.gdpa_prefix_softmax_fwd(plan, *y[:5], o=o, lse=lse, stream=PerThread)
+                gd.gdpa_prefix_softmax_bwd(plan, *y[:5], o, y[5], lse, *g, stream=PerThread)
+            # (a thread's exit destroys its stream, which must not have work left)
+            torch.cuda.ExternalStream(PerThread.cuda_stream).synchronize()
+        except Exception as e:   # noqa: BLE001  (shown below)
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=(i,), daemon=True) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not failed and not any(t.is_alive() for t in threads), failed
+    torch.cuda.synchronize()
+    plan.check()
+    for i in range(2):
+        for call in outs[i]:
+            for a, b in zip(call, want[i]):
+                assert torch.equal(a, b)
