@@ -600,7 +600,8 @@ gdpa_status gdpa_rope_apply(const gdpa_rope* rope, int inverse, gdpa_dtype dtype
  * workspace its calls share: calls on one plan from several streams are
  * ordered by the library, calls from several host threads serialised.  Calls
  * may be captured into a CUDA graph (the first backward of a plan allocates
- * and is refused with ALLOC while capturing); the plan must outlive the
+ * and is refused with ALLOC while capturing), where those of one capture are
+ * ordered alike, on whichever of its streams; the plan must outlive the
  * graph, and replays that share a plan must not overlap on the GPU with each
  * other or with other calls on the plan.
  */

@@ -34,6 +34,7 @@ void free_prefix(PrefixPlan* p) {
         for (void* b : bufs)
             if (b) cudaFreeAsync(b, fs);
         if (p->last) cudaEventDestroy(p->last);
+        if (p->in_capture) cudaEventDestroy(p->in_capture);
         if (p->ready) cudaEventDestroy(p->ready);
         if (fs) cudaStreamDestroy(fs);
         if (cur >= 0 && cur != p->device) cudaSetDevice(cur);
@@ -47,29 +48,39 @@ gdpa_status check_device(const PrefixPlan& p) {
     return cur == p.device ? GDPA_OK : GDPA_ERR_INVALID_ARG;
 }
 
-bool capturing(cudaStream_t st) {
-    cudaStreamCaptureStatus s = cudaStreamCaptureStatusNone;
-    return cudaStreamIsCapturing(st, &s) == cudaSuccess && s != cudaStreamCaptureStatusNone;
-}
+// A call's stream, and the capture that it is in (0: none).
+struct Call {
+    cudaStream_t st;
+    unsigned long long capture = 0;
+    explicit Call(cudaStream_t s) : st(s) {
+        cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+        if (cudaStreamGetCaptureInfo(s, &status, &capture) != cudaSuccess ||
+            status == cudaStreamCaptureStatusNone)
+            capture = 0;
+    }
+};
 
-// Order work on `st` after the plan's upload and, the workspace being one,
-// after the plan's work so far.  That is waited for whatever the handle: equal
-// ones need not be the same stream (the per-thread default stream is another
-// one in every thread, a new stream may get a destroyed one's handle).  A
-// captured launch cannot depend on events from outside its graph: the host
-// makes sure that they have happened.
-gdpa_status begin_work(PrefixPlan& p, cudaStream_t st, bool captured) {
+// Order work on the call's stream after the plan's upload and, the workspace
+// being one, after the plan's work so far.  That is waited for whatever the
+// handle: equal ones need not be the same stream (the per-thread default stream
+// is another one in every thread, a new stream may get a destroyed one's
+// handle).  A captured launch cannot depend on events from outside its graph:
+// the host makes sure that they have happened.  It follows the plan's last call
+// of the same capture, which may be on another stream of it.
+gdpa_status begin_work(PrefixPlan& p, const Call& c) {
     p.chain = 0;
-    if (captured) {
+    if (c.capture) {
         cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
         if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return GDPA_ERR_CUDA;
         const bool ok = cudaEventSynchronize(p.ready) == cudaSuccess &&
                         (!p.has_work || cudaEventSynchronize(p.last) == cudaSuccess);
         cudaThreadExchangeStreamCaptureMode(&mode);
-        return ok ? GDPA_OK : GDPA_ERR_CUDA;
+        if (!ok || (p.capture == c.capture && cudaStreamWaitEvent(c.st, p.in_capture, 0) != cudaSuccess))
+            return GDPA_ERR_CUDA;
+        return GDPA_OK;
     }
     if (!p.is_ready) {
-        if (cudaStreamWaitEvent(st, p.ready, 0) != cudaSuccess) return GDPA_ERR_CUDA;
+        if (cudaStreamWaitEvent(c.st, p.ready, 0) != cudaSuccess) return GDPA_ERR_CUDA;
         // (a query could spoil a capture that another thread has under way)
         cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
         if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return GDPA_ERR_CUDA;
@@ -77,13 +88,18 @@ gdpa_status begin_work(PrefixPlan& p, cudaStream_t st, bool captured) {
         cudaThreadExchangeStreamCaptureMode(&mode);
         if (!p.is_ready) cudaGetLastError();   // not ready is not an error
     }
-    if (p.has_work && cudaStreamWaitEvent(st, p.last, 0) != cudaSuccess) return GDPA_ERR_CUDA;
+    if (p.has_work && cudaStreamWaitEvent(c.st, p.last, 0) != cudaSuccess) return GDPA_ERR_CUDA;
     return GDPA_OK;
 }
 
-gdpa_status end_work(PrefixPlan& p, cudaStream_t st, bool captured) {
-    if (captured) return GDPA_OK;   // the graph's replays are the caller's to order
-    if (cudaEventRecord(p.last, st) != cudaSuccess) return GDPA_ERR_CUDA;
+gdpa_status end_work(PrefixPlan& p, const Call& c) {
+    if (c.capture) {   // (the graph's replays are the caller's to order)
+        p.capture = 0;
+        if (cudaEventRecord(p.in_capture, c.st) != cudaSuccess) return GDPA_ERR_CUDA;
+        p.capture = c.capture;
+        return GDPA_OK;
+    }
+    if (cudaEventRecord(p.last, c.st) != cudaSuccess) return GDPA_ERR_CUDA;
     p.has_work = true;
     return GDPA_OK;
 }
@@ -178,6 +194,7 @@ gdpa_status create(const int32_t* q_off, const int32_t* kv_off, int B, const int
             (cudaMemsetAsync(p->dev_err(), 0, 16, st) != cudaSuccess ||
              cudaEventCreateWithFlags(&p->ready, cudaEventDisableTiming) != cudaSuccess ||
              cudaEventCreateWithFlags(&p->last, cudaEventDisableTiming) != cudaSuccess ||
+             cudaEventCreateWithFlags(&p->in_capture, cudaEventDisableTiming) != cudaSuccess ||
              cudaEventRecord(p->ready, st) != cudaSuccess))
             s = GDPA_ERR_CUDA;
         if (s != GDPA_OK) cudaStreamSynchronize(st);
@@ -219,8 +236,8 @@ gdpa_status fwd(gdpa_prefix_plan plan, gdpa_dtype dtype, const PrefixIO& io, voi
     if (p.Tq == 0) return GDPA_OK;
     cudaStream_t st = (cudaStream_t)stream;
     std::lock_guard<std::mutex> hold(p.lock);
-    const bool cap = capturing(st);
-    if (gdpa_status s = begin_work(p, st, cap)) return s;
+    const Call call(st);
+    if (gdpa_status s = begin_work(p, call)) return s;
     gdpa_status s;
     if (use_tc(p, dtype)) {
         s = gdpa::launch_prefix_own_fwd(p, io, st);
@@ -229,7 +246,7 @@ gdpa_status fwd(gdpa_prefix_plan plan, gdpa_dtype dtype, const PrefixIO& io, voi
         s = gdpa::launch_prefix_simt_fwd(p, dtype, io, st);
     }
     if (s == GDPA_OK) s = gdpa::launch_prefix_merge(p, dtype, io.o, sm ? io.lse : nullptr, sm, st);
-    const gdpa_status e = end_work(p, st, cap);
+    const gdpa_status e = end_work(p, call);
     return s != GDPA_OK ? s : e;
 }
 
@@ -249,11 +266,11 @@ gdpa_status bwd(gdpa_prefix_plan plan, gdpa_dtype dtype, const PrefixIO& io, voi
     if (gdpa_status s = check_device(p)) return s;
     cudaStream_t st = (cudaStream_t)stream;
     std::lock_guard<std::mutex> hold(p.lock);
-    const bool cap = capturing(st);
+    const Call call(st);
     const size_t unit_parts = (size_t)p.n_unit_parts * 2 * gdpa::kBN * p.d;   // floats
     const size_t need = (unit_parts + (size_t)p.Tq * p.H) * sizeof(float);
-    if (p.grad_bytes < need && cap) return GDPA_ERR_ALLOC;   // a graph must not own the workspace
-    if (gdpa_status s = begin_work(p, st, cap)) return s;
+    if (p.grad_bytes < need && call.capture) return GDPA_ERR_ALLOC;   // a graph must not own the workspace
+    if (gdpa_status s = begin_work(p, call)) return s;
     if (p.grad_bytes < need) {
         if (cudaMallocAsync((void**)&p.d_grad, need, st) != cudaSuccess) {
             p.d_grad = nullptr;
@@ -274,7 +291,7 @@ gdpa_status bwd(gdpa_prefix_plan plan, gdpa_dtype dtype, const PrefixIO& io, voi
     }
     if (s == GDPA_OK) s = gdpa::launch_prefix_join(p, dtype, io, st);
     if (s == GDPA_OK) s = gdpa::launch_prefix_merge(p, dtype, io.dq, nullptr, false, st);
-    const gdpa_status e = end_work(p, st, cap);
+    const gdpa_status e = end_work(p, call);
     return s != GDPA_OK ? s : e;
 }
 

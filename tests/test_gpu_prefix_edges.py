@@ -129,3 +129,47 @@ def test_threads_on_the_per_thread_stream_share_a_plan():
         for call in outs[i]:
             for a, b in zip(call, want[i]):
                 assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dt,d", [("bf16", 128), ("f32", 32)])
+def test_calls_on_two_streams_of_one_capture(dt, d):
+    """Forwards and backwards of different inputs on two branches of a captured
+    graph share the plan's workspace: every replay gives each its own results."""
+    offs = batch([5, 300, 1], [4, 310, 0], [2, 1], [2000, 9000])
+    plan = gd.PrefixPlan(*offs, 4, d, kv_heads=2)
+    x = [make(offs, 4, 2, d, dt, seed=i) for i in range(2)]
+    want = [both(plan, y, "softmax") for y in x]
+    outs = [[torch.zeros_like(t) for t in want[i]] for i in range(2)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        for part in ("fwd", "bwd"):
+            for i, stream in enumerate((None, side)):
+                o, lse, *g = outs[i]
+                if part == "fwd":
+                    gd.gdpa_prefix_softmax_fwd(plan, *x[i][:5], o=o, lse=lse, stream=stream)
+                else:
+                    gd.gdpa_prefix_softmax_bwd(plan, *x[i][:5], o, x[i][5], lse, *g, stream=stream)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(10):
+        for call in outs:
+            for t in call:
+                t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            for a, b in zip(outs[i], want[i]):
+                assert torch.equal(a, b)
+    # another capture of the plan, and eager calls, afterwards
+    again = torch.cuda.CUDAGraph()
+    o, lse, *g = outs[0]
+    with torch.cuda.graph(again):
+        gd.gdpa_prefix_softmax_fwd(plan, *x[0][:5], o=o, lse=lse)
+    o.zero_()
+    again.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want[0][0])
+    for a, b in zip(both(plan, x[1], "softmax"), want[1]):
+        assert torch.equal(a, b)
