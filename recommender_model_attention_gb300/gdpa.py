@@ -3,6 +3,10 @@
 Argument marshalling only: every step of planning and of the forward and
 backward passes runs in the C++/CUDA library.  There is no fallback: if the
 library has not been built, every call raises.
+
+``stream=`` (default: the current stream): the call only enqueues work there.
+Its inputs must be ready on that stream; outputs that it allocates are the
+stream's, to be waited for before other streams read them.
 """
 
 from __future__ import annotations
@@ -323,6 +327,21 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t.numel() else ctypes.c_void_p(0)
 
 
+def _new(shape, dtype, device, stream):
+    """An output tensor for work on ``stream`` (None: the current one).  Memory
+    belongs to the stream it is allocated on: there it is free to be written,
+    and it is not given out again before the current stream's uses are over."""
+    if _empty is None:
+        _torch_names()
+    if stream is None:
+        return _empty(shape, dtype=dtype, device=device)
+    import torch
+    with torch.cuda.stream(stream):
+        t = _empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def gdpa_fwd(plan: Plan, q, k, v, o=None, alpha=None, act: str = "gelu_erf", stream=None):
     """O = act(alpha Q K^T) V per sample and head; returns O ([Tq, H, d], dtype of q)."""
     import torch
@@ -330,7 +349,7 @@ def gdpa_fwd(plan: Plan, q, k, v, o=None, alpha=None, act: str = "gelu_erf", str
     _check(k, plan.Tkv, plan, "k", q.dtype)
     _check(v, plan.Tkv, plan, "v", q.dtype)
     if o is None:
-        o = torch.empty((plan.Tq, plan.H, plan.d), dtype=q.dtype, device=q.device)
+        o = _new((plan.Tq, plan.H, plan.d), q.dtype, q.device, stream)
     _check(o, plan.Tq, plan, "o", q.dtype)
     alpha = plan.d ** -0.5 if alpha is None else float(alpha)
     _ok(lib().gdpa_fwd(plan.handle, _dtype_id(q), _ptr(q), _ptr(k), _ptr(v), _ptr(o),
@@ -348,9 +367,9 @@ def gdpa_bwd(plan: Plan, q, k, v, do, dq=None, dk=None, dv=None, alpha=None,
     _check(v, plan.Tkv, plan, "v", q.dtype)
     _check(do, plan.Tq, plan, "do", q.dtype)
     f32 = torch.float32
-    dq = torch.empty(q.shape, dtype=f32, device=q.device) if dq is None else dq
-    dk = torch.empty(k.shape, dtype=f32, device=k.device) if dk is None else dk
-    dv = torch.empty(v.shape, dtype=f32, device=v.device) if dv is None else dv
+    dq = _new(q.shape, f32, q.device, stream) if dq is None else dq
+    dk = _new(k.shape, f32, k.device, stream) if dk is None else dk
+    dv = _new(v.shape, f32, v.device, stream) if dv is None else dv
     _check(dq, plan.q_rows, plan, "dq", f32)
     _check(dk, plan.Tkv, plan, "dk", f32)
     _check(dv, plan.Tkv, plan, "dv", f32)
@@ -375,8 +394,8 @@ def mx_quantise(x, stream=None) -> MX:
         raise ValueError("mx_quantise takes a contiguous bfloat16 CUDA tensor")
     if x.shape[-1] % 32:
         raise ValueError("the last axis must be a multiple of 32")
-    el = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
-    sc = torch.empty(x.shape[:-1] + (x.shape[-1] // 32,), dtype=torch.uint8, device=x.device)
+    el = _new(x.shape, torch.uint8, x.device, stream)
+    sc = _new(x.shape[:-1] + (x.shape[-1] // 32,), torch.uint8, x.device, stream)
     _ok(lib().gdpa_mx_quantise(_ptr(x), x.numel(), _ptr(el), _ptr(sc), _stream_ptr(stream)),
         "gdpa_mx_quantise")
     return MX(el, sc)
@@ -387,7 +406,7 @@ def mx_dequantise(m: MX, stream=None):
     import torch
     el, sc = m
     _mx_check(el, sc, 0, None, "x")
-    x = torch.empty(el.shape, dtype=torch.bfloat16, device=el.device)
+    x = _new(el.shape, torch.bfloat16, el.device, stream)
     _ok(lib().gdpa_mx_dequantise(_ptr(el), _ptr(sc), el.numel(), _ptr(x), _stream_ptr(stream)),
         "gdpa_mx_dequantise")
     return x
@@ -413,7 +432,7 @@ def gdpa_fwd_mx(plan: Plan, q: MX, k: MX, v, o=None, alpha=None, act: str = "gel
     _mx_check(k.elements, k.scales, plan.Tkv, plan, "k")
     _check(v, plan.Tkv, plan, "v", torch.bfloat16)
     if o is None:
-        o = torch.empty((plan.Tq, plan.H, plan.d), dtype=torch.bfloat16, device=v.device)
+        o = _new((plan.Tq, plan.H, plan.d), torch.bfloat16, v.device, stream)
     _check(o, plan.Tq, plan, "o", torch.bfloat16)
     alpha = plan.d ** -0.5 if alpha is None else float(alpha)
     _ok(lib().gdpa_fwd_mx(plan.handle, _ptr(q.elements), _ptr(q.scales), _ptr(k.elements),
@@ -438,9 +457,9 @@ def gdpa_bwd_mx(plan: Plan, q, k, v, do, dq=None, dk=None, dv=None, alpha=None,
     _check(v, plan.Tkv, plan, "v", torch.bfloat16)
     _check(do, plan.Tq, plan, "do", torch.bfloat16)
     f32 = torch.float32
-    dq = torch.empty((plan.q_rows, plan.H, plan.d), dtype=f32, device=v.device) if dq is None else dq
-    dk = torch.empty(v.shape, dtype=f32, device=v.device) if dk is None else dk
-    dv = torch.empty(v.shape, dtype=f32, device=v.device) if dv is None else dv
+    dq = _new((plan.q_rows, plan.H, plan.d), f32, v.device, stream) if dq is None else dq
+    dk = _new(v.shape, f32, v.device, stream) if dk is None else dk
+    dv = _new(v.shape, f32, v.device, stream) if dv is None else dv
     _check(dq, plan.q_rows, plan, "dq", f32)
     _check(dk, plan.Tkv, plan, "dk", f32)
     _check(dv, plan.Tkv, plan, "dv", f32)
@@ -523,8 +542,8 @@ def act_eval(x, act: str = "gelu_erf", fast=True, stream=None):
     import torch
     if x.dtype != torch.float32 or not x.is_cuda or not x.is_contiguous():
         raise ValueError("x must be a contiguous float32 CUDA tensor")
-    y = torch.empty_like(x)
-    dy = torch.empty_like(x)
+    y = _new(x.shape, x.dtype, x.device, stream)
+    dy = _new(x.shape, x.dtype, x.device, stream)
     mode = 2 if fast == 2 else (1 if fast else 0)
     _ok(lib().gdpa_act_eval(ACT[act], mode, _ptr(x), _ptr(y), _ptr(dy),
                             ctypes.c_int64(x.numel()), _stream_ptr(stream)), "gdpa_act_eval")
@@ -539,10 +558,10 @@ def gdpa_softmax_fwd(plan: Plan, q, k, v, o=None, lse=None, alpha=None, stream=N
     _check(k, plan.Tkv, plan, "k", q.dtype)
     _check(v, plan.Tkv, plan, "v", q.dtype)
     if o is None:
-        o = torch.empty((plan.Tq, plan.H, plan.d), dtype=q.dtype, device=q.device)
+        o = _new((plan.Tq, plan.H, plan.d), q.dtype, q.device, stream)
     _check(o, plan.Tq, plan, "o", q.dtype)
     if lse is None:
-        lse = torch.empty((plan.Tq, plan.H), dtype=torch.float32, device=q.device)
+        lse = _new((plan.Tq, plan.H), torch.float32, q.device, stream)
     if lse.dtype != torch.float32 or tuple(lse.shape) != (plan.Tq, plan.H) or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 [Tq, H] tensor")
     alpha = plan.d ** -0.5 if alpha is None else float(alpha)
@@ -564,9 +583,9 @@ def gdpa_softmax_bwd(plan: Plan, q, k, v, o, do, lse, dq=None, dk=None, dv=None,
     _check(do, plan.Tq, plan, "do", q.dtype)
     if lse.dtype != f32 or tuple(lse.shape) != (plan.Tq, plan.H) or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 [Tq, H] tensor")
-    dq = torch.empty(q.shape, dtype=f32, device=q.device) if dq is None else dq
-    dk = torch.empty(k.shape, dtype=f32, device=k.device) if dk is None else dk
-    dv = torch.empty(v.shape, dtype=f32, device=v.device) if dv is None else dv
+    dq = _new(q.shape, f32, q.device, stream) if dq is None else dq
+    dk = _new(k.shape, f32, k.device, stream) if dk is None else dk
+    dv = _new(v.shape, f32, v.device, stream) if dv is None else dv
     for t, n, rows in ((dq, "dq", plan.q_rows), (dk, "dk", plan.Tkv), (dv, "dv", plan.Tkv)):
         _check(t, rows, plan, n, f32)
     alpha = plan.d ** -0.5 if alpha is None else float(alpha)
@@ -614,7 +633,7 @@ class Rope:
 _rope_tensor = struct.Struct("=QQi4xqqqq").pack
 
 
-def _rope_rows(x, y, T, d, dtype, dev, name):
+def _rope_rows(x, y, T, d, dtype, dev, name, stream):
     """One tensor of a rope call: checks; its output, and its packed record."""
     shape, xs = x.shape, x.stride()
     if len(shape) != 3 or shape[0] != T or shape[2] != d or x.device != dev:
@@ -624,7 +643,7 @@ def _rope_rows(x, y, T, d, dtype, dev, name):
         raise TypeError("%s must be %s" % (name, dtype))
     heads = shape[1]
     if y is None:
-        y = _empty(shape, dtype=dtype, device=dev)
+        y = _new(shape, dtype, dev, stream)
         ys = (heads * d, d, 1)
     else:
         if y.shape != shape or y.dtype != dtype or y.device != dev:
@@ -649,10 +668,10 @@ def _rope(rope, inverse, q, k, positions, offsets, starts, q_out, k_out, stream)
         raise ValueError("give either positions or offsets")
     if starts is not None and offsets is None:
         raise ValueError("starts belong to offsets")
-    q_out, rows = _rope_rows(q, q_out, T, d, dtype, dev, "q")
+    q_out, rows = _rope_rows(q, q_out, T, d, dtype, dev, "q", stream)
     n = 1
     if k is not None:
-        k_out, more = _rope_rows(k, k_out, T, d, dtype, dev, "k")
+        k_out, more = _rope_rows(k, k_out, T, d, dtype, dev, "k", stream)
         rows += more
         n = 2
     elif k_out is not None:
@@ -849,7 +868,7 @@ def _prefix_call(f, what, plan, args, alpha, act, stream):
 def _prefix_fwd(plan, q, kp, vp, k, v, o, lse_ptr, alpha, act, stream):
     args = _prefix_inputs(plan, q, kp, vp, k, v)
     if o is None:
-        o = _empty(plan._rows, dtype=q.dtype, device=plan.device)
+        o = _new(plan._rows, q.dtype, plan.device, stream)
         out = o.data_ptr()
     else:
         out = _prefix_tensor(o, plan._rows, plan, "o", q.dtype)
@@ -872,7 +891,7 @@ def gdpa_prefix_softmax_fwd(plan: PrefixPlan, q, kp, vp, k=None, v=None, o=None,
     if plan.device is None:
         raise ValueError("a host-only plan cannot launch")
     if lse is None:
-        lse = _empty(plan._lse, dtype=_f32, device=plan.device)
+        lse = _new(plan._lse, _f32, plan.device, stream)
         ptr = lse.data_ptr()
     else:
         ptr = _prefix_lse(lse, plan)
@@ -888,7 +907,7 @@ def _prefix_bwd(plan, q, kp, vp, k, v, o, do, lse, grads, alpha, act, stream):
     for g, shape, name in zip(grads, (plan._rows, plan._prefix, plan._prefix, plan._keys, plan._keys),
                               ("dq", "dkp", "dvp", "dk", "dv")):
         if g is None:
-            g = _empty(shape, dtype=dt, device=plan.device)
+            g = _new(shape, dt, plan.device, stream)
             args += (g.data_ptr(),)
         else:
             args += (_prefix_tensor(g, shape, plan, name, dt),)
