@@ -117,6 +117,7 @@ gdpa_status create(const int32_t* q_off, const int32_t* kv_off, int B, const int
     if (mask == GDPA_MASK_CAUSAL_WINDOW && window < 1) return GDPA_ERR_INVALID_ARG;
     if (d > 128 || d % 4 != 0 || H / Hkv > gdpa::kBM) return GDPA_ERR_UNSUPPORTED;
     if ((int64_t)H * d > (1 << 20) || num_sms > 65536) return GDPA_ERR_UNSUPPORTED;
+    if (!host_only && Call(st).capture) return GDPA_ERR_ALLOC;   // a graph must not own the buffers
     PrefixPlan* p = nullptr;
     gdpa_status s = GDPA_OK;
     try {   // the planner's tables grow with the batch

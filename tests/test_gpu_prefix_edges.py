@@ -173,3 +173,20 @@ def test_calls_on_two_streams_of_one_capture(dt, d):
     assert torch.equal(o, want[0][0])
     for a, b in zip(both(plan, x[1], "softmax"), want[1]):
         assert torch.equal(a, b)
+
+
+def test_plans_are_refused_on_a_stream_that_is_captured():
+    offs = batch([5], [4], [1], [30])
+    x = make(offs, 2, 2, 64, "bf16")
+    out = torch.zeros(3, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(gd.GdpaError) as e:
+            gd.PrefixPlan(*offs, 2, 64)
+        out.fill_(2)   # the capture goes on
+    assert e.value.status == 4
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.all(out == 2)
+    both(gd.PrefixPlan(*offs, 2, 64), x, "softmax")
