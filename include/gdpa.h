@@ -613,9 +613,11 @@ typedef struct gdpa_prefix_plan_s* gdpa_prefix_plan;
  * The tables are uploaded on `stream`; launches on any stream wait for them.
  * INVALID_ARG for NULL pointers, bad sizes or offsets (not starting at 0,
  * decreasing, group_off[G] != B), H not a multiple of Hkv, window < 1 with
- * the window mask; UNSUPPORTED for other d, H * d > 2^20 or more than 128
- * query heads per key head; ALLOC, also while `stream` is being captured (a
- * graph must not own the plan's memory); CUDA.  *out is NULL on failure.
+ * the window mask; UNSUPPORTED for other d, H * d > 2^20, more than 128 query
+ * heads per key head, or more than 2^31 - 4096 rows of q, of kp or of k (and
+ * where the rows' parts in the workspace would be more than 2^31 - 1 rows);
+ * ALLOC, also while `stream` is being captured (a graph must not own the plan's
+ * memory); CUDA.  *out is NULL on failure.
  */
 gdpa_status gdpa_prefix_create(const int32_t* q_off, const int32_t* kv_off, int B,
                                const int32_t* group_off, const int32_t* prefix_off, int G, int H,

@@ -22,6 +22,10 @@ constexpr int kPieceCost = 3;   // steps a piece costs beside its own
 constexpr int kSmallRows = 64;
 constexpr int kSmallKeys = 512;
 
+// Rows of a kind: a walk in blocks steps past the last one by less than two
+// blocks, in 32 bits.
+constexpr int64_t kMaxRows = 0x7fffffff - 4095;
+
 constexpr int kSplitTiles = 4;   // row tiles that a range of a split backward unit has at least
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -128,6 +132,7 @@ gdpa_status build_prefix_plan(PrefixPlan& p, const int32_t* q_off, const int32_t
     p.Tq = q_off[p.B];
     p.Tkv = kv_off[p.B];
     p.Tp = prefix_off[p.G];
+    if (p.Tq > kMaxRows || p.Tkv > kMaxRows || p.Tp > kMaxRows) return GDPA_ERR_UNSUPPORTED;
     const int tpt = p.tpt;
     int64_t parts = 0;   // rows of the workspace given out
     std::vector<Unit> units;
