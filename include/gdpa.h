@@ -537,8 +537,9 @@ gdpa_status gdpa_rope_init_freqs(gdpa_rope* rope, int rot_dim, gdpa_rope_layout 
 
 /* Rows x of `heads` heads, and where they go: element (t, h, c) at x[t *
  * x_token + h * x_head + c], strides in elements (a packed projection's Q or
- * K part, say).  y may be x with the same strides (in place); it must not
- * overlap x otherwise. */
+ * K part, say; a single row's x_token and a single head's x_head do not
+ * matter).  y may be x with the same strides (in place); it must not overlap
+ * it, or the call's other tensor, otherwise. */
 typedef struct {
     const void* x;
     void* y;

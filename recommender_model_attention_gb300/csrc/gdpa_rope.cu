@@ -321,6 +321,9 @@ gdpa_status gdpa_rope_apply(const gdpa_rope* rope, int inverse, gdpa_dtype dtype
             (!t.x || !t.y || (uintptr_t)t.x % esize || (uintptr_t)t.y % esize))
             return GDPA_ERR_INVALID_ARG;
         a.t[i] = t;
+        // strides that are never stepped: a single row's, a single head's
+        if (T <= 1) a.t[i].x_token = a.t[i].y_token = 0;
+        if (t.heads <= 1) a.t[i].x_head = a.t[i].y_head = 0;
         a.heads += t.heads;
     }
     if (T == 0 || a.heads == 0) return GDPA_OK;
@@ -344,7 +347,7 @@ gdpa_status gdpa_rope_apply(const gdpa_rope* rope, int inverse, gdpa_dtype dtype
     // the interleaved layout takes pairs of columns at a time
     if (inter)
         for (int i = 0; i < n; ++i) {
-            const gdpa_rope_tensor& t = tensors[i];
+            const gdpa_rope_tensor& t = a.t[i];
             if (t.heads == 0) continue;
             if ((t.x_token | t.x_head | t.y_token | t.y_head | d) % 2 ||
                 ((uintptr_t)t.x | (uintptr_t)t.y) % (2 * esize))
