@@ -40,3 +40,27 @@ def test_strides_that_are_never_stepped(T, H, layout, dt):
     assert torch.equal(a, want) and torch.equal(b, want)
     gd.gdpa_rope_fwd(rope, x, positions=pos, q_out=x)
     assert torch.equal(x, want)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("B", [255, 256, 257, 600, 2046, 2047, 2048, 5000])
+def test_positions_counted_from_many_offsets(B, dt):
+    """More offsets than a block has threads, and more than it counts through:
+    the same bits as the positions given, also where many samples are empty."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(B)
+    lens = torch.randint(0, 5, (B,), generator=g, device="cuda")
+    lens[torch.rand(B, generator=g, device="cuda") < 0.3] = 0
+    lens[B // 2] = 700   # over several blocks
+    off = torch.cat([torch.zeros(1, device="cuda", dtype=torch.int64), lens.cumsum(0)]).int()
+    starts = torch.randint(-1000, 100000, (B,), generator=g, device="cuda", dtype=torch.int32)
+    n = int(off[-1])
+    x = rows(n + 9, 2, 64, dt)
+    sample = torch.repeat_interleave(torch.arange(B, device="cuda"), lens)
+    pos = torch.arange(n, device="cuda") - off[sample].long() + starts[sample].long()
+    rope = gd.Rope(64)
+    want = gd.gdpa_rope_fwd(rope, x[:n], positions=pos)
+    got = gd.gdpa_rope_fwd(rope, x, offsets=off, starts=starts, q_out=torch.full_like(x, 3.25))
+    assert torch.equal(got[:n], want) and torch.all(got[n:] == 3.25)
+    at = [0, n // 3, n - 1]
+    check(want[at], x[at], [int(pos[i]) for i in at], orc.frequencies(64), "half")
