@@ -43,7 +43,7 @@ def test_strides_that_are_never_stepped(T, H, layout, dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-@pytest.mark.parametrize("B", [255, 256, 257, 600, 2046, 2047, 2048, 5000])
+@pytest.mark.parametrize("B", [255, 256, 257, 600, 1022, 1023, 1024, 2047, 2048, 5000])
 def test_positions_counted_from_many_offsets(B, dt):
     """More offsets than a block has threads, and more than it counts through:
     the same bits as the positions given, also where many samples are empty."""
