@@ -15,12 +15,21 @@
 namespace gdpa {
 namespace {
 
-constexpr int kPieceCost = 3;   // steps a piece costs beside its own
+// Steps a piece costs beside its own.  (Forward of 512 rows on 16384 keys, 8
+// heads: 60 us; 81 with 0, 69 with 1, 62 with 6.  2 x 2048 rows on 32768 keys:
+// 423 us; 437, 434, 427.)
+constexpr int kPieceCost = 3;
 
-// Own keys of samples with at most this many packed rows and keys are streamed
-// by warp-level kernels (prefix_own.cu), without a tile's latency.
+// Own keys of samples with at most this many packed rows, keys, and pairs of
+// them are streamed by warp-level kernels (prefix_own.cu), without a tile's
+// latency; with more pairs the tensor core's products are worth it.  Forward
+// and backward in us, d = 128, 4 heads, with this limit of pairs, with 512 and
+// with none: 300 samples of 16 to 64 rows on 8 to 64 keys, d = 64: 58, 141; 88,
+// 166; 57, 140.  500 of 6 to 8 rows on 100 to 500 keys, d = 64: 56, 86; 94, 170;
+// 55, 86.  200 of 48 to 64 rows on 64 to 400 keys: 69, 144; 62, 116; 115, 311.
 constexpr int kSmallRows = 64;
 constexpr int kSmallKeys = 512;
+constexpr int kSmallPairs = 4096;
 
 // Rows of a kind: a walk in blocks steps past the last one by less than two
 // blocks, in 32 bits.
@@ -44,7 +53,8 @@ bool good_offsets(const int32_t* off, int n) {
 }
 
 bool is_small(const PrefixPlan& p, int32_t lq, int32_t lk) {
-    return (p.d == 64 || p.d == 128) && (int64_t)lq * p.r <= kSmallRows && lk <= kSmallKeys;
+    const int64_t rows = (int64_t)lq * p.r;
+    return (p.d == 64 || p.d == 128) && rows <= kSmallRows && lk <= kSmallKeys && rows * lk <= kSmallPairs;
 }
 
 int64_t steps_of(const PrefixPiece& p) {
