@@ -640,6 +640,33 @@ gdpa_status gdpa_prefix_create_host(const int32_t* q_off, const int32_t* kv_off,
  * the count). */
 gdpa_status gdpa_prefix_export(gdpa_prefix_plan plan, int32_t* pieces, int64_t cap, int64_t* n,
                                int32_t* seg);
+/* The plan's other lists, for inspection: int32 rows of the width given, of
+ * which *n receives the number (INVALID_ARG if cap is smaller). */
+typedef enum {
+    /* backward units of at most 128 keys, 8: first key row; keys; first token;
+     * tokens; key head; flags (1 own keys; 256 (i + 1): one of several ranges of
+     * the tokens, its sums in part i); position of the token and of the key in
+     * their sample.  The tensor-core kernels' queues first, then small samples'. */
+    GDPA_PREFIX_UNITS = 0,
+    GDPA_PREFIX_UNIT_SEG = 1, /* first unit of each queue, 1: [num_sms + 1] */
+    /* units in ranges, 8: as units, the first of their parts and how many in
+     * place of the tokens */
+    GDPA_PREFIX_JOINS = 2,
+    GDPA_PREFIX_SMALLS = 3, /* whole small samples, 8: as units */
+    GDPA_PREFIX_EIGHTS = 4, /* these in 8 packed rows, 8: the first in place of the key's position */
+    GDPA_PREFIX_BLOCKS = 5, /* the CUDA cores' row blocks, 2: piece; 2 x block + slot */
+    /* row tiles, 8: first token; tokens; key head; first row of the prefix parts
+     * in the workspace; parts; 0, 0, 0 */
+    GDPA_PREFIX_TILES = 6,
+    /* per token, its own keys' parts, 4: first row of head 0's; row of the token
+     * in a part; parts a head; rows of a part */
+    GDPA_PREFIX_OWN = 7,
+    /* 1 row of 4: rows of the workspace; parts of ranges; small samples of at
+     * most 8 packed rows (the first of their list); rows a warp in the blocks */
+    GDPA_PREFIX_COUNTS = 8
+} gdpa_prefix_list;
+gdpa_status gdpa_prefix_export_list(gdpa_prefix_plan plan, gdpa_prefix_list which, int32_t* rows,
+                                    int64_t cap, int64_t* n);
 /* As gdpa_plan_set_kernel: AUTO runs bf16 with d = 64 or 128 on the tensor
  * cores and everything else on the CUDA cores. */
 gdpa_status gdpa_prefix_set_kernel(gdpa_prefix_plan plan, gdpa_kernel kernel);

@@ -327,6 +327,36 @@ gdpa_status gdpa_prefix_export(gdpa_prefix_plan plan, int32_t* pieces, int64_t c
     return GDPA_OK;
 }
 
+gdpa_status gdpa_prefix_export_list(gdpa_prefix_plan plan, gdpa_prefix_list which, int32_t* rows,
+                                    int64_t cap, int64_t* n) {
+    if (!plan) return GDPA_ERR_INVALID_ARG;
+    const PrefixPlan& p = *(PrefixPlan*)plan;
+    const int32_t counts[4] = {(int32_t)p.n_part_rows, (int32_t)p.n_unit_parts, (int32_t)p.n_small8, p.warp_rows};
+    const void* src = nullptr;
+    size_t count = 0, bytes = 0;
+    auto list = [&](const auto& v) {
+        src = v.data();
+        count = v.size();
+        bytes = sizeof(v[0]);
+    };
+    switch (which) {
+    case GDPA_PREFIX_UNITS: list(p.units); break;
+    case GDPA_PREFIX_UNIT_SEG: list(p.useg); break;
+    case GDPA_PREFIX_JOINS: list(p.joins); break;
+    case GDPA_PREFIX_SMALLS: list(p.smalls); break;
+    case GDPA_PREFIX_EIGHTS: list(p.eights); break;
+    case GDPA_PREFIX_BLOCKS: list(p.blocks); break;
+    case GDPA_PREFIX_TILES: list(p.tiles); break;
+    case GDPA_PREFIX_OWN: list(p.own); break;
+    case GDPA_PREFIX_COUNTS: src = counts, count = 1, bytes = sizeof(counts); break;
+    default: return GDPA_ERR_INVALID_ARG;
+    }
+    if (n) *n = (int64_t)count;
+    if (cap < (int64_t)count || (count && !rows)) return GDPA_ERR_INVALID_ARG;
+    if (count) memcpy(rows, src, count * bytes);
+    return GDPA_OK;
+}
+
 gdpa_status gdpa_prefix_set_kernel(gdpa_prefix_plan plan, gdpa_kernel kernel) {
     if (!plan || kernel < GDPA_KERNEL_AUTO || kernel > GDPA_KERNEL_SIMT) return GDPA_ERR_INVALID_ARG;
     ((PrefixPlan*)plan)->kernel = kernel;

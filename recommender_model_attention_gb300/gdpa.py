@@ -28,6 +28,9 @@ SCHED = {"zigzag": 0, "round_robin": 1, "zigzag_timed": 2}
 KERNEL = {"auto": 0, "tcgen05": 1, "simt": 2}
 ROPE_LAYOUT = {"half": 0, "interleaved": 1}
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
+# lists of a shared-prefix plan: (index, columns)
+PREFIX_LIST = {"units": (0, 8), "unit_seg": (1, 1), "joins": (2, 8), "smalls": (3, 8), "eights": (4, 8),
+               "blocks": (5, 2), "tiles": (6, 8), "own": (7, 4), "counts": (8, 4)}
 KV_SPLIT_AUTO = -1   # max_kv_blocks_per_tile: the planner chooses
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported configuration", 3: "CUDA error",
           4: "allocation failed", 5: "kernel barrier wait timed out",
@@ -103,6 +106,7 @@ def lib():
             "gdpa_prefix_create_host": [i32p, i32p, st, i32p, i32p, st, st, st, st, st, st, st,
                                         ctypes.POINTER(vp)],
             "gdpa_prefix_export": [vp, i32p, ctypes.c_int64, i64p, i32p],
+            "gdpa_prefix_export_list": [vp, st, i32p, ctypes.c_int64, i64p],
             "gdpa_prefix_set_kernel": [vp, st],
             "gdpa_prefix_fwd": [vp, st] + [vp] * 7 + [ctypes.c_float, st, vp],
             "gdpa_prefix_bwd": [vp, st] + [vp] * 13 + [ctypes.c_float, st, vp],
@@ -789,6 +793,17 @@ class PrefixPlan:
                                      None if seg is None else seg.ctypes.data_as(i32p)),
             "gdpa_prefix_export")
         return pieces[:n.value], seg
+
+    def export_list(self, name: str):
+        """int32 [n, columns]: a list of the plan (PREFIX_LIST), as
+        gdpa_prefix_export_list."""
+        which, width = PREFIX_LIST[name]
+        n = ctypes.c_int64()
+        lib().gdpa_prefix_export_list(self.handle, which, None, 0, ctypes.byref(n))
+        rows = np.zeros((max(1, n.value), width), dtype=np.int32)
+        _ok(lib().gdpa_prefix_export_list(self.handle, which, rows.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)),
+                                          n.value, ctypes.byref(n)), "gdpa_prefix_export_list")
+        return rows[:n.value]
 
     def set_kernel(self, kernel: str):
         _ok(lib().gdpa_prefix_set_kernel(self.handle, KERNEL[kernel]), "gdpa_prefix_set_kernel")
