@@ -671,6 +671,11 @@ gdpa_status gdpa_prefix_export_list(gdpa_prefix_plan plan, gdpa_prefix_list whic
  * cores and everything else on the CUDA cores. */
 gdpa_status gdpa_prefix_set_kernel(gdpa_prefix_plan plan, gdpa_kernel kernel);
 
+/* Failure-path test hook, as gdpa_plan_set_wait_test: stall 1 makes CTA 0 of
+ * the forward's and of the dK, dV kernel never load its first queries, 2 of the
+ * dQ kernel; INVALID_ARG for others. */
+gdpa_status gdpa_prefix_set_wait_test(gdpa_prefix_plan plan, int limit_us, int stall);
+
 /* Forward.  lse (may be NULL) is written for GDPA_ACT_SOFTMAX only. */
 gdpa_status gdpa_prefix_fwd(gdpa_prefix_plan plan, gdpa_dtype dtype, const void* q, const void* kp,
                             const void* vp, const void* k, const void* v, void* o, float* lse,

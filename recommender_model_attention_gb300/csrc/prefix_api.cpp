@@ -363,6 +363,14 @@ gdpa_status gdpa_prefix_set_kernel(gdpa_prefix_plan plan, gdpa_kernel kernel) {
     return GDPA_OK;
 }
 
+gdpa_status gdpa_prefix_set_wait_test(gdpa_prefix_plan plan, int limit_us, int stall) {
+    if (!plan || limit_us < 0 || stall < 0 || stall > 2) return GDPA_ERR_INVALID_ARG;
+    PrefixPlan& p = *(PrefixPlan*)plan;
+    p.wait_limit_us = (uint32_t)limit_us;
+    p.stall = stall;
+    return GDPA_OK;
+}
+
 gdpa_status gdpa_prefix_fwd(gdpa_prefix_plan plan, gdpa_dtype dtype, const void* q, const void* kp,
                             const void* vp, const void* k, const void* v, void* o, float* lse,
                             float alpha, gdpa_act act, void* stream) {

@@ -80,6 +80,8 @@ struct PrefixPlan {
     int B = 0, G = 0, H = 0, Hkv = 0, r = 1, d = 0, mask = 0, window = 0, S = 0;
     int tpt = 128;               // tokens of a row tile
     int kernel = GDPA_KERNEL_AUTO;
+    uint32_t wait_limit_us = 0;  // test hook (gdpa_prefix_set_wait_test)
+    int stall = 0;
     int64_t Tq = 0, Tkv = 0, Tp = 0;
     int64_t n_part_rows = 0;
     std::vector<RowBlock> blocks;   // of the CUDA-core kernels, 4 warp_rows rows each

@@ -71,6 +71,7 @@ struct BwArgs {
     float alpha;
     int32_t* err;
     uint64_t wait_ns;
+    int stall;   // test hook: CTA 0 never loads its first query tile
 };
 
 // weights and score gradients of two pairs
@@ -152,10 +153,12 @@ __device__ __forceinline__ void kv_producer(const CUtensorMap* tmQ, const CUtens
     int32_t armed[3] = {-1, -1, -1};
     uint32_t ph = 7;   // per pair: the parity of "empty" to wait for
     Places at;
-    // a pair is free: arm it for the next load
+    bool stall = a.stall && blockIdx.x == 0;
+    // a pair is free: arm it for the next load (of nothing: it stays empty)
     auto take = [&](uint32_t pair, uint32_t bytes) -> bool {
         if (!mbar_wait<true>(&bars[C::kEmpty + pair], (ph >> pair) & 1, ab, 81)) return false;
         ph ^= 1u << pair;
+        if (bytes == 0) return true;
         mbar_arrive_expect_tx(&bars[C::kFull + pair], bytes);
         armed[pair] = (int32_t)((ph >> pair) & 1);
         return true;
@@ -175,7 +178,11 @@ __device__ __forceinline__ void kv_producer(const CUtensorMap* tmQ, const CUtens
         }
         for (int m = 0; m < tiles; ++m) {
             const uint32_t pair = at.tile(m);
-            if (!take(pair, 2 * (uint32_t)a.q_bytes)) goto unwind;
+            if (!take(pair, stall ? 0 : 2 * (uint32_t)a.q_bytes)) goto unwind;
+            if (stall) {
+                stall = false;
+                continue;
+            }
 #pragma unroll
             for (int hf = 0; hf < C::kHalves; ++hf) {
                 uint8_t* dst = smem + pair * C::kPair + hf * kHalfBytes;
@@ -584,12 +591,14 @@ __device__ __forceinline__ void dq_producer(const CUtensorMap* tmQ, const CUtens
         const Run run(p, t & 1, a.r);
         if (run.blocks == 0) continue;
         if (!mbar_wait<true>(&bars[C::kQEmpty], (nr & 1) ^ 1, ab, 101)) goto unwind;
-        mbar_arrive_expect_tx(&bars[C::kQFull], 2 * (uint32_t)a.q_bytes);
-        q_armed = (int32_t)(nr & 1);
+        if (!(a.stall && blockIdx.x == 0 && nr == 0)) {
+            mbar_arrive_expect_tx(&bars[C::kQFull], 2 * (uint32_t)a.q_bytes);
+            q_armed = (int32_t)(nr & 1);
 #pragma unroll
-        for (int hf = 0; hf < C::kHalves; ++hf) {
-            tma_load_3d(tmQ, &bars[C::kQFull], smem + C::kOffQ + hf * kHalfBytes, hf * 64, p.hk * a.r, run.tok, once);
-            tma_load_3d(tmDO, &bars[C::kQFull], smem + C::kOffDO + hf * kHalfBytes, hf * 64, p.hk * a.r, run.tok, once);
+            for (int hf = 0; hf < C::kHalves; ++hf) {
+                tma_load_3d(tmQ, &bars[C::kQFull], smem + C::kOffQ + hf * kHalfBytes, hf * 64, p.hk * a.r, run.tok, once);
+                tma_load_3d(tmDO, &bars[C::kQFull], smem + C::kOffDO + hf * kHalfBytes, hf * 64, p.hk * a.r, run.tok, once);
+            }
         }
         const bool own = p.flags & kPieceOwn;
         for (int j = 0; j < run.blocks; ++j)
@@ -859,11 +868,13 @@ gdpa_status launch(PrefixPlan& p, const CUtensorMap* m, BwArgs& a, cudaStream_t 
     gdpa_status s = GDPA_OK;
     if (p.useg[p.S] > 0) {
         a.seg = p.dev_useg();
+        a.stall = p.stall == 1;
         static std::atomic<uint64_t> done{0};
         s = go(prefix_dkv_kernel<D, ACT>, kKvThreads, KvCfg<D>::kSmem, done, p, m, a, st);
     }
     if (s == GDPA_OK && p.seg[p.S] > 0) {
         a.seg = p.dev_seg();
+        a.stall = p.stall == 2;
         static std::atomic<uint64_t> done{0};
         s = go(prefix_dq_kernel<D, ACT>, kThreads, DqCfg<D>::kSmem, done, p, m, a, st);
     }
@@ -909,7 +920,8 @@ gdpa_status launch_prefix_tc_bwd(PrefixPlan& p, const PrefixIO& io, const float*
     a.q_bytes = p.tpt * p.r * p.d * 2;
     a.alpha = io.alpha;
     a.err = p.dev_err();
-    a.wait_ns = tc::wait_limit_ns(0);
+    a.wait_ns = tc::wait_limit_ns(p.wait_limit_us);
+    a.stall = 0;
     gdpa_status s = GDPA_OK;
     if (p.d == 128) {
         if (io.act == kSoftmax)

@@ -72,6 +72,7 @@ struct PfParams {
     float alpha;
     int32_t* err;
     uint64_t wait_ns;
+    int stall;        // test hook: CTA 0 never loads its first queries
 };
 
 // Blocks of a piece, of each slot, and where they lie in the ring (counted
@@ -105,13 +106,15 @@ __device__ __forceinline__ void pf_producer(const CUtensorMap* tmQ, const CUtens
         const Walk w(p);
         const uint32_t n = (uint32_t)(t - seg0);
         if (!mbar_wait<true>(&bars[C::kQEmpty], (n & 1) ^ 1, ab, 61)) goto unwind;
-        mbar_arrive_expect_tx(&bars[C::kQFull], (uint32_t)(prm.q_bytes * (p.nB > 0 ? 2 : 1)));
-        q_armed = (int32_t)(n & 1);
-        for (int half = 0; half < (p.nB > 0 ? 2 : 1); ++half)
+        if (!(prm.stall && blockIdx.x == 0 && n == 0)) {
+            mbar_arrive_expect_tx(&bars[C::kQFull], (uint32_t)(prm.q_bytes * (p.nB > 0 ? 2 : 1)));
+            q_armed = (int32_t)(n & 1);
+            for (int half = 0; half < (p.nB > 0 ? 2 : 1); ++half)
 #pragma unroll
-            for (int hf = 0; hf < C::kHalves; ++hf)
-                tma_load_3d(tmQ, &bars[C::kQFull], smem + C::kOffQ + half * C::kTile + hf * kHalfBytes,
-                            hf * 64, p.hk * prm.r, p.tok + half * p.nA, once);
+                for (int hf = 0; hf < C::kHalves; ++hf)
+                    tma_load_3d(tmQ, &bars[C::kQFull], smem + C::kOffQ + half * C::kTile + hf * kHalfBytes,
+                                hf * 64, p.hk * prm.r, p.tok + half * p.nA, once);
+        }
         const bool own = p.flags & kPieceOwn;
         const CUtensorMap* mk = own ? tmK : tmKp;
         const CUtensorMap* mv = own ? tmV : tmVp;
@@ -548,7 +551,8 @@ gdpa_status launch_prefix_tc_fwd(PrefixPlan& p, const PrefixIO& io, cudaStream_t
     prm.q_bytes = p.tpt * p.r * p.d * 2;
     prm.alpha = io.alpha;
     prm.err = p.dev_err();
-    prm.wait_ns = tc::wait_limit_ns(0);
+    prm.wait_ns = tc::wait_limit_ns(p.wait_limit_us);
+    prm.stall = p.stall == 1;
     gdpa_status s = GDPA_OK;
     if (p.d == 128) {
         if (io.act == kSoftmax)

@@ -108,6 +108,7 @@ def lib():
             "gdpa_prefix_export": [vp, i32p, ctypes.c_int64, i64p, i32p],
             "gdpa_prefix_export_list": [vp, st, i32p, ctypes.c_int64, i64p],
             "gdpa_prefix_set_kernel": [vp, st],
+            "gdpa_prefix_set_wait_test": [vp, st, st],
             "gdpa_prefix_fwd": [vp, st] + [vp] * 7 + [ctypes.c_float, st, vp],
             "gdpa_prefix_bwd": [vp, st] + [vp] * 13 + [ctypes.c_float, st, vp],
             "gdpa_prefix_check": [vp, vp],
@@ -808,14 +809,25 @@ class PrefixPlan:
     def set_kernel(self, kernel: str):
         _ok(lib().gdpa_prefix_set_kernel(self.handle, KERNEL[kernel]), "gdpa_prefix_set_kernel")
 
+    def set_wait_test(self, limit_us: int = 0, stall: int = 0):
+        """Failure-path test hook: bounded-wait limit (microseconds, 0 = the
+        default), and whether CTA 0's first query load is skipped, so that a
+        wait expires: 1 in the forward and the dK, dV kernel, 2 in the dQ one."""
+        _ok(lib().gdpa_prefix_set_wait_test(self.handle, int(limit_us), int(stall)),
+            "gdpa_prefix_set_wait_test")
+
+    def error_detail(self):
+        """As Plan.error_detail."""
+        d = (ctypes.c_int32 * 4)()
+        _ok(lib().gdpa_prefix_error_detail(self.handle, d), "gdpa_prefix_error_detail")
+        return tuple(int(v) for v in d)
+
     def check(self, stream=None):
         """Wait for the plan's work; raise if a kernel reported a failure."""
         status = lib().gdpa_prefix_check(self.handle, _stream_ptr(stream))
         if status != 0:
-            d = (ctypes.c_int32 * 4)()
-            lib().gdpa_prefix_error_detail(self.handle, d)
             raise GdpaError(status, "gdpa_prefix_check (device code %d, wait site %d, CTA %d, %d)"
-                            % tuple(int(v) for v in d))
+                            % self.error_detail())
 
     @property
     def launches(self) -> int:
