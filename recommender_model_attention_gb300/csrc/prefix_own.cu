@@ -215,7 +215,6 @@ __global__ void __launch_bounds__(kThreads, 4) own_fwd_kernel(const OwnArgs a) {
             mma16816(acc[e], a0, a1, a2, a3, b0, b1);
         }
     }
-    if (ow.layers == 0) return;   // no row of the sample sees an own key
     const int64_t part = (int64_t)ow.part + (int64_t)u.hk * ow.rows;
     store_part<D>(acc, 1.0f, a.parts, part, ow.rows, rows.row0, rows.nrows, g, q);
     if (kSm) {
@@ -405,7 +404,6 @@ __global__ void __launch_bounds__(kThreads, 2) own_bwd8_kernel(const OwnArgs a) 
             mma16816(acc[e], a0, a1, a2, a3, b0, b1);
         }
     }
-    if (ow.layers == 0) return;
     store_part<D>(acc, a.alpha, a.parts, (int64_t)ow.part + (int64_t)u.hk * ow.rows, ow.rows, 0, rows.nrows, g, q);
 }
 

@@ -230,7 +230,6 @@ __global__ void __launch_bounds__(kThreads) own_bwd_kernel(const OwnBwArgs a) {
                 }
             }
             const PrefixOwn ow = a.own[u.tok];
-            if (ow.layers == 0) continue;   // no row sees a key of its own: no part
             const int64_t part = (int64_t)ow.part + (int64_t)u.hk * ow.rows;
             float4* out = reinterpret_cast<float4*>(a.parts) + part * (D / 4);
 #pragma unroll

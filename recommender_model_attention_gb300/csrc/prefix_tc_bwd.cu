@@ -56,6 +56,15 @@ constexpr int kKvThreads = 512; // and one that drains dK and dV
 constexpr int kHalfBytes = 128 * 128;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kItem = 64;   // columns of an item
+// Items of every tile but a unit's last: tiles of 128 / r whole tokens of r rows
+// have more rows than one.
+constexpr int kTileItems = 2;
+constexpr int fewest_tile_rows() {
+    int n = kBM;
+    for (int r = 1; r <= kBM; ++r) n = kBM / r * r < n ? kBM / r * r : n;
+    return n;
+}
+static_assert(fewest_tile_rows() > kItem && kBM <= kTileItems * kItem, "items of a tile");
 
 struct BwArgs {
     const PrefixUnit* units;
@@ -124,9 +133,9 @@ __device__ __forceinline__ int tile_rows(const PrefixUnit& u, const BwArgs& a, i
 }
 
 // Items of a unit (0: no row sees its keys).
-__device__ __forceinline__ int unit_items(const PrefixUnit& u, const BwArgs& a, int full) {
+__device__ __forceinline__ int unit_items(const PrefixUnit& u, const BwArgs& a) {
     const int tiles = (u.ntok + a.tpt - 1) / a.tpt;
-    return tiles == 0 ? 0 : (tiles - 1) * full + (tile_rows(u, a, tiles - 1) + kItem - 1) / kItem;
+    return tiles == 0 ? 0 : (tiles - 1) * kTileItems + (tile_rows(u, a, tiles - 1) + kItem - 1) / kItem;
 }
 
 // Which of the three pairs of buffers hold a unit's keys and its tiles (in
@@ -204,7 +213,7 @@ struct ItemWalk {
     PrefixUnit u;
     Places at;
     int t, tiles, items, x, last_rows;
-    __device__ __forceinline__ void load(const BwArgs& a, int full, int seg1) {
+    __device__ __forceinline__ void load(const BwArgs& a, int seg1) {
         for (; t < seg1; ++t) {   // units without rows have no items
             u = load_unit(a.units + t);
             tiles = (u.ntok + a.tpt - 1) / a.tpt;
@@ -213,15 +222,15 @@ struct ItemWalk {
         x = 0;
         if (t < seg1) {
             last_rows = tile_rows(u, a, tiles - 1);
-            items = (tiles - 1) * full + (last_rows + kItem - 1) / kItem;
+            items = (tiles - 1) * kTileItems + (last_rows + kItem - 1) / kItem;
         }
     }
     __device__ __forceinline__ bool last() const { return x == items - 1; }
-    __device__ __forceinline__ void next(const BwArgs& a, int full, int seg1) {
+    __device__ __forceinline__ void next(const BwArgs& a, int seg1) {
         if (++x < items) return;
         at.next(tiles);
         ++t;
-        load(a, full, seg1);
+        load(a, seg1);
     }
 };
 
@@ -234,16 +243,15 @@ __device__ __forceinline__ void kv_mma(const BwArgs& a, uint8_t* smem, uint64_t*
     constexpr uint64_t kPairDesc = C::kPair >> 4, kTileDesc = C::kTile >> 4, kItemDesc = (kItem * 128) >> 4;
     const uint64_t k_major = smem_desc_sw128(smem_u32(smem), 16, 1024);
     const uint64_t mn_major = smem_desc_sw128(smem_u32(smem), kHalfBytes, 1024);
-    const int full = a.tpt * a.r > kItem ? 2 : 1;   // items of every tile but a unit's last
     // rows of an item, in 16s
     auto rows16 = [&](const ItemWalk& w, int half) {
-        const int n = w.x >= (w.tiles - 1) * full ? w.last_rows : a.tpt * a.r;
+        const int n = w.x >= (w.tiles - 1) * kTileItems ? w.last_rows : a.tpt * a.r;
         return (uint32_t)((min(kItem, n - half * kItem) + 15) & ~15);
     };
     ItemWalk A, B;
     A.t = B.t = seg0;
-    A.load(a, full, seg1);
-    B.load(a, full, seg1);
+    A.load(a, seg1);
+    B.load(a, seg1);
     uint32_t slotA = 0, slotB = 0, p_ph = 0, acc_ph = 1, ph = 0;
     auto landed = [&](uint32_t pair) -> bool {
         if (!mbar_wait<true>(&bars[C::kFull + pair], (ph >> pair) & 1, ab, 83)) return false;
@@ -251,7 +259,7 @@ __device__ __forceinline__ void kv_mma(const BwArgs& a, uint8_t* smem, uint64_t*
         return true;
     };
     auto scores = [&]() -> bool {
-        const int m = full == 2 ? A.x >> 1 : A.x, half = full == 2 ? A.x & 1 : 0;
+        const int m = A.x >> 1, half = A.x & 1;
         const uint32_t pair = A.at.tile(m);
         if (A.x == 0 && !landed(A.at.kv)) return false;
         if (half == 0 && !landed(pair)) return false;
@@ -263,13 +271,13 @@ __device__ __forceinline__ void kv_mma(const BwArgs& a, uint8_t* smem, uint64_t*
         one_commit(&bars[C::kSDFull + slotA]);
         if (A.last()) one_commit(&bars[C::kEmpty + A.at.kv]);
         slotA ^= 1;
-        A.next(a, full, seg1);
+        A.next(a, seg1);
         return true;
     };
     for (int i = 0; i < 2; ++i)
         if (A.t < seg1 && !scores()) return;
     while (B.t < seg1) {
-        const int m = full == 2 ? B.x >> 1 : B.x, half = full == 2 ? B.x & 1 : 0;
+        const int m = B.x >> 1, half = B.x & 1;
         const uint32_t pair = B.at.tile(m), col = tmem + slotB * 128;
         const bool last = B.last();
         if (B.x == 0) {   // the accumulators of the unit before have been read
@@ -284,20 +292,20 @@ __device__ __forceinline__ void kv_mma(const BwArgs& a, uint8_t* smem, uint64_t*
         one_sums(tmem + 384, col + 64, col + 80, qd, idesc_acc, steps, B.x > 0);
         p_ph ^= slotB;
         slotB ^= 1;
-        if (half == full - 1 || last) one_commit(&bars[C::kEmpty + pair]);
+        if (half || last) one_commit(&bars[C::kEmpty + pair]);
         if (last) one_commit(&bars[C::kAccFull]);
-        B.next(a, full, seg1);
+        B.next(a, seg1);
         if (A.t < seg1 && !scores()) return;
     }
 }
 
 // The (lse, delta) of row 32 half + lane of item x of a unit.
 template <bool kSm>
-__device__ __forceinline__ float2 row_stats(const PrefixUnit& u, const BwArgs& a, int full, int items, int x,
+__device__ __forceinline__ float2 row_stats(const PrefixUnit& u, const BwArgs& a, int items, int x,
                                             int half, int lane) {
     float2 v = make_float2(INFINITY, 0.0f);
     if (kSm && x < items) {
-        const int m = full == 2 ? x >> 1 : x, row = (full == 2 ? (x & 1) * kItem : 0) + 32 * half + lane;
+        const int m = x >> 1, row = (x & 1) * kItem + 32 * half + lane;
         if (row < tile_rows(u, a, m)) {
             const int tt = row / a.r;
             const int64_t at = (int64_t)(u.tok + m * a.tpt + tt) * a.H + u.hk * a.r + (row - tt * a.r);
@@ -321,38 +329,37 @@ __device__ __forceinline__ void kv_rows(const BwArgs& a, uint8_t* smem, uint64_t
     // a warp's row statistics, two items' in turn
     float2* stat = reinterpret_cast<float2*>(smem + C::kOffStat) + (warp - 4) * 128;
     const ActScale ks = act_scale<ACT>(a.alpha);
-    const int full = a.tpt * a.r > kItem ? 2 : 1;
     uint32_t e0 = 0;
     Places at;
     PrefixUnit u = load_unit(a.units + seg0);
-    int items = unit_items(u, a, full);
+    int items = unit_items(u, a);
     // the statistics of this slot's next item, on their way while the one
     // before it is worked on
-    float2 next0 = row_stats<kSm>(u, a, full, items, s, 0, lane);
-    float2 next1 = row_stats<kSm>(u, a, full, items, s, 1, lane);
+    float2 next0 = row_stats<kSm>(u, a, items, s, 0, lane);
+    float2 next1 = row_stats<kSm>(u, a, items, s, 1, lane);
     for (int t = seg0; t < seg1; ++t) {
         const PrefixUnit coming = load_unit(a.units + min(t + 1, seg1 - 1));
         const bool banded = (u.flags & kPieceOwn) && a.windowed;
         const int jpos = u.j0 + key;
         // this slot's items of the unit: those with e0 + x of its parity
         int x = (int)((e0 ^ (uint32_t)s) & 1);
-        const int coming_items = unit_items(coming, a, full), coming_x = (int)((e0 + items) ^ (uint32_t)s) & 1;
+        const int coming_items = unit_items(coming, a), coming_x = (int)((e0 + items) ^ (uint32_t)s) & 1;
         if (x >= items) {   // none: the next unit's instead
-            next0 = row_stats<kSm>(coming, a, full, coming_items, coming_x, 0, lane);
-            next1 = row_stats<kSm>(coming, a, full, coming_items, coming_x, 1, lane);
+            next0 = row_stats<kSm>(coming, a, coming_items, coming_x, 0, lane);
+            next1 = row_stats<kSm>(coming, a, coming_items, coming_x, 1, lane);
         }
         for (; x < items; x += 2) {
             const uint32_t e = e0 + x;
-            const int m = full == 2 ? x >> 1 : x, r0 = full == 2 ? (x & 1) * kItem : 0;
+            const int m = x >> 1, r0 = (x & 1) * kItem;
             const int n = min(kItem, tile_rows(u, a, m) - r0);
             float2* sb = stat + ((e >> 1) & 1) * 64;
             if (kSm) {
                 sb[lane] = next0;
                 sb[32 + lane] = next1;
                 const bool more = x + 2 < items;
-                next0 = row_stats<kSm>(more ? u : coming, a, full, more ? items : coming_items, more ? x + 2 : coming_x,
+                next0 = row_stats<kSm>(more ? u : coming, a, more ? items : coming_items, more ? x + 2 : coming_x,
                                        0, lane);
-                next1 = row_stats<kSm>(more ? u : coming, a, full, more ? items : coming_items, more ? x + 2 : coming_x,
+                next1 = row_stats<kSm>(more ? u : coming, a, more ? items : coming_items, more ? x + 2 : coming_x,
                                        1, lane);
                 __syncwarp();
             }

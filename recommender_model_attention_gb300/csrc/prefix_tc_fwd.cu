@@ -67,7 +67,7 @@ struct PfParams {
     const int32_t* seg;
     float* parts;
     float* ml;
-    int r, tpt, windowed, window;
+    int r, windowed, window;
     int q_bytes;      // bytes of one query tile's load
     float alpha;
     int32_t* err;
@@ -545,7 +545,6 @@ gdpa_status launch_prefix_tc_fwd(PrefixPlan& p, const PrefixIO& io, cudaStream_t
     prm.parts = p.d_parts;
     prm.ml = p.d_ml;
     prm.r = p.r;
-    prm.tpt = p.tpt;
     prm.windowed = p.mask == GDPA_MASK_CAUSAL_WINDOW;
     prm.window = p.window;
     prm.q_bytes = p.tpt * p.r * p.d * 2;
