@@ -8,8 +8,8 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import recommender_model_attention_gb300 as gd  # noqa: E402
-from prefix_util import batch  # noqa: E402
-from test_gpu_prefix import make  # noqa: E402
+from prefix_util import batch, f64, orc, ref  # noqa: E402
+from test_gpu_prefix import make, run  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -190,3 +190,44 @@ def test_plans_are_refused_on_a_stream_that_is_captured():
     torch.cuda.synchronize()
     assert torch.all(out == 2)
     both(gd.PrefixPlan(*offs, 2, 64), x, "softmax")
+
+
+@pytest.mark.parametrize("d", [32, 128])
+def test_large_scores_float32(d):
+    """Scores of hundreds in float32, to a bound that weights or rows rounded to
+    bf16 would break.
+
+    A score is d products summed in float32, off by at most d 2^-24 of its
+    absolute terms A, and its scale's product by 2^-24 of it: e = (d + 1) 2^-24
+    max_j A_ij for a row i.  The weights over their sum are then off by a factor
+    of e^(2 e), and by what exp (2 ulp), the 900 sums of weights and values and
+    the joining of parts add, below 1000 * 2^-24 of the absolute sum together."""
+    offs = batch([50, 3], [33, 2], [2], [900])
+    x = make(offs, 2, 2, d, "f32")
+    x[1] = x[1] * torch.linspace(0.1, 30, 900, device="cuda")[:, None, None]
+    plan = gd.PrefixPlan(*offs, 2, d)
+    o, lse = gd.gdpa_prefix_softmax_fwd(plan, *x[:5])
+    plan.check()
+    y = f64(*x[:5])
+    want, wlse, size = orc.fwd(offs, *y, d ** -0.5, "softmax")
+    terms = np.zeros(wlse.shape)
+    for rows, pre, own, see in orc.groups(*offs):
+        for h in range(2):
+            a = np.abs(y[0][rows, h]) @ np.abs(np.concatenate([y[1][pre, h], y[3][own, h]])).T * d ** -0.5
+            terms[rows, h] = np.where(see, a, 0.0).max(1)
+    e = (d + 1) * 2.0 ** -24 * terms
+    assert wlse.max() > 50
+    err = np.abs(ref.to_f64(o) - want)
+    bound = (np.exp(2 * e) - 1 + 1000 * 2.0 ** -24)[..., None] * size[0]
+    assert np.all(err <= bound), np.max(err / bound)
+    assert np.all(np.abs(ref.to_f64(lse) - wlse) <= e + 1000 * 2.0 ** -24 + 2.0 ** -22 * np.abs(wlse))
+    # the bound sees a rounding to bf16: the plain form with bf16 rows breaks it
+    r = [ref.to_f64(t.bfloat16()) for t in x[:5]]
+    assert np.any(np.abs(orc.fwd(offs, *r, d ** -0.5, "softmax")[0] - want) > bound)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("d", range(4, 129, 4))
+def test_every_head_dim(d, dt):
+    offs = batch([3, 1, 0, 40], [2, 0, 5, 40], [2, 2], [4, 70])
+    run(offs, 2, 1, d, dt, "softmax", window=7)
