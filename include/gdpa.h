@@ -682,7 +682,9 @@ gdpa_status gdpa_prefix_fwd(gdpa_prefix_plan plan, gdpa_dtype dtype, const void*
                             float alpha, gdpa_act act, void* stream);
 /* Gradients of every input, all overwritten: dkp, dvp summed over the group's
  * samples, all key gradients over the query heads that share the head.  o and
- * lse: the forward's outputs (softmax; ignored otherwise). */
+ * lse: the forward's outputs (softmax; ignored otherwise).  dq (as the forward's
+ * o) may lie over an input; INVALID_ARG if another gradient does, or two
+ * gradients over each other. */
 gdpa_status gdpa_prefix_bwd(gdpa_prefix_plan plan, gdpa_dtype dtype, const void* q, const void* kp,
                             const void* vp, const void* k, const void* v, const void* o,
                             const void* d_o, const float* lse, void* dq, void* dkp, void* dvp,

@@ -221,6 +221,29 @@ gdpa_status check_inputs(const PrefixPlan& p, gdpa_dtype dtype, const PrefixIO& 
     return GDPA_OK;
 }
 
+// Gradients of a backward that would be written where something is still read,
+// or written twice: dq is stored last, after everything has been read, the key
+// gradients are not.
+bool gradients_clash(const PrefixPlan& p, gdpa_dtype dt, const PrefixIO& io) {
+    struct Range { uintptr_t at; size_t n; };
+    const size_t e = dt == GDPA_BF16 ? 2 : 4, row = (size_t)p.d * e;
+    const size_t nq = (size_t)p.Tq * p.H * row, np = (size_t)p.Tp * p.Hkv * row, nk = (size_t)p.Tkv * p.Hkv * row;
+    const bool sm = io.act == GDPA_ACT_SOFTMAX;
+    const Range out[] = {{(uintptr_t)io.dkp, np}, {(uintptr_t)io.dvp, np}, {(uintptr_t)io.dk, nk},
+                         {(uintptr_t)io.dv, nk}, {(uintptr_t)io.dq, nq}};
+    const Range in[] = {{(uintptr_t)io.q, nq}, {(uintptr_t)io.kp, np}, {(uintptr_t)io.vp, np}, {(uintptr_t)io.k, nk},
+                        {(uintptr_t)io.v, nk}, {(uintptr_t)io.d_o, nq}, {(uintptr_t)io.o, sm ? nq : 0},
+                        {(uintptr_t)io.lse, sm ? (size_t)p.Tq * p.H * 4 : 0}};
+    auto meet = [](const Range& a, const Range& b) { return a.at < b.at + b.n && b.at < a.at + a.n && a.n && b.n; };
+    for (int i = 0; i < 4; ++i) {
+        for (const Range& x : in)
+            if (meet(out[i], x)) return true;
+        for (int j = i + 1; j < 5; ++j)
+            if (meet(out[i], out[j])) return true;
+    }
+    return false;
+}
+
 // true when this plan and type run on the tensor-core kernels
 bool use_tc(const PrefixPlan& p, gdpa_dtype dt) {
     return dt == GDPA_BF16 && p.kernel != GDPA_KERNEL_SIMT && (p.d == 64 || p.d == 128);
@@ -262,7 +285,7 @@ gdpa_status bwd(gdpa_prefix_plan plan, gdpa_dtype dtype, const PrefixIO& io, voi
     const void* out[] = {io.d_o, io.dq, io.dkp, io.dvp, io.dk, io.dv, sm ? io.o : nullptr};
     for (const void* x : out)
         if (!aligned16(x)) return GDPA_ERR_INVALID_ARG;
-    if ((uintptr_t)io.lse % 4) return GDPA_ERR_INVALID_ARG;
+    if ((uintptr_t)io.lse % 4 || gradients_clash(p, dtype, io)) return GDPA_ERR_INVALID_ARG;
     if (p.kernel == GDPA_KERNEL_TCGEN05 && !use_tc(p, dtype)) return GDPA_ERR_UNSUPPORTED;
     if (gdpa_status s = check_device(p)) return s;
     cudaStream_t st = (cudaStream_t)stream;

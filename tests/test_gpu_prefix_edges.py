@@ -231,3 +231,44 @@ def test_large_scores_float32(d):
 def test_every_head_dim(d, dt):
     offs = batch([3, 1, 0, 40], [2, 0, 5, 40], [2, 2], [4, 70])
     run(offs, 2, 1, d, dt, "softmax", window=7)
+
+
+@pytest.mark.parametrize("act", ["softmax", "silu"])
+@pytest.mark.parametrize("dt,d", [("bf16", 128), ("f32", 32)])
+def test_outputs_over_inputs(dt, d, act):
+    """o and dq may be an input's memory, being stored last; key gradients, which
+    are stored while keys are still read, are refused there and over each other."""
+    offs = batch([5, 60, 1], [4, 70, 0], [2, 1], [300, 600])
+    x = make(offs, 4, 2, d, dt)
+    plan = gd.PrefixPlan(*offs, 4, d, kv_heads=2)
+    want = both(plan, x, act)
+    sm = act == "softmax"
+    o, lse = want[0], want[1] if sm else None
+
+    def bwd(y, do, o=o, **kw):
+        if sm:
+            return gd.gdpa_prefix_softmax_bwd(plan, *y, o, do, lse, **kw)
+        return gd.gdpa_prefix_bwd(plan, *y, do, act=act, **kw)
+    for name in ("q", "do", "o"):
+        y, do, o2 = [t.clone() for t in x[:5]], x[5].clone(), o.clone()
+        got = bwd(y, do, o2, dq={"q": y[0], "do": do, "o": o2}[name])
+        for a, b in zip(got, want[-5:]):
+            assert torch.equal(a, b)
+    q = x[0].clone()
+    if sm:
+        got = gd.gdpa_prefix_softmax_fwd(plan, q, *x[1:5], o=q)[0]
+    else:
+        got = gd.gdpa_prefix_fwd(plan, q, *x[1:5], act=act, o=q)
+    assert torch.equal(got, o)
+    spare = torch.zeros(2 * x[1].numel(), dtype=x[1].dtype, device="cuda")
+    half = x[1].numel() - 64   # (a multiple of 16 bytes)
+    over = dict(dkp=spare[:x[1].numel()].view(x[1].shape), dvp=spare[half:half + x[1].numel()].view(x[1].shape))
+    for kw in (dict(dk=x[3]), dict(dv=x[4]), dict(dkp=x[1]), dict(dvp=x[2]), dict(dkp=x[2]), dict(dv=x[3]), over,
+               dict(dk=torch.empty_like(x[3]), dv=None)):
+        if kw.get("dv", 0) is None:
+            kw["dv"] = kw["dk"]
+        with pytest.raises(gd.GdpaError) as e:
+            bwd(x[:5], x[5], **kw)
+        assert e.value.status == 1
+    for a, b in zip(both(plan, x, act), want):
+        assert torch.equal(a, b)
