@@ -9,7 +9,7 @@ torch = pytest.importorskip("torch")
 
 import recommender_model_attention_gb300 as gd  # noqa: E402
 from prefix_util import batch, f64, orc, ref  # noqa: E402
-from test_gpu_prefix import make, run  # noqa: E402
+from test_gpu_prefix import DT, make, run  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -272,3 +272,27 @@ def test_outputs_over_inputs(dt, d, act):
         assert e.value.status == 1
     for a, b in zip(both(plan, x, act), want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dt,H,kernel", [("bf16", 8, "auto"), ("f32", 8, "auto"), ("bf16", 8, "simt")])
+def test_far_own_keys_past_32_bit_offsets(dt, H, kernel):
+    """Own keys whose element and byte offsets pass 2^32: a small sample, one of
+    9 to 64 rows and a large one behind a sample without rows that owns 2^22 keys."""
+    d, n = 128, 2 ** 22
+    lq, lkv = [0, 2, 30, 100], [n, 40, 50, 90]
+    offs, small = batch(lq, lkv, [4], [60]), batch(lq[1:], lkv[1:], [3], [60])
+    x = make(small, H, H, d, dt)
+    alone = gd.PrefixPlan(*small, H, d)
+    alone.set_kernel(kernel)
+    want = both(alone, x, "softmax")
+    k, v = (torch.zeros((n + 180, H, d), dtype=DT[dt], device="cuda") for _ in "kv")
+    k[n:], v[n:] = x[3], x[4]
+    plan = gd.PrefixPlan(*offs, H, d)
+    plan.set_kernel(kernel)
+    got = both(plan, [x[0], x[1], x[2], k, v, x[5]], "softmax")
+    for a, b in zip(got[5:], want[5:]):
+        assert torch.all(a[:n] == 0)
+        # (pieces are dealt to the queues in other places: other parts' sums)
+        assert float((a[n:].float() - b.float()).abs().max()) <= 2.0 ** -7 * float(b.float().abs().max())
+    for a, b in zip(got[:5], want[:5]):
+        assert float((a.float() - b.float()).abs().max()) <= 2.0 ** -7 * float(b.float().abs().max())

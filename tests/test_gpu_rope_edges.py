@@ -64,3 +64,18 @@ def test_positions_counted_from_many_offsets(B, dt):
     assert torch.equal(got[:n], want) and torch.all(got[n:] == 3.25)
     at = [0, n // 3, n - 1]
     check(want[at], x[at], [int(pos[i]) for i in at], orc.frequencies(64), "half")
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rows_past_32_bit_offsets(layout):
+    """Values whose element offsets pass 2^31 and byte offsets 2^32, in place."""
+    H, d = 8, 128
+    T = 2 ** 31 // (H * d) + 77
+    x = torch.zeros((T, H, d), dtype=torch.bfloat16, device="cuda")
+    at = [0, 1, T // 2, T - 78, T - 77, T - 1]
+    mine = rows(len(at), H, d, "bf16")
+    x[at] = mine
+    pos = torch.arange(T, device="cuda")
+    assert gd.gdpa_rope_fwd(gd.Rope(d, layout=layout), x, positions=pos, q_out=x) is x
+    check(x[at], mine, at, orc.frequencies(d), layout)
+    assert int(torch.count_nonzero(x)) == int(torch.count_nonzero(x[at]))
