@@ -12,15 +12,16 @@
 // accumulator to operand layout by movmatrix.  The work is bounded by reading
 // the keys once; a 128-row tile on the fifth-generation tensor core would cost
 // every sample its whole chain of latencies for a row or two.  Forward, 16
-// warps an SM, keys in registers: 75 MB of keys of 512 candidates in 20 us
-// (through shared memory as below 19, and slower for d = 64).
+// warps an SM, keys in registers: 75 MB of keys of 512 candidates in 19 us
+// (through shared memory as below the same, and slower for d = 64).
 //
 // The backward of a unit of at most 8 rows runs in one warp too: each key's
 // dK and dV are done in its step, dQ^T = K^T dS^T adds up over the steps, so
 // every sum has one owner and one order.  It has registers for 8 warps an SM
 // only, so the next step's keys are copied to shared memory meanwhile, and dK
-// and dV leave as whole sectors: 47 us for a training batch of 32 users (0.2
-// GB in all); keys loaded into registers 54, with 12 warps 54, half sectors 54.
+// and dV leave as whole sectors: 44 us for a training batch of 32 users (0.2
+// GB in all), 47 with the keys prefetched into L2 as well; beside that, keys
+// loaded into registers 54, with 12 warps 54, half sectors 54.
 #include "act.cuh"
 #include "prefix_internal.h"
 #include "prefix_mma.cuh"
