@@ -67,3 +67,26 @@ def test_outputs_of_a_call_on_another_stream(name):
     for a, b in zip(copies, want):
         assert torch.equal(a, b)
     del more
+
+
+@pytest.mark.parametrize("name", ["rope", "prefix", "prefix_bwd"])
+def test_outputs_allocated_for_another_stream_of_a_capture(name):
+    """A captured call on a branch of the graph that allocates its outputs."""
+    call = _calls()[name]
+    want = call()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        for _ in range(3):   # outputs freed while capturing, then some that are kept
+            got = call(stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        copies = [t.clone() for t in got]
+    for _ in range(2):
+        for t in copies:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b, c in zip(got, copies, want):
+            assert torch.equal(a, c) and torch.equal(b, c)
