@@ -602,9 +602,10 @@ gdpa_status gdpa_rope_apply(const gdpa_rope* rope, int inverse, gdpa_dtype dtype
  * ordered by the library, calls from several host threads serialised.  Calls
  * may be captured into a CUDA graph (the first backward of a plan allocates
  * and is refused with ALLOC while capturing), where those of one capture are
- * ordered alike, on whichever of its streams; the plan must outlive the
- * graph, and replays that share a plan must not overlap on the GPU with each
- * other or with other calls on the plan.
+ * ordered alike, on whichever of its streams (with up to 16 captures of one plan
+ * under way at once); the plan must outlive the graph, and replays that share a
+ * plan must not overlap on the GPU with each other or with other calls on the
+ * plan.
  */
 typedef struct gdpa_prefix_plan_s* gdpa_prefix_plan;
 

@@ -2,6 +2,7 @@
 // workspaces, ordering of a plan's work, dispatch.
 #include <string.h>
 
+#include <algorithm>
 #include <new>
 
 #include "prefix_internal.h"
@@ -10,6 +11,8 @@ using gdpa::PrefixIO;
 using gdpa::PrefixPlan;
 
 namespace {
+
+constexpr size_t kCaptures = 16;   // captures under way at once on one plan
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -34,7 +37,7 @@ void free_prefix(PrefixPlan* p) {
         for (void* b : bufs)
             if (b) cudaFreeAsync(b, fs);
         if (p->last) cudaEventDestroy(p->last);
-        if (p->in_capture) cudaEventDestroy(p->in_capture);
+        for (const PrefixPlan::InCapture& e : p->captures) cudaEventDestroy(e.event);
         if (p->ready) cudaEventDestroy(p->ready);
         if (fs) cudaStreamDestroy(fs);
         if (cur >= 0 && cur != p->device) cudaSetDevice(cur);
@@ -75,8 +78,9 @@ gdpa_status begin_work(PrefixPlan& p, const Call& c) {
         const bool ok = cudaEventSynchronize(p.ready) == cudaSuccess &&
                         (!p.has_work || cudaEventSynchronize(p.last) == cudaSuccess);
         cudaThreadExchangeStreamCaptureMode(&mode);
-        if (!ok || (p.capture == c.capture && cudaStreamWaitEvent(c.st, p.in_capture, 0) != cudaSuccess))
-            return GDPA_ERR_CUDA;
+        if (!ok) return GDPA_ERR_CUDA;
+        for (const PrefixPlan::InCapture& e : p.captures)
+            if (e.id == c.capture && cudaStreamWaitEvent(c.st, e.event, 0) != cudaSuccess) return GDPA_ERR_CUDA;
         return GDPA_OK;
     }
     if (!p.is_ready) {
@@ -94,9 +98,24 @@ gdpa_status begin_work(PrefixPlan& p, const Call& c) {
 
 gdpa_status end_work(PrefixPlan& p, const Call& c) {
     if (c.capture) {   // (the graph's replays are the caller's to order)
-        p.capture = 0;
-        if (cudaEventRecord(p.in_capture, c.st) != cudaSuccess) return GDPA_ERR_CUDA;
-        p.capture = c.capture;
+        // captures may be under way side by side; the place of the one that the
+        // plan was not in for longest is taken by a new one
+        auto& all = p.captures;
+        size_t i = 0;
+        while (i < all.size() && all[i].id != c.capture) ++i;
+        if (i == all.size()) {
+            if (all.size() < kCaptures) {
+                PrefixPlan::InCapture e{0, nullptr};
+                if (cudaEventCreateWithFlags(&e.event, cudaEventDisableTiming) != cudaSuccess) return GDPA_ERR_CUDA;
+                all.push_back(e);
+            } else {
+                i = 0;
+            }
+        }
+        std::rotate(all.begin() + i, all.begin() + i + 1, all.end());
+        all.back().id = 0;
+        if (cudaEventRecord(all.back().event, c.st) != cudaSuccess) return GDPA_ERR_CUDA;
+        all.back().id = c.capture;
         return GDPA_OK;
     }
     if (cudaEventRecord(p.last, c.st) != cudaSuccess) return GDPA_ERR_CUDA;
@@ -141,6 +160,7 @@ gdpa_status create(const int32_t* q_off, const int32_t* kv_off, int B, const int
             }
         }
         p->S = num_sms;
+        p->captures.reserve(kCaptures);
         std::vector<int32_t> none;
         if (!kv_off) {
             none.assign((size_t)B + 1, 0);
@@ -195,7 +215,6 @@ gdpa_status create(const int32_t* q_off, const int32_t* kv_off, int B, const int
             (cudaMemsetAsync(p->dev_err(), 0, 16, st) != cudaSuccess ||
              cudaEventCreateWithFlags(&p->ready, cudaEventDisableTiming) != cudaSuccess ||
              cudaEventCreateWithFlags(&p->last, cudaEventDisableTiming) != cudaSuccess ||
-             cudaEventCreateWithFlags(&p->in_capture, cudaEventDisableTiming) != cudaSuccess ||
              cudaEventRecord(p->ready, st) != cudaSuccess))
             s = GDPA_ERR_CUDA;
         if (s != GDPA_OK) cudaStreamSynchronize(st);

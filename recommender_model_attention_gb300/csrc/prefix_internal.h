@@ -111,8 +111,9 @@ struct PrefixPlan {
     int chain = 0;                   // kernels of the current call that a next one may start beside
     cudaEvent_t ready = nullptr;     // the upload, on the creation stream
     cudaEvent_t last = nullptr;      // the plan's latest work
-    cudaEvent_t in_capture = nullptr;   // its latest captured work, of the capture
-    unsigned long long capture = 0;     // with this id (0: none yet)
+    // its latest work in each of the captures that it was in last
+    struct InCapture { unsigned long long id; cudaEvent_t event; };
+    std::vector<InCapture> captures;
     bool has_work = false, is_ready = false;   // is_ready: the upload is known to be over
     std::mutex lock;                 // host state above
 

@@ -296,3 +296,80 @@ def test_far_own_keys_past_32_bit_offsets(dt, H, kernel):
         assert float((a[n:].float() - b.float()).abs().max()) <= 2.0 ** -7 * float(b.float().abs().max())
     for a, b in zip(got[:5], want[:5]):
         assert float((a.float() - b.float()).abs().max()) <= 2.0 ** -7 * float(b.float().abs().max())
+
+
+def test_two_captures_under_way_at_once():
+    """Calls of two captures alternate; each capture has two branches, so a call
+    has to find the plan's call before it in its own."""
+    import ctypes
+    rt = ctypes.CDLL("libcudart.so.13")
+
+    def ok(e):
+        assert e == 0, e
+    offs = batch([5, 300, 1], [4, 310, 0], [2, 1], [2000, 9000])
+    d = 128
+    plan = gd.PrefixPlan(*offs, 4, d, kv_heads=2)
+    x = [make(offs, 4, 2, d, "bf16", seed=i) for i in range(4)]
+    want = [both(plan, y, "softmax") for y in x]
+    outs = [[torch.zeros_like(t) for t in want[i]] for i in range(4)]
+    main, side, event = ([torch.cuda.Stream() for _ in range(2)], [torch.cuda.Stream() for _ in range(2)],
+                         [[ctypes.c_void_p() for _ in range(2)] for _ in range(2)])
+    torch.cuda.synchronize()
+    for m, s, e in zip(main, side, event):   # (relaxed: allocations elsewhere do not end them)
+        for one in e:
+            ok(rt.cudaEventCreateWithFlags(ctypes.byref(one), 2))
+        ok(rt.cudaStreamBeginCapture(ctypes.c_void_p(m.cuda_stream), 2))
+        ok(rt.cudaEventRecord(e[0], ctypes.c_void_p(m.cuda_stream)))
+        ok(rt.cudaStreamWaitEvent(ctypes.c_void_p(s.cuda_stream), e[0], 0))
+    for part in ("fwd", "bwd"):
+        for branch in range(2):
+            for c in range(2):
+                i = 2 * c + branch
+                o, lse, *g = outs[i]
+                st = (main, side)[branch][c]
+                if part == "fwd":
+                    gd.gdpa_prefix_softmax_fwd(plan, *x[i][:5], o=o, lse=lse, stream=st)
+                else:
+                    gd.gdpa_prefix_softmax_bwd(plan, *x[i][:5], o, x[i][5], lse, *g, stream=st)
+    graphs = []
+    for m, s, e in zip(main, side, event):
+        graph, run_it = ctypes.c_void_p(), ctypes.c_void_p()
+        ok(rt.cudaEventRecord(e[1], ctypes.c_void_p(s.cuda_stream)))
+        ok(rt.cudaStreamWaitEvent(ctypes.c_void_p(m.cuda_stream), e[1], 0))
+        ok(rt.cudaStreamEndCapture(ctypes.c_void_p(m.cuda_stream), ctypes.byref(graph)))
+        ok(rt.cudaGraphInstantiate(ctypes.byref(run_it), graph, ctypes.c_ulonglong(0)))
+        graphs.append((graph, run_it))
+    for _ in range(10):
+        for call in outs:
+            for t in call:
+                t.zero_()
+        torch.cuda.synchronize()
+        for _, run_it in graphs:   # one after the other
+            ok(rt.cudaGraphLaunch(run_it, ctypes.c_void_p(main[0].cuda_stream)))
+        torch.cuda.synchronize()
+        for i in range(4):
+            for a, b in zip(outs[i], want[i]):
+                assert torch.equal(a, b)
+    for graph, run_it in graphs:
+        ok(rt.cudaGraphExecDestroy(run_it))
+        ok(rt.cudaGraphDestroy(graph))
+    for e in event:
+        for one in e:
+            ok(rt.cudaEventDestroy(one))
+
+
+def test_more_captures_than_are_remembered():
+    offs = batch([5, 60, 1], [4, 70, 0], [2, 1], [300, 600])
+    x = make(offs, 4, 2, 64, "bf16")
+    plan = gd.PrefixPlan(*offs, 4, 64, kv_heads=2)
+    want = both(plan, x, "softmax")
+    o, lse = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    for _ in range(40):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            gd.gdpa_prefix_softmax_fwd(plan, *x[:5], o=o, lse=lse)
+            gd.gdpa_prefix_softmax_fwd(plan, *x[:5], o=o, lse=lse)
+        o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[0])
