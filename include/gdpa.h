@@ -697,6 +697,117 @@ gdpa_status gdpa_prefix_error_detail(gdpa_prefix_plan plan, int32_t* detail);
 int64_t gdpa_prefix_launches(gdpa_prefix_plan plan);
 void gdpa_prefix_destroy(gdpa_prefix_plan plan);
 
+/*
+ * History cache: the keys and values of events, kept in pages for serving, and
+ * the attention of new rows over them.  A page holds `page` consecutive events
+ * of one sample (a power of two, 16 .. 1024) for all key heads; a sample's
+ * events lie on the pages of its row of the table, in order: event e on page
+ * table[b * stride + e / page].  Pages may be shared by samples that read them.
+ *
+ * Rows are held as they are (BF16, F32) or in 8 bits (E4M3): codes c_i and one
+ * power of two a row and head, x_i ~ c_i 2^e, with the least e >= -126 for which
+ * the row's largest magnitude is at most 448 2^e; x_i 2^-e is rounded to the
+ * nearest E4M3 code, ties to the even one.  A row of one head that holds an
+ * infinity or a NaN is all NaN.  How rows are arranged inside a page is the
+ * library's own; gdpa_cache_read gives them back.
+ *
+ * A gdpa_cache is plain host data over the caller's device memory (k, v and,
+ * for E4M3, k_scale, v_scale, 128-byte aligned, of the sizes that
+ * gdpa_cache_bytes gives), copied into each launch: it serves any stream and
+ * thread, and calls that write events and calls that read them are ordered by
+ * the caller, as for any memory.  The kernels check every table entry and event
+ * against the cache: what lies outside is neither read nor written, and the
+ * first such entry is recorded in `error` (4 device words, zero at first), for
+ * gdpa_cache_check to report.
+ */
+typedef enum { GDPA_STORE_BF16 = 0, GDPA_STORE_F32 = 1, GDPA_STORE_E4M3 = 2 } gdpa_store;
+typedef struct {
+    void *k, *v;
+    uint8_t *k_scale, *v_scale;
+    int32_t* error;
+    int32_t pages, page, heads, d, store;
+} gdpa_cache;
+
+/* Rows of a call: element (t, h, c) at x[t * token + h * head + c], strides in
+ * elements. */
+typedef struct {
+    const void* x;
+    int64_t token, head;
+} gdpa_cache_rows;
+
+/* Which events a call's rows are: sample b's are rows [off[b], off[b + 1]), its
+ * i-th row being event starts[b] + i (starts NULL: from 0); rows behind off[B]
+ * are left alone.  All device int32; table [B] rows of `width` pages, `stride`
+ * apart. */
+typedef struct {
+    const int32_t *table, *off, *starts;
+    int64_t stride;
+    int32_t width, B;
+} gdpa_cache_where;
+
+/* Bytes of k (and of v), and of k_scale (and of v_scale; 0 but for E4M3).
+ * UNSUPPORTED for d > 128, rows that are not a multiple of 16 bytes in the
+ * cache, other page sizes, more than 4096 heads. */
+gdpa_status gdpa_cache_bytes(const gdpa_cache* cache, int64_t* rows, int64_t* scales);
+
+/* Write T rows of K and V to their events / read them back, in one launch.
+ * dtype: the cache's own type; E4M3 takes and gives bf16 or float32 (each value
+ * rounded once).  An event written twice in one call holds either row.  Reads
+ * want rows and strides that are multiples of 16 bytes; an event outside the
+ * cache reads as zeros.  INVALID_ARG for bad pointers, sizes or types;
+ * UNSUPPORTED as gdpa_cache_bytes and for width * page > 2^31 - 65537.  Enqueued on
+ * `stream`, no allocation, capturable. */
+gdpa_status gdpa_cache_write(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T,
+                             const gdpa_cache_rows* k, const gdpa_cache_rows* v,
+                             const gdpa_cache_where* where, void* stream);
+gdpa_status gdpa_cache_read(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T,
+                            const gdpa_cache_rows* k, const gdpa_cache_rows* v,
+                            const gdpa_cache_where* where, void* stream);
+
+/* Attention of T new rows over the cached events of their samples:
+ *     O_i = sum_j w_ij V_j,   w = act(alpha q_i.k_j), or softmax over the row's
+ * visible events.  Which events row i of sample b sees, by `mask`:
+ *   CAUSAL   events 0 .. starts[b] + i: the history and the new rows up to
+ *            itself, whose K and V were written before (position starts[b] + i);
+ *   HISTORY  events 0 .. starts[b] - 1 (position starts[b]; nothing of the new
+ *            rows is looked at);
+ *   TREE     the history, itself and its ancestors among the new rows: row i's
+ *            K and V are event starts[b] + i, its parent is new row parents[off[b]
+ *            + i] < i of its sample (anything else: none), its position
+ *            starts[b] + its number of ancestors, a history event's its index.
+ * With window W > 0 only those at positions above p - W for a row at position
+ * p, and the events at positions below `sinks`, which stay visible.  A row that
+ * sees nothing gives O = 0, lse = -inf.  What an event that a row does not see
+ * holds does not matter to the row, whatever it is.
+ *
+ * q [T] rows of H heads (q->x, strides), o [T][H][d] and lse [T][H] (float32,
+ * may be NULL, softmax only) contiguous; H a multiple of the cache's key heads,
+ * H / heads <= 128.  dtype: as for gdpa_cache_write.  bf16 with d = 64 or 128
+ * runs on the tensor cores, everything else on the CUDA cores.  workspace:
+ * gdpa_cache_workspace bytes of device memory (16-byte aligned) for this call
+ * alone while it runs.  Nothing depends on host knowledge of lengths: one
+ * captured graph serves growing histories.
+ * INVALID_ARG, UNSUPPORTED as above. */
+typedef enum { GDPA_CACHE_CAUSAL = 0, GDPA_CACHE_HISTORY = 1, GDPA_CACHE_TREE = 2 } gdpa_cache_mask;
+typedef struct {
+    int32_t mask, window, sinks;
+    int32_t act;
+    float alpha;
+    const int32_t* parents;   /* TREE: device int32 [T] */
+} gdpa_cache_attn;
+gdpa_status gdpa_cache_workspace(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T, int H, int B,
+                                 int64_t* bytes);
+gdpa_status gdpa_cache_fwd(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T, int H,
+                           const gdpa_cache_rows* q, void* o, float* lse,
+                           const gdpa_cache_where* where, const gdpa_cache_attn* attn,
+                           void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Waits for `stream`; DEVICE if a call since the last check met a table entry or
+ * an event outside the cache: detail (int32 [4]) receives 2, what it was (1 a
+ * page, 2 an event behind the table's pages or before 0, 3 a negative start),
+ * the sample and the value, and the record is cleared. */
+gdpa_status gdpa_cache_check(const gdpa_cache* cache, int32_t* detail, void* stream);
+
 /* Activation test hook.
  *
  * Evaluates act(x) and act'(x) element-wise with the same device functions

@@ -14,6 +14,7 @@ from .gdpa import (  # noqa: F401
     BLOCK_M,
     BLOCK_N,
     GdpaError,
+    KVCache,
     LIB_PATH,
     MASK,
     MX,
@@ -25,6 +26,10 @@ from .gdpa import (  # noqa: F401
     act_eval,
     gdpa_bwd,
     gdpa_bwd_mx,
+    gdpa_cache_fwd,
+    gdpa_cache_read,
+    gdpa_cache_softmax_fwd,
+    gdpa_cache_write,
     gdpa_fwd,
     gdpa_fwd_mx,
     gdpa_fwd_noalloc,

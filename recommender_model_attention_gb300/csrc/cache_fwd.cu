@@ -1,0 +1,236 @@
+// Attention over the history cache: the C entry points and the kernel that
+// joins the parts of items that several CTAs share.
+#include <string.h>
+
+#include <atomic>
+
+#include "cache_attn.cuh"
+
+namespace gdpa {
+namespace {
+
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+constexpr int kMaxGrid = 2048;   // CTAs of an attention kernel at most (their records fit a block's shared memory)
+
+// A block a row: its warps take turns over the row's parts, then add up in
+// shared memory, always in the same order.
+template <typename E, bool SM>
+__global__ void __launch_bounds__(kJoinThreads)
+cache_join_kernel(const __grid_constant__ AttnArgs a, int ctas) {
+    __shared__ int first[kMaxGrid + 1];   // rows of the items before
+    __shared__ int tmp[kJoinWarps];
+    __shared__ float4 sums[kJoinWarps][32];
+    __shared__ float2 ml[kJoinWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int d = a.c.d, ld = a.TM * (d + 2);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int base = 0;
+    for (int c0 = 0; c0 < ctas; c0 += kJoinThreads) {
+        const int c = c0 + tid;
+        int n = 0;
+        if (c < ctas) n = a.desc[c].parts > 1 ? a.desc[c].rows : 0;
+        int x = n;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, m);
+            if (lane >= m) x += y;
+        }
+        if (lane == 31) tmp[warp] = x;
+        __syncthreads();
+        int before = base;
+        for (int i = 0; i < kJoinWarps; ++i) {
+            if (i < warp) before += tmp[i];
+            base += tmp[i];
+        }
+        if (c < ctas) first[c] = before + x - n;
+        __syncthreads();
+    }
+    if (tid == 0) first[ctas] = base;
+    __syncthreads();
+    for (int i = blockIdx.x; i < base; i += gridDim.x) {
+        int lo = 0, hi = ctas;   // the item whose rows hold i (the last one with first <= i and rows)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (first[mid] <= i) lo = mid; else hi = mid;
+        }
+        const CacheDesc t = a.desc[lo];
+        const int r = i - first[lo];
+        // part p: slot 2 lo + 1, then 2 (lo + 1), 2 (lo + 2), ...
+        const auto slot = [&](int p) { return a.part + (int64_t)(p == 0 ? 2 * lo + 1 : 2 * (lo + p)) * ld; };
+        float M = -INFINITY;
+        if (SM) {
+            for (int p = lane; p < t.parts; p += 32) M = fmaxf(M, slot(p)[a.TM * d + r]);
+#pragma unroll
+            for (int m = 1; m < 32; m <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
+        }
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float l = 0.0f;
+#pragma unroll 4
+        for (int p = warp; p < t.parts; p += kJoinWarps) {
+            const float* s = slot(p);
+            float f = 1.0f;
+            if (SM) {
+                const float m = s[a.TM * d + r], n = s[a.TM * (d + 1) + r];
+                f = m == -INFINITY ? (n == 0.0f ? 0.0f : n) : ex2_approx(m - M);   // (n: a NaN)
+                l += n * f;
+            }
+            if (4 * lane < d) {
+                const float4 y = *reinterpret_cast<const float4*>(s + r * d + 4 * lane);
+                x.x += y.x * f;
+                x.y += y.y * f;
+                x.z += y.z * f;
+                x.w += y.w * f;
+            }
+        }
+        sums[warp][lane] = x;
+        if (lane == 0) ml[warp] = make_float2(M, l);
+        __syncthreads();
+        if (warp == 0) {
+            for (int w = 1; w < kJoinWarps; ++w) {
+                const float4 y = sums[w][lane];
+                x.x += y.x;
+                x.y += y.y;
+                x.z += y.z;
+                x.w += y.w;
+                l += ml[w].y;
+            }
+            const int rho = t.rho0 + r, tok = rho / a.G;
+            const int64_t row = (int64_t)(t.t0 + tok) * a.H + t.h * a.G + (rho - tok * a.G);
+            float f = 1.0f;
+            if (SM) {
+                f = l == 0.0f ? 0.0f : 1.0f / l;
+                if (lane == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.693147180559945309f;
+            }
+            const float y[4] = {x.x * f, x.y * f, x.z * f, x.w * f};
+            if (4 * lane < d) put4((E*)a.o + row * d + 4 * lane, y);
+        }
+        __syncthreads();
+    }
+}
+
+template <typename E, bool SM>
+gdpa_status launch_join(const AttnArgs& a, int ctas, int sms, cudaStream_t st) {
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3((unsigned)(4 * sms));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at;
+    memset(&at, 0, sizeof(at));
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, cache_join_kernel<E, SM>, a, ctas) == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+}
+
+// SMs of the current device (looked up once a device), 0 if there is none
+int device_sms() {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+struct Shape {
+    bool tc;
+    int RT, TM, grid, sms;
+    int64_t bytes;
+};
+
+// The kernel, its tile and its workspace: rules on types and sizes alone.
+gdpa_status shape(const CacheView& c, gdpa_dtype dt, int64_t T, int H, int B, Shape& s) {
+    s.tc = dt == GDPA_BF16 && (c.d == 64 || c.d == 128);
+    // row tiles of 16 that a CTA holds: as many as an average sample fills
+    const int64_t rows = B > 0 ? T * (H / c.heads) / B : 0;
+    s.RT = !s.tc || rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    s.TM = 16 * s.RT;
+    s.sms = device_sms();
+    if (s.sms == 0) return GDPA_ERR_CUDA;
+    s.grid = s.sms * (s.tc ? kCacheTcPerSm : kCacheSimtPerSm);
+    if (s.grid > kMaxGrid) s.grid = kMaxGrid;
+    s.bytes = (int64_t)s.grid * (sizeof(CacheDesc) + 2ll * s.TM * (c.d + 2) * 4);
+    return GDPA_OK;
+}
+
+}  // namespace
+}  // namespace gdpa
+
+extern "C" {
+
+gdpa_status gdpa_cache_workspace(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T, int H, int B,
+                                 int64_t* bytes) {
+    gdpa::CacheView c;
+    gdpa_status s;
+    if (!gdpa::cache_view(cache, c, &s)) return s;
+    if (!bytes || T < 0 || B < 0 || H < 1 || H % c.heads) return GDPA_ERR_INVALID_ARG;
+    if (dtype != GDPA_BF16 && dtype != GDPA_F32) return GDPA_ERR_INVALID_ARG;
+    gdpa::Shape p;
+    s = gdpa::shape(c, dtype, T, H, B, p);
+    if (s == GDPA_OK) *bytes = p.bytes;
+    return s;
+}
+
+gdpa_status gdpa_cache_fwd(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T, int H,
+                           const gdpa_cache_rows* q, void* o, float* lse, const gdpa_cache_where* where,
+                           const gdpa_cache_attn* attn, void* workspace, int64_t workspace_bytes, void* stream) {
+    using namespace gdpa;
+    AttnArgs a;
+    memset(&a, 0, sizeof(a));
+    gdpa_status s;
+    if (!cache_view(cache, a.c, &s)) return s;
+    if (dtype != GDPA_BF16 && dtype != GDPA_F32) return GDPA_ERR_INVALID_ARG;
+    if ((a.c.store == GDPA_STORE_BF16 && dtype != GDPA_BF16) || (a.c.store == GDPA_STORE_F32 && dtype != GDPA_F32))
+        return GDPA_ERR_INVALID_ARG;
+    if (T < 0 || H < 1 || H % a.c.heads || !q || !attn) return GDPA_ERR_INVALID_ARG;
+    s = cache_where(where, T, a.c, a.w);
+    if (s != GDPA_OK) return s;
+    if (attn->mask < GDPA_CACHE_CAUSAL || attn->mask > GDPA_CACHE_TREE || attn->window < 0 || attn->sinks < 0)
+        return GDPA_ERR_INVALID_ARG;
+    if (attn->sinks > 0 && attn->window == 0) return GDPA_ERR_INVALID_ARG;
+    if (attn->act < GDPA_ACT_GELU_ERF || attn->act > GDPA_ACT_SOFTMAX) return GDPA_ERR_INVALID_ARG;
+    if (!(attn->alpha - attn->alpha == 0.0f)) return GDPA_ERR_INVALID_ARG;   // infinite or NaN
+    if (lse && (attn->act != GDPA_ACT_SOFTMAX || (uintptr_t)lse % 4)) return GDPA_ERR_INVALID_ARG;
+    const bool tree = attn->mask == GDPA_CACHE_TREE;
+    if (T > 0 && tree && (!attn->parents || (uintptr_t)attn->parents % 4)) return GDPA_ERR_INVALID_ARG;
+    a.G = H / a.c.heads;
+    if (a.G > 128 || T * H > 0x7fffffff) return GDPA_ERR_UNSUPPORTED;
+    if (T == 0 || a.w.B == 0) return GDPA_OK;
+    const size_t es = dtype == GDPA_BF16 ? 2 : 4;
+    if (!q->x || (uintptr_t)q->x % es || !o || (uintptr_t)o % 16) return GDPA_ERR_INVALID_ARG;
+    Shape p;
+    s = shape(a.c, dtype, T, H, a.w.B, p);
+    if (s != GDPA_OK) return s;
+    if (!workspace || (uintptr_t)workspace % 16 || workspace_bytes < p.bytes) return GDPA_ERR_INVALID_ARG;
+    a.q = q->x;
+    a.qt = T > 1 ? q->token : 0;
+    a.qh = H > 1 ? q->head : 0;
+    a.q_wide = (uintptr_t)q->x % 16 == 0 && a.qt * (int64_t)es % 16 == 0 && a.qh * (int64_t)es % 16 == 0;
+    a.o = o;
+    a.lse = lse;
+    a.parents = tree ? attn->parents : nullptr;
+    a.H = H;
+    a.mask = attn->mask;
+    a.window = attn->window;
+    a.sinks = attn->sinks;
+    a.act = attn->act;
+    a.TM = p.TM;
+    a.RT = p.RT;
+    a.min_share = 4 / p.RT;
+    a.desc = (CacheDesc*)workspace;
+    a.part = (float*)(a.desc + p.grid);
+    const bool sm = a.act == kSoftmax;
+    // the tensor-core kernel's scores are in powers of two
+    a.alpha = p.tc && sm ? attn->alpha * kLog2e : attn->alpha;
+    cudaStream_t st = (cudaStream_t)stream;
+    s = p.tc ? launch_cache_tc(a, p.grid, st) : launch_cache_simt(a, dtype, p.grid, st);
+    if (s != GDPA_OK) return s;
+    if (dtype == GDPA_BF16)
+        return sm ? launch_join<__nv_bfloat16, true>(a, p.grid, p.sms, st) : launch_join<__nv_bfloat16, false>(a, p.grid, p.sms, st);
+    return sm ? launch_join<float, true>(a, p.grid, p.sms, st) : launch_join<float, false>(a, p.grid, p.sms, st);
+}
+
+}  // extern "C"

@@ -28,6 +28,8 @@ SCHED = {"zigzag": 0, "round_robin": 1, "zigzag_timed": 2}
 KERNEL = {"auto": 0, "tcgen05": 1, "simt": 2}
 ROPE_LAYOUT = {"half": 0, "interleaved": 1}
 ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
+STORE = {"bf16": 0, "f32": 1, "e4m3": 2}
+CACHE_MASK = {"causal": 0, "history": 1, "tree": 2}
 # lists of a shared-prefix plan: (index, columns)
 PREFIX_LIST = {"units": (0, 8), "unit_seg": (1, 1), "joins": (2, 8), "smalls": (3, 8), "eights": (4, 8),
                "blocks": (5, 2), "tiles": (6, 8), "own": (7, 4), "counts": (8, 4)}
@@ -45,6 +47,12 @@ _lib = None
 class _RopeSpec(ctypes.Structure):
     _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("scale", ctypes.c_float),
                 ("reserved", ctypes.c_int32), ("turns", ctypes.c_uint64 * 64)]
+
+
+class _CacheSpec(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("error", ctypes.c_void_p)] + [
+                    (n, ctypes.c_int32) for n in ("pages", "page", "heads", "d", "store")]
 
 
 class GdpaError(RuntimeError):
@@ -113,6 +121,13 @@ def lib():
             "gdpa_prefix_bwd": [vp, st] + [vp] * 13 + [ctypes.c_float, st, vp],
             "gdpa_prefix_check": [vp, vp],
             "gdpa_prefix_error_detail": [vp, i32p],
+            "gdpa_cache_bytes": [ctypes.POINTER(_CacheSpec), i64p, i64p],
+            "gdpa_cache_write": [ctypes.POINTER(_CacheSpec), st, ctypes.c_int64, vp, vp, vp, vp],
+            "gdpa_cache_read": [ctypes.POINTER(_CacheSpec), st, ctypes.c_int64, vp, vp, vp, vp],
+            "gdpa_cache_workspace": [ctypes.POINTER(_CacheSpec), st, ctypes.c_int64, st, st, i64p],
+            "gdpa_cache_fwd": [ctypes.POINTER(_CacheSpec), st, ctypes.c_int64, st, vp, vp, vp, vp, vp, vp,
+                               ctypes.c_int64, vp],
+            "gdpa_cache_check": [ctypes.POINTER(_CacheSpec), i32p, vp],
         }
         for name, args in sig.items():
             f = getattr(L, name)
@@ -134,13 +149,13 @@ def lib():
 
 # What the calls need of torch, looked up once by lib(): these entry points are
 # also used for a handful of rows, where marshalling is most of the time.
-_DTYPE_ID = _POSITION_BITS = _empty = _raw_stream = _current_device = _on_device = _f32 = None
+_DTYPE_ID = _POSITION_BITS = _empty = _raw_stream = _current_device = _on_device = _f32 = _u8 = None
 
 
 def _torch_names():
-    global _DTYPE_ID, _POSITION_BITS, _empty, _raw_stream, _current_device, _on_device, _f32
+    global _DTYPE_ID, _POSITION_BITS, _empty, _raw_stream, _current_device, _on_device, _f32, _u8
     import torch
-    _f32 = torch.float32
+    _f32, _u8 = torch.float32, torch.uint8
     _DTYPE_ID = {torch.bfloat16: 0, torch.float32: 1}
     _POSITION_BITS = {torch.int32: 32, torch.int64: 64}
     _empty = torch.empty
@@ -959,3 +974,213 @@ def gdpa_prefix_softmax_bwd(plan: PrefixPlan, q, kp, vp, k, v, o, do, lse, dq=No
     """(dQ, dKp, dVp, dK, dV) of the softmax variant from its forward's O and lse."""
     return _prefix_bwd(plan, q, kp, vp, k, v, o, do, lse, (dq, dkp, dvp, dk, dv), alpha, "softmax",
                        stream)
+
+
+class KVCache:
+    """Keys and values of events, in pages, for serving.
+
+    pages: how many pages of ``page`` events (a power of two, 16 to 1024) it
+    has, each for all ``heads`` key heads of ``d`` columns.  store: "bf16" or
+    "f32" (rows as they are) or "e4m3" (8-bit codes with one power of two a row
+    and head).  Which pages hold whose events is the caller's, in page tables:
+    event e of sample b lies on page table[b, e // page].
+
+    Device memory and sizes only: calls on any stream or thread may use it, and
+    the caller orders those that write events before those that read them.
+    """
+
+    def __init__(self, pages: int, heads: int, d: int, page: int = 64, store: str = "bf16", device=None):
+        import torch
+        self.pages, self.heads, self.d, self.page, self.store = int(pages), int(heads), int(d), int(page), store
+        self.spec = _CacheSpec(pages=self.pages, heads=self.heads, d=self.d, page=self.page, store=STORE[store])
+        self._ref = ctypes.byref(self.spec)
+        rows, scales = ctypes.c_int64(), ctypes.c_int64()
+        _ok(lib().gdpa_cache_bytes(self._ref, ctypes.byref(rows), ctypes.byref(scales)), "gdpa_cache_bytes")
+        self.device = torch.device("cuda" if device is None else device)
+        if self.device.type != "cuda":
+            raise ValueError("a KVCache is in CUDA memory")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.kinds = {"bf16": (torch.bfloat16,), "f32": (torch.float32,),
+                      "e4m3": (torch.bfloat16, torch.float32)}[store]
+        # (256 bytes at least: an empty tensor has no address)
+        new = lambda n: torch.zeros(max(n, 256), dtype=torch.uint8, device=self.device)  # noqa: E731
+        self.k, self.v = new(rows.value), new(rows.value)
+        self.k_scale, self.v_scale = new(scales.value), new(scales.value)
+        self.error = torch.zeros(4, dtype=torch.int32, device=self.device)
+        for n in ("k", "v", "k_scale", "v_scale", "error"):
+            setattr(self.spec, n, getattr(self, n).data_ptr())
+
+    @property
+    def nbytes(self) -> int:
+        return sum(t.numel() for t in (self.k, self.v, self.k_scale, self.v_scale))
+
+    def check(self, stream=None):
+        """Wait for ``stream``; raise if a call since the last check met a page
+        or an event outside the cache."""
+        d = (ctypes.c_int32 * 4)()
+        with _on_device(self.device.index):
+            status = lib().gdpa_cache_check(self._ref, d, _stream_ptr(stream))
+        if status != 0:
+            what = {1: "page", 2: "event behind its table", 3: "negative start"}.get(d[1], "wait")
+            raise GdpaError(status, "gdpa_cache_check (code %d, %s, sample %d, %d)" % (d[0], what, d[2], d[3]))
+
+
+_cache_rows = struct.Struct("=Qqq").pack        # gdpa_cache_rows
+_cache_where = struct.Struct("=QQQqii").pack    # gdpa_cache_where
+_cache_attn = struct.Struct("=iiiifxxxxQ").pack   # gdpa_cache_attn
+
+
+def _cache_at(cache, table, offsets, starts):
+    dev = cache.device
+    if (_POSITION_BITS.get(table.dtype) != 32 or table.dim() != 2 or table.device != dev
+            or (table.shape[1] > 1 and table.stride(1) != 1)):
+        raise ValueError("table must be an int32 [B, pages] tensor with contiguous rows on the cache's device")
+    for t, what in ((offsets, "offsets"), (starts, "starts")):
+        if t is not None and (_POSITION_BITS.get(t.dtype) != 32 or t.dim() != 1
+                              or not t.is_contiguous() or t.device != dev):
+            raise ValueError("%s must be a contiguous int32 tensor on the cache's device" % what)
+    B, width = table.shape
+    if offsets is None or offsets.shape[0] != B + 1 or (starts is not None and starts.shape[0] != B):
+        raise ValueError("offsets must have B + 1 entries and starts B")
+    return B, _cache_where(table.data_ptr(), offsets.data_ptr(), starts.data_ptr() if starts is not None else 0,
+                           table.stride(0), width, B)
+
+
+def _cache_kind(cache, dtype):
+    if dtype not in cache.kinds:
+        raise TypeError("a %s cache takes rows of %s, got %s" % (cache.store, " or ".join(map(str, cache.kinds)), dtype))
+    return _DTYPE_ID[dtype]
+
+
+def _cache_tensor(t, T, heads, d, dtype, dev, name, out=False):
+    if t.dim() != 3 or t.shape != (T, heads, d) or t.device != dev:
+        raise ValueError("%s must be a [%d, %d, %d] tensor on %s, got %s on %s"
+                         % (name, T, heads, d, dev, tuple(t.shape), t.device))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s" % (name, dtype))
+    s = t.stride()
+    if d > 1 and s[2] != 1:
+        raise ValueError("%s: the columns of a row must be contiguous" % name)
+    if out and ((T > 1 and s[0] == 0) or (heads > 1 and s[1] == 0)):
+        raise ValueError("%s must not be an expanded tensor" % name)
+    return _cache_rows(t.data_ptr(), s[0], s[1])
+
+
+def _cache_call(f, what, cache, args, stream):
+    index = cache.device.index
+    args += (_raw_stream(index) if stream is None else stream.cuda_stream,)
+    if index == _current_device():
+        _ok(f(cache._ref, *args), what)
+    else:
+        with _on_device(index):
+            _ok(f(cache._ref, *args), what)
+
+
+def gdpa_cache_write(cache: KVCache, k, v, table, offsets, starts=None, stream=None):
+    """Write new rows' keys and values to their pages, in one launch.
+
+    k, v: [T, heads, d] CUDA tensors (of any token and head strides: parts of a
+    packed projection) of the cache's type; bf16 or float32 for "e4m3".  offsets
+    (int32 [B + 1]), starts (int32 [B], None: zeros), table (int32 [B, pages]),
+    on the GPU: row t of sample b is its event starts[b] + t - offsets[b], and
+    rows behind the last offset are not written."""
+    T = k.shape[0]
+    kind = _cache_kind(cache, k.dtype)
+    args = (kind, T, _cache_tensor(k, T, cache.heads, cache.d, k.dtype, cache.device, "k"),
+            _cache_tensor(v, T, cache.heads, cache.d, k.dtype, cache.device, "v"))
+    B, where = _cache_at(cache, table, offsets, starts)
+    if T and B:
+        _cache_call(lib().gdpa_cache_write, "gdpa_cache_write", cache, args + (where,), stream)
+
+
+def gdpa_cache_read(cache: KVCache, rows: int, table, offsets, starts=None, dtype=None, k_out=None,
+                    v_out=None, stream=None):
+    """(K, V) of ``rows`` events as [rows, heads, d] tensors: the values that the
+    cache holds, row t of sample b being its event starts[b] + t - offsets[b]
+    (arguments as gdpa_cache_write's).  dtype: "e4m3" caches give bf16 (default)
+    or float32.  Rows behind the last offset are not written; events outside the
+    cache read as zeros."""
+    dtype = cache.kinds[0] if dtype is None else dtype
+    kind = _cache_kind(cache, dtype)
+    rows = int(rows)
+    out = []
+    args = (kind, rows)
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is None:
+            t = _new((rows, cache.heads, cache.d), dtype, cache.device, stream)
+        out.append(t)
+        args += (_cache_tensor(t, rows, cache.heads, cache.d, dtype, cache.device, name, out=True),)
+    B, where = _cache_at(cache, table, offsets, starts)
+    if rows and B:
+        _cache_call(lib().gdpa_cache_read, "gdpa_cache_read", cache, args + (where,), stream)
+    return tuple(out)
+
+
+def _cache_attend(cache, q, table, offsets, starts, mask, window, sinks, parents, o, lse, alpha, act, stream):
+    if q.dim() != 3:
+        raise ValueError("q must be a [T, heads, d] tensor")
+    T, H = q.shape[0], q.shape[1]
+    dt, dev = q.dtype, cache.device
+    kind = _cache_kind(cache, dt)
+    rows = _cache_tensor(q, T, H, cache.d, dt, dev, "q")
+    B, where = _cache_at(cache, table, offsets, starts)
+    if mask == "tree":
+        if (parents is None or _POSITION_BITS.get(parents.dtype) != 32 or parents.shape != (T,)
+                or not parents.is_contiguous() or parents.device != dev):
+            raise ValueError("a tree needs parents, a contiguous int32 [T] tensor on the cache's device")
+    elif parents is not None:
+        raise ValueError("parents belong to mask=\"tree\"")
+    if o is None:
+        o = _new((T, H, cache.d), dt, dev, stream)
+    elif o.shape != q.shape or o.dtype != dt or o.device != dev or not o.is_contiguous():
+        raise ValueError("o must be a contiguous tensor of q's shape, dtype and device")
+    if lse is not None and (lse.dtype != _f32 or lse.shape != (T, H) or not lse.is_contiguous() or lse.device != dev):
+        raise ValueError("lse must be a contiguous float32 [T, heads] tensor on the cache's device")
+    attn = _cache_attn(CACHE_MASK[mask], window, sinks, ACT[act], cache.d ** -0.5 if alpha is None else alpha,
+                       parents.data_ptr() if parents is not None else 0)
+    L = lib()
+    size = ctypes.c_int64()
+    _ok_on(cache, L.gdpa_cache_workspace, "gdpa_cache_workspace", (kind, T, H, B, ctypes.byref(size)))
+    work = _new((size.value,), _u8, dev, stream)
+    _cache_call(L.gdpa_cache_fwd, "gdpa_cache_fwd", cache,
+                (kind, T, H, rows, o.data_ptr(), lse.data_ptr() if lse is not None else None, where, attn,
+                 work.data_ptr(), size.value), stream)
+    return o
+
+
+def _ok_on(cache, f, what, args):
+    """A call that asks the cache's device, not a stream of it."""
+    if cache.device.index == _current_device():
+        _ok(f(cache._ref, *args), what)
+    else:
+        with _on_device(cache.device.index):
+            _ok(f(cache._ref, *args), what)
+
+
+def gdpa_cache_fwd(cache: KVCache, q, table, offsets, starts=None, mask: str = "causal", window: int = 0,
+                   sinks: int = 0, parents=None, o=None, alpha=None, act: str = "gelu_erf", stream=None):
+    """O ([T, H, d], dtype of q) of new rows over the cached events of their samples.
+
+    q: [T, H, d] with any token and head strides, H a multiple of the cache's
+    heads.  table, offsets, starts as gdpa_cache_write's.  mask: which events row
+    i of sample b sees: "causal" its history and the new rows up to itself,
+    written before (position p = starts[b] + i); "history" the starts[b] events
+    before (p = starts[b]); "tree" the history, its ancestors among the new rows
+    and itself: parents int32 [T], the parent's index in its sample, below its
+    own (anything else: none); p = starts[b] + number of ancestors.  window > 0:
+    only events at positions above p - window, and below ``sinks``."""
+    if act == "softmax":
+        raise ValueError("the softmax variant is gdpa_cache_softmax_fwd")
+    return _cache_attend(cache, q, table, offsets, starts, mask, window, sinks, parents, o, None, alpha, act, stream)
+
+
+def gdpa_cache_softmax_fwd(cache: KVCache, q, table, offsets, starts=None, mask: str = "causal",
+                           window: int = 0, sinks: int = 0, parents=None, o=None, lse=None, alpha=None,
+                           stream=None):
+    """The softmax variant of gdpa_cache_fwd: (O, lse [T, H] float32); a row that
+    sees no event gives 0 and -inf."""
+    if lse is None:
+        lse = _new(tuple(q.shape[:2]), _f32, cache.device, stream)
+    o = _cache_attend(cache, q, table, offsets, starts, mask, window, sinks, parents, o, lse, alpha, "softmax", stream)
+    return o, lse

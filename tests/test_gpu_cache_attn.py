@@ -1,0 +1,353 @@
+"""Attention over the history cache on the GPU against the float64 oracle.
+Bounds: cache_util.check_o."""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import recommender_model_attention_gb300 as gd  # noqa: E402
+from cache_util import Batch, check_lse, check_o, dev, offsets, orc, ref  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+KINDS = [("bf16", "bf16", 128), ("bf16", "bf16", 64), ("e4m3", "bf16", 128), ("e4m3", "bf16", 64),
+         ("f32", "f32", 32), ("e4m3", "f32", 64), ("bf16", "bf16", 40), ("e4m3", "bf16", 48), ("f32", "f32", 128)]
+SHAPES = {
+    "one event": ([1], [0]),
+    "one row": ([1], [100]),
+    "single rows": ([1] * 9, [0, 1, 15, 16, 17, 63, 64, 65, 200]),
+    "ragged": ([3, 0, 1, 20, 2, 9], [0, 5, 300, 33, 1, 0]),
+    "group edges": ([16, 15, 17, 1], [16, 17, 15, 47]),
+    "many rows": ([70, 130], [40, 3]),
+}
+
+
+def setup_module(_):
+    gd.build()
+
+
+def tree(new, seed=0):
+    """Parents of drafted rows: chains, wide trees and several roots."""
+    rng = np.random.Generator(np.random.PCG64(seed))
+    return [int(rng.integers(max(-1, i - 6), i)) for n in new for i in range(n)]
+
+
+@pytest.mark.parametrize("store,dtype,d", KINDS)
+@pytest.mark.parametrize("act", ["softmax", "silu"])
+@pytest.mark.parametrize("shape", list(SHAPES))
+def test_shapes(shape, act, store, dtype, d):
+    b = Batch(*SHAPES[shape], H=4, Hkv=2, d=d, store=store, dtype=dtype).fill()
+    b.check(act)
+
+
+@pytest.mark.parametrize("store,dtype,d", KINDS[:6])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (7, 0), (20, 1), (20, 5), (33, 40), (1, 16), (1000, 4),
+                                          (2 ** 31 - 1, 2 ** 31 - 1)])
+@pytest.mark.parametrize("mask", ["causal", "history", "tree"])
+def test_windows_and_sinks(store, dtype, d, window, sinks, mask):
+    new = [1, 30, 5, 0, 18]
+    b = Batch(new, [150, 70, 0, 40, 19], d=d, store=store, dtype=dtype,
+              parents=tree(new) if mask == "tree" else None).fill()
+    b.check("softmax", mask=mask, window=window, sinks=sinks)
+    b.check("gelu_tanh", mask=mask, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("store,dtype,d", KINDS[:6])
+@pytest.mark.parametrize("act", ["softmax", "gelu_erf"])
+def test_trees(store, dtype, d, act):
+    new = [24, 1, 64, 0, 7, 100]
+    for seed, hist in enumerate(([130, 0, 17, 9, 0, 40], [0] * 6)):
+        b = Batch(new, hist, H=4, Hkv=1, d=d, store=store, dtype=dtype, parents=tree(new, seed)).fill()
+        b.check(act, mask="tree")
+
+
+def test_special_trees():
+    n = 40
+    chain = [i - 1 for i in range(n)]
+    b = Batch([n], [37], parents=chain).fill()
+    o, lse = b.check(mask="tree")
+    c, clse = b.run(mask="tree"), None
+    b.parents, b.parents_host = None, None
+    o2, lse2 = b.run(mask="causal")     # a chain is the causal mask
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    Batch([n], [37], parents=[-1] * n).fill().check(mask="tree")              # no two rows see each other
+    Batch([n], [37], parents=[-1] + [0] * (n - 1)).fill().check(mask="tree")  # a star
+    # what is no row before the own one is no parent
+    odd = [0, 5, 1, 3, -7, 2 ** 31 - 1, 2, -2 ** 31]
+    Batch([8], [3], parents=odd).fill().check(mask="tree")
+
+
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (8, 8), (8, 1), (6, 2), (40, 1), (128, 1), (24, 8)])
+@pytest.mark.parametrize("store,dtype,d", [("bf16", "bf16", 128), ("e4m3", "bf16", 64), ("f32", "f32", 16)])
+def test_shared_key_heads(H, Hkv, store, dtype, d):
+    b = Batch([1, 3, 0, 2], [40, 7, 3, 130], H=H, Hkv=Hkv, d=d, store=store, dtype=dtype).fill()
+    b.check()
+    b.check("gelu_tanh")
+
+
+@pytest.mark.parametrize("act", ["softmax", "gelu_erf", "gelu_tanh", "silu", "gelu_taylor6", "identity"])
+@pytest.mark.parametrize("store,dtype,d", [("bf16", "bf16", 128), ("e4m3", "bf16", 128), ("e4m3", "f32", 48)])
+def test_activations(act, store, dtype, d):
+    b = Batch([5, 1, 9], [100, 30, 0], d=d, store=store, dtype=dtype, gain=0.5).fill()   # the polynomial's range
+    b.check(act)
+    b.check(act, alpha=0.0)
+    b.check(act, alpha=-0.05)
+
+
+@pytest.mark.parametrize("page", [16, 32, 128, 1024])
+@pytest.mark.parametrize("store", ["bf16", "e4m3"])
+def test_pages(page, store):
+    Batch([3, 1, 20], [100, 1500, 15], page=page, store=store, extra_width=2).fill().check()
+
+
+@pytest.mark.parametrize("store,dtype,d", [("bf16", "bf16", 128), ("e4m3", "bf16", 128), ("f32", "f32", 32)])
+def test_long_histories_are_split(store, dtype, d):
+    """One user's events over all CTAs, beside short ones; rows of several tiles."""
+    b = Batch([1, 2, 1], [30000, 11, 4000], H=2, Hkv=1, d=d, store=store, dtype=dtype, page=64).fill()
+    b.check()
+    b.check("silu", alpha=0.01)
+    b = Batch([40, 1], [9000, 100], H=2, Hkv=1, d=d, store=store, dtype=dtype, page=64).fill()
+    b.check()
+
+
+def test_many_samples():
+    n = 1500
+    new = [(i * 5) % 3 for i in range(n)]
+    Batch(new, [(i * 11) % 40 for i in range(n)], H=1, Hkv=1, d=64).fill().check()
+    # few samples with rows between many without
+    new = [0] * n
+    new[3], new[700], new[1499] = 2, 1, 3
+    Batch(new, [20] * n, H=1, Hkv=1, d=64, store="e4m3").fill().check()
+
+
+@pytest.mark.parametrize("store,dtype,d", KINDS[:6])
+def test_rows_that_see_nothing(store, dtype, d):
+    b = Batch([2, 1, 3], [0, 50, 0], d=d, store=store, dtype=dtype).fill()
+    o, lse = b.check(mask="history")
+    assert (o[:2] == 0).all() and (o[3:] == 0).all() and torch.isinf(lse[:2]).all()
+    assert (b.check("silu", mask="history")[0][:2] == 0).all()
+
+
+@pytest.mark.parametrize("store,dtype,d", KINDS[:6])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("act", ["softmax", "silu"])
+def test_hidden_events_may_hold_anything(store, dtype, d, bad, act):
+    """Rows hidden by the window, by the causal order or by the tree hold NaN or
+    infinities: rows that do not see them are as without them."""
+    new, hist = [20, 3], [40, 33]
+    parents = tree(new, 3)
+    for mask in ("causal", "tree", "history"):
+        b = Batch(new, hist, d=d, store=store, dtype=dtype, parents=parents if mask == "tree" else None)
+        clean, clean_lse = b.fill().run(act, mask=mask, window=9, sinks=2)
+        kw = dict(mask=mask, window=9, sinks=2)
+        see = [orc.sees(n, h, mask, 9, 2, parents[:20] if i == 0 else parents[20:]) for i, (n, h) in enumerate(zip(new, hist))]
+        victim = 43 if mask != "history" else 36      # a new row of sample 0; an event that its window hides later
+        for x in (b.k_all, b.v_all):
+            x[victim] = bad
+            x[60 + 5] = bad                           # an event of sample 1 that nobody sees
+        o, lse = b.fill().run(act, **kw)
+        assert not see[1][:, 5].any()
+        hit = np.concatenate([see[0][:, victim], np.zeros(3, dtype=bool)])
+        assert hit.any() and not hit.all() or mask == "history"
+        ok = torch.from_numpy(~hit).cuda()
+        assert torch.equal(o[ok], clean[ok])
+        assert torch.isnan(o[~ok]).all() or act != "softmax"
+        if lse is not None:
+            assert torch.equal(lse[ok], clean_lse[ok])
+
+
+@pytest.mark.parametrize("act", ["softmax", "silu"])
+def test_value_rows_of_very_different_sizes(act):
+    """8-bit rows whose powers of two span 2^-40 .. 2^40: to each output's own
+    terms, wherever in the history the large ones lie."""
+    for seed, order in enumerate((1, -1, 0)):
+        b = Batch([1, 2], [600, 333], store="e4m3", seed=seed, gain=2.0)
+        n = b.v_all.shape[0]
+        e = np.linspace(-40, 40, n).round()[::order or 1]
+        if order == 0:
+            e = np.random.Generator(np.random.PCG64(5)).permutation(e)
+        b.v_all = b.v_all * torch.from_numpy(np.ldexp(1.0, e.astype(int))).to(torch.bfloat16)[:, None, None]
+        b.fill().check(act)
+
+
+@pytest.mark.parametrize("store,dtype,d", KINDS[:5])
+def test_large_scores(store, dtype, d):
+    """Scores of hundreds that rise along the history: the reference moves at
+    most groups, and at the end one event has nearly all the weight."""
+    b = Batch([2, 1], [700, 90], d=d, store=store, dtype=dtype)
+    n = b.k_all.shape[0]
+    b.k_all = (b.k_all.float() * torch.linspace(0.1, 30, n)[:, None, None]).to(b.k_all.dtype)
+    o, lse = b.fill().run()
+    want, wlse, size = b.want(d ** -0.5, "softmax")
+    err = np.abs(ref.to_f64(o) - want)
+    # a score of up to X = 30 * 1.5 * sqrt(d) is summed in float32 from d terms of
+    # together at most X: off by d 2^-24 X at most, 128 * 2^-24 * 510 = 3.9e-3, which
+    # a weight is off by relatively
+    assert np.all(err <= 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 2 * 3.9e-3) * size[0] + 1e-30)
+    assert np.max(np.abs(ref.to_f64(lse) - wlse)) <= 2 * 3.9e-3
+
+
+def test_strided_queries():
+    b = Batch([5, 3], [50, 20], H=4, Hkv=2, d=64).fill()
+    want, lse = b.run()
+    for shift in (0, 1, 8):
+        w = torch.zeros(8, 9 * 64 + shift, dtype=torch.bfloat16, device="cuda")
+        q = torch.as_strided(w, (8, 4, 64), (w.stride(0), 128, 1), shift)
+        q.copy_(b.q)
+        o, l2 = gd.gdpa_cache_softmax_fwd(b.cache, q, b.table, b.off, b.starts)
+        assert torch.equal(o, want) and torch.equal(l2, lse)
+
+
+def test_rows_behind_the_last_sample_stay():
+    b = Batch([5, 3], [50, 20]).fill()
+    q = torch.cat([b.q, b.q])
+    o = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    gd.gdpa_cache_softmax_fwd(b.cache, q, b.table, b.off, b.starts, o=o, lse=lse)
+    w, wl = b.run()
+    assert torch.equal(o[:8], w) and torch.equal(lse[:8], wl) and (o[8:] == 7).all() and (lse[8:] == 7).all()
+
+
+def test_same_bits_every_time():
+    b = Batch([1, 2, 7], [20000, 33, 500], H=8, Hkv=2, store="e4m3", page=64).fill()
+    first = b.run()
+    for _ in range(5):
+        again = b.run()
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("store,dtype", [("bf16", "bf16"), ("e4m3", "bf16"), ("f32", "f32")])
+def test_pages_outside_the_cache_are_not_read(store, dtype):
+    b = Batch([1, 2], [100, 60], d=64, store=store, dtype=dtype).fill()
+    good, _ = b.run()
+    b.table_host[1, 1] = 1 << 20     # events 16 .. 31 of sample 1
+    b.table = dev(b.table_host)
+    o, _ = b.run()
+    with pytest.raises(gd.GdpaError):
+        b.cache.check()
+    assert torch.equal(o[:1], good[:1])
+    # as if these events were hidden
+    keep = np.array([j for j in range(62) if not 16 <= j < 32])
+    x = [orc.held(ref.to_f64(t), store) for t in (b.k_all, b.v_all)]
+    k, v = ([t[101:][keep]] for t in x)
+    for i in range(2):
+        see = keep <= 60 + i
+        want, _, size = orc.attend([0, 1], [see.sum() - 1], ref.to_f64(b.q[1 + i:2 + i]), [k[0][see]], [v[0][see]],
+                                   64 ** -0.5, "softmax")
+        check_o(o[1 + i:2 + i], want, size, "softmax", b)
+
+
+def test_events_and_starts_outside_the_table():
+    b = Batch([2, 1], [30, 60]).fill()
+    good, _ = b.run()
+    st = dev([-5, 60])
+    o, lse = gd.gdpa_cache_softmax_fwd(b.cache, b.q, b.table, b.off, st)
+    with pytest.raises(gd.GdpaError):
+        b.cache.check()
+    assert (o[:2] == 0).all() and torch.isinf(lse[:2]).all() and torch.equal(o[2:], good[2:])
+    # a table too short for the events
+    gd.gdpa_cache_softmax_fwd(b.cache, b.q, b.table[:, :3], b.off, b.starts)
+    with pytest.raises(gd.GdpaError):
+        b.cache.check()
+    b.run()
+    b.cache.check()
+
+
+def test_a_run_of_them_as_a_server_makes_it():
+    """Rotary positions, new rows written, scored, drafted continuations scored
+    as a tree, all from one captured graph over growing histories."""
+    H, Hkv, d, B, P = 4, 2, 64, 3, 16
+    rope = gd.Rope(d)
+    cache = gd.KVCache(40, Hkv, d, page=P, store="e4m3")
+    table = dev(np.random.Generator(np.random.PCG64(1)).permutation(39).reshape(3, 13))
+    off = dev(np.arange(B + 1))
+    starts = dev([0, 5, 31])
+    g = torch.Generator(device="cuda").manual_seed(3)
+    hist_k = torch.randn((36, Hkv, d), generator=g, device="cuda").bfloat16()
+    hist_v = torch.randn((36, Hkv, d), generator=g, device="cuda").bfloat16()
+    hoff = dev([0, 0, 5, 36])
+    gd.gdpa_cache_write(cache, gd.gdpa_rope_fwd(rope, hist_k, offsets=hoff), hist_v, table, hoff)
+    x = [torch.zeros((B, h, d), dtype=torch.bfloat16, device="cuda") for h in (H, Hkv, Hkv)]
+
+    def step():
+        q, k = gd.gdpa_rope_fwd(rope, x[0], x[1], offsets=off, starts=starts)
+        gd.gdpa_cache_write(cache, k, x[2], table, off, starts)
+        return gd.gdpa_cache_softmax_fwd(cache, q, table, off, starts)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = step()
+    ks, vs = [hist_k[:0], hist_k[:5], hist_k[5:]], [hist_v[:0], hist_v[:5], hist_v[5:]]
+    for _ in range(20):
+        for t in x:
+            t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        ks = [torch.cat([a, x[1][i:i + 1]]) for i, a in enumerate(ks)]
+        vs = [torch.cat([a, x[2][i:i + 1]]) for i, a in enumerate(vs)]
+        n = [len(a) for a in ks]
+        turned = gd.gdpa_rope_fwd(rope, torch.cat(ks), offsets=dev(offsets(n)))
+        q = gd.gdpa_rope_fwd(rope, x[0], offsets=off, starts=starts)
+        k64 = np.split(orc.held(ref.to_f64(turned), "e4m3"), np.cumsum(n)[:-1])
+        v64 = np.split(orc.held(ref.to_f64(torch.cat(vs)), "e4m3"), np.cumsum(n)[:-1])
+        want, wlse, size = orc.attend(np.arange(B + 1), [m - 1 for m in n], ref.to_f64(q), k64, v64, d ** -0.5, "softmax")
+
+        class Of:
+            dt, store = torch.bfloat16, "e4m3"
+        Of.d = d
+        check_o(o, want, size, "softmax", Of)
+        check_lse(lse, wlse)
+        starts += 1
+    cache.check()
+
+
+def test_streams():
+    """Calls on several streams at once, each with its own rows, one cache."""
+    b = Batch([1, 4], [3000, 200], H=8, Hkv=2, store="e4m3", page=64).fill()
+    want, lse = b.run()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    out = []
+    for _ in range(6):
+        for s in streams:
+            out.append(gd.gdpa_cache_softmax_fwd(b.cache, b.q, b.table, b.off, b.starts, stream=s))
+    torch.cuda.synchronize()
+    for o, l2 in out:
+        assert torch.equal(o, want) and torch.equal(l2, lse)
+
+
+def test_refusals():
+    b = Batch([2], [5], H=4, Hkv=2, d=64).fill()
+    a = (b.cache, b.q, b.table, b.off, b.starts)
+    f = gd.gdpa_cache_softmax_fwd
+    with pytest.raises(ValueError):
+        gd.gdpa_cache_fwd(*a, act="softmax")
+    with pytest.raises(KeyError):
+        f(*a, mask="none")
+    with pytest.raises(ValueError):
+        f(*a, mask="tree")
+    with pytest.raises(ValueError):
+        f(*a, parents=dev([0, 0]))
+    with pytest.raises(ValueError):
+        f(*a, mask="tree", parents=dev([0, 0, 0]))
+    for kw in (dict(sinks=2), dict(window=-1), dict(window=3, sinks=-1), dict(alpha=float("nan")), dict(alpha=float("inf"))):
+        with pytest.raises(gd.GdpaError) as e:
+            f(*a, **kw)
+        assert e.value.status == 1
+    with pytest.raises(gd.GdpaError):
+        f(b.cache, b.q[:, :3], *a[2:])           # 3 heads on 2 key heads
+    for bad in (b.q.float(), b.q.half()):
+        with pytest.raises(TypeError):
+            f(b.cache, bad, *a[2:])
+    for bad in (b.q[:, :, :32], b.q[0], b.q.cpu()):
+        with pytest.raises(ValueError):
+            f(b.cache, bad, *a[2:])
+    with pytest.raises(ValueError):
+        f(*a, o=torch.empty_like(b.q).transpose(0, 1))
+    with pytest.raises(ValueError):
+        f(*a, lse=torch.empty(2, 4, dtype=torch.bfloat16, device="cuda"))
