@@ -343,8 +343,10 @@ __device__ __forceinline__ void finish_segment(const AttnArgs& a, const Segment&
     }
 }
 
-gdpa_status launch_cache_tc(const AttnArgs& a, int grid, cudaStream_t st);
+gdpa_status launch_cache_mma(const AttnArgs& a, int grid, cudaStream_t st);
+gdpa_status launch_cache_tc_bf16(const AttnArgs& a, int grid, cudaStream_t st);
+gdpa_status launch_cache_tc_e4m3(const AttnArgs& a, int grid, cudaStream_t st);
 gdpa_status launch_cache_simt(const AttnArgs& a, gdpa_dtype dt, int grid, cudaStream_t st);
-constexpr int kCacheTcPerSm = 2, kCacheSimtPerSm = 2;
+constexpr int kCacheMmaPerSm = 2, kCacheSimtPerSm = 2;
 
 }  // namespace gdpa

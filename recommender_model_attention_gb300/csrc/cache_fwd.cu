@@ -135,22 +135,32 @@ int device_sms() {
     return n;
 }
 
+enum Kind { kSimt, kMma, kTc };
 struct Shape {
-    bool tc;
-    int RT, TM, grid, sms;
+    Kind kind;
+    int RT, TM, grid, sms, min_share;
     int64_t bytes;
 };
 
 // The kernel, its tile and its workspace: rules on types and sizes alone.
 gdpa_status shape(const CacheView& c, gdpa_dtype dt, int64_t T, int H, int B, Shape& s) {
-    s.tc = dt == GDPA_BF16 && (c.d == 64 || c.d == 128);
-    // row tiles of 16 that a CTA holds: as many as an average sample fills
-    const int64_t rows = B > 0 ? T * (H / c.heads) / B : 0;
-    s.RT = !s.tc || rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-    s.TM = 16 * s.RT;
+    const int64_t rows = B > 0 ? T * (H / c.heads) / B : 0;   // of an average sample and key head
+    const bool tc = dt == GDPA_BF16 && (c.d == 64 || c.d == 128);
+    s.kind = !tc ? kSimt : rows <= 64 ? kMma : kTc;
     s.sms = device_sms();
     if (s.sms == 0) return GDPA_ERR_CUDA;
-    s.grid = s.sms * (s.tc ? kCacheTcPerSm : kCacheSimtPerSm);
+    if (s.kind == kTc) {
+        s.RT = 0;
+        s.TM = rows <= 128 ? 128 : 256;
+        s.grid = s.sms;
+        s.min_share = 16;
+    } else {
+        // row tiles of 16 that a CTA holds: as many as an average sample fills
+        s.RT = s.kind == kSimt || rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+        s.TM = 16 * s.RT;
+        s.grid = s.sms * (s.kind == kMma ? kCacheMmaPerSm : kCacheSimtPerSm);
+        s.min_share = 4 / s.RT;
+    }
     if (s.grid > kMaxGrid) s.grid = kMaxGrid;
     s.bytes = (int64_t)s.grid * (sizeof(CacheDesc) + 2ll * s.TM * (c.d + 2) * 4);
     return GDPA_OK;
@@ -219,14 +229,16 @@ gdpa_status gdpa_cache_fwd(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T,
     a.act = attn->act;
     a.TM = p.TM;
     a.RT = p.RT;
-    a.min_share = 4 / p.RT;
+    a.min_share = p.min_share;
     a.desc = (CacheDesc*)workspace;
     a.part = (float*)(a.desc + p.grid);
     const bool sm = a.act == kSoftmax;
-    // the tensor-core kernel's scores are in powers of two
-    a.alpha = p.tc && sm ? attn->alpha * kLog2e : attn->alpha;
+    // the warp-level kernel's scores are in powers of two
+    a.alpha = p.kind == kMma && sm ? attn->alpha * kLog2e : attn->alpha;
     cudaStream_t st = (cudaStream_t)stream;
-    s = p.tc ? launch_cache_tc(a, p.grid, st) : launch_cache_simt(a, dtype, p.grid, st);
+    s = p.kind == kSimt ? launch_cache_simt(a, dtype, p.grid, st)
+        : p.kind == kMma ? launch_cache_mma(a, p.grid, st)
+        : a.c.store == GDPA_STORE_E4M3 ? launch_cache_tc_e4m3(a, p.grid, st) : launch_cache_tc_bf16(a, p.grid, st);
     if (s != GDPA_OK) return s;
     if (dtype == GDPA_BF16)
         return sm ? launch_join<__nv_bfloat16, true>(a, p.grid, p.sms, st) : launch_join<__nv_bfloat16, false>(a, p.grid, p.sms, st);

@@ -78,7 +78,7 @@ __device__ __forceinline__ int64_t cache_block(const CacheView& c, const CacheWh
     return (int64_t)p * c.heads + head;
 }
 
-// 2^(byte - 127) of a scale byte (1 .. 254)
+// 2^(byte - 127) of a scale byte (1 .. 247; 255, of a row of NaNs, gives infinity)
 __device__ __forceinline__ float cache_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
 
 bool cache_view(const gdpa_cache* c, CacheView& v, gdpa_status* s);

@@ -125,7 +125,7 @@ __device__ __forceinline__ float inverse_power(float x) {
 }
 
 template <int D, bool FP8, bool SM>
-__global__ void __launch_bounds__(kThreads, kCacheTcPerSm)
+__global__ void __launch_bounds__(kThreads, kCacheMmaPerSm)
 cache_mma_kernel(const __grid_constant__ AttnArgs a) {
     using C = Cfg<D, FP8>;
     constexpr int KSTEPS = D / 16, NT = D / 8;
@@ -563,7 +563,7 @@ gdpa_status launch(const AttnArgs& a, int grid, cudaStream_t st) {
 
 }  // namespace
 
-gdpa_status launch_cache_tc(const AttnArgs& a, int grid, cudaStream_t st) {
+gdpa_status launch_cache_mma(const AttnArgs& a, int grid, cudaStream_t st) {
     const bool fp8 = a.c.store == GDPA_STORE_E4M3, sm = a.act == kSoftmax;
     if (a.c.d == 128)
         return fp8 ? sm ? launch<128, true, true>(a, grid, st) : launch<128, true, false>(a, grid, st)

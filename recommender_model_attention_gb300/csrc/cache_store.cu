@@ -146,7 +146,7 @@ cache_write_kernel(const __grid_constant__ StoreArgs a) {
             if (live && blk >= 0) {
                 using T = typename Codes<N>::T;
                 *reinterpret_cast<T*>(dst + piece_at<true, N>(a.c, e, c)) = *reinterpret_cast<const T*>(p);
-                if (c == 0) (is_v ? a.c.vs : a.c.ks)[(blk << a.c.page_log) + e] = (uint8_t)(odd ? 127 : ex + 127);
+                if (c == 0) (is_v ? a.c.vs : a.c.ks)[(blk << a.c.page_log) + e] = (uint8_t)(odd ? 255 : ex + 127);
             }
         } else {
             if (live && blk >= 0)

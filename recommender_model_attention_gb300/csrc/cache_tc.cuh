@@ -1,0 +1,781 @@
+// Attention over the history cache for many query rows a key head (bf16, d = 64
+// or 128), on tcgen05: whole chunks of new events, wide trees, many heads a key
+// head.
+//
+// With more than a few rows a cached byte meets so many of them that products,
+// not bytes, bound the work.  A tile is up to 256 rows against a segment's
+// events in blocks of 128, in two slots of TMEM (128 columns of scores and d of
+// sums each), a warpgroup each, a thread a row:
+//   more than 128 rows: slot s holds rows 128 s .. of the tile, both read the
+//                       same blocks;
+//   else:               slot s takes the blocks s, s + 2, ... of the same rows,
+//                       and slot 0's threads join the two at the end.
+// One warp loads: each group of 16 events is a plain bulk copy (the cache holds
+// rows in the operands' swizzle), its page looked up 32 groups ahead.  One lane
+// issues S = Q K^T and O += P V; the order of loads and products, the lazily
+// moved reference and the exponentials in multiply-adds are shared-prefix
+// attention's (prefix_tc_fwd.cu says why).
+//
+// 8-bit caches: six worker warps expand each tile of codes to bf16 between the
+// copy and the products, exactly (a code has 4 bits): its 7 bits behind the sign
+// moved to bf16's place are the value times 2^-120, subnormal codes included,
+// and one bf16 product by 2^(e + 120) (two where that leaves bf16's range) gives
+// it.  So the row threads do not meet the scales.
+//
+// A block that some row does not see is masked by selection, event by event, and
+// workers clear the infinities and NaNs in its values (0 times them would be
+// NaN); that this happened is noted, and at the end the rows that do see such
+// events have them added.
+#pragma once
+
+#include "cache_attn.cuh"
+#include "prefix_tc.cuh"
+
+namespace gdpa {
+namespace cache_tc {
+
+using namespace tc;
+
+constexpr int kHalfBytes = 128 * 128;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRise = 8.0f;   // the reference follows a maximum this far above it
+
+template <int D, bool FP8>
+struct Cfg {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kTile = 128 * D * 2;
+    static constexpr int kStages = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
+    static constexpr int kRawTile = 128 * D;
+    static constexpr int kRaw = FP8 ? (D == 128 ? 3 : 6) : 0;
+    static constexpr int kWorkers = FP8 ? 6 : 2;             // warps
+    static constexpr int kRows0 = 2 + kWorkers;              // first row warp
+    static constexpr int kThreads = 32 * (kRows0 + 8);
+    static constexpr int kLow = FP8 ? 56 : 88, kHigh = FP8 ? 200 : 208;   // registers (of 128 and 168 at launch)
+    static constexpr int kOffKV = 2 * kTile;
+    static constexpr int kOffRaw = kOffKV + kStages * kTile;
+    static constexpr int kOffScale = kOffRaw + kRaw * kRawTile;
+    static constexpr int kOffMl = kOffScale + kRaw * 128;
+    static constexpr int kOffScan = kOffMl + 128 * 8;
+    static constexpr int kOffBar = kOffScan + (kThreads / 32 + 2) * 8;
+    enum {
+        kQFull = 0, kQEmpty, kDual, kMmaDone, kSFull, kPFull = kSFull + 2, kOFull = kPFull + 4, kOFree = kOFull + 2,
+        kFull = kOFree + 2,              // stage: the copy has landed (bf16) / its tile is ready (8-bit)
+        kEmpty = kFull + kStages,
+        kReady = kEmpty + kStages,       // bf16: workers have seen it
+        kRawFull = kReady + kStages, kRawEmpty = kRawFull + kRaw, kNumBars = kRawEmpty + kRaw
+    };
+    static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // Misc
+    static constexpr int kSmem = kOffMisc + 32 + 1024;
+    static_assert(kSmem <= 232448, "shared memory");
+};
+
+struct Misc {
+    uint32_t tmem;
+    int abort_flag;
+    int dirty;           // workers cleared something (of this or an earlier segment)
+    uint8_t gone[16];    // by block: groups without a page
+};
+
+// Blocks of a segment, as both slots take them, and which are masked.
+struct Walk {
+    int nb, n0, n1, hi_min, lo_max;
+    bool dual;
+    __device__ __forceinline__ Walk(const AttnArgs& a, const Segment& g) {
+        nb = (g.n + 7) >> 3;
+        dual = g.rows <= 128;
+        n0 = dual ? (nb + 1) >> 1 : nb;
+        n1 = dual ? nb >> 1 : nb;
+        const int i0 = g.rho0 / a.G, i1 = (g.rho0 + g.rows - 1) / a.G;
+        hi_min = min(g.s.end, g.s.start + (a.mask == GDPA_CACHE_CAUSAL ? i0 + 1 : 0));
+        lo_max = a.window > 0 ? g.s.start + (a.mask == GDPA_CACHE_HISTORY ? 0 : i1) - a.window + 1 : 0;
+    }
+    __device__ __forceinline__ int blocks(int s) const { return s ? n1 : n0; }
+    __device__ __forceinline__ int block(int s, int j) const { return dual ? 2 * j + s : j; }
+    __device__ __forceinline__ int groups(const Segment& g, int b) const { return min(8, g.n - 8 * b); }
+    __device__ __forceinline__ bool masked(const Segment& g, int b) const {
+        const int first = segment_group(g, 8 * b) * kCacheGroup;
+        const int last = segment_group(g, 8 * b + groups(g, b) - 1) * kCacheGroup + kCacheGroup - 1;
+        return last >= hi_min || first < lo_max;
+    }
+    // the tiles in the order of the ring: f(block, is V) until it returns false.
+    // more than 128 rows: K0 V0 K1 V1 ...; else: K0 K1 V0 K2 V1 K3 ...
+    template <typename F>
+    __device__ __forceinline__ bool tiles(F f) const {
+        const int lag = dual ? 2 : 1;
+        for (int b = 0; b < nb + lag; ++b) {
+            if (dual) {
+                if (b >= 2 && !f(b - 2, true)) return false;
+                if (b < nb && !f(b, false)) return false;
+            } else if (b < nb) {
+                if (!f(b, false) || !f(b, true)) return false;
+            }
+        }
+        return true;
+    }
+};
+
+__device__ __forceinline__ void bulk_load(uint64_t* bar, void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// The loader (a whole warp).
+template <int D, bool FP8>
+__device__ __forceinline__ void load_tiles(const AttnArgs& a, uint8_t* smem, uint64_t* bars, Misc& misc, Share sh,
+                                           const Abort& ab) {
+    using C = Cfg<D, FP8>;
+    constexpr int N = FP8 ? C::kRaw : C::kStages, kFullBar = FP8 ? C::kRawFull : C::kFull,
+                  kEmptyBar = FP8 ? C::kRawEmpty : C::kEmpty;
+    constexpr uint32_t kGroupBytes = FP8 ? 16 * D + 16 : 16 * D * 2;
+    const int lane = threadIdx.x & 31;
+    uint32_t c = 0, block0 = 0;
+    while (sh.u < sh.u_end) {
+        const Segment g = next_segment(a, sh);
+        const Walk w(a, g);
+        // page of group 32 i + lane of the segment
+        const auto pages = [&](int i) {
+            const int j = 32 * i + lane;
+            if (j >= g.n) return -1;
+            const int e = segment_group(g, j);
+            const int at = e >> (a.c.page_log - 4);
+            if (at >= a.w.width) return -1;   // (events behind the table are none of the segment's)
+            const int p = __ldg(a.w.table + g.b * a.w.stride + at);
+            if ((unsigned)p >= (unsigned)a.c.pages) {
+                cache_bad(a.c.err, kCacheBadPage, g.b, p);
+                return -1;
+            }
+            return p;
+        };
+        int prev = -1, cur = pages(0), next = pages(1), at = 0;
+        const bool ok = w.tiles([&](int b, bool is_v) {
+            if (!is_v && (b >> 2) > at) {
+                ++at;
+                prev = cur;
+                cur = next;
+                next = pages(at + 1);
+            }
+            const int ng = w.groups(g, b);
+            const int p = __shfl_sync(0xffffffffu, (b >> 2) == at ? cur : prev, 8 * (b & 3) + (lane & 7));
+            const uint32_t there = __ballot_sync(0xffffffffu, lane < ng && p >= 0);
+            const uint32_t st = c % N;
+            if (!__all_sync(0xffffffffu, mbar_wait<true>(&bars[kEmptyBar + st], ((c / N) & 1) ^ 1, ab, 62))) return false;
+            uint8_t* dst = smem + (FP8 ? C::kOffRaw + st * C::kRawTile : C::kOffKV + st * C::kTile);
+            uint8_t* sc = smem + C::kOffScale + st * 128;
+            if (!is_v && lane == 0) misc.gone[(block0 + b) & 15] = (uint8_t)(~there & ((1u << ng) - 1));
+            if (there != (1u << ng) - 1) {   // groups without a page hold zeros
+                for (int i = 0; i < ng; ++i) {
+                    if (there >> i & 1) continue;
+                    if constexpr (FP8) {
+                        for (int x = lane; x < D; x += 32) *reinterpret_cast<uint4*>(dst + i * 16 * D + 16 * x) = make_uint4(0, 0, 0, 0);
+                        if (lane == 0) *reinterpret_cast<uint4*>(sc + 16 * i) = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
+                    } else {
+                        for (int x = lane; x < 2 * D; x += 32)
+                            *reinterpret_cast<uint4*>(dst + (x >> 7) * kHalfBytes + i * 2048 + (x & 127) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&bars[kFullBar + st], kGroupBytes * __popc(there));
+            __syncwarp();
+            const int i = lane & 7, hf = lane >> 3;
+            if ((there >> i & 1) && hf < (FP8 ? 1 : C::kHalves)) {
+                const int e0 = (segment_group(g, 8 * b + i) * kCacheGroup) & ((1 << a.c.page_log) - 1);
+                const int64_t blk = (int64_t)p * a.c.heads + g.h;
+                const uint8_t* src = (is_v ? a.c.v : a.c.k) + blk * a.c.block;
+                if constexpr (FP8) {
+                    bulk_load(&bars[kFullBar + st], dst + i * 16 * D, src + e0 * D, 16 * D);
+                    bulk_load(&bars[kFullBar + st], sc + 16 * i, (is_v ? a.c.vs : a.c.ks) + (blk << a.c.page_log) + e0, 16);
+                } else {
+                    bulk_load(&bars[kFullBar + st], dst + hf * kHalfBytes + i * 2048,
+                              src + (((int64_t)hf << a.c.page_log) + e0) * 128, 2048);
+                }
+            }
+            ++c;
+            return true;
+        });
+        block0 += (uint32_t)w.nb;
+        if (!ok) break;
+    }
+    // never leave the CTA with a copy still in flight
+    for (uint32_t i = c > (uint32_t)N ? c - N : 0; i < c; ++i) mbar_wait_teardown(&bars[kFullBar + i % N], (i / N) & 1);
+}
+
+// 8 codes (8 bytes) to 8 bf16 values: m is 2^(e + 120), m2 a second factor.
+__device__ __forceinline__ uint4 expand8(uint32_t lo, uint32_t hi, uint32_t m, uint32_t m2) {
+    uint4 r;
+    uint32_t* o = &r.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t p = __byte_perm(i < 2 ? lo : hi, 0, (i & 1) ? 0x3424 : 0x1404);   // codes in the upper bytes
+        uint32_t x = ((p >> 4) & 0x07f007f0u) | (p & 0x80008000u);
+        __nv_bfloat162 y = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&m));
+        if (m2) y = __hmul2(y, *reinterpret_cast<const __nv_bfloat162*>(&m2));
+        o[i] = *reinterpret_cast<uint32_t*>(&y);
+    }
+    return r;
+}
+
+// The workers (warps; whole).
+template <int D, bool FP8>
+__device__ __forceinline__ void work_tiles(const AttnArgs& a, uint8_t* smem, uint64_t* bars, Misc& misc, Share sh,
+                                           const Abort& ab) {
+    using C = Cfg<D, FP8>;
+    const int lane = threadIdx.x & 31, who = threadIdx.x - 64;
+    uint32_t c = 0;
+    while (sh.u < sh.u_end) {
+        const Segment g = next_segment(a, sh);
+        const Walk w(a, g);
+        const bool ok = w.tiles([&](int b, bool is_v) {
+            const uint32_t st = c % C::kStages, ph = (c / C::kStages) & 1;
+            const int ng = w.groups(g, b);
+            if (!__all_sync(0xffffffffu, mbar_wait<true>(&bars[C::kEmpty + st], ph ^ 1, ab, 67))) return false;
+            uint8_t* dst = smem + C::kOffKV + st * C::kTile;
+            const bool clean = is_v && w.masked(g, b);
+            bool odd = false;
+            if constexpr (FP8) {
+                const uint32_t rs = c % C::kRaw;
+                if (!__all_sync(0xffffffffu, mbar_wait<true>(&bars[C::kRawFull + rs], (c / C::kRaw) & 1, ab, 69))) return false;
+                const uint8_t* src = smem + C::kOffRaw + rs * C::kRawTile;
+                const uint8_t* sc = smem + C::kOffScale + rs * 128;
+                constexpr int kChunks = D / 16;
+#pragma unroll 2
+                for (int x = who; x < 16 * ng * kChunks; x += 32 * C::kWorkers) {
+                    const int e = x / kChunks, ch = x % kChunks;
+                    const uint4 q = *reinterpret_cast<const uint4*>(src + cache_chunk(D, 7, e, ch));
+                    uint32_t s = sc[e];
+                    uint32_t m = (s + 120u) << 7, m2 = 0;
+                    if (s > 134u) {      // 2^(e + 120) passes bf16's range
+                        m = 254u << 7;
+                        m2 = (s - 7u) << 7;
+                        m2 |= m2 << 16;
+                    }
+                    if (s == 255u) {     // a row of NaNs
+                        m = clean ? 0u : 0x7fc0u;
+                        m2 = 0;
+                        odd |= clean;
+                    }
+                    // events behind the last one: whatever their memory holds
+                    if (clean && segment_group(g, 8 * b + (e >> 4)) * kCacheGroup + (e & 15) >= g.s.end) m = m2 = 0;
+                    m |= m << 16;
+                    uint8_t* row = dst + (ch >> 2) * kHalfBytes + e * 128;
+                    *reinterpret_cast<uint4*>(row + (((2 * ch) & 7) ^ (e & 7)) * 16) = expand8(q.x, q.y, m, m2);
+                    *reinterpret_cast<uint4*>(row + (((2 * ch + 1) & 7) ^ (e & 7)) * 16) = expand8(q.z, q.w, m, m2);
+                }
+                fence_proxy_async_smem();
+            } else if (clean) {
+                if (!__all_sync(0xffffffffu, mbar_wait<true>(&bars[C::kFull + st], ph, ab, 69))) return false;
+                for (int x = who; x < 16 * ng * (D / 8); x += 32 * C::kWorkers) {
+                    uint4* at = reinterpret_cast<uint4*>(dst + (x & 7) * 16 + ((x >> 3) % (16 * ng)) * 128 + ((x >> 3) / (16 * ng)) * kHalfBytes);
+                    uint4 v = *at;
+                    uint32_t any = 0;
+                    uint32_t* p = &v.x;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t z = __vcmpeq2(p[i] & 0x7f807f80u, 0x7f807f80u);
+                        any |= z;
+                        p[i] &= ~z;
+                    }
+                    if (any) {
+                        *at = v;
+                        odd = true;
+                    }
+                }
+                fence_proxy_async_smem();
+            }
+            if (odd) misc.dirty = 1;
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bars[(FP8 ? C::kFull : C::kReady) + st]);
+                if constexpr (FP8) mbar_arrive(&bars[C::kRawEmpty + c % C::kRaw]);
+            }
+            ++c;
+            return true;
+        });
+        if (!ok) return;
+    }
+}
+
+// The issuer of one segment (one lane).  State that goes on between segments.
+template <int STAGES>
+struct Issuer {
+    RingAt<STAGES> ring;
+    uint32_t p_ph[2] = {0, 0}, o_ph[2] = {1, 1}, q_ph = 0;
+};
+
+template <int D, bool FP8>
+__device__ __forceinline__ bool issue_segment(Issuer<Cfg<D, FP8>::kStages>& z, const Segment& g, const Walk& w,
+                                              uint8_t* smem, uint64_t* bars, uint32_t tmem, const Abort& ab) {
+    using C = Cfg<D, FP8>;
+    constexpr uint32_t idesc_pv = idesc_bf16(128, D, false, true);
+    constexpr uint32_t idesc_full = idesc_bf16(128, 128, false, false);
+    constexpr uint64_t kStageDesc = C::kTile >> 4;
+    const uint64_t q_desc = smem_desc_sw128(smem_u32(smem), 16, 1024);
+    const uint64_t k_desc = smem_desc_sw128(smem_u32(smem + C::kOffKV), 16, 1024);
+    const uint64_t v_desc = smem_desc_sw128(smem_u32(smem + C::kOffKV), kHalfBytes, 1024);
+    const int nb = w.nb;
+    const uint32_t last_keys = (uint32_t)(16 * w.groups(g, nb - 1));
+    const uint32_t idesc_last = idesc_bf16(128, last_keys, false, false);
+    const uint64_t q2 = q_desc + (w.dual ? 0 : kStageDesc);
+    auto full = [&](bool is_v) -> bool {
+        if (!mbar_wait<true>(&bars[C::kFull + z.ring.st], z.ring.ph, ab, 64)) return false;
+        if (!FP8 && is_v && !mbar_wait<true>(&bars[C::kReady + z.ring.st], z.ring.ph, ab, 70)) return false;
+        tc_fence_after();
+        return true;
+    };
+    auto scores = [&](int s, int b) {
+        one_scores<D>(tmem + s * 128, s ? q2 : q_desc, k_desc + z.ring.st * kStageDesc, b == nb - 1 ? idesc_last : idesc_full);
+        one_commit(&bars[C::kSFull + s]);
+    };
+    auto sums = [&](int s, int b, bool first) -> bool {
+        const uint32_t sc = tmem + s * 128, oc = tmem + 256 + s * 128;
+        const uint64_t vd = v_desc + z.ring.st * kStageDesc;
+        if (first) {   // the slot's sums of its last segment have been read
+            if (!mbar_wait<true>(&bars[C::kOFree + s], z.o_ph[s], ab, 65)) return false;
+            z.o_ph[s] ^= 1;
+        }
+        if (!mbar_wait<true>(&bars[C::kPFull + 2 * s], z.p_ph[s], ab, 66)) return false;
+        tc_fence_after();
+        const uint32_t keys = b == nb - 1 ? last_keys : 128u;
+        one_sums(oc, sc, sc + 16, vd, idesc_pv, keys >> 4, first ? 0 : 1);
+        if (!mbar_wait<true>(&bars[C::kPFull + 2 * s + 1], z.p_ph[s], ab, 68)) return false;
+        z.p_ph[s] ^= 1;
+        if (keys > 64) {
+            tc_fence_after();
+            one_sums(oc, sc + 32, sc + 48, vd + mnmajor_step(4), idesc_pv, (keys - 64) >> 4, 1);
+        }
+        return true;
+    };
+    if (!mbar_wait<true>(&bars[C::kQFull], z.q_ph, ab, 63)) return false;
+    z.q_ph ^= 1;
+    if (!w.dual) {
+        for (int b = -1; b < nb; ++b) {
+            const RingAt<C::kStages> v = z.ring;   // V of block b, then K of block b + 1
+            if (b >= 0) {
+                if (!full(true) || !sums(0, b, b == 0)) return false;
+                z.ring.next();
+            }
+            if (b + 1 < nb) {
+                if (!full(false)) return false;
+                scores(0, b + 1);
+            } else {
+                one_commit(&bars[C::kOFull]);
+            }
+            const RingAt<C::kStages> k = z.ring;
+            if (b >= 0) {
+                z.ring = v;
+                if (!sums(1, b, b == 0)) return false;
+                one_commit(&bars[C::kEmpty + v.st]);
+                z.ring = k;
+            }
+            if (b + 1 < nb) {
+                scores(1, b + 1);
+                one_commit(&bars[C::kEmpty + z.ring.st]);
+                if (b + 2 == nb) one_commit(&bars[C::kQEmpty]);   // the queries may be replaced
+                z.ring.next();
+            } else {
+                one_commit(&bars[C::kOFull + 1]);
+            }
+        }
+    } else {
+        for (int b = -2; b < nb; ++b) {
+            const int s = b & 1;
+            if (b >= 0) {
+                if (!full(true) || !sums(s, b, b < 2)) return false;
+                one_commit(&bars[C::kEmpty + z.ring.st]);
+                z.ring.next();
+                if (b + 2 >= nb) one_commit(&bars[C::kOFull + s]);
+            }
+            if (b + 2 < nb) {
+                if (!full(false)) return false;
+                scores(s, b + 2);
+                one_commit(&bars[C::kEmpty + z.ring.st]);
+                z.ring.next();
+                if (b + 3 == nb) one_commit(&bars[C::kQEmpty]);
+            }
+        }
+    }
+    return true;
+}
+
+// Infinities and NaNs of the masked blocks' values (left out of the products)
+// added to columns c0 .. c0 + 31 of a row that sees their events; element-wise
+// activations give NaN there.
+template <int D, bool FP8, bool SM>
+__device__ __noinline__ void add_odd(const AttnArgs& a, const Segment& g, const Walk& w, const RowView& rv, int c0, float* o) {
+    for (int b = 0; b < w.nb; ++b) {
+        if (!w.masked(g, b)) continue;
+        for (int i = 8 * b; i < 8 * b + w.groups(g, b); ++i) {
+            const int e0 = segment_group(g, i) * kCacheGroup;
+            const uint32_t bits = row_bits(a, g, rv, e0);
+            const int64_t blk = bits ? cache_block(a.c, a.w, g.b, e0, g.h) : -1;
+            if (blk < 0) continue;
+            for (int j = 0; j < 16; ++j) {
+                if (!(bits >> j & 1u)) continue;
+                const int e = (e0 + j) & ((1 << a.c.page_log) - 1);
+                const uint8_t* v = a.c.v + blk * a.c.block;
+                const bool nan = FP8 && a.c.vs[(blk << a.c.page_log) + e] == 255;
+                for (int c = 0; c < 32; ++c) {
+                    const int col = c0 + c;
+                    float y = nan ? __uint_as_float(0x7fc00000u) : 0.0f;
+                    if (!FP8)
+                        y = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(v + cache_chunk(2 * D, a.c.page_log, e, col >> 3) + 2 * (col & 7)));
+                    if (!isfinite(y)) o[c] += SM ? y : y - y;
+                }
+            }
+        }
+    }
+}
+
+template <int D, bool FP8, int ACT>
+__device__ __forceinline__ void tile_rows(const AttnArgs& a, uint8_t* smem, uint64_t* bars, Misc& misc, uint32_t tmem,
+                                          Share sh, const Abort& ab) {
+    using C = Cfg<D, FP8>;
+    constexpr bool kSm = ACT == kSoftmax;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int s = (warp - C::kRows0) >> 2;
+    const int quarter = warp & 3;
+    static_assert(C::kRows0 % 4 == 0, "a warpgroup a slot");
+    const int row = quarter * 32 + lane;
+    const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t sc = trow + s * 128, oc = trow + 256 + s * 128;
+    float2* ml1 = reinterpret_cast<float2*>(smem + C::kOffMl);
+    const bool flip = kSm && a.alpha < 0.0f;
+    ActScale ks = act_scale<ACT>(a.alpha);
+    if (kSm) {   // (a zero scale would make NaN of masked scores)
+        ks.c0 = fabsf(ks.c0);
+        if (ks.c0 < 1e-30f) ks.c0 = 1e-30f;
+    }
+    uint32_t items = 0, used[2] = {0, 0}, duals = 0, q_ph = 1, block0 = 0;
+    while (sh.u < sh.u_end) {
+        const Segment g = next_segment(a, sh);
+        const Walk w(a, g);
+        const int n = w.blocks(s);
+        const int r = (w.dual ? 0 : 128 * s) + row;      // of the tile
+        const bool real = r < g.rows;
+        const RowView rv = row_view(a, g, r);
+        if (w.nb > 0) {
+            // queries, a row a thread
+            if (!wg_wait<true>(&bars[C::kQEmpty], q_ph, ab, 61)) return;
+            q_ph ^= 1;
+            if (!(w.dual && s)) {
+                uint8_t* dst = smem + (w.dual ? 0 : s) * C::kTile + row * 128;
+                const int tok = max(rv.tok, 0);
+                const __nv_bfloat16* src = (const __nv_bfloat16*)a.q + (g.s.t0 + tok) * a.qt + (g.h * a.G + g.rho0 + r - tok * a.G) * a.qh;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (real) {
+                        if (a.q_wide) {
+                            v = __ldg(reinterpret_cast<const uint4*>(src) + c);
+                        } else {
+                            const uint16_t* h = reinterpret_cast<const uint16_t*>(src) + 8 * c;
+                            uint32_t* p = &v.x;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) p[i] = h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
+                        }
+                    }
+                    *reinterpret_cast<uint4*>(dst + (c >> 3) * kHalfBytes + (((c & 7) ^ (row & 7)) << 4)) = v;
+                }
+                fence_proxy_async_smem();
+            }
+            mbar_arrive(&bars[C::kQFull]);
+        }
+        float ref = -INFINITY, sum = 0.0f;
+        for (int j = 0; j < n; ++j) {
+            const int b = w.block(s, j);
+            if (!wg_wait<true>(&bars[C::kSFull + s], (items + j) & 1, ab, 71)) return;
+            tc_fence_after();
+            uint32_t x[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(sc + c * 32, *reinterpret_cast<uint32_t(*)[32]>(x + c * 32));
+            tmem_ld_wait();
+            if (flip) {
+#pragma unroll
+                for (int e = 0; e < 128; ++e) x[e] ^= 0x80000000u;
+            }
+            const uint32_t gone = *reinterpret_cast<volatile uint8_t*>(&misc.gone[(block0 + b) & 15]);
+            const int ng = w.groups(g, b);
+            const bool cut = ng < 8 || gone || w.masked(g, b);
+            if (cut) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    uint32_t bits = 0;
+                    if (q < ng && !(gone >> q & 1u)) bits = row_bits(a, g, rv, segment_group(g, 8 * b + q) * kCacheGroup);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (!(bits >> e & 1u)) x[16 * q + e] = 0xff800000u;   // -inf
+                }
+            }
+            if constexpr (kSm) {
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int e = 0; e < 128; e += 8)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        m4[u] = max3_nan(m4[u], __uint_as_float(x[e + u]), __uint_as_float(x[e + 4 + u]));
+                const float top = max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]) * ks.c0;
+                if (top != top) {   // (exp2_poly would take a NaN for a number)
+                    sum = top;
+                    if (ref == -INFINITY) ref = 0.0f;   // the part counts
+                }
+                const bool up = real && top > ref + kRise;   // also from -inf
+                if (__any_sync(0xffffffffu, up)) {
+                    const float nref = up ? top : ref;
+                    const float f = up ? ex2_approx(ref - nref) : 1.0f;   // 0 from -inf
+                    ref = nref;
+                    sum *= f;
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(oc + c, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st16(oc + c, o);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+            }
+            const float nref = kSm ? (ref == -INFINITY ? 0.0f : -ref) : 0.0f;
+            uint64_t sum2 = f2_make(0.0f, 0.0f);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int c = 2 * h; c < 2 * h + 2; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float p0, p1;
+                        const float s0 = __uint_as_float(x[c * 32 + e]), s1 = __uint_as_float(x[c * 32 + e + 1]);
+                        if constexpr (kSm) {
+                            const float2 tt = f2_split(
+                                f2_fma(f2_make(s0, s1), f2_make(ks.c0, ks.c0), f2_make(nref, nref)));
+                            if (e % 6 == 4) {   // one pair of three
+                                const float2 y = exp2_poly(tt);
+                                p0 = y.x;
+                                p1 = y.y;
+                            } else {
+                                p0 = ex2_approx(tt.x);
+                                p1 = ex2_approx(tt.y);
+                            }
+                            sum2 = f2_fma(f2_make(p0, p1), f2_make(1.0f, 1.0f), sum2);
+                        } else {
+                            act_s2<ACT>(s0, s1, ks, p0, p1);
+                            if (cut) {
+                                if (s0 == -INFINITY) p0 = 0.0f;
+                                if (s1 == -INFINITY) p1 = 0.0f;
+                            }
+                        }
+                        pk[e >> 1] = pack_bf16x2(p0, p1);
+                    }
+                    tmem_st16(sc + c * 16, pk);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&bars[C::kPFull + 2 * s + h]);
+            }
+            if constexpr (kSm) {
+                const float2 y = f2_split(sum2);
+                sum += y.x + y.y;
+            }
+        }
+        items += n;
+        block0 += (uint32_t)w.nb;
+        const bool both = w.dual && w.n1 > 0;   // slot 0 joins slot 1's sums to its own
+        if (n > 0) {
+            if (!wg_wait<true>(&bars[C::kOFull + s], used[s] & 1, ab, 73)) return;
+            tc_fence_after();
+        }
+        if (both && s) {
+            ml1[row] = make_float2(ref, sum);
+            tc_fence_before();
+            mbar_arrive(&bars[C::kDual]);
+        }
+        float f0 = 1.0f, f1 = 0.0f;
+        if (both && !s) {
+            if (!wg_wait<true>(&bars[C::kOFull + 1], used[1] & 1, ab, 74) || !wg_wait<true>(&bars[C::kDual], duals & 1, ab, 75)) return;
+            tc_fence_after();
+            f1 = 1.0f;
+            if constexpr (kSm) {
+                const float2 y = ml1[row];
+                const float m = fmaxf(ref, y.x), m0 = m == -INFINITY ? 0.0f : m;
+                f0 = ex2_approx(ref - m0);
+                f1 = ex2_approx(y.x - m0);
+                sum = sum * f0 + y.y * f1;
+                ref = m;
+            }
+        }
+        if (!(w.dual && s)) {
+            const bool dirty = *reinterpret_cast<volatile int*>(&misc.dirty) != 0;
+            float* slot = nullptr;
+            if (!g.whole) slot = a.part + (int64_t)(2 * blockIdx.x + (g.head ? 1 : 0)) * a.TM * (D + 2);
+            const float inv = kSm ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
+            const int rho = g.rho0 + r, tok = max(rv.tok, 0);
+            const int64_t out = (int64_t)(g.s.t0 + tok) * a.H + g.h * a.G + (rho - tok * a.G);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                float y[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) y[e] = 0.0f;
+                if (n > 0) {
+                    tmem_ld32(oc + c * 32, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) y[e] = f0 == 0.0f ? 0.0f : __uint_as_float(o[e]) * f0;
+                }
+                if (both) {
+                    tmem_ld32(oc + 128 + c * 32, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) y[e] = fmaf(__uint_as_float(o[e]), f1, y[e]);
+                }
+                if (dirty && real) {
+                    float z[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) z[e] = y[e];
+                    add_odd<D, FP8, kSm>(a, g, w, rv, 32 * c, z);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) y[e] = z[e];
+                }
+                if (real) {
+                    if (slot) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            reinterpret_cast<float4*>(slot + r * D + 32 * c)[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+                    } else {
+                        uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)a.o + out * D + 32 * c);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            dst[e] = make_uint4(pack_bf16x2(y[8 * e] * inv, y[8 * e + 1] * inv), pack_bf16x2(y[8 * e + 2] * inv, y[8 * e + 3] * inv),
+                                                pack_bf16x2(y[8 * e + 4] * inv, y[8 * e + 5] * inv), pack_bf16x2(y[8 * e + 6] * inv, y[8 * e + 7] * inv));
+                    }
+                }
+            }
+            if (kSm && real) {
+                if (slot) {
+                    slot[a.TM * D + r] = ref;
+                    slot[a.TM * (D + 1) + r] = sum;
+                } else if (a.lse) {
+                    a.lse[out] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.693147180559945309f;
+                }
+            }
+            if (slot && g.head && threadIdx.x == 32 * C::kRows0) {
+                CacheDesc& t = a.desc[blockIdx.x];
+                t.rows = g.rows;
+                t.t0 = g.s.t0;
+                t.h = g.h;
+                t.rho0 = g.rho0;
+                t.parts = g.parts;
+            }
+            tc_fence_before();
+            if (n > 0) mbar_arrive(&bars[C::kOFree + s]);
+            if (both) mbar_arrive(&bars[C::kOFree + 1]);
+        }
+        used[0] += w.n0 > 0;
+        used[1] += w.n1 > 0;
+        duals += both;
+    }
+}
+
+template <int D, bool FP8, int ACT>
+__global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
+cache_tc_kernel(const __grid_constant__ AttnArgs a) {
+    using C = Cfg<D, FP8>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+    Misc& misc = *reinterpret_cast<Misc*>(smem + C::kOffMisc);
+    const int warp = threadIdx.x >> 5;
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (threadIdx.x == 32 * C::kRows0) a.desc[blockIdx.x].parts = 0;   // (the thread that may set it)
+    if (threadIdx.x == 0) {
+        for (int b = 0; b < C::kNumBars; ++b) {
+            uint32_t n = 1;
+            if (b == C::kQFull) n = 256;
+            if (b == C::kDual || (b >= C::kPFull && b < C::kPFull + 4) || (b >= C::kOFree && b < C::kOFree + 2)) n = 128;
+            if ((FP8 && b >= C::kFull && b < C::kFull + C::kStages) || (b >= C::kReady && b < C::kReady + C::kStages) ||
+                (b >= C::kRawEmpty && b < C::kRawEmpty + C::kRaw))
+                n = C::kWorkers;
+            mbar_init(&bars[b], n);
+        }
+        misc.abort_flag = 0;
+        misc.dirty = 0;
+        fence_mbar_init();
+    }
+    const Share sh = find_share<C::kThreads>(a, reinterpret_cast<int64_t*>(smem + C::kOffScan));
+    if (sh.u >= sh.u_end) return;   // the whole CTA
+    if (warp == 1) tmem_alloc(&misc.tmem, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = misc.tmem;
+    const Abort ab{&misc.abort_flag, a.c.err, kWaitLimitNs};
+    if (warp < C::kRows0) {
+        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 0) {
+            load_tiles<D, FP8>(a, smem, bars, misc, sh, ab);
+        } else if (warp == 1) {
+            Issuer<C::kStages> z;
+            Share mine = sh;
+            bool ok = true;
+            while (mine.u < mine.u_end && ok) {
+                const Segment g = next_segment(a, mine);
+                const Walk w(a, g);
+                if (w.nb == 0) continue;
+                if (elect_one()) ok = issue_segment<D, FP8>(z, g, w, smem, bars, tmem, ab);
+                // the elected lane keeps the state; all agree on whether to go on
+                ok = __all_sync(0xffffffffu, ok);
+            }
+            if (elect_one()) {
+                // all of its products complete before TMEM is released
+                one_commit(&bars[C::kMmaDone]);
+                mbar_wait_teardown(&bars[C::kMmaDone], 0);
+            }
+            __syncwarp();
+        } else {
+            work_tiles<D, FP8>(a, smem, bars, misc, sh, ab);
+        }
+    } else {
+        if constexpr (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        tile_rows<D, FP8, ACT>(a, smem, bars, misc, tmem, sh, ab);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int D, bool FP8, int ACT>
+gdpa_status launch(const AttnArgs& a, int grid, cudaStream_t st) {
+    using C = Cfg<D, FP8>;
+    if (cudaFuncSetAttribute(cache_tc_kernel<D, FP8, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+        return GDPA_ERR_CUDA;
+    cache_tc_kernel<D, FP8, ACT><<<grid, C::kThreads, C::kSmem, st>>>(a);
+    return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
+}
+
+template <bool FP8>
+gdpa_status launch_any(const AttnArgs& a, int grid, cudaStream_t st) {
+    gdpa_status s = GDPA_OK;
+    if (a.c.d == 128) {
+        if (a.act == kSoftmax) return launch<128, FP8, kSoftmax>(a, grid, st);
+        GDPA_DISPATCH_ACT(a.act, A, s = launch<128, FP8, A>(a, grid, st))
+    } else {
+        if (a.act == kSoftmax) return launch<64, FP8, kSoftmax>(a, grid, st);
+        GDPA_DISPATCH_ACT(a.act, A, s = launch<64, FP8, A>(a, grid, st))
+    }
+    return s;
+}
+
+}  // namespace cache_tc
+}  // namespace gdpa
