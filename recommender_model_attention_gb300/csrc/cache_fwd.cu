@@ -12,12 +12,34 @@ namespace {
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kMaxGrid = 2048;   // CTAs of an attention kernel at most (their records fit a block's shared memory)
 
-// A block a row: its warps take turns over the row's parts, then add up in
-// shared memory, always in the same order.
+// Rows of few parts are a warp each, eight a block; a row of many parts is a
+// block's, whose warps take turns over the parts and add up in shared memory.
+// Both always add in the same order.  (A block a row throughout: 120 us for the
+// 38400 rows of 2 or 3 parts that 8 x 512 rows on 16384 events leave.)
+constexpr int kFewParts = 8;
+
+template <typename E, bool SM>
+__device__ __forceinline__ void put_row(const AttnArgs& a, const CacheDesc& t, int r, int lane, const float4& x, float M, float l) {
+    const int rho = t.rho0 + r, tok = rho / a.G;
+    const int64_t row = (int64_t)(t.t0 + tok) * a.H + t.h * a.G + (rho - tok * a.G);
+    float f = 1.0f;
+    if (SM) {
+        f = l == 0.0f ? 0.0f : 1.0f / l;
+        if (lane == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.693147180559945309f;
+    }
+    const float y[4] = {x.x * f, x.y * f, x.z * f, x.w * f};
+    if (4 * lane < a.c.d) put4((E*)a.o + row * a.c.d + 4 * lane, y);
+}
+
+// a part's factor and sum, given the row's maximum
+__device__ __forceinline__ float part_factor(float m, float n, float M) {
+    return m == -INFINITY ? (n == 0.0f ? 0.0f : n) : ex2_approx(m - M);   // (n: a NaN)
+}
+
 template <typename E, bool SM>
 __global__ void __launch_bounds__(kJoinThreads)
 cache_join_kernel(const __grid_constant__ AttnArgs a, int ctas) {
-    __shared__ int first[kMaxGrid + 1];   // rows of the items before
+    __shared__ int first[kMaxGrid + 1];   // units of the items before: rows, or eights of them
     __shared__ int tmp[kJoinWarps];
     __shared__ float4 sums[kJoinWarps][32];
     __shared__ float2 ml[kJoinWarps];
@@ -28,7 +50,11 @@ cache_join_kernel(const __grid_constant__ AttnArgs a, int ctas) {
     for (int c0 = 0; c0 < ctas; c0 += kJoinThreads) {
         const int c = c0 + tid;
         int n = 0;
-        if (c < ctas) n = a.desc[c].parts > 1 ? a.desc[c].rows : 0;
+        if (c < ctas) {
+            const int parts = a.desc[c].parts;
+            n = parts > 1 ? a.desc[c].rows : 0;
+            if (parts <= kFewParts) n = (n + 7) >> 3;
+        }
         int x = n;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
@@ -54,9 +80,41 @@ cache_join_kernel(const __grid_constant__ AttnArgs a, int ctas) {
             if (first[mid] <= i) lo = mid; else hi = mid;
         }
         const CacheDesc t = a.desc[lo];
-        const int r = i - first[lo];
         // part p: slot 2 lo + 1, then 2 (lo + 1), 2 (lo + 2), ...
         const auto slot = [&](int p) { return a.part + (int64_t)(p == 0 ? 2 * lo + 1 : 2 * (lo + p)) * ld; };
+        if (t.parts <= kFewParts) {
+            const int r = 8 * (i - first[lo]) + warp;
+            if (r >= t.rows) continue;
+            float m = -INFINITY, n = 0.0f;
+            if (SM && lane < t.parts) {
+                m = slot(lane)[a.TM * d + r];
+                n = slot(lane)[a.TM * (d + 1) + r];
+            }
+            float4 y[kFewParts];
+#pragma unroll
+            for (int p = 0; p < kFewParts; ++p)
+                if (p < t.parts && 4 * lane < d) y[p] = *reinterpret_cast<const float4*>(slot(p) + r * d + 4 * lane);
+            float M = m;
+#pragma unroll
+            for (int k = 1; k < kFewParts; k <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+            M = __shfl_sync(0xffffffffu, M, 0);
+            const float f = SM ? part_factor(m, n, M) : 1.0f;
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float l = 0.0f;
+#pragma unroll
+            for (int p = 0; p < kFewParts; ++p) {
+                if (p >= t.parts) break;
+                const float g = __shfl_sync(0xffffffffu, f, p);
+                l += __shfl_sync(0xffffffffu, n, p) * g;
+                x.x += y[p].x * g;
+                x.y += y[p].y * g;
+                x.z += y[p].z * g;
+                x.w += y[p].w * g;
+            }
+            put_row<E, SM>(a, t, r, lane, x, M, l);
+            continue;
+        }
+        const int r = i - first[lo];
         float M = -INFINITY;
         if (SM) {
             for (int p = lane; p < t.parts; p += 32) M = fmaxf(M, slot(p)[a.TM * d + r]);
@@ -71,7 +129,7 @@ cache_join_kernel(const __grid_constant__ AttnArgs a, int ctas) {
             float f = 1.0f;
             if (SM) {
                 const float m = s[a.TM * d + r], n = s[a.TM * (d + 1) + r];
-                f = m == -INFINITY ? (n == 0.0f ? 0.0f : n) : ex2_approx(m - M);   // (n: a NaN)
+                f = part_factor(m, n, M);
                 l += n * f;
             }
             if (4 * lane < d) {
@@ -94,15 +152,7 @@ cache_join_kernel(const __grid_constant__ AttnArgs a, int ctas) {
                 x.w += y.w;
                 l += ml[w].y;
             }
-            const int rho = t.rho0 + r, tok = rho / a.G;
-            const int64_t row = (int64_t)(t.t0 + tok) * a.H + t.h * a.G + (rho - tok * a.G);
-            float f = 1.0f;
-            if (SM) {
-                f = l == 0.0f ? 0.0f : 1.0f / l;
-                if (lane == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.693147180559945309f;
-            }
-            const float y[4] = {x.x * f, x.y * f, x.z * f, x.w * f};
-            if (4 * lane < d) put4((E*)a.o + row * d + 4 * lane, y);
+            put_row<E, SM>(a, t, r, lane, x, M, l);
         }
         __syncthreads();
     }
@@ -138,7 +188,7 @@ int device_sms() {
 enum Kind { kSimt, kMma, kTc };
 struct Shape {
     Kind kind;
-    int RT, TM, grid, sms, min_share;
+    int RT, TM, grid, sms, min_share, lead;
     int64_t bytes;
 };
 
@@ -153,13 +203,15 @@ gdpa_status shape(const CacheView& c, gdpa_dtype dt, int64_t T, int H, int B, Sh
         s.RT = 0;
         s.TM = rows <= 128 ? 128 : 256;
         s.grid = s.sms;
-        s.min_share = 16;
+        s.min_share = 48;
+        s.lead = 32;
     } else {
         // row tiles of 16 that a CTA holds: as many as an average sample fills
         s.RT = s.kind == kSimt || rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
         s.TM = 16 * s.RT;
         s.grid = s.sms * (s.kind == kMma ? kCacheMmaPerSm : kCacheSimtPerSm);
-        s.min_share = 4 / s.RT;
+        s.lead = 12 / s.RT;
+        s.min_share = s.lead + 4 / s.RT;
     }
     if (s.grid > kMaxGrid) s.grid = kMaxGrid;
     s.bytes = (int64_t)s.grid * (sizeof(CacheDesc) + 2ll * s.TM * (c.d + 2) * 4);
@@ -230,6 +282,7 @@ gdpa_status gdpa_cache_fwd(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T,
     a.TM = p.TM;
     a.RT = p.RT;
     a.min_share = p.min_share;
+    a.lead = p.lead;
     a.desc = (CacheDesc*)workspace;
     a.part = (float*)(a.desc + p.grid);
     const bool sm = a.act == kSoftmax;

@@ -60,6 +60,7 @@ cache_simt_kernel(const __grid_constant__ AttnArgs a) {
     Share sh = find_share<kThreads>(a, scan_tmp);
     while (sh.u < sh.u_end) {
         const Segment g = next_segment(a, sh);
+        if (g.rows == 0) break;
         for (int i = tid; i < 16 * d; i += kThreads) {
             const int x = i / d, c = i - x * d, rho = g.rho0 + x, tok = rho / a.G;
             Q[x * ld + c] = x < g.rows ? to_f(((const E*)a.q)[(g.s.t0 + tok) * a.qt + (g.h * a.G + rho - tok * a.G) * a.qh + c]) : 0.0f;

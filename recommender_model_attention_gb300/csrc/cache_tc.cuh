@@ -133,6 +133,7 @@ __device__ __forceinline__ void load_tiles(const AttnArgs& a, uint8_t* smem, uin
     uint32_t c = 0, block0 = 0;
     while (sh.u < sh.u_end) {
         const Segment g = next_segment(a, sh);
+        if (g.rows == 0) break;
         const Walk w(a, g);
         // page of group 32 i + lane of the segment
         const auto pages = [&](int i) {
@@ -227,6 +228,7 @@ __device__ __forceinline__ void work_tiles(const AttnArgs& a, uint8_t* smem, uin
     uint32_t c = 0;
     while (sh.u < sh.u_end) {
         const Segment g = next_segment(a, sh);
+        if (g.rows == 0) break;
         const Walk w(a, g);
         const bool ok = w.tiles([&](int b, bool is_v) {
             const uint32_t st = c % C::kStages, ph = (c / C::kStages) & 1;
@@ -451,6 +453,7 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& a, uint8_t* smem, uint
     uint32_t items = 0, used[2] = {0, 0}, duals = 0, q_ph = 1, block0 = 0;
     while (sh.u < sh.u_end) {
         const Segment g = next_segment(a, sh);
+        if (g.rows == 0) break;
         const Walk w(a, g);
         const int n = w.blocks(s);
         const int r = (w.dual ? 0 : 128 * s) + row;      // of the tile
@@ -727,6 +730,7 @@ cache_tc_kernel(const __grid_constant__ AttnArgs a) {
             bool ok = true;
             while (mine.u < mine.u_end && ok) {
                 const Segment g = next_segment(a, mine);
+                if (g.rows == 0) break;
                 const Walk w(a, g);
                 if (w.nb == 0) continue;
                 if (elect_one()) ok = issue_segment<D, FP8>(z, g, w, smem, bars, tmem, ab);
