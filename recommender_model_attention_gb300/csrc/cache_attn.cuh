@@ -360,6 +360,6 @@ gdpa_status launch_cache_mma(const AttnArgs& a, int grid, cudaStream_t st);
 gdpa_status launch_cache_tc_bf16(const AttnArgs& a, int grid, cudaStream_t st);
 gdpa_status launch_cache_tc_e4m3(const AttnArgs& a, int grid, cudaStream_t st);
 gdpa_status launch_cache_simt(const AttnArgs& a, gdpa_dtype dt, int grid, cudaStream_t st);
-constexpr int kCacheMmaPerSm = 2, kCacheSimtPerSm = 2;
+constexpr int kCacheSimtPerSm = 2;
 
 }  // namespace gdpa

@@ -208,8 +208,8 @@ gdpa_status shape(const CacheView& c, gdpa_dtype dt, int64_t T, int H, int B, Sh
     } else {
         // row tiles of 16 that a CTA holds: as many as an average sample fills
         s.RT = s.kind == kSimt || rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-        s.TM = 16 * s.RT;
-        s.grid = s.sms * (s.kind == kMma ? kCacheMmaPerSm : kCacheSimtPerSm);
+        s.TM = s.kind == kMma && rows <= 8 ? 8 : 16 * s.RT;
+        s.grid = s.sms * (s.kind == kSimt ? kCacheSimtPerSm : s.TM == 8 ? 3 : 2);   // resident
         s.lead = 12 / s.RT;
         s.min_share = s.lead + 4 / s.RT;
     }
