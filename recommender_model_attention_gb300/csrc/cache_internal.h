@@ -10,8 +10,8 @@
 // chunk of 8 events, or 8 chunks of every second one, meet no bank twice.  It
 // is also the 128-byte swizzle of tcgen05 operands, which a plain copy of
 // whole events therefore brings into shared memory ready to use.  Rows of 64
-// bytes lie two to a line, chunk c of event e at (4 (e & 1) + c) ^ (2 ((e >> 1)
-// & 3)), for the same reason; all other widths lie row after row.
+// bytes lie row after row, chunk c of event e at c ^ ((e >> 1) & 3), the 64-byte
+// swizzle; all other widths plainly.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -48,7 +48,7 @@ struct CacheWhere {
 __host__ __device__ __forceinline__ int cache_chunk(int row, int page_log, int e, int c) {
     if ((row & 127) == 0)
         return ((((c >> 3) << page_log) + e) << 7) + (((c & 7) ^ (e & 7)) << 4);
-    if (row == 64) return ((e >> 1) << 7) + (((4 * (e & 1) + c) ^ (2 * ((e >> 1) & 3))) << 4);
+    if (row == 64) return (e << 6) + ((c ^ ((e >> 1) & 3)) << 4);
     return e * row + (c << 4);
 }
 

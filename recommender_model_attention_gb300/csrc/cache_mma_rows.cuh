@@ -74,17 +74,6 @@ __device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// two values of a query row (at most 256) as E4M3 codes, and 2^5 times what these leave of them
-__device__ __forceinline__ void split_q(float x, float y, uint32_t& hi, uint32_t& lo) {
-    uint16_t h, l;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(y), "f"(x));
-    uint32_t f;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(h));
-    const float2 v = __half22float2(*reinterpret_cast<__half2*>(&f));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(l) : "f"((y - v.y) * 32.0f), "f"((x - v.x) * 32.0f));
-    hi = h;
-    lo = l;
-}
 template <bool FP8>
 __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     if constexpr (FP8) mma_f16(c, a[0], a[1], a[2], a[3], b0, b1);
@@ -115,18 +104,12 @@ __device__ __forceinline__ uint32_t odd_bits(uint32_t w) {
     return __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u);
 }
 
-// the power of two 2^-floor(log2 x), x > 0 finite and normal; kept within f32
-__device__ __forceinline__ float inverse_power(float x) {
-    const uint32_t e = __float_as_uint(x) >> 23;
-    return __uint_as_float((uint32_t)(min(max(254 - (int)e, 1), 254)) << 23);
-}
-
 
 // where the 16-byte piece c (of those that a thread with this t takes) of event e's keys lies in a group
 template <int D, bool FP8>
 __device__ __forceinline__ uint4 key_piece(const uint8_t* kp, int e, int t, int c) {
     if constexpr (FP8 && D == 64)
-        return *reinterpret_cast<const uint4*>(kp + (e >> 1) * 128 + (((4 * (e & 1) + t) ^ (2 * ((e >> 1) & 3))) << 4));
+        return *reinterpret_cast<const uint4*>(kp + e * 64 + ((t ^ ((e >> 1) & 3)) << 4));
     else
         return *reinterpret_cast<const uint4*>(kp + (c >> 1) * 2048 + e * 128 + (((2 * t + (c & 1)) ^ (e & 7)) << 4));
 }
@@ -138,7 +121,7 @@ __device__ __forceinline__ void value_words(const uint8_t* vp, int e, int gq, ui
         *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(vp + e * 128 + ((gq ^ (e & 7)) << 4));
     } else if constexpr (FP8) {
         *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(
-            vp + (e >> 1) * 128 + (((4 * (e & 1) + (gq >> 1)) ^ (2 * ((e >> 1) & 3))) << 4) + 8 * (gq & 1));
+            vp + e * 64 + (((gq >> 1) ^ ((e >> 1) & 3)) << 4) + 8 * (gq & 1));
     } else {
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
@@ -201,7 +184,7 @@ __device__ __forceinline__ float split_query(const uint32_t (&w)[STEPS][2], uint
     for (int s = 0; s < STEPS; ++s) {
         uint32_t h[2], l[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) split_q(bf16_lo(w[s][j]) * f * 128.0f, bf16_hi(w[s][j]) * f * 128.0f, h[j], l[j]);
+        for (int j = 0; j < 2; ++j) split_q<true>(bf16_lo(w[s][j]) * f * 128.0f, bf16_hi(w[s][j]) * f * 128.0f, h[j], l[j]);
         hi[s >> 1][s & 1] = h[0] | h[1] << 16;
         lo[s >> 1][s & 1] = l[0] | l[1] << 16;
     }

@@ -16,11 +16,15 @@
 // moved reference and the exponentials in multiply-adds are shared-prefix
 // attention's (prefix_tc_fwd.cu says why).
 //
-// 8-bit caches: six worker warps expand each tile of codes to bf16 between the
-// copy and the products, exactly (a code has 4 bits): its 7 bits behind the sign
-// moved to bf16's place are the value times 2^-120, subnormal codes included,
-// and one bf16 product by 2^(e + 120) (two where that leaves bf16's range) gives
-// it.  So the row threads do not meet the scales.
+// 8-bit caches.  Keys are multiplied as they are (kind::f8f6f4): a query row,
+// scaled by a power of two to below 256, is split into E4M3 codes and E5M2 codes
+// of what they leave, at most 8 units of bf16's last place, which 3 bits hold
+// (elements below 2^-13 of the largest lose bits, at most 2^-21 of it): two
+// products of double rate; the keys' powers of two are applied to the scores.  Values are expanded to bf16 by six worker warps, exactly
+// (a code has 4 bits): its 7 bits behind the sign moved to bf16's place are the
+// value times 2^-120, subnormal codes included, and one bf16 product by 2^(e +
+// 120) (two where that leaves bf16's range) gives it.  (Keys expanded as well:
+// the workers bound the kernel, 480 us for 8 x 512 rows on 16384 events.)
 //
 // A block that some row does not see is masked by selection, event by event, and
 // workers clear the infinities and NaNs in its values (0 times them would be
@@ -43,26 +47,33 @@ constexpr float kRise = 8.0f;   // the reference follows a maximum this far abov
 template <int D, bool FP8>
 struct Cfg {
     static constexpr int kHalves = D / 64;
-    static constexpr int kTile = 128 * D * 2;
-    static constexpr int kStages = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
-    static constexpr int kRawTile = 128 * D;
-    static constexpr int kRaw = FP8 ? (D == 128 ? 3 : 6) : 0;
+    static constexpr int kTile = 128 * D * 2;                // 128 rows in bf16
+    static constexpr int kCodes = 128 * D;                   // ... in 8 bits
+    static constexpr int kKTile = FP8 ? kCodes : kTile;
+    static constexpr int kK = FP8 ? (D == 128 ? 3 : 4) : (D == 128 ? 3 : 4);   // stages: keys
+    static constexpr int kV = D == 128 ? 2 : 4;                                // values in bf16
+    static constexpr int kR = FP8 ? (D == 128 ? 2 : 3) : 0;                    // values in 8 bits
     static constexpr int kWorkers = FP8 ? 6 : 2;             // warps
     static constexpr int kRows0 = 2 + kWorkers;              // first row warp
     static constexpr int kThreads = 32 * (kRows0 + 8);
-    static constexpr int kLow = FP8 ? 56 : 88, kHigh = FP8 ? 200 : 208;   // registers (of 128 and 168 at launch)
-    static constexpr int kOffKV = 2 * kTile;
-    static constexpr int kOffRaw = kOffKV + kStages * kTile;
-    static constexpr int kOffScale = kOffRaw + kRaw * kRawTile;
-    static constexpr int kOffMl = kOffScale + kRaw * 128;
+    static constexpr int kOffK = 2 * kTile;                  // behind two tiles of queries (8-bit: each as two)
+    static constexpr int kOffV = kOffK + kK * kKTile;
+    static constexpr int kOffR = kOffV + kV * kTile;
+    static constexpr int kOffKScale = kOffR + kR * kCodes;   // bytes of the K stages, of the 8-bit V stages
+    static constexpr int kOffVScale = kOffKScale + (FP8 ? kK * 128 : 0);
+    static constexpr int kOffScale = kOffVScale + kR * 128;  // powers of two of the last 8 blocks' keys
+    static constexpr int kOffMl = kOffScale + (FP8 ? 8 * 512 : 0);
     static constexpr int kOffScan = kOffMl + 128 * 8;
     static constexpr int kOffBar = kOffScan + (kThreads / 32 + 2) * 8;
     enum {
         kQFull = 0, kQEmpty, kDual, kMmaDone, kSFull, kPFull = kSFull + 2, kOFull = kPFull + 4, kOFree = kOFull + 2,
-        kFull = kOFree + 2,              // stage: the copy has landed (bf16) / its tile is ready (8-bit)
-        kEmpty = kFull + kStages,
-        kReady = kEmpty + kStages,       // bf16: workers have seen it
-        kRawFull = kReady + kStages, kRawEmpty = kRawFull + kRaw, kNumBars = kRawEmpty + kRaw
+        kKFull = kOFree + 2,             // keys have landed
+        kKReady = kKFull + kK,           // 8-bit: their powers of two are in place
+        kKEmpty = kKReady + kK,
+        kVFull = kKEmpty + kK,           // bf16: values have landed
+        kVReady = kVFull + kV,           // workers have cleaned or expanded them
+        kVEmpty = kVReady + kV,
+        kRFull = kVEmpty + kV, kREmpty = kRFull + kR, kNumBars = kREmpty + kR
     };
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // Misc
     static constexpr int kSmem = kOffMisc + 32 + 1024;
@@ -126,11 +137,13 @@ template <int D, bool FP8>
 __device__ __forceinline__ void load_tiles(const AttnArgs& a, uint8_t* smem, uint64_t* bars, Misc& misc, Share sh,
                                            const Abort& ab) {
     using C = Cfg<D, FP8>;
-    constexpr int N = FP8 ? C::kRaw : C::kStages, kFullBar = FP8 ? C::kRawFull : C::kFull,
-                  kEmptyBar = FP8 ? C::kRawEmpty : C::kEmpty;
     constexpr uint32_t kGroupBytes = FP8 ? 16 * D + 16 : 16 * D * 2;
+    constexpr int NV = FP8 ? C::kR : C::kV, kVFullBar = FP8 ? C::kRFull : C::kVFull, kVEmptyBar = FP8 ? C::kREmpty : C::kVEmpty;
     const int lane = threadIdx.x & 31;
-    uint32_t c = 0, block0 = 0;
+    uint32_t block0 = 0;
+    RingAt<C::kK> rk;
+    RingAt<NV> rv;
+    uint32_t nk = 0, nv = 0;
     while (sh.u < sh.u_end) {
         const Segment g = next_segment(a, sh);
         if (g.rows == 0) break;
@@ -139,8 +152,7 @@ __device__ __forceinline__ void load_tiles(const AttnArgs& a, uint8_t* smem, uin
         const auto pages = [&](int i) {
             const int j = 32 * i + lane;
             if (j >= g.n) return -1;
-            const int e = segment_group(g, j);
-            const int at = e >> (a.c.page_log - 4);
+            const int at = segment_group(g, j) >> (a.c.page_log - 4);
             if (at >= a.w.width) return -1;   // (events behind the table are none of the segment's)
             const int p = __ldg(a.w.table + g.b * a.w.stride + at);
             if ((unsigned)p >= (unsigned)a.c.pages) {
@@ -160,10 +172,11 @@ __device__ __forceinline__ void load_tiles(const AttnArgs& a, uint8_t* smem, uin
             const int ng = w.groups(g, b);
             const int p = __shfl_sync(0xffffffffu, (b >> 2) == at ? cur : prev, 8 * (b & 3) + (lane & 7));
             const uint32_t there = __ballot_sync(0xffffffffu, lane < ng && p >= 0);
-            const uint32_t st = c % N;
-            if (!__all_sync(0xffffffffu, mbar_wait<true>(&bars[kEmptyBar + st], ((c / N) & 1) ^ 1, ab, 62))) return false;
-            uint8_t* dst = smem + (FP8 ? C::kOffRaw + st * C::kRawTile : C::kOffKV + st * C::kTile);
-            uint8_t* sc = smem + C::kOffScale + st * 128;
+            const uint32_t st = is_v ? rv.st : rk.st;
+            uint64_t* full = &bars[(is_v ? kVFullBar : C::kKFull) + st];
+            if (!__all_sync(0xffffffffu, mbar_wait<true>(&bars[(is_v ? kVEmptyBar : C::kKEmpty) + st], (is_v ? rv.ph : rk.ph) ^ 1, ab, 62))) return false;
+            uint8_t* dst = smem + (!is_v ? C::kOffK + st * C::kKTile : FP8 ? C::kOffR + st * C::kCodes : C::kOffV + st * C::kTile);
+            uint8_t* sc = smem + (is_v ? C::kOffVScale : C::kOffKScale) + st * 128;
             if (!is_v && lane == 0) misc.gone[(block0 + b) & 15] = (uint8_t)(~there & ((1u << ng) - 1));
             if (there != (1u << ng) - 1) {   // groups without a page hold zeros
                 for (int i = 0; i < ng; ++i) {
@@ -179,7 +192,7 @@ __device__ __forceinline__ void load_tiles(const AttnArgs& a, uint8_t* smem, uin
                 fence_proxy_async_smem();
                 __syncwarp();
             }
-            if (lane == 0) mbar_arrive_expect_tx(&bars[kFullBar + st], kGroupBytes * __popc(there));
+            if (lane == 0) mbar_arrive_expect_tx(full, kGroupBytes * __popc(there));
             __syncwarp();
             const int i = lane & 7, hf = lane >> 3;
             if ((there >> i & 1) && hf < (FP8 ? 1 : C::kHalves)) {
@@ -187,21 +200,27 @@ __device__ __forceinline__ void load_tiles(const AttnArgs& a, uint8_t* smem, uin
                 const int64_t blk = (int64_t)p * a.c.heads + g.h;
                 const uint8_t* src = (is_v ? a.c.v : a.c.k) + blk * a.c.block;
                 if constexpr (FP8) {
-                    bulk_load(&bars[kFullBar + st], dst + i * 16 * D, src + e0 * D, 16 * D);
-                    bulk_load(&bars[kFullBar + st], sc + 16 * i, (is_v ? a.c.vs : a.c.ks) + (blk << a.c.page_log) + e0, 16);
+                    bulk_load(full, dst + i * 16 * D, src + e0 * D, 16 * D);
+                    bulk_load(full, sc + 16 * i, (is_v ? a.c.vs : a.c.ks) + (blk << a.c.page_log) + e0, 16);
                 } else {
-                    bulk_load(&bars[kFullBar + st], dst + hf * kHalfBytes + i * 2048,
-                              src + (((int64_t)hf << a.c.page_log) + e0) * 128, 2048);
+                    bulk_load(full, dst + hf * kHalfBytes + i * 2048, src + (((int64_t)hf << a.c.page_log) + e0) * 128, 2048);
                 }
             }
-            ++c;
+            if (is_v) {
+                rv.next();
+                ++nv;
+            } else {
+                rk.next();
+                ++nk;
+            }
             return true;
         });
         block0 += (uint32_t)w.nb;
         if (!ok) break;
     }
     // never leave the CTA with a copy still in flight
-    for (uint32_t i = c > (uint32_t)N ? c - N : 0; i < c; ++i) mbar_wait_teardown(&bars[kFullBar + i % N], (i / N) & 1);
+    for (uint32_t i = nk > (uint32_t)C::kK ? nk - C::kK : 0; i < nk; ++i) mbar_wait_teardown(&bars[C::kKFull + i % C::kK], (i / C::kK) & 1);
+    for (uint32_t i = nv > (uint32_t)NV ? nv - NV : 0; i < nv; ++i) mbar_wait_teardown(&bars[kVFullBar + i % NV], (i / NV) & 1);
 }
 
 // 8 codes (8 bytes) to 8 bf16 values: m is 2^(e + 120), m2 a second factor.
@@ -225,29 +244,48 @@ __device__ __forceinline__ void work_tiles(const AttnArgs& a, uint8_t* smem, uin
                                            const Abort& ab) {
     using C = Cfg<D, FP8>;
     const int lane = threadIdx.x & 31, who = threadIdx.x - 64;
-    uint32_t c = 0;
+    RingAt<C::kK> rk;
+    RingAt<C::kV> rv;
+    RingAt<FP8 ? C::kR : 1> rr;
+    uint32_t block0 = 0;
     while (sh.u < sh.u_end) {
         const Segment g = next_segment(a, sh);
         if (g.rows == 0) break;
         const Walk w(a, g);
         const bool ok = w.tiles([&](int b, bool is_v) {
-            const uint32_t st = c % C::kStages, ph = (c / C::kStages) & 1;
             const int ng = w.groups(g, b);
-            if (!__all_sync(0xffffffffu, mbar_wait<true>(&bars[C::kEmpty + st], ph ^ 1, ab, 67))) return false;
-            uint8_t* dst = smem + C::kOffKV + st * C::kTile;
-            const bool clean = is_v && w.masked(g, b);
+            if (!is_v) {
+                if constexpr (FP8) {
+                    if (!__all_sync(0xffffffffu, mbar_wait<true>(&bars[C::kKFull + rk.st], rk.ph, ab, 76))) return false;
+                    if (who < 128)
+                        reinterpret_cast<float*>(smem + C::kOffScale)[((block0 + b) & 7) * 128 + who] = cache_scale(smem[C::kOffKScale + rk.st * 128 + who]);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[C::kKReady + rk.st]);
+                    rk.next();
+                }
+                return true;
+            }
+            if (!__all_sync(0xffffffffu, mbar_wait<true>(&bars[C::kVEmpty + rv.st], rv.ph ^ 1, ab, 67))) return false;
+            uint8_t* dst = smem + C::kOffV + rv.st * C::kTile;
+            const bool clean = w.masked(g, b);
             bool odd = false;
             if constexpr (FP8) {
-                const uint32_t rs = c % C::kRaw;
-                if (!__all_sync(0xffffffffu, mbar_wait<true>(&bars[C::kRawFull + rs], (c / C::kRaw) & 1, ab, 69))) return false;
-                const uint8_t* src = smem + C::kOffRaw + rs * C::kRawTile;
-                const uint8_t* sc = smem + C::kOffScale + rs * 128;
-                constexpr int kChunks = D / 16;
+                if (!__all_sync(0xffffffffu, mbar_wait<true>(&bars[C::kRFull + rr.st], rr.ph, ab, 69))) return false;
+                const uint8_t* src = smem + C::kOffR + rr.st * C::kCodes;
+                const uint8_t* sc = smem + C::kOffVScale + rr.st * 128;
+                // a thread takes the same piece of every kRows-th row, where the
+                // swizzle is the same: one address that moves
+                constexpr int kChunks = D / 16, kRows = 32 * C::kWorkers / kChunks;
+                static_assert(kRows % 8 == 0, "rows of the same swizzle");
+                const int ch = who % kChunks, e1 = 16 * ng;
+                int e = who / kChunks;
+                src += cache_chunk(D, 7, e, ch);
+                uint8_t* lo = dst + (ch >> 2) * kHalfBytes + e * 128 + (((2 * ch) & 7) ^ (e & 7)) * 16;
+                uint8_t* hi = dst + (ch >> 2) * kHalfBytes + e * 128 + (((2 * ch + 1) & 7) ^ (e & 7)) * 16;
 #pragma unroll 2
-                for (int x = who; x < 16 * ng * kChunks; x += 32 * C::kWorkers) {
-                    const int e = x / kChunks, ch = x % kChunks;
-                    const uint4 q = *reinterpret_cast<const uint4*>(src + cache_chunk(D, 7, e, ch));
-                    uint32_t s = sc[e];
+                for (; e < e1; e += kRows, src += kRows * D, lo += kRows * 128, hi += kRows * 128) {
+                    const uint4 q = *reinterpret_cast<const uint4*>(src);
+                    const uint32_t s = sc[e];
                     uint32_t m = (s + 120u) << 7, m2 = 0;
                     if (s > 134u) {      // 2^(e + 120) passes bf16's range
                         m = 254u << 7;
@@ -262,13 +300,12 @@ __device__ __forceinline__ void work_tiles(const AttnArgs& a, uint8_t* smem, uin
                     // events behind the last one: whatever their memory holds
                     if (clean && segment_group(g, 8 * b + (e >> 4)) * kCacheGroup + (e & 15) >= g.s.end) m = m2 = 0;
                     m |= m << 16;
-                    uint8_t* row = dst + (ch >> 2) * kHalfBytes + e * 128;
-                    *reinterpret_cast<uint4*>(row + (((2 * ch) & 7) ^ (e & 7)) * 16) = expand8(q.x, q.y, m, m2);
-                    *reinterpret_cast<uint4*>(row + (((2 * ch + 1) & 7) ^ (e & 7)) * 16) = expand8(q.z, q.w, m, m2);
+                    *reinterpret_cast<uint4*>(lo) = expand8(q.x, q.y, m, m2);
+                    *reinterpret_cast<uint4*>(hi) = expand8(q.z, q.w, m, m2);
                 }
                 fence_proxy_async_smem();
             } else if (clean) {
-                if (!__all_sync(0xffffffffu, mbar_wait<true>(&bars[C::kFull + st], ph, ab, 69))) return false;
+                if (!__all_sync(0xffffffffu, mbar_wait<true>(&bars[C::kVFull + rv.st], rv.ph, ab, 69))) return false;
                 for (int x = who; x < 16 * ng * (D / 8); x += 32 * C::kWorkers) {
                     uint4* at = reinterpret_cast<uint4*>(dst + (x & 7) * 16 + ((x >> 3) % (16 * ng)) * 128 + ((x >> 3) / (16 * ng)) * kHalfBytes);
                     uint4 v = *at;
@@ -290,50 +327,93 @@ __device__ __forceinline__ void work_tiles(const AttnArgs& a, uint8_t* smem, uin
             if (odd) misc.dirty = 1;
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&bars[(FP8 ? C::kFull : C::kReady) + st]);
-                if constexpr (FP8) mbar_arrive(&bars[C::kRawEmpty + c % C::kRaw]);
+                mbar_arrive(&bars[C::kVReady + rv.st]);
+                if constexpr (FP8) mbar_arrive(&bars[C::kREmpty + rr.st]);
             }
-            ++c;
+            rv.next();
+            rr.next();
             return true;
         });
+        block0 += (uint32_t)w.nb;
         if (!ok) return;
     }
 }
 
-// The issuer of one segment (one lane).  State that goes on between segments.
-template <int STAGES>
+__device__ __forceinline__ void one_mma_ss_8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// K-major tiles of 8-bit rows: D bytes a row (128: 128-byte swizzle, 64: 64-byte).
+template <int D>
+__device__ __forceinline__ uint64_t codes_desc(uint32_t saddr) {
+    uint64_t d = smem_desc_sw128(saddr, 16, 8 * D);
+    if constexpr (D == 64) d ^= (uint64_t)(2 ^ 4) << 61;   // swizzle mode 4
+    return d;
+}
+// Instruction descriptor of kind::f8f6f4 with A of E4M3 (format 0) or E5M2 (1), B
+// of E4M3, fp32 D; the rest as idesc_bf16.
+constexpr uint32_t kRestE5m2 = 1u << 7;
+__host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N) {
+    return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// The issuer (one lane).  State that goes on between segments.
+template <int D, bool FP8>
 struct Issuer {
-    RingAt<STAGES> ring;
+    RingAt<Cfg<D, FP8>::kK> rk;
+    RingAt<Cfg<D, FP8>::kV> rv;
     uint32_t p_ph[2] = {0, 0}, o_ph[2] = {1, 1}, q_ph = 0;
 };
 
 template <int D, bool FP8>
-__device__ __forceinline__ bool issue_segment(Issuer<Cfg<D, FP8>::kStages>& z, const Segment& g, const Walk& w,
-                                              uint8_t* smem, uint64_t* bars, uint32_t tmem, const Abort& ab) {
+__device__ __forceinline__ bool issue_segment(Issuer<D, FP8>& z, const Segment& g, const Walk& w, uint8_t* smem,
+                                              uint64_t* bars, uint32_t tmem, const Abort& ab) {
     using C = Cfg<D, FP8>;
     constexpr uint32_t idesc_pv = idesc_bf16(128, D, false, true);
-    constexpr uint32_t idesc_full = idesc_bf16(128, 128, false, false);
-    constexpr uint64_t kStageDesc = C::kTile >> 4;
-    const uint64_t q_desc = smem_desc_sw128(smem_u32(smem), 16, 1024);
-    const uint64_t k_desc = smem_desc_sw128(smem_u32(smem + C::kOffKV), 16, 1024);
-    const uint64_t v_desc = smem_desc_sw128(smem_u32(smem + C::kOffKV), kHalfBytes, 1024);
+    constexpr uint64_t kKDesc = C::kKTile >> 4, kVDesc = C::kTile >> 4;
+    const uint64_t q_desc = FP8 ? codes_desc<D>(smem_u32(smem)) : smem_desc_sw128(smem_u32(smem), 16, 1024);
+    const uint64_t k_desc = FP8 ? codes_desc<D>(smem_u32(smem + C::kOffK)) : smem_desc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
+    const uint64_t v_desc = smem_desc_sw128(smem_u32(smem + C::kOffV), kHalfBytes, 1024);
     const int nb = w.nb;
     const uint32_t last_keys = (uint32_t)(16 * w.groups(g, nb - 1));
-    const uint32_t idesc_last = idesc_bf16(128, last_keys, false, false);
-    const uint64_t q2 = q_desc + (w.dual ? 0 : kStageDesc);
-    auto full = [&](bool is_v) -> bool {
-        if (!mbar_wait<true>(&bars[C::kFull + z.ring.st], z.ring.ph, ab, 64)) return false;
-        if (!FP8 && is_v && !mbar_wait<true>(&bars[C::kReady + z.ring.st], z.ring.ph, ab, 70)) return false;
+    const uint32_t idesc_full = FP8 ? idesc_e4m3(128, 128) : idesc_bf16(128, 128, false, false);
+    const uint32_t idesc_last = FP8 ? idesc_e4m3(128, last_keys) : idesc_bf16(128, last_keys, false, false);
+    const uint64_t q2 = q_desc + (w.dual ? 0 : (uint64_t)(C::kTile >> 4));
+    auto keys = [&]() -> bool {
+        if (!mbar_wait<true>(&bars[C::kKFull + z.rk.st], z.rk.ph, ab, 64)) return false;
+        if (FP8 && !mbar_wait<true>(&bars[C::kKReady + z.rk.st], z.rk.ph, ab, 70)) return false;
+        tc_fence_after();
+        return true;
+    };
+    auto values = [&]() -> bool {
+        if (!FP8 && !mbar_wait<true>(&bars[C::kVFull + z.rv.st], z.rv.ph, ab, 64)) return false;
+        if (!mbar_wait<true>(&bars[C::kVReady + z.rv.st], z.rv.ph, ab, 70)) return false;
         tc_fence_after();
         return true;
     };
     auto scores = [&](int s, int b) {
-        one_scores<D>(tmem + s * 128, s ? q2 : q_desc, k_desc + z.ring.st * kStageDesc, b == nb - 1 ? idesc_last : idesc_full);
+        const uint64_t q = s ? q2 : q_desc, k = k_desc + z.rk.st * kKDesc;
+        const uint32_t id = b == nb - 1 ? idesc_last : idesc_full;
+        if constexpr (FP8) {   // both parts of the queries, 32 columns a step
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i)
+                    one_mma_ss_8(tmem + s * 128, q + part * (C::kCodes >> 4) + 2 * i, k + 2 * i,
+                                 id | (part ? kRestE5m2 : 0), part + i > 0);
+        } else {
+            one_scores<D>(tmem + s * 128, q, k, id);
+        }
         one_commit(&bars[C::kSFull + s]);
     };
     auto sums = [&](int s, int b, bool first) -> bool {
         const uint32_t sc = tmem + s * 128, oc = tmem + 256 + s * 128;
-        const uint64_t vd = v_desc + z.ring.st * kStageDesc;
+        const uint64_t vd = v_desc + z.rv.st * kVDesc;
         if (first) {   // the slot's sums of its last segment have been read
             if (!mbar_wait<true>(&bars[C::kOFree + s], z.o_ph[s], ab, 65)) return false;
             z.o_ph[s] ^= 1;
@@ -351,32 +431,28 @@ __device__ __forceinline__ bool issue_segment(Issuer<Cfg<D, FP8>::kStages>& z, c
         return true;
     };
     if (!mbar_wait<true>(&bars[C::kQFull], z.q_ph, ab, 63)) return false;
+    tc_fence_after();
     z.q_ph ^= 1;
     if (!w.dual) {
+        // both slots: S(b + 1) follows each slot's P V(b)
         for (int b = -1; b < nb; ++b) {
-            const RingAt<C::kStages> v = z.ring;   // V of block b, then K of block b + 1
-            if (b >= 0) {
-                if (!full(true) || !sums(0, b, b == 0)) return false;
-                z.ring.next();
-            }
+            if (b >= 0 && (!values() || !sums(0, b, b == 0))) return false;
             if (b + 1 < nb) {
-                if (!full(false)) return false;
+                if (!keys()) return false;
                 scores(0, b + 1);
             } else {
                 one_commit(&bars[C::kOFull]);
             }
-            const RingAt<C::kStages> k = z.ring;
             if (b >= 0) {
-                z.ring = v;
                 if (!sums(1, b, b == 0)) return false;
-                one_commit(&bars[C::kEmpty + v.st]);
-                z.ring = k;
+                one_commit(&bars[C::kVEmpty + z.rv.st]);
+                z.rv.next();
             }
             if (b + 1 < nb) {
                 scores(1, b + 1);
-                one_commit(&bars[C::kEmpty + z.ring.st]);
+                one_commit(&bars[C::kKEmpty + z.rk.st]);
+                z.rk.next();
                 if (b + 2 == nb) one_commit(&bars[C::kQEmpty]);   // the queries may be replaced
-                z.ring.next();
             } else {
                 one_commit(&bars[C::kOFull + 1]);
             }
@@ -385,16 +461,16 @@ __device__ __forceinline__ bool issue_segment(Issuer<Cfg<D, FP8>::kStages>& z, c
         for (int b = -2; b < nb; ++b) {
             const int s = b & 1;
             if (b >= 0) {
-                if (!full(true) || !sums(s, b, b < 2)) return false;
-                one_commit(&bars[C::kEmpty + z.ring.st]);
-                z.ring.next();
+                if (!values() || !sums(s, b, b < 2)) return false;
+                one_commit(&bars[C::kVEmpty + z.rv.st]);
+                z.rv.next();
                 if (b + 2 >= nb) one_commit(&bars[C::kOFull + s]);
             }
             if (b + 2 < nb) {
-                if (!full(false)) return false;
+                if (!keys()) return false;
                 scores(s, b + 2);
-                one_commit(&bars[C::kEmpty + z.ring.st]);
-                z.ring.next();
+                one_commit(&bars[C::kKEmpty + z.rk.st]);
+                z.rk.next();
                 if (b + 3 == nb) one_commit(&bars[C::kQEmpty]);
             }
         }
@@ -431,6 +507,44 @@ __device__ __noinline__ void add_odd(const AttnArgs& a, const Segment& g, const 
     }
 }
 
+// The unit of a row's codes (read again by the slot that does not write them).
+template <int D>
+__device__ __forceinline__ float query_unit(const AttnArgs& a, const Segment& g, const RowView& rv, int r) {
+    if (rv.tok < 0) return 1.0f;
+    const __nv_bfloat16* src = (const __nv_bfloat16*)a.q + (g.s.t0 + rv.tok) * a.qt + (g.h * a.G + g.rho0 + r - rv.tok * a.G) * a.qh;
+    float top = 0.0f;
+    if (a.q_wide) {
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + c);
+            const uint32_t p[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(bf16_lo(p[i])), fabsf(bf16_hi(p[i]))));
+        }
+    } else {
+        for (int c = 0; c < D; ++c) top = fmaxf(top, fabsf(__bfloat162float(src[c])));
+    }
+    return 0x1p-7f / inverse_power(top);
+}
+
+// row_bits of the 8 groups of a block.  (Out of line: the instruction cache holds
+// little more than the loop that is to go on.)
+static __device__ __noinline__ uint4 block_bits(const AttnArgs& a, const Segment& g, const RowView& v, int i) {
+    uint4 r;
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
+        uint32_t bits = 0;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h)
+            if (i + 2 * q + h < g.n) bits |= row_bits(a, g, v, segment_group(g, i + 2 * q + h) * kCacheGroup) << (16 * h);
+        if (q == 0) r.x = bits;
+        else if (q == 1) r.y = bits;
+        else if (q == 2) r.z = bits;
+        else r.w = bits;
+    }
+    return r;
+}
+
 template <int D, bool FP8, int ACT>
 __device__ __forceinline__ void tile_rows(const AttnArgs& a, uint8_t* smem, uint64_t* bars, Misc& misc, uint32_t tmem,
                                           Share sh, const Abort& ab) {
@@ -445,11 +559,15 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& a, uint8_t* smem, uint
     const uint32_t sc = trow + s * 128, oc = trow + 256 + s * 128;
     float2* ml1 = reinterpret_cast<float2*>(smem + C::kOffMl);
     const bool flip = kSm && a.alpha < 0.0f;
-    ActScale ks = act_scale<ACT>(a.alpha);
-    if (kSm) {   // (a zero scale would make NaN of masked scores)
-        ks.c0 = fabsf(ks.c0);
-        if (ks.c0 < 1e-30f) ks.c0 = 1e-30f;
-    }
+    const auto scale_of = [&](float alpha) {
+        ActScale k = act_scale<ACT>(alpha);
+        if (kSm) {   // (a zero scale would make NaN of masked scores)
+            k.c0 = fabsf(k.c0);
+            if (k.c0 < 1e-30f) k.c0 = 1e-30f;
+        }
+        return k;
+    };
+    ActScale ks = scale_of(a.alpha);
     uint32_t items = 0, used[2] = {0, 0}, duals = 0, q_ph = 1, block0 = 0;
     while (sh.u < sh.u_end) {
         const Segment g = next_segment(a, sh);
@@ -459,57 +577,112 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& a, uint8_t* smem, uint
         const int r = (w.dual ? 0 : 128 * s) + row;      // of the tile
         const bool real = r < g.rows;
         const RowView rv = row_view(a, g, r);
+        float q_unit = 1.0f;   // 8-bit: what the codes' scores are to be multiplied by
         if (w.nb > 0) {
             // queries, a row a thread
             if (!wg_wait<true>(&bars[C::kQEmpty], q_ph, ab, 61)) return;
             q_ph ^= 1;
             if (!(w.dual && s)) {
-                uint8_t* dst = smem + (w.dual ? 0 : s) * C::kTile + row * 128;
+                uint8_t* dst = smem + (w.dual ? 0 : s) * C::kTile;
                 const int tok = max(rv.tok, 0);
                 const __nv_bfloat16* src = (const __nv_bfloat16*)a.q + (g.s.t0 + tok) * a.qt + (g.h * a.G + g.rho0 + r - tok * a.G) * a.qh;
+                uint4 q[D / 8];
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
+                    q[c] = make_uint4(0, 0, 0, 0);
                     if (real) {
                         if (a.q_wide) {
-                            v = __ldg(reinterpret_cast<const uint4*>(src) + c);
+                            q[c] = __ldg(reinterpret_cast<const uint4*>(src) + c);
                         } else {
                             const uint16_t* h = reinterpret_cast<const uint16_t*>(src) + 8 * c;
-                            uint32_t* p = &v.x;
+                            uint32_t* p = &q[c].x;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) p[i] = h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
                         }
                     }
-                    *reinterpret_cast<uint4*>(dst + (c >> 3) * kHalfBytes + (((c & 7) ^ (row & 7)) << 4)) = v;
+                }
+                if constexpr (FP8) {
+                    float top = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) {
+                        const uint32_t* p = &q[c].x;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(bf16_lo(p[i])), fabsf(bf16_hi(p[i]))));
+                    }
+                    const float f = inverse_power(top);   // of infinities: whatever, their products are
+                    q_unit = 0x1p-7f / f;
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) {    // 16 columns: a piece of codes, and of what they leave
+                        uint4 hi, lo;
+                        uint32_t *h = &hi.x, *l = &lo.x;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4& v = q[2 * c + (i >> 1)];
+                            const uint32_t p0 = i & 1 ? v.z : v.x, p1 = i & 1 ? v.w : v.y;
+                            uint32_t h0, h1, l0, l1;
+                            split_q<false>(bf16_lo(p0) * f * 128.0f, bf16_hi(p0) * f * 128.0f, h0, l0);
+                            split_q<false>(bf16_lo(p1) * f * 128.0f, bf16_hi(p1) * f * 128.0f, h1, l1);
+                            h[i] = h0 | h1 << 16;
+                            l[i] = l0 | l1 << 16;
+                        }
+                        const int at = cache_chunk(D, 7, row, c);
+                        *reinterpret_cast<uint4*>(dst + at) = hi;
+                        *reinterpret_cast<uint4*>(dst + C::kCodes + at) = lo;
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c)
+                        *reinterpret_cast<uint4*>(dst + row * 128 + (c >> 3) * kHalfBytes + (((c & 7) ^ (row & 7)) << 4)) = q[c];
                 }
                 fence_proxy_async_smem();
             }
             mbar_arrive(&bars[C::kQFull]);
+            if constexpr (FP8) {
+                // both slots of the same rows score them in the same unit
+                if (w.dual && s) q_unit = query_unit<D>(a, g, rv, r);
+                ks = scale_of(a.alpha * q_unit);
+            }
         }
         float ref = -INFINITY, sum = 0.0f;
         for (int j = 0; j < n; ++j) {
             const int b = w.block(s, j);
+            // what the row sees of the block, made while its scores are
+            const bool masked = w.groups(g, b) < 8 || w.masked(g, b);
+            uint4 vis = make_uint4(~0u, ~0u, ~0u, ~0u);
+            if (masked) vis = block_bits(a, g, rv, 8 * b);
             if (!wg_wait<true>(&bars[C::kSFull + s], (items + j) & 1, ab, 71)) return;
             tc_fence_after();
             uint32_t x[128];
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld32(sc + c * 32, *reinterpret_cast<uint32_t(*)[32]>(x + c * 32));
             tmem_ld_wait();
+            if constexpr (FP8) {   // the keys' powers of two
+                const float4* p = reinterpret_cast<const float4*>(smem + C::kOffScale) + ((block0 + b) & 7) * 32;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const float4 y = p[e];
+                    const float2 u = f2_split(f2_mul(f2_make(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1])), f2_make(y.x, y.y)));
+                    const float2 v = f2_split(f2_mul(f2_make(__uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3])), f2_make(y.z, y.w)));
+                    x[4 * e] = __float_as_uint(u.x);
+                    x[4 * e + 1] = __float_as_uint(u.y);
+                    x[4 * e + 2] = __float_as_uint(v.x);
+                    x[4 * e + 3] = __float_as_uint(v.y);
+                }
+            }
             if (flip) {
 #pragma unroll
                 for (int e = 0; e < 128; ++e) x[e] ^= 0x80000000u;
             }
             const uint32_t gone = *reinterpret_cast<volatile uint8_t*>(&misc.gone[(block0 + b) & 15]);
-            const int ng = w.groups(g, b);
-            const bool cut = ng < 8 || gone || w.masked(g, b);
+            const bool cut = masked || gone;
             if (cut) {
+                const uint32_t bits[4] = {vis.x, vis.y, vis.z, vis.w};
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
-                    uint32_t bits = 0;
-                    if (q < ng && !(gone >> q & 1u)) bits = row_bits(a, g, rv, segment_group(g, 8 * b + q) * kCacheGroup);
+                    const uint32_t see = gone >> q & 1u ? 0u : bits[q >> 1] >> (16 * (q & 1));
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
-                        if (!(bits >> e & 1u)) x[16 * q + e] = 0xff800000u;   // -inf
+                        if (!(see >> e & 1u)) x[16 * q + e] = 0xff800000u;   // -inf
                 }
             }
             if constexpr (kSm) {
@@ -558,7 +731,7 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& a, uint8_t* smem, uint
                         if constexpr (kSm) {
                             const float2 tt = f2_split(
                                 f2_fma(f2_make(s0, s1), f2_make(ks.c0, ks.c0), f2_make(nref, nref)));
-                            if (e % 6 == 4) {   // one pair of three
+                            if (!FP8 && e % 6 == 4) {   // one pair of three (8-bit: issue slots are scarcer)
                                 const float2 y = exp2_poly(tt);
                                 p0 = y.x;
                                 p1 = y.y;
@@ -702,9 +875,7 @@ cache_tc_kernel(const __grid_constant__ AttnArgs a) {
             uint32_t n = 1;
             if (b == C::kQFull) n = 256;
             if (b == C::kDual || (b >= C::kPFull && b < C::kPFull + 4) || (b >= C::kOFree && b < C::kOFree + 2)) n = 128;
-            if ((FP8 && b >= C::kFull && b < C::kFull + C::kStages) || (b >= C::kReady && b < C::kReady + C::kStages) ||
-                (b >= C::kRawEmpty && b < C::kRawEmpty + C::kRaw))
-                n = C::kWorkers;
+            if ((b >= C::kKReady && b < C::kKEmpty) || (b >= C::kVReady && b < C::kVEmpty) || b >= C::kREmpty) n = C::kWorkers;
             mbar_init(&bars[b], n);
         }
         misc.abort_flag = 0;
@@ -725,7 +896,7 @@ cache_tc_kernel(const __grid_constant__ AttnArgs a) {
         if (warp == 0) {
             load_tiles<D, FP8>(a, smem, bars, misc, sh, ab);
         } else if (warp == 1) {
-            Issuer<C::kStages> z;
+            Issuer<D, FP8> z;
             Share mine = sh;
             bool ok = true;
             while (mine.u < mine.u_end && ok) {
