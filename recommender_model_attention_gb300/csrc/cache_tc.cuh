@@ -12,15 +12,14 @@
 //                       and slot 0's threads join the two at the end.
 // One warp loads: each group of 16 events is a plain bulk copy (the cache holds
 // rows in the operands' swizzle), its page looked up 32 groups ahead.  One lane
-// issues S = Q K^T and O += P V; the order of loads and products, the lazily
-// moved reference and the exponentials in multiply-adds are shared-prefix
-// attention's (prefix_tc_fwd.cu says why).
+// issues S = Q K^T and O += P V; the order of loads and products and the lazily
+// moved reference are shared-prefix attention's (prefix_tc_fwd.cu says why).
 //
 // 8-bit caches.  Keys are multiplied as they are (kind::f8f6f4): a query row,
 // scaled by a power of two to below 256, is split into E4M3 codes and E5M2 codes
 // of what they leave, at most 8 units of bf16's last place, which 3 bits hold
 // (elements below 2^-13 of the largest lose bits, at most 2^-21 of it): two
-// products of double rate; the keys' powers of two are applied to the scores.  Values are expanded to bf16 by six worker warps, exactly
+// products of double rate; the keys' powers of two are applied to the scores.  Values are expanded to bf16 by the worker warps, exactly
 // (a code has 4 bits): its 7 bits behind the sign moved to bf16's place are the
 // value times 2^-120, subnormal codes included, and one bf16 product by 2^(e +
 // 120) (two where that leaves bf16's range) gives it.  (Keys expanded as well:
@@ -44,42 +43,6 @@ constexpr int kHalfBytes = 128 * 128;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRise = 8.0f;   // the reference follows a maximum this far above it
 
-template <int D, bool FP8>
-struct Cfg {
-    static constexpr int kHalves = D / 64;
-    static constexpr int kTile = 128 * D * 2;                // 128 rows in bf16
-    static constexpr int kCodes = 128 * D;                   // ... in 8 bits
-    static constexpr int kKTile = FP8 ? kCodes : kTile;
-    static constexpr int kK = FP8 ? (D == 128 ? 3 : 4) : (D == 128 ? 3 : 4);   // stages: keys
-    static constexpr int kV = D == 128 ? 2 : 4;                                // values in bf16
-    static constexpr int kR = FP8 ? (D == 128 ? 2 : 3) : 0;                    // values in 8 bits
-    static constexpr int kWorkers = FP8 ? 6 : 2;             // warps
-    static constexpr int kRows0 = 2 + kWorkers;              // first row warp
-    static constexpr int kThreads = 32 * (kRows0 + 8);
-    static constexpr int kOffK = 2 * kTile;                  // behind two tiles of queries (8-bit: each as two)
-    static constexpr int kOffV = kOffK + kK * kKTile;
-    static constexpr int kOffR = kOffV + kV * kTile;
-    static constexpr int kOffKScale = kOffR + kR * kCodes;   // bytes of the K stages, of the 8-bit V stages
-    static constexpr int kOffVScale = kOffKScale + (FP8 ? kK * 128 : 0);
-    static constexpr int kOffScale = kOffVScale + kR * 128;  // powers of two of the last 8 blocks' keys
-    static constexpr int kOffMl = kOffScale + (FP8 ? 8 * 512 : 0);
-    static constexpr int kOffScan = kOffMl + 128 * 8;
-    static constexpr int kOffBar = kOffScan + (kThreads / 32 + 2) * 8;
-    enum {
-        kQFull = 0, kQEmpty, kDual, kMmaDone, kSFull, kPFull = kSFull + 2, kOFull = kPFull + 4, kOFree = kOFull + 2,
-        kKFull = kOFree + 2,             // keys have landed
-        kKReady = kKFull + kK,           // 8-bit: their powers of two are in place
-        kKEmpty = kKReady + kK,
-        kVFull = kKEmpty + kK,           // bf16: values have landed
-        kVReady = kVFull + kV,           // workers have cleaned or expanded them
-        kVEmpty = kVReady + kV,
-        kRFull = kVEmpty + kV, kREmpty = kRFull + kR, kNumBars = kREmpty + kR
-    };
-    static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // Misc
-    static constexpr int kSmem = kOffMisc + 32 + 1024;
-    static_assert(kSmem <= 232448, "shared memory");
-};
-
 struct Misc {
     uint32_t tmem;
     int abort_flag;
@@ -89,25 +52,26 @@ struct Misc {
 
 // Blocks of a segment, as both slots take them, and which are masked.
 struct Walk {
-    int nb, n0, n1, hi_min, lo_max;
+    int nb, n1, n;
+    int open0, open1;   // blocks of which every row sees everything
     bool dual;
-    __device__ __forceinline__ Walk(const AttnArgs& a, const Segment& g) {
-        nb = (g.n + 7) >> 3;
+    __device__ __forceinline__ void set(const AttnArgs& a, const Segment& g) {
+        n = g.n;
+        nb = (n + 7) >> 3;
         dual = g.rows <= 128;
-        n0 = dual ? (nb + 1) >> 1 : nb;
         n1 = dual ? nb >> 1 : nb;
         const int i0 = g.rho0 / a.G, i1 = (g.rho0 + g.rows - 1) / a.G;
-        hi_min = min(g.s.end, g.s.start + (a.mask == GDPA_CACHE_CAUSAL ? i0 + 1 : 0));
-        lo_max = a.window > 0 ? g.s.start + (a.mask == GDPA_CACHE_HISTORY ? 0 : i1) - a.window + 1 : 0;
+        // events below hi that are at or above lo are seen by all rows
+        const int hi = min(g.s.end, g.s.start + (a.mask == GDPA_CACHE_CAUSAL ? i0 + 1 : 0));
+        const int lo = a.window > 0 ? max(0, g.s.start + (a.mask == GDPA_CACHE_HISTORY ? 0 : i1) - a.window + 1) : 0;
+        // in groups of the segment, behind the sinks
+        const int from = max(g.na, (lo + 15) / 16 - g.b0), to = min(n, hi / 16 - g.b0);
+        open0 = (from + 7) >> 3;
+        open1 = to >> 3;
     }
-    __device__ __forceinline__ int blocks(int s) const { return s ? n1 : n0; }
-    __device__ __forceinline__ int block(int s, int j) const { return dual ? 2 * j + s : j; }
-    __device__ __forceinline__ int groups(const Segment& g, int b) const { return min(8, g.n - 8 * b); }
-    __device__ __forceinline__ bool masked(const Segment& g, int b) const {
-        const int first = segment_group(g, 8 * b) * kCacheGroup;
-        const int last = segment_group(g, 8 * b + groups(g, b) - 1) * kCacheGroup + kCacheGroup - 1;
-        return last >= hi_min || first < lo_max;
-    }
+    __device__ __forceinline__ int blocks(int s) const { return s ? n1 : dual ? nb - n1 : nb; }
+    __device__ __forceinline__ int groups(int b) const { return min(8, n - 8 * b); }
+    __device__ __forceinline__ bool masked(int b) const { return b < open0 || b >= open1; }
     // the tiles in the order of the ring: f(block, is V) until it returns false.
     // more than 128 rows: K0 V0 K1 V1 ...; else: K0 K1 V0 K2 V1 K3 ...
     template <typename F>
@@ -125,6 +89,73 @@ struct Walk {
     }
 };
 
+// A warp's place in the work, in shared memory: in registers it would be spilled,
+// and with this much shared memory taken local memory is as far as L2 (the row
+// threads' 250 instructions a block took 6000 cycles).
+struct Place {
+    Share sh;
+    Segment g;
+    Walk w;
+};
+
+// The next segment; false: no more.  (Whole warps.)
+__device__ __forceinline__ bool advance(const AttnArgs& a, Place& p) {
+    Share sh = p.sh;
+    Segment g;
+    g.rows = 0;
+    if (sh.u < sh.u_end) g = next_segment(a, sh);
+    Walk w;
+    if (g.rows > 0) w.set(a, g);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+        p.sh = sh;
+        p.g = g;
+        p.w = w;
+    }
+    __syncwarp();
+    return g.rows > 0;
+}
+
+template <int D, bool FP8>
+struct Cfg {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kTile = 128 * D * 2;                // 128 rows in bf16
+    static constexpr int kCodes = 128 * D;                   // ... in 8 bits
+    static constexpr int kKTile = FP8 ? kCodes : kTile;
+    static constexpr int kK = D == 128 ? 3 : 4;                                // stages: keys
+    static constexpr int kV = D == 128 ? 2 : 4;                                // values in bf16
+    static constexpr int kR = FP8 ? (D == 128 ? 2 : 3) : 0;                    // values in 8 bits
+    static constexpr int kWorkers = FP8 ? 6 : 2;             // warps
+    static constexpr int kRows0 = 2 + kWorkers;              // first row warp
+    static constexpr int kThreads = 32 * (kRows0 + 8);
+    static constexpr int kOffK = 2 * kTile;                  // behind two tiles of queries (8-bit: each as two)
+    static constexpr int kOffV = kOffK + kK * kKTile;
+    static constexpr int kOffR = kOffV + kV * kTile;
+    static constexpr int kOffKScale = kOffR + kR * kCodes;   // bytes of the K stages, of the 8-bit V stages
+    static constexpr int kOffVScale = kOffKScale + (FP8 ? kK * 128 : 0);
+    static constexpr int kOffScale = kOffVScale + kR * 128;  // powers of two of the last 8 blocks' keys
+    static constexpr int kOffUnit = kOffScale + (FP8 ? 8 * 512 : 0);   // 8-bit: units of the tile's rows
+    static constexpr int kOffFin = kOffUnit + (FP8 ? 256 * 4 : 0);
+    static constexpr bool kStageApart = FP8 && D == 64;
+    static constexpr int kOffStage = kOffFin + 128 * 8;
+    static constexpr int kOffPlace = kOffStage + (kStageApart ? 8 * 4096 : 0);
+    static constexpr int kOffScan = kOffPlace;               // (used before the places are)
+    static constexpr int kOffBar = (kOffPlace + (int)sizeof(Place) * (kThreads / 32) + 15) & ~15;
+    enum {
+        kQFull = 0, kQEmpty, kFin, kMmaDone, kSFull, kPFull = kSFull + 2, kOFull = kPFull + 2, kOFree = kOFull + 2,
+        kKFull = kOFree + 2,             // keys have landed
+        kKReady = kKFull + kK,           // 8-bit: their powers of two are in place
+        kKEmpty = kKReady + kK,
+        kVFull = kKEmpty + kK,           // bf16: values have landed
+        kVReady = kVFull + kV,           // workers have cleaned or expanded them
+        kVEmpty = kVReady + kV,
+        kRFull = kVEmpty + kV, kREmpty = kRFull + kR, kNumBars = kREmpty + kR
+    };
+    static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // Misc
+    static constexpr int kSmem = kOffMisc + 32;
+    static_assert(kSmem <= 232448, "shared memory");
+};
+
 __device__ __forceinline__ void bulk_load(uint64_t* bar, void* dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                      smem_u32(dst)),
@@ -134,7 +165,7 @@ __device__ __forceinline__ void bulk_load(uint64_t* bar, void* dst, const void* 
 
 // The loader (a whole warp).
 template <int D, bool FP8>
-__device__ __forceinline__ void load_tiles(const AttnArgs& a, uint8_t* smem, uint64_t* bars, Misc& misc, Share sh,
+__device__ __forceinline__ void load_tiles(const AttnArgs& a, uint8_t* smem, uint64_t* bars, Misc& misc, Place& at,
                                            const Abort& ab) {
     using C = Cfg<D, FP8>;
     constexpr uint32_t kGroupBytes = FP8 ? 16 * D + 16 : 16 * D * 2;
@@ -144,33 +175,32 @@ __device__ __forceinline__ void load_tiles(const AttnArgs& a, uint8_t* smem, uin
     RingAt<C::kK> rk;
     RingAt<NV> rv;
     uint32_t nk = 0, nv = 0;
-    while (sh.u < sh.u_end) {
-        const Segment g = next_segment(a, sh);
-        if (g.rows == 0) break;
-        const Walk w(a, g);
+    const Segment& g = at.g;
+    const Walk& w = at.w;
+    while (advance(a, at)) {
         // page of group 32 i + lane of the segment
         const auto pages = [&](int i) {
             const int j = 32 * i + lane;
             if (j >= g.n) return -1;
-            const int at = segment_group(g, j) >> (a.c.page_log - 4);
-            if (at >= a.w.width) return -1;   // (events behind the table are none of the segment's)
-            const int p = __ldg(a.w.table + g.b * a.w.stride + at);
+            const int i_page = segment_group(g, j) >> (a.c.page_log - 4);
+            if (i_page >= a.w.width) return -1;   // (events behind the table are none of the segment's)
+            const int p = __ldg(a.w.table + g.b * a.w.stride + i_page);
             if ((unsigned)p >= (unsigned)a.c.pages) {
                 cache_bad(a.c.err, kCacheBadPage, g.b, p);
                 return -1;
             }
             return p;
         };
-        int prev = -1, cur = pages(0), next = pages(1), at = 0;
+        int prev = -1, cur = pages(0), next = pages(1), set = 0;
         const bool ok = w.tiles([&](int b, bool is_v) {
-            if (!is_v && (b >> 2) > at) {
-                ++at;
+            if (!is_v && (b >> 2) > set) {
+                ++set;
                 prev = cur;
                 cur = next;
-                next = pages(at + 1);
+                next = pages(set + 1);
             }
-            const int ng = w.groups(g, b);
-            const int p = __shfl_sync(0xffffffffu, (b >> 2) == at ? cur : prev, 8 * (b & 3) + (lane & 7));
+            const int ng = w.groups(b);
+            const int p = __shfl_sync(0xffffffffu, (b >> 2) == set ? cur : prev, 8 * (b & 3) + (lane & 7));
             const uint32_t there = __ballot_sync(0xffffffffu, lane < ng && p >= 0);
             const uint32_t st = is_v ? rv.st : rk.st;
             uint64_t* full = &bars[(is_v ? kVFullBar : C::kKFull) + st];
@@ -240,7 +270,7 @@ __device__ __forceinline__ uint4 expand8(uint32_t lo, uint32_t hi, uint32_t m, u
 
 // The workers (warps; whole).
 template <int D, bool FP8>
-__device__ __forceinline__ void work_tiles(const AttnArgs& a, uint8_t* smem, uint64_t* bars, Misc& misc, Share sh,
+__device__ __forceinline__ void work_tiles(const AttnArgs& a, uint8_t* smem, uint64_t* bars, Misc& misc, Place& at,
                                            const Abort& ab) {
     using C = Cfg<D, FP8>;
     const int lane = threadIdx.x & 31, who = threadIdx.x - 64;
@@ -248,17 +278,16 @@ __device__ __forceinline__ void work_tiles(const AttnArgs& a, uint8_t* smem, uin
     RingAt<C::kV> rv;
     RingAt<FP8 ? C::kR : 1> rr;
     uint32_t block0 = 0;
-    while (sh.u < sh.u_end) {
-        const Segment g = next_segment(a, sh);
-        if (g.rows == 0) break;
-        const Walk w(a, g);
+    const Segment& g = at.g;
+    const Walk& w = at.w;
+    while (advance(a, at)) {
         const bool ok = w.tiles([&](int b, bool is_v) {
-            const int ng = w.groups(g, b);
+            const int ng = w.groups(b);
             if (!is_v) {
                 if constexpr (FP8) {
                     if (!__all_sync(0xffffffffu, mbar_wait<true>(&bars[C::kKFull + rk.st], rk.ph, ab, 76))) return false;
-                    if (who < 128)
-                        reinterpret_cast<float*>(smem + C::kOffScale)[((block0 + b) & 7) * 128 + who] = cache_scale(smem[C::kOffKScale + rk.st * 128 + who]);
+                    for (int i = who; i < 128; i += 32 * C::kWorkers)
+                        reinterpret_cast<float*>(smem + C::kOffScale)[((block0 + b) & 7) * 128 + i] = cache_scale(smem[C::kOffKScale + rk.st * 128 + i]);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars[C::kKReady + rk.st]);
                     rk.next();
@@ -267,7 +296,7 @@ __device__ __forceinline__ void work_tiles(const AttnArgs& a, uint8_t* smem, uin
             }
             if (!__all_sync(0xffffffffu, mbar_wait<true>(&bars[C::kVEmpty + rv.st], rv.ph ^ 1, ab, 67))) return false;
             uint8_t* dst = smem + C::kOffV + rv.st * C::kTile;
-            const bool clean = w.masked(g, b);
+            const bool clean = w.masked(b);
             bool odd = false;
             if constexpr (FP8) {
                 if (!__all_sync(0xffffffffu, mbar_wait<true>(&bars[C::kRFull + rr.st], rr.ph, ab, 69))) return false;
@@ -307,8 +336,8 @@ __device__ __forceinline__ void work_tiles(const AttnArgs& a, uint8_t* smem, uin
             } else if (clean) {
                 if (!__all_sync(0xffffffffu, mbar_wait<true>(&bars[C::kVFull + rv.st], rv.ph, ab, 69))) return false;
                 for (int x = who; x < 16 * ng * (D / 8); x += 32 * C::kWorkers) {
-                    uint4* at = reinterpret_cast<uint4*>(dst + (x & 7) * 16 + ((x >> 3) % (16 * ng)) * 128 + ((x >> 3) / (16 * ng)) * kHalfBytes);
-                    uint4 v = *at;
+                    uint4* piece = reinterpret_cast<uint4*>(dst + (x & 7) * 16 + ((x >> 3) % (16 * ng)) * 128 + ((x >> 3) / (16 * ng)) * kHalfBytes);
+                    uint4 v = *piece;
                     uint32_t any = 0;
                     uint32_t* p = &v.x;
 #pragma unroll
@@ -318,7 +347,7 @@ __device__ __forceinline__ void work_tiles(const AttnArgs& a, uint8_t* smem, uin
                         p[i] &= ~z;
                     }
                     if (any) {
-                        *at = v;
+                        *piece = v;
                         odd = true;
                     }
                 }
@@ -371,8 +400,8 @@ struct Issuer {
 };
 
 template <int D, bool FP8>
-__device__ __forceinline__ bool issue_segment(Issuer<D, FP8>& z, const Segment& g, const Walk& w, uint8_t* smem,
-                                              uint64_t* bars, uint32_t tmem, const Abort& ab) {
+__device__ __forceinline__ bool issue_segment(Issuer<D, FP8>& z, const Walk& w, uint8_t* smem, uint64_t* bars,
+                                              uint32_t tmem, const Abort& ab) {
     using C = Cfg<D, FP8>;
     constexpr uint32_t idesc_pv = idesc_bf16(128, D, false, true);
     constexpr uint64_t kKDesc = C::kKTile >> 4, kVDesc = C::kTile >> 4;
@@ -380,7 +409,7 @@ __device__ __forceinline__ bool issue_segment(Issuer<D, FP8>& z, const Segment& 
     const uint64_t k_desc = FP8 ? codes_desc<D>(smem_u32(smem + C::kOffK)) : smem_desc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
     const uint64_t v_desc = smem_desc_sw128(smem_u32(smem + C::kOffV), kHalfBytes, 1024);
     const int nb = w.nb;
-    const uint32_t last_keys = (uint32_t)(16 * w.groups(g, nb - 1));
+    const uint32_t last_keys = (uint32_t)(16 * w.groups(nb - 1));
     const uint32_t idesc_full = FP8 ? idesc_e4m3(128, 128) : idesc_bf16(128, 128, false, false);
     const uint32_t idesc_last = FP8 ? idesc_e4m3(128, last_keys) : idesc_bf16(128, last_keys, false, false);
     const uint64_t q2 = q_desc + (w.dual ? 0 : (uint64_t)(C::kTile >> 4));
@@ -418,16 +447,12 @@ __device__ __forceinline__ bool issue_segment(Issuer<D, FP8>& z, const Segment& 
             if (!mbar_wait<true>(&bars[C::kOFree + s], z.o_ph[s], ab, 65)) return false;
             z.o_ph[s] ^= 1;
         }
-        if (!mbar_wait<true>(&bars[C::kPFull + 2 * s], z.p_ph[s], ab, 66)) return false;
+        if (!mbar_wait<true>(&bars[C::kPFull + s], z.p_ph[s], ab, 66)) return false;
+        z.p_ph[s] ^= 1;
         tc_fence_after();
         const uint32_t keys = b == nb - 1 ? last_keys : 128u;
         one_sums(oc, sc, sc + 16, vd, idesc_pv, keys >> 4, first ? 0 : 1);
-        if (!mbar_wait<true>(&bars[C::kPFull + 2 * s + 1], z.p_ph[s], ab, 68)) return false;
-        z.p_ph[s] ^= 1;
-        if (keys > 64) {
-            tc_fence_after();
-            one_sums(oc, sc + 32, sc + 48, vd + mnmajor_step(4), idesc_pv, (keys - 64) >> 4, 1);
-        }
+        if (keys > 64) one_sums(oc, sc + 32, sc + 48, vd + mnmajor_step(4), idesc_pv, (keys - 64) >> 4, 1);
         return true;
     };
     if (!mbar_wait<true>(&bars[C::kQFull], z.q_ph, ab, 63)) return false;
@@ -482,10 +507,11 @@ __device__ __forceinline__ bool issue_segment(Issuer<D, FP8>& z, const Segment& 
 // added to columns c0 .. c0 + 31 of a row that sees their events; element-wise
 // activations give NaN there.
 template <int D, bool FP8, bool SM>
-__device__ __noinline__ void add_odd(const AttnArgs& a, const Segment& g, const Walk& w, const RowView& rv, int c0, float* o) {
+__device__ __noinline__ void add_odd(const AttnArgs& a, const Segment& g, const Walk& w, int row, int c0, float* o) {
+    const RowView rv = row_view(a, g, row);
     for (int b = 0; b < w.nb; ++b) {
-        if (!w.masked(g, b)) continue;
-        for (int i = 8 * b; i < 8 * b + w.groups(g, b); ++i) {
+        if (!w.masked(b)) continue;
+        for (int i = 8 * b; i < 8 * b + w.groups(b); ++i) {
             const int e0 = segment_group(g, i) * kCacheGroup;
             const uint32_t bits = row_bits(a, g, rv, e0);
             const int64_t blk = bits ? cache_block(a.c, a.w, g.b, e0, g.h) : -1;
@@ -507,57 +533,114 @@ __device__ __noinline__ void add_odd(const AttnArgs& a, const Segment& g, const 
     }
 }
 
-// The unit of a row's codes (read again by the slot that does not write them).
-template <int D>
-__device__ __forceinline__ float query_unit(const AttnArgs& a, const Segment& g, const RowView& rv, int r) {
-    if (rv.tok < 0) return 1.0f;
-    const __nv_bfloat16* src = (const __nv_bfloat16*)a.q + (g.s.t0 + rv.tok) * a.qt + (g.h * a.G + g.rho0 + r - rv.tok * a.G) * a.qh;
-    float top = 0.0f;
-    if (a.q_wide) {
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + c);
-            const uint32_t p[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(bf16_lo(p[i])), fabsf(bf16_hi(p[i]))));
-        }
-    } else {
-        for (int c = 0; c < D; ++c) top = fmaxf(top, fabsf(__bfloat162float(src[c])));
-    }
-    return 0x1p-7f / inverse_power(top);
-}
-
 // row_bits of the 8 groups of a block.  (Out of line: the instruction cache holds
 // little more than the loop that is to go on.)
-static __device__ __noinline__ uint4 block_bits(const AttnArgs& a, const Segment& g, const RowView& v, int i) {
-    uint4 r;
+static __device__ __noinline__ uint4 block_bits(const AttnArgs& a, const Segment& g, int row, int i) {
+    const RowView v = row_view(a, g, row);
+    uint4 r = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 1
-    for (int q = 0; q < 4; ++q) {
-        uint32_t bits = 0;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h)
-            if (i + 2 * q + h < g.n) bits |= row_bits(a, g, v, segment_group(g, i + 2 * q + h) * kCacheGroup) << (16 * h);
-        if (q == 0) r.x = bits;
-        else if (q == 1) r.y = bits;
-        else if (q == 2) r.z = bits;
-        else r.w = bits;
+    for (int h = 0; h < 8; ++h) {
+        if (i + h >= g.n) break;
+        const uint32_t bits = row_bits(a, g, v, segment_group(g, i + h) * kCacheGroup) << (16 * (h & 1));
+        if (h < 2) r.x |= bits;
+        else if (h < 4) r.y |= bits;
+        else if (h < 6) r.z |= bits;
+        else r.w |= bits;
     }
     return r;
 }
 
+// A row's sums times f, where they lie.
+template <int D>
+__device__ __forceinline__ void scale_sums(uint32_t oc, float f) {
+#pragma unroll 1
+    for (int c = 0; c < D; c += 16) {
+        uint32_t o[16];
+        tmem_ld16(oc + c, o);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+        tmem_st16(oc + c, o);
+    }
+    tmem_st_wait();
+}
+
+// A warp's 32 rows of queries, from row r0 of the tile, to shared memory: whole
+// rows in neighbouring lanes, as operands.  8-bit: in units that make a row's
+// largest value lie in [128, 256), and what undoes that.
+template <int D, bool FP8>
+__device__ __forceinline__ void put_queries(const AttnArgs& a, const Segment& g, int r0, int row0, uint8_t* dst, float* unit) {
+    constexpr int kLanes = D / 8, kEach = 32 / kLanes;   // lanes a row, rows at a time
+    // several loads on their way at once; more would cost more in fetching the
+    // instructions of a loop that is run a few times a segment
+    constexpr int kAhead = FP8 ? 4 : 8;
+    const int lane = threadIdx.x & 31, c = lane % kLanes;
+    int64_t at = -1;   // of row r0 + lane
+    if (r0 + lane < g.rows) {
+        const int rho = g.rho0 + r0 + lane, tok = rho / a.G;
+        at = (g.s.t0 + tok) * a.qt + (g.h * a.G + rho - tok * a.G) * a.qh;
+    }
+#pragma unroll 1
+    for (int i0 = lane / kLanes; i0 < 32; i0 += kAhead * kEach) {
+        uint4 q[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t from = __shfl_sync(0xffffffffu, at, i0 + k * kEach);
+            q[k] = make_uint4(0, 0, 0, 0);
+            if (from >= 0) {
+                const __nv_bfloat16* src = (const __nv_bfloat16*)a.q + from + 8 * c;
+                if (a.q_wide) {
+                    q[k] = __ldg(reinterpret_cast<const uint4*>(src));
+                } else {
+                    const uint16_t* h = reinterpret_cast<const uint16_t*>(src);
+                    uint32_t* p = &q[k].x;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) p[i] = h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const uint4 v = q[k];
+            const int i = i0 + k * kEach, row = row0 + i;
+            if constexpr (FP8) {
+                const uint32_t p[4] = {v.x, v.y, v.z, v.w};
+                float top = 0.0f;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) top = fmaxf(top, fmaxf(fabsf(bf16_lo(p[x])), fabsf(bf16_hi(p[x]))));
+#pragma unroll
+                for (int m = 1; m < kLanes; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+                const float f = inverse_power(top);   // of infinities: whatever, their products are
+                uint32_t h[4], l[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) split_q<false>(bf16_lo(p[x]) * f * 128.0f, bf16_hi(p[x]) * f * 128.0f, h[x], l[x]);
+                const int to = cache_chunk(D, 7, row, c >> 1) + 8 * (c & 1);
+                *reinterpret_cast<uint2*>(dst + to) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+                *reinterpret_cast<uint2*>(dst + 128 * D + to) = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+                if (c == 0) unit[i] = 0x1p-7f / f;
+            } else {
+                *reinterpret_cast<uint4*>(dst + row * 128 + (c >> 3) * kHalfBytes + (((c & 7) ^ (row & 7)) << 4)) = v;
+            }
+        }
+    }
+}
+
 template <int D, bool FP8, int ACT>
 __device__ __forceinline__ void tile_rows(const AttnArgs& a, uint8_t* smem, uint64_t* bars, Misc& misc, uint32_t tmem,
-                                          Share sh, const Abort& ab) {
+                                          Place& at, const Abort& ab) {
     using C = Cfg<D, FP8>;
     constexpr bool kSm = ACT == kSoftmax;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int s = (warp - C::kRows0) >> 2;
     const int quarter = warp & 3;
-    static_assert(C::kRows0 % 4 == 0, "a warpgroup a slot");
+    static_assert(C::kRows0 % 4 == 0, "whole warpgroups");
     const int row = quarter * 32 + lane;
     const uint32_t trow = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t sc = trow + s * 128, oc = trow + 256 + s * 128;
-    float2* ml1 = reinterpret_cast<float2*>(smem + C::kOffMl);
+    float2* const fin = reinterpret_cast<float2*>(smem + C::kOffFin) + row;
+    // for outputs on their way: the place of the warp's own queries, which no other
+    // warp writes to (8-bit rows of 64 are too short: a place apart)
+    uint8_t* const stage = smem + (C::kStageApart ? C::kOffStage + (s * 4 + quarter) * 4096 : s * C::kTile + quarter * 4096);
     const bool flip = kSm && a.alpha < 0.0f;
     const auto scale_of = [&](float alpha) {
         ActScale k = act_scale<ACT>(alpha);
@@ -568,90 +651,44 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& a, uint8_t* smem, uint
         return k;
     };
     ActScale ks = scale_of(a.alpha);
-    uint32_t items = 0, used[2] = {0, 0}, duals = 0, q_ph = 1, block0 = 0;
-    while (sh.u < sh.u_end) {
-        const Segment g = next_segment(a, sh);
-        if (g.rows == 0) break;
-        const Walk w(a, g);
-        const int n = w.blocks(s);
-        const int r = (w.dual ? 0 : 128 * s) + row;      // of the tile
+    const Segment& g = at.g;
+    const Walk& w = at.w;
+    uint32_t items = 0, used[2] = {0, 0}, fins = 0, q_ph = 1, block0 = 0;
+    while (advance(a, at)) {
+        const int n = w.blocks(s), n1 = w.n1, nb = w.nb, open0 = w.open0, open1 = w.open1;
+        const bool dual = w.dual;
+        const int tile0 = dual ? 0 : 128 * s;            // first row of the slot
+        const int r = tile0 + row;                       // of the tile
         const bool real = r < g.rows;
-        const RowView rv = row_view(a, g, r);
-        float q_unit = 1.0f;   // 8-bit: what the codes' scores are to be multiplied by
-        if (w.nb > 0) {
-            // queries, a row a thread
+        if (nb > 0) {
             if (!wg_wait<true>(&bars[C::kQEmpty], q_ph, ab, 61)) return;
             q_ph ^= 1;
-            if (!(w.dual && s)) {
-                uint8_t* dst = smem + (w.dual ? 0 : s) * C::kTile;
-                const int tok = max(rv.tok, 0);
-                const __nv_bfloat16* src = (const __nv_bfloat16*)a.q + (g.s.t0 + tok) * a.qt + (g.h * a.G + g.rho0 + r - tok * a.G) * a.qh;
-                uint4 q[D / 8];
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    q[c] = make_uint4(0, 0, 0, 0);
-                    if (real) {
-                        if (a.q_wide) {
-                            q[c] = __ldg(reinterpret_cast<const uint4*>(src) + c);
-                        } else {
-                            const uint16_t* h = reinterpret_cast<const uint16_t*>(src) + 8 * c;
-                            uint32_t* p = &q[c].x;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) p[i] = h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
-                        }
-                    }
-                }
-                if constexpr (FP8) {
-                    float top = 0.0f;
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c) {
-                        const uint32_t* p = &q[c].x;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(bf16_lo(p[i])), fabsf(bf16_hi(p[i]))));
-                    }
-                    const float f = inverse_power(top);   // of infinities: whatever, their products are
-                    q_unit = 0x1p-7f / f;
-#pragma unroll
-                    for (int c = 0; c < D / 16; ++c) {    // 16 columns: a piece of codes, and of what they leave
-                        uint4 hi, lo;
-                        uint32_t *h = &hi.x, *l = &lo.x;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint4& v = q[2 * c + (i >> 1)];
-                            const uint32_t p0 = i & 1 ? v.z : v.x, p1 = i & 1 ? v.w : v.y;
-                            uint32_t h0, h1, l0, l1;
-                            split_q<false>(bf16_lo(p0) * f * 128.0f, bf16_hi(p0) * f * 128.0f, h0, l0);
-                            split_q<false>(bf16_lo(p1) * f * 128.0f, bf16_hi(p1) * f * 128.0f, h1, l1);
-                            h[i] = h0 | h1 << 16;
-                            l[i] = l0 | l1 << 16;
-                        }
-                        const int at = cache_chunk(D, 7, row, c);
-                        *reinterpret_cast<uint4*>(dst + at) = hi;
-                        *reinterpret_cast<uint4*>(dst + C::kCodes + at) = lo;
-                    }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c)
-                        *reinterpret_cast<uint4*>(dst + row * 128 + (c >> 3) * kHalfBytes + (((c & 7) ^ (row & 7)) << 4)) = q[c];
-                }
+            if (!(dual && s)) {
+                put_queries<D, FP8>(a, g, tile0 + quarter * 32, quarter * 32, smem + (dual ? 0 : s) * C::kTile,
+                                    reinterpret_cast<float*>(smem + C::kOffUnit) + tile0 + quarter * 32);
                 fence_proxy_async_smem();
             }
             mbar_arrive(&bars[C::kQFull]);
-            if constexpr (FP8) {
-                // both slots of the same rows score them in the same unit
-                if (w.dual && s) q_unit = query_unit<D>(a, g, rv, r);
-                ks = scale_of(a.alpha * q_unit);
-            }
         }
-        float ref = -INFINITY, sum = 0.0f;
+        float ref = -INFINITY, sum = 0.0f;   // reference and sum of the weights
         for (int j = 0; j < n; ++j) {
-            const int b = w.block(s, j);
+            const int b = dual ? 2 * j + s : j;
             // what the row sees of the block, made while its scores are
-            const bool masked = w.groups(g, b) < 8 || w.masked(g, b);
+            const bool masked = b < open0 || b >= open1;
             uint4 vis = make_uint4(~0u, ~0u, ~0u, ~0u);
-            if (masked) vis = block_bits(a, g, rv, 8 * b);
+            if (masked) vis = block_bits(a, g, r, 8 * b);
             if (!wg_wait<true>(&bars[C::kSFull + s], (items + j) & 1, ab, 71)) return;
             tc_fence_after();
+            if (FP8 && j == 0) ks = scale_of(a.alpha * reinterpret_cast<const float*>(smem + C::kOffUnit)[r]);
+            const uint32_t gone = *reinterpret_cast<volatile uint8_t*>(&misc.gone[(block0 + b) & 15]);
+            const bool cut = masked || gone;
+            if (gone) {
+                const auto lost = [&](int i) { return (gone >> i & 1u ? 0xffffu : 0u) | (gone >> i & 2u ? 0xffff0000u : 0u); };
+                vis.x &= ~lost(0);
+                vis.y &= ~lost(2);
+                vis.z &= ~lost(4);
+                vis.w &= ~lost(6);
+            }
             uint32_t x[128];
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld32(sc + c * 32, *reinterpret_cast<uint32_t(*)[32]>(x + c * 32));
@@ -673,17 +710,11 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& a, uint8_t* smem, uint
 #pragma unroll
                 for (int e = 0; e < 128; ++e) x[e] ^= 0x80000000u;
             }
-            const uint32_t gone = *reinterpret_cast<volatile uint8_t*>(&misc.gone[(block0 + b) & 15]);
-            const bool cut = masked || gone;
             if (cut) {
-                const uint32_t bits[4] = {vis.x, vis.y, vis.z, vis.w};
+                const uint32_t see[4] = {vis.x, vis.y, vis.z, vis.w};
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const uint32_t see = gone >> q & 1u ? 0u : bits[q >> 1] >> (16 * (q & 1));
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (!(see >> e & 1u)) x[16 * q + e] = 0xff800000u;   // -inf
-                }
+                for (int e = 0; e < 128; ++e)
+                    if (!(see[e >> 5] >> (e & 31) & 1u)) x[e] = 0xff800000u;   // -inf
             }
             if constexpr (kSm) {
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -693,92 +724,71 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& a, uint8_t* smem, uint
                     for (int u = 0; u < 4; ++u)
                         m4[u] = max3_nan(m4[u], __uint_as_float(x[e + u]), __uint_as_float(x[e + 4 + u]));
                 const float top = max3_nan(max3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]) * ks.c0;
-                if (top != top) {   // (exp2_poly would take a NaN for a number)
+                if (top != top) {
                     sum = top;
                     if (ref == -INFINITY) ref = 0.0f;   // the part counts
                 }
+                // the reference moves when it would be passed by more than 2^8 (that
+                // the scores are complete says that the sums before them are)
                 const bool up = real && top > ref + kRise;   // also from -inf
                 if (__any_sync(0xffffffffu, up)) {
                     const float nref = up ? top : ref;
                     const float f = up ? ex2_approx(ref - nref) : 1.0f;   // 0 from -inf
                     ref = nref;
                     sum *= f;
-                    if (j > 0) {
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 16) {
-                            uint32_t o[16];
-                            tmem_ld16(oc + c, o);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st16(oc + c, o);
-                        }
-                        tmem_st_wait();
-                    }
+                    if (j > 0) scale_sums<D>(oc, f);
                 }
             }
             const float nref = kSm ? (ref == -INFINITY ? 0.0f : -ref) : 0.0f;
             uint64_t sum2 = f2_make(0.0f, 0.0f);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int c = 0; c < 4; ++c) {
+                uint32_t pk[16];
 #pragma unroll
-                for (int c = 2 * h; c < 2 * h + 2; ++c) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        float p0, p1;
-                        const float s0 = __uint_as_float(x[c * 32 + e]), s1 = __uint_as_float(x[c * 32 + e + 1]);
-                        if constexpr (kSm) {
-                            const float2 tt = f2_split(
-                                f2_fma(f2_make(s0, s1), f2_make(ks.c0, ks.c0), f2_make(nref, nref)));
-                            if (!FP8 && e % 6 == 4) {   // one pair of three (8-bit: issue slots are scarcer)
-                                const float2 y = exp2_poly(tt);
-                                p0 = y.x;
-                                p1 = y.y;
-                            } else {
-                                p0 = ex2_approx(tt.x);
-                                p1 = ex2_approx(tt.y);
-                            }
-                            sum2 = f2_fma(f2_make(p0, p1), f2_make(1.0f, 1.0f), sum2);
-                        } else {
-                            act_s2<ACT>(s0, s1, ks, p0, p1);
-                            if (cut) {
-                                if (s0 == -INFINITY) p0 = 0.0f;
-                                if (s1 == -INFINITY) p1 = 0.0f;
-                            }
+                for (int e = 0; e < 32; e += 2) {
+                    float p0, p1;
+                    const float s0 = __uint_as_float(x[c * 32 + e]), s1 = __uint_as_float(x[c * 32 + e + 1]);
+                    if constexpr (kSm) {
+                        const float2 tt = f2_split(f2_fma(f2_make(s0, s1), f2_make(ks.c0, ks.c0), f2_make(nref, nref)));
+                        p0 = ex2_approx(tt.x);
+                        p1 = ex2_approx(tt.y);
+                        sum2 = f2_fma(f2_make(p0, p1), f2_make(1.0f, 1.0f), sum2);
+                    } else {
+                        act_s2<ACT>(s0, s1, ks, p0, p1);
+                        if (cut) {
+                            if (s0 == -INFINITY) p0 = 0.0f;
+                            if (s1 == -INFINITY) p1 = 0.0f;
                         }
-                        pk[e >> 1] = pack_bf16x2(p0, p1);
                     }
-                    tmem_st16(sc + c * 16, pk);
+                    pk[e >> 1] = pack_bf16x2(p0, p1);
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive(&bars[C::kPFull + 2 * s + h]);
+                tmem_st16(sc + c * 16, pk);
             }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&bars[C::kPFull + s]);
             if constexpr (kSm) {
                 const float2 y = f2_split(sum2);
                 sum += y.x + y.y;
             }
         }
         items += n;
-        block0 += (uint32_t)w.nb;
-        const bool both = w.dual && w.n1 > 0;   // slot 0 joins slot 1's sums to its own
-        if (n > 0) {
-            if (!wg_wait<true>(&bars[C::kOFull + s], used[s] & 1, ab, 73)) return;
-            tc_fence_after();
-        }
-        if (both && s) {
-            ml1[row] = make_float2(ref, sum);
-            tc_fence_before();
-            mbar_arrive(&bars[C::kDual]);
-        }
+        block0 += (uint32_t)nb;
+        const bool both = dual && n1 > 0;   // slot 0's threads join slot 1's sums to their own
+        if (n > 0 && !wg_wait<true>(&bars[C::kOFull + s], used[s] & 1, ab, 73)) return;
+        tc_fence_after();
         float f0 = 1.0f, f1 = 0.0f;
+        if (both && s) {
+            *fin = make_float2(ref, sum);
+            tc_fence_before();
+            mbar_arrive(&bars[C::kFin]);
+        }
         if (both && !s) {
-            if (!wg_wait<true>(&bars[C::kOFull + 1], used[1] & 1, ab, 74) || !wg_wait<true>(&bars[C::kDual], duals & 1, ab, 75)) return;
+            if (!wg_wait<true>(&bars[C::kOFull + 1], used[1] & 1, ab, 74) || !wg_wait<true>(&bars[C::kFin], fins & 1, ab, 75)) return;
             tc_fence_after();
             f1 = 1.0f;
             if constexpr (kSm) {
-                const float2 y = ml1[row];
+                const float2 y = *fin;
                 const float m = fmaxf(ref, y.x), m0 = m == -INFINITY ? 0.0f : m;
                 f0 = ex2_approx(ref - m0);
                 f1 = ex2_approx(y.x - m0);
@@ -786,27 +796,29 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& a, uint8_t* smem, uint
                 ref = m;
             }
         }
-        if (!(w.dual && s)) {
+        fins += both;
+        if (!(dual && s)) {
             const bool dirty = *reinterpret_cast<volatile int*>(&misc.dirty) != 0;
             float* slot = nullptr;
             if (!g.whole) slot = a.part + (int64_t)(2 * blockIdx.x + (g.head ? 1 : 0)) * a.TM * (D + 2);
             const float inv = kSm ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
-            const int rho = g.rho0 + r, tok = max(rv.tok, 0);
-            const int64_t out = (int64_t)(g.s.t0 + tok) * a.H + g.h * a.G + (rho - tok * a.G);
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
+            // outputs, 32 columns at a time, through shared memory, so that a row's
+            // lie in neighbouring lanes (the queries' products are over)
+            const int warp_rows = min(32, g.rows - tile0 - quarter * 32);
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
                 float y[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) y[e] = 0.0f;
                 if (n > 0) {
-                    tmem_ld32(oc + c * 32, o);
+                    tmem_ld32(oc + c, o);
                     tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < 32; ++e) y[e] = f0 == 0.0f ? 0.0f : __uint_as_float(o[e]) * f0;
                 }
                 if (both) {
-                    tmem_ld32(oc + 128 + c * 32, o);
+                    tmem_ld32(oc + 128 + c, o);
                     tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < 32; ++e) y[e] = fmaf(__uint_as_float(o[e]), f1, y[e]);
@@ -815,30 +827,42 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& a, uint8_t* smem, uint
                     float z[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) z[e] = y[e];
-                    add_odd<D, FP8, kSm>(a, g, w, rv, 32 * c, z);
+                    add_odd<D, FP8, kSm>(a, g, w, r, c, z);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) y[e] = z[e];
                 }
-                if (real) {
-                    if (slot) {
+                if (slot) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            reinterpret_cast<float4*>(slot + r * D + 32 * c)[e] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-                    } else {
-                        uint4* dst = reinterpret_cast<uint4*>((__nv_bfloat16*)a.o + out * D + 32 * c);
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<float4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+                    __syncwarp();
+                    float* to = slot + (tile0 + quarter * 32) * D + c;
+                    for (int i = lane >> 3; i < warp_rows; i += 4)
+                        reinterpret_cast<float4*>(to + i * D)[lane & 7] = *reinterpret_cast<const float4*>(stage + i * 128 + (((lane & 7) ^ (i & 7)) << 4));
+                } else {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            dst[e] = make_uint4(pack_bf16x2(y[8 * e] * inv, y[8 * e + 1] * inv), pack_bf16x2(y[8 * e + 2] * inv, y[8 * e + 3] * inv),
-                                                pack_bf16x2(y[8 * e + 4] * inv, y[8 * e + 5] * inv), pack_bf16x2(y[8 * e + 6] * inv, y[8 * e + 7] * inv));
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) =
+                            make_uint4(pack_bf16x2(y[8 * e] * inv, y[8 * e + 1] * inv), pack_bf16x2(y[8 * e + 2] * inv, y[8 * e + 3] * inv),
+                                       pack_bf16x2(y[8 * e + 4] * inv, y[8 * e + 5] * inv), pack_bf16x2(y[8 * e + 6] * inv, y[8 * e + 7] * inv));
+                    __syncwarp();
+                    for (int i = lane >> 2; i < warp_rows; i += 8) {
+                        const int rho = g.rho0 + tile0 + quarter * 32 + i, tok = rho / a.G;
+                        const int64_t out = (int64_t)(g.s.t0 + tok) * a.H + g.h * a.G + (rho - tok * a.G);
+                        reinterpret_cast<uint4*>((__nv_bfloat16*)a.o + out * D + c)[lane & 3] =
+                            *reinterpret_cast<const uint4*>(stage + i * 64 + (((lane & 3) ^ ((i >> 1) & 3)) << 4));
                     }
                 }
+                __syncwarp();
             }
             if (kSm && real) {
                 if (slot) {
                     slot[a.TM * D + r] = ref;
                     slot[a.TM * (D + 1) + r] = sum;
                 } else if (a.lse) {
-                    a.lse[out] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.693147180559945309f;
+                    const int rho = g.rho0 + r, tok = rho / a.G;
+                    a.lse[(int64_t)(g.s.t0 + tok) * a.H + g.h * a.G + (rho - tok * a.G)] =
+                        sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.693147180559945309f;
                 }
             }
             if (slot && g.head && threadIdx.x == 32 * C::kRows0) {
@@ -853,9 +877,8 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& a, uint8_t* smem, uint
             if (n > 0) mbar_arrive(&bars[C::kOFree + s]);
             if (both) mbar_arrive(&bars[C::kOFree + 1]);
         }
-        used[0] += w.n0 > 0;
-        used[1] += w.n1 > 0;
-        duals += both;
+        used[0] += nb > 0;
+        used[1] += n1 > 0;
     }
 }
 
@@ -863,8 +886,7 @@ template <int D, bool FP8, int ACT>
 __global__ void __launch_bounds__(Cfg<D, FP8>::kThreads, 1)
 cache_tc_kernel(const __grid_constant__ AttnArgs a) {
     using C = Cfg<D, FP8>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) uint8_t smem[];   // (the operands' swizzle starts at 1024 bytes)
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
     Misc& misc = *reinterpret_cast<Misc*>(smem + C::kOffMisc);
     const int warp = threadIdx.x >> 5;
@@ -874,7 +896,7 @@ cache_tc_kernel(const __grid_constant__ AttnArgs a) {
         for (int b = 0; b < C::kNumBars; ++b) {
             uint32_t n = 1;
             if (b == C::kQFull) n = 256;
-            if (b == C::kDual || (b >= C::kPFull && b < C::kPFull + 4) || (b >= C::kOFree && b < C::kOFree + 2)) n = 128;
+            if (b == C::kFin || (b >= C::kPFull && b < C::kPFull + 2) || (b >= C::kOFree && b < C::kOFree + 2)) n = 128;
             if ((b >= C::kKReady && b < C::kKEmpty) || (b >= C::kVReady && b < C::kVEmpty) || b >= C::kREmpty) n = C::kWorkers;
             mbar_init(&bars[b], n);
         }
@@ -890,21 +912,21 @@ cache_tc_kernel(const __grid_constant__ AttnArgs a) {
     tc_fence_after();
     const uint32_t tmem = misc.tmem;
     const Abort ab{&misc.abort_flag, a.c.err, kWaitLimitNs};
+    Place& at = reinterpret_cast<Place*>(smem + C::kOffPlace)[warp];
+    if ((threadIdx.x & 31) == 0) at.sh = sh;
+    __syncwarp();
     if (warp < C::kRows0) {
+        // 384 threads start with 168 registers: 88 + 2 * 208; 512 with 128: 2 * 56 + 2 * 200
         if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 0) {
-            load_tiles<D, FP8>(a, smem, bars, misc, sh, ab);
+            load_tiles<D, FP8>(a, smem, bars, misc, at, ab);
         } else if (warp == 1) {
             Issuer<D, FP8> z;
-            Share mine = sh;
             bool ok = true;
-            while (mine.u < mine.u_end && ok) {
-                const Segment g = next_segment(a, mine);
-                if (g.rows == 0) break;
-                const Walk w(a, g);
-                if (w.nb == 0) continue;
-                if (elect_one()) ok = issue_segment<D, FP8>(z, g, w, smem, bars, tmem, ab);
+            while (ok && advance(a, at)) {
+                if (at.w.nb == 0) continue;
+                if (elect_one()) ok = issue_segment<D, FP8>(z, at.w, smem, bars, tmem, ab);
                 // the elected lane keeps the state; all agree on whether to go on
                 ok = __all_sync(0xffffffffu, ok);
             }
@@ -915,12 +937,12 @@ cache_tc_kernel(const __grid_constant__ AttnArgs a) {
             }
             __syncwarp();
         } else {
-            work_tiles<D, FP8>(a, smem, bars, misc, sh, ab);
+            work_tiles<D, FP8>(a, smem, bars, misc, at, ab);
         }
     } else {
         if constexpr (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        tile_rows<D, FP8, ACT>(a, smem, bars, misc, tmem, sh, ab);
+        tile_rows<D, FP8, ACT>(a, smem, bars, misc, tmem, at, ab);
     }
     tc_fence_before();
     __syncthreads();
