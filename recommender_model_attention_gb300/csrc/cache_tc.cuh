@@ -253,19 +253,25 @@ __device__ __forceinline__ void load_tiles(const AttnArgs& a, uint8_t* smem, uin
     for (uint32_t i = nv > (uint32_t)NV ? nv - NV : 0; i < nv; ++i) mbar_wait_teardown(&bars[kVFullBar + i % NV], (i / NV) & 1);
 }
 
-// 8 codes (8 bytes) to 8 bf16 values: m is 2^(e + 120), m2 a second factor.
-__device__ __forceinline__ uint4 expand8(uint32_t lo, uint32_t hi, uint32_t m, uint32_t m2) {
-    uint4 r;
-    uint32_t* o = &r.x;
+// 16 codes to 16 bf16 values: m is 2^(e + 120), m2 a second factor (0: none).
+__device__ __forceinline__ void expand16(const uint4& q, uint32_t m, uint32_t m2, uint4& a, uint4& b) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    uint32_t o[8];
+    const auto times = [](uint32_t x, uint32_t y) {
+        const __nv_bfloat162 z = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&x), *reinterpret_cast<__nv_bfloat162*>(&y));
+        return *reinterpret_cast<const uint32_t*>(&z);
+    };
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t p = __byte_perm(i < 2 ? lo : hi, 0, (i & 1) ? 0x3424 : 0x1404);   // codes in the upper bytes
-        uint32_t x = ((p >> 4) & 0x07f007f0u) | (p & 0x80008000u);
-        __nv_bfloat162 y = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&m));
-        if (m2) y = __hmul2(y, *reinterpret_cast<const __nv_bfloat162*>(&m2));
-        o[i] = *reinterpret_cast<uint32_t*>(&y);
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t p = __byte_perm(w[i >> 1], 0, (i & 1) ? 0x3424 : 0x1404);   // codes in the upper bytes
+        o[i] = times(((p >> 4) & 0x07f007f0u) | (p & 0x80008000u), m);
     }
-    return r;
+    if (m2) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = times(o[i], m2);
+    }
+    a = make_uint4(o[0], o[1], o[2], o[3]);
+    b = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 // The workers (warps; whole).
@@ -303,7 +309,9 @@ __device__ __forceinline__ void work_tiles(const AttnArgs& a, uint8_t* smem, uin
                 const uint8_t* src = smem + C::kOffR + rr.st * C::kCodes;
                 const uint8_t* sc = smem + C::kOffVScale + rr.st * 128;
                 // a thread takes the same piece of every kRows-th row, where the
-                // swizzle is the same: one address that moves
+                // swizzle is the same: one address that moves.  (Unrolled twice: 8 x
+                // 512 rows on 16384 events 373 us, not 331; four times 471: the roles'
+                // loops together are more than the instruction cache holds.)
                 constexpr int kChunks = D / 16, kRows = 32 * C::kWorkers / kChunks;
                 static_assert(kRows % 8 == 0, "rows of the same swizzle");
                 const int ch = who % kChunks, e1 = 16 * ng;
@@ -311,7 +319,7 @@ __device__ __forceinline__ void work_tiles(const AttnArgs& a, uint8_t* smem, uin
                 src += cache_chunk(D, 7, e, ch);
                 uint8_t* lo = dst + (ch >> 2) * kHalfBytes + e * 128 + (((2 * ch) & 7) ^ (e & 7)) * 16;
                 uint8_t* hi = dst + (ch >> 2) * kHalfBytes + e * 128 + (((2 * ch + 1) & 7) ^ (e & 7)) * 16;
-#pragma unroll 2
+#pragma unroll 1
                 for (; e < e1; e += kRows, src += kRows * D, lo += kRows * 128, hi += kRows * 128) {
                     const uint4 q = *reinterpret_cast<const uint4*>(src);
                     const uint32_t s = sc[e];
@@ -329,8 +337,7 @@ __device__ __forceinline__ void work_tiles(const AttnArgs& a, uint8_t* smem, uin
                     // events behind the last one: whatever their memory holds
                     if (clean && segment_group(g, 8 * b + (e >> 4)) * kCacheGroup + (e & 15) >= g.s.end) m = m2 = 0;
                     m |= m << 16;
-                    *reinterpret_cast<uint4*>(lo) = expand8(q.x, q.y, m, m2);
-                    *reinterpret_cast<uint4*>(hi) = expand8(q.z, q.w, m, m2);
+                    expand16(q, m, m2, *reinterpret_cast<uint4*>(lo), *reinterpret_cast<uint4*>(hi));
                 }
                 fence_proxy_async_smem();
             } else if (clean) {
@@ -566,10 +573,11 @@ __device__ __forceinline__ void scale_sums(uint32_t oc, float f) {
 }
 
 // A warp's 32 rows of queries, from row r0 of the tile, to shared memory: whole
-// rows in neighbouring lanes, as operands.  8-bit: in units that make a row's
+// rows in neighbouring lanes, as operands (flip: the sign bits, for a negative
+// scale of the scores).  8-bit: in units that make a row's
 // largest value lie in [128, 256), and what undoes that.
 template <int D, bool FP8>
-__device__ __forceinline__ void put_queries(const AttnArgs& a, const Segment& g, int r0, int row0, uint8_t* dst, float* unit) {
+__device__ __forceinline__ void put_queries(const AttnArgs& a, const Segment& g, int r0, int row0, uint32_t flip, uint8_t* dst, float* unit) {
     constexpr int kLanes = D / 8, kEach = 32 / kLanes;   // lanes a row, rows at a time
     // several loads on their way at once; more would cost more in fetching the
     // instructions of a loop that is run a few times a segment
@@ -601,7 +609,7 @@ __device__ __forceinline__ void put_queries(const AttnArgs& a, const Segment& g,
         }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            const uint4 v = q[k];
+            const uint4 v = make_uint4(q[k].x ^ flip, q[k].y ^ flip, q[k].z ^ flip, q[k].w ^ flip);
             const int i = i0 + k * kEach, row = row0 + i;
             if constexpr (FP8) {
                 const uint32_t p[4] = {v.x, v.y, v.z, v.w};
@@ -641,7 +649,6 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& a, uint8_t* smem, uint
     // for outputs on their way: the place of the warp's own queries, which no other
     // warp writes to (8-bit rows of 64 are too short: a place apart)
     uint8_t* const stage = smem + (C::kStageApart ? C::kOffStage + (s * 4 + quarter) * 4096 : s * C::kTile + quarter * 4096);
-    const bool flip = kSm && a.alpha < 0.0f;
     const auto scale_of = [&](float alpha) {
         ActScale k = act_scale<ACT>(alpha);
         if (kSm) {   // (a zero scale would make NaN of masked scores)
@@ -664,7 +671,7 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& a, uint8_t* smem, uint
             if (!wg_wait<true>(&bars[C::kQEmpty], q_ph, ab, 61)) return;
             q_ph ^= 1;
             if (!(dual && s)) {
-                put_queries<D, FP8>(a, g, tile0 + quarter * 32, quarter * 32, smem + (dual ? 0 : s) * C::kTile,
+                put_queries<D, FP8>(a, g, tile0 + quarter * 32, quarter * 32, kSm && a.alpha < 0.0f ? 0x80008000u : 0u, smem + (dual ? 0 : s) * C::kTile,
                                     reinterpret_cast<float*>(smem + C::kOffUnit) + tile0 + quarter * 32);
                 fence_proxy_async_smem();
             }
@@ -705,10 +712,6 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& a, uint8_t* smem, uint
                     x[4 * e + 2] = __float_as_uint(v.x);
                     x[4 * e + 3] = __float_as_uint(v.y);
                 }
-            }
-            if (flip) {
-#pragma unroll
-                for (int e = 0; e < 128; ++e) x[e] ^= 0x80000000u;
             }
             if (cut) {
                 const uint32_t see[4] = {vis.x, vis.y, vis.z, vis.w};
@@ -916,8 +919,8 @@ cache_tc_kernel(const __grid_constant__ AttnArgs a) {
     if ((threadIdx.x & 31) == 0) at.sh = sh;
     __syncwarp();
     if (warp < C::kRows0) {
-        // 384 threads start with 168 registers: 88 + 2 * 208; 512 with 128: 2 * 56 + 2 * 200
-        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        // 384 threads start with 168 registers: 88 + 2 * 208; 512 with 128: 2 * 64 + 2 * 192
+        if constexpr (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 0) {
             load_tiles<D, FP8>(a, smem, bars, misc, at, ab);
@@ -940,7 +943,7 @@ cache_tc_kernel(const __grid_constant__ AttnArgs a) {
             work_tiles<D, FP8>(a, smem, bars, misc, at, ab);
         }
     } else {
-        if constexpr (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        if constexpr (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         tile_rows<D, FP8, ACT>(a, smem, bars, misc, tmem, at, ab);
     }
