@@ -89,6 +89,12 @@ __device__ __forceinline__ void sample_check(const AttnArgs& a, int b) {
         cache_bad(a.c.err, kCacheBadEvent, b, s.end);
 }
 
+// x / y for x >= 0, y > 0: in 32 bits where they fit (a fifth of the instructions)
+__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
+    if ((x | y) >> 32 == 0) return (uint32_t)x / (uint32_t)y;
+    return x / y;
+}
+
 // A CTA's place in the work: its share [u, u_end) of the units, the sample b
 // that holds u, and the unit at which b starts.
 struct Share {
@@ -132,7 +138,7 @@ __device__ __forceinline__ Share find_share(const AttnArgs& a, int64_t* tmp) {
     const int64_t scan0 = block_scan<NT>(first, tmp, total);   // of the first NT samples
     if (a.w.B > NT) block_scan<NT>(mine, tmp, all); else all = total;
     Share s;
-    s.size = max((all + gridDim.x - 1) / (int64_t)gridDim.x, (int64_t)a.min_share);
+    s.size = max(divide(all + gridDim.x - 1, gridDim.x), (int64_t)a.min_share);
     s.u = min((int64_t)blockIdx.x * s.size, all);
     s.u_end = min(s.u + s.size, all);
     if (threadIdx.x == 0) tmp[NT / 32] = -1;
@@ -198,7 +204,7 @@ __device__ __forceinline__ Segment next_segment(const AttnArgs& a, Share& s) {
     }
     const int size = g.s.groups + a.lead;
     const int64_t in = s.u - s.b_first;
-    const int item = (int)(in / size);
+    const int item = (int)divide(in, size);
     int u0 = (int)(in - (int64_t)item * size);
     if (u0 <= a.lead) {          // (the share's first segment, or an item's start)
         s.u -= u0;
@@ -217,7 +223,7 @@ __device__ __forceinline__ Segment next_segment(const AttnArgs& a, Share& s) {
     g.head = u0 == 0;
     g.whole = g.head && u1 == size;
     // up to the CTA that holds the item's last unit
-    g.parts = g.head ? (int)((s.u + size - 1) / s.size - blockIdx.x) + 1 : 0;
+    g.parts = g.head ? (int)(divide(s.u + size - 1, s.size) - blockIdx.x) + 1 : 0;
     s.u += u1 - u0;
     u0 = max(0, u0 - a.lead);
     u1 -= a.lead;

@@ -43,6 +43,7 @@ cache_join_kernel(const __grid_constant__ AttnArgs a, int ctas) {
     __shared__ int tmp[kJoinWarps];
     __shared__ float4 sums[kJoinWarps][32];
     __shared__ float2 ml[kJoinWarps];
+    __shared__ float factor[kMaxGrid];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int d = a.c.d, ld = a.TM * (d + 2);
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -115,25 +116,40 @@ cache_join_kernel(const __grid_constant__ AttnArgs a, int ctas) {
             continue;
         }
         const int r = i - first[lo];
-        float M = -INFINITY;
-        if (SM) {
-            for (int p = lane; p < t.parts; p += 32) M = fmaxf(M, slot(p)[a.TM * d + r]);
+        float M = -INFINITY, l = 0.0f;
+        if (SM) {   // a thread a part: the largest maximum, the parts' factors and the sum
+            float m = -INFINITY, n = 0.0f;
+            if (tid < t.parts) {
+                m = slot(tid)[a.TM * d + r];
+                n = slot(tid)[a.TM * (d + 1) + r];
+            }
+            M = m;
+            for (int p = tid + kJoinThreads; p < t.parts; p += kJoinThreads) M = fmaxf(M, slot(p)[a.TM * d + r]);
 #pragma unroll
-            for (int m = 1; m < 32; m <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
-        }
-        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        float l = 0.0f;
-#pragma unroll 4
-        for (int p = warp; p < t.parts; p += kJoinWarps) {
-            const float* s = slot(p);
-            float f = 1.0f;
-            if (SM) {
-                const float m = s[a.TM * d + r], n = s[a.TM * (d + 1) + r];
-                f = part_factor(m, n, M);
+            for (int k = 1; k < 32; k <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+            if (lane == 0) ml[warp].x = M;
+            __syncthreads();
+            for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, ml[w].x);
+            for (int p = tid; p < t.parts; p += kJoinThreads) {
+                if (p != tid) {
+                    m = slot(p)[a.TM * d + r];
+                    n = slot(p)[a.TM * (d + 1) + r];
+                }
+                const float f = part_factor(m, n, M);
+                factor[p] = f;
                 l += n * f;
             }
+#pragma unroll
+            for (int k = 1; k < 32; k <<= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+            if (lane == 0) ml[warp].y = l;
+            __syncthreads();
+        }
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+        for (int p = warp; p < t.parts; p += kJoinWarps) {
             if (4 * lane < d) {
-                const float4 y = *reinterpret_cast<const float4*>(s + r * d + 4 * lane);
+                const float4 y = *reinterpret_cast<const float4*>(slot(p) + r * d + 4 * lane);
+                const float f = SM ? factor[p] : 1.0f;
                 x.x += y.x * f;
                 x.y += y.y * f;
                 x.z += y.z * f;
@@ -141,16 +157,18 @@ cache_join_kernel(const __grid_constant__ AttnArgs a, int ctas) {
             }
         }
         sums[warp][lane] = x;
-        if (lane == 0) ml[warp] = make_float2(M, l);
         __syncthreads();
         if (warp == 0) {
-            for (int w = 1; w < kJoinWarps; ++w) {
-                const float4 y = sums[w][lane];
-                x.x += y.x;
-                x.y += y.y;
-                x.z += y.z;
-                x.w += y.w;
-                l += ml[w].y;
+            l = 0.0f;
+            for (int w = 0; w < kJoinWarps; ++w) {
+                if (w > 0) {
+                    const float4 y = sums[w][lane];
+                    x.x += y.x;
+                    x.y += y.y;
+                    x.z += y.z;
+                    x.w += y.w;
+                }
+                if (SM) l += ml[w].y;
             }
             put_row<E, SM>(a, t, r, lane, x, M, l);
         }
@@ -203,15 +221,15 @@ gdpa_status shape(const CacheView& c, gdpa_dtype dt, int64_t T, int H, int B, Sh
         s.RT = 0;
         s.TM = rows <= 128 ? 128 : 256;
         s.grid = s.sms;
-        s.min_share = 48;
-        s.lead = 32;
+        s.min_share = 16;
+        s.lead = 64;
     } else {
         // row tiles of 16 that a CTA holds: as many as an average sample fills
         s.RT = s.kind == kSimt || rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
         s.TM = s.kind == kMma && rows <= 8 ? 8 : 16 * s.RT;
         s.grid = s.sms * (s.kind == kSimt ? kCacheSimtPerSm : s.TM == 8 ? 3 : 2);   // resident
-        s.lead = 12 / s.RT;
-        s.min_share = s.lead + 4 / s.RT;
+        s.lead = 20 / s.RT;
+        s.min_share = 4 / s.RT;
     }
     if (s.grid > kMaxGrid) s.grid = kMaxGrid;
     s.bytes = (int64_t)s.grid * (sizeof(CacheDesc) + 2ll * s.TM * (c.d + 2) * 4);
