@@ -300,18 +300,14 @@ __device__ __forceinline__ float inverse_power(float x) {
 }
 
 // two values of a query row (below 256) as E4M3 codes, and what these leave of
-// them: E4M3 codes of 2^5 times it (LIFT: for sums of their own) or E5M2 ones
-template <bool LIFT>
+// them as E5M2 ones
 __device__ __forceinline__ void split_q(float x, float y, uint32_t& hi, uint32_t& lo) {
     uint16_t h, l;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(y), "f"(x));
     uint32_t f;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(h));
     const float2 v = __half22float2(*reinterpret_cast<__half2*>(&f));
-    if constexpr (LIFT)
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(l) : "f"((y - v.y) * 32.0f), "f"((x - v.x) * 32.0f));
-    else
-        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(l) : "f"(y - v.y), "f"(x - v.x));
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(l) : "f"(y - v.y), "f"(x - v.x));
     hi = h;
     lo = l;
 }

@@ -14,12 +14,12 @@
 // (KS = 4 / RT of them, the others hold further 16-row tiles of the same events)
 // and join their sums in shared memory.
 //
-// 8-bit keys are multiplied as they are (m16n8k32): S = 2^(e_k + e_q) (q' + 2^-5
-// q'') . c, where q' are the codes of the row scaled by a power of two to below
-// 256 and q'' those of 2^5 times the rest, two E4M3 numbers of 4 bits for bf16's 8
-// (elements below 2^-15 of the largest lose bits, at most 2^-22 of it).  Such a
-// product takes half of an f16 one's time for twice the depth, and saves the
-// conversions.  8-bit values become f16 (exactly).  Their rows' powers of two go
+// 8-bit codes become f16 (exactly) and their products are f16 ones: S =
+// 2^(e_k + e_q) q' . c, where q' is the row scaled by a power of two to below 2,
+// in f16 (bf16's 8 bits fit; elements below 2^-14 of the largest lose bits, at
+// most 2^-25 of it).  (Products of E4M3 operands, m16n8k32, are converted to f16
+// ones by the compiler, and Q needs two of them: 217 us, not 197, for 256 users'
+// 8-bit histories.)  The value rows' powers of two go
 // into the weights, w 2^e_v F, rounded to f16; F is a power of two that keeps the
 // largest w 2^e_v that O holds within [2^-6, 2^8], moved (and O with it) when
 // it leaves that range, so that rows of any size keep f16's 11 bits.  bf16

@@ -69,11 +69,6 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 template <bool FP8>
 __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     if constexpr (FP8) mma_f16(c, a[0], a[1], a[2], a[3], b0, b1);
@@ -167,11 +162,10 @@ __device__ __forceinline__ void load_query(const AttnArgs& a, const Segment& g, 
     }
 }
 
-// The same for 8-bit keys: codes of the row times a power of two, and of 2^5
-// times what they leave; two words (8 codes) a step of 32.  Returns the factor
-// that undoes the power.
+// The same for 8-bit keys: f16 values of the row times a power of two that brings
+// its largest to [1, 2).  Returns the factor that undoes it.
 template <int STEPS>
-__device__ __forceinline__ float split_query(const uint32_t (&w)[STEPS][2], uint32_t (&hi)[STEPS / 2][2], uint32_t (&lo)[STEPS / 2][2]) {
+__device__ __forceinline__ float scale_query(uint32_t (&w)[STEPS][2]) {
     float top = 0.0f;
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)
@@ -181,14 +175,10 @@ __device__ __forceinline__ float split_query(const uint32_t (&w)[STEPS][2], uint
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const float f = inverse_power(top);   // of infinities: whatever, their products are
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-        uint32_t h[2], l[2];
+    for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) split_q<true>(bf16_lo(w[s][j]) * f * 128.0f, bf16_hi(w[s][j]) * f * 128.0f, h[j], l[j]);
-        hi[s >> 1][s & 1] = h[0] | h[1] << 16;
-        lo[s >> 1][s & 1] = l[0] | l[1] << 16;
-    }
-    return 0x1p-7f / f;
+        for (int j = 0; j < 2; ++j) w[s][j] = pack_f16(bf16_lo(w[s][j]) * f, bf16_hi(w[s][j]) * f);
+    return 1.0f / f;
 }
 
 // The running state of a thread's two rows, and what is the same for both forms.
@@ -247,23 +237,29 @@ struct RowState {
     // scale(f): the rows' O times f.
     template <int NE, typename Event, typename Over, typename Scale>
     __device__ __forceinline__ void weigh(const AttnArgs& a, float (&s)[2][NE], const float (&vs)[NE], Event event, Over over, Scale scale) {
-        const auto hidden = [&](int x, int k) { return masked && !(bits[x][event(k) >> 4] >> (event(k) & 15) & 1u); };
+        // of what no row hides nothing is looked at
+        const auto where_hidden = [&](float v) {
+            if (!masked) return;
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int k = 0; k < NE; ++k)
+                    if (!(bits[x][event(k) >> 4] >> (event(k) & 15) & 1u)) s[x][k] = v;
+        };
         float f[2];
         if constexpr (SM) {
+            where_hidden(-INFINITY);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                float mt = -INFINITY;
+                float mt = s[x][0];
 #pragma unroll
-                for (int k = 0; k < NE; ++k) {
-                    if (hidden(x, k)) s[x][k] = -INFINITY;
-                    mt = fmaxf(mt, s[x][k]);
-                }
+                for (int k = 1; k < NE; ++k) mt = fmaxf(mt, s[x][k]);
                 mt = over(mt);
                 // the reference moves when it would be passed by more than 8 (weights below 2^8)
                 f[x] = 1.0f;
                 if (mt > m[x] + 8.0f || m[x] == -INFINITY) {
                     f[x] = m[x] == -INFINITY ? 0.0f : ex2_approx(m[x] - mt);
-                    m[x] = mt;
+                    m[x] = fmaxf(mt, -INFINITY);   // (of NaNs alone: none)
                 }
             }
             if (__any_sync(0xffffffffu, f[0] != 1.0f || f[1] != 1.0f)) {
@@ -296,19 +292,21 @@ struct RowState {
                         case kTaylor6: w = act_f<kTaylor6, true>(w); break;
                         default: break;
                     }
-                    if (hidden(x, k)) w = 0.0f;
                 }
+            if constexpr (!FP8) where_hidden(0.0f);
         }
         if constexpr (FP8) {
             // weights times the values' powers of two, in units of 1 / F
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                float big = 0.0f;
+            for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int k = 0; k < NE; ++k) {
-                    s[x][k] = hidden(x, k) ? 0.0f : s[x][k] * vs[k];
-                    big = fmaxf(big, fabsf(s[x][k]));
-                }
+                for (int k = 0; k < NE; ++k) s[x][k] *= vs[k];
+            where_hidden(0.0f);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float big = fabsf(s[x][0]);
+#pragma unroll
+                for (int k = 1; k < NE; ++k) big = fmaxf(big, fabsf(s[x][k]));
                 big = over(big);
                 top[x] = fmaxf(top[x], big);
                 const float now = top[x] * F[x];
@@ -360,22 +358,11 @@ struct Rows16 : RowState<D, FP8, SM, Cfg<D, FP8, false>::kTake> {
             uint32_t w[STEPS][2];
             load_query<D, FP8>(a, g, r0 + gq + 8 * x, this->rv[x].tok, t, w);
             this->qs[x] = a.alpha;
-            if constexpr (FP8) {
-                uint32_t hi[STEPS / 2][2], lo[STEPS / 2][2];
-                this->qs[x] *= split_query<STEPS>(w, hi, lo);
+            if constexpr (FP8) this->qs[x] *= scale_query<STEPS>(w);
 #pragma unroll
-                for (int s = 0; s < STEPS / 2; ++s)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        qf[s][2 * j + x] = hi[s][j];
-                        qf[STEPS / 2 + s][2 * j + x] = lo[s][j];
-                    }
-            } else {
-#pragma unroll
-                for (int s = 0; s < STEPS; ++s) {
-                    qf[s][x] = w[s][0];
-                    qf[s][2 + x] = w[s][1];
-                }
+            for (int s = 0; s < STEPS; ++s) {
+                qf[s][x] = w[s][0];
+                qf[s][2 + x] = w[s][1];
             }
         }
 #pragma unroll
@@ -392,7 +379,7 @@ struct Rows16 : RowState<D, FP8, SM, Cfg<D, FP8, false>::kTake> {
                                           const uint8_t* kv, const uint8_t* scales, int lane) {
         const int gq = lane >> 2, t = lane & 3;
         // S: events 8 n + gq are B columns; the thread's scores are events 8 n + 2 t + j
-        constexpr int SPLIT = FP8 || GN == 1 ? 2 : 1;   // independent sums: what is left of Q apart (8-bit), or every second step
+        constexpr int SPLIT = GN == 1 ? 2 : 1;   // independent sums of a tile: every second step apart
         float acc[2 * GN][SPLIT][4];
 #pragma unroll
         for (int n = 0; n < 2 * GN; ++n)
@@ -405,13 +392,12 @@ struct Rows16 : RowState<D, FP8, SM, Cfg<D, FP8, false>::kTake> {
             for (int n = 0; n < 2 * GN; ++n) w[n] = key_piece<D, FP8>(kv + (n >> 1) * 2 * C::kKeys, 8 * (n & 1) + gq, t, c);
             if constexpr (FP8) {
 #pragma unroll
-                for (int y = 0; y < 2; ++y)
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int n = 0; n < 2 * GN; ++n) mma_e4m3(acc[n][y], qf[y * (STEPS / 2) + 2 * c], w[n].x, w[n].y);
-#pragma unroll
-                for (int y = 0; y < 2; ++y)
-#pragma unroll
-                    for (int n = 0; n < 2 * GN; ++n) mma_e4m3(acc[n][y], qf[y * (STEPS / 2) + 2 * c + 1], w[n].z, w[n].w);
+                    for (int n = 0; n < 2 * GN; ++n) {
+                        const uint32_t x = (&w[n].x)[j];
+                        mma16<true>(acc[n][j % SPLIT], qf[4 * c + j], codes_lo(x), codes_hi(x));
+                    }
             } else {
 #pragma unroll
                 for (int n = 0; n < 2 * GN; ++n) mma16<false>(acc[n][0], qf[2 * c], w[n].x, w[n].y);
@@ -437,7 +423,7 @@ struct Rows16 : RowState<D, FP8, SM, Cfg<D, FP8, false>::kTake> {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int i = 2 * x + j;
-                    const float y = SPLIT == 1 ? acc[n][0][i] : FP8 ? fmaf(acc[n][SPLIT - 1][i], 0x1p-5f, acc[n][0][i]) : acc[n][0][i] + acc[n][SPLIT - 1][i];
+                    const float y = SPLIT == 1 ? acc[n][0][i] : acc[n][0][i] + acc[n][SPLIT - 1][i];
                     s[x][2 * n + j] = y * ks[j] * this->qs[x];
                 }
         }
@@ -553,23 +539,14 @@ struct Rows8 : RowState<D, FP8, SM, Cfg<D, FP8, true>::kTake> {
         load_query<D, FP8>(a, g, r0 + gq, row_view(a, g, r0 + gq).tok, t, w);
         this->qs[0] = this->qs[1] = a.alpha;
         if constexpr (FP8) {
-            uint32_t hi[STEPS / 2][2], lo[STEPS / 2][2];
-            const float f = split_query<STEPS>(w, hi, lo);
+            const float f = scale_query<STEPS>(w);
 #pragma unroll
             for (int x = 0; x < 2; ++x) this->qs[x] *= __shfl_sync(0xffffffffu, f, 4 * (2 * t + x));
+        }
 #pragma unroll
-            for (int s = 0; s < STEPS / 2; ++s)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    qf[s][j] = hi[s][j];
-                    qf[STEPS / 2 + s][j] = lo[s][j];
-                }
-        } else {
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-                qf[s][0] = w[s][0];
-                qf[s][1] = w[s][1];
-            }
+        for (int s = 0; s < STEPS; ++s) {
+            qf[s][0] = w[s][0];
+            qf[s][1] = w[s][1];
         }
 #pragma unroll
         for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
@@ -585,7 +562,7 @@ struct Rows8 : RowState<D, FP8, SM, Cfg<D, FP8, true>::kTake> {
                                           const uint8_t* kv, const uint8_t* scales, int lane) {
         const int gq = lane >> 2, t = lane & 3;
         // S^T: events gq and gq + 8 of a group are A rows, and the thread's scores with rows 2 t, 2 t + 1
-        constexpr int SPLIT = 2;   // independent sums: what is left of Q apart (8-bit), or every second step
+        constexpr int SPLIT = 2;   // independent sums of a group: every second step apart
         float acc[GN][SPLIT][4];
 #pragma unroll
         for (int u = 0; u < GN; ++u)
@@ -598,25 +575,24 @@ struct Rows8 : RowState<D, FP8, SM, Cfg<D, FP8, true>::kTake> {
             for (int u = 0; u < GN; ++u)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) w[u][h] = key_piece<D, FP8>(kv + u * 2 * C::kKeys, 8 * h + gq, t, c);
+            if constexpr (FP8) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                uint32_t k[GN][4];
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int u = 0; u < GN; ++u) {
-                    k[u][0] = j ? w[u][0].z : w[u][0].x;
-                    k[u][1] = j ? w[u][1].z : w[u][1].x;
-                    k[u][2] = j ? w[u][0].w : w[u][0].y;
-                    k[u][3] = j ? w[u][1].w : w[u][1].y;
-                }
-                if constexpr (FP8) {
+                    for (int u = 0; u < GN; ++u) {
+                        const uint32_t x = (&w[u][0].x)[j], y = (&w[u][1].x)[j];
+                        const uint32_t k[4] = {codes_lo(x), codes_lo(y), codes_hi(x), codes_hi(y)};
+                        mma16<true>(acc[u][j & 1], k, qf[4 * c + j][0], qf[4 * c + j][1]);
+                    }
+            } else {
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
-                        for (int u = 0; u < GN; ++u) mma_e4m3(acc[u][y], k[u], qf[y * (STEPS / 2) + 2 * c + j][0], qf[y * (STEPS / 2) + 2 * c + j][1]);
-                } else {
-#pragma unroll
-                    for (int u = 0; u < GN; ++u) mma16<false>(acc[u][j], k[u], qf[2 * c + j][0], qf[2 * c + j][1]);
-                }
+                    for (int u = 0; u < GN; ++u) {
+                        const uint32_t k[4] = {j ? w[u][0].z : w[u][0].x, j ? w[u][1].z : w[u][1].x, j ? w[u][0].w : w[u][0].y,
+                                               j ? w[u][1].w : w[u][1].y};
+                        mma16<false>(acc[u][j], k, qf[2 * c + j][0], qf[2 * c + j][1]);
+                    }
             }
         }
         float s[2][2 * GN], vs[2 * GN];
@@ -634,7 +610,7 @@ struct Rows8 : RowState<D, FP8, SM, Cfg<D, FP8, true>::kTake> {
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const int i = 2 * h + x;
-                    const float y = FP8 ? fmaf(acc[u][1][i], 0x1p-5f, acc[u][0][i]) : acc[u][0][i] + acc[u][1][i];
+                    const float y = acc[u][0][i] + acc[u][1][i];
                     s[x][2 * u + h] = y * ks * this->qs[x];
                 }
             }

@@ -14,8 +14,12 @@
 // What bounds it: every value is read and written once, so device memory; for
 // a handful of rows, the launch.  A thread owns 16 bytes of a bf16 or float32
 // row, neighbouring lanes the rest of the row, so that its largest value is a
-// few shuffles away and both sides are whole sectors.
+// few shuffles away and both sides are whole sectors; kPasses such pieces, whose
+// loads are all on their way before anything is done with the first (one after the
+// other: 156 us for the 430 MB of 256 histories written and read back).
 #include <string.h>
+
+#include <type_traits>
 
 #include "cache_internal.h"
 
@@ -23,6 +27,8 @@ namespace gdpa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kPasses = 4;       // pieces a thread takes
+constexpr int kMaxTokens = 512;  // of a block: pieces of two rows of one piece
 constexpr int kCounted = 1023;   // samples whose offsets a block counts through (as rotary positions do)
 
 struct StoreArgs {
@@ -31,7 +37,8 @@ struct StoreArgs {
     const void *k, *v;            // rows; written by reads
     int64_t kt, kh, vt, vh;       // strides in elements
     int items, lanes;             // 16-byte pieces of a row; rounded up to a power of two
-    int tokens;                   // of a block
+    int tokens, rows;             // of a block: tokens, and of the heads' K and V rows of each
+    int step_tok, step_row;       // a pass further on: tokens, rows (a pass's rows in tokens and the rest)
 };
 
 // The last sample that starts at or before `row`, among [lo, hi).
@@ -43,20 +50,62 @@ __device__ __forceinline__ int sample_of(const int32_t* off, int64_t row, int lo
     return lo;
 }
 
-// The samples that the block's rows [row0, row0 + n) can belong to.
-__device__ __forceinline__ void block_samples(const CacheWhere& w, int64_t row0, int n, int& lo, int& hi) {
-    lo = 0;
-    hi = w.B;
-    if (w.B > kCounted) return;
-    int n0 = 0, n1 = 0;
-    for (int i = threadIdx.x; i - (int)threadIdx.x <= w.B; i += kThreads) {
-        const int64_t o = i <= w.B ? w.off[i] : INT64_MAX;
-        n0 += __syncthreads_count(o <= row0);
-        n1 += __syncthreads_count(o <= row0 + n - 1);
+// Where the block's tokens lie: a thread a token.  (The samples that they can
+// belong to by looking at all offsets at once.)
+struct Tokens {
+    int page[kMaxTokens], e[kMaxTokens];   // -1: no row of a sample, or outside the cache
+};
+
+__device__ __forceinline__ void find_tokens(const StoreArgs& a, int64_t row0, Tokens& t) {
+    const CacheWhere& w = a.w;
+    int lo = 0, hi = w.B;
+    if (w.B <= kCounted) {
+        int n0 = 0, n1 = 0;
+        for (int i = threadIdx.x; i - (int)threadIdx.x <= w.B; i += kThreads) {
+            const int64_t o = i <= w.B ? w.off[i] : INT64_MAX;
+            n0 += __syncthreads_count(o <= row0);
+            n1 += __syncthreads_count(o <= row0 + a.tokens - 1);
+        }
+        lo = max(n0 - 1, 0);
+        hi = min(n1, w.B);
     }
-    lo = max(n0 - 1, 0);
-    hi = min(n1, w.B);
+    const int64_t last = min(w.T, (int64_t)__ldg(w.off + w.B));
+    for (int i = threadIdx.x; i < a.tokens; i += kThreads) {
+        const int64_t row = row0 + i;
+        t.page[i] = t.e[i] = -1;
+        if (row >= last) continue;
+        const int b = sample_of(w.off, row, lo, hi);
+        const int64_t ev = row - __ldg(w.off + b) + (w.starts ? __ldg(w.starts + b) : 0);
+        const int64_t page = cache_block(a.c, w, b, ev, 0);
+        t.e[i] = 0;   // (a row, if not one with a page)
+        if (page < 0) continue;
+        t.page[i] = (int)(page / a.c.heads);
+        t.e[i] = (int)(ev & ((1 << a.c.page_log) - 1));
+    }
+    __syncthreads();
 }
+
+// What a thread's pieces are of, one pass after the other.
+struct Walk {
+    int tok, hv;      // token of the block, row of the token's 2 heads
+    const StoreArgs& a;
+    const int hv0;
+    __device__ __forceinline__ Walk(const StoreArgs& a, int first) : a(a), hv0(blockIdx.y * a.rows) {
+        tok = first / a.rows;
+        hv = first - tok * a.rows;
+    }
+    __device__ __forceinline__ void next() {
+        tok += a.step_tok;
+        hv += a.step_row;
+        if (hv >= a.rows) {
+            hv -= a.rows;
+            ++tok;
+        }
+    }
+    __device__ __forceinline__ bool is_v() const { return hv0 + hv >= a.c.heads; }
+    __device__ __forceinline__ int head() const { return hv0 + hv - (is_v() ? a.c.heads : 0); }
+    __device__ __forceinline__ bool inside() const { return tok < a.tokens && hv0 + hv < 2 * a.c.heads; }
+};
 
 __device__ __forceinline__ uint16_t to_e4m3x2(float lo, float hi) {
     uint16_t r;
@@ -85,72 +134,73 @@ __device__ __forceinline__ int piece_at(const CacheView& v, int e, int c) {
 template <int N> struct Codes;
 template <> struct Codes<8> { using T = uint2; };
 template <> struct Codes<4> { using T = uint32_t; };
+template <> struct Codes<16> { using T = uint4; };
 
 // E: the rows' type; FP8: 8-bit cache; WIDE: rows in 16-byte loads.
 template <typename E, bool FP8, bool WIDE>
 __global__ void __launch_bounds__(kThreads)
 cache_write_kernel(const __grid_constant__ StoreArgs a) {
     constexpr int N = 16 / (int)sizeof(E);               // values of a piece
+    __shared__ Tokens at;
     const int64_t row0 = (int64_t)blockIdx.x * a.tokens;
-    int lo, hi;
-    block_samples(a.w, row0, a.tokens, lo, hi);
-    const int sub = threadIdx.x / a.lanes, c = threadIdx.x % a.lanes;
-    const int per = kThreads / a.lanes;                  // rows a pass
-    const int heads2 = 2 * a.c.heads;
-    const int64_t last = min(a.w.T, (int64_t)__ldg(a.w.off + a.w.B));
-    const int n = a.tokens * heads2;
-    for (int i0 = 0; i0 < n; i0 += per) {                // whole warps stay together
-        const int i = i0 + sub;
-        const int tok = i / heads2, hv = i - tok * heads2;
-        const bool is_v = hv >= a.c.heads;
-        const int h = is_v ? hv - a.c.heads : hv;
-        const int64_t row = row0 + tok;
-        bool live = i < n && row < last && c < a.items;
-        alignas(16) E x[N] = {};
-        int64_t blk = -1;
-        int e = 0;
-        if (live) {
-            const E* src = is_v ? (const E*)a.v + row * a.vt + h * a.vh : (const E*)a.k + row * a.kt + h * a.kh;
+    const int sub = threadIdx.x / a.lanes, c = threadIdx.x - sub * a.lanes;
+    alignas(16) E xs[kPasses][N];
+    const Walk start(a, sub);
+    Walk w = start;
+#pragma unroll
+    for (int k = 0; k < kPasses; ++k, w.next()) {
+        const int64_t row = row0 + w.tok;
+        *reinterpret_cast<uint4*>(xs[k]) = make_uint4(0, 0, 0, 0);
+        if (w.inside() && row < a.w.T && c < a.items) {
+            const E* src = w.is_v() ? (const E*)a.v + row * a.vt + w.head() * a.vh : (const E*)a.k + row * a.kt + w.head() * a.kh;
             if constexpr (WIDE) {
-                *reinterpret_cast<uint4*>(x) = __ldg(reinterpret_cast<const uint4*>(src) + c);
+                *reinterpret_cast<uint4*>(xs[k]) = __ldg(reinterpret_cast<const uint4*>(src) + c);
             } else {
 #pragma unroll
-                for (int j = 0; j < N; ++j) x[j] = src[c * N + j];
+                for (int j = 0; j < N; ++j) xs[k][j] = src[c * N + j];
             }
-            const int b = sample_of(a.w.off, row, lo, hi);
-            const int64_t ev = row - __ldg(a.w.off + b) + (a.w.starts ? __ldg(a.w.starts + b) : 0);
-            blk = cache_block(a.c, a.w, b, ev, h);
-            e = (int)(ev & ((1 << a.c.page_log) - 1));
         }
+    }
+    find_tokens(a, row0, at);
+    Walk v = start;
+#pragma unroll
+    for (int k = 0; k < kPasses; ++k, v.next()) {        // whole warps stay together
+        const bool live = v.inside() && c < a.items && at.page[v.tok] >= 0;
+        const bool is_v = v.is_v();
+        const E (&x)[N] = xs[k];
+        const int64_t blk = live ? (int64_t)at.page[v.tok] * a.c.heads + v.head() : 0;
+        const int e = live ? at.e[v.tok] : 0;
         uint8_t* dst = (is_v ? a.c.v : a.c.k) + blk * a.c.block;
         if constexpr (FP8) {
-            float top = 0.0f;
-            bool odd = false;                            // an infinity or a NaN
+            // the row's largest magnitude as float32 bits: those of an infinity or
+            // a NaN are above every number's
+            uint32_t top = 0;
+            if constexpr (sizeof(E) == 2) {
+                const uint32_t* p = reinterpret_cast<const uint32_t*>(x);
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const float f = fabsf(to_f(x[j]));
-                odd |= !(f <= 3.402823466e38f);
-                top = fmaxf(top, f);
+                for (int j = 0; j < N / 2; ++j) top = __vmaxu2(top, p[j] & 0x7fff7fffu);
+                for (int m = 1; m < a.lanes; m <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, m));
+                top = max(top & 0xffff0000u, top << 16);
+            } else {
+                const uint32_t* p = reinterpret_cast<const uint32_t*>(x);
+#pragma unroll
+                for (int j = 0; j < N; ++j) top = max(top, p[j] & 0x7fffffffu);
+                for (int m = 1; m < a.lanes; m <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
             }
-            for (int m = 1; m < a.lanes; m <<= 1) {
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-                odd |= __shfl_xor_sync(0xffffffffu, (int)odd, m) != 0;
-            }
+            const bool odd = top >= 0x7f800000u;
             // top = m 2^x with m in [1, 2): 448 = 1.75 2^8
-            const uint32_t bits = __float_as_uint(top);
-            const int ex = max((int)(bits >> 23) - 127 - ((bits & 0x7fffffu) <= 0x600000u ? 8 : 7), -126);
+            const int ex = max((int)(top >> 23) - 127 - ((top & 0x7fffffu) <= 0x600000u ? 8 : 7), -126);
             const float inv = odd ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 - ex) << 23);
             alignas(8) uint16_t p[N / 2];
 #pragma unroll
             for (int j = 0; j < N / 2; ++j) p[j] = to_e4m3x2(to_f(x[2 * j]) * inv, to_f(x[2 * j + 1]) * inv);
-            if (live && blk >= 0) {
+            if (live) {
                 using T = typename Codes<N>::T;
                 *reinterpret_cast<T*>(dst + piece_at<true, N>(a.c, e, c)) = *reinterpret_cast<const T*>(p);
                 if (c == 0) (is_v ? a.c.vs : a.c.ks)[(blk << a.c.page_log) + e] = (uint8_t)(odd ? 255 : ex + 127);
             }
         } else {
-            if (live && blk >= 0)
-                *reinterpret_cast<uint4*>(dst + piece_at<false, N>(a.c, e, c)) = *reinterpret_cast<const uint4*>(x);
+            if (live) *reinterpret_cast<uint4*>(dst + piece_at<false, N>(a.c, e, c)) = *reinterpret_cast<const uint4*>(x);
         }
     }
 }
@@ -160,59 +210,63 @@ template <typename E, bool FP8>
 __global__ void __launch_bounds__(kThreads)
 cache_read_kernel(const __grid_constant__ StoreArgs a) {
     constexpr int N = 16 / (int)sizeof(E);
+    __shared__ Tokens at;
     const int64_t row0 = (int64_t)blockIdx.x * a.tokens;
-    int lo, hi;
-    block_samples(a.w, row0, a.tokens, lo, hi);
-    const int heads2 = 2 * a.c.heads;
-    const int64_t last = min(a.w.T, (int64_t)__ldg(a.w.off + a.w.B));
-    const int n = a.tokens * heads2 * a.items;
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        const int r = i / a.items, c = i - r * a.items;
-        const int tok = r / heads2, hv = r - tok * heads2;
-        const bool is_v = hv >= a.c.heads;
-        const int h = is_v ? hv - a.c.heads : hv;
-        const int64_t row = row0 + tok;
-        if (row >= last) break;                          // (rows ascend with i)
-        const int b = sample_of(a.w.off, row, lo, hi);
-        const int64_t ev = row - __ldg(a.w.off + b) + (a.w.starts ? __ldg(a.w.starts + b) : 0);
-        const int64_t blk = cache_block(a.c, a.w, b, ev, h);
-        alignas(16) E x[N] = {};                         // rows without a page read as zeros
-        if (blk >= 0) {
-            const int e = (int)(ev & ((1 << a.c.page_log) - 1));
-            const uint8_t* src = (is_v ? a.c.v : a.c.k) + blk * a.c.block;
-            const uint8_t* q = src + piece_at<FP8, N>(a.c, e, c);
-            if constexpr (FP8) {
-                using T = typename Codes<N>::T;
-                const float s = cache_scale((is_v ? a.c.vs : a.c.ks)[(blk << a.c.page_log) + e]);
-                alignas(8) uint16_t p[N / 2];
-                *reinterpret_cast<T*>(p) = *reinterpret_cast<const T*>(q);
+    find_tokens(a, row0, at);
+    const int sub = threadIdx.x / a.items, c = threadIdx.x - sub * a.items;
+    if (sub >= kThreads / a.items) return;               // (threads that a pass leaves over)
+    using T = typename std::conditional_t<FP8, Codes<N>, Codes<16>>::T;   // a piece as the cache holds it
+    T qs[kPasses];
+    uint32_t sc[kPasses];
+    const Walk start(a, sub);
+    Walk w = start;
 #pragma unroll
-                for (int j = 0; j < N / 2; ++j) {
-                    const float2 f = from_e4m3x2(p[j]);
-                    put(x[2 * j], f.x * s);
-                    put(x[2 * j + 1], f.y * s);
-                }
-            } else {
-                *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(q);
-            }
+    for (int k = 0; k < kPasses; ++k, w.next()) {
+        qs[k] = T{};                                     // rows without a page read as zeros
+        sc[k] = 127;
+        if (w.inside() && at.page[w.tok] >= 0) {
+            const int64_t blk = (int64_t)at.page[w.tok] * a.c.heads + w.head();
+            const int e = at.e[w.tok];
+            qs[k] = *reinterpret_cast<const T*>((w.is_v() ? a.c.v : a.c.k) + blk * a.c.block + piece_at<FP8, N>(a.c, e, c));
+            if constexpr (FP8) sc[k] = (w.is_v() ? a.c.vs : a.c.ks)[(blk << a.c.page_log) + e];
         }
-        E* dst = is_v ? (E*)a.v + row * a.vt + h * a.vh : (E*)a.k + row * a.kt + h * a.kh;
+    }
+    Walk v = start;
+#pragma unroll
+    for (int k = 0; k < kPasses; ++k, v.next()) {
+        if (!v.inside() || at.e[v.tok] < 0) continue;
+        const int64_t row = row0 + v.tok;
+        alignas(16) E x[N];
+        if constexpr (FP8) {
+            const float s = cache_scale(sc[k]);
+            alignas(8) uint16_t p[N / 2];
+            *reinterpret_cast<T*>(p) = qs[k];
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) {
+                const float2 f = from_e4m3x2(p[j]);
+                put(x[2 * j], f.x * s);
+                put(x[2 * j + 1], f.y * s);
+            }
+        } else {
+            *reinterpret_cast<T*>(x) = qs[k];
+        }
+        E* dst = v.is_v() ? (E*)a.v + row * a.vt + v.head() * a.vh : (E*)a.k + row * a.kt + v.head() * a.kh;
         reinterpret_cast<uint4*>(dst)[c] = *reinterpret_cast<const uint4*>(x);
     }
 }
 
-// Tokens a block: about 4 passes of its threads, fewer while that leaves SMs idle.
-int block_tokens(int64_t T, int items) {
-    int64_t tok = 4 * kThreads / items;
-    while (tok > 1 && (T + tok - 1) / tok < 4 * 152) tok = (tok + 1) / 2;
-    return (int)(tok < 1 ? 1 : tok);
-}
-
-gdpa_status launch(void (*f)(const StoreArgs), StoreArgs& a, int items, cudaStream_t st) {
-    a.tokens = block_tokens(a.w.T, items);
+// A block's part: as many of a token's rows as its passes hold (`width` threads a
+// row), and then as many tokens, fewer while that leaves SMs idle.
+gdpa_status launch(void (*f)(const StoreArgs), StoreArgs& a, int width, cudaStream_t st) {
+    const int heads2 = 2 * a.c.heads, room = kPasses * (kThreads / width);
+    a.rows = heads2 < room ? heads2 : room;
+    a.tokens = room / a.rows;
+    while (a.tokens > 1 && (a.w.T + a.tokens - 1) / a.tokens < 4 * 152) a.tokens = (a.tokens + 1) / 2;
+    a.step_tok = kThreads / width / a.rows;
+    a.step_row = kThreads / width - a.step_tok * a.rows;
     const int64_t blocks = (a.w.T + a.tokens - 1) / a.tokens;
     if (blocks > 0x7fffffff) return GDPA_ERR_UNSUPPORTED;
-    f<<<(unsigned)blocks, kThreads, 0, st>>>(a);
+    f<<<dim3((unsigned)blocks, (unsigned)((heads2 + a.rows - 1) / a.rows)), kThreads, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
 }
 
@@ -326,7 +380,7 @@ gdpa_status gdpa_cache_write(const gdpa_cache* cache, gdpa_dtype dtype, int64_t 
         f = fp8 ? wide ? cache_write_kernel<E, true, true> : cache_write_kernel<E, true, false>
                 : wide ? cache_write_kernel<E, false, true> : cache_write_kernel<E, false, false>;
     }
-    return launch(f, a, 2 * a.c.heads * a.lanes, (cudaStream_t)stream);
+    return launch(f, a, a.lanes, (cudaStream_t)stream);
 }
 
 gdpa_status gdpa_cache_read(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T, const gdpa_cache_rows* k,
@@ -344,7 +398,7 @@ gdpa_status gdpa_cache_read(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T
         f = fp8 ? cache_read_kernel<__nv_bfloat16, true> : cache_read_kernel<__nv_bfloat16, false>;
     else
         f = fp8 ? cache_read_kernel<float, true> : cache_read_kernel<float, false>;
-    return launch(f, a, 2 * a.c.heads * a.items, (cudaStream_t)stream);
+    return launch(f, a, a.items, (cudaStream_t)stream);
 }
 
 gdpa_status gdpa_cache_check(const gdpa_cache* cache, int32_t* detail, void* stream) {

@@ -621,7 +621,7 @@ __device__ __forceinline__ void put_queries(const AttnArgs& a, const Segment& g,
                 const float f = inverse_power(top);   // of infinities: whatever, their products are
                 uint32_t h[4], l[4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) split_q<false>(bf16_lo(p[x]) * f * 128.0f, bf16_hi(p[x]) * f * 128.0f, h[x], l[x]);
+                for (int x = 0; x < 4; ++x) split_q(bf16_lo(p[x]) * f * 128.0f, bf16_hi(p[x]) * f * 128.0f, h[x], l[x]);
                 const int to = cache_chunk(D, 7, row, c >> 1) + 8 * (c & 1);
                 *reinterpret_cast<uint2*>(dst + to) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
                 *reinterpret_cast<uint2*>(dst + 128 * D + to) = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
