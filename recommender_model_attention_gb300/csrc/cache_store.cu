@@ -19,8 +19,6 @@
 // other: 156 us for the 430 MB of 256 histories written and read back).
 #include <string.h>
 
-#include <type_traits>
-
 #include "cache_internal.h"
 
 namespace gdpa {
@@ -28,7 +26,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPasses = 4;       // pieces a thread takes
-constexpr int kMaxTokens = 512;  // of a block: pieces of two rows of one piece
+constexpr int kMaxTokens = 512;  // of a block: two rows of one piece each
 constexpr int kCounted = 1023;   // samples whose offsets a block counts through (as rotary positions do)
 
 struct StoreArgs {
@@ -36,7 +34,8 @@ struct StoreArgs {
     CacheWhere w;
     const void *k, *v;            // rows; written by reads
     int64_t kt, kh, vt, vh;       // strides in elements
-    int items, lanes;             // 16-byte pieces of a row; rounded up to a power of two
+    int items, lanes;             // 16-byte pieces of a cache row; rounded up to a power of two
+    int sectors;                  // rows in whole sectors of 32 bytes
     int tokens, rows;             // of a block: tokens, and of the heads' K and V rows of each
     int step_tok, step_row;       // a pass further on: tokens, rows (a pass's rows in tokens and the rest)
 };
@@ -124,23 +123,36 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float
 __device__ __forceinline__ void put(float& y, float v) { y = v; }
 __device__ __forceinline__ void put(__nv_bfloat16& y, float v) { y = __float2bfloat16_rn(v); }
 
-// Where the N values of piece c of a row's N-value pieces lie within a block.
-template <bool FP8, int N>
-__device__ __forceinline__ int piece_at(const CacheView& v, int e, int c) {
-    if constexpr (!FP8) return cache_chunk(v.row, v.page_log, e, c);
-    constexpr int P = 16 / N;   // pieces of a chunk
-    return cache_chunk(v.row, v.page_log, e, c / P) + (c % P) * N;
+// N values at p, in 16-byte loads.
+template <typename E, int N>
+__device__ __forceinline__ void load_piece(const E* p, E (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N * (int)sizeof(E) / 16; ++i) reinterpret_cast<uint4*>(x)[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
 }
-template <int N> struct Codes;
-template <> struct Codes<8> { using T = uint2; };
-template <> struct Codes<4> { using T = uint32_t; };
-template <> struct Codes<16> { using T = uint4; };
+// N values to p: whole sectors in one store where they are aligned to them.
+template <typename E, int N>
+__device__ __forceinline__ void store_piece(E* p, const E (&x)[N], bool sectors) {
+    const uint32_t* v = reinterpret_cast<const uint32_t*>(x);
+    if constexpr (N * sizeof(E) >= 32) {
+        if (sectors) {
+#pragma unroll
+            for (int i = 0; i < N * (int)sizeof(E) / 32; ++i)
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"((char*)p + 32 * i), "r"(v[8 * i]),
+                             "r"(v[8 * i + 1]), "r"(v[8 * i + 2]), "r"(v[8 * i + 3]), "r"(v[8 * i + 4]), "r"(v[8 * i + 5]),
+                             "r"(v[8 * i + 6]), "r"(v[8 * i + 7])
+                             : "memory");
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N * (int)sizeof(E) / 16; ++i) reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(x)[i];
+}
 
 // E: the rows' type; FP8: 8-bit cache; WIDE: rows in 16-byte loads.
 template <typename E, bool FP8, bool WIDE>
 __global__ void __launch_bounds__(kThreads)
 cache_write_kernel(const __grid_constant__ StoreArgs a) {
-    constexpr int N = 16 / (int)sizeof(E);               // values of a piece
+    constexpr int N = FP8 ? 16 : 16 / (int)sizeof(E);    // values of a piece
     __shared__ Tokens at;
     const int64_t row0 = (int64_t)blockIdx.x * a.tokens;
     const int sub = threadIdx.x / a.lanes, c = threadIdx.x - sub * a.lanes;
@@ -150,11 +162,12 @@ cache_write_kernel(const __grid_constant__ StoreArgs a) {
 #pragma unroll
     for (int k = 0; k < kPasses; ++k, w.next()) {
         const int64_t row = row0 + w.tok;
-        *reinterpret_cast<uint4*>(xs[k]) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < N * (int)sizeof(E) / 16; ++j) reinterpret_cast<uint4*>(xs[k])[j] = make_uint4(0, 0, 0, 0);
         if (w.inside() && row < a.w.T && c < a.items) {
             const E* src = w.is_v() ? (const E*)a.v + row * a.vt + w.head() * a.vh : (const E*)a.k + row * a.kt + w.head() * a.kh;
             if constexpr (WIDE) {
-                *reinterpret_cast<uint4*>(xs[k]) = __ldg(reinterpret_cast<const uint4*>(src) + c);
+                load_piece<E, N>(src + c * N, xs[k]);
             } else {
 #pragma unroll
                 for (int j = 0; j < N; ++j) xs[k][j] = src[c * N + j];
@@ -191,16 +204,15 @@ cache_write_kernel(const __grid_constant__ StoreArgs a) {
             // top = m 2^x with m in [1, 2): 448 = 1.75 2^8
             const int ex = max((int)(top >> 23) - 127 - ((top & 0x7fffffu) <= 0x600000u ? 8 : 7), -126);
             const float inv = odd ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)(127 - ex) << 23);
-            alignas(8) uint16_t p[N / 2];
+            alignas(16) uint16_t p[N / 2];
 #pragma unroll
             for (int j = 0; j < N / 2; ++j) p[j] = to_e4m3x2(to_f(x[2 * j]) * inv, to_f(x[2 * j + 1]) * inv);
             if (live) {
-                using T = typename Codes<N>::T;
-                *reinterpret_cast<T*>(dst + piece_at<true, N>(a.c, e, c)) = *reinterpret_cast<const T*>(p);
+                *reinterpret_cast<uint4*>(dst + cache_chunk(a.c.row, a.c.page_log, e, c)) = *reinterpret_cast<const uint4*>(p);
                 if (c == 0) (is_v ? a.c.vs : a.c.ks)[(blk << a.c.page_log) + e] = (uint8_t)(odd ? 255 : ex + 127);
             }
         } else {
-            if (live) *reinterpret_cast<uint4*>(dst + piece_at<false, N>(a.c, e, c)) = *reinterpret_cast<const uint4*>(x);
+            if (live) *reinterpret_cast<uint4*>(dst + cache_chunk(a.c.row, a.c.page_log, e, c)) = *reinterpret_cast<const uint4*>(x);
         }
     }
 }
@@ -209,25 +221,24 @@ cache_write_kernel(const __grid_constant__ StoreArgs a) {
 template <typename E, bool FP8>
 __global__ void __launch_bounds__(kThreads)
 cache_read_kernel(const __grid_constant__ StoreArgs a) {
-    constexpr int N = 16 / (int)sizeof(E);
+    constexpr int N = FP8 ? 16 : 16 / (int)sizeof(E);
     __shared__ Tokens at;
     const int64_t row0 = (int64_t)blockIdx.x * a.tokens;
     find_tokens(a, row0, at);
     const int sub = threadIdx.x / a.items, c = threadIdx.x - sub * a.items;
     if (sub >= kThreads / a.items) return;               // (threads that a pass leaves over)
-    using T = typename std::conditional_t<FP8, Codes<N>, Codes<16>>::T;   // a piece as the cache holds it
-    T qs[kPasses];
+    uint4 qs[kPasses];
     uint32_t sc[kPasses];
     const Walk start(a, sub);
     Walk w = start;
 #pragma unroll
     for (int k = 0; k < kPasses; ++k, w.next()) {
-        qs[k] = T{};                                     // rows without a page read as zeros
+        qs[k] = make_uint4(0, 0, 0, 0);                  // rows without a page read as zeros
         sc[k] = 127;
         if (w.inside() && at.page[w.tok] >= 0) {
             const int64_t blk = (int64_t)at.page[w.tok] * a.c.heads + w.head();
             const int e = at.e[w.tok];
-            qs[k] = *reinterpret_cast<const T*>((w.is_v() ? a.c.v : a.c.k) + blk * a.c.block + piece_at<FP8, N>(a.c, e, c));
+            qs[k] = *reinterpret_cast<const uint4*>((w.is_v() ? a.c.v : a.c.k) + blk * a.c.block + cache_chunk(a.c.row, a.c.page_log, e, c));
             if constexpr (FP8) sc[k] = (w.is_v() ? a.c.vs : a.c.ks)[(blk << a.c.page_log) + e];
         }
     }
@@ -239,8 +250,8 @@ cache_read_kernel(const __grid_constant__ StoreArgs a) {
         alignas(16) E x[N];
         if constexpr (FP8) {
             const float s = cache_scale(sc[k]);
-            alignas(8) uint16_t p[N / 2];
-            *reinterpret_cast<T*>(p) = qs[k];
+            alignas(16) uint16_t p[8];
+            *reinterpret_cast<uint4*>(p) = qs[k];
 #pragma unroll
             for (int j = 0; j < N / 2; ++j) {
                 const float2 f = from_e4m3x2(p[j]);
@@ -248,10 +259,10 @@ cache_read_kernel(const __grid_constant__ StoreArgs a) {
                 put(x[2 * j + 1], f.y * s);
             }
         } else {
-            *reinterpret_cast<T*>(x) = qs[k];
+            *reinterpret_cast<uint4*>(x) = qs[k];
         }
         E* dst = v.is_v() ? (E*)a.v + row * a.vt + v.head() * a.vh : (E*)a.k + row * a.kt + v.head() * a.kh;
-        reinterpret_cast<uint4*>(dst)[c] = *reinterpret_cast<const uint4*>(x);
+        store_piece<E, N>(dst + c * N, x, a.sectors);
     }
 }
 
@@ -284,16 +295,18 @@ gdpa_status store_args(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T, con
     const size_t es = dtype == GDPA_BF16 ? 2 : 4;
     const gdpa_cache_rows* r[2] = {k, v};
     wide = true;
+    a.sectors = 1;
     for (int i = 0; i < 2; ++i) {
         if (T > 0 && (!r[i]->x || (uintptr_t)r[i]->x % es)) return GDPA_ERR_INVALID_ARG;
         // strides that are never stepped: a single row's, a single head's
         const int64_t t = T > 1 ? r[i]->token : 0, h = a.c.heads > 1 ? r[i]->head : 0;
         if ((uintptr_t)r[i]->x % 16 || t * es % 16 || h * es % 16) wide = false;
+        if ((uintptr_t)r[i]->x % 32 || t * es % 32 || h * es % 32) a.sectors = 0;
         (i ? a.v : a.k) = r[i]->x;
         (i ? a.vt : a.kt) = t;
         (i ? a.vh : a.kh) = h;
     }
-    a.items = a.c.d * (int)es / 16;
+    a.items = a.c.row / 16;
     for (a.lanes = 1; a.lanes < a.items; a.lanes *= 2) {}
     return GDPA_OK;
 }
