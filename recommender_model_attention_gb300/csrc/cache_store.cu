@@ -25,7 +25,9 @@ namespace gdpa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPasses = 4;       // pieces a thread takes
+// Pieces a thread takes (430 MB of 8-bit and bf16 rows: 88 us with 2, 82 with 4, 95
+// with 8; 64 bytes each, of float32 rows to write in 8 bits: 123 us with 2, 130 with 4)
+constexpr int kPasses = 4, kPassesLong = 2;
 constexpr int kMaxTokens = 512;  // of a block: two rows of one piece each
 constexpr int kCounted = 1023;   // samples whose offsets a block counts through (as rotary positions do)
 
@@ -156,11 +158,12 @@ cache_write_kernel(const __grid_constant__ StoreArgs a) {
     __shared__ Tokens at;
     const int64_t row0 = (int64_t)blockIdx.x * a.tokens;
     const int sub = threadIdx.x / a.lanes, c = threadIdx.x - sub * a.lanes;
-    alignas(16) E xs[kPasses][N];
+    constexpr int kN = FP8 && sizeof(E) == 4 ? kPassesLong : kPasses;
+    alignas(16) E xs[kN][N];
     const Walk start(a, sub);
     Walk w = start;
 #pragma unroll
-    for (int k = 0; k < kPasses; ++k, w.next()) {
+    for (int k = 0; k < kN; ++k, w.next()) {
         const int64_t row = row0 + w.tok;
 #pragma unroll
         for (int j = 0; j < N * (int)sizeof(E) / 16; ++j) reinterpret_cast<uint4*>(xs[k])[j] = make_uint4(0, 0, 0, 0);
@@ -177,7 +180,7 @@ cache_write_kernel(const __grid_constant__ StoreArgs a) {
     find_tokens(a, row0, at);
     Walk v = start;
 #pragma unroll
-    for (int k = 0; k < kPasses; ++k, v.next()) {        // whole warps stay together
+    for (int k = 0; k < kN; ++k, v.next()) {        // whole warps stay together
         const bool live = v.inside() && c < a.items && at.page[v.tok] >= 0;
         const bool is_v = v.is_v();
         const E (&x)[N] = xs[k];
@@ -268,8 +271,8 @@ cache_read_kernel(const __grid_constant__ StoreArgs a) {
 
 // A block's part: as many of a token's rows as its passes hold (`width` threads a
 // row), and then as many tokens, fewer while that leaves SMs idle.
-gdpa_status launch(void (*f)(const StoreArgs), StoreArgs& a, int width, cudaStream_t st) {
-    const int heads2 = 2 * a.c.heads, room = kPasses * (kThreads / width);
+gdpa_status launch(void (*f)(const StoreArgs), StoreArgs& a, int width, int passes, cudaStream_t st) {
+    const int heads2 = 2 * a.c.heads, room = passes * (kThreads / width);
     a.rows = heads2 < room ? heads2 : room;
     a.tokens = room / a.rows;
     while (a.tokens > 1 && (a.w.T + a.tokens - 1) / a.tokens < 4 * 152) a.tokens = (a.tokens + 1) / 2;
@@ -393,7 +396,7 @@ gdpa_status gdpa_cache_write(const gdpa_cache* cache, gdpa_dtype dtype, int64_t 
         f = fp8 ? wide ? cache_write_kernel<E, true, true> : cache_write_kernel<E, true, false>
                 : wide ? cache_write_kernel<E, false, true> : cache_write_kernel<E, false, false>;
     }
-    return launch(f, a, a.lanes, (cudaStream_t)stream);
+    return launch(f, a, a.lanes, fp8 && dtype == GDPA_F32 ? kPassesLong : kPasses, (cudaStream_t)stream);
 }
 
 gdpa_status gdpa_cache_read(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T, const gdpa_cache_rows* k,
@@ -411,7 +414,7 @@ gdpa_status gdpa_cache_read(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T
         f = fp8 ? cache_read_kernel<__nv_bfloat16, true> : cache_read_kernel<__nv_bfloat16, false>;
     else
         f = fp8 ? cache_read_kernel<float, true> : cache_read_kernel<float, false>;
-    return launch(f, a, a.items, (cudaStream_t)stream);
+    return launch(f, a, a.items, kPasses, (cudaStream_t)stream);
 }
 
 gdpa_status gdpa_cache_check(const gdpa_cache* cache, int32_t* detail, void* stream) {
