@@ -17,6 +17,8 @@
 // repeat bit for bit.
 #pragma once
 
+#include <atomic>
+
 #include "act.cuh"
 #include "cache_internal.h"
 
@@ -379,6 +381,17 @@ __device__ __forceinline__ void finish_segment(const AttnArgs& a, const Segment&
         }
         put4((E*)a.o + row * d + c, x);
     }
+}
+
+// Let a kernel take `bytes` of shared memory; once a kernel and device.
+inline bool cache_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
 }
 
 gdpa_status launch_cache_mma(const AttnArgs& a, int grid, cudaStream_t st);

@@ -186,8 +186,8 @@ cache_mma_kernel(const __grid_constant__ AttnArgs a) {
 template <int D, bool FP8, bool SM, bool R8>
 gdpa_status launch(const AttnArgs& a, int grid, cudaStream_t st) {
     using C = Cfg<D, FP8, R8>;
-    if (cudaFuncSetAttribute(cache_mma_kernel<D, FP8, SM, R8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kBytes) != cudaSuccess)
-        return GDPA_ERR_CUDA;
+    static std::atomic<uint64_t> done{0};
+    if (!cache_smem((const void*)cache_mma_kernel<D, FP8, SM, R8>, C::kBytes, done)) return GDPA_ERR_CUDA;
     cache_mma_kernel<D, FP8, SM, R8><<<grid, kThreads, C::kBytes, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
 }

@@ -175,8 +175,8 @@ cache_simt_kernel(const __grid_constant__ AttnArgs a) {
 template <typename E, int STORE, bool SM>
 gdpa_status launch(const AttnArgs& a, int grid, cudaStream_t st) {
     const int bytes = 9 * 16 * (a.c.d + 4) * 4;
-    if (cudaFuncSetAttribute(cache_simt_kernel<E, STORE, SM>, cudaFuncAttributeMaxDynamicSharedMemorySize, 9 * 16 * 132 * 4) != cudaSuccess)
-        return GDPA_ERR_CUDA;
+    static std::atomic<uint64_t> done{0};
+    if (!cache_smem((const void*)cache_simt_kernel<E, STORE, SM>, 9 * 16 * 132 * 4, done)) return GDPA_ERR_CUDA;
     cache_simt_kernel<E, STORE, SM><<<grid, kThreads, bytes, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
 }

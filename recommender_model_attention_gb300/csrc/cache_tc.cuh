@@ -958,8 +958,8 @@ cache_tc_kernel(const __grid_constant__ AttnArgs a) {
 template <int D, bool FP8, int ACT>
 gdpa_status launch(const AttnArgs& a, int grid, cudaStream_t st) {
     using C = Cfg<D, FP8>;
-    if (cudaFuncSetAttribute(cache_tc_kernel<D, FP8, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
-        return GDPA_ERR_CUDA;
+    static std::atomic<uint64_t> done{0};
+    if (!cache_smem((const void*)cache_tc_kernel<D, FP8, ACT>, C::kSmem, done)) return GDPA_ERR_CUDA;
     cache_tc_kernel<D, FP8, ACT><<<grid, C::kThreads, C::kSmem, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
 }

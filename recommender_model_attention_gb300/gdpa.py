@@ -149,13 +149,13 @@ def lib():
 
 # What the calls need of torch, looked up once by lib(): these entry points are
 # also used for a handful of rows, where marshalling is most of the time.
-_DTYPE_ID = _POSITION_BITS = _empty = _raw_stream = _current_device = _on_device = _f32 = _u8 = None
+_DTYPE_ID = _POSITION_BITS = _empty = _raw_stream = _current_device = _on_device = _f32 = _u8 = _i32_type = None
 
 
 def _torch_names():
-    global _DTYPE_ID, _POSITION_BITS, _empty, _raw_stream, _current_device, _on_device, _f32, _u8
+    global _DTYPE_ID, _POSITION_BITS, _empty, _raw_stream, _current_device, _on_device, _f32, _u8, _i32_type
     import torch
-    _f32, _u8 = torch.float32, torch.uint8
+    _f32, _u8, _i32_type = torch.float32, torch.uint8, torch.int32
     _DTYPE_ID = {torch.bfloat16: 0, torch.float32: 1}
     _POSITION_BITS = {torch.int32: 32, torch.int64: 64}
     _empty = torch.empty
@@ -994,6 +994,7 @@ class KVCache:
         self.pages, self.heads, self.d, self.page, self.store = int(pages), int(heads), int(d), int(page), store
         self.spec = _CacheSpec(pages=self.pages, heads=self.heads, d=self.d, page=self.page, store=STORE[store])
         self._ref = ctypes.byref(self.spec)
+        self._sizes = {}
         rows, scales = ctypes.c_int64(), ctypes.c_int64()
         _ok(lib().gdpa_cache_bytes(self._ref, ctypes.byref(rows), ctypes.byref(scales)), "gdpa_cache_bytes")
         self.device = torch.device("cuda" if device is None else device)
@@ -1032,19 +1033,21 @@ _cache_attn = struct.Struct("=iiiifxxxxQ").pack   # gdpa_cache_attn
 
 
 def _cache_at(cache, table, offsets, starts):
-    dev = cache.device
-    if (_POSITION_BITS.get(table.dtype) != 32 or table.dim() != 2 or table.device != dev
-            or (table.shape[1] > 1 and table.stride(1) != 1)):
+    dev, i32 = cache.device, _i32_type
+    shape, step = table.shape, table.stride()
+    if len(shape) != 2 or table.dtype != i32 or table.device != dev or (step[1] != 1 and shape[1] > 1):
         raise ValueError("table must be an int32 [B, pages] tensor with contiguous rows on the cache's device")
-    for t, what in ((offsets, "offsets"), (starts, "starts")):
-        if t is not None and (_POSITION_BITS.get(t.dtype) != 32 or t.dim() != 1
-                              or not t.is_contiguous() or t.device != dev):
-            raise ValueError("%s must be a contiguous int32 tensor on the cache's device" % what)
-    B, width = table.shape
-    if offsets is None or offsets.shape[0] != B + 1 or (starts is not None and starts.shape[0] != B):
-        raise ValueError("offsets must have B + 1 entries and starts B")
-    return B, _cache_where(table.data_ptr(), offsets.data_ptr(), starts.data_ptr() if starts is not None else 0,
-                           table.stride(0), width, B)
+    B, width = shape
+    if (offsets is None or offsets.dtype != i32 or offsets.shape != (B + 1,) or offsets.device != dev
+            or not offsets.is_contiguous()):
+        raise ValueError("offsets must be a contiguous int32 [B + 1] tensor on the cache's device")
+    if starts is None:
+        first = 0
+    elif starts.dtype != i32 or starts.shape != (B,) or starts.device != dev or not starts.is_contiguous():
+        raise ValueError("starts must be a contiguous int32 [B] tensor on the cache's device")
+    else:
+        first = starts.data_ptr()
+    return B, _cache_where(table.data_ptr(), offsets.data_ptr(), first, step[0], width, B)
 
 
 def _cache_kind(cache, dtype):
@@ -1054,7 +1057,7 @@ def _cache_kind(cache, dtype):
 
 
 def _cache_tensor(t, T, heads, d, dtype, dev, name, out=False):
-    if t.dim() != 3 or t.shape != (T, heads, d) or t.device != dev:
+    if t.shape != (T, heads, d) or t.device != dev:
         raise ValueError("%s must be a [%d, %d, %d] tensor on %s, got %s on %s"
                          % (name, T, heads, d, dev, tuple(t.shape), t.device))
     if t.dtype != dtype:
@@ -1118,44 +1121,47 @@ def gdpa_cache_read(cache: KVCache, rows: int, table, offsets, starts=None, dtyp
 
 
 def _cache_attend(cache, q, table, offsets, starts, mask, window, sinks, parents, o, lse, alpha, act, stream):
-    if q.dim() != 3:
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("q must be a [T, heads, d] tensor")
-    T, H = q.shape[0], q.shape[1]
+    T, H, d = shape
     dt, dev = q.dtype, cache.device
     kind = _cache_kind(cache, dt)
     rows = _cache_tensor(q, T, H, cache.d, dt, dev, "q")
     B, where = _cache_at(cache, table, offsets, starts)
+    up = 0
     if mask == "tree":
-        if (parents is None or _POSITION_BITS.get(parents.dtype) != 32 or parents.shape != (T,)
+        if (parents is None or parents.dtype != _i32_type or parents.shape != (T,)
                 or not parents.is_contiguous() or parents.device != dev):
             raise ValueError("a tree needs parents, a contiguous int32 [T] tensor on the cache's device")
+        up = parents.data_ptr()
     elif parents is not None:
         raise ValueError("parents belong to mask=\"tree\"")
     if o is None:
-        o = _new((T, H, cache.d), dt, dev, stream)
-    elif o.shape != q.shape or o.dtype != dt or o.device != dev or not o.is_contiguous():
+        o = _new(shape, dt, dev, stream)
+    elif o.shape != shape or o.dtype != dt or o.device != dev or not o.is_contiguous():
         raise ValueError("o must be a contiguous tensor of q's shape, dtype and device")
-    if lse is not None and (lse.dtype != _f32 or lse.shape != (T, H) or not lse.is_contiguous() or lse.device != dev):
-        raise ValueError("lse must be a contiguous float32 [T, heads] tensor on the cache's device")
-    attn = _cache_attn(CACHE_MASK[mask], window, sinks, ACT[act], cache.d ** -0.5 if alpha is None else alpha,
-                       parents.data_ptr() if parents is not None else 0)
-    L = lib()
-    size = ctypes.c_int64()
-    _ok_on(cache, L.gdpa_cache_workspace, "gdpa_cache_workspace", (kind, T, H, B, ctypes.byref(size)))
-    work = _new((size.value,), _u8, dev, stream)
-    _cache_call(L.gdpa_cache_fwd, "gdpa_cache_fwd", cache,
-                (kind, T, H, rows, o.data_ptr(), lse.data_ptr() if lse is not None else None, where, attn,
-                 work.data_ptr(), size.value), stream)
-    return o
-
-
-def _ok_on(cache, f, what, args):
-    """A call that asks the cache's device, not a stream of it."""
-    if cache.device.index == _current_device():
-        _ok(f(cache._ref, *args), what)
-    else:
-        with _on_device(cache.device.index):
-            _ok(f(cache._ref, *args), what)
+    sums = None
+    if act == "softmax":
+        if lse is None:
+            lse = _new((T, H), _f32, dev, stream)
+        elif lse.dtype != _f32 or lse.shape != (T, H) or not lse.is_contiguous() or lse.device != dev:
+            raise ValueError("lse must be a contiguous float32 [T, heads] tensor on the cache's device")
+        sums = lse.data_ptr()
+    attn = _cache_attn(CACHE_MASK[mask], window, sinks, ACT[act], cache.d ** -0.5 if alpha is None else alpha, up)
+    # what a call of these sizes needs (the memory itself is each call's own)
+    size = cache._sizes.get((kind, T, H, B))
+    if size is None:
+        n = ctypes.c_int64()
+        with _on_device(dev.index):
+            _ok(lib().gdpa_cache_workspace(cache._ref, kind, T, H, B, ctypes.byref(n)), "gdpa_cache_workspace")
+        if len(cache._sizes) >= 4096:
+            cache._sizes.clear()
+        size = cache._sizes[kind, T, H, B] = n.value
+    work = _new(size, _u8, dev, stream)
+    _cache_call(lib().gdpa_cache_fwd, "gdpa_cache_fwd", cache,
+                (kind, T, H, rows, o.data_ptr(), sums, where, attn, work.data_ptr(), size), stream)
+    return o, lse
 
 
 def gdpa_cache_fwd(cache: KVCache, q, table, offsets, starts=None, mask: str = "causal", window: int = 0,
@@ -1172,7 +1178,7 @@ def gdpa_cache_fwd(cache: KVCache, q, table, offsets, starts=None, mask: str = "
     only events at positions above p - window, and below ``sinks``."""
     if act == "softmax":
         raise ValueError("the softmax variant is gdpa_cache_softmax_fwd")
-    return _cache_attend(cache, q, table, offsets, starts, mask, window, sinks, parents, o, None, alpha, act, stream)
+    return _cache_attend(cache, q, table, offsets, starts, mask, window, sinks, parents, o, None, alpha, act, stream)[0]
 
 
 def gdpa_cache_softmax_fwd(cache: KVCache, q, table, offsets, starts=None, mask: str = "causal",
@@ -1180,7 +1186,4 @@ def gdpa_cache_softmax_fwd(cache: KVCache, q, table, offsets, starts=None, mask:
                            stream=None):
     """The softmax variant of gdpa_cache_fwd: (O, lse [T, H] float32); a row that
     sees no event gives 0 and -inf."""
-    if lse is None:
-        lse = _new(tuple(q.shape[:2]), _f32, cache.device, stream)
-    o = _cache_attend(cache, q, table, offsets, starts, mask, window, sinks, parents, o, lse, alpha, "softmax", stream)
-    return o, lse
+    return _cache_attend(cache, q, table, offsets, starts, mask, window, sinks, parents, o, lse, alpha, "softmax", stream)
