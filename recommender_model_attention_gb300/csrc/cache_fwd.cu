@@ -214,9 +214,17 @@ struct Shape {
 gdpa_status shape(const CacheView& c, gdpa_dtype dt, int64_t T, int H, int B, Shape& s) {
     const int64_t rows = B > 0 ? T * (H / c.heads) / B : 0;   // of an average sample and key head
     const bool tc = dt == GDPA_BF16 && (c.d == 64 || c.d == 128);
-    s.kind = !tc ? kSimt : rows <= 64 ? kMma : kTc;
+    // Warp-level products up to 32 rows, tcgen05 above, whose tiles of 128 rows cost
+    // much before the first event (32 users of 4 heads a key head, us, warp-level
+    // and tcgen05: 32 rows on 300 events 19 and 24, on 4000 events 52 and 53; 64
+    // rows 27 and 25, 89 and 55; 128 rows 42 and 29, 156 and 57).
+    s.kind = !tc ? kSimt : rows <= 32 ? kMma : kTc;
     s.sms = device_sms();
     if (s.sms == 0) return GDPA_ERR_CUDA;
+    // What an item costs beside its events, in groups of 16 of them, and the fewest
+    // that are worth a CTA (measured on the same; trees of 32 users on tcgen05: 75
+    // us at 32 groups an item, 61 at 64, 71 at 160; windows of 1024 events of 128
+    // users: 31 us at 12, 25 at 24, but 512 users' newest events 232 and 240).
     if (s.kind == kTc) {
         s.RT = 0;
         s.TM = rows <= 128 ? 128 : 256;
@@ -225,7 +233,7 @@ gdpa_status shape(const CacheView& c, gdpa_dtype dt, int64_t T, int H, int B, Sh
         s.lead = 64;
     } else {
         // row tiles of 16 that a CTA holds: as many as an average sample fills
-        s.RT = s.kind == kSimt || rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+        s.RT = s.kind == kSimt || rows <= 16 ? 1 : 2;
         s.TM = s.kind == kMma && rows <= 8 ? 8 : 16 * s.RT;
         s.grid = s.sms * (s.kind == kSimt ? kCacheSimtPerSm : s.TM == 8 ? 3 : 2);   // resident
         s.lead = 20 / s.RT;

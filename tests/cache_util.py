@@ -23,7 +23,7 @@ class Batch:
                  parents=None, extra_width=0):
         self.new, self.hist = np.asarray(new, dtype=np.int64), np.asarray(hist, dtype=np.int64)
         self.H, self.Hkv, self.d, self.store, self.page = H, Hkv, d, store, page
-        self.few = len(self.new) == 0 or int(self.new.sum()) * (H // Hkv) // len(self.new) <= 64
+        self.few = len(self.new) == 0 or int(self.new.sum()) * (H // Hkv) // len(self.new) <= 32
         self.dt = DT[dtype or ("f32" if store == "f32" else "bf16")]
         rng = np.random.Generator(np.random.PCG64(seed))
         total = self.new + self.hist
@@ -91,7 +91,7 @@ def check_o(got, want, size, act, b):
     """float32 rows, or bf16 ones of a head dim that the CUDA cores take: 1e-5 of
     the largest value and the output's rounding.  bf16 on the tensor cores: half
     a step (2^-8) of the value for its own rounding; of every term, half a step of
-    its weight's type (bf16 2^-8; f16 2^-11 for 8-bit caches and at most 64 rows a
+    its weight's type (bf16 2^-8; f16 2^-11 for 8-bit caches and at most 32 rows a
     sample and key head on average) and 2^-12 for the float32 sums behind it; the
     activation's error; 2% for products of these."""
     if b.dt == torch.float32:
