@@ -24,6 +24,10 @@
 
 namespace gdpa {
 
+// Floats of a slot of the workspace: a tile's sums, maxima and sums of weights, in
+// whole 16-byte pieces (tiles of one row are not).
+__host__ __device__ __forceinline__ int cache_slot(int TM, int d) { return (TM * (d + 2) + 3) & ~3; }
+
 struct CacheDesc {
     int32_t parts;      // parts of the item that starts in this CTA (0: none to join)
     int32_t rows;       // real rows of its tile
@@ -332,7 +336,7 @@ __device__ __forceinline__ void finish_segment(const AttnArgs& a, const Segment&
     const int d = a.c.d, d4 = d / 4;
     float* slot = nullptr;
     if (!g.whole) {
-        slot = a.part + (int64_t)(2 * blockIdx.x + (g.head ? 1 : 0)) * a.TM * (d + 2);
+        slot = a.part + (int64_t)(2 * blockIdx.x + (g.head ? 1 : 0)) * cache_slot(a.TM, d);
         if (g.head && threadIdx.x == 0) {
             CacheDesc& t = a.desc[blockIdx.x];
             t.rows = g.rows;
@@ -397,7 +401,15 @@ inline bool cache_smem(const void* kernel, int bytes, std::atomic<uint64_t>& don
 gdpa_status launch_cache_mma(const AttnArgs& a, int grid, cudaStream_t st);
 gdpa_status launch_cache_tc_bf16(const AttnArgs& a, int grid, cudaStream_t st);
 gdpa_status launch_cache_tc_e4m3(const AttnArgs& a, int grid, cudaStream_t st);
+// Values of 16 bytes of a cache row, and the CTAs an SM that the registers of R
+// rows' queries and sums of so many columns leave room for.
+__host__ __device__ constexpr int cache_per_chunk(int store) {
+    return store == GDPA_STORE_F32 ? 4 : store == GDPA_STORE_BF16 ? 8 : 16;
+}
+__host__ __device__ constexpr int cache_few_per_sm(int store, int R) {
+    return R * cache_per_chunk(store) <= 16 ? 4 : R * cache_per_chunk(store) <= 32 ? 3 : 2;
+}
+gdpa_status launch_cache_few(const AttnArgs& a, gdpa_dtype dt, int grid, cudaStream_t st);
 gdpa_status launch_cache_simt(const AttnArgs& a, gdpa_dtype dt, int grid, cudaStream_t st);
-constexpr int kCacheSimtPerSm = 2;
 
 }  // namespace gdpa

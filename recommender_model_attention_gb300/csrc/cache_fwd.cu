@@ -45,7 +45,7 @@ cache_join_kernel(const __grid_constant__ AttnArgs a, int ctas) {
     __shared__ float2 ml[kJoinWarps];
     __shared__ float factor[kMaxGrid];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int d = a.c.d, ld = a.TM * (d + 2);
+    const int d = a.c.d, ld = cache_slot(a.TM, d);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     int base = 0;
     for (int c0 = 0; c0 < ctas; c0 += kJoinThreads) {
@@ -203,7 +203,7 @@ int device_sms() {
     return n;
 }
 
-enum Kind { kSimt, kMma, kTc };
+enum Kind { kFew, kSimt, kMma, kTc };
 struct Shape {
     Kind kind;
     int RT, TM, grid, sms, min_share, lead;
@@ -218,7 +218,9 @@ gdpa_status shape(const CacheView& c, gdpa_dtype dt, int64_t T, int H, int B, Sh
     // much before the first event (32 users of 4 heads a key head, us, warp-level
     // and tcgen05: 32 rows on 300 events 19 and 24, on 4000 events 52 and 53; 64
     // rows 27 and 25, 89 and 55; 128 rows 42 and 29, 156 and 57).
-    s.kind = !tc ? kSimt : rows <= 32 ? kMma : kTc;
+    // On the CUDA cores: straight from the pages up to 4 rows, through shared memory
+    // above (float32, 512 users of a row 3318 and 560 us).
+    s.kind = !tc ? rows <= 4 ? kFew : kSimt : rows <= 32 ? kMma : kTc;
     s.sms = device_sms();
     if (s.sms == 0) return GDPA_ERR_CUDA;
     // What an item costs beside its events, in groups of 16 of them, and the fewest
@@ -233,14 +235,14 @@ gdpa_status shape(const CacheView& c, gdpa_dtype dt, int64_t T, int H, int B, Sh
         s.lead = 64;
     } else {
         // row tiles of 16 that a CTA holds: as many as an average sample fills
-        s.RT = s.kind == kSimt || rows <= 16 ? 1 : 2;
-        s.TM = s.kind == kMma && rows <= 8 ? 8 : 16 * s.RT;
-        s.grid = s.sms * (s.kind == kSimt ? kCacheSimtPerSm : s.TM == 8 ? 3 : 2);   // resident
+        s.RT = s.kind != kMma || rows <= 16 ? 1 : 2;
+        s.TM = s.kind == kFew ? (rows <= 1 ? 1 : rows <= 2 ? 2 : 4) : s.kind == kMma && rows <= 8 ? 8 : 16 * s.RT;
+        s.grid = s.sms * (s.kind == kFew ? cache_few_per_sm(c.store, s.TM) : s.kind == kMma && s.TM == 8 ? 3 : 2);   // resident
         s.lead = 20 / s.RT;
         s.min_share = 4 / s.RT;
     }
     if (s.grid > kMaxGrid) s.grid = kMaxGrid;
-    s.bytes = (int64_t)s.grid * (sizeof(CacheDesc) + 2ll * s.TM * (c.d + 2) * 4);
+    s.bytes = (int64_t)s.grid * (sizeof(CacheDesc) + 2ll * cache_slot(s.TM, c.d) * 4);
     return GDPA_OK;
 }
 
@@ -315,7 +317,8 @@ gdpa_status gdpa_cache_fwd(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T,
     // the warp-level kernel's scores are in powers of two
     a.alpha = p.kind == kMma && sm ? attn->alpha * kLog2e : attn->alpha;
     cudaStream_t st = (cudaStream_t)stream;
-    s = p.kind == kSimt ? launch_cache_simt(a, dtype, p.grid, st)
+    s = p.kind == kFew ? launch_cache_few(a, dtype, p.grid, st)
+        : p.kind == kSimt ? launch_cache_simt(a, dtype, p.grid, st)
         : p.kind == kMma ? launch_cache_mma(a, p.grid, st)
         : a.c.store == GDPA_STORE_E4M3 ? launch_cache_tc_e4m3(a, p.grid, st) : launch_cache_tc_bf16(a, p.grid, st);
     if (s != GDPA_OK) return s;

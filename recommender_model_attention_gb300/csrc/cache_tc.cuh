@@ -803,7 +803,7 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& a, uint8_t* smem, uint
         if (!(dual && s)) {
             const bool dirty = *reinterpret_cast<volatile int*>(&misc.dirty) != 0;
             float* slot = nullptr;
-            if (!g.whole) slot = a.part + (int64_t)(2 * blockIdx.x + (g.head ? 1 : 0)) * a.TM * (D + 2);
+            if (!g.whole) slot = a.part + (int64_t)(2 * blockIdx.x + (g.head ? 1 : 0)) * cache_slot(a.TM, D);
             const float inv = kSm ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
             // outputs, 32 columns at a time, through shared memory, so that a row's
             // lie in neighbouring lanes (the queries' products are over)
