@@ -738,7 +738,7 @@ typedef struct {
 /* Which events a call's rows are: sample b's are rows [off[b], off[b + 1]), its
  * i-th row being event starts[b] + i (starts NULL: from 0); rows behind off[B]
  * are left alone.  All device int32; table [B] rows of `width` pages, `stride`
- * apart. */
+ * apart (0: samples that share their pages). */
 typedef struct {
     const int32_t *table, *off, *starts;
     int64_t stride;
@@ -753,8 +753,8 @@ gdpa_status gdpa_cache_bytes(const gdpa_cache* cache, int64_t* rows, int64_t* sc
 /* Write T rows of K and V to their events / read them back, in one launch.
  * dtype: the cache's own type; E4M3 takes and gives bf16 or float32 (each value
  * rounded once).  An event written twice in one call holds either row.  Reads
- * want rows and strides that are multiples of 16 bytes; an event outside the
- * cache reads as zeros.  INVALID_ARG for bad pointers, sizes or types;
+ * want rows and strides that are multiples of 16 bytes, K and V apart from each
+ * other; an event outside the cache reads as zeros.  INVALID_ARG for bad pointers, sizes or types;
  * UNSUPPORTED as gdpa_cache_bytes and for width * page > 2^31 - 65537.  Enqueued on
  * `stream`, no allocation, capturable. */
 gdpa_status gdpa_cache_write(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T,
@@ -782,8 +782,10 @@ gdpa_status gdpa_cache_read(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T
  *
  * q [T] rows of H heads (q->x, strides), o [T][H][d] and lse [T][H] (float32,
  * may be NULL, softmax only) contiguous; H a multiple of the cache's key heads,
- * H / heads <= 128.  dtype: as for gdpa_cache_write.  bf16 with d = 64 or 128
- * runs on the tensor cores, everything else on the CUDA cores.  workspace:
+ * H / heads <= 128; o may lie over a contiguous q.  dtype: as for
+ * gdpa_cache_write.  bf16 with d = 64 or 128 runs on the tensor cores (weights
+ * rounded to bf16, or f16 for 8-bit caches and few rows), everything else on the
+ * CUDA cores in float32.  workspace:
  * gdpa_cache_workspace bytes of device memory (16-byte aligned) for this call
  * alone while it runs.  Nothing depends on host knowledge of lengths: one
  * captured graph serves growing histories.

@@ -134,6 +134,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* tmp, int64_t& 
 template <int NT>
 __device__ __forceinline__ Share find_share(const AttnArgs& a, int64_t* tmp) {
     int64_t mine = 0, first = 0;
+#pragma unroll 4
     for (int b = threadIdx.x; b < a.w.B; b += NT) {
         const int64_t n = sample_units(a, b);
         if (b < NT) first = n;
@@ -274,7 +275,8 @@ __device__ __forceinline__ RowView row_view(const AttnArgs& a, const Segment& g,
         v.hi = g.s.start;
         if (a.mask == GDPA_CACHE_TREE) {
             v.depth = 0;
-            for (int i = tree_parent(a, g.s, v.tok); i >= 0; i = tree_parent(a, g.s, i)) ++v.depth;
+            if (a.window > 0)   // (what positions are for)
+                for (int i = tree_parent(a, g.s, v.tok); i >= 0; i = tree_parent(a, g.s, i)) ++v.depth;
             pos += v.depth;
         }
     }

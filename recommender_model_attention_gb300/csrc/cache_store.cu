@@ -345,7 +345,7 @@ bool cache_view(const gdpa_cache* c, CacheView& v, gdpa_status* s) {
 }
 
 gdpa_status cache_where(const gdpa_cache_where* w, int64_t T, const CacheView& c, CacheWhere& o) {
-    if (!w || w->B < 0 || w->width < 0 || !w->off || (uintptr_t)w->off % 4) return GDPA_ERR_INVALID_ARG;
+    if (!w || w->B < 0 || w->width < 0 || w->stride < 0 || !w->off || (uintptr_t)w->off % 4) return GDPA_ERR_INVALID_ARG;
     if (w->B > 0 && w->width > 0 && (!w->table || (uintptr_t)w->table % 4)) return GDPA_ERR_INVALID_ARG;
     if ((uintptr_t)w->starts % 4) return GDPA_ERR_INVALID_ARG;
     if (((int64_t)w->width << c.page_log) > 0x7fffffff - 65536 || T > 0x7fffffff) return GDPA_ERR_UNSUPPORTED;

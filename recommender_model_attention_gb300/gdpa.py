@@ -1011,6 +1011,9 @@ class KVCache:
         self.error = torch.zeros(4, dtype=torch.int32, device=self.device)
         for n in ("k", "v", "k_scale", "v_scale", "error"):
             setattr(self.spec, n, getattr(self, n).data_ptr())
+        # its zeros are in place before any stream writes to it (and a graph that
+        # is being captured cannot own it)
+        torch.cuda.current_stream(self.device).synchronize()
 
     @property
     def nbytes(self) -> int:

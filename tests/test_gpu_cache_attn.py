@@ -188,6 +188,123 @@ def test_large_scores(store, dtype, d):
     assert np.max(np.abs(ref.to_f64(lse) - wlse)) <= 2 * 3.9e-3
 
 
+MANY = ([70, 130, 0, 33, 1], [40, 3, 20, 300, 0])   # more than 32 rows a sample on average
+TC = [("bf16", 128), ("bf16", 64), ("e4m3", 128), ("e4m3", 64)]
+
+
+@pytest.mark.parametrize("store,d", TC)
+@pytest.mark.parametrize("window,sinks", [(1, 0), (20, 5), (64, 130), (150, 0), (2 ** 31 - 1, 1)])
+@pytest.mark.parametrize("mask", ["causal", "history", "tree"])
+def test_many_rows_windows_and_sinks(store, d, window, sinks, mask):
+    b = Batch(*MANY, d=d, store=store, parents=tree(MANY[0]) if mask == "tree" else None).fill()
+    b.check("softmax", mask=mask, window=window, sinks=sinks)
+    b.check("silu", mask=mask, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("store,d", TC)
+@pytest.mark.parametrize("act", ["softmax", "gelu_erf", "gelu_tanh", "silu", "gelu_taylor6", "identity"])
+def test_many_rows_activations(store, d, act):
+    b = Batch(*MANY, H=4, Hkv=2, d=d, store=store, gain=0.5, page=64).fill()
+    b.check(act)
+    b.check(act, alpha=0.0)
+    b.check(act, alpha=-0.05)
+    b.check(act, mask="history")
+
+
+@pytest.mark.parametrize("store,d", TC)
+@pytest.mark.parametrize("H,Hkv", [(3, 1), (128, 1), (10, 2)])
+def test_many_rows_shared_key_heads(store, d, H, Hkv):
+    """Tiles of one, two and more row blocks, and of tokens cut between them."""
+    Batch([2, 45, 7], [300, 130, 1], H=H, Hkv=Hkv, d=d, store=store).fill().check()
+
+
+@pytest.mark.parametrize("store,d", TC)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_many_rows_hidden_events_may_hold_anything(store, d, bad):
+    new, hist = [90, 40], [70, 33]
+    parents = tree(new, 3)
+    for mask, act in (("causal", "softmax"), ("tree", "softmax"), ("causal", "silu")):
+        b = Batch(new, hist, d=d, store=store, parents=parents if mask == "tree" else None)
+        kw = dict(mask=mask, window=30, sinks=2)
+        clean, clean_lse = b.fill().run(act, **kw)
+        see = orc.sees(90, 70, mask, 30, 2, parents[:90])
+        b.k_all[100], b.v_all[100] = bad, bad       # new row 30 of sample 0
+        b.v_all[120, 1, 5] = bad                    # one value of new row 50
+        o, lse = b.fill().run(act, **kw)
+        hit = np.concatenate([see[:, 100], np.zeros(40, dtype=bool)])
+        part = np.concatenate([see[:, 120], np.zeros(40, dtype=bool)])
+        assert hit.any() and part.any() and not (hit | part).all()
+        ok = torch.from_numpy(~(hit | part)).cuda()
+        assert torch.equal(o[ok], clean[ok])
+        assert not torch.isfinite(o[torch.from_numpy(hit).cuda()]).any() or act != "softmax"
+        only = torch.from_numpy(part & ~hit).cuda()
+        assert not torch.isfinite(o[only][:, 1, 5]).any()
+        if store == "bf16":                         # (8-bit: the whole row of that head is NaN)
+            keep = torch.ones(d, dtype=torch.bool, device="cuda")
+            keep[5] = False
+            assert torch.equal(o[only][:, 0], clean[only][:, 0]) and torch.equal(o[only][:, 1][:, keep], clean[only][:, 1][:, keep])
+        if lse is not None:
+            assert torch.equal(lse[ok], clean_lse[ok])
+
+
+@pytest.mark.parametrize("store,d", TC)
+def test_many_rows_pages_outside_the_cache(store, d):
+    """Missing pages are as hidden events, also inside blocks that every row sees."""
+    b = Batch([64, 50], [500, 30], d=d, store=store).fill()
+    good, _ = b.run()
+    b.table_host[0, 3] = 1 << 20     # events 48 .. 63 of sample 0
+    b.table_host[0, 33] = -1         # events 528 .. 543, new rows 28 .. 43
+    b.table = dev(b.table_host)
+    o, _ = b.run()
+    with pytest.raises(gd.GdpaError):
+        b.cache.check()
+    assert torch.equal(o[64:], good[64:])
+    keep = np.array([j for j in range(564) if not 48 <= j < 64 and not 528 <= j < 544])
+    k, v = (orc.held(ref.to_f64(x), store)[:564][keep] for x in (b.k_all, b.v_all))
+    for i in (0, 30, 63):
+        see = keep <= 500 + i
+        want, _, size = orc.attend([0, 1], [see.sum() - 1], ref.to_f64(b.q[i:i + 1]), [k[see]], [v[see]], d ** -0.5, "softmax")
+        check_o(o[i:i + 1], want, size, "softmax", b)
+
+
+def test_many_rows_large_scores_and_sizes():
+    """References that move along the history, and 8-bit rows of sizes 2^-40 .. 2^40."""
+    for store in ("bf16", "e4m3"):
+        b = Batch([40, 60], [700, 90], store=store)
+        n = b.k_all.shape[0]
+        b.k_all = (b.k_all.float() * torch.linspace(0.1, 30, n)[:, None, None]).to(b.k_all.dtype)
+        o, lse = b.fill().run()
+        want, wlse, size = b.want(128 ** -0.5, "softmax")
+        # as test_large_scores
+        assert np.all(np.abs(ref.to_f64(o) - want) <= 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 2 * 3.9e-3) * size[0] + 1e-30)
+        assert np.max(np.abs(ref.to_f64(lse) - wlse)) <= 2 * 3.9e-3
+        b = Batch([40, 60], [300, 90], store=store, seed=2)
+        n = b.v_all.shape[0]
+        e = np.random.Generator(np.random.PCG64(5)).permutation(np.linspace(-40, 40, n).round())
+        b.v_all = b.v_all * torch.from_numpy(np.ldexp(1.0, e.astype(int))).to(torch.bfloat16)[:, None, None]
+        b.fill().check()
+        b.check("silu")
+
+
+def test_outputs_over_the_queries():
+    for new, H, store, dtype, d in (([1, 3], 8, "e4m3", "bf16", 128), ([70, 90], 2, "bf16", "bf16", 64), ([1, 2], 1, "f32", "f32", 64)):
+        b = Batch(new, [5000, 300], H=H, Hkv=1, d=d, store=store, dtype=dtype, page=64).fill()
+        want, lse = b.run()
+        q = b.q.clone()
+        o, l2 = gd.gdpa_cache_softmax_fwd(b.cache, q, b.table, b.off, b.starts, o=q)
+        assert torch.equal(o, want) and torch.equal(l2, lse)
+
+
+def test_samples_that_share_pages():
+    """One history for all samples (a table that is expanded)."""
+    b = Batch([1], [400], H=4, Hkv=2, d=64, store="e4m3").fill()
+    q = torch.randn(6, 4, 64, device="cuda").bfloat16()
+    many = gd.gdpa_cache_softmax_fwd(b.cache, q, b.table.expand(6, -1), dev(np.arange(7)), dev([400] * 6), mask="history")
+    one = gd.gdpa_cache_softmax_fwd(b.cache, q, b.table, dev([0, 6]), dev([400]), mask="history")
+    for x, y in zip(many, one):   # other tiles: other orders of the sums
+        assert torch.allclose(x.float(), y.float(), rtol=2.0 ** -7, atol=2.0 ** -8)
+
+
 def test_strided_queries():
     b = Batch([5, 3], [50, 20], H=4, Hkv=2, d=64).fill()
     want, lse = b.run()
@@ -246,6 +363,11 @@ def test_events_and_starts_outside_the_table():
     with pytest.raises(gd.GdpaError):
         b.cache.check()
     assert (o[:2] == 0).all() and torch.isinf(lse[:2]).all() and torch.equal(o[2:], good[2:])
+    # starts that leave 32 bits behind
+    o, lse = gd.gdpa_cache_softmax_fwd(b.cache, b.q, b.table, b.off, dev([2 ** 31 - 2, 60]), window=5)
+    with pytest.raises(gd.GdpaError):
+        b.cache.check()
+    assert torch.equal(o[2:], gd.gdpa_cache_softmax_fwd(b.cache, b.q, b.table, b.off, b.starts, window=5)[0][2:])
     # a table too short for the events
     gd.gdpa_cache_softmax_fwd(b.cache, b.q, b.table[:, :3], b.off, b.starts)
     with pytest.raises(gd.GdpaError):
