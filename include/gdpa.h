@@ -736,8 +736,8 @@ typedef struct {
 } gdpa_cache_rows;
 
 /* Which events a call's rows are: sample b's are rows [off[b], off[b + 1]), its
- * i-th row being event starts[b] + i (starts NULL: from 0); rows behind off[B]
- * are left alone.  All device int32; table [B] rows of `width` pages, `stride`
+ * i-th row being event starts[b] + i (starts NULL: from 0); rows before off[0]
+ * and behind off[B] are left alone.  All device int32; table [B] rows of `width` pages, `stride`
  * apart (0: samples that share their pages). */
 typedef struct {
     const int32_t *table, *off, *starts;
@@ -752,11 +752,12 @@ gdpa_status gdpa_cache_bytes(const gdpa_cache* cache, int64_t* rows, int64_t* sc
 
 /* Write T rows of K and V to their events / read them back, in one launch.
  * dtype: the cache's own type; E4M3 takes and gives bf16 or float32 (each value
- * rounded once).  An event written twice in one call holds either row.  Reads
- * want rows and strides that are multiples of 16 bytes, K and V apart from each
- * other; an event outside the cache reads as zeros.  INVALID_ARG for bad pointers, sizes or types;
- * UNSUPPORTED as gdpa_cache_bytes and for width * page > 2^31 - 65537.  Enqueued on
- * `stream`, no allocation, capturable. */
+ * rounded once).  The rows of one write are different events (one written
+ * twice holds some of either row).  Reads want rows and strides that are
+ * multiples of 16 bytes, K and V apart from each other; an event outside the
+ * cache reads as zeros.  INVALID_ARG for bad pointers, sizes or types;
+ * UNSUPPORTED as gdpa_cache_bytes and for width * page or T >= 2^30.  Enqueued
+ * on `stream`, no allocation, capturable. */
 gdpa_status gdpa_cache_write(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T,
                              const gdpa_cache_rows* k, const gdpa_cache_rows* v,
                              const gdpa_cache_where* where, void* stream);
@@ -775,6 +776,8 @@ gdpa_status gdpa_cache_read(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T
  *            K and V are event starts[b] + i, its parent is new row parents[off[b]
  *            + i] < i of its sample (anything else: none), its position
  *            starts[b] + its number of ancestors, a history event's its index.
+ *            (A row walks up its path for every 16 new events: meant for drafts
+ *            of up to some thousand rows.)
  * With window W > 0 only those at positions above p - W for a row at position
  * p, and the events at positions below `sinks`, which stay visible.  A row that
  * sees nothing gives O = 0, lse = -inf.  What an event that a row does not see
@@ -807,7 +810,8 @@ gdpa_status gdpa_cache_fwd(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T,
 /* Waits for `stream`; DEVICE if a call since the last check met a table entry or
  * an event outside the cache: detail (int32 [4]) receives 2, what it was (1 a
  * page, 2 an event behind the table's pages or before 0, 3 a negative start),
- * the sample and the value, and the record is cleared. */
+ * the sample and the value, and the record is cleared.  TIMEOUT if a kernel gave
+ * up waiting (its outputs are unspecified): 1, where, the CTA. */
 gdpa_status gdpa_cache_check(const gdpa_cache* cache, int32_t* detail, void* stream);
 
 /* Activation test hook.

@@ -66,7 +66,7 @@ __device__ __forceinline__ Sample sample_info(const AttnArgs& a, int b) {
     const int T = (int)a.w.T;
     s.t0 = min(max(__ldg(a.w.off + b), 0), T);
     s.n = min(max(__ldg(a.w.off + b + 1), s.t0), T) - s.t0;
-    s.start = a.w.starts ? __ldg(a.w.starts + b) : 0;
+    s.start = a.w.starts ? min(__ldg(a.w.starts + b), kCacheMost) : 0;   // (behind every table: so that sums fit 32 bits)
     const int64_t cap = (int64_t)a.w.width << a.c.page_log;
     int64_t end = (int64_t)s.start + (a.mask == GDPA_CACHE_HISTORY ? 0 : s.n);
     if (s.start < 0) end = 0;

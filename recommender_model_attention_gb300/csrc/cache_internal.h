@@ -23,6 +23,7 @@
 
 namespace gdpa {
 
+constexpr int kCacheMost = 0x3fffffff;   // events of a sample, rows of a call
 constexpr int kCacheGroup = 16;   // events read together; a page is a multiple of it
 
 struct CacheView {

@@ -173,7 +173,7 @@ __device__ __forceinline__ float scale_query(uint32_t (&w)[STEPS][2]) {
         for (int j = 0; j < 2; ++j) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[s][j])), fabsf(bf16_hi(w[s][j]))));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const float f = inverse_power(top);   // of infinities: whatever, their products are
+    const float f = inverse_power(top);   // (infinities stay what they are)
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)
 #pragma unroll

@@ -76,7 +76,9 @@ __device__ __forceinline__ void find_tokens(const StoreArgs& a, int64_t row0, To
         t.page[i] = t.e[i] = -1;
         if (row >= last) continue;
         const int b = sample_of(w.off, row, lo, hi);
-        const int64_t ev = row - __ldg(w.off + b) + (w.starts ? __ldg(w.starts + b) : 0);
+        const int first = __ldg(w.off + b);
+        if (row < first) continue;   // (before the first sample)
+        const int64_t ev = row - first + (w.starts ? __ldg(w.starts + b) : 0);
         const int64_t page = cache_block(a.c, w, b, ev, 0);
         t.e[i] = 0;   // (a row, if not one with a page)
         if (page < 0) continue;
@@ -348,7 +350,7 @@ gdpa_status cache_where(const gdpa_cache_where* w, int64_t T, const CacheView& c
     if (!w || w->B < 0 || w->width < 0 || w->stride < 0 || !w->off || (uintptr_t)w->off % 4) return GDPA_ERR_INVALID_ARG;
     if (w->B > 0 && w->width > 0 && (!w->table || (uintptr_t)w->table % 4)) return GDPA_ERR_INVALID_ARG;
     if ((uintptr_t)w->starts % 4) return GDPA_ERR_INVALID_ARG;
-    if (((int64_t)w->width << c.page_log) > 0x7fffffff - 65536 || T > 0x7fffffff) return GDPA_ERR_UNSUPPORTED;
+    if (((int64_t)w->width << c.page_log) > kCacheMost || T > kCacheMost) return GDPA_ERR_UNSUPPORTED;
     o.table = w->table;
     o.stride = w->B > 1 ? w->stride : 0;
     o.width = w->width;
@@ -431,7 +433,7 @@ gdpa_status gdpa_cache_check(const gdpa_cache* cache, int32_t* detail, void* str
     if (e[0] == 0) return GDPA_OK;
     if (cudaMemsetAsync(v.err, 0, sizeof(e), st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess)
         return GDPA_ERR_CUDA;
-    return GDPA_ERR_DEVICE;
+    return e[0] == gdpa::kDevTimeout ? GDPA_ERR_TIMEOUT : GDPA_ERR_DEVICE;
 }
 
 }  // extern "C"

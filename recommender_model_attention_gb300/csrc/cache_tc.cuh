@@ -618,7 +618,8 @@ __device__ __forceinline__ void put_queries(const AttnArgs& a, const Segment& g,
                 for (int x = 0; x < 4; ++x) top = fmaxf(top, fmaxf(fabsf(bf16_lo(p[x])), fabsf(bf16_hi(p[x]))));
 #pragma unroll
                 for (int m = 1; m < kLanes; m <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-                const float f = inverse_power(top);   // of infinities: whatever, their products are
+                // (codes hold no infinities: such a row's scores are NaN, as its softmax is)
+                const float f = top < INFINITY ? inverse_power(top) : __uint_as_float(0x7fc00000u);
                 uint32_t h[4], l[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) split_q(bf16_lo(p[x]) * f * 128.0f, bf16_hi(p[x]) * f * 128.0f, h[x], l[x]);

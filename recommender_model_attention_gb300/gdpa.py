@@ -1021,13 +1021,15 @@ class KVCache:
 
     def check(self, stream=None):
         """Wait for ``stream``; raise if a call since the last check met a page
-        or an event outside the cache."""
+        or an event outside the cache, or gave up waiting."""
         d = (ctypes.c_int32 * 4)()
         with _on_device(self.device.index):
             status = lib().gdpa_cache_check(self._ref, d, _stream_ptr(stream))
-        if status != 0:
-            what = {1: "page", 2: "event behind its table", 3: "negative start"}.get(d[1], "wait")
-            raise GdpaError(status, "gdpa_cache_check (code %d, %s, sample %d, %d)" % (d[0], what, d[2], d[3]))
+        if status in (5, 6):
+            what = ("wait %d, CTA %d" % (d[1], d[2]) if status == 5 else
+                    "%s, sample %d, %d" % ({1: "page", 2: "event behind its table"}.get(d[1], "negative start"), d[2], d[3]))
+            raise GdpaError(status, "gdpa_cache_check (%s)" % what)
+        _ok(status, "gdpa_cache_check")
 
 
 _cache_rows = struct.Struct("=Qqq").pack        # gdpa_cache_rows
@@ -1090,7 +1092,8 @@ def gdpa_cache_write(cache: KVCache, k, v, table, offsets, starts=None, stream=N
     packed projection) of the cache's type; bf16 or float32 for "e4m3".  offsets
     (int32 [B + 1]), starts (int32 [B], None: zeros), table (int32 [B, pages]),
     on the GPU: row t of sample b is its event starts[b] + t - offsets[b], and
-    rows behind the last offset are not written."""
+    rows before the first offset and behind the last are not written.  The rows are
+    different events: one written twice holds some of either row."""
     T = k.shape[0]
     kind = _cache_kind(cache, k.dtype)
     args = (kind, T, _cache_tensor(k, T, cache.heads, cache.d, k.dtype, cache.device, "k"),
@@ -1105,8 +1108,8 @@ def gdpa_cache_read(cache: KVCache, rows: int, table, offsets, starts=None, dtyp
     """(K, V) of ``rows`` events as [rows, heads, d] tensors: the values that the
     cache holds, row t of sample b being its event starts[b] + t - offsets[b]
     (arguments as gdpa_cache_write's).  dtype: "e4m3" caches give bf16 (default)
-    or float32.  Rows behind the last offset are not written; events outside the
-    cache read as zeros."""
+    or float32.  Rows before the first offset and behind the last are not written;
+    events outside the cache read as zeros."""
     dtype = cache.kinds[0] if dtype is None else dtype
     kind = _cache_kind(cache, dtype)
     rows = int(rows)

@@ -139,7 +139,8 @@ def test_sizes():
     (dict(w=where(off=A + 2)), INVALID), (dict(w=where(table=0)), INVALID), (dict(w=where(table=A + 1)), INVALID),
     (dict(w=where(starts=A + 1)), INVALID), (dict(w=where(B=-1)), INVALID), (dict(w=where(width=-1)), INVALID),
     (dict(w=where(stride=-4)), INVALID),
-    (dict(w=where(width=1 << 25)), UNSUPPORTED), (dict(T=1 << 31), UNSUPPORTED), (dict(T=0), OK), (dict(w=where(B=0, table=0)), OK)])
+    (dict(w=where(width=1 << 25)), UNSUPPORTED), (dict(T=1 << 31), UNSUPPORTED), (dict(T=0), OK), (dict(w=where(B=0, table=0)), OK),
+    (dict(w=where(width=1 << 24)), UNSUPPORTED), (dict(T=1 << 30), UNSUPPORTED)])
 def test_rows_refused(kw, status):
     L, c = raw.lib(), cache()
     a = dict(dt=0, T=5, k=rows(), v=rows(), w=where())

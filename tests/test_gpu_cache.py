@@ -191,6 +191,35 @@ def test_offsets_that_pass_32_bits():
     assert torch.equal(o, gd.gdpa_cache_fwd(small, q, dev([[0, 1]]), off, act="identity"))
 
 
+@pytest.mark.parametrize("store", ["bf16", "e4m3"])
+def test_rows_before_the_first_sample(store):
+    """A part of a batch, by a part of its offsets: the others' rows stay as they are."""
+    cache = gd.KVCache(4, 2, 64, page=16, store=store)
+    x = torch.randn(20, 2, 64).bfloat16().cuda()
+    gd.gdpa_cache_write(cache, x, x, dev([[0, 1]]), dev([0, 20]))
+    want = [t.clone() for t in gd.gdpa_cache_read(cache, 20, dev([[0, 1]]), dev([0, 20]))]
+    y = torch.randn(12, 2, 64).bfloat16().cuda()
+    gd.gdpa_cache_write(cache, y, y, dev([[2], [0]]), dev([5, 9, 11]), dev([0, 14]))   # (events 9 .. 13 are whose rows 0 .. 4 would be)
+    cache.check()
+    k, v = gd.gdpa_cache_read(cache, 20, dev([[0, 1]]), dev([0, 20]))
+    keep = [i for i in range(20) if i not in (14, 15)]
+    assert torch.equal(k[keep], want[0][keep]) and torch.equal(v[keep], want[1][keep])
+    out = torch.full((12, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    k, _ = gd.gdpa_cache_read(cache, 12, dev([[2], [0]]), dev([5, 9, 11]), dev([0, 14]), k_out=out)
+    assert (k[:5] == 7).all() and (k[11:] == 7).all()
+    if store == "bf16":
+        assert torch.equal(k[5:11], y[5:11])
+
+
+def test_a_wait_that_ran_out_is_a_timeout():
+    cache = gd.KVCache(1, 1, 64)
+    cache.error.copy_(dev([1, 71, 3, 0]))
+    with pytest.raises(gd.GdpaError) as e:
+        cache.check()
+    assert e.value.status == 5 and "wait 71" in str(e.value)
+    cache.check()
+
+
 def test_refusals():
     with pytest.raises(KeyError):
         gd.KVCache(1, 1, 64, store="int8")

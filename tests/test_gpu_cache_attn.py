@@ -286,6 +286,60 @@ def test_many_rows_large_scores_and_sizes():
         b.check("silu")
 
 
+@pytest.mark.parametrize("new,H,store,dtype,d", [([1, 1], 2, "f32", "f32", 64), ([9, 7], 2, "f32", "f32", 64), ([1, 1], 2, "e4m3", "bf16", 48)]
+                         + [(n, 2, s, "bf16", d) for n in ([3, 2], [12, 20], [20, 40], [90, 100], [200, 90]) for s, d in TC])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_queries_with_infinities_and_nans(new, H, store, dtype, d, bad):
+    """Their rows are NaN, and theirs alone."""
+    b = Batch(new, [40, 200], H=H, Hkv=2, d=d, store=store, dtype=dtype).fill()
+    good, lse = b.run()
+    b.q[1, 0, 3] = bad
+    o, l2 = b.run()
+    assert torch.isnan(o[1, 0]).all() and torch.isnan(l2[1, 0])
+    same = torch.ones(o.shape[:2], dtype=torch.bool, device="cuda")
+    same[1, 0] = False
+    assert torch.equal(o[same], good[same]) and torch.equal(l2[same], lse[same])
+
+
+def test_part_of_a_batch():
+    """Offsets that start behind the first row: others' outputs stay as they are."""
+    for store, d, dtype in (("bf16", 128, None), ("f32", 64, None), ("e4m3", 48, "bf16")):
+        for new in ([1, 2, 1, 1], [9, 3, 7, 20], [60, 40, 90, 33]):
+            b = Batch(new, [50, 7, 90, 300], d=d, store=store, dtype=dtype).fill()
+            want, _ = b.run()
+            o = torch.full_like(b.q, 7.0)
+            gd.gdpa_cache_softmax_fwd(b.cache, b.q, b.table[1:3], b.off[1:4].clone(), b.starts[1:3].clone(), o=o)
+            lo, hi = int(b.off_host[1]), int(b.off_host[3])
+            assert (o[:lo] == 7).all() and (o[hi:] == 7).all()
+            assert torch.allclose(o[lo:hi].float(), want[lo:hi].float(), rtol=2.0 ** -6, atol=2.0 ** -7)
+
+
+def test_two_graphs_and_two_streams_at_once():
+    """Two captured calls and one of another stream, of three batches, under way
+    side by side: each has its own workspace."""
+    sizes = ([[1] * 8, [5000] * 8], [[40] * 6, [900] * 6], [[6] * 7, [3000] * 7])
+    batches = [Batch(n, h, H=4, Hkv=2, d=128, store="e4m3", page=64, seed=i).fill() for i, (n, h) in enumerate(sizes)]
+    want = [b.run() for b in batches]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for b in batches[:2]:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(b.run())
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    eager = []
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        b = batches[2]
+        eager.append(gd.gdpa_cache_softmax_fwd(b.cache, b.q, b.table, b.off, b.starts, stream=streams[2]))
+    torch.cuda.synchronize()
+    for (o, lse), (wo, wl) in zip(outs + eager, want[:2] + [want[2]] * 20):
+        assert torch.equal(o, wo) and torch.equal(lse, wl)
+
+
 def test_outputs_over_the_queries():
     for new, H, store, dtype, d in (([1, 3], 8, "e4m3", "bf16", 128), ([70, 90], 2, "bf16", "bf16", 64), ([1, 2], 1, "f32", "f32", 64)):
         b = Batch(new, [5000, 300], H=H, Hkv=1, d=d, store=store, dtype=dtype, page=64).fill()
