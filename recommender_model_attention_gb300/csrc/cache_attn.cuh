@@ -102,10 +102,13 @@ __device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
 }
 
 // A CTA's place in the work: its share [u, u_end) of the units, the sample b
-// that holds u, and the unit at which b starts.
+// that holds u, and the unit at which b starts.  Where it starts inside an item,
+// the `last` units that are left of that item come last: then the CTAs that hold
+// tiles of the same sample read the same events at about the same time, from L2.
 struct Share {
     int64_t u, u_end, size, b_first;
-    int b;
+    int b, last;
+    __device__ __forceinline__ bool more() const { return u < u_end || last > 0; }
 };
 
 template <int NT>
@@ -168,6 +171,16 @@ __device__ __forceinline__ Share find_share(const AttnArgs& a, int64_t* tmp) {
     s.b = (int)tmp[NT / 32];
     s.b_first = tmp[NT / 32 + 1];
     if (s.b < 0) s.u_end = s.u;
+    s.last = 0;
+    if (s.u < s.u_end) {
+        const Sample x = sample_info(a, s.b);
+        const int64_t size = x.groups + a.lead, in = s.u - s.b_first, item = divide(in, size);
+        const int64_t end = s.b_first + (item + 1) * size;
+        if (in - item * size > a.lead && end < s.u_end && s.u_end <= s.b_first + x.tiles * a.c.heads * size) {
+            s.last = (int)(end - s.u);
+            s.u = end;
+        }
+    }
     __syncthreads();
     return s;
 }
@@ -190,6 +203,14 @@ __device__ __forceinline__ Segment next_segment(const AttnArgs& a, Share& s) {
     Segment g;
     const int lane = threadIdx.x & 31;
     g.rows = g.n = g.na = g.parts = 0;
+    const auto rest = [&] {   // on to what comes last; false: nothing does
+        if (s.last <= 0) return false;
+        s.u = (int64_t)blockIdx.x * s.size;
+        s.u_end = s.u + s.last;
+        s.last = 0;
+        return true;
+    };
+    if (s.u >= s.u_end && !rest()) return g;
     for (;;) {   // the sample of s.u, 32 at a time over samples without rows
         g.s = sample_info(a, s.b);
         const int64_t n = (int64_t)g.s.tiles * a.c.heads * (g.s.groups + a.lead);
@@ -210,16 +231,17 @@ __device__ __forceinline__ Segment next_segment(const AttnArgs& a, Share& s) {
         }
     }
     const int size = g.s.groups + a.lead;
-    const int64_t in = s.u - s.b_first;
-    const int item = (int)divide(in, size);
-    int u0 = (int)(in - (int64_t)item * size);
-    if (u0 <= a.lead) {          // (the share's first segment, or an item's start)
-        s.u -= u0;
+    int item, u0;
+    for (;;) {
+        const int64_t in = s.u - s.b_first;
+        item = (int)divide(in, size);
+        u0 = (int)(in - (int64_t)item * size);
+        if (u0 > a.lead) break;
+        s.u -= u0;                   // (the share's first segment, or an item's start)
         u0 = 0;
-        if (s.u_end - s.u <= a.lead) {   // the next share starts here
-            s.u = s.u_end;
-            return g;
-        }
+        if (s.u_end - s.u > a.lead) break;
+        s.u = s.u_end;               // the next share starts here
+        if (!rest()) return g;
     }
     int u1 = (int)min((int64_t)size, u0 + (s.u_end - s.u));
     g.b = s.b;

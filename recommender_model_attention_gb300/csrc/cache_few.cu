@@ -65,7 +65,7 @@ cache_few_kernel(const __grid_constant__ AttnArgs a) {
     asm volatile("griddepcontrol.launch_dependents;");
     if (tid == 0) a.desc[blockIdx.x].parts = 0;
     Share sh = find_share<kThreads>(a, scan_tmp);
-    while (sh.u < sh.u_end) {
+    while (sh.more()) {
         const Segment g = next_segment(a, sh);
         if (g.rows == 0) break;
         float q[R][N], o[R][N], m[R], l[R];

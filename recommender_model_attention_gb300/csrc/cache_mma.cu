@@ -84,7 +84,7 @@ cache_mma_kernel(const __grid_constant__ AttnArgs a) {
             ph ^= 1;
         }
     };
-    while (sh.u < sh.u_end) {
+    while (sh.more()) {
         const Segment g = next_segment(a, sh);
         if (g.rows == 0) break;
         constexpr int GN = C::kTake;

@@ -58,7 +58,7 @@ cache_simt_kernel(const __grid_constant__ AttnArgs a) {
     asm volatile("griddepcontrol.launch_dependents;");
     if (tid == 0) a.desc[blockIdx.x].parts = 0;
     Share sh = find_share<kThreads>(a, scan_tmp);
-    while (sh.u < sh.u_end) {
+    while (sh.more()) {
         const Segment g = next_segment(a, sh);
         if (g.rows == 0) break;
         for (int i = tid; i < 16 * d; i += kThreads) {

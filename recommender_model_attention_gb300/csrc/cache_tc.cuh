@@ -103,7 +103,7 @@ __device__ __forceinline__ bool advance(const AttnArgs& a, Place& p) {
     Share sh = p.sh;
     Segment g;
     g.rows = 0;
-    if (sh.u < sh.u_end) g = next_segment(a, sh);
+    if (sh.more()) g = next_segment(a, sh);
     Walk w;
     if (g.rows > 0) w.set(a, g);
     __syncwarp();
@@ -224,16 +224,20 @@ __device__ __forceinline__ void load_tiles(const AttnArgs& a, uint8_t* smem, uin
             }
             if (lane == 0) mbar_arrive_expect_tx(full, kGroupBytes * __popc(there));
             __syncwarp();
-            const int i = lane & 7, hf = lane >> 3;
-            if ((there >> i & 1) && hf < (FP8 ? 1 : C::kHalves)) {
-                const int e0 = (segment_group(g, 8 * b + i) * kCacheGroup) & ((1 << a.c.page_log) - 1);
+            // groups that lie behind each other on a page come in one copy: a copy takes
+            // the warp some 80 cycles, whatever its size
+            const int i = lane & 7, hf = lane >> 3, at_g = segment_group(g, 8 * b + i);
+            const int e0 = (at_g * kCacheGroup) & ((1 << a.c.page_log) - 1);
+            const uint32_t starts = __ballot_sync(0xffffffffu, i == 0 || i >= ng || e0 == 0 || at_g != segment_group(g, 8 * b + i - 1) + 1) & 0xff;
+            if ((there & starts) >> i & 1 && hf < (FP8 ? 1 : C::kHalves)) {
+                const uint32_t n = __ffs((starts | 0x100) >> (i + 1));
                 const int64_t blk = (int64_t)p * a.c.heads + g.h;
                 const uint8_t* src = (is_v ? a.c.v : a.c.k) + blk * a.c.block;
                 if constexpr (FP8) {
-                    bulk_load(full, dst + i * 16 * D, src + e0 * D, 16 * D);
-                    bulk_load(full, sc + 16 * i, (is_v ? a.c.vs : a.c.ks) + (blk << a.c.page_log) + e0, 16);
+                    bulk_load(full, dst + i * 16 * D, src + e0 * D, n * 16 * D);
+                    bulk_load(full, sc + 16 * i, (is_v ? a.c.vs : a.c.ks) + (blk << a.c.page_log) + e0, n * 16);
                 } else {
-                    bulk_load(full, dst + hf * kHalfBytes + i * 2048, src + (((int64_t)hf << a.c.page_log) + e0) * 128, 2048);
+                    bulk_load(full, dst + hf * kHalfBytes + i * 2048, src + (((int64_t)hf << a.c.page_log) + e0) * 128, n * 2048);
                 }
             }
             if (is_v) {
