@@ -37,7 +37,7 @@ __device__ __forceinline__ float part_factor(float m, float n, float M) {
 }
 
 template <typename E, bool SM>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinThreads, 4)   // (one wave of them)
 cache_join_kernel(const __grid_constant__ AttnArgs a, int ctas) {
     __shared__ int first[kMaxGrid + 1];   // units of the items before: rows, or eights of them
     __shared__ int tmp[kJoinWarps];

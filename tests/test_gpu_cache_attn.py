@@ -340,6 +340,22 @@ def test_two_graphs_and_two_streams_at_once():
         assert torch.equal(o, wo) and torch.equal(lse, wl)
 
 
+@pytest.mark.parametrize("store", ["bf16", "e4m3"])
+def test_long_shares_of_many_tiles(store):
+    """Shares of more than 512 groups, which take what another began of an item last."""
+    rng = np.random.Generator(np.random.PCG64(3))
+    b = Batch([512, 700, 300, 512, 640, 90, 512, 800], rng.integers(8000, 11000, 8), H=8, Hkv=2, store=store, page=64).fill()
+    o, lse = b.run()
+    b.cache.check()
+    for s, (k, v) in enumerate(zip(b.split(b.k_all), b.split(b.v_all))):
+        k, v = (orc.held(ref.to_f64(x), store) for x in (k, v))
+        for i in sorted({0, 63, int(b.new[s]) // 2, int(b.new[s]) - 1} & set(range(int(b.new[s])))):
+            t, see = int(b.off_host[s]) + i, int(b.hist[s]) + i + 1
+            want, wlse, size = orc.attend([0, 1], [see - 1], ref.to_f64(b.q[t:t + 1]), [k[:see]], [v[:see]], 128 ** -0.5, "softmax")
+            check_o(o[t:t + 1], want, size, "softmax", b)
+            check_lse(lse[t:t + 1], wlse)
+
+
 def test_outputs_over_the_queries():
     for new, H, store, dtype, d in (([1, 3], 8, "e4m3", "bf16", 128), ([70, 90], 2, "bf16", "bf16", 64), ([1, 2], 1, "f32", "f32", 64)):
         b = Batch(new, [5000, 300], H=H, Hkv=1, d=d, store=store, dtype=dtype, page=64).fill()
