@@ -345,6 +345,14 @@ __device__ __forceinline__ void split_q(float x, float y, uint32_t& hi, uint32_t
     lo = l;
 }
 
+// sum += x with what the rounding leaves of it kept in `lost` (Kahan's compensated
+// sum): thousands of equal weights on a larger sum would drift by 2^-24 of it each.
+__device__ __forceinline__ void add_compensated(float& sum, float& lost, float x) {
+    const float y = x - lost, t = sum + y;
+    lost = (t - sum) - y;
+    sum = t;
+}
+
 // Four values to the row type.
 __device__ __forceinline__ void put4(float* p, const float (&x)[4]) {
     *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);

@@ -9,7 +9,7 @@
 // over the event's lanes.  Each run of lanes keeps a softmax of its own over the
 // events that it took; they are joined at the end of a segment.  Four events a
 // lane are on their way at a time, and two to four CTAs an SM.  (512 users' newest events
-// on 3 GB of float32 rows: 609 us, 4.9 TB/s; 3318 by the kernel for 16 rows a warp.)
+// on 3 GB of float32 rows: 620 us, 4.8 TB/s; 3318 by the kernel for 16 rows a warp.)
 #include "cache_attn.cuh"
 
 namespace gdpa {
@@ -25,29 +25,32 @@ constexpr int per_chunk() {
     return cache_per_chunk(STORE);
 }
 
-// value i of 16 bytes of a cache row (8-bit: as its code's value)
+// the values of word i of 16 bytes of a cache row
 template <int STORE>
-__device__ __forceinline__ void expand(const uint4& q, float (&x)[per_chunk<STORE>()]) {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+__device__ __forceinline__ void expand_word(uint32_t w, float (&x)[per_chunk<STORE>() / 4]) {
     if constexpr (STORE == GDPA_STORE_F32) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(w[i]);
+        x[0] = __uint_as_float(w);
     } else if constexpr (STORE == GDPA_STORE_BF16) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+        x[0] = __uint_as_float(w << 16);
+        x[1] = __uint_as_float(w & 0xffff0000u);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 2; ++i) {
             uint32_t h;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[i >> 1] >> (16 * (i & 1)))));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w >> (16 * i))));
             const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
             x[2 * i] = f.x;
             x[2 * i + 1] = f.y;
         }
     }
+}
+
+// value by value of 16 bytes of a cache row (8-bit: as its code's value)
+template <int STORE>
+__device__ __forceinline__ void expand(const uint4& q, float (&x)[per_chunk<STORE>()]) {
+    constexpr int V = per_chunk<STORE>() / 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) expand_word<STORE>((&q.x)[i], *reinterpret_cast<float(*)[V]>(x + V * i));
 }
 
 template <typename E, int STORE, bool SM, int R>
@@ -68,14 +71,14 @@ cache_few_kernel(const __grid_constant__ AttnArgs a) {
     while (sh.more()) {
         const Segment g = next_segment(a, sh);
         if (g.rows == 0) break;
-        float q[R][N], o[R][N], m[R], l[R];
+        float q[R][N], o[R][N], m[R], l[R], lost[R];
         RowView rv[R];
         int hi_min = 0x7fffffff, lo_max = 0;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             rv[r] = row_view(a, g, r);
             m[r] = -INFINITY;
-            l[r] = 0.0f;
+            l[r] = lost[r] = 0.0f;
             const int rho = g.rho0 + r, tok = max(rv[r].tok, 0);
             const E* src = (const E*)a.q + (g.s.t0 + tok) * a.qt + (g.h * a.G + rho - tok * a.G) * a.qh + c * N;
 #pragma unroll
@@ -151,15 +154,18 @@ cache_few_kernel(const __grid_constant__ AttnArgs a) {
                             const float f = m[r] == -INFINITY ? 0.0f : expf(m[r] - top);
                             m[r] = top;
                             l[r] *= f;
+                            lost[r] *= f;
 #pragma unroll
                             for (int j = 0; j < N; ++j) o[r][j] *= f;
                         }
                         const float ref = m[r] == -INFINITY ? 0.0f : m[r];
+                        float sum = 0.0f;
 #pragma unroll
                         for (int p = 0; p < kAhead; ++p) {
                             s[r][p] = expf(s[r][p] - ref);
-                            l[r] += s[r][p];
+                            sum += s[r][p];
                         }
+                        add_compensated(l[r], lost[r], sum);
                     } else {
 #pragma unroll
                         for (int p = 0; p < kAhead; ++p) {
@@ -175,6 +181,33 @@ cache_few_kernel(const __grid_constant__ AttnArgs a) {
                         }
                     }
                 }
+                if constexpr (STORE == GDPA_STORE_E4M3) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int p = 0; p < kAhead; ++p) s[r][p] *= vs[p];
+                }
+                if (!masked) {
+                    // the events of a step among themselves first: O is rounded once for them
+                    // (events that there are not: weights and values of 0)
+                    constexpr int V = N / 4;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float x[kAhead][V];
+#pragma unroll
+                        for (int p = 0; p < kAhead; ++p) expand_word<STORE>((&vq[p].x)[i], x[p]);
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+#pragma unroll
+                            for (int j = 0; j < V; ++j) {
+                                float y = s[r][0] * x[0][j];
+#pragma unroll
+                                for (int p = 1; p < kAhead; ++p) y = fmaf(s[r][p], x[p][j], y);
+                                o[r][V * i + j] += y;
+                            }
+                    }
+                    continue;
+                }
 #pragma unroll
                 for (int p = 0; p < kAhead; ++p) {
                     float x[N];
@@ -182,9 +215,8 @@ cache_few_kernel(const __grid_constant__ AttnArgs a) {
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
                         if (!sees(r, p)) continue;   // whatever a hidden event holds
-                        const float w = STORE == GDPA_STORE_E4M3 ? s[r][p] * vs[p] : s[r][p];
 #pragma unroll
-                        for (int j = 0; j < N; ++j) o[r][j] = fmaf(w, x[j], o[r][j]);
+                        for (int j = 0; j < N; ++j) o[r][j] = fmaf(s[r][p], x[j], o[r][j]);
                     }
                 }
             }

@@ -273,11 +273,13 @@ struct RowState {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const float ref = m[x] == -INFINITY ? 0.0f : m[x];
+                float sum = 0.0f;   // (apart: one rounding to the size of l for all of them)
 #pragma unroll
                 for (int k = 0; k < NE; ++k) {
                     s[x][k] = ex2_approx(s[x][k] - ref);
-                    l[x] += s[x][k];
+                    sum += s[x][k];
                 }
+                l[x] += sum;
             }
         } else {
 #pragma unroll

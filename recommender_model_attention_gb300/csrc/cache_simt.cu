@@ -70,7 +70,7 @@ cache_simt_kernel(const __grid_constant__ AttnArgs a) {
         float o[16][4];
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-        float m = -INFINITY, l = 0.0f;
+        float m = -INFINITY, l = 0.0f, lost = 0.0f;
         for (int i = warp; i < g.n; i += 4) {
             const int e0 = segment_group(g, i) * kCacheGroup;
             const int64_t blk = cache_block(a.c, a.w, g.b, e0, g.h);
@@ -111,11 +111,14 @@ cache_simt_kernel(const __grid_constant__ AttnArgs a) {
                 m = mt;
                 const float ref = m == -INFINITY ? 0.0f : m;
                 l *= f;
+                lost *= f;
+                float sum = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     s[j] = expf(s[j] - ref);
-                    l += s[j];
+                    sum += s[j];
                 }
+                add_compensated(l, lost, sum);
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -138,6 +141,30 @@ cache_simt_kernel(const __grid_constant__ AttnArgs a) {
                 for (int x = 0; x < 16; ++x)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) o[x][j] *= f;
+            }
+            if (__all_sync(0xffffffffu, bits == 0xffffu || r >= g.rows)) {
+                // the group's events among themselves first: O is rounded once for them
+                float w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = wsm[warp][r][e];
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    const int c = 2 * x + half;
+                    if (c >= d4) break;
+                    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const float4 v = *reinterpret_cast<const float4*>(V + e * ld + 4 * c);
+                        y[0] = fmaf(w[e], v.x, y[0]);
+                        y[1] = fmaf(w[e], v.y, y[1]);
+                        y[2] = fmaf(w[e], v.z, y[2]);
+                        y[3] = fmaf(w[e], v.w, y[3]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[x][j] += y[j];
+                }
+                __syncwarp();
+                continue;
             }
             for (int e = 0; e < 16; ++e) {
                 if (!(bits >> e & 1u)) continue;     // whatever a hidden event holds

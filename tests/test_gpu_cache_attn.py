@@ -188,6 +188,45 @@ def test_large_scores(store, dtype, d):
     assert np.max(np.abs(ref.to_f64(lse) - wlse)) <= 2 * 3.9e-3
 
 
+def flat_tail(new, H, d, nats, events, spread, at, store, dtype=None):
+    """One event `nats` above a tail of scores N(0, spread), new * H rows."""
+    b = Batch([new], [events], H=H, Hkv=1, d=d, store=store, dtype=dtype, page=64)
+    g = torch.Generator().manual_seed(at + 1)
+    u = torch.randn((d,), generator=g).bfloat16().float()
+    b.q = (u * (1 + torch.arange(new * H) / 256.0)[:, None]).view(new, H, d).to(b.dt).cuda()
+    unit = d ** 0.5 / u.square().sum()           # of a key along u whose score is 1
+    n = events + new
+    b.k_all = (spread * d ** 0.5 / u.norm() * torch.randn((n, 1, d), generator=g)).to(b.dt)
+    b.k_all[at, 0] = (u * unit * nats).to(b.dt)
+    b.v_all = (2.5 + 2.5 * torch.rand((n, 1, d), generator=g)).to(b.dt)
+    b.v_all[:, :, 7] = 5.0                       # fixes the rows' powers of two
+    b.v_all[at, :, :4] = 0.0
+    return b
+
+
+def run_shared(b, many):
+    """The batch's one sample, many times on the same pages (so that most of a
+    history is one CTA's), against what it should give once."""
+    new, events = int(b.new[0]), int(b.hist[0])
+    b.fill()
+    want, wlse, size = b.want(b.d ** -0.5, "softmax", mask="history")
+    o, lse = gd.gdpa_cache_softmax_fwd(b.cache, b.q.repeat(many, 1, 1), b.table.expand(many, -1),
+                                       dev(new * np.arange(many + 1)), dev([events] * many), mask="history")
+    b.cache.check()
+    rep = lambda x: np.tile(x, (many,) + (1,) * (x.ndim - 1))  # noqa: E731
+    check_o(o, rep(want), [rep(x) for x in size], "softmax", b)
+    check_lse(lse, rep(wlse))
+
+
+@pytest.mark.parametrize("store,dtype,d,new,H", [("bf16", "bf16", 128, 1, 1), ("bf16", "bf16", 64, 2, 8), ("bf16", "bf16", 128, 4, 8),
+                                                 ("bf16", "bf16", 64, 9, 8), ("bf16", "bf16", 48, 1, 1), ("f32", "f32", 128, 1, 1),
+                                                 ("f32", "f32", 32, 1, 4), ("e4m3", "f32", 64, 1, 1), ("f32", "f32", 64, 2, 8)])
+def test_sums_of_many_equal_weights(store, dtype, d, new, H):
+    """Thousands of equal weights beside one of e^9: their sum is not to drift with
+    the rounding of each (one after the other, up to 2^-24 of the sum each)."""
+    run_shared(flat_tail(new, H, d, 9, 16000, 0.0, 0, store, dtype), 600)
+
+
 MANY = ([70, 130, 0, 33, 1], [40, 3, 20, 300, 0])   # more than 32 rows a sample on average
 TC = [("bf16", 128), ("bf16", 64), ("e4m3", 128), ("e4m3", 64)]
 
