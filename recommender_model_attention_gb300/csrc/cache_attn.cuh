@@ -326,10 +326,10 @@ __device__ __forceinline__ uint32_t row_bits(const AttnArgs& a, const Segment& g
     return bits;
 }
 
-// the power of two 2^-floor(log2 x), x > 0 finite and normal; kept within f32
-__device__ __forceinline__ float inverse_power(float x) {
+// the power of two 2^(to - floor(log2 x)), x > 0 finite and normal; kept within f32
+__device__ __forceinline__ float inverse_power(float x, int to = 0) {
     const uint32_t e = __float_as_uint(x) >> 23;
-    return __uint_as_float((uint32_t)(min(max(254 - (int)e, 1), 254)) << 23);
+    return __uint_as_float((uint32_t)(min(max(254 + to - (int)e, 1), 254)) << 23);
 }
 
 // two values of a query row (below 256) as E4M3 codes, and what these leave of

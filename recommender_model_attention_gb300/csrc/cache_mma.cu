@@ -20,14 +20,17 @@
 // most 2^-25 of it).  (Products of E4M3 operands, m16n8k32, are converted to f16
 // ones by the compiler, and Q needs two of them: 217 us, not 197, for 256 users'
 // 8-bit histories.)  The value rows' powers of two go
-// into the weights, w 2^e_v F, rounded to f16; F is a power of two that keeps the
-// largest w 2^e_v that O holds within [2^-6, 2^8], moved (and O with it) when
-// it leaves that range, so that rows of any size keep f16's 11 bits.  bf16
-// caches use bf16 products, weights rounded to bf16 (2^-9 of each).
+// into the weights, w 2^e_v F, rounded to f16 (2^-11 of each); F is a power of two
+// that brings the largest w 2^e_v of the 32 events that are taken together to
+// [2^7, 2^15], moved (and O with it) when they leave that range.  f16 has its 11 bits
+// down to 2^-14, so weights down to 2^-21 of the largest of those 32 have them,
+// whatever went before: a long flat tail of events keeps its share behind one event
+// far above it.  (Weights more than 2^-94 below all that O holds may be lost.)  bf16
+// caches use bf16 products, weights rounded to bf16 (2^-8 of each).
 // Scores, maxima, sums and O are float32.
 //
 // Newest events of 512 users (1.5 GB of bf16 rows) 240 us, 6.2 TB/s; 256 users'
-// 8-bit histories, 4 heads a key head (1.1 GB) 197 us, 5.8 TB/s.
+// 8-bit histories, 4 heads a key head (1.1 GB) 198 us, 5.8 TB/s.
 //
 // A group that some row does not see is masked bit by bit.  A hidden event's
 // weight is 0, and 0 times an infinity or a NaN would be NaN: a masked group's

@@ -188,7 +188,7 @@ struct RowState {
     int hi_min, lo_max, hi_max;   // of all rows of the warp
     float qs[2];                  // scale of the scores
     float m[2], l[2];             // softmax: reference, sum
-    float top[2], F[2];           // 8-bit: largest w 2^e_v in O; O's unit
+    float top[2], F[2];           // 8-bit: largest w 2^e_v in O; O is in units of 1 / F
     uint32_t bits[2][GN];         // events of the stage that the rows see
     bool masked;
 
@@ -310,12 +310,15 @@ struct RowState {
 #pragma unroll
                 for (int k = 1; k < NE; ++k) big = fmaxf(big, fabsf(s[x][k]));
                 big = over(big);
+                const bool none = top[x] == 0.0f;   // O holds nothing yet
                 top[x] = fmaxf(top[x], big);
-                const float now = top[x] * F[x];
+                const float now = big * F[x];
                 f[x] = 1.0f;
-                if (top[x] > 0.0f && !(now >= 0x1p-6f && now <= 0x1p8f)) {
-                    const float next = inverse_power(top[x]);
-                    f[x] = fminf(next / F[x], 0x1p100f);   // (what O held is nothing by then)
+                if (big > 0.0f && !(now >= 0x1p7f && now <= 0x1p15f)) {
+                    // (what O holds stays below 2^80 times the codes and their number, and the step is a float)
+                    float next = fminf(inverse_power(big, 14), inverse_power(top[x], 80));
+                    if (!none) next = fminf(next, F[x] * 0x1p126f);
+                    f[x] = fminf(next / F[x], 0x1p126f);
                     F[x] = next;
                 }
             }

@@ -227,6 +227,19 @@ def test_sums_of_many_equal_weights(store, dtype, d, new, H):
     run_shared(flat_tail(new, H, d, 9, 16000, 0.0, 0, store, dtype), 600)
 
 
+@pytest.mark.parametrize("nats,events,spread", [(9, 16000, 0.0), (11.5, 16000, 0.0), (14, 16000, 0.0), (13, 16000, 1.0),
+                                                (30, 60000, 0.0)])
+@pytest.mark.parametrize("new,H", [(1, 1), (1, 8), (2, 8), (4, 8)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_event_far_above_a_long_flat_tail(d, new, H, nats, events, spread):
+    """What `sinks` are for: the tail keeps its share, also in columns that the
+    event above it does not fill.  (30 nats: the 31 events that are weighed beside it
+    may be lost, 31 / 60000 of the tail, 2^-10.9 of such a column's value: less than
+    the 2^-11 + 2^-12 of the terms that the bound has for rounded weights.)"""
+    for at in (0, events // 2):
+        run_shared(flat_tail(new, H, d, nats, events, spread, at, "e4m3"), 600)
+
+
 MANY = ([70, 130, 0, 33, 1], [40, 3, 20, 300, 0])   # more than 32 rows a sample on average
 TC = [("bf16", 128), ("bf16", 64), ("e4m3", 128), ("e4m3", 64)]
 
