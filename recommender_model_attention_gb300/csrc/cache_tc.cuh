@@ -27,7 +27,7 @@
 //
 // Those 8 x 512 rows (4 heads a key head): bf16 218 us with the joining, 1.28
 // PFLOP/s, bound by a slot's chain of scores, weights and sums (tensor pipe 60%
-// busy); 8-bit 313 us: the row threads' instructions beside the workers'.
+// busy); 8-bit 315 us: the row threads' instructions beside the workers'.
 //
 // A block that some row does not see is masked by selection, event by event, and
 // workers clear the infinities and NaNs in its values (0 times them would be
@@ -282,6 +282,65 @@ __device__ __forceinline__ void expand16(const uint4& q, uint32_t m, uint32_t m2
     b = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
+// Clears the infinities and NaNs among 8 bf16 values; whether there were any.
+__device__ __forceinline__ bool clear_odd(uint4& v) {
+    uint32_t any = 0;
+    uint32_t* p = &v.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t z = __vcmpeq2(p[i] & 0x7f807f80u, 0x7f807f80u);
+        any |= z;
+        p[i] &= ~z;
+    }
+    return any != 0;
+}
+// Scale bytes from which on values may be infinite: 256 * 2^120 is.
+constexpr uint32_t kOddScale = 247;
+
+// The factors of a row's codes: 2^(e + 120) in both halves of m, and a second factor
+// where that leaves bf16's range (else 0).
+__device__ __forceinline__ void value_factors(uint32_t s, uint32_t& m, uint32_t& m2) {
+    m = (s + 120u) << 7;
+    m2 = 0;
+    if (s > 134u) {
+        m = 254u << 7;
+        m2 = (s - 7u) << 7;
+        m2 |= m2 << 16;
+    }
+}
+
+// A masked block's values: what is infinite or a NaN, and events behind the last one
+// (whatever their memory holds), are zeros.  Whether the former were any.  (Out of
+// line: the blocks that every row sees are the loop that is to go on.)
+template <int D, int NT>
+__device__ __noinline__ bool expand_masked(const Segment& g, int i0, const uint8_t* codes, const uint8_t* sc, uint8_t* dst, int who, int events) {
+    constexpr int kChunks = D / 16;
+    const int ch = who % kChunks;
+    bool odd = false;
+#pragma unroll 1
+    for (int e = who / kChunks; e < events; e += NT / kChunks) {
+        uint4* lo = reinterpret_cast<uint4*>(dst + (ch >> 2) * kHalfBytes + e * 128 + (((2 * ch) & 7) ^ (e & 7)) * 16);
+        uint4* hi = reinterpret_cast<uint4*>(dst + (ch >> 2) * kHalfBytes + e * 128 + (((2 * ch + 1) & 7) ^ (e & 7)) * 16);
+        const uint4 q = *reinterpret_cast<const uint4*>(codes + cache_chunk(D, 7, e, ch));
+        const uint32_t s = sc[e];
+        const bool there = segment_group(g, i0 + (e >> 4)) * kCacheGroup + (e & 15) < g.s.end;
+        uint32_t m, m2;
+        value_factors(s, m, m2);
+        if (s == 255u) odd |= there;      // a row of NaNs
+        if (s == 255u || !there) m = m2 = 0;
+        m |= m << 16;
+        uint4 x, y;
+        expand16(q, m, m2, x, y);
+        if (s >= kOddScale) {
+            odd |= clear_odd(x);
+            odd |= clear_odd(y);
+        }
+        *lo = x;
+        *hi = y;
+    }
+    return odd;
+}
+
 // The workers (warps; whole).
 template <int D, bool FP8>
 __device__ __forceinline__ void work_tiles(const AttnArgs& a, uint8_t* smem, uint64_t* bars, Misc& misc, Place& at,
@@ -323,29 +382,26 @@ __device__ __forceinline__ void work_tiles(const AttnArgs& a, uint8_t* smem, uin
                 constexpr int kChunks = D / 16, kRows = 32 * C::kWorkers / kChunks;
                 static_assert(kRows % 8 == 0, "rows of the same swizzle");
                 const int ch = who % kChunks, e1 = 16 * ng;
-                int e = who / kChunks;
-                src += cache_chunk(D, 7, e, ch);
-                uint8_t* lo = dst + (ch >> 2) * kHalfBytes + e * 128 + (((2 * ch) & 7) ^ (e & 7)) * 16;
-                uint8_t* hi = dst + (ch >> 2) * kHalfBytes + e * 128 + (((2 * ch + 1) & 7) ^ (e & 7)) * 16;
+                if (clean) {
+                    odd = expand_masked<D, 32 * C::kWorkers>(g, 8 * b, src, sc, dst, who, e1);
+                } else {
+                    int e = who / kChunks;
+                    src += cache_chunk(D, 7, e, ch);
+                    uint8_t* lo = dst + (ch >> 2) * kHalfBytes + e * 128 + (((2 * ch) & 7) ^ (e & 7)) * 16;
+                    uint8_t* hi = dst + (ch >> 2) * kHalfBytes + e * 128 + (((2 * ch + 1) & 7) ^ (e & 7)) * 16;
 #pragma unroll 1
-                for (; e < e1; e += kRows, src += kRows * D, lo += kRows * 128, hi += kRows * 128) {
-                    const uint4 q = *reinterpret_cast<const uint4*>(src);
-                    const uint32_t s = sc[e];
-                    uint32_t m = (s + 120u) << 7, m2 = 0;
-                    if (s > 134u) {      // 2^(e + 120) passes bf16's range
-                        m = 254u << 7;
-                        m2 = (s - 7u) << 7;
-                        m2 |= m2 << 16;
+                    for (; e < e1; e += kRows, src += kRows * D, lo += kRows * 128, hi += kRows * 128) {
+                        const uint4 q = *reinterpret_cast<const uint4*>(src);
+                        const uint32_t s = sc[e];
+                        uint32_t m, m2;
+                        value_factors(s, m, m2);
+                        if (s == 255u) {     // a row of NaNs
+                            m = 0x7fc0u;
+                            m2 = 0;
+                        }
+                        m |= m << 16;
+                        expand16(q, m, m2, *reinterpret_cast<uint4*>(lo), *reinterpret_cast<uint4*>(hi));
                     }
-                    if (s == 255u) {     // a row of NaNs
-                        m = clean ? 0u : 0x7fc0u;
-                        m2 = 0;
-                        odd |= clean;
-                    }
-                    // events behind the last one: whatever their memory holds
-                    if (clean && segment_group(g, 8 * b + (e >> 4)) * kCacheGroup + (e & 15) >= g.s.end) m = m2 = 0;
-                    m |= m << 16;
-                    expand16(q, m, m2, *reinterpret_cast<uint4*>(lo), *reinterpret_cast<uint4*>(hi));
                 }
                 fence_proxy_async_smem();
             } else if (clean) {
@@ -353,15 +409,7 @@ __device__ __forceinline__ void work_tiles(const AttnArgs& a, uint8_t* smem, uin
                 for (int x = who; x < 16 * ng * (D / 8); x += 32 * C::kWorkers) {
                     uint4* piece = reinterpret_cast<uint4*>(dst + (x & 7) * 16 + ((x >> 3) % (16 * ng)) * 128 + ((x >> 3) / (16 * ng)) * kHalfBytes);
                     uint4 v = *piece;
-                    uint32_t any = 0;
-                    uint32_t* p = &v.x;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t z = __vcmpeq2(p[i] & 0x7f807f80u, 0x7f807f80u);
-                        any |= z;
-                        p[i] &= ~z;
-                    }
-                    if (any) {
+                    if (clear_odd(v)) {
                         *piece = v;
                         odd = true;
                     }
@@ -535,12 +583,19 @@ __device__ __noinline__ void add_odd(const AttnArgs& a, const Segment& g, const 
                 if (!(bits >> j & 1u)) continue;
                 const int e = (e0 + j) & ((1 << a.c.page_log) - 1);
                 const uint8_t* v = a.c.v + blk * a.c.block;
-                const bool nan = FP8 && a.c.vs[(blk << a.c.page_log) + e] == 255;
+                const uint32_t scale = FP8 ? a.c.vs[(blk << a.c.page_log) + e] : 0u;
+                if (FP8 && scale < kOddScale) continue;
                 for (int c = 0; c < 32; ++c) {
                     const int col = c0 + c;
-                    float y = nan ? __uint_as_float(0x7fc00000u) : 0.0f;
-                    if (!FP8)
+                    float y;
+                    if constexpr (FP8) {
+                        uint32_t h;
+                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)v[cache_chunk(D, a.c.page_log, e, col >> 4) + (col & 15)]));
+                        y = __half22float2(*reinterpret_cast<__half2*>(&h)).x * cache_scale(scale);
+                        if (scale == 255u) y = __uint_as_float(0x7fc00000u);
+                    } else {
                         y = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(v + cache_chunk(2 * D, a.c.page_log, e, col >> 3) + 2 * (col & 7)));
+                    }
                     if (!isfinite(y)) o[c] += SM ? y : y - y;
                 }
             }

@@ -299,6 +299,43 @@ def test_many_rows_hidden_events_may_hold_anything(store, d, bad):
             assert torch.equal(lse[ok], clean_lse[ok])
 
 
+def poke(b, event, scale, code):
+    """The values of an event of sample 0 in an 8-bit cache's memory: `code` in
+    every column and a scale byte (a page that was never written, or another's)."""
+    page, e = int(b.table_host[0, event // b.page]), event % b.page
+    block = b.cache.v.view(-1)[:b.cache.pages * b.Hkv * b.page * b.d].view(b.cache.pages, b.Hkv, b.page, b.d)
+    block[page, :, e] = code      # (a row's bytes lie together, in some order)
+    b.cache.v_scale.view(-1)[:b.cache.pages * b.Hkv * b.page].view(b.cache.pages, b.Hkv, b.page)[page, :, e] = scale
+
+
+@pytest.mark.parametrize("new", [[90, 40], [300, 10], [3, 2], [1, 1], [20, 12]])
+@pytest.mark.parametrize("d,dtype", [(128, "bf16"), (64, "bf16"), (64, "f32")])
+@pytest.mark.parametrize("act", ["softmax", "silu"])
+def test_hidden_values_of_any_scale(act, d, dtype, new):
+    """Codes and scales whose product no float32 holds, in events that some rows do
+    not see: those rows are as without them."""
+    hist = [70, 33]
+    b = Batch(new, hist, d=d, store="e4m3", dtype=dtype)
+    kw = dict(window=30, sinks=2)
+    clean, clean_lse = b.fill().run(act, **kw)
+    see = orc.sees(new[0], hist[0], "causal", 30, 2)
+    for scale in (246, 247, 248, 251, 254, 255):
+        for code in (0x7e, 0xfe, 0x78, 0x08, 0x00):
+            for victim in {69, hist[0] + new[0] // 3, 20}:
+                b.fill()
+                poke(b, victim, scale, code)
+                o, lse = b.run(act, **kw)
+                hit = np.concatenate([see[:, victim], np.zeros(new[1], dtype=bool)])
+                ok = torch.from_numpy(~hit).cuda()
+                assert torch.equal(o[ok], clean[ok]), (scale, code, victim)
+                if lse is not None:
+                    assert torch.equal(lse, clean_lse)
+                if scale == 255 and hit.any():      # (the byte of rows of NaNs)
+                    assert not torch.isfinite(o[~ok]).any()
+                if code == 0 and scale == 246:
+                    assert torch.isfinite(o).all()
+
+
 @pytest.mark.parametrize("store,d", TC)
 def test_many_rows_pages_outside_the_cache(store, d):
     """Missing pages are as hidden events, also inside blocks that every row sees."""
