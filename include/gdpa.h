@@ -707,7 +707,9 @@ void gdpa_prefix_destroy(gdpa_prefix_plan plan);
  * Rows are held as they are (BF16, F32) or in 8 bits (E4M3): codes c_i and one
  * power of two a row and head, x_i ~ c_i 2^e, with the least e >= -126 for which
  * the row's largest magnitude is at most 448 2^e; x_i 2^-e is rounded to the
- * nearest E4M3 code, ties to the even one.  A row of one head that holds an
+ * nearest E4M3 code, ties to the even one, among those whose value float32 holds
+ * (magnitudes from 248 2^120 = 3.2965e38 on are held as 240 2^120, not as the
+ * infinity 256 2^120).  A row of one head that holds an
  * infinity or a NaN is all NaN.  How rows are arranged inside a page is the
  * library's own; gdpa_cache_read gives them back.
  *

@@ -31,7 +31,7 @@ def row_exponent(top: float) -> int:
 
 
 def held(rows, store: str):
-    """The values that a cache holds for float64 rows [..., d]."""
+    """The values that a cache holds for float64 rows [..., d] (those of float32)."""
     if store != "e4m3":
         return rows.copy()
     codes = e4m3_values()
@@ -47,6 +47,7 @@ def held(rows, store: str):
         below, above = codes[j - 1], codes[j]
         # nearest, ties to the even code
         up = (y - below > above - y) | ((y - below == above - y) & (j % 2 == 0))
+        up &= np.ldexp(above, e) < 2.0 ** 128      # codes whose value float32 does not hold
         out[i] = np.copysign(np.ldexp(np.where(up, above, below), e), x)
     return out
 

@@ -6,7 +6,9 @@
 // row's largest magnitude to 448 or less.  A power of two costs no precision
 // that a freely chosen scale would keep (E4M3's steps are relative), and makes
 // every product by it exact: a value is rounded once, x_i 2^-e to the nearest
-// code, ties to the even one, at most 2^-4 of it (2^-10 2^e near zero).  One
+// code, ties to the even one, at most 2^-4 of it (2^-10 2^e near zero).  At e = 120
+// the code 256 stands for 2^128, which float32 does not hold: values from 248 2^120 on
+// take 240, the largest whose value it does.  One
 // scale a row and not one a block of columns, because then the attention that
 // reads the cache may multiply whole scores and weights by it.  A row that
 // holds an infinity or a NaN is all NaN.
@@ -30,6 +32,8 @@ constexpr int kThreads = 256;
 constexpr int kPasses = 4, kPassesLong = 2;
 constexpr int kMaxTokens = 512;  // of a block: two rows of one piece each
 constexpr int kCounted = 1023;   // samples whose offsets a block counts through (as rotary positions do)
+
+constexpr int kTopExponent = 120;   // of the largest finite rows
 
 struct StoreArgs {
     CacheView c;
@@ -212,6 +216,11 @@ cache_write_kernel(const __grid_constant__ StoreArgs a) {
             alignas(16) uint16_t p[N / 2];
 #pragma unroll
             for (int j = 0; j < N / 2; ++j) p[j] = to_e4m3x2(to_f(x[2 * j]) * inv, to_f(x[2 * j + 1]) * inv);
+            if (ex == kTopExponent) {   // (above it there are no finite rows)
+                uint32_t* w = reinterpret_cast<uint32_t*>(p);
+#pragma unroll
+                for (int j = 0; j < N / 4; ++j) w[j] -= __vcmpeq4(w[j] & 0x7f7f7f7fu, 0x78787878u) & 0x01010101u;
+            }
             if (live) {
                 *reinterpret_cast<uint4*>(dst + cache_chunk(a.c.row, a.c.page_log, e, c)) = *reinterpret_cast<const uint4*>(p);
                 if (c == 0) (is_v ? a.c.vs : a.c.ks)[(blk << a.c.page_log) + e] = (uint8_t)(odd ? 255 : ex + 127);

@@ -40,6 +40,14 @@ def test_held_rounds_to_nearest_even():
     assert np.all(np.abs(orc.held(y, "e4m3") - y) <= np.maximum(2.0 ** -4 * np.abs(y), 2.0 ** -17))
 
 
+def test_finite_rows_are_held_finite():
+    top = 2.0 ** 128 - 2.0 ** 104                              # of float32
+    x = np.array([[top, 248 * 2.0 ** 120, 247.9 * 2.0 ** 120, 1.0], [448 * 2.0 ** 119] * 4])
+    want = [[240 * 2.0 ** 120] * 3 + [0.0], [448 * 2.0 ** 119] * 4]
+    assert orc.held(x, "e4m3").tolist() == want
+    assert (orc.held(-x, "e4m3") == -np.array(want)).all()
+
+
 @pytest.mark.parametrize("top,e", [(448.0, 0), (448.5, 1), (224.0, -1), (1.0, -8), (1.75, -8), (1.76, -7),
                                    (0.0, -126), (2.0 ** -140, -126), (3e38, 120)])
 def test_exponents(top, e):

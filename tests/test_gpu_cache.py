@@ -68,6 +68,29 @@ def test_every_code_and_every_border_between_two(dtype):
     same(k16, ref.to_f64(k.bfloat16()))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_largest_finite_rows_stay_finite(dtype):
+    """Magnitudes whose nearest code stands for 2^128: the largest code below it."""
+    top = torch.finfo(DT[dtype]).max
+    rows = [top, 3.3e38, 248 * 2.0 ** 120, 247 * 2.0 ** 120, 232 * 2.0 ** 120, 448 * 2.0 ** 119]
+    x = torch.zeros(2 * len(rows), 1, 64, dtype=torch.float64)
+    for i, r in enumerate(rows):
+        x[2 * i, 0, ::3] = r                       # beside zeros, and beside what rounds to less
+        x[2 * i + 1, 0] = torch.linspace(-r, r, 64, dtype=torch.float64)
+    x = x.to(DT[dtype])
+    assert torch.isfinite(x).all()
+    n = x.shape[0]
+    cache = gd.KVCache(1, 1, 64, store="e4m3")
+    args = (torch.zeros((1, 1), dtype=torch.int32, device="cuda"), dev([0, n]))
+    gd.gdpa_cache_write(cache, x.cuda(), -x.cuda(), *args)
+    for kind in (torch.float32, torch.bfloat16):
+        k, v = gd.gdpa_cache_read(cache, n, *args, dtype=kind)
+        want = orc.held(ref.to_f64(x), "e4m3")
+        assert np.isfinite(want).all()
+        same(k, want)
+        same(v, -want)
+
+
 @pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
 def test_a_row_with_an_infinity_is_all_nan(bad):
     x = torch.randn(4, 2, 64)
