@@ -783,7 +783,10 @@ gdpa_status gdpa_cache_read(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T
  * With window W > 0 only those at positions above p - W for a row at position
  * p, and the events at positions below `sinks`, which stay visible.  A row that
  * sees nothing gives O = 0, lse = -inf.  What an event that a row does not see
- * holds does not matter to the row, whatever it is.
+ * holds does not matter to the row, whatever it is.  An infinity or a NaN in a value
+ * row that a row sees makes that column of the row's output no finite number, and
+ * no other column (8-bit: all columns of the head, as the value row is held);
+ * whether an infinity or a NaN depends on the kernel and on how the work is cut.
  *
  * q [T] rows of H heads (q->x, strides), o [T][H][d] and lse [T][H] (float32,
  * may be NULL, softmax only) contiguous; H a multiple of the cache's key heads,

@@ -882,7 +882,7 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& a, uint8_t* smem, uint
                     tmem_ld32(oc + c, o);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) y[e] = f0 == 0.0f ? 0.0f : __uint_as_float(o[e]) * f0;
+                    for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(o[e]) * f0;
                 }
                 if (both) {
                     tmem_ld32(oc + 128 + c, o);

@@ -299,6 +299,38 @@ def test_many_rows_hidden_events_may_hold_anything(store, d, bad):
             assert torch.equal(lse[ok], clean_lse[ok])
 
 
+@pytest.mark.parametrize("store,dtype,d", [("bf16", "bf16", 128), ("bf16", "bf16", 64), ("f32", "f32", 64), ("bf16", "bf16", 48),
+                                           ("e4m3", "bf16", 128), ("e4m3", "f32", 64)])
+@pytest.mark.parametrize("new,H", [([1, 1], 2), ([3, 2], 2), ([9, 12], 2), ([20, 30], 2), ([40, 100], 2), ([100, 100], 2), ([300, 9], 2)])
+@pytest.mark.parametrize("act", ["softmax", "silu"])
+def test_visible_infinities_and_nans_are_seen(act, new, H, store, dtype, d):
+    """Wherever such an event lies, in blocks that all rows see or some, the rows that
+    see it have no finite number in its column, and all else is as without it, also
+    where the event's weight is tiny (its key far below the others)."""
+    hist = [700, 300]
+    for far in (False, True) if act == "softmax" else (False,):
+        for event in (0, 130, 255, 640, 699, hist[0] + new[0] // 2):
+            b = Batch(new, hist, H=H, Hkv=2, d=d, store=store, dtype=dtype, gain=0.5)
+            if far:                                  # all but the 128 around it 150 nats above
+                b.q[:new[0]] = 1.0
+                b.k_all[:hist[0] + new[0]] = 0.5
+                at = event - event % 128
+                b.k_all[at:min(at + 128, hist[0] + new[0])] = 0.5 - 150 * d ** -0.5
+            clean, lse = b.fill().run(act)
+            hit = np.concatenate([event <= hist[0] + np.arange(new[0]), np.zeros(new[1], dtype=bool)])
+            on = torch.from_numpy(hit).cuda()
+            same = torch.ones(clean.shape, dtype=torch.bool, device="cuda")
+            same[on, 1] = store != "e4m3"            # (8-bit: the whole row of that head is NaN)
+            same[on, 1, 5] = False
+            for bad in (float("inf"), -float("inf"), float("nan")):
+                b.v_all[event, 1, 5] = bad
+                o, l2 = b.fill().run(act)
+                assert not torch.isfinite(o[on][:, 1, 5]).any(), (bad, event, far)
+                assert torch.equal(o[same], clean[same]), (bad, event, far)
+                if lse is not None:
+                    assert torch.equal(l2, lse)
+
+
 def poke(b, event, scale, code):
     """The values of an event of sample 0 in an 8-bit cache's memory: `code` in
     every column and a scale byte (a page that was never written, or another's)."""
