@@ -731,7 +731,7 @@ typedef struct {
 } gdpa_cache;
 
 /* Rows of a call: element (t, h, c) at x[t * token + h * head + c], strides in
- * elements. */
+ * elements, of either sign. */
 typedef struct {
     const void* x;
     int64_t token, head;

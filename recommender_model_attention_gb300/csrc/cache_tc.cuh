@@ -646,7 +646,7 @@ __device__ __forceinline__ void put_queries(const AttnArgs& a, const Segment& g,
     // instructions of a loop that is run a few times a segment
     constexpr int kAhead = FP8 ? 4 : 8;
     const int lane = threadIdx.x & 31, c = lane % kLanes;
-    int64_t at = -1;   // of row r0 + lane
+    int64_t at = 0;   // of row r0 + lane
     if (r0 + lane < g.rows) {
         const int rho = g.rho0 + r0 + lane, tok = rho / a.G;
         at = (g.s.t0 + tok) * a.qt + (g.h * a.G + rho - tok * a.G) * a.qh;
@@ -658,7 +658,7 @@ __device__ __forceinline__ void put_queries(const AttnArgs& a, const Segment& g,
         for (int k = 0; k < kAhead; ++k) {
             const int64_t from = __shfl_sync(0xffffffffu, at, i0 + k * kEach);
             q[k] = make_uint4(0, 0, 0, 0);
-            if (from >= 0) {
+            if (r0 + i0 + k * kEach < g.rows) {
                 const __nv_bfloat16* src = (const __nv_bfloat16*)a.q + from + 8 * c;
                 if (a.q_wide) {
                     q[k] = __ldg(reinterpret_cast<const uint4*>(src));

@@ -1,12 +1,15 @@
 """Attention over the history cache on the GPU against the float64 oracle.
 Bounds: cache_util.check_o."""
 
+import ctypes
+
 import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 
 import recommender_model_attention_gb300 as gd  # noqa: E402
+from recommender_model_attention_gb300 import gdpa as raw  # noqa: E402
 from cache_util import Batch, check_lse, check_o, dev, offsets, orc, ref  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -505,6 +508,55 @@ def test_strided_queries():
         q.copy_(b.q)
         o, l2 = gd.gdpa_cache_softmax_fwd(b.cache, q, b.table, b.off, b.starts)
         assert torch.equal(o, want) and torch.equal(l2, lse)
+
+
+@pytest.mark.parametrize("store,dtype,d,new,H", [("bf16", "bf16", 128, [1, 1], 2), ("bf16", "bf16", 64, [9, 12], 2), ("e4m3", "bf16", 128, [20, 30], 2),
+                                                 ("bf16", "bf16", 128, [60, 100], 2), ("e4m3", "bf16", 64, [90, 40], 4),
+                                                 ("f32", "f32", 64, [1, 1], 2), ("f32", "f32", 64, [9, 12], 2)])
+@pytest.mark.parametrize("turn", ["tokens", "heads", "both"])
+def test_strides_of_either_sign(turn, store, dtype, d, new, H):
+    """Rows and heads that lie in memory from the last to the first (C callers)."""
+    b = Batch(new, [50, 200], H=H, Hkv=2, d=d, store=store, dtype=dtype).fill()
+    want, lse = b.run()
+    axes = {"tokens": (0,), "heads": (1,), "both": (0, 1)}[turn]
+
+    def rows(x):
+        """The memory (to be kept) and the rows of x, turned."""
+        m = x.flip(axes).contiguous()
+        at, (t, h, _) = 0, m.stride()
+        if 0 in axes:
+            at, t = at + (x.shape[0] - 1) * t, -t
+        if 1 in axes:
+            at, h = at + (x.shape[1] - 1) * h, -h
+        return m, raw._cache_rows(m.data_ptr() + at * m.element_size(), t, h)
+    L, ref_, st = raw.lib(), b.cache._ref, torch.cuda.current_stream().cuda_stream
+    kind, T, B = raw._DTYPE_ID[b.dt], sum(new), len(new)
+    where = raw._cache_where(b.table.data_ptr(), b.off.data_ptr(), b.starts.data_ptr(), b.table.stride(0), b.table.shape[1], B)
+    # written and read back
+    k, v = (x[:T].cuda() for x in (b.k_all, b.v_all))
+    mk, rk = rows(k)
+    mv, rv = rows(v)
+    before = gd.gdpa_cache_read(b.cache, T, b.table, b.off, b.starts, dtype=b.dt)
+    assert L.gdpa_cache_write(ref_, kind, T, rk, rv, where, st) == 0
+    straight = gd.gdpa_cache_read(b.cache, T, b.table, b.off, b.starts, dtype=b.dt)
+    gd.gdpa_cache_write(b.cache, k, v, b.table, b.off, b.starts)
+    for x, y in zip(straight, gd.gdpa_cache_read(b.cache, T, b.table, b.off, b.starts, dtype=b.dt)):
+        assert torch.equal(x, y)
+    mk, rk = rows(torch.zeros_like(k))
+    mv, rv = rows(torch.zeros_like(v))
+    assert L.gdpa_cache_read(ref_, kind, T, rk, rv, where, st) == 0
+    assert torch.equal(mk.flip(axes), straight[0]) and torch.equal(mv.flip(axes), straight[1])
+    gd.gdpa_cache_write(b.cache, *before, b.table, b.off, b.starts)
+    # queries
+    mq, rq = rows(b.q)
+    o, l2 = torch.empty_like(b.q), torch.empty_like(lse)
+    n = ctypes.c_int64()
+    assert L.gdpa_cache_workspace(ref_, kind, T, H, B, ctypes.byref(n)) == 0
+    work = torch.empty(n.value, dtype=torch.uint8, device="cuda")
+    attn = raw._cache_attn(0, 0, 0, raw.ACT["softmax"], d ** -0.5, 0)
+    assert L.gdpa_cache_fwd(ref_, kind, T, H, rq, o.data_ptr(), l2.data_ptr(), where, attn, work.data_ptr(), n.value, st) == 0
+    b.cache.check()
+    assert torch.equal(o, want) and torch.equal(l2, lse)
 
 
 def test_rows_behind_the_last_sample_stay():
