@@ -793,7 +793,8 @@ gdpa_status gdpa_cache_read(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T
  * H / heads <= 128; o may lie over a contiguous q.  dtype: as for
  * gdpa_cache_write.  bf16 with d = 64 or 128 runs on the tensor cores (weights
  * rounded to bf16, or f16 for 8-bit caches and few rows), everything else on the
- * CUDA cores in float32.  workspace:
+ * CUDA cores in float32.  Scores are float32 products on the way, too: 8-bit keys
+ * above 2^100 may give infinite ones where tiny queries make them finite.  workspace:
  * gdpa_cache_workspace bytes of device memory (16-byte aligned) for this call
  * alone while it runs.  Nothing depends on host knowledge of lengths: one
  * captured graph serves growing histories.

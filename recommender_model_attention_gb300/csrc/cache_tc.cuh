@@ -715,10 +715,8 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& a, uint8_t* smem, uint
     uint8_t* const stage = smem + (C::kStageApart ? C::kOffStage + (s * 4 + quarter) * 4096 : s * C::kTile + quarter * 4096);
     const auto scale_of = [&](float alpha) {
         ActScale k = act_scale<ACT>(alpha);
-        if (kSm) {   // (a zero scale would make NaN of masked scores)
-            k.c0 = fabsf(k.c0);
-            if (k.c0 < 1e-30f) k.c0 = 1e-30f;
-        }
+        // (a zero scale would make NaN of masked scores; the least normal number is none to any that are not)
+        if (kSm) k.c0 = fmaxf(fabsf(k.c0), 0x1p-126f);
         return k;
     };
     ActScale ks = scale_of(a.alpha);

@@ -510,6 +510,17 @@ def test_strided_queries():
         assert torch.equal(o, want) and torch.equal(l2, lse)
 
 
+@pytest.mark.parametrize("store,dtype,d", [("bf16", "bf16", 128), ("e4m3", "bf16", 128), ("e4m3", "bf16", 64), ("e4m3", "f32", 64), ("f32", "f32", 64)])
+@pytest.mark.parametrize("new", [[1, 1], [9, 12], [20, 30], [60, 100]])
+@pytest.mark.parametrize("q2,k2,alpha", [(-95, 95, None), (95, -95, None), (55, 55, 1e-33), (-50, -50, 1e30)])
+def test_tiny_and_huge_factors_of_ordinary_scores(q2, k2, alpha, new, store, dtype, d):
+    b = Batch(new, [50, 200], d=d, store=store, dtype=dtype)
+    b.q = (b.q.float() * 2.0 ** q2).to(b.dt)
+    b.k_all = (b.k_all.float() * 2.0 ** k2).to(b.dt)
+    b.fill().check("softmax", alpha)
+    b.check("silu", alpha)
+
+
 @pytest.mark.parametrize("store,dtype,d,new,H", [("bf16", "bf16", 128, [1, 1], 2), ("bf16", "bf16", 64, [9, 12], 2), ("e4m3", "bf16", 128, [20, 30], 2),
                                                  ("bf16", "bf16", 128, [60, 100], 2), ("e4m3", "bf16", 64, [90, 40], 4),
                                                  ("f32", "f32", 64, [1, 1], 2), ("f32", "f32", 64, [9, 12], 2)])
