@@ -816,7 +816,8 @@ gdpa_status gdpa_cache_fwd(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T,
 /* Waits for `stream`; DEVICE if a call since the last check met a table entry or
  * an event outside the cache: detail (int32 [4]) receives 2, what it was (1 a
  * page, 2 an event behind the table's pages or before 0, 3 a negative start),
- * the sample and the value, and the record is cleared.  TIMEOUT if a kernel gave
+ * the sample and the value (the table's entry; the event's number, of attention's
+ * the first behind the table; the start), and the record is cleared.  TIMEOUT if a kernel gave
  * up waiting (its outputs are unspecified): 1, where, the CTA. */
 gdpa_status gdpa_cache_check(const gdpa_cache* cache, int32_t* detail, void* stream);
 

@@ -1,11 +1,14 @@
 """The history cache on the GPU: rows written and read back, bit for bit."""
 
+import ctypes
+
 import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 
 import recommender_model_attention_gb300 as gd  # noqa: E402
+from recommender_model_attention_gb300 import gdpa as raw  # noqa: E402
 from cache_util import Batch, DT, dev, offsets, orc, ref  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -130,6 +133,23 @@ def test_strided_rows(store, dtype, shift):
     assert (out[0, :, H:] == 7).all() and (out[1, :, :H] == 7).all()
 
 
+@pytest.mark.parametrize("store,dtype", [("bf16", "bf16"), ("e4m3", "bf16"), ("e4m3", "f32"), ("f32", "f32")])
+def test_strided_rows_with_heads_in_another_order(store, dtype):
+    """K and V of strides of their own: V's heads lie further apart than its tokens."""
+    n, H, d = 37, 2, 64
+    k = torch.randn(n, H, d).to(DT[dtype]).cuda()
+    v = torch.randn(H, n, d).to(DT[dtype]).cuda().transpose(0, 1)
+    assert v.stride(0) < v.stride(1)
+    cache = gd.KVCache(3, H, d, page=16, store=store)
+    table, off = dev([[2, 0, 1]]), dev([0, n])
+    gd.gdpa_cache_write(cache, k, v, table, off)
+    out = torch.zeros(H, n, d, dtype=DT[dtype], device="cuda").transpose(0, 1)
+    a, b = gd.gdpa_cache_read(cache, n, table, off, dtype=DT[dtype], v_out=out)
+    same(a, orc.held(ref.to_f64(k), store))
+    same(b, orc.held(ref.to_f64(v), store))
+    assert b is out
+
+
 def test_many_samples():
     """More samples than a block counts through."""
     n = 3000
@@ -195,6 +215,44 @@ def test_pages_and_events_outside_the_cache(table, off, starts, code):
     inside = [0 <= starts[0] + i < 16 and code != 1 for i in range(3)]
     assert [bool((k[i] == 1).all()) for i in range(3)] == inside
     assert [bool((k[i] == 0).all()) for i in range(3)] == [not x for x in inside]
+
+
+def detail(cache):
+    """The record that gdpa_cache_check gives and clears: (status, what, sample, value)."""
+    d = (ctypes.c_int32 * 4)()
+    status = raw.lib().gdpa_cache_check(cache._ref, d, torch.cuda.current_stream().cuda_stream)
+    if status:
+        assert status == 6 and d[0] == 2
+    return (status,) + tuple(d)[1:]
+
+
+@pytest.mark.parametrize("table,start,what,values", [
+    ([[0, 1], [2, 7]], 14, 1, {7}), ([[0, 1], [2, -3]], 14, 1, {-3}), ([[0, 1], [2, 1 << 30]], 14, 1, {1 << 30}),
+    ([[0, 1], [2, 3]], 30, 2, {32}), ([[0, 1], [2, 3]], 100, 2, {100, 101, 102}), ([[0, 1], [2, 3]], -2, 2, {-2, -1}),
+    ([[0, 1], [2, 3]], 2 ** 30, 2, {2 ** 30, 2 ** 30 + 1, 2 ** 30 + 2})])
+def test_what_a_check_reports_of_rows(table, start, what, values):
+    """Sample 1 of two is outside the cache: what, whose and which."""
+    cache = gd.KVCache(4, 1, 64, page=16)
+    x = torch.ones(5, 1, 64, dtype=torch.bfloat16, device="cuda")
+    args = (dev(table), dev([0, 2, 5]), dev([3, start]))
+    for call in (lambda: gd.gdpa_cache_write(cache, x, x, *args), lambda: gd.gdpa_cache_read(cache, 5, *args)):
+        call()
+        status, kind, sample, value = detail(cache)
+        assert (status, kind, sample) == (6, what, 1) and value in values
+        assert detail(cache) == (0, 0, 0, 0)
+
+
+@pytest.mark.parametrize("store,dtype,d", [("bf16", "bf16", 64), ("f32", "f32", 64), ("bf16", "bf16", 48)])
+@pytest.mark.parametrize("new", [1, 6, 80])
+@pytest.mark.parametrize("table,start,what,value", [
+    ([[0, 1, 2, 3, 4, 5, 6], [7, 99, 9, 10, 11, 12, 13]], 30, 1, 99), ([[0, 1, 2, 3, 4, 5, 6], [7, -8, 9, 10, 11, 12, 13]], 30, 1, -8),
+    ([[0, 1, 2, 3, 4, 5, 6], [7, 8, 9, 10, 11, 12, 13]], 112, 2, 112), ([[0, 1, 2, 3, 4, 5, 6], [7, 8, 9, 10, 11, 12, 13]], -5, 3, -5)])
+def test_what_a_check_reports_of_attention(table, start, what, value, new, store, dtype, d):
+    cache = gd.KVCache(14, 1, d, page=16, store=store)
+    q = torch.ones(2 * new, 1, d, dtype=DT[dtype], device="cuda")
+    gd.gdpa_cache_softmax_fwd(cache, q, dev(table), dev([0, new, 2 * new]), dev([3, start]))
+    assert detail(cache) == (6, what, 1, value)
+    assert detail(cache) == (0, 0, 0, 0)
 
 
 def test_offsets_that_pass_32_bits():
