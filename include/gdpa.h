@@ -821,6 +821,14 @@ gdpa_status gdpa_cache_fwd(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T,
  * up waiting (its outputs are unspecified): 1, where, the CTA. */
 gdpa_status gdpa_cache_check(const gdpa_cache* cache, int32_t* detail, void* stream);
 
+/* Failure-path test hook, as gdpa_plan_set_wait_test, for all later calls of
+ * gdpa_cache_fwd of this process: limit_us > 0 shortens the waits of its
+ * tensor-core kernels (2 s), stall 1 makes the barriers of every CTA's first keys
+ * expect an arrival that never comes, so that waits for them run out; 0, 0 restores
+ * normal launches.  INVALID_ARG
+ * for other values. */
+gdpa_status gdpa_cache_set_wait_test(int limit_us, int stall);
+
 /* Activation test hook.
  *
  * Evaluates act(x) and act'(x) element-wise with the same device functions

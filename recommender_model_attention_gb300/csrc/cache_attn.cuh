@@ -49,6 +49,8 @@ struct AttnArgs {
     int H, G, mask, window, sinks, act;
     int TM, RT;         // rows of a tile; row tiles of 16 side by side in a CTA
     int min_share, lead;
+    uint64_t wait_ns;   // limit of a wait
+    int stall;          // test hook: no CTA's first keys are ever complete
     float* part;
     CacheDesc* desc;
 };

@@ -5,6 +5,7 @@
 #include <atomic>
 
 #include "cache_attn.cuh"
+#include "tc_common.cuh"
 
 namespace gdpa {
 namespace {
@@ -203,6 +204,10 @@ int device_sms() {
     return n;
 }
 
+// gdpa_cache_set_wait_test
+std::atomic<uint32_t> wait_limit_us{0};
+std::atomic<int> wait_stall{0};
+
 enum Kind { kFew, kSimt, kMma, kTc };
 struct Shape {
     Kind kind;
@@ -264,6 +269,13 @@ gdpa_status gdpa_cache_workspace(const gdpa_cache* cache, gdpa_dtype dtype, int6
     return s;
 }
 
+gdpa_status gdpa_cache_set_wait_test(int limit_us, int stall) {
+    if (limit_us < 0 || stall < 0 || stall > 1) return GDPA_ERR_INVALID_ARG;
+    gdpa::wait_limit_us.store((uint32_t)limit_us, std::memory_order_relaxed);
+    gdpa::wait_stall.store(stall, std::memory_order_relaxed);
+    return GDPA_OK;
+}
+
 gdpa_status gdpa_cache_fwd(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T, int H,
                            const gdpa_cache_rows* q, void* o, float* lse, const gdpa_cache_where* where,
                            const gdpa_cache_attn* attn, void* workspace, int64_t workspace_bytes, void* stream) {
@@ -311,6 +323,8 @@ gdpa_status gdpa_cache_fwd(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T,
     a.RT = p.RT;
     a.min_share = p.min_share;
     a.lead = p.lead;
+    a.wait_ns = tc::wait_limit_ns(wait_limit_us.load(std::memory_order_relaxed));
+    a.stall = wait_stall.load(std::memory_order_relaxed);
     a.desc = (CacheDesc*)workspace;
     a.part = (float*)(a.desc + p.grid);
     const bool sm = a.act == kSoftmax;

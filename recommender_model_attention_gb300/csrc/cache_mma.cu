@@ -71,12 +71,12 @@ cache_mma_kernel(const __grid_constant__ AttnArgs a) {
     if (tid == 0) {
         abort_flag = 0;
         for (int i = 0; i < C::kRing; ++i) {
-            mbar_init(&full[i], 1);
+            mbar_init(&full[i], a.stall ? 2 : 1);   // (an arrival that never comes)
             mbar_init(&empty[i], RT);
         }
         fence_mbar_init();
     }
-    const Abort ab{&abort_flag, a.c.err, kWaitLimitNs};
+    const Abort ab{&abort_flag, a.c.err, a.wait_ns};
     asm volatile("griddepcontrol.launch_dependents;");
     if (tid == 0) a.desc[blockIdx.x].parts = 0;
     Share sh = find_share<kThreads>(a, scan_tmp);   // (synchronises the CTA)

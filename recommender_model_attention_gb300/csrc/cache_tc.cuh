@@ -961,6 +961,7 @@ cache_tc_kernel(const __grid_constant__ AttnArgs a) {
         for (int b = 0; b < C::kNumBars; ++b) {
             uint32_t n = 1;
             if (b == C::kQFull) n = 256;
+            if (b == C::kKFull && a.stall) n = 2;   // (an arrival that never comes)
             if (b == C::kFin || (b >= C::kPFull && b < C::kPFull + 2) || (b >= C::kOFree && b < C::kOFree + 2)) n = 128;
             if ((b >= C::kKReady && b < C::kKEmpty) || (b >= C::kVReady && b < C::kVEmpty) || b >= C::kREmpty) n = C::kWorkers;
             mbar_init(&bars[b], n);
@@ -976,7 +977,7 @@ cache_tc_kernel(const __grid_constant__ AttnArgs a) {
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc.tmem;
-    const Abort ab{&misc.abort_flag, a.c.err, kWaitLimitNs};
+    const Abort ab{&misc.abort_flag, a.c.err, a.wait_ns};
     Place& at = reinterpret_cast<Place*>(smem + C::kOffPlace)[warp];
     if ((threadIdx.x & 31) == 0) at.sh = sh;
     __syncwarp();

@@ -127,6 +127,7 @@ def lib():
             "gdpa_cache_workspace": [ctypes.POINTER(_CacheSpec), st, ctypes.c_int64, st, st, i64p],
             "gdpa_cache_fwd": [ctypes.POINTER(_CacheSpec), st, ctypes.c_int64, st, vp, vp, vp, vp, vp, vp,
                                ctypes.c_int64, vp],
+            "gdpa_cache_set_wait_test": [st, st],
             "gdpa_cache_check": [ctypes.POINTER(_CacheSpec), i32p, vp],
         }
         for name, args in sig.items():
@@ -1018,6 +1019,12 @@ class KVCache:
     @property
     def nbytes(self) -> int:
         return sum(t.numel() for t in (self.k, self.v, self.k_scale, self.v_scale))
+
+    @staticmethod
+    def set_wait_test(limit_us: int = 0, stall: int = 0):
+        """Test hook, of all caches: shorten the attention kernels' waits to
+        ``limit_us`` microseconds and/or make their first keys never arrive."""
+        _ok(lib().gdpa_cache_set_wait_test(int(limit_us), int(stall)), "gdpa_cache_set_wait_test")
 
     def check(self, stream=None):
         """Wait for ``stream``; raise if a call since the last check met a page

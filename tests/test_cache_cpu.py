@@ -196,3 +196,10 @@ def test_binding_refuses_host_memory():
     pytest.importorskip("torch")
     with pytest.raises(ValueError):
         gd.KVCache(1, 1, 64, device="cpu")
+
+
+def test_wait_hook_refused():
+    L = raw.lib()
+    for args in ((-1, 0), (0, -1), (0, 2)):
+        assert L.gdpa_cache_set_wait_test(*args) == INVALID
+    assert L.gdpa_cache_set_wait_test(0, 0) == OK
