@@ -27,7 +27,7 @@
 //
 // Those 8 x 512 rows (4 heads a key head): bf16 218 us with the joining, 1.28
 // PFLOP/s, bound by a slot's chain of scores, weights and sums (tensor pipe 60%
-// busy); 8-bit 315 us: the row threads' instructions beside the workers'.
+// busy); 8-bit 321 us: the row threads' instructions beside the workers'.
 //
 // A block that some row does not see is masked by selection, event by event, and
 // workers clear the infinities and NaNs in its values (0 times them would be
@@ -50,9 +50,13 @@ constexpr float kRise = 8.0f;   // the reference follows a maximum this far abov
 struct Misc {
     uint32_t tmem;
     int abort_flag;
-    int dirty;           // workers cleared something (of this or an earlier segment)
+    uint8_t odd[8];      // by segment with blocks: its tag, if workers cleared something
     uint8_t gone[16];    // by block: groups without a page
 };
+// Workers are at most as many segments ahead of the row threads as there are stages
+// of values (4): a place is not another's while it is needed.  (A tag that was left
+// 1024 segments ago only costs time.)
+__device__ __forceinline__ uint8_t odd_tag(uint32_t segment) { return (uint8_t)((segment >> 3 & 127u) + 1u); }
 
 // Blocks of a segment, as both slots take them, and which are masked.
 struct Walk {
@@ -350,7 +354,7 @@ __device__ __forceinline__ void work_tiles(const AttnArgs& a, uint8_t* smem, uin
     RingAt<C::kK> rk;
     RingAt<C::kV> rv;
     RingAt<FP8 ? C::kR : 1> rr;
-    uint32_t block0 = 0;
+    uint32_t block0 = 0, segment = 0;   // segments: those with blocks
     const Segment& g = at.g;
     const Walk& w = at.w;
     while (advance(a, at)) {
@@ -370,7 +374,6 @@ __device__ __forceinline__ void work_tiles(const AttnArgs& a, uint8_t* smem, uin
             if (!__all_sync(0xffffffffu, mbar_wait<true>(&bars[C::kVEmpty + rv.st], rv.ph ^ 1, ab, 67))) return false;
             uint8_t* dst = smem + C::kOffV + rv.st * C::kTile;
             const bool clean = w.masked(b);
-            bool odd = false;
             if constexpr (FP8) {
                 if (!__all_sync(0xffffffffu, mbar_wait<true>(&bars[C::kRFull + rr.st], rr.ph, ab, 69))) return false;
                 const uint8_t* src = smem + C::kOffR + rr.st * C::kCodes;
@@ -383,7 +386,7 @@ __device__ __forceinline__ void work_tiles(const AttnArgs& a, uint8_t* smem, uin
                 static_assert(kRows % 8 == 0, "rows of the same swizzle");
                 const int ch = who % kChunks, e1 = 16 * ng;
                 if (clean) {
-                    odd = expand_masked<D, 32 * C::kWorkers>(g, 8 * b, src, sc, dst, who, e1);
+                    if (expand_masked<D, 32 * C::kWorkers>(g, 8 * b, src, sc, dst, who, e1)) misc.odd[segment & 7] = odd_tag(segment);
                 } else {
                     int e = who / kChunks;
                     src += cache_chunk(D, 7, e, ch);
@@ -406,17 +409,19 @@ __device__ __forceinline__ void work_tiles(const AttnArgs& a, uint8_t* smem, uin
                 fence_proxy_async_smem();
             } else if (clean) {
                 if (!__all_sync(0xffffffffu, mbar_wait<true>(&bars[C::kVFull + rv.st], rv.ph, ab, 69))) return false;
+                bool odd = false;
                 for (int x = who; x < 16 * ng * (D / 8); x += 32 * C::kWorkers) {
                     uint4* piece = reinterpret_cast<uint4*>(dst + (x & 7) * 16 + ((x >> 3) % (16 * ng)) * 128 + ((x >> 3) / (16 * ng)) * kHalfBytes);
                     uint4 v = *piece;
-                    if (clear_odd(v)) {
+                    if (clear_odd(v)) {   // (what lies behind the last event is nobody's)
+                        const int e = (x >> 3) % (16 * ng);
                         *piece = v;
-                        odd = true;
+                        odd |= segment_group(g, 8 * b + (e >> 4)) * kCacheGroup + (e & 15) < g.s.end;
                     }
                 }
+                if (odd) misc.odd[segment & 7] = odd_tag(segment);
                 fence_proxy_async_smem();
             }
-            if (odd) misc.dirty = 1;
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&bars[C::kVReady + rv.st]);
@@ -428,6 +433,7 @@ __device__ __forceinline__ void work_tiles(const AttnArgs& a, uint8_t* smem, uin
         });
         block0 += (uint32_t)w.nb;
         if (!ok) return;
+        segment += w.nb > 0;
     }
 }
 
@@ -585,18 +591,28 @@ __device__ __noinline__ void add_odd(const AttnArgs& a, const Segment& g, const 
                 const uint8_t* v = a.c.v + blk * a.c.block;
                 const uint32_t scale = FP8 ? a.c.vs[(blk << a.c.page_log) + e] : 0u;
                 if (FP8 && scale < kOddScale) continue;
-                for (int c = 0; c < 32; ++c) {
-                    const int col = c0 + c;
-                    float y;
-                    if constexpr (FP8) {
-                        uint32_t h;
-                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)v[cache_chunk(D, a.c.page_log, e, col >> 4) + (col & 15)]));
-                        y = __half22float2(*reinterpret_cast<__half2*>(&h)).x * cache_scale(scale);
-                        if (scale == 255u) y = __uint_as_float(0x7fc00000u);
-                    } else {
-                        y = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(v + cache_chunk(2 * D, a.c.page_log, e, col >> 3) + 2 * (col & 7)));
-                    }
+                const auto add = [&](int c, float y) {
                     if (!isfinite(y)) o[c] += SM ? y : y - y;
+                };
+                if constexpr (FP8) {
+                    for (int c = 0; c < 32; ++c) {
+                        uint32_t h;
+                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)v[cache_chunk(D, a.c.page_log, e, (c0 + c) >> 4) + (c & 15)]));
+                        add(c, scale == 255u ? __uint_as_float(0x7fc00000u) : __half22float2(*reinterpret_cast<__half2*>(&h)).x * cache_scale(scale));
+                    }
+                } else {
+                    uint4 q[4], z;   // (whole pieces, few of which hold any)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) q[k] = *reinterpret_cast<const uint4*>(v + cache_chunk(2 * D, a.c.page_log, e, (c0 >> 3) + k));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (!clear_odd(z = q[k])) continue;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            add(8 * k + 2 * c, bf16_lo((&q[k].x)[c]));
+                            add(8 * k + 2 * c + 1, bf16_hi((&q[k].x)[c]));
+                        }
+                    }
                 }
             }
         }
@@ -863,7 +879,7 @@ __device__ __forceinline__ void tile_rows(const AttnArgs& a, uint8_t* smem, uint
         }
         fins += both;
         if (!(dual && s)) {
-            const bool dirty = *reinterpret_cast<volatile int*>(&misc.dirty) != 0;
+            const bool dirty = *reinterpret_cast<volatile uint8_t*>(&misc.odd[used[0] & 7]) == odd_tag(used[0]);
             float* slot = nullptr;
             if (!g.whole) slot = a.part + (int64_t)(2 * blockIdx.x + (g.head ? 1 : 0)) * cache_slot(a.TM, D);
             const float inv = kSm ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
@@ -967,7 +983,7 @@ cache_tc_kernel(const __grid_constant__ AttnArgs a) {
             mbar_init(&bars[b], n);
         }
         misc.abort_flag = 0;
-        misc.dirty = 0;
+        for (int i = 0; i < 8; ++i) misc.odd[i] = 0;
         fence_mbar_init();
     }
     const Share sh = find_share<C::kThreads>(a, reinterpret_cast<int64_t*>(smem + C::kOffScan));

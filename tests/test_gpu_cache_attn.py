@@ -334,6 +334,27 @@ def test_visible_infinities_and_nans_are_seen(act, new, H, store, dtype, d):
                     assert torch.equal(l2, lse)
 
 
+@pytest.mark.parametrize("store,d", [("bf16", 128), ("bf16", 64), ("e4m3", 128), ("e4m3", 64)])
+@pytest.mark.parametrize("act", ["softmax", "silu"])
+@pytest.mark.parametrize("every", [1, 5, 7])
+def test_bad_events_of_some_samples_among_many(every, act, store, d):
+    """Several samples a CTA one after the other: those with a NaN in a block that
+    some of their rows do not see, and those without."""
+    n = 1600
+    new = [40 + i % 3 for i in range(n)]
+    b = Batch(new, [(i * 37) % 150 for i in range(n)], H=1, Hkv=1, d=d, store=store).fill()
+    clean, lse = b.run(act)
+    first = np.cumsum(b.new + b.hist) - (b.new + b.hist)
+    hit = np.zeros(sum(new), dtype=bool)
+    for s in range(0, n, every):
+        b.v_all[first[s] + b.hist[s] + 20] = float("nan")   # new row 20
+        hit[b.off_host[s] + 20:b.off_host[s + 1]] = True
+    o, l2 = b.fill().run(act)
+    hit = torch.from_numpy(hit).cuda()
+    assert torch.isnan(o[hit]).all() and torch.equal(o[~hit], clean[~hit])
+    assert lse is None or torch.equal(l2, lse)
+
+
 def poke(b, event, scale, code):
     """The values of an event of sample 0 in an 8-bit cache's memory: `code` in
     every column and a scale byte (a page that was never written, or another's)."""
