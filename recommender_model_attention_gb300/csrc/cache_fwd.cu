@@ -215,6 +215,9 @@ struct Shape {
     int64_t bytes;
 };
 
+// Rows and heads (a multiple of the cache's) that the kernels' counts hold.
+bool sizes_fit(const CacheView& c, int64_t T, int H) { return T <= kCacheMost && H / c.heads <= 128 && T * H <= 0x7fffffff; }
+
 // The kernel, its tile and its workspace: rules on types and sizes alone.
 gdpa_status shape(const CacheView& c, gdpa_dtype dt, int64_t T, int H, int B, Shape& s) {
     const int64_t rows = B > 0 ? T * (H / c.heads) / B : 0;   // of an average sample and key head
@@ -263,6 +266,7 @@ gdpa_status gdpa_cache_workspace(const gdpa_cache* cache, gdpa_dtype dtype, int6
     if (!gdpa::cache_view(cache, c, &s)) return s;
     if (!bytes || T < 0 || B < 0 || H < 1 || H % c.heads) return GDPA_ERR_INVALID_ARG;
     if (dtype != GDPA_BF16 && dtype != GDPA_F32) return GDPA_ERR_INVALID_ARG;
+    if (!gdpa::sizes_fit(c, T, H)) return GDPA_ERR_UNSUPPORTED;
     gdpa::Shape p;
     s = gdpa::shape(c, dtype, T, H, B, p);
     if (s == GDPA_OK) *bytes = p.bytes;
@@ -299,7 +303,7 @@ gdpa_status gdpa_cache_fwd(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T,
     const bool tree = attn->mask == GDPA_CACHE_TREE;
     if (T > 0 && tree && (!attn->parents || (uintptr_t)attn->parents % 4)) return GDPA_ERR_INVALID_ARG;
     a.G = H / a.c.heads;
-    if (a.G > 128 || T * H > 0x7fffffff) return GDPA_ERR_UNSUPPORTED;
+    if (!sizes_fit(a.c, T, H)) return GDPA_ERR_UNSUPPORTED;
     if (T == 0 || a.w.B == 0) return GDPA_OK;
     const size_t es = dtype == GDPA_BF16 ? 2 : 4;
     if (!q->x || (uintptr_t)q->x % es || !o || (uintptr_t)o % 16) return GDPA_ERR_INVALID_ARG;

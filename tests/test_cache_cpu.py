@@ -192,6 +192,14 @@ def test_workspace_refused():
     assert L.gdpa_cache_workspace(ctypes.byref(c), 0, 5, 4, 2, None) == INVALID
 
 
+@pytest.mark.parametrize("T,H", [(1 << 30, 4), (1 << 62, 4), ((1 << 63) - 1, 2), (5, 258), (1 << 29, 8), (1 << 24, 256)])
+def test_workspace_of_sizes_that_attention_refuses(T, H):
+    """... is refused the same way (products of such sizes leave 64 bits)."""
+    L, c, n = raw.lib(), cache(), ctypes.c_int64(-7)
+    assert L.gdpa_cache_workspace(ctypes.byref(c), 0, T, H, 2, ctypes.byref(n)) == UNSUPPORTED and n.value == -7
+    assert L.gdpa_cache_fwd(ctypes.byref(c), 0, T, H, rows(), A, None, where(), attn(), A, 1 << 40, None) == UNSUPPORTED
+
+
 def test_binding_refuses_host_memory():
     pytest.importorskip("torch")
     with pytest.raises(ValueError):
