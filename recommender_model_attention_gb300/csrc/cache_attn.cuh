@@ -355,6 +355,39 @@ __device__ __forceinline__ void add_compensated(float& sum, float& lost, float x
     sum = t;
 }
 
+// values of 16 bytes of a cache row
+__host__ __device__ constexpr int cache_per_chunk(int store) {
+    return store == GDPA_STORE_F32 ? 4 : store == GDPA_STORE_BF16 ? 8 : 16;
+}
+
+// the values of a word of 16 bytes of a cache row
+template <int STORE>
+__device__ __forceinline__ void expand_word(uint32_t w, float (&x)[cache_per_chunk(STORE) / 4]) {
+    if constexpr (STORE == GDPA_STORE_F32) {
+        x[0] = __uint_as_float(w);
+    } else if constexpr (STORE == GDPA_STORE_BF16) {
+        x[0] = __uint_as_float(w << 16);
+        x[1] = __uint_as_float(w & 0xffff0000u);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t h;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w >> (16 * i))));
+            const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
+    }
+}
+
+// value by value of 16 bytes of a cache row (8-bit: as its code's value)
+template <int STORE>
+__device__ __forceinline__ void expand(const uint4& q, float (&x)[cache_per_chunk(STORE)]) {
+    constexpr int V = cache_per_chunk(STORE) / 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) expand_word<STORE>((&q.x)[i], *reinterpret_cast<float(*)[V]>(x + V * i));
+}
+
 // Four values to the row type.
 __device__ __forceinline__ void put4(float* p, const float (&x)[4]) {
     *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
@@ -438,11 +471,7 @@ inline bool cache_smem(const void* kernel, int bytes, std::atomic<uint64_t>& don
 gdpa_status launch_cache_mma(const AttnArgs& a, int grid, cudaStream_t st);
 gdpa_status launch_cache_tc_bf16(const AttnArgs& a, int grid, cudaStream_t st);
 gdpa_status launch_cache_tc_e4m3(const AttnArgs& a, int grid, cudaStream_t st);
-// Values of 16 bytes of a cache row, and the CTAs an SM that the registers of R
-// rows' queries and sums of so many columns leave room for.
-__host__ __device__ constexpr int cache_per_chunk(int store) {
-    return store == GDPA_STORE_F32 ? 4 : store == GDPA_STORE_BF16 ? 8 : 16;
-}
+// CTAs an SM that the registers of R rows' queries and sums leave room for.
 __host__ __device__ constexpr int cache_few_per_sm(int store, int R) {
     return R * cache_per_chunk(store) <= 16 ? 4 : R * cache_per_chunk(store) <= 32 ? 3 : 2;
 }

@@ -17,46 +17,10 @@ namespace {
 
 constexpr int kThreads = 128, kAhead = 4;
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-
-template <int STORE>
-constexpr int per_chunk() {
-    return cache_per_chunk(STORE);
-}
-
-// the values of word i of 16 bytes of a cache row
-template <int STORE>
-__device__ __forceinline__ void expand_word(uint32_t w, float (&x)[per_chunk<STORE>() / 4]) {
-    if constexpr (STORE == GDPA_STORE_F32) {
-        x[0] = __uint_as_float(w);
-    } else if constexpr (STORE == GDPA_STORE_BF16) {
-        x[0] = __uint_as_float(w << 16);
-        x[1] = __uint_as_float(w & 0xffff0000u);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            uint32_t h;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w >> (16 * i))));
-            const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
-        }
-    }
-}
-
-// value by value of 16 bytes of a cache row (8-bit: as its code's value)
-template <int STORE>
-__device__ __forceinline__ void expand(const uint4& q, float (&x)[per_chunk<STORE>()]) {
-    constexpr int V = per_chunk<STORE>() / 4;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) expand_word<STORE>((&q.x)[i], *reinterpret_cast<float(*)[V]>(x + V * i));
-}
-
 template <typename E, int STORE, bool SM, int R>
 __global__ void __launch_bounds__(kThreads, cache_few_per_sm(STORE, R))
 cache_few_kernel(const __grid_constant__ AttnArgs a) {
-    constexpr int N = per_chunk<STORE>();
+    constexpr int N = cache_per_chunk(STORE);
     __shared__ int64_t scan_tmp[kThreads / 32 + 2];
     __shared__ float2 ml[4][4];
     __shared__ __align__(16) float sums[4][R][132];

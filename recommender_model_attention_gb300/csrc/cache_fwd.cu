@@ -193,17 +193,6 @@ gdpa_status launch_join(const AttnArgs& a, int ctas, int sms, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, cache_join_kernel<E, SM>, a, ctas) == cudaSuccess ? GDPA_OK : GDPA_ERR_CUDA;
 }
 
-// SMs of the current device (looked up once a device), 0 if there is none
-int device_sms() {
-    static std::atomic<int> known[64];
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
-    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
-    return n;
-}
-
 // gdpa_cache_set_wait_test
 std::atomic<uint32_t> wait_limit_us{0};
 std::atomic<int> wait_stall{0};
@@ -227,9 +216,9 @@ gdpa_status shape(const CacheView& c, gdpa_dtype dt, int64_t T, int H, int B, Sh
     // and tcgen05: 32 rows on 300 events 19 and 24, on 4000 events 52 and 53; 64
     // rows 27 and 25, 89 and 55; 128 rows 42 and 29, 156 and 57).
     // On the CUDA cores: straight from the pages up to 4 rows, through shared memory
-    // above (512 users of one float32 row: 609 and 3318 us).
+    // above (512 users of one float32 row: 620 and 3318 us).
     s.kind = !tc ? rows <= 4 ? kFew : kSimt : rows <= 32 ? kMma : kTc;
-    s.sms = device_sms();
+    s.sms = cache_sms();
     if (s.sms == 0) return GDPA_ERR_CUDA;
     // What an item costs beside its events, in groups of 16 of them, and the fewest
     // that are worth a CTA (measured on the same; trees of 32 users on tcgen05: 75

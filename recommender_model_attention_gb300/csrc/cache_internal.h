@@ -82,7 +82,11 @@ __device__ __forceinline__ int64_t cache_block(const CacheView& c, const CacheWh
 // 2^(byte - 127) of a scale byte (1 .. 247; 255, of a row of NaNs, gives infinity)
 __device__ __forceinline__ float cache_scale(uint32_t byte) { return __uint_as_float(byte << 23); }
 
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+
 bool cache_view(const gdpa_cache* c, CacheView& v, gdpa_status* s);
 gdpa_status cache_where(const gdpa_cache_where* w, int64_t T, const CacheView& c, CacheWhere& o);
+int cache_sms();   // SMs of the current device (looked up once a device), 0 if there is none
 
 }  // namespace gdpa

@@ -7,7 +7,7 @@
 // its own events: groups of 16 come in by bulk copies through a ring in shared
 // memory, several groups ahead, and are used from there as operands without any
 // rearrangement (the cache lies in the order that needs none): a thread's 16
-// bytes of a key row are the B operand of S = Q K^T for 4 (8-bit: 8) steps of
+// bytes of a key row are the B operand of S = Q K^T for 2 (8-bit: 4) steps of
 // the contraction, whose order over d is free as long as Q has the same; two
 // value rows' bytes interleaved are the B operand of O += P V, each thread's
 // columns of O being a run of d.  A CTA's four warps take turns over the groups
@@ -45,13 +45,6 @@ namespace {
 
 using namespace tc;
 using namespace cache_mma;
-
-__device__ __forceinline__ void bulk_load(uint64_t* bar, void* dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
 
 template <int D, bool FP8, bool SM, bool R8>
 __global__ void __launch_bounds__(kThreads, Cfg<D, FP8, R8>::kPerSm)

@@ -7,7 +7,7 @@
 // Rows8: events, then columns of d, are the m: S^T = K Q^T, O^T += V^T P^T.  Half
 // the products and a quarter of the scores a thread for the same operands from
 // shared memory; the weights are turned by movmatrix between the two.
-// In both a thread's 16 bytes of a key row are operands of 4 (8-bit: 8) steps of
+// In both a thread's 16 bytes of a key row are operands of 2 (8-bit: 4) steps of
 // the contraction, whose order over d is free as long as Q has the same, and two
 // value rows' bytes interleaved are operands of the second product, each thread's
 // part of O being runs of d.

@@ -14,38 +14,20 @@ namespace {
 
 constexpr int kThreads = 128;
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-
 // 16 bytes of a cache row as float32 values
 template <int STORE>
-__device__ __forceinline__ void expand(float* dst, const uint4& q, float scale) {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    if constexpr (STORE == GDPA_STORE_F32) {
+__device__ __forceinline__ void expand_to(float* dst, const uint4& q, float scale) {
+    constexpr int N = cache_per_chunk(STORE);
+    float x[N];
+    expand<STORE>(q, x);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dst[i] = __uint_as_float(w[i]);
-    } else if constexpr (STORE == GDPA_STORE_BF16) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            dst[2 * i] = __uint_as_float(w[i] << 16);
-            dst[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint32_t h;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[i >> 1] >> (16 * (i & 1)))));
-            const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
-            dst[2 * i] = f.x * scale;
-            dst[2 * i + 1] = f.y * scale;
-        }
-    }
+    for (int i = 0; i < N; ++i) dst[i] = STORE == GDPA_STORE_E4M3 ? x[i] * scale : x[i];
 }
 
 template <typename E, int STORE, bool SM>
 __global__ void __launch_bounds__(kThreads)
 cache_simt_kernel(const __grid_constant__ AttnArgs a) {
-    constexpr int kPer = STORE == GDPA_STORE_F32 ? 4 : STORE == GDPA_STORE_BF16 ? 8 : 16;   // values a chunk
+    constexpr int kPer = cache_per_chunk(STORE);   // values a chunk
     extern __shared__ __align__(16) float fsm[];
     __shared__ int64_t scan_tmp[kThreads / 32 + 2];
     __shared__ float wsm[4][16][17];
@@ -84,8 +66,8 @@ cache_simt_kernel(const __grid_constant__ AttnArgs a) {
                     sk = cache_scale(a.c.ks[(blk << a.c.page_log) + in + e]);
                     sv = cache_scale(a.c.vs[(blk << a.c.page_log) + in + e]);
                 }
-                expand<STORE>(K + e * ld + c * kPer, *reinterpret_cast<const uint4*>(a.c.k + blk * a.c.block + at), sk);
-                expand<STORE>(V + e * ld + c * kPer, *reinterpret_cast<const uint4*>(a.c.v + blk * a.c.block + at), sv);
+                expand_to<STORE>(K + e * ld + c * kPer, *reinterpret_cast<const uint4*>(a.c.k + blk * a.c.block + at), sk);
+                expand_to<STORE>(V + e * ld + c * kPer, *reinterpret_cast<const uint4*>(a.c.v + blk * a.c.block + at), sv);
             }
             __syncwarp();
             float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};

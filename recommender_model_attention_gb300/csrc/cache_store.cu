@@ -21,6 +21,8 @@
 // other: 156 us for the 430 MB of 256 histories written and read back).
 #include <string.h>
 
+#include <atomic>
+
 #include "cache_internal.h"
 
 namespace gdpa {
@@ -126,8 +128,6 @@ __device__ __forceinline__ float2 from_e4m3x2(uint16_t v) {
     return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void put(float& y, float v) { y = v; }
 __device__ __forceinline__ void put(__nv_bfloat16& y, float v) { y = __float2bfloat16_rn(v); }
 
@@ -286,7 +286,9 @@ gdpa_status launch(void (*f)(const StoreArgs), StoreArgs& a, int width, int pass
     const int heads2 = 2 * a.c.heads, room = passes * (kThreads / width);
     a.rows = heads2 < room ? heads2 : room;
     a.tokens = room / a.rows;
-    while (a.tokens > 1 && (a.w.T + a.tokens - 1) / a.tokens < 4 * 152) a.tokens = (a.tokens + 1) / 2;
+    const int sms = cache_sms();
+    if (sms == 0) return GDPA_ERR_CUDA;
+    while (a.tokens > 1 && (a.w.T + a.tokens - 1) / a.tokens < 4 * sms) a.tokens = (a.tokens + 1) / 2;
     a.step_tok = kThreads / width / a.rows;
     a.step_row = kThreads / width - a.step_tok * a.rows;
     const int64_t blocks = (a.w.T + a.tokens - 1) / a.tokens;
@@ -353,6 +355,16 @@ bool cache_view(const gdpa_cache* c, CacheView& v, gdpa_status* s) {
     v.block = (int64_t)v.row << v.page_log;
     *s = GDPA_OK;
     return true;
+}
+
+int cache_sms() {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 gdpa_status cache_where(const gdpa_cache_where* w, int64_t T, const CacheView& c, CacheWhere& o) {

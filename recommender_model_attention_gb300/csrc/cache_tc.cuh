@@ -164,13 +164,6 @@ struct Cfg {
     static_assert(kSmem <= 232448, "shared memory");
 };
 
-__device__ __forceinline__ void bulk_load(uint64_t* bar, void* dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
-
 // The loader (a whole warp).
 template <int D, bool FP8>
 __device__ __forceinline__ void load_tiles(const AttnArgs& a, uint8_t* smem, uint64_t* bars, Misc& misc, Place& at,

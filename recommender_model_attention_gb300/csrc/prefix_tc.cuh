@@ -1,6 +1,6 @@
 // What the tensor-core kernels of shared-prefix attention share (and the history
-// cache's takes from them): the issue of products by one elected lane,
-// exponentials in multiply-adds, and the records they walk.
+// cache's takes from them): the issue of products by one elected lane, a maximum
+// that keeps NaNs, and the records they walk.
 #pragma once
 
 #include "prefix_internal.h"
@@ -87,27 +87,6 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap* map, uint64_t* ba
         ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
         : "memory");
-}
-
-// 2^t of two values t <= 126 in multiply-adds: t = n + f with |f| <= 1/2
-// (adding 1.5 * 2^23 leaves n in the low bits), a minimax polynomial of degree
-// 4 for 2^f (of the relative error, by exchange, then rounded to float32 with the
-// mean near 0: at most 2.7e-6, mean 4e-8, against the weights' rounding
-// to bf16 of 2^-8), n added to the exponent; below -126, 0.
-__device__ __forceinline__ float2 exp2_poly(float2 t) {
-    constexpr float kMagic = 12582912.0f;
-    const uint64_t x = f2_make(t.x, t.y), one = f2_make(1.0f, 1.0f);
-    const uint64_t r = f2_fma(x, one, f2_make(kMagic, kMagic));
-    const uint64_t n = f2_fma(r, one, f2_make(-kMagic, -kMagic));
-    const uint64_t f = f2_fma(n, f2_make(-1.0f, -1.0f), x);
-    uint64_t p = f2_fma(f, f2_make(0.009570101276f, 0.009570101276f), f2_make(0.05591785908f, 0.05591785908f));
-    p = f2_fma(p, f, f2_make(0.2402474433f, 0.2402474433f));
-    p = f2_fma(p, f, f2_make(0.6931217909f, 0.6931217909f));
-    p = f2_fma(p, f, f2_make(0.9999992847f, 0.9999992847f));
-    const float2 pf = f2_split(p), rf = f2_split(r);
-    const float a = __uint_as_float(__float_as_uint(pf.x) + (__float_as_uint(rf.x) << 23));
-    const float b = __uint_as_float(__float_as_uint(pf.y) + (__float_as_uint(rf.y) << 23));
-    return make_float2(t.x < -126.0f ? 0.0f : a, t.y < -126.0f ? 0.0f : b);
 }
 
 // the largest of three, NaN if any is
