@@ -797,7 +797,10 @@ gdpa_status gdpa_cache_read(const gdpa_cache* cache, gdpa_dtype dtype, int64_t T
  * above 2^100 may give infinite ones where tiny queries make them finite.  workspace:
  * gdpa_cache_workspace bytes of device memory (16-byte aligned) for this call
  * alone while it runs.  Nothing depends on host knowledge of lengths: one
- * captured graph serves growing histories.
+ * captured graph serves growing histories.  Which kernel runs goes by T H / heads /
+ * B, the rows of an average sample and key head, where samples without rows and rows
+ * behind the last one count: a few long samples beside many single rows, or many
+ * more rows than the samples use, are right, but not fast.
  * INVALID_ARG, UNSUPPORTED as above. */
 typedef enum { GDPA_CACHE_CAUSAL = 0, GDPA_CACHE_HISTORY = 1, GDPA_CACHE_TREE = 2 } gdpa_cache_mask;
 typedef struct {

@@ -9,7 +9,7 @@
 // over the event's lanes.  Each run of lanes keeps a softmax of its own over the
 // events that it took; they are joined at the end of a segment.  Four events a
 // lane are on their way at a time, and two to four CTAs an SM.  (512 users' newest events
-// on 3 GB of float32 rows: 620 us, 4.8 TB/s; 3318 by the kernel for 16 rows a warp.)
+// on 3 GB of float32 rows: 620 us, 4.8 TB/s; 3199 by the kernel for 16 rows a warp.)
 #include "cache_attn.cuh"
 
 namespace gdpa {

@@ -25,7 +25,7 @@
 // 120) (two where that leaves bf16's range) gives it.  (Keys expanded as well:
 // the workers bound the kernel, 480 us for 8 x 512 rows on 16384 events.)
 //
-// Those 8 x 512 rows (4 heads a key head): bf16 218 us with the joining, 1.28
+// Those 8 x 512 rows (4 heads a key head): bf16 222 us with the joining, 1.26
 // PFLOP/s, bound by a slot's chain of scores, weights and sums (tensor pipe 60%
 // busy); 8-bit 321 us: the row threads' instructions beside the workers'.
 //
