@@ -25,9 +25,9 @@
 // 120) (two where that leaves bf16's range) gives it.  (Keys expanded as well:
 // the workers bound the kernel, 480 us for 8 x 512 rows on 16384 events.)
 //
-// Those 8 x 512 rows (4 heads a key head): bf16 222 us with the joining, 1.26
+// Those 8 x 512 rows (4 heads a key head): bf16 220 us with the joining, 1.27
 // PFLOP/s, bound by a slot's chain of scores, weights and sums (tensor pipe 60%
-// busy); 8-bit 321 us: the row threads' instructions beside the workers'.
+// busy); 8-bit 317 us: the row threads' instructions beside the workers'.
 //
 // A block that some row does not see is masked by selection, event by event, and
 // workers clear the infinities and NaNs in its values (0 times them would be
@@ -307,10 +307,11 @@ __device__ __forceinline__ void value_factors(uint32_t s, uint32_t& m, uint32_t&
 }
 
 // A masked block's values: what is infinite or a NaN, and events behind the last one
-// (whatever their memory holds), are zeros.  Whether the former were any.  (Out of
-// line: the blocks that every row sees are the loop that is to go on.)
+// (whatever their memory holds), are zeros; the former are noted.  (Out of line: the
+// blocks that every row sees are the loop that is to go on.)
 template <int D, int NT>
-__device__ __noinline__ bool expand_masked(const Segment& g, int i0, const uint8_t* codes, const uint8_t* sc, uint8_t* dst, int who, int events) {
+__device__ __noinline__ void expand_masked(const Segment& g, int i0, const uint8_t* codes, const uint8_t* sc, uint8_t* dst, int who, int events,
+                                            uint8_t* mark, uint32_t segment) {
     constexpr int kChunks = D / 16;
     const int ch = who % kChunks;
     bool odd = false;
@@ -335,7 +336,7 @@ __device__ __noinline__ bool expand_masked(const Segment& g, int i0, const uint8
         *lo = x;
         *hi = y;
     }
-    return odd;
+    if (odd) mark[segment & 7] = odd_tag(segment);
 }
 
 // The workers (warps; whole).
@@ -379,7 +380,7 @@ __device__ __forceinline__ void work_tiles(const AttnArgs& a, uint8_t* smem, uin
                 static_assert(kRows % 8 == 0, "rows of the same swizzle");
                 const int ch = who % kChunks, e1 = 16 * ng;
                 if (clean) {
-                    if (expand_masked<D, 32 * C::kWorkers>(g, 8 * b, src, sc, dst, who, e1)) misc.odd[segment & 7] = odd_tag(segment);
+                    expand_masked<D, 32 * C::kWorkers>(g, 8 * b, src, sc, dst, who, e1, misc.odd, segment);
                 } else {
                     int e = who / kChunks;
                     src += cache_chunk(D, 7, e, ch);
